@@ -63,6 +63,7 @@ def lib() -> ctypes.CDLL:
     import torch  # noqa: F401
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    f32 = ctypes.c_float
     sig = {
         "nf4moe_quantize": [ctypes.c_int, vp, i64, i64, vp, vp, vp],
         "nf4moe_dequantize": [ctypes.c_int, vp, vp, i64, i64, vp, vp],
@@ -81,6 +82,14 @@ def lib() -> ctypes.CDLL:
         "nf4moe_moe_forward_noalloc": [ctypes.POINTER(Layer), vp, i32, vp, vp, vp, vp],
         "nf4moe_moe_forward_profiled": [ctypes.POINTER(Layer), vp, i32, vp, vp, sz, vp,
                                         ctypes.POINTER(ctypes.c_void_p)],
+        "nf4moe_ckpt8_quantize": [ctypes.c_int, vp, ctypes.c_int, i64, i64, vp, vp, vp],
+        "nf4moe_ckpt8_dequantize": [ctypes.c_int, vp, vp, i64, i64, vp, ctypes.c_int, vp],
+        "nf4moe_glu_forward": [vp, ctypes.c_int, i64, i32, i32, f32, f32, i32, vp, ctypes.c_int, vp, vp, vp],
+        "nf4moe_glu_backward": [vp, ctypes.c_int, ctypes.c_int, vp, vp, i64, i32, i32, f32, f32, i32, vp, vp,
+                                vp, vp, vp],
+        "nf4moe_block_norm_forward": [vp, vp, vp, i64, vp, vp, vp, vp, vp],
+        "nf4moe_block_norm_workspace_bytes": [i32, i64],
+        "nf4moe_block_norm_backward": [vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp],
         "nf4moe_codebook": [ctypes.c_int, ctypes.POINTER(ctypes.c_float)],
         "nf4moe_auto_path": [ctypes.c_int, i64, i64],
         "nf4moe_stream_read_sink_words": [i64, i32],
@@ -96,7 +105,7 @@ def lib() -> ctypes.CDLL:
         fn.argtypes = args
         fn.restype = ctypes.c_int
     for name in ("nf4moe_route_workspace_bytes", "nf4moe_gemm_workspace_bytes", "nf4moe_workspace_bytes",
-                 "nf4moe_router_workspace_bytes"):
+                 "nf4moe_router_workspace_bytes", "nf4moe_block_norm_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_size_t
     L.nf4moe_stream_read_sink_words.restype = ctypes.c_int64
     L.nf4moe_mfma_peak_flops.restype = ctypes.c_int64
@@ -530,3 +539,9 @@ def moe_forward(layer: MoELayer, x, return_routing: bool = False):
     w = torch.empty(T, layer.top_k, dtype=torch.float32, device=x.device)
     out = fwd(x, topk_ids=ids, topk_w=w)
     return out, ids, w
+
+
+# fine-tuning and multi-adapter serving around the frozen 4-bit layer
+from .train import (CKPT_MXFP8, CKPT_MXINT8, GATE_IDENTITY, GATE_SIGMOID, GATE_TANH, Ckpt8,  # noqa: E402
+                    block_norm_backward, block_norm_forward, ckpt8_dequantize, ckpt8_quantize, glu_backward,
+                    glu_forward)

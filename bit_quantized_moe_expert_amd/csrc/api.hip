@@ -12,6 +12,7 @@
 #include "dgrad.h"
 #include "internal.h"
 #include "probe.h"
+#include "status.h"
 
 using namespace nf4moe;
 
@@ -21,9 +22,9 @@ using namespace nf4moe;
 // per-device address hipGetSymbolAddress returns.
 static __device__ __align__(256) uint8_t scratch[NF4MOE_NOALLOC_SCRATCH_BYTES];
 
-namespace {
+static thread_local char g_err[512] = "";
 
-thread_local char g_err[512] = "";
+namespace nf4moe {
 
 nf4moe_status_t fail(nf4moe_status_t st, const char *fmt, ...) {
   va_list ap;
@@ -38,7 +39,9 @@ nf4moe_status_t hip_status(hipError_t e, const char *what) {
   return fail(NF4MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+}  // namespace nf4moe
+
+namespace {
 
 bool fmt_nf4(nf4moe_format_t f) { return f == NF4MOE_FMT_NF4_B64 || f == NF4MOE_FMT_NF4_B64_BF16ABS; }
 int fmt_block(nf4moe_format_t f) { return fmt_nf4(f) ? 64 : 32; }

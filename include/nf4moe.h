@@ -330,6 +330,116 @@ nf4moe_status_t nf4moe_moe_forward_profiled(const nf4moe_layer_t *layer, const u
                                             int32_t T, uint16_t *out, void *ws, size_t ws_bytes,
                                             void *stream, void *const *events);
 
+/* ---------------------------------------------------------------------------
+ * Fine-tuning and multi-adapter serving around the frozen 4-bit layer. These
+ * calls follow the same conventions (caller-owned device memory, checks before
+ * anything is enqueued, one stream, no host synchronisation, capturable).
+ *
+ * 8-bit activation checkpoints. A tensor [rows, K] kept for the backward pass as
+ * one byte per value and one e8m0 scale byte b per 32 consecutive k (multiplier
+ * 2^(b - 127)), the OCP MX v1.0 element formats:
+ *   MXINT8  X = floor(log2 amax); code int8 = RNE(v / 2^(X - 6)) in [-127, 127]
+ *   MXFP8   X = floor(log2 amax) - 8; code = e4m3 RNE(v / 2^X), saturated at 448
+ * X at least -127, b = X + 127. Every code is an exact function of the input
+ * (power-of-two scale, ties to even) and every decoded value is exact in bf16
+ * where bf16 has the range. A block holding a NaN or an infinity gets b = 255
+ * and decodes to NaN as a whole. K % 32 == 0; any alignment of codes and scale.
+ * ------------------------------------------------------------------------- */
+typedef enum { NF4MOE_CKPT_MXINT8 = 0, NF4MOE_CKPT_MXFP8 = 1 } nf4moe_ckpt8_t;
+
+/* How a tensor that the backward reads is held: as values, or as a checkpoint
+ * (codes, with the scales beside them). */
+typedef enum {
+  NF4MOE_SRC_F32 = 0,
+  NF4MOE_SRC_BF16 = 1,
+  NF4MOE_SRC_MXINT8 = 2,
+  NF4MOE_SRC_MXFP8 = 3
+} nf4moe_src_t;
+
+/* nf4moe_ckpt8_quantize / _dequantize -- x fp32 or bf16 [rows, K] -> codes uint8
+ * [rows, K], scale uint8 [rows, K/32], and back to fp32 or bf16. rows == 0 is a
+ * no-op. Errors: INVALID_ARG (format, dtype, rows < 0, K not a positive multiple
+ * of 32, null pointers, x or out not aligned to its element). */
+nf4moe_status_t nf4moe_ckpt8_quantize(nf4moe_ckpt8_t fmt, const void *x, nf4moe_dtype_t x_dtype, int64_t rows, int64_t K,
+                                      uint8_t *codes, uint8_t *scale, void *stream);
+nf4moe_status_t nf4moe_ckpt8_dequantize(nf4moe_ckpt8_t fmt, const uint8_t *codes, const uint8_t *scale, int64_t rows,
+                                        int64_t K, void *out, nf4moe_dtype_t out_dtype, void *stream);
+
+/* nf4moe_glu_forward -- h[r] = the gated activation (nf4moe_glu_t) of the gate_up
+ * product gu [R, 2I] (fp32 or bf16; gate and up in halves, or interleaved as in
+ * nf4moe_layer_t), bf16 RNE [R, I]. With codes / scale the same pass also writes
+ * gu's 8-bit checkpoint ([R, 2I] and [R, 2I/32], format ckpt); both NULL saves
+ * nothing. I % 32 == 0. R == 0 is a no-op. Errors: INVALID_ARG. */
+nf4moe_status_t nf4moe_glu_forward(const void *gu, nf4moe_dtype_t gu_dtype, int64_t R, int32_t I, int32_t glu,
+                                   float glu_alpha, float glu_limit, int32_t glu_interleaved, uint16_t *h,
+                                   nf4moe_ckpt8_t ckpt, uint8_t *codes, uint8_t *scale, void *stream);
+
+/* nf4moe_glu_backward -- gradient of nf4moe_glu_forward at the gu that is held
+ * (gu_src: values, or a checkpoint decoded in registers; gu_scale only for a
+ * checkpoint). dh [R, I] is the gradient of h for a row weight of 1 (fp32 or
+ * bf16); row_w fp32 [R] (NULL: 1) scales each row's gradient, as the router's
+ * weight scales an expert's output:
+ *   dgu    bf16 [R, 2I]   row_w[r] * dh[r] through the activation, in gu's layout
+ *   h      bf16 [R, I]    the activation recomputed (optional)
+ *   drow_w fp32 [R]       sum_c dh[r, c] * h[r, c], the gradient of row_w (optional)
+ * The clamped form's gradient is that of the unclamped side at the limit itself.
+ * Errors: INVALID_ARG. */
+nf4moe_status_t nf4moe_glu_backward(const void *dh, nf4moe_dtype_t dh_dtype, nf4moe_src_t gu_src, const void *gu,
+                                    const uint8_t *gu_scale, int64_t R, int32_t I, int32_t glu, float glu_alpha,
+                                    float glu_limit, int32_t glu_interleaved, const float *row_w, uint16_t *dgu,
+                                    uint16_t *h, float *drow_w, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms around a block, fused with its gate and residual scale. Row by row
+ * over [T, H], with the residual stream x, the block's output f and, where the
+ * next block has one, its pre norm:
+ *   z  = f * rstd_post * w_post      rstd_post = 1 / sqrt(mean(f^2) + eps); z = f
+ *                                    without w_post
+ *   x' = x + alpha * phi(gate) * z   stored as x_dtype, one rounding
+ *   y  = x' * rstd_pre * w_pre       of the stored x', bf16
+ * One pass; fp32 in registers. gate: none, one value per channel [H], per row
+ * [T], or per element [T, H] (fp32 or bf16); phi the identity, sigmoid or tanh.
+ * f NULL: a pre norm alone (x is left where it is). w_pre NULL: no pre norm.
+ * H is 1..16384; rows are contiguous; no alignment beyond the element's.
+ * ------------------------------------------------------------------------- */
+typedef enum { NF4MOE_GATE_NONE = 0, NF4MOE_GATE_CHANNEL = 1, NF4MOE_GATE_ROW = 2, NF4MOE_GATE_FULL = 3 } nf4moe_gate_kind_t;
+typedef enum { NF4MOE_GATE_IDENTITY = 0, NF4MOE_GATE_SIGMOID = 1, NF4MOE_GATE_TANH = 2 } nf4moe_gate_fn_t;
+
+typedef struct {
+  int32_t H;
+  int32_t x_dtype;       /* nf4moe_dtype_t of x, x', dx', dx                   */
+  const float *w_post;   /* [H] or NULL                                        */
+  const float *w_pre;    /* [H] or NULL                                        */
+  const void *gate;      /* by gate_kind; NULL with NF4MOE_GATE_NONE           */
+  int32_t gate_kind;     /* nf4moe_gate_kind_t                                 */
+  int32_t gate_dtype;    /* nf4moe_dtype_t                                     */
+  int32_t gate_fn;       /* nf4moe_gate_fn_t                                   */
+  float alpha;           /* residual scale, finite                             */
+  float eps;             /* finite, >= 0                                       */
+} nf4moe_block_norm_t;
+
+/* nf4moe_block_norm_forward -- x [T, H], f bf16 [T, H] or NULL -> x_new [T, H]
+ * (may be x itself; not written without f), y bf16 [T, H] (with w_pre),
+ * rstd_post / rstd_pre fp32 [T] (with w_post / w_pre; the backward reads them).
+ * T == 0 is a no-op. Errors: INVALID_ARG. */
+nf4moe_status_t nf4moe_block_norm_forward(const nf4moe_block_norm_t *norm, const void *x, const uint16_t *f, int64_t T,
+                                          void *x_new, uint16_t *y, float *rstd_post, float *rstd_pre, void *stream);
+
+/* nf4moe_block_norm_workspace_bytes -- workspace of the backward (0 for T < 1). */
+size_t nf4moe_block_norm_workspace_bytes(int32_t H, int64_t T);
+
+/* nf4moe_block_norm_backward -- gradients of the forward from dx_new (of x', in
+ * x_dtype; NULL: zero) and dy (of y, bf16; with w_pre), with what the forward
+ * read and returned (x_new: the stored x'; without f, x):
+ *   dx in x_dtype; df bf16 (with f); dgate fp32 in the gate's shape; dw_post,
+ *   dw_pre fp32 [H]. Sums over rows are added in a fixed order (the same bits on
+ *   every run). T == 0 writes zeros to dw_post, dw_pre and a per-channel dgate.
+ * Errors: INVALID_ARG, WORKSPACE. */
+nf4moe_status_t nf4moe_block_norm_backward(const nf4moe_block_norm_t *norm, const void *dx_new, const uint16_t *dy,
+                                           const void *x_new, const uint16_t *f, const float *rstd_post,
+                                           const float *rstd_pre, int64_t T, void *dx, uint16_t *df, float *dgate,
+                                           float *dw_post, float *dw_pre, void *ws, size_t ws_bytes, void *stream);
+
 /* nf4moe_stream_read -- a measurement aid, not part of the layer: one launch
  * that reads `bytes` bytes of `buf` (device, 16-byte aligned, bytes a positive
  * multiple of 16) once with 16-byte loads, loads_per_thread (1, 2, 4, 8 or 16)
