@@ -90,6 +90,12 @@ def lib() -> ctypes.CDLL:
         "nf4moe_block_norm_forward": [vp, vp, vp, i64, vp, vp, vp, vp, vp],
         "nf4moe_block_norm_workspace_bytes": [i32, i64],
         "nf4moe_block_norm_backward": [vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp],
+        "nf4moe_adapter_plan_bytes": [i32, i32],
+        "nf4moe_adapter_plan": [vp, i32, i32, vp, sz, vp],
+        "nf4moe_adapter_workspace_bytes": [vp, i32, i32],
+        "nf4moe_adapter_forward": [vp, vp, i32, vp, vp, vp, sz, i32, vp, vp, ctypes.c_int, vp, vp, sz, vp],
+        "nf4moe_adapter_backward": [vp, vp, ctypes.c_int, vp, vp, i32, vp, vp, vp, vp, sz, i32, vp, vp,
+                                    ctypes.c_int, vp, vp, vp, sz, vp],
         "nf4moe_codebook": [ctypes.c_int, ctypes.POINTER(ctypes.c_float)],
         "nf4moe_auto_path": [ctypes.c_int, i64, i64],
         "nf4moe_stream_read_sink_words": [i64, i32],
@@ -105,7 +111,8 @@ def lib() -> ctypes.CDLL:
         fn.argtypes = args
         fn.restype = ctypes.c_int
     for name in ("nf4moe_route_workspace_bytes", "nf4moe_gemm_workspace_bytes", "nf4moe_workspace_bytes",
-                 "nf4moe_router_workspace_bytes", "nf4moe_block_norm_workspace_bytes"):
+                 "nf4moe_router_workspace_bytes", "nf4moe_block_norm_workspace_bytes",
+                 "nf4moe_adapter_plan_bytes", "nf4moe_adapter_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_size_t
     L.nf4moe_stream_read_sink_words.restype = ctypes.c_int64
     L.nf4moe_mfma_peak_flops.restype = ctypes.c_int64
@@ -542,6 +549,6 @@ def moe_forward(layer: MoELayer, x, return_routing: bool = False):
 
 
 # fine-tuning and multi-adapter serving around the frozen 4-bit layer
-from .train import (CKPT_MXFP8, CKPT_MXINT8, GATE_IDENTITY, GATE_SIGMOID, GATE_TANH, Ckpt8,  # noqa: E402
-                    block_norm_backward, block_norm_forward, ckpt8_dequantize, ckpt8_quantize, glu_backward,
-                    glu_forward)
+from .train import (CKPT_MXFP8, CKPT_MXINT8, GATE_IDENTITY, GATE_SIGMOID, GATE_TANH, AdapterPlan,  # noqa: E402
+                    Ckpt8, adapter_backward, adapter_forward, adapter_plan, block_norm_backward,
+                    block_norm_forward, ckpt8_dequantize, ckpt8_quantize, glu_backward, glu_forward)

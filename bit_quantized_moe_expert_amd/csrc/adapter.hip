@@ -1,0 +1,691 @@
+// Low-rank adapters of many requests or experts beside a shared projection.
+//
+//   t[r] = A_l x[m(r)],  out[r] = base[r] + s_l B_l t[r]          (l = ids[r])
+//   u[r] = s_l B_l^T dy[r],  dx[r] = dx_base[r] + A_l^T u[r]
+//   dA_l = sum_r u[r] x[m(r)]^T,  dB_l = s_l sum_r dy[r] t[r]^T
+//
+// The rank is small (8..128), so every product is bound by the traffic of the
+// wide operands (x, base / out, dy, dx), and the matrix cores have room to spare.
+// That room buys exactness: t and u stay fp32, and enter the second product as
+// the exact sum of three bf16 parts (8 + 8 + 8 significant bits by truncation),
+// so nothing but the fp32 additions is rounded before the output.
+//
+// Rows are grouped by adapter once per call (or once per batch, by the caller): a
+// stable counting sort, then a table of tiles of up to 64 rows of one adapter.
+#include "ckpt8.h"
+#include "internal.h"
+#include "train.h"
+
+namespace nf4moe {
+
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ inline f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
+  // 16x16x32: a holds row lane & 15, b column lane & 15, both k = 8 (lane >> 4) ..;
+  // c holds column lane & 15, rows 4 (lane >> 4) ..
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Eight fp32 values as three bf16 parts whose sum is the value exactly: each part
+// takes the next 8 significant bits by truncation (so a finite value never
+// becomes infinite). An infinity or NaN is its own first part, the others 0.
+__device__ inline void split3(const float (&v)[8], uint4 &hi, uint4 &mid, uint4 &lo) {
+  uint32_t h[8], m[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t b = __float_as_uint(v[i]);
+    const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+    if (!finite && (b & 0x7fffffu)) b |= 0x400000u;  // a NaN whose payload is in the low half stays one
+    h[i] = b;
+    const float r = finite ? v[i] - __uint_as_float(b & 0xffff0000u) : 0.0f;
+    m[i] = __float_as_uint(r);
+    l[i] = __float_as_uint(r - __uint_as_float(m[i] & 0xffff0000u));
+  }
+  auto top = [](uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); };  // high halves of a, b
+  hi = make_uint4(top(h[0], h[1]), top(h[2], h[3]), top(h[4], h[5]), top(h[6], h[7]));
+  mid = make_uint4(top(m[0], m[1]), top(m[2], m[3]), top(m[4], m[5]), top(m[6], m[7]));
+  lo = make_uint4(top(l[0], l[1]), top(l[2], l[3]), top(l[4], l[5]), top(l[6], l[7]));
+}
+
+// ------------------------------------------------------------------ grouping
+constexpr int kPlanThreads = 1024;
+
+// Rows of one plan workgroup: 1024, or more where (workgroups) x (bins) would
+// exceed 64 K counters, which every workgroup reads.
+int plan_rows(int R, int L) {
+  const int64_t blocks = cdiv(R, kPlanThreads);
+  const int64_t per = cdiv(blocks * (L + 1), 65536);
+  return (int)(kPlanThreads * (per < 1 ? 1 : per));
+}
+
+__device__ inline int bin_of(int id, int L) { return id < 0 || id >= L ? L : id; }
+
+__global__ __launch_bounds__(kPlanThreads) void k_plan_hist(const int32_t *__restrict__ ids, int R, int L, int per,
+                                                            int32_t *__restrict__ hist) {
+  __shared__ int32_t cnt[kMaxAdapters + 1];
+  for (int b = threadIdx.x; b <= L; b += kPlanThreads) cnt[b] = 0;
+  __syncthreads();
+  const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
+  for (int r = r0 + (int)threadIdx.x; r < r1; r += kPlanThreads) atomicAdd(&cnt[bin_of(ids[r], L)], 1);
+  __syncthreads();
+  for (int b = threadIdx.x; b <= L; b += kPlanThreads) hist[(int64_t)blockIdx.x * (L + 1) + b] = cnt[b];
+}
+
+// Exclusive prefix of v over the workgroup's threads in order; total in *sum.
+__device__ inline int32_t block_prefix(int32_t v, int32_t *wsum, int32_t *sum) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t y = __shfl_up(x, d, kWave);
+    if (lane >= d) x += y;
+  }
+  if (lane == 63) wsum[wave] = x;
+  __syncthreads();
+  int32_t before = 0, all = 0;
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    const int32_t s = wsum[w];
+    if (w < wave) before += s;
+    all += s;
+  }
+  __syncthreads();
+  *sum = all;
+  return before + x - v;
+}
+
+// One workgroup per `per` rows. Each finds, for every bin, where its own rows of
+// that bin begin (all counters of the earlier workgroups and bins), then places
+// its rows in order, 1024 at a time: ranks inside a wave by ballots, and one
+// turn per wave for the running counters, so the order is stable. Workgroup 0
+// also writes the tile and chunk tables.
+__global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__restrict__ ids, int R, int L, int per,
+                                                               int groups, int chunk_rows, AdapterPlan p) {
+  __shared__ int32_t next[kMaxAdapters + 1];
+  __shared__ int32_t wsum[kPlanThreads / 64];
+  const int tid = threadIdx.x, nb = L + 1;
+  const int seg = (nb + kPlanThreads - 1) / kPlanThreads, b0 = tid * seg, b1 = min(nb, b0 + seg);  // this thread's bins
+  constexpr int kSeg = (kMaxAdapters + 1 + kPlanThreads - 1) / kPlanThreads;
+  int32_t total[kSeg], mine[kSeg];
+  if (groups == 1) {
+    for (int b = tid; b < nb; b += kPlanThreads) next[b] = 0;
+    __syncthreads();
+    for (int r = tid; r < R; r += kPlanThreads) atomicAdd(&next[bin_of(ids[r], L)], 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kSeg; ++i) {
+    total[i] = mine[i] = 0;
+    if (b0 + i >= b1) continue;
+    if (groups == 1) {
+      total[i] = next[b0 + i];
+    } else {
+      for (int g = 0; g < groups; ++g) {
+        const int32_t c = p.hist[(int64_t)g * nb + b0 + i];
+        total[i] += c;
+        if (g < (int)blockIdx.x) mine[i] += c;
+      }
+    }
+  }
+  int32_t rows = 0, sum;
+#pragma unroll
+  for (int i = 0; i < kSeg; ++i) rows += total[i];
+  int32_t off = block_prefix(rows, wsum, &sum);  // (its barriers also end the reads of next above)
+  int32_t first[kSeg];
+#pragma unroll
+  for (int i = 0; i < kSeg; ++i) {
+    first[i] = off;
+    if (b0 + i < b1) next[b0 + i] = off + mine[i];
+    off += total[i];
+  }
+  if (blockIdx.x == 0) {
+    int32_t nt = 0, nc = 0, ns = 0;
+#pragma unroll
+    for (int i = 0; i < kSeg; ++i) {
+      nt += (total[i] + kAdTile - 1) / kAdTile;
+      const int32_t c = b0 + i < L ? (total[i] + chunk_rows - 1) / chunk_rows : 0;
+      nc += c;
+      ns += c > 1 ? c : 0;
+    }
+    int32_t t_all, c_all, s_all;
+    int32_t t = block_prefix(nt, wsum, &t_all);
+    int32_t c = block_prefix(nc, wsum, &c_all);
+    int32_t s = block_prefix(ns, wsum, &s_all);
+    if (tid == 0) {
+      p.counts[0] = t_all;
+      p.counts[1] = c_all;
+    }
+#pragma unroll
+    for (int i = 0; i < kSeg; ++i) {
+      const int b = b0 + i;
+      if (b >= b1) continue;
+      for (int32_t r = 0; r < total[i]; r += kAdTile)
+        p.tiles[t++] = make_int4(b < L ? b : -1, first[i] + r, min(kAdTile, total[i] - r), 0);
+      if (b >= L) continue;
+      const int32_t n = (total[i] + chunk_rows - 1) / chunk_rows;
+      p.chunks_of[b] = make_int2(n, s);
+      for (int32_t k = 0; k < n; ++k)
+        p.chunks[c++] = make_int4(b, first[i] + k * chunk_rows, min(chunk_rows, total[i] - k * chunk_rows), n > 1 ? s + k : -1);
+      if (n > 1) s += n;
+    }
+  }
+  __syncthreads();
+  const int lane = tid & 63, wave = tid >> 6;
+  const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
+  for (int base = r0; base < r1; base += kPlanThreads) {
+    const int r = base + tid;
+    const bool live = r < r1;
+    const int b = live ? bin_of(ids[r], L) : -1;
+    uint64_t todo = __ballot(live), same = 0;
+    while (todo) {
+      const int lead = __builtin_ctzll(todo);
+      const int lb = __shfl(b, lead, kWave);
+      const uint64_t m = __ballot(live && b == lb);
+      if (b == lb) same = m;
+      todo &= ~m;
+    }
+    const int rank = __popcll(same & lanemask_lt());
+    const int lead = same ? __builtin_ctzll(same) : 0;
+    int32_t at = 0;
+    for (int w = 0; w < kPlanThreads / 64; ++w) {
+      if (wave == w && live && lane == lead) {
+        at = next[b];
+        next[b] = at + __popcll(same);
+      }
+      __syncthreads();
+    }
+    at = __shfl(at, lead, kWave);
+    if (live) p.order[at + rank] = r;
+  }
+}
+
+// ------------------------------------------------------------------ shrink
+// One workgroup per tile; its four waves take every fourth 64-wide step of K for
+// all the tile's rows, so each adapter row is read once per workgroup, and add
+// their sums in order through LDS. A lane's two 16-byte pieces of a step are
+// neighbours (k = 16 q .. + 15), the same places in both operands, so a row's
+// step is one whole 128-byte line.
+template <int RT>
+__global__ __launch_bounds__(256) void k_shrink(ShrinkArgs p) {
+  constexpr int kPad = RT * 16 + 4;
+  __shared__ __attribute__((aligned(16))) float red[kAdTile][kPad];
+  if ((int)blockIdx.x >= p.plan.counts[0]) return;
+  const int4 tile = p.plan.tiles[blockIdx.x];
+  const int l = tile.x, n = tile.z, rank = p.rank;
+  const int32_t *order = p.plan.order + tile.y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  if (l >= 0) {
+    const uint16_t *xrow[4], *wrow[RT];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      int r = order[min(16 * s + l16, n - 1)];
+      if (p.row_of) r = min(max(p.row_of[r], 0), p.x_rows - 1);
+      xrow[s] = p.x + (int64_t)r * p.K;
+    }
+#pragma unroll
+    for (int j = 0; j < RT; ++j) wrow[j] = p.W + ((int64_t)l * rank + min(16 * j + l16, rank - 1)) * p.K;
+    f32x4_t acc[4][RT] = {};
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int k0 = 64 * wave; k0 < p.K; k0 += 256) {
+      const int k = k0 + 16 * q;
+      const bool ok0 = k < p.K, ok1 = k + 8 < p.K;
+      uint4 w0[RT], w1[RT];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        w0[j] = ok0 ? load16(wrow[j] + k) : zero;
+        w1[j] = ok1 ? load16(wrow[j] + k + 8) : zero;
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (16 * s >= n) break;  // the same for the whole workgroup
+        const uint4 x0 = ok0 ? load16(xrow[s] + k) : zero;
+        const uint4 x1 = ok1 ? load16(xrow[s] + k + 8) : zero;
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          acc[s][j] = mfma16(w0[j], x0, acc[s][j]);
+          acc[s][j] = mfma16(w1[j], x1, acc[s][j]);
+        }
+      }
+    }
+    // lane: row 16 s + l16, ranks 16 j + 4 q ..
+    for (int w = 0; w < 4; ++w) {
+      if (wave == w) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int j = 0; j < RT; ++j) {
+            f32x4_t *d = reinterpret_cast<f32x4_t *>(&red[16 * s + l16][16 * j + 4 * q]);
+            *d = w == 0 ? acc[s][j] : *d + acc[s][j];
+          }
+      }
+      lds_barrier();
+    }
+  }
+  const float m = l >= 0 && p.scale ? p.scale[l] : 1.0f;
+  const int per = rank / 4;
+  for (int i = tid; i < n * per; i += 256) {
+    const int row = i / per, j = 4 * (i % per);
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (l >= 0) v = *reinterpret_cast<const f32x4_t *>(&red[row][j]) * m;
+    *reinterpret_cast<f32x4_t *>(p.out + (int64_t)order[row] * rank + j) = v;
+  }
+}
+
+// ------------------------------------------------------------------ expand
+// One workgroup per tile and 256 columns, 64 columns a wave. The product is taken
+// transposed (columns as the matrix rows), so a lane ends with neighbouring
+// columns of one row: 8 (bf16, by pairing two column blocks) or 4 (fp32), 64
+// contiguous bytes of a row per access, and base, product and out meet in
+// registers. t's tile is scaled and split into three bf16 parts once, in LDS; the
+// 32 k places of a matrix instruction hold 32 ranks of one part, or for rank 8 all
+// three parts at once and for rank 16 two (PACK).
+template <int PACK, bool BF>
+__global__ __launch_bounds__(256) void k_expand(ExpandArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t parts[];
+  if ((int)blockIdx.x >= p.plan.counts[0]) return;
+  const int4 tile = p.plan.tiles[blockIdx.x];
+  const int l = tile.x, n = tile.z, rank = p.rank, nr8 = rank / 8;
+  if (l < 0 && p.base == p.out) return;  // nothing to add
+  const int32_t *order = p.plan.order + tile.y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  const int nb = (nr8 + 3) / 4;                                   // blocks of 32 ranks (PACK 0)
+  const int steps = PACK == 1 ? 1 : PACK == 2 ? 2 : 3 * nb;
+  const int pstride = PACK == 1 ? 8 : PACK == 2 ? 16 : 32 * nb;   // elements from part to part
+  const int rstride = steps * 32 + 8;                             // elements from row to row
+  f32x4_t acc[4][4] = {};                                         // [16 rows][16 columns]
+  const int c0 = blockIdx.y * 256 + wave * 64;
+  if (l >= 0) {
+    const float m = p.scale ? p.scale[l] : 1.0f;
+    const int g8 = PACK == 0 ? 4 * nb : nr8;                      // groups of 8 places per part
+    for (int i = tid; i < kAdTile * g8; i += 256) {
+      const int row = i / g8, r8 = i % g8;
+      float v[8] = {};
+      if (row < n && r8 < nr8) {
+        load_elems8<false>(p.t, (int64_t)order[row] * rank + 8 * r8, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= m;
+      }
+      uint4 hi, mid, lo;
+      split3(v, hi, mid, lo);
+      uint16_t *d = parts + row * rstride + 8 * r8;
+      *reinterpret_cast<uint4 *>(d) = hi;
+      *reinterpret_cast<uint4 *>(d + pstride) = mid;
+      *reinterpret_cast<uint4 *>(d + 2 * pstride) = lo;
+      if (PACK != 0 && r8 == 0) {
+        *reinterpret_cast<uint4 *>(parts + row * rstride + 3 * pstride) = make_uint4(0, 0, 0, 0);
+        if (PACK == 2) *reinterpret_cast<uint4 *>(parts + row * rstride + 3 * pstride + 8) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    lds_barrier();
+    const uint16_t *wrow[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = BF ? 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3) : 16 * j + l16;
+      wrow[j] = p.W + ((int64_t)l * p.N + min(c0 + c, p.N - 1)) * rank;
+    }
+    const int outer = PACK == 0 ? nb : steps;
+    for (int o = 0; o < outer; ++o) {
+      // the ranks of this lane's 8 places; places of no part hold zeros
+      const int g = 4 * o + q;
+      const int r8 = PACK == 1 ? 0 : PACK == 2 ? (g & 1) : g;
+      const bool ok = PACK == 1 ? q < 3 : PACK == 2 ? g < 6 : r8 < nr8;
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = ok ? load16(wrow[j] + 8 * r8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int part = 0; part < (PACK == 0 ? 3 : 1); ++part) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          if (16 * s >= n) break;
+          const uint4 t = *reinterpret_cast<const uint4 *>(parts + (16 * s + l16) * rstride + part * pstride + 32 * o + 8 * q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t, acc[s][j]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int i = 16 * s + l16;
+    if (i >= n) continue;
+    const int64_t at = (int64_t)order[i] * p.N;
+    if constexpr (BF) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0 + 32 * h + 8 * q;
+        if (c >= p.N) continue;
+        float v[8] = {};
+        if (p.base) load_elems8<true>(p.base, at + c, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] += acc[s][2 * h][k];
+          v[4 + k] += acc[s][2 * h + 1][k];
+        }
+        store_elems8<true>(p.out, at + c, v);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + 16 * j + 4 * q;
+        if (c >= p.N) continue;
+        uint4 b = make_uint4(0, 0, 0, 0);
+        if (p.base) b = load16(reinterpret_cast<const float *>(p.base) + at + c);
+        store16(reinterpret_cast<float *>(p.out) + at + c,
+                make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[s][j][0]), __float_as_uint(__uint_as_float(b.y) + acc[s][j][1]),
+                           __float_as_uint(__uint_as_float(b.z) + acc[s][j][2]), __float_as_uint(__uint_as_float(b.w) + acc[s][j][3])));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ weight gradients
+// Sums over rows: the contraction runs along the rows, across the storage order of
+// both operands. A lane loads 8 neighbouring columns of 8 rows and turns the 8 x 8
+// block in registers (one v_perm_b32 per pair of values), which gives it, for each
+// of its 8 columns, 8 consecutive rows: the matrix operand, with no LDS. 32 rows and
+// 128 columns a wave and step. p's rows are split into three bf16 parts in
+// registers. An adapter with one chunk is written straight out; the chunks of
+// others go to partial sums that k_rowgrad_join adds in order.
+template <int SRC, int RT>
+__global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p) {
+  if ((int)blockIdx.x >= p.plan.counts[1]) return;
+  const int4 chunk = p.plan.chunks[blockIdx.x];
+  const int l = chunk.x, n = chunk.z;
+  const int32_t *order = p.plan.order + chunk.y;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int l16 = lane & 15, q = lane >> 4;
+  const int cw = blockIdx.y * 512 + wave * 128;
+  if (cw >= p.C) return;
+  const int j0 = blockIdx.z * (16 * RT);
+  const int c = min(cw + 8 * l16, p.C - 8);  // past the end: a valid place, not stored
+  f32x4_t acc[RT][8] = {};
+  for (int r0 = 0; r0 < n; r0 += 32) {
+    int32_t row[8];
+    uint32_t blk[4][8];  // rows (2 i, 2 i + 1) of column k as one word: [i][k]
+    uint4 raw[8];
+    uint32_t sc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) row[i] = order[min(r0 + 8 * q + i, n - 1)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int r = row[i];
+      if (p.row_of) r = min(max(p.row_of[r], 0), p.v_rows - 1);
+      const int64_t at = (int64_t)r * p.C + c;
+      if constexpr (SRC == SRC_BF16) {
+        raw[i] = load16(reinterpret_cast<const uint16_t *>(p.v) + at);
+      } else {
+        const uint2 w = load8(reinterpret_cast<const uint8_t *>(p.v) + at);
+        raw[i] = make_uint4(w.x, w.y, 0, 0);
+        sc[i] = p.v_scale[at >> 5];
+      }
+    }
+    if (r0 + 32 > n) {  // places past the chunk hold zeros in both operands (0 x infinity is not 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r0 + 8 * q + i >= n) {
+          raw[i] = make_uint4(0, 0, 0, 0);
+          sc[i] = 0;
+        }
+    }
+    uint4 a[RT][3];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int j = j0 + 16 * t + l16;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = r0 + 8 * q + i < n && j < p.rank ? p.p[(int64_t)row[i] * p.rank + j] : 0.0f;
+      split3(v, a[t][0], a[t][1], a[t][2]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (SRC == SRC_BF16) {
+        const uint32_t u[4] = {raw[2 * i].x, raw[2 * i].y, raw[2 * i].z, raw[2 * i].w};
+        const uint32_t w[4] = {raw[2 * i + 1].x, raw[2 * i + 1].y, raw[2 * i + 1].z, raw[2 * i + 1].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          blk[i][2 * k] = __builtin_amdgcn_perm(w[k], u[k], 0x05040100u);
+          blk[i][2 * k + 1] = __builtin_amdgcn_perm(w[k], u[k], 0x07060302u);
+        }
+      } else {
+        constexpr int F = SRC - SRC_MXINT8;
+        float x[8], y[8];
+        ckpt8_decode8<F>(make_uint2(raw[2 * i].x, raw[2 * i].y), sc[2 * i], x);
+        ckpt8_decode8<F>(make_uint2(raw[2 * i + 1].x, raw[2 * i + 1].y), sc[2 * i + 1], y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) blk[i][k] = f32x2_to_bf16x2_rne(x[k], y[k]);  // exact
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 b = make_uint4(blk[0][k], blk[1][k], blk[2][k], blk[3][k]);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int part = 0; part < 3; ++part) acc[t][k] = mfma16(a[t][part], b, acc[t][k]);
+    }
+  }
+  // lane: columns cw + 8 l16 + k, ranks j0 + 16 t + 4 q ..
+  if (cw + 8 * l16 >= p.C) return;
+  const int64_t size = (int64_t)p.rank * p.C;
+  float *out = chunk.w < 0 ? p.out + l * size : p.partial + chunk.w * size;
+  const float m = p.scale ? p.scale[l] : 1.0f;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int j = j0 + 16 * t + 4 * q;
+    if (j >= p.rank) continue;
+    if (p.transposed) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) *reinterpret_cast<f32x4_t *>(out + (int64_t)(c + k) * p.rank + j) = acc[t][k] * m;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = acc[t][k][i] * m;
+        store_elems8<false>(out, (int64_t)(j + i) * p.C + c, v);
+      }
+    }
+  }
+}
+
+// The chunks of an adapter, added in order; zeros for an adapter without rows.
+__global__ __launch_bounds__(256) void k_rowgrad_join(const int2 *__restrict__ chunks_of, const float *__restrict__ partial,
+                                                      int64_t size, float *__restrict__ out) {
+  const int2 c = chunks_of[blockIdx.y];
+  if (c.x == 1) return;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= size) return;
+  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = 0; k < c.x; ++k) s += *reinterpret_cast<const f32x4_t *>(partial + (c.y + k) * size + i);
+  *reinterpret_cast<f32x4_t *>(out + blockIdx.y * size + i) = s;
+}
+
+__global__ __launch_bounds__(256) void k_zero_f32(float *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
+}
+
+__global__ __launch_bounds__(256) void k_transpose_bf16(const uint16_t *__restrict__ in, uint16_t *__restrict__ out, int P,
+                                                        int Q) {
+  __shared__ uint16_t tile[64][66];
+  const int64_t base = (int64_t)blockIdx.z * P * Q;
+  const int p0 = blockIdx.y * 64, q0 = blockIdx.x * 64;
+  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+  for (int i = y; i < 64; i += 4)
+    if (p0 + i < P && q0 + x < Q) tile[i][x] = in[base + (int64_t)(p0 + i) * Q + q0 + x];
+  __syncthreads();
+  for (int i = y; i < 64; i += 4)
+    if (q0 + i < Q && p0 + x < P) out[base + (int64_t)(q0 + i) * P + p0 + x] = tile[x][i];
+}
+
+// ------------------------------------------------------------------ few rows
+// One launch, no plan: a workgroup per row and 256 columns. Its four waves take
+// the ranks in turn (a dot product over K each), then every thread one column.
+// Each workgroup of a row repeats the row's shrink: A_l comes from L2 after the
+// first, and a second launch would cost more.
+template <bool BF>
+__global__ __launch_bounds__(256) void k_adapter_rows(AdapterRowsArgs p) {
+  __shared__ float ts[kMaxRank];
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l = p.ids[r], rank = p.rank;
+  const bool has = l >= 0 && l < p.L;
+  const int c = blockIdx.y * 256 + tid;
+  const int64_t at = (int64_t)r * p.N + c;
+  float b = 0.0f;
+  if (p.base && c < p.N)
+    b = BF ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p.base)[at]) : reinterpret_cast<const float *>(p.base)[at];
+  if (has) {
+    int xr = r;
+    if (p.row_of) xr = min(max(p.row_of[r], 0), p.x_rows - 1);
+    const uint16_t *x = p.x + (int64_t)xr * p.K;
+    const uint16_t *A = p.A + (int64_t)l * rank * p.K;
+    for (int j = wave; j < rank; j += 8) {  // two ranks at a time: j and j + 4 (rank is a multiple of 8)
+      float s0 = 0.0f, s1 = 0.0f;
+      for (int k = 8 * lane; k < p.K; k += 512) {
+        float xv[8], a0[8], a1[8];
+        load_elems8<true>(x, k, xv);
+        load_elems8<true>(A, (int64_t)j * p.K + k, a0);
+        load_elems8<true>(A, (int64_t)(j + 4) * p.K + k, a1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s0 += xv[i] * a0[i];
+          s1 += xv[i] * a1[i];
+        }
+      }
+      s0 = wave_sum(s0);
+      s1 = wave_sum(s1);
+      if (lane == 0) ts[j] = s0, ts[j + 4] = s1;
+    }
+  }
+  lds_barrier();
+  if (p.t && blockIdx.y == 0)
+    for (int j = tid; j < rank; j += 256) p.t[(int64_t)r * rank + j] = has ? ts[j] : 0.0f;
+  if (c >= p.N) return;
+  if (has) {
+    const uint16_t *w = p.B + ((int64_t)l * p.N + c) * rank;
+    float s = 0.0f;
+    for (int j = 0; j < rank; j += 8) {
+      float v[8];
+      load_elems8<true>(w, j, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i] * ts[j + i];
+    }
+    b += p.scale ? p.scale[l] * s : s;
+  }
+  if (BF) reinterpret_cast<uint16_t *>(p.out)[at] = (uint16_t)f32_to_bf16_rne(b);
+  else reinterpret_cast<float *>(p.out)[at] = b;
+}
+
+}  // namespace
+
+// Rows of a gradient chunk: about 64 chunks' worth of rows, 64 to 2048.
+int adapter_chunk_rows(int R) {
+  const int64_t c = cdiv(cdiv(R, 64), kAdTile) * kAdTile;
+  return (int)(c < kAdTile ? kAdTile : c > 2048 ? 2048 : c);
+}
+
+size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p) {
+  const int bins = R < L + 1 ? R : L + 1;
+  const int64_t ch = adapter_chunk_rows(R);
+  AdapterPlan q;
+  q.max_tiles = (int)cdiv(R, kAdTile) + bins;
+  q.max_chunks = (int)cdiv(R, ch) + bins;
+  // an adapter of n > 1 chunks has more than (n - 1) ch rows, so n <= 2 rows / ch
+  q.max_slots = (int)(2 * cdiv(R, ch));
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    char *at = base ? (char *)base + off : nullptr;
+    off = align_up(off + bytes);
+    return (void *)at;
+  };
+  q.order = (int32_t *)take(sizeof(int32_t) * (size_t)R);
+  q.counts = (int32_t *)take(sizeof(int32_t) * 2);
+  q.chunks_of = (int2 *)take(sizeof(int2) * (size_t)L);
+  q.tiles = (int4 *)take(sizeof(int4) * (size_t)q.max_tiles);
+  q.chunks = (int4 *)take(sizeof(int4) * (size_t)q.max_chunks);
+  q.hist = (int32_t *)take(sizeof(int32_t) * (size_t)cdiv(R, plan_rows(R, L)) * (L + 1));
+  if (p) *p = q;
+  return off;
+}
+
+hipError_t launch_adapter_plan(const int32_t *ids, int R, int L, const AdapterPlan &p, hipStream_t s) {
+  const int per = plan_rows(R, L);
+  const int groups = (int)cdiv(R, per);
+  if (groups > 1) hipLaunchKernelGGL(k_plan_hist, dim3(groups), dim3(kPlanThreads), 0, s, ids, R, L, per, p.hist);
+  hipLaunchKernelGGL(k_plan_scatter, dim3(groups), dim3(kPlanThreads), 0, s, ids, R, L, per, groups, adapter_chunk_rows(R), p);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_shrink(const ShrinkArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)a.plan.max_tiles), block(256);
+  if (a.rank <= 16) hipLaunchKernelGGL(k_shrink<1>, grid, block, 0, s, a);
+  else if (a.rank <= 32) hipLaunchKernelGGL(k_shrink<2>, grid, block, 0, s, a);
+  else if (a.rank <= 64) hipLaunchKernelGGL(k_shrink<4>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(k_shrink<8>, grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_expand(const ExpandArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)a.plan.max_tiles, (unsigned)cdiv(a.N, 256)), block(256);
+  const int pack = a.rank == 8 ? 1 : a.rank == 16 ? 2 : 0;
+  const int steps = pack ? pack : 3 * (int)cdiv(a.rank, 32);
+  const size_t lds = (size_t)kAdTile * (steps * 32 + 8) * sizeof(uint16_t);  // at most 50 KB
+  if (pack == 1) {
+    if (a.bf16) hipLaunchKernelGGL((k_expand<1, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_expand<1, false>), grid, block, lds, s, a);
+  } else if (pack == 2) {
+    if (a.bf16) hipLaunchKernelGGL((k_expand<2, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_expand<2, false>), grid, block, lds, s, a);
+  } else {
+    if (a.bf16) hipLaunchKernelGGL((k_expand<0, true>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((k_expand<0, false>), grid, block, lds, s, a);
+  }
+  return hipGetLastError();
+}
+
+template <int SRC>
+static void rowgrad_src(const RowGradArgs &a, hipStream_t s) {
+  const dim3 block(256);
+  const unsigned gx = (unsigned)a.plan.max_chunks, gy = (unsigned)cdiv(a.C, 512);
+  if (a.rank <= 16) hipLaunchKernelGGL((k_rowgrad<SRC, 1>), dim3(gx, gy, 1), block, 0, s, a);
+  else if (a.rank <= 32) hipLaunchKernelGGL((k_rowgrad<SRC, 2>), dim3(gx, gy, 1), block, 0, s, a);
+  else hipLaunchKernelGGL((k_rowgrad<SRC, 4>), dim3(gx, gy, (unsigned)cdiv(a.rank, 64)), block, 0, s, a);
+}
+
+hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s) {
+  if (a.src == SRC_BF16) rowgrad_src<SRC_BF16>(a, s);
+  else if (a.src == SRC_MXINT8) rowgrad_src<SRC_MXINT8>(a, s);
+  else rowgrad_src<SRC_MXFP8>(a, s);
+  const int64_t size = (int64_t)a.rank * a.C;  // a multiple of 64
+  hipLaunchKernelGGL(k_rowgrad_join, dim3((unsigned)cdiv(size, 1024), (unsigned)a.L), dim3(256), 0, s, a.plan.chunks_of,
+                     a.partial, size, a.out);
+  return hipGetLastError();
+}
+
+hipError_t launch_fill_f32_zero(float *p, int64_t n, hipStream_t s) {
+  const int64_t g = cdiv(n, 256);
+  hipLaunchKernelGGL(k_zero_f32, dim3((unsigned)(g < 4096 ? g : 4096)), dim3(256), 0, s, p, n);
+  return hipGetLastError();
+}
+
+hipError_t launch_transpose_bf16(const uint16_t *in, uint16_t *out, int L, int P, int Q, hipStream_t s) {
+  hipLaunchKernelGGL(k_transpose_bf16, dim3((unsigned)cdiv(Q, 64), (unsigned)cdiv(P, 64), (unsigned)L), dim3(256), 0, s, in,
+                     out, P, Q);
+  return hipGetLastError();
+}
+
+// Up to 32 rows and 64 KB of A per workgroup and row.
+bool adapter_rows_supported(int R, int K, int rank) { return R <= 32 && (int64_t)K * rank <= 65536; }
+
+hipError_t launch_adapter_rows(const AdapterRowsArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)a.R, (unsigned)cdiv(a.N, 256)), block(256);
+  if (a.bf16) hipLaunchKernelGGL(k_adapter_rows<true>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(k_adapter_rows<false>, grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace nf4moe

@@ -70,6 +70,60 @@ NormArgs norm_args(const nf4moe_block_norm_t &n, int64_t T) {
   return a;
 }
 
+nf4moe_status_t check_adapters(const nf4moe_adapters_t *a, int64_t R) {
+  if (!a) return fail(NF4MOE_ERR_INVALID_ARG, "adapters is NULL");
+  if (a->L < 1 || a->L > kMaxAdapters) return fail(NF4MOE_ERR_INVALID_ARG, "L=%d outside 1..%d", a->L, kMaxAdapters);
+  if (a->rank < 8 || a->rank > kMaxRank || a->rank % 8)
+    return fail(NF4MOE_ERR_INVALID_ARG, "rank=%d must be a multiple of 8 in 8..%d", a->rank, kMaxRank);
+  if (a->K < 8 || a->K % 8 || a->K > (1 << 20) || a->N < 8 || a->N % 8 || a->N > (1 << 20))
+    return fail(NF4MOE_ERR_INVALID_ARG, "K=%d and N=%d must be multiples of 8 in 8..2^20", a->K, a->N);
+  if (R < 0 || R > (1 << 30)) return fail(NF4MOE_ERR_INVALID_ARG, "R=%lld outside 0..2^30", (long long)R);
+  if (R > 0 && (!a->A || !a->B)) return fail(NF4MOE_ERR_INVALID_ARG, "adapter weight pointer is NULL");
+  if (!aligned(a->A, 2) || !aligned(a->B, 2) || !aligned(a->scale, 4))
+    return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  return NF4MOE_OK;
+}
+
+// Bump allocator over the caller's workspace (sizes alone with a null base).
+struct Bump {
+  char *base;
+  size_t off = 0;
+  template <class T>
+  T *take(size_t count) {
+    T *p = base ? (T *)(base + off) : nullptr;
+    off = align_up(off + count * sizeof(T));
+    return p;
+  }
+};
+
+struct AdapterCarve {
+  void *plan;
+  float *t;                     // forward: [R, rank]
+  float *u;                     // backward
+  uint16_t *At, *Bt;            // [L, K, rank], [L, rank, N]
+  float *partial;
+  size_t bytes;
+};
+
+// The calls' scratch: with `plan` given by the caller its part is left out; the
+// rest has one size whatever outputs are asked for.
+AdapterCarve carve_adapter(void *ws, const nf4moe_adapters_t &a, int R, bool backward) {
+  AdapterCarve c = {};
+  Bump b{(char *)ws};
+  AdapterPlan lay;
+  c.plan = b.take<char>(adapter_plan_layout(R, a.L, nullptr, &lay));
+  if (!backward) {
+    c.t = b.take<float>((size_t)R * a.rank);
+  } else {
+    c.u = b.take<float>((size_t)R * a.rank);
+    c.At = b.take<uint16_t>((size_t)a.L * a.K * a.rank);
+    c.Bt = b.take<uint16_t>((size_t)a.L * a.N * a.rank);
+    c.partial = b.take<float>((size_t)lay.max_slots * a.rank * (a.K > a.N ? a.K : a.N));
+  }
+  c.bytes = b.off;
+  return c;
+}
+
 }  // namespace
 
 extern "C" {
@@ -193,6 +247,138 @@ nf4moe_status_t nf4moe_block_norm_backward(const nf4moe_block_norm_t *norm, cons
   a.dw_post = n.w_post ? dw_post : nullptr, a.dw_pre = n.w_pre ? dw_pre : nullptr;
   a.partial = (float *)ws, a.groups = norm_backward_groups(T, n.H);
   return hip_status(launch_norm_backward(a, s), "norm backward launch");
+}
+
+size_t nf4moe_adapter_plan_bytes(int32_t R, int32_t L) {
+  if (R < 1 || R > (1 << 30) || L < 1 || L > kMaxAdapters) return 0;
+  return adapter_plan_layout(R, L, nullptr, nullptr);
+}
+
+nf4moe_status_t nf4moe_adapter_plan(const int32_t *ids, int32_t R, int32_t L, void *plan, size_t plan_bytes, void *stream) {
+  if (L < 1 || L > kMaxAdapters) return fail(NF4MOE_ERR_INVALID_ARG, "L=%d outside 1..%d", L, kMaxAdapters);
+  if (R < 0 || R > (1 << 30)) return fail(NF4MOE_ERR_INVALID_ARG, "R=%d outside 0..2^30", R);
+  if (R == 0) return NF4MOE_OK;
+  if (!ids) return fail(NF4MOE_ERR_INVALID_ARG, "ids is NULL");
+  if (!aligned(ids, 4)) return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  const size_t need = nf4moe_adapter_plan_bytes(R, L);
+  if (!plan || plan_bytes < need) return fail(NF4MOE_ERR_WORKSPACE, "plan %zu bytes < %zu required", plan_bytes, need);
+  if (!aligned(plan, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "plan must be 256-byte aligned");
+  AdapterPlan p;
+  adapter_plan_layout(R, L, plan, &p);
+  return hip_status(launch_adapter_plan(ids, R, L, p, (hipStream_t)stream), "adapter plan launch");
+}
+
+size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, int32_t backward) {
+  if (!ad || R < 1 || R > (1 << 30) || ad->L < 1 || ad->L > kMaxAdapters || ad->rank < 8 || ad->rank > kMaxRank ||
+      ad->K < 8 || ad->N < 8)
+    return 0;
+  return carve_adapter(nullptr, *ad, R, backward != 0).bytes;
+}
+
+// Rows, gather, ids and plan, as both directions take them.
+static nf4moe_status_t check_adapter_rows(int32_t R, int32_t x_rows, const int32_t *x_row_of, const int32_t *ids,
+                                          const void *plan, size_t plan_bytes, int32_t L) {
+  if (x_rows < 1 || (!x_row_of && x_rows < R))
+    return fail(NF4MOE_ERR_INVALID_ARG, "x_rows=%d too small for R=%d%s", x_rows, R, x_row_of ? "" : " without a gather");
+  if (!ids) return fail(NF4MOE_ERR_INVALID_ARG, "ids is NULL");
+  if (!aligned(ids, 4) || !aligned(x_row_of, 4)) return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  if (plan) {
+    if (plan_bytes < nf4moe_adapter_plan_bytes(R, L))
+      return fail(NF4MOE_ERR_WORKSPACE, "plan %zu bytes < %zu required", plan_bytes, nf4moe_adapter_plan_bytes(R, L));
+    if (!aligned(plan, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "plan must be 256-byte aligned");
+  }
+  return NF4MOE_OK;
+}
+
+nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16_t *x, int32_t x_rows,
+                                       const int32_t *x_row_of, const int32_t *ids, const void *plan, size_t plan_bytes,
+                                       int32_t R, const void *base, void *out, nf4moe_dtype_t dtype, float *t, void *ws,
+                                       size_t ws_bytes, void *stream) {
+  nf4moe_status_t st = check_adapters(ad, R);
+  if (st != NF4MOE_OK) return st;
+  if (!dt_ok(dtype)) return fail(NF4MOE_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if (R == 0) return NF4MOE_OK;
+  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L)) != NF4MOE_OK) return st;
+  if (!x || !out) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(x, 2) || !aligned(base, dt_bytes(dtype)) || !aligned(out, dt_bytes(dtype)) || !aligned(t, 16))
+    return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  const AdapterCarve need = carve_adapter(nullptr, *ad, R, false);
+  if (!ws || ws_bytes < need.bytes)
+    return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need.bytes);
+  if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  hipStream_t s = (hipStream_t)stream;
+  const bool bf = dtype == NF4MOE_DT_BF16;
+  if (adapter_rows_supported(R, ad->K, ad->rank)) {
+    AdapterRowsArgs a = {x, x_row_of, ids, x_rows, R, ad->L, ad->K, ad->N, ad->rank, ad->A, ad->B, ad->scale, base, out, bf, t};
+    return hip_status(launch_adapter_rows(a, s), "adapter launch");
+  }
+  const AdapterCarve c = carve_adapter(ws, *ad, R, false);
+  AdapterPlan p;
+  adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
+  hipError_t e = plan ? hipSuccess : launch_adapter_plan(ids, R, ad->L, p, s);
+  if (e != hipSuccess) return hip_status(e, "adapter plan launch");
+  float *low = t ? t : c.t;
+  e = launch_adapter_shrink({p, x, x_row_of, x_rows, ad->A, nullptr, ad->K, ad->rank, low}, s);
+  if (e != hipSuccess) return hip_status(e, "adapter shrink launch");
+  return hip_status(launch_adapter_expand({p, low, ad->B, ad->scale, ad->N, ad->rank, base, out, bf}, s), "adapter expand launch");
+}
+
+nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint16_t *dy, nf4moe_src_t x_src, const void *x,
+                                        const uint8_t *x_scale, int32_t x_rows, const int32_t *x_row_of, const float *t,
+                                        const int32_t *ids, const void *plan, size_t plan_bytes, int32_t R,
+                                        const void *dx_base, void *dx, nf4moe_dtype_t dx_dtype, float *dA, float *dB,
+                                        void *ws, size_t ws_bytes, void *stream) {
+  nf4moe_status_t st = check_adapters(ad, R);
+  if (st != NF4MOE_OK) return st;
+  if (!dt_ok(dx_dtype)) return fail(NF4MOE_ERR_INVALID_ARG, "unknown dtype %d", (int)dx_dtype);
+  if (x_src < NF4MOE_SRC_BF16 || x_src > NF4MOE_SRC_MXFP8)
+    return fail(NF4MOE_ERR_INVALID_ARG, "x must be bf16 or an 8-bit checkpoint, got source %d", (int)x_src);
+  const bool held = x_src >= NF4MOE_SRC_MXINT8;
+  if (held && ad->K % 32) return fail(NF4MOE_ERR_INVALID_ARG, "an 8-bit x needs K %% 32 == 0 (K=%d)", ad->K);
+  if (!aligned(dA, 16) || !aligned(dB, 16)) return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (R == 0) {  // sums over no rows
+    if (dA) e = launch_fill_f32_zero(dA, (int64_t)ad->L * ad->rank * ad->K, s);
+    if (e == hipSuccess && dB) e = launch_fill_f32_zero(dB, (int64_t)ad->L * ad->rank * ad->N, s);
+    return hip_status(e, "fill launch");
+  }
+  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L)) != NF4MOE_OK) return st;
+  if (!dy || (dA && (!x || (held && !x_scale))) || (dB && !t)) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(dy, 2) || !aligned(x, held ? 1 : 2) || !aligned(t, 16) || !aligned(dx_base, dt_bytes(dx_dtype)) ||
+      !aligned(dx, dt_bytes(dx_dtype)))
+    return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  const AdapterCarve need = carve_adapter(nullptr, *ad, R, true);
+  if (!ws || ws_bytes < need.bytes)
+    return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need.bytes);
+  if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (!dx && !dA && !dB) return NF4MOE_OK;
+  const AdapterCarve c = carve_adapter(ws, *ad, R, true);
+  AdapterPlan p;
+  adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
+  if (!plan && (e = launch_adapter_plan(ids, R, ad->L, p, s)) != hipSuccess) return hip_status(e, "adapter plan launch");
+  if (dx || dA) {
+    // u = s B^T dy: the shrink with B as [L, rank, N]
+    e = launch_transpose_bf16(ad->B, c.Bt, ad->L, ad->N, ad->rank, s);
+    if (e == hipSuccess) e = launch_adapter_shrink({p, dy, nullptr, R, c.Bt, ad->scale, ad->N, ad->rank, c.u}, s);
+    if (e != hipSuccess) return hip_status(e, "adapter backward shrink launch");
+  }
+  if (dx) {
+    // dx = dx_base + A^T u: the expand with A as [L, K, rank]
+    e = launch_transpose_bf16(ad->A, c.At, ad->L, ad->rank, ad->K, s);
+    if (e == hipSuccess)
+      e = launch_adapter_expand({p, c.u, c.At, nullptr, ad->K, ad->rank, dx_base, dx, dx_dtype == NF4MOE_DT_BF16}, s);
+    if (e != hipSuccess) return hip_status(e, "adapter backward expand launch");
+  }
+  if (dA) {
+    e = launch_adapter_rowgrad({p, c.u, x, x_scale, x_src, x_row_of, x_rows, nullptr, ad->L, ad->K, ad->rank, false, dA, c.partial}, s);
+    if (e != hipSuccess) return hip_status(e, "adapter dA launch");
+  }
+  if (dB) {
+    e = launch_adapter_rowgrad({p, t, dy, nullptr, SRC_BF16, nullptr, R, ad->scale, ad->L, ad->N, ad->rank, true, dB, c.partial}, s);
+    if (e != hipSuccess) return hip_status(e, "adapter dB launch");
+  }
+  return NF4MOE_OK;
 }
 
 }  // extern "C"

@@ -69,4 +69,84 @@ hipError_t launch_norm_backward(const NormArgs &a, hipStream_t s);
 int norm_backward_groups(int64_t T, int H);
 constexpr int kNormMaxH = 16384;
 
+// Adapters. Rows are grouped by adapter (stable, rows without one last) into
+// tiles of up to 64 rows and chunks of up to adapter_chunk_rows(R) rows.
+constexpr int kMaxAdapters = 4096;
+constexpr int kMaxRank = 128;
+constexpr int kAdTile = 64;
+struct AdapterPlan {
+  int32_t *order;      // [R] row of each place in grouped order
+  int32_t *counts;     // [0] tiles, [1] chunks
+  int2 *chunks_of;     // [L] (chunks of the adapter, first partial slot)
+  int4 *tiles;         // (adapter or -1, first place, rows, 0)
+  int4 *chunks;        // (adapter, first place, rows, partial slot or -1 when the adapter has one chunk)
+  int32_t *hist;       // scratch
+  int max_tiles, max_chunks, max_slots;
+};
+int adapter_chunk_rows(int R);
+size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p);   // bytes
+hipError_t launch_adapter_plan(const int32_t *ids, int R, int L, const AdapterPlan &p, hipStream_t s);
+
+// out[row][j] = m_l sum_k x[row'][k] W_l[j][k] for the rows of adapter l (W [L, rank, K]
+// bf16); zeros for rows without one. m: scale [L] or null; row' by row_of.
+struct ShrinkArgs {
+  AdapterPlan plan;
+  const uint16_t *x;
+  const int32_t *row_of;
+  int x_rows;
+  const uint16_t *W;
+  const float *scale;
+  int K, rank;
+  float *out;
+};
+hipError_t launch_adapter_shrink(const ShrinkArgs &a, hipStream_t s);
+
+// out[row][n] = base[row][n] + m_l sum_j t[row][j] W_l[n][j] (W [L, N, rank] bf16).
+struct ExpandArgs {
+  AdapterPlan plan;
+  const float *t;
+  const uint16_t *W;
+  const float *scale;
+  int N, rank;
+  const void *base;    // or null: zeros
+  void *out;
+  bool bf16;           // base and out
+};
+hipError_t launch_adapter_expand(const ExpandArgs &a, hipStream_t s);
+
+// out_l[j][c] (or [c][j], transposed) = m_l sum over the rows of l of p[row][j] v[row'][c].
+struct RowGradArgs {
+  AdapterPlan plan;
+  const float *p;      // [R, rank]
+  const void *v;       // [*, C] by src
+  const uint8_t *v_scale;
+  int src;
+  const int32_t *row_of;
+  int v_rows;
+  const float *scale;
+  int L, C, rank;
+  bool transposed;     // out [L, C, rank]
+  float *out, *partial;
+};
+hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s);
+hipError_t launch_fill_f32_zero(float *p, int64_t n, hipStream_t s);
+
+// [L][P][Q] -> [L][Q][P], bf16.
+hipError_t launch_transpose_bf16(const uint16_t *in, uint16_t *out, int L, int P, int Q, hipStream_t s);
+
+// The forward of few rows in one launch, without a plan.
+struct AdapterRowsArgs {
+  const uint16_t *x;
+  const int32_t *row_of, *ids;
+  int x_rows, R, L, K, N, rank;
+  const uint16_t *A, *B;
+  const float *scale;
+  const void *base;
+  void *out;
+  bool bf16;
+  float *t;            // or null
+};
+bool adapter_rows_supported(int R, int K, int rank);
+hipError_t launch_adapter_rows(const AdapterRowsArgs &a, hipStream_t s);
+
 }  // namespace nf4moe

@@ -1,6 +1,7 @@
 """Python binding of the fine-tuning operators around the frozen 4-bit MoE layer:
 8-bit activation checkpoints, the gated activation that writes and reads them,
-and the norms around the block with their gate and residual scale.
+the norms around the block with their gate and residual scale, and the low-rank
+adapters of many requests or experts beside a shared projection.
 
 Like the rest of the binding this only marshals arguments; every step runs in the
 library's HIP kernels, on the current stream of the tensors' device. Tensors are
@@ -288,4 +289,151 @@ def block_norm_backward(dx_new, dy, x_new, f=None, *, rstd_post=None, rstd_pre=N
          _p(rstd_post) if w_post is not None else None, _p(rstd_pre) if w_pre is not None else None, T,
          out["dx"].data_ptr(), _p(out.get("df")), _p(out.get("dgate")), _p(out.get("dw_post")), _p(out.get("dw_pre")),
          wsp, nb)
+    return out
+
+
+class _Adapters(ctypes.Structure):
+    """Mirror of nf4moe_adapters_t."""
+    _fields_ = [("L", ctypes.c_int32), ("rank", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+@dataclass
+class AdapterPlan:
+    """The rows of one batch grouped by adapter (adapter_plan); holds for the ids it
+    was made from."""
+    buffer: object
+    ptr: int
+    nbytes: int
+    R: int
+    L: int
+
+
+def _ids(ids):
+    torch = M._torch()
+    M._shape(ids, "ids", (None,))
+    if ids.dtype != torch.int32:
+        raise TypeError(f"ids must be torch.int32, got {ids.dtype}")
+    return ids.shape[0]
+
+
+def adapter_plan(ids, num_adapters: int) -> AdapterPlan:
+    """Group the rows of ids int32 [R] by adapter once, for several calls on the same
+    batch (adapter_forward and adapter_backward otherwise do it in each call)."""
+    torch = M._torch()
+    R = _ids(ids)
+    _on(ids)
+    L = M.lib()
+    ws, wsp, nb = M._workspace(L.nf4moe_adapter_plan_bytes(R, num_adapters), ids.device)
+    _run(ids.device, L.nf4moe_adapter_plan, ids.data_ptr(), R, num_adapters, wsp, nb)
+    return AdapterPlan(ws, wsp.value, nb, R, num_adapters)
+
+
+def _adapter_struct(A, B, ids, scale, plan):
+    torch = M._torch()
+    M._shape(A, "A", (None, None, None))
+    L, rank, K = A.shape
+    M._shape(B, "B", (L, None, rank))
+    M._shape(scale, "scale", (L,))
+    R = _ids(ids)
+    for name, t, dt in (("A", A, torch.bfloat16), ("B", B, torch.bfloat16), ("scale", scale, torch.float32)):
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if plan is not None and (plan.R != R or plan.L != L):
+        raise ValueError(f"the plan is for {plan.R} rows of {plan.L} adapters, not {R} of {L}")
+    return _Adapters(L, rank, K, B.shape[1], A.data_ptr(), B.data_ptr(), _p(scale)), R, K, B.shape[1], rank, L
+
+
+def _gather(x_row_of, R, rows):
+    torch = M._torch()
+    M._shape(x_row_of, "x_row_of", (R,))
+    if x_row_of is not None and x_row_of.dtype != torch.int32:
+        raise TypeError(f"x_row_of must be torch.int32, got {x_row_of.dtype}")
+    if x_row_of is None and rows != R:
+        raise ValueError(f"x has {rows} rows, expected {R} (or an x_row_of gather)")
+
+
+def adapter_forward(x, A, B, ids, *, base=None, scale=None, x_row_of=None, out=None, out_dtype=None, plan=None,
+                    return_t: bool = False):
+    """Low-rank adapters beside a shared projection:
+        out[r] = base[r] + scale[l] * B[l] (A[l] x[r]),  l = ids[r]
+    x bf16 [rows, K] (row r of the call reads x[x_row_of[r]], or x[r]); A bf16 [L,
+    rank, K], B bf16 [L, N, rank] (rank a multiple of 8 up to 128); ids int32 [R], an
+    id outside [0, L) means no adapter; scale fp32 [L] or None; base bf16 or fp32 [R,
+    N], the shared projection's output, or None (zeros); out: where the result goes
+    (may be base), else a new tensor of base's type or out_dtype. Returns out, or
+    (out, t) with t = A x fp32 [R, rank] for adapter_backward."""
+    torch = M._torch()
+    st, R, K, N, rank, _ = _adapter_struct(A, B, ids, scale, plan)
+    M._shape(x, "x", (None, K))
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be torch.bfloat16, got {x.dtype}")
+    _gather(x_row_of, R, x.shape[0])
+    M._shape(base, "base", (R, N))
+    M._shape(out, "out", (R, N))
+    dtype = out.dtype if out is not None else base.dtype if base is not None else out_dtype or torch.bfloat16
+    dt = _out_dt(dtype)
+    if out_dtype is not None and out_dtype != dtype or base is not None and base.dtype != dtype:
+        raise TypeError(f"base, out and out_dtype must agree on {dtype}")
+    _on(x, A=A, B=B, ids=ids, scale=scale, x_row_of=x_row_of, base=base, out=out, plan=plan and plan.buffer)
+    if out is None:
+        out = _empty((R, N), dtype, x)
+    t = _empty((R, rank), torch.float32, x) if return_t else None
+    lib = M.lib()
+    ws, wsp, nb = M._workspace(lib.nf4moe_adapter_workspace_bytes(ctypes.addressof(st), R, 0), x.device)
+    _run(x.device, lib.nf4moe_adapter_forward, ctypes.addressof(st), x.data_ptr(), x.shape[0], _p(x_row_of),
+         ids.data_ptr(), plan and plan.ptr, plan.nbytes if plan else 0, R, _p(base), out.data_ptr(), dt, _p(t), wsp, nb)
+    return (out, t) if return_t else out
+
+
+def adapter_backward(dy, x, t, A, B, ids, *, scale=None, x_row_of=None, dx_base=None, dx=None, dx_dtype=None, plan=None,
+                     need=("dx", "dA", "dB")):
+    """Gradients of adapter_forward for dy bf16 [R, N]. x as in the forward, bf16 or a
+    Ckpt8 of it (read in 8 bits; K % 32 == 0); t the forward's. Returns a dict of
+    those in `need`: dx [R, K] = dx_base + A^T u per row (dx_base bf16 or fp32 or None;
+    dx: where it goes, may be dx_base), dA fp32 [L, rank, K], dB fp32 [L, N, rank].
+    x may be None without dA, t without dB. The same bits on every run."""
+    torch = M._torch()
+    st, R, K, N, rank, L = _adapter_struct(A, B, ids, scale, plan)
+    if not set(need) <= {"dx", "dA", "dB"}:
+        raise ValueError(f"need names {set(need)}, expected some of dx, dA, dB")
+    M._shape(dy, "dy", (R, N))
+    if dy.dtype != torch.bfloat16:
+        raise TypeError(f"dy must be torch.bfloat16, got {dy.dtype}")
+    src, values, xs = M.DT_BF16, x, None
+    if isinstance(x, Ckpt8):
+        x.check("x")
+        src, values, xs = _SRC[x.fmt], x.codes, x.scale
+    elif x is not None and x.dtype != torch.bfloat16:
+        raise TypeError(f"x must be torch.bfloat16 or a Ckpt8, got {x.dtype}")
+    if "dA" in need and x is None:
+        raise ValueError("dA needs x")
+    if "dB" in need and t is None:
+        raise ValueError("dB needs t")
+    M._shape(values, "x", (None, K))
+    rows = R if x is None else values.shape[0]
+    _gather(x_row_of, R, rows)
+    M._shape(t, "t", (R, rank))
+    if t is not None and t.dtype != torch.float32:
+        raise TypeError(f"t must be torch.float32, got {t.dtype}")
+    M._shape(dx_base, "dx_base", (R, K))
+    M._shape(dx, "dx", (R, K))
+    dtype = dx.dtype if dx is not None else dx_base.dtype if dx_base is not None else dx_dtype or torch.bfloat16
+    dt = _out_dt(dtype)
+    if dx_dtype is not None and dx_dtype != dtype or dx_base is not None and dx_base.dtype != dtype:
+        raise TypeError(f"dx_base, dx and dx_dtype must agree on {dtype}")
+    _on(dy, A=A, B=B, ids=ids, scale=scale, x=values, x_scale=xs, x_row_of=x_row_of, t=t, dx_base=dx_base, dx=dx,
+        plan=plan and plan.buffer)
+    out = {}
+    if "dx" in need:
+        out["dx"] = _empty((R, K), dtype, dy) if dx is None else dx
+    if "dA" in need:
+        out["dA"] = _empty((L, rank, K), torch.float32, dy)
+    if "dB" in need:
+        out["dB"] = _empty((L, N, rank), torch.float32, dy)
+    lib = M.lib()
+    ws, wsp, nb = M._workspace(lib.nf4moe_adapter_workspace_bytes(ctypes.addressof(st), R, 1), dy.device)
+    _run(dy.device, lib.nf4moe_adapter_backward, ctypes.addressof(st), dy.data_ptr(), src, _p(values), _p(xs), max(rows, 1),
+         _p(x_row_of), _p(t), ids.data_ptr(), plan and plan.ptr, plan.nbytes if plan else 0, R, _p(dx_base),
+         _p(out.get("dx")), dt, _p(out.get("dA")), _p(out.get("dB")), wsp, nb)
     return out

@@ -440,6 +440,75 @@ nf4moe_status_t nf4moe_block_norm_backward(const nf4moe_block_norm_t *norm, cons
                                            const float *rstd_pre, int64_t T, void *dx, uint16_t *df, float *dgate,
                                            float *dw_post, float *dw_pre, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests or experts beside a shared projection (the
+ * frozen 4-bit one of nf4moe_grouped_gemm, or any other). Row r of R has adapter
+ * l = ids[r]; an id outside [0, L) means none:
+ *   t[r]   = A_l x[x_row_of[r]]                 fp32
+ *   out[r] = base[r] + scale_l * B_l t[r]       one rounding; rows without an
+ *                                               adapter: base[r]
+ * Rows may come in any order; one adapter per expert is ids = the rows' experts,
+ * one per (request, expert) an id that counts both. A NaN or an infinity reaches
+ * the values that are computed from it and no others; those are then not finite
+ * (NaN where the plain formula may have an infinity: the fp32 low-rank values are
+ * multiplied as three exact parts).
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t L;           /* adapters, 1..4096                                    */
+  int32_t rank;        /* a multiple of 8 in 8..128 (pad smaller ones with 0)  */
+  int32_t K, N;        /* input and output width, multiples of 8, at most 2^20 */
+  const uint16_t *A;   /* bf16 [L, rank, K]                                    */
+  const uint16_t *B;   /* bf16 [L, N, rank]                                    */
+  const float *scale;  /* fp32 [L], or NULL: 1                                 */
+} nf4moe_adapters_t;
+
+/* nf4moe_adapter_plan -- the grouping of ids [R] (device) by adapter, which the
+ * calls below otherwise make for themselves: a batch that runs through several
+ * projections builds it once. plan: nf4moe_adapter_plan_bytes(R, L) bytes, device,
+ * 256-byte aligned; it holds for these ids, R and L only. R at most 2^30; R == 0
+ * is a no-op. Errors: INVALID_ARG, WORKSPACE. */
+size_t nf4moe_adapter_plan_bytes(int32_t R, int32_t L);
+nf4moe_status_t nf4moe_adapter_plan(const int32_t *ids, int32_t R, int32_t L, void *plan, size_t plan_bytes, void *stream);
+
+/* nf4moe_adapter_workspace_bytes -- workspace of the forward (backward = 0) or the
+ * backward (1) for R rows; 0 for invalid sizes or R < 1. */
+size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, int32_t backward);
+
+/* nf4moe_adapter_forward -- out [R, N] (may be base) from x bf16 [x_rows, K] and
+ * base [R, N] or NULL (zeros), both in dtype.
+ *   x_row_of int32 [R] (device) or NULL: row r reads x[x_row_of[r]], clamped into
+ *            [0, x_rows); NULL means x[r] (then x_rows >= R)
+ *   plan     from nf4moe_adapter_plan for the same ids, or NULL
+ *   t        fp32 [R, rank] (16-byte aligned) or NULL: the low-rank product, which
+ *            the backward takes (0 for rows without an adapter)
+ * t is summed in fp32 and enters the second product exactly; the output has one
+ * rounding. R == 0 is a no-op. Calls of at most 32 rows with K * rank <= 65536 run
+ * in one launch and ignore the plan; results differ from the grouped kernels' in
+ * summation order only. Errors: INVALID_ARG, WORKSPACE. */
+nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16_t *x, int32_t x_rows,
+                                       const int32_t *x_row_of, const int32_t *ids, const void *plan, size_t plan_bytes,
+                                       int32_t R, const void *base, void *out, nf4moe_dtype_t dtype, float *t, void *ws,
+                                       size_t ws_bytes, void *stream);
+
+/* nf4moe_adapter_backward -- for dy bf16 [R, N], the gradient of out:
+ *   u[r] = scale_l * B_l^T dy[r]                                  (kept in fp32)
+ *   dx[r] = dx_base[r] + A_l^T u[r]    [R, K] in dx_dtype; dx_base NULL: zeros, may
+ *                                      be dx; rows without an adapter: dx_base[r].
+ *                                      Per routed row, as nf4moe_grouped_dgrad
+ *   dA_l = sum_r u[r] x[x_row_of[r]]^T    fp32 [L, rank, K]
+ *   dB_l = scale_l * sum_r dy[r] t[r]^T   fp32 [L, N, rank]
+ * over the rows of adapter l, zeros for an adapter without rows; dx, dA and dB may
+ * each be NULL. x is read for dA only: bf16, or an 8-bit checkpoint (x_src, with
+ * x_scale; K % 32 == 0) decoded in registers. t is the forward's (for dB). The sums
+ * over rows are added in a fixed order: the same bits on every run. dA and dB
+ * 16-byte aligned. R == 0 writes zeros to dA and dB. Errors: INVALID_ARG,
+ * WORKSPACE. */
+nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint16_t *dy, nf4moe_src_t x_src, const void *x,
+                                        const uint8_t *x_scale, int32_t x_rows, const int32_t *x_row_of, const float *t,
+                                        const int32_t *ids, const void *plan, size_t plan_bytes, int32_t R,
+                                        const void *dx_base, void *dx, nf4moe_dtype_t dx_dtype, float *dA, float *dB,
+                                        void *ws, size_t ws_bytes, void *stream);
+
 /* nf4moe_stream_read -- a measurement aid, not part of the layer: one launch
  * that reads `bytes` bytes of `buf` (device, 16-byte aligned, bytes a positive
  * multiple of 16) once with 16-byte loads, loads_per_thread (1, 2, 4, 8 or 16)

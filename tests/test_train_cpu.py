@@ -98,6 +98,29 @@ def test_norm_gradient_reference_by_differences(gate):
             assert np.allclose(got[key], num, rtol=2e-5, atol=2e-5), (fn, name)
 
 
+def test_adapter_gradient_reference_by_differences():
+    rng = np.random.default_rng(4)
+    L_, r, K, N, ids, row_of = 3, 2, 4, 5, np.array([1, -1, 0, 1, 9, 0]), np.array([0, 1, 1, 2, 0, 2])
+    v = dict(x=rng.standard_normal((3, K)), A=rng.standard_normal((L_, r, K)), B=rng.standard_normal((L_, N, r)))
+    scale, cy = rng.random(L_) + 0.5, rng.standard_normal((6, N))
+
+    def loss(v):
+        return (cy * R.adapter_forward(v["x"], v["A"], v["B"], ids, scale, None, row_of)[0]).sum()
+    t = R.adapter_forward(v["x"], v["A"], v["B"], ids, scale, None, row_of)[1]
+    got, _ = R.adapter_backward(cy, v["x"], t, v["A"], v["B"], ids, scale, None, row_of)
+    dx = np.zeros((3, K))
+    np.add.at(dx, row_of, got["dx"])
+    for name, g in (("x", dx), ("A", got["dA"]), ("B", got["dB"])):
+        num = np.zeros_like(v[name])
+        for i in np.ndindex(*num.shape):
+            for sgn in (1, -1):
+                q = {k: a.copy() for k, a in v.items()}
+                q[name][i] += sgn * 1e-6
+                num[i] += sgn * loss(q) / 2e-6
+        assert np.allclose(g, num, rtol=1e-6, atol=1e-7), name
+    assert np.all(got["dA"][2] == 0) and np.all(got["dx"][[1, 4]] == 0)
+
+
 # ------------------------------------------------------------------ refusals of the C ABI
 def test_ckpt8_validation():
     for q in (lambda f, x, dt, rows, K, c, s: L.nf4moe_ckpt8_quantize(f, x, dt, rows, K, c, s, None),
@@ -189,6 +212,63 @@ def test_block_norm_validation():
     assert bw(12, FAKE + 16) == INVALID
 
 
+def test_adapter_validation():
+    import ctypes
+
+    from bit_quantized_moe_expert_amd import train
+
+    def desc(L_=4, rank=16, K=64, N=64, A=FAKE, B=FAKE, scale=None):
+        st = train._Adapters(L_, rank, K, N, A, B, scale)
+        return st, ctypes.addressof(st)
+    st, a = desc()
+    assert L.nf4moe_adapter_plan_bytes(0, 4) == 0 and L.nf4moe_adapter_plan_bytes(8, 0) == 0
+    assert L.nf4moe_adapter_plan_bytes(8, 4097) == 0 and L.nf4moe_adapter_plan_bytes(8, 4096) > 0
+    pb, wf, wb = (L.nf4moe_adapter_plan_bytes(100, 4), L.nf4moe_adapter_workspace_bytes(a, 100, 0),
+                  L.nf4moe_adapter_workspace_bytes(a, 100, 1))
+    assert pb > 0 and wf >= pb and wb > wf - 100 * 64
+    assert L.nf4moe_adapter_workspace_bytes(a, 0, 0) == 0 and L.nf4moe_adapter_workspace_bytes(None, 8, 0) == 0
+    plan = L.nf4moe_adapter_plan
+    assert plan(FAKE, 100, 0, FAKE, pb, None) == INVALID and plan(FAKE, 100, 4097, FAKE, pb, None) == INVALID
+    assert plan(FAKE, -1, 4, FAKE, pb, None) == INVALID and plan(None, 100, 4, FAKE, pb, None) == INVALID
+    assert plan(FAKE + 2, 100, 4, FAKE, pb, None) == INVALID and plan(FAKE, 100, 4, FAKE + 16, pb, None) == INVALID
+    assert plan(FAKE, 100, 4, None, pb, None) == WORKSPACE and plan(FAKE, 100, 4, FAKE, pb - 1, None) == WORKSPACE
+    assert plan(None, 0, 4, None, 0, None) == OK
+
+    names = ["x", "x_rows", "row_of", "ids", "plan", "pb", "R", "base", "out", "dt", "t", "ws", "wsb"]
+    dflt = dict(x=FAKE, x_rows=100, row_of=None, ids=FAKE, plan=None, pb=0, R=100, base=FAKE, out=FAKE, dt=1, t=None,
+                ws=FAKE, wsb=wf)
+
+    def fwd(d=None, **kw):
+        keep = d or desc()
+        return L.nf4moe_adapter_forward(keep[1], *[dict(dflt, **kw)[n] for n in names], None)
+    bnames = ["dy", "src", "x", "xs", "x_rows", "row_of", "t", "ids", "plan", "pb", "R", "dxb", "dx", "dt", "dA", "dB", "ws", "wsb"]
+    bdflt = dict(dy=FAKE, src=1, x=FAKE, xs=None, x_rows=100, row_of=None, t=FAKE, ids=FAKE, plan=None, pb=0, R=100, dxb=None,
+                 dx=FAKE, dt=1, dA=FAKE, dB=FAKE, ws=FAKE, wsb=wb)
+
+    def bwd(d=None, **kw):
+        keep = d or desc()
+        return L.nf4moe_adapter_backward(keep[1], *[dict(bdflt, **kw)[n] for n in bnames], None)
+    for call in (fwd, bwd):
+        for bad in (dict(L_=0), dict(L_=4097), dict(rank=0), dict(rank=4), dict(rank=20), dict(rank=136), dict(K=4), dict(K=60),
+                    dict(N=0), dict(N=12), dict(K=1 << 21), dict(A=None), dict(B=None), dict(A=ODD), dict(scale=FAKE + 2)):
+            assert call(desc(**bad)) == INVALID, bad
+        assert call(R=-1) == INVALID and call(R=(1 << 30) + 1) == INVALID
+        assert call(dt=2) == INVALID and call(ids=None) == INVALID and call(ids=ODD) == INVALID
+        assert call(x_rows=99) == INVALID and call(x_rows=0, row_of=FAKE) == INVALID and call(row_of=ODD) == INVALID
+        assert call(plan=FAKE, pb=pb - 1) == WORKSPACE and call(plan=FAKE + 16, pb=pb) == INVALID
+        assert call(ws=None) == WORKSPACE and call(wsb=10) == WORKSPACE and call(ws=FAKE + 16) == INVALID
+        assert call(t=FAKE + 4) == INVALID and call(x=ODD) == INVALID
+    assert L.nf4moe_adapter_forward(None, *[dflt[n] for n in names], None) == INVALID
+    assert fwd(x=None) == INVALID and fwd(out=None) == INVALID and fwd(out=ODD) == INVALID and fwd(base=ODD) == INVALID
+    assert fwd(R=0, x=None, ids=None, out=None, ws=None, wsb=0) == OK
+    assert bwd(src=0) == INVALID and bwd(src=4) == INVALID and bwd(src=2) == INVALID      # fp32; unknown; no scales
+    assert bwd(desc(K=40), src=2, xs=FAKE) == INVALID                                     # 8-bit x: K % 32
+    assert bwd(dy=None) == INVALID and bwd(x=None) == INVALID and bwd(t=None) == INVALID
+    assert bwd(dA=FAKE + 4) == INVALID and bwd(dB=FAKE + 4) == INVALID and bwd(dx=ODD) == INVALID
+    assert bwd(dx=None, dA=None, dB=None) == OK
+    assert bwd(R=0, dA=None, dB=None) == OK
+
+
 # ------------------------------------------------------------------ refusals of the binding
 def test_binding_refuses_before_the_device():
     M = pkg
@@ -224,3 +304,29 @@ def test_binding_refuses_before_the_device():
         M.block_norm_forward(bf, bf, w_pre=w)
     with pytest.raises(ValueError, match="cpu"):
         M.block_norm_backward(bf, bf, bf, bf, w_pre=w, rstd_pre=torch.ones(4))
+
+
+def test_binding_refuses_bad_adapters():
+    M = pkg
+    x, ids = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    A, B = torch.zeros(3, 16, 64, dtype=torch.bfloat16), torch.zeros(3, 32, 16, dtype=torch.bfloat16)
+    t = torch.zeros(4, 16)
+    dy = torch.zeros(4, 32, dtype=torch.bfloat16)
+    for err, kw in ((ValueError, dict(B=B[:2])), (ValueError, dict(B=torch.zeros(3, 32, 8, dtype=torch.bfloat16))),
+                    (TypeError, dict(A=A.float())), (TypeError, dict(ids=ids.long())), (ValueError, dict(x=x[:, :32])),
+                    (ValueError, dict(x=x[:3])), (TypeError, dict(x=x.float())), (ValueError, dict(scale=torch.ones(4))),
+                    (TypeError, dict(scale=torch.ones(3).double())), (ValueError, dict(base=torch.zeros(4, 31))),
+                    (TypeError, dict(base=torch.zeros(4, 32), out_dtype=torch.bfloat16)),
+                    (TypeError, dict(x_row_of=ids.long())), (ValueError, dict(x_row_of=ids[:3])),
+                    (TypeError, dict(out_dtype=torch.float16)),
+                    (ValueError, dict(plan=M.AdapterPlan(x, 0, 0, 5, 3))), (ValueError, dict())):
+        with pytest.raises(err):
+            M.adapter_forward(**dict(dict(x=x, A=A, B=B, ids=ids), **kw))
+    for err, kw in ((ValueError, dict(need=("dz",))), (ValueError, dict(dy=dy[:, :16])), (TypeError, dict(dy=dy.float())),
+                    (ValueError, dict(x=None)), (ValueError, dict(t=None)), (TypeError, dict(t=t.double())),
+                    (ValueError, dict(t=t[:3])), (ValueError, dict(x=x[:3])), (TypeError, dict(x=x.float())),
+                    (TypeError, dict(dx_base=torch.zeros(4, 64), dx_dtype=torch.bfloat16)), (ValueError, dict())):
+        with pytest.raises(err):
+            M.adapter_backward(**dict(dict(dy=dy, x=x, t=t, A=A, B=B, ids=ids), **kw))
+    with pytest.raises(ValueError, match="cpu"):
+        M.adapter_plan(ids, 3)

@@ -176,3 +176,36 @@ def norm_backward(dx_new, dy, x_new, f, rp, r, w_post, w_pre, gate, fn, alpha):
         dzm = rp[:, None] * (am + np.abs(n) * (am * np.abs(n)).sum(1, keepdims=True) / H)
     out["df"], mag["df"] = dz, dzm
     return out, mag
+
+
+# ------------------------------------------------------------------ adapters
+def adapter_rows(ids, L):
+    ids = np.asarray(ids)
+    return {l: np.flatnonzero(ids == l) for l in np.unique(ids) if 0 <= l < L}
+
+
+def adapter_forward(x, A, B, ids, scale, base, row_of):
+    """out, t, and the sums of the magnitudes of their terms (base left out)."""
+    R, (L, r, K), N = len(ids), A.shape, B.shape[1]
+    xr = x if row_of is None else x[row_of]
+    t, tm, d, dm = np.zeros((R, r)), np.zeros((R, r)), np.zeros((R, N)), np.zeros((R, N))
+    for l, rows in adapter_rows(ids, L).items():
+        t[rows], tm[rows] = xr[rows] @ A[l].T, np.abs(xr[rows]) @ np.abs(A[l]).T
+        d[rows], dm[rows] = scale[l] * (t[rows] @ B[l].T), abs(scale[l]) * (tm[rows] @ np.abs(B[l]).T)
+    return (d if base is None else base + d), t, dm, tm
+
+
+def adapter_backward(dy, x, t, A, B, ids, scale, dx_base, row_of):
+    """dx, dA, dB and the sums of the magnitudes of their terms (dx_base left out)."""
+    R, (L, r, K), N = len(ids), A.shape, B.shape[1]
+    xr = x if row_of is None else x[row_of]
+    out = dict(dx=np.zeros((R, K)) if dx_base is None else dx_base.copy(), dA=np.zeros((L, r, K)), dB=np.zeros((L, N, r)))
+    mag = dict(dx=np.zeros((R, K)), dA=np.zeros((L, r, K)), dB=np.zeros((L, N, r)))
+    for l, rows in adapter_rows(ids, L).items():
+        g, gm = dy[rows], np.abs(dy[rows])
+        u, um = scale[l] * (g @ B[l]), abs(scale[l]) * (gm @ np.abs(B[l]))
+        out["dx"][rows] += u @ A[l]
+        mag["dx"][rows] = um @ np.abs(A[l])
+        out["dA"][l], mag["dA"][l] = u.T @ xr[rows], um.T @ np.abs(xr[rows])
+        out["dB"][l], mag["dB"][l] = scale[l] * (g.T @ t[rows]), abs(scale[l]) * (gm.T @ np.abs(t[rows]))
+    return out, mag
