@@ -272,6 +272,7 @@ size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, in
   if (!ad || R < 1 || R > (1 << 30) || ad->L < 1 || ad->L > kMaxAdapters || ad->rank < 8 || ad->rank > kMaxRank ||
       ad->K < 8 || ad->N < 8)
     return 0;
+  if (!backward && adapter_rows_supported(R, ad->K, ad->rank)) return 0;
   return carve_adapter(nullptr, *ad, R, backward != 0).bytes;
 }
 
@@ -302,16 +303,16 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   if (!x || !out) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(x, 2) || !aligned(base, dt_bytes(dtype)) || !aligned(out, dt_bytes(dtype)) || !aligned(t, 16))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
-  const AdapterCarve need = carve_adapter(nullptr, *ad, R, false);
-  if (!ws || ws_bytes < need.bytes)
-    return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need.bytes);
-  if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   hipStream_t s = (hipStream_t)stream;
   const bool bf = dtype == NF4MOE_DT_BF16;
   if (adapter_rows_supported(R, ad->K, ad->rank)) {
     AdapterRowsArgs a = {x, x_row_of, ids, x_rows, R, ad->L, ad->K, ad->N, ad->rank, ad->A, ad->B, ad->scale, base, out, bf, t};
     return hip_status(launch_adapter_rows(a, s), "adapter launch");
   }
+  const AdapterCarve need = carve_adapter(nullptr, *ad, R, false);
+  if (!ws || ws_bytes < need.bytes)
+    return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need.bytes);
+  if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   const AdapterCarve c = carve_adapter(ws, *ad, R, false);
   AdapterPlan p;
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);

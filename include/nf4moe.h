@@ -471,7 +471,8 @@ size_t nf4moe_adapter_plan_bytes(int32_t R, int32_t L);
 nf4moe_status_t nf4moe_adapter_plan(const int32_t *ids, int32_t R, int32_t L, void *plan, size_t plan_bytes, void *stream);
 
 /* nf4moe_adapter_workspace_bytes -- workspace of the forward (backward = 0) or the
- * backward (1) for R rows; 0 for invalid sizes or R < 1. */
+ * backward (1) for R rows; 0 for invalid sizes or R < 1, and where the forward
+ * needs none (its one-launch form). */
 size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, int32_t backward);
 
 /* nf4moe_adapter_forward -- out [R, N] (may be base) from x bf16 [x_rows, K] and
