@@ -202,181 +202,263 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
 }
 
 // ------------------------------------------------------------------ shrink
-// One workgroup per tile; its four waves take every fourth 64-wide step of K for
-// all the tile's rows, so each adapter row is read once per workgroup, and add
-// their sums in order through LDS. A lane's two 16-byte pieces of a step are
-// neighbours (k = 16 q .. + 15), the same places in both operands, so a row's
-// step is one whole 128-byte line.
-template <int RT>
-__global__ __launch_bounds__(256) void k_shrink(ShrinkArgs p) {
-  constexpr int kPad = RT * 16 + 4;
-  __shared__ __attribute__((aligned(16))) float red[kAdTile][kPad];
-  if ((int)blockIdx.x >= p.plan.counts[0]) return;
-  const int4 tile = p.plan.tiles[blockIdx.x];
-  const int l = tile.x, n = tile.z, rank = p.rank;
-  const int32_t *order = p.plan.order + tile.y;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, q = lane >> 4;
-  if (l >= 0) {
-    const uint16_t *xrow[4], *wrow[RT];
+// K is taken in slices, one workgroup per tile and slice, and the workgroups of a
+// slice on one XCD (workgroups go to the XCDs in turn): the slice's columns of a
+// gathered x (each token's row is read by every expert that it was routed to) and
+// of all adapters then stay in that XCD's L2 (4 slices: a pair of XCDs a slice). Few
+// rows still make many workgroups.
+// Inside, the four waves take every fourth 64-wide step of the slice for all the
+// tile's rows, so each adapter row is read once per workgroup; a row's step is one
+// whole 128-byte line, taken as two 64-byte halves.
+constexpr int kSliceMin = 256;   // no slice is narrower
+
+template <int RT, int NS>
+__device__ inline void shrink_rows(const LowRankArgs &p, const int32_t *order, int n, int l, int k, int k1, f32x4_t (&acc)[4][RT]) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const uint16_t *xrow[NS], *wrow[RT];
+  int r[NS];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      int r = order[min(16 * s + l16, n - 1)];
-      if (p.row_of) r = min(max(p.row_of[r], 0), p.x_rows - 1);
-      xrow[s] = p.x + (int64_t)r * p.K;
+  for (int s = 0; s < NS; ++s) r[s] = order[min(16 * s + l16, n - 1)];
+  if (p.row_of) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) r[s] = p.row_of[r[s]];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) r[s] = min(max(r[s], 0), p.x_rows - 1);
+  }
+#pragma unroll
+  for (int s = 0; s < NS; ++s) xrow[s] = p.x + (int64_t)r[s] * p.K;
+#pragma unroll
+  for (int j = 0; j < RT; ++j) wrow[j] = p.W1 + ((int64_t)l * p.rank + min(16 * j + l16, p.rank - 1)) * p.K;
+  for (; k < k1; k += 256) {
+    // Every load is made (places past the slice read its last ones, against zero
+    // weights): no branch splits a step's loads.
+    uint4 x[NS][2], w[RT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int kc = min(k + 32 * h + 8 * q, k1 - 8);
+#pragma unroll
+      for (int j = 0; j < RT; ++j) w[j][h] = load16(wrow[j] + kc);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) x[s][h] = load16(xrow[s] + kc);
     }
 #pragma unroll
-    for (int j = 0; j < RT; ++j) wrow[j] = p.W + ((int64_t)l * rank + min(16 * j + l16, rank - 1)) * p.K;
-    f32x4_t acc[4][RT] = {};
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int k0 = 64 * wave; k0 < p.K; k0 += 256) {
-      const int k = k0 + 16 * q;
-      const bool ok0 = k < p.K, ok1 = k + 8 < p.K;
-      uint4 w0[RT], w1[RT];
+    for (int h = 0; h < 2; ++h) {
+      const bool ok = k + 32 * h + 8 * q < k1;
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
-        w0[j] = ok0 ? load16(wrow[j] + k) : zero;
-        w1[j] = ok1 ? load16(wrow[j] + k + 8) : zero;
-      }
+        const uint4 wv = ok ? w[j][h] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (16 * s >= n) break;  // the same for the whole workgroup
-        const uint4 x0 = ok0 ? load16(xrow[s] + k) : zero;
-        const uint4 x1 = ok1 ? load16(xrow[s] + k + 8) : zero;
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          acc[s][j] = mfma16(w0[j], x0, acc[s][j]);
-          acc[s][j] = mfma16(w1[j], x1, acc[s][j]);
-        }
+        for (int s = 0; s < NS; ++s) acc[s][j] = mfma16(wv, x[s][h], acc[s][j]);
       }
     }
-    // lane: row 16 s + l16, ranks 16 j + 4 q ..
-    for (int w = 0; w < 4; ++w) {
-      if (wave == w) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int j = 0; j < RT; ++j) {
-            f32x4_t *d = reinterpret_cast<f32x4_t *>(&red[16 * s + l16][16 * j + 4 * q]);
-            *d = w == 0 ? acc[s][j] : *d + acc[s][j];
-          }
-      }
-      lds_barrier();
-    }
-  }
-  const float m = l >= 0 && p.scale ? p.scale[l] : 1.0f;
-  const int per = rank / 4;
-  for (int i = tid; i < n * per; i += 256) {
-    const int row = i / per, j = 4 * (i % per);
-    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (l >= 0) v = *reinterpret_cast<const f32x4_t *>(&red[row][j]) * m;
-    *reinterpret_cast<f32x4_t *>(p.out + (int64_t)order[row] * rank + j) = v;
   }
 }
 
-// ------------------------------------------------------------------ expand
-// One workgroup per tile and 256 columns, 64 columns a wave. The product is taken
-// transposed (columns as the matrix rows), so a lane ends with neighbouring
-// columns of one row: 8 (bf16, by pairing two column blocks) or 4 (fp32), 64
-// contiguous bytes of a row per access, and base, product and out meet in
-// registers. t's tile is scaled and split into three bf16 parts once, in LDS; the
-// 32 k places of a matrix instruction hold 32 ranks of one part, or for rank 8 all
-// three parts at once and for rank 16 two (PACK).
-template <int PACK, bool BF>
-__global__ __launch_bounds__(256) void k_expand(ExpandArgs p) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t parts[];
-  if ((int)blockIdx.x >= p.plan.counts[0]) return;
-  const int4 tile = p.plan.tiles[blockIdx.x];
-  const int l = tile.x, n = tile.z, rank = p.rank, nr8 = rank / 8;
-  if (l < 0 && p.base == p.out) return;  // nothing to add
+template <int RT>
+__global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int slice) {
+  constexpr int kPad = RT * 16 + 4, SL = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) float red[SL][kAdTile][kPad];
+  const int si = blockIdx.x % slices, ti = blockIdx.x / slices;
+  if (ti >= p.plan.counts[0]) return;
+  const int4 tile = p.plan.tiles[ti];
+  const int l = tile.x, n = tile.z, rank = p.rank;
+  if (l < 0) return;
   const int32_t *order = p.plan.order + tile.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
-  const int nb = (nr8 + 3) / 4;                                   // blocks of 32 ranks (PACK 0)
-  const int steps = PACK == 1 ? 1 : PACK == 2 ? 2 : 3 * nb;
-  const int pstride = PACK == 1 ? 8 : PACK == 2 ? 16 : 32 * nb;   // elements from part to part
-  const int rstride = steps * 32 + 8;                             // elements from row to row
-  f32x4_t acc[4][4] = {};                                         // [16 rows][16 columns]
-  const int c0 = blockIdx.y * 256 + wave * 64;
-  if (l >= 0) {
-    const float m = p.scale ? p.scale[l] : 1.0f;
-    const int g8 = PACK == 0 ? 4 * nb : nr8;                      // groups of 8 places per part
-    for (int i = tid; i < kAdTile * g8; i += 256) {
-      const int row = i / g8, r8 = i % g8;
-      float v[8] = {};
-      if (row < n && r8 < nr8) {
-        load_elems8<false>(p.t, (int64_t)order[row] * rank + 8 * r8, v);
+  const int k = si * slice + 64 * wave, k1 = min(p.K, (si + 1) * slice);
+  f32x4_t acc[4][RT] = {};
+  if (n <= 16) shrink_rows<RT, 1>(p, order, n, l, k, k1, acc);
+  else if (n <= 32) shrink_rows<RT, 2>(p, order, n, l, k, k1, acc);
+  else shrink_rows<RT, 4>(p, order, n, l, k, k1, acc);
+  // lane: row 16 s + l16, ranks 16 j + 4 q ..; the waves' sums in a fixed order, SL of them at a time
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] *= m;
-      }
-      uint4 hi, mid, lo;
-      split3(v, hi, mid, lo);
-      uint16_t *d = parts + row * rstride + 8 * r8;
-      *reinterpret_cast<uint4 *>(d) = hi;
-      *reinterpret_cast<uint4 *>(d + pstride) = mid;
-      *reinterpret_cast<uint4 *>(d + 2 * pstride) = lo;
-      if (PACK != 0 && r8 == 0) {
-        *reinterpret_cast<uint4 *>(parts + row * rstride + 3 * pstride) = make_uint4(0, 0, 0, 0);
-        if (PACK == 2) *reinterpret_cast<uint4 *>(parts + row * rstride + 3 * pstride + 8) = make_uint4(0, 0, 0, 0);
-      }
+  for (int turn = 0; turn < 4 / SL; ++turn) {
+    if (wave / SL == turn) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          f32x4_t *d = reinterpret_cast<f32x4_t *>(&red[wave % SL][16 * s + l16][16 * j + 4 * q]);
+          *d = turn == 0 ? acc[s][j] : *d + acc[s][j];
+        }
     }
     lds_barrier();
-    const uint16_t *wrow[4];
+  }
+  float *out = p.partial + ((int64_t)si * p.R + tile.y) * rank;
+  const int r4 = rank / 4;
+  for (int i = tid; i < n * r4; i += 256) {
+    f32x4_t v = *reinterpret_cast<const f32x4_t *>(&red[0][i / r4][4 * (i % r4)]);
+#pragma unroll
+    for (int w = 1; w < SL; ++w) v += *reinterpret_cast<const f32x4_t *>(&red[w][i / r4][4 * (i % r4)]);
+    *reinterpret_cast<f32x4_t *>(out + 4 * i) = v;
+  }
+}
+
+// How the second product takes the low-rank values: `steps` matrix instructions of
+// 32 places a row and 16 columns. The places hold the three bf16 parts of the
+// scaled values: for rank 8 all three parts in one step (PACK 1), for rank 16 two
+// and then the third (PACK 2), else 32 ranks of one part a step, the parts of a
+// block of 32 ranks following each other (PACK 0). Other places hold zeros.
+__host__ __device__ inline int part_pack(int rank) { return rank == 8 ? 1 : rank == 16 ? 2 : 0; }
+__host__ __device__ inline int part_steps(int rank) { return rank <= 16 ? rank / 8 : 3 * ((rank + 31) / 32); }
+__device__ inline int part_place(int pack, int r8, int part) {  // place of ranks 8 r8 .. of one part in a row
+  return pack == 1 ? 8 * part : pack == 2 ? 16 * part + 8 * r8 : 96 * (r8 >> 2) + 32 * part + 8 * (r8 & 3);
+}
+
+// The slices' sums, added in order, for 8 ranks of one place a thread: out by row,
+// and the scaled value's parts in grouped order.
+__global__ __launch_bounds__(256) void k_shrink_join(LowRankArgs p, int slices, int L, const int32_t *__restrict__ ids) {
+  const int pack = part_pack(p.rank), nr8 = p.rank / 8, g8 = pack ? nr8 : (nr8 + 3) / 4 * 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int place = (int)(i / g8), r8 = (int)(i % g8);
+  if (place >= p.R) return;
+  const int row = p.plan.order[place], l = bin_of(ids[row], L);
+  float v[8] = {};
+  if (l < L && r8 < nr8) {
+    for (int s = 0; s < slices; ++s) {
+      float u[8];
+      load_elems8<false>(p.partial, ((int64_t)s * p.R + place) * p.rank + 8 * r8, u);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] += u[k];
+    }
+  }
+  const float m = p.scale && l < L ? p.scale[l] : 1.0f;
+  float sv[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sv[k] = v[k] * m;
+  if (p.low && r8 < nr8) store_elems8<false>(p.low, (int64_t)row * p.rank + 8 * r8, p.low_scaled ? sv : v);
+  if (!p.parts) return;
+  uint4 hi, mid, lo;
+  split3(sv, hi, mid, lo);
+  uint16_t *d = p.parts + (int64_t)place * (32 * part_steps(p.rank));
+  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 0)) = hi;
+  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 1)) = mid;
+  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 2)) = lo;
+  if (pack && r8 == 0)
+    for (int c = 24 * pack; c < 32 * pack; c += 8) *reinterpret_cast<uint4 *>(d + c) = make_uint4(0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ expand
+// One workgroup per tile and 256 columns, 64 columns a wave; no LDS and no
+// barrier. The product is taken transposed (columns as the matrix rows), so a lane
+// ends with neighbouring columns of one row: 8 (bf16, by pairing two column blocks)
+// or 4 (fp32), 64 contiguous bytes of a row per access, and base, product and out
+// meet in registers. The low-rank values come ready for the matrix instructions.
+template <int PACK, bool BF>
+__global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
+  const int ti = blockIdx.x / blocks;  // a tile's column blocks follow each other: whole rows are in flight together
+  if (ti >= p.plan.counts[0]) return;
+  const int4 tile = p.plan.tiles[ti];
+  const int l = tile.x, n = tile.z, rank = p.rank, nr8 = rank / 8;
+  if (l < 0 && p.base == p.out) return;  // nothing to add
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, q = lane >> 4;
+  const int c0 = (int)(blockIdx.x % blocks) * 128 + (wave >> 1) * 64, r0 = (wave & 1) * 32;
+  if (r0 >= n) return;
+  const int32_t *order = p.plan.order + tile.y;
+  int rows[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) rows[s] = order[min(r0 + 16 * s + l16, n - 1)];
+  const uint16_t *trow[2], *wrow[4];
+  const int width = 32 * part_steps(rank);
+  uint4 w[4], t[PACK ? PACK : 1][2];
+  // the weights of the ranks that this lane's 8 places of block o hold; places of no part meet zeros
+  auto load_w = [&](int o) {
+    const int r8 = PACK == 1 ? 0 : PACK == 2 ? (q & 1) : 4 * o + q;
+    const bool ok = PACK == 1 ? q < 3 : PACK == 2 ? true : r8 < nr8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = ok ? load16(wrow[j] + 8 * r8) : make_uint4(0, 0, 0, 0);
+  };
+  if (l >= 0) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) trow[s] = p.parts + (int64_t)(tile.y + min(r0 + 16 * s + l16, n - 1)) * width + 8 * q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = BF ? 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3) : 16 * j + l16;
-      wrow[j] = p.W + ((int64_t)l * p.N + min(c0 + c, p.N - 1)) * rank;
+      wrow[j] = p.W2 + ((int64_t)l * p.N + min(c0 + c, p.N - 1)) * rank;
     }
-    const int outer = PACK == 0 ? nb : steps;
-    for (int o = 0; o < outer; ++o) {
-      // the ranks of this lane's 8 places; places of no part hold zeros
-      const int g = 4 * o + q;
-      const int r8 = PACK == 1 ? 0 : PACK == 2 ? (g & 1) : g;
-      const bool ok = PACK == 1 ? q < 3 : PACK == 2 ? g < 6 : r8 < nr8;
-      uint4 w[4];
+    load_w(0);
+    if constexpr (PACK != 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = ok ? load16(wrow[j] + 8 * r8) : make_uint4(0, 0, 0, 0);
+      for (int o = 0; o < PACK; ++o)
 #pragma unroll
-      for (int part = 0; part < (PACK == 0 ? 3 : 1); ++part) {
+        for (int s = 0; s < 2; ++s) t[o][s] = *reinterpret_cast<const uint4 *>(trow[s] + 32 * o);
+    }
+  }
+  // base of this lane's rows 16 s + l16, in flight during the product (rows and
+  // columns past the end read the last ones and are not stored)
+  constexpr int BH = BF ? 2 : 4;
+  uint4 base[2][BH];
+  if (p.base) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          if (16 * s >= n) break;
-          const uint4 t = *reinterpret_cast<const uint4 *>(parts + (16 * s + l16) * rstride + part * pstride + 32 * o + 8 * q);
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t, acc[s][j]);
+      for (int h = 0; h < BH; ++h) {
+        const int64_t at = (int64_t)rows[s] * p.N + min(BF ? c0 + 32 * h + 8 * q : c0 + 16 * h + 4 * q, p.N - (BF ? 8 : 4));
+        base[s][h] = BF ? load16(reinterpret_cast<const uint16_t *>(p.base) + at) : load16(reinterpret_cast<const float *>(p.base) + at);
+      }
+  } else {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int h = 0; h < BH; ++h) base[s][h] = make_uint4(0, 0, 0, 0);
+  }
+  f32x4_t acc[2][4] = {};  // [16 rows][16 columns]
+  if (l >= 0) {
+    if constexpr (PACK != 0) {
+#pragma unroll
+      for (int o = 0; o < PACK; ++o) {
+        if (o == 1 && q >= 2) {  // the third part and 16 empty places; the other weights are the first step's
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (r0 + 16 * s >= n) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t[o][s], acc[s][j]);
+        }
+      }
+    } else {
+      for (int o = 0; o < (nr8 + 3) / 4; ++o) {
+        if (o > 0) load_w(o);
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) t[0][s] = *reinterpret_cast<const uint4 *>(trow[s] + 96 * o + 32 * part);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (r0 + 16 * s >= n) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t[0][s], acc[s][j]);
+          }
         }
       }
     }
   }
 #pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    const int i = 16 * s + l16;
-    if (i >= n) continue;
-    const int64_t at = (int64_t)order[i] * p.N;
-    if constexpr (BF) {
+  for (int s = 0; s < 2; ++s) {
+    if (r0 + 16 * s + l16 >= n) continue;
+    const int64_t at = (int64_t)rows[s] * p.N;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = c0 + 32 * h + 8 * q;
-        if (c >= p.N) continue;
-        float v[8] = {};
-        if (p.base) load_elems8<true>(p.base, at + c, v);
+    for (int h = 0; h < BH; ++h) {
+      const int c = c0 + (BF ? 32 * h + 8 * q : 16 * h + 4 * q);
+      if (c >= p.N) continue;
+      if constexpr (BF) {
+        float v[8];
+        unpack_bf16x8(base[s][h], v);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           v[k] += acc[s][2 * h][k];
           v[4 + k] += acc[s][2 * h + 1][k];
         }
         store_elems8<true>(p.out, at + c, v);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 16 * j + 4 * q;
-        if (c >= p.N) continue;
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (p.base) b = load16(reinterpret_cast<const float *>(p.base) + at + c);
+      } else {
+        const uint4 b = base[s][h];
         store16(reinterpret_cast<float *>(p.out) + at + c,
-                make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[s][j][0]), __float_as_uint(__uint_as_float(b.y) + acc[s][j][1]),
-                           __float_as_uint(__uint_as_float(b.z) + acc[s][j][2]), __float_as_uint(__uint_as_float(b.w) + acc[s][j][3])));
+                make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[s][h][0]), __float_as_uint(__uint_as_float(b.y) + acc[s][h][1]),
+                           __float_as_uint(__uint_as_float(b.z) + acc[s][h][2]), __float_as_uint(__uint_as_float(b.w) + acc[s][h][3])));
       }
     }
   }
@@ -620,29 +702,38 @@ hipError_t launch_adapter_plan(const int32_t *ids, int R, int L, const AdapterPl
   return hipGetLastError();
 }
 
-hipError_t launch_adapter_shrink(const ShrinkArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)a.plan.max_tiles), block(256);
-  if (a.rank <= 16) hipLaunchKernelGGL(k_shrink<1>, grid, block, 0, s, a);
-  else if (a.rank <= 32) hipLaunchKernelGGL(k_shrink<2>, grid, block, 0, s, a);
-  else if (a.rank <= 64) hipLaunchKernelGGL(k_shrink<4>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_shrink<8>, grid, block, 0, s, a);
-  return hipGetLastError();
+// Slices of K, each a multiple of 64 and at least kSliceMin wide: up to 8 where
+// there are few tiles to fill the chip with, else up to 4 (1003 rows of rank 32, K =
+// 1440: 5.1 us with 8, 5.9 with 4, 10.2 with 1; 32768 rows of rank 16, K = 2048,
+// product and join: 37.3, 33.7 and 38.4 us).
+static int slice_width(int R, int K) {
+  const int w = (int)cdiv(cdiv(K, R < 4096 ? 8 : 4), 64) * 64;
+  return w < kSliceMin ? kSliceMin : w;
 }
+int adapter_slices(int R, int K) { return (int)cdiv(K, slice_width(R, K)); }
+size_t adapter_parts_elems(int R, int rank) { return (size_t)R * 32 * part_steps(rank); }
 
-hipError_t launch_adapter_expand(const ExpandArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)a.plan.max_tiles, (unsigned)cdiv(a.N, 256)), block(256);
-  const int pack = a.rank == 8 ? 1 : a.rank == 16 ? 2 : 0;
-  const int steps = pack ? pack : 3 * (int)cdiv(a.rank, 32);
-  const size_t lds = (size_t)kAdTile * (steps * 32 + 8) * sizeof(uint16_t);  // at most 50 KB
+hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
+  const int slice = slice_width(a.R, a.K), slices = adapter_slices(a.R, a.K), pack = part_pack(a.rank);
+  const dim3 grid((unsigned)(a.plan.max_tiles * slices)), block(256);
+  if (a.rank <= 16) hipLaunchKernelGGL(k_shrink<1>, grid, block, 0, s, a, slices, slice);
+  else if (a.rank <= 32) hipLaunchKernelGGL(k_shrink<2>, grid, block, 0, s, a, slices, slice);
+  else if (a.rank <= 64) hipLaunchKernelGGL(k_shrink<4>, grid, block, 0, s, a, slices, slice);
+  else hipLaunchKernelGGL(k_shrink<8>, grid, block, 0, s, a, slices, slice);
+  const int64_t items = (int64_t)a.R * (pack ? a.rank / 8 : cdiv(a.rank, 32) * 4);
+  hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices, a.L, a.ids);
+  if (!a.out) return hipGetLastError();
+  const int blocks = (int)cdiv(a.N, 128);
+  const dim3 eg((unsigned)(a.plan.max_tiles * blocks));
   if (pack == 1) {
-    if (a.bf16) hipLaunchKernelGGL((k_expand<1, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_expand<1, false>), grid, block, lds, s, a);
+    if (a.bf16) hipLaunchKernelGGL((k_expand<1, true>), eg, block, 0, s, a, blocks);
+    else hipLaunchKernelGGL((k_expand<1, false>), eg, block, 0, s, a, blocks);
   } else if (pack == 2) {
-    if (a.bf16) hipLaunchKernelGGL((k_expand<2, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_expand<2, false>), grid, block, lds, s, a);
+    if (a.bf16) hipLaunchKernelGGL((k_expand<2, true>), eg, block, 0, s, a, blocks);
+    else hipLaunchKernelGGL((k_expand<2, false>), eg, block, 0, s, a, blocks);
   } else {
-    if (a.bf16) hipLaunchKernelGGL((k_expand<0, true>), grid, block, lds, s, a);
-    else hipLaunchKernelGGL((k_expand<0, false>), grid, block, lds, s, a);
+    if (a.bf16) hipLaunchKernelGGL((k_expand<0, true>), eg, block, 0, s, a, blocks);
+    else hipLaunchKernelGGL((k_expand<0, false>), eg, block, 0, s, a, blocks);
   }
   return hipGetLastError();
 }

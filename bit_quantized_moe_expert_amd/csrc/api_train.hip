@@ -98,8 +98,9 @@ struct Bump {
 
 struct AdapterCarve {
   void *plan;
-  float *t;                     // forward: [R, rank]
-  float *u;                     // backward
+  float *slices;                // partial low-rank products
+  uint16_t *parts;              // the low-rank product for the second one
+  float *u;                     // backward: [R, rank]
   uint16_t *At, *Bt;            // [L, K, rank], [L, rank, N]
   float *partial;
   size_t bytes;
@@ -112,9 +113,9 @@ AdapterCarve carve_adapter(void *ws, const nf4moe_adapters_t &a, int R, bool bac
   Bump b{(char *)ws};
   AdapterPlan lay;
   c.plan = b.take<char>(adapter_plan_layout(R, a.L, nullptr, &lay));
-  if (!backward) {
-    c.t = b.take<float>((size_t)R * a.rank);
-  } else {
+  c.slices = b.take<float>((size_t)adapter_slices(R, backward ? a.N : a.K) * R * a.rank);
+  c.parts = b.take<uint16_t>(adapter_parts_elems(R, a.rank));
+  if (backward) {
     c.u = b.take<float>((size_t)R * a.rank);
     c.At = b.take<uint16_t>((size_t)a.L * a.K * a.rank);
     c.Bt = b.take<uint16_t>((size_t)a.L * a.N * a.rank);
@@ -276,9 +277,13 @@ size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, in
   return carve_adapter(nullptr, *ad, R, backward != 0).bytes;
 }
 
-// Rows, gather, ids and plan, as both directions take them.
+// Rows, gather, ids and plan, as both directions take them; `cols` is the widest
+// output (the last kernel runs a workgroup per 64 rows and 256 columns).
 static nf4moe_status_t check_adapter_rows(int32_t R, int32_t x_rows, const int32_t *x_row_of, const int32_t *ids,
-                                          const void *plan, size_t plan_bytes, int32_t L) {
+                                          const void *plan, size_t plan_bytes, int32_t L, int32_t cols) {
+  const int64_t tiles = cdiv(R, kAdTile) + (R < L + 1 ? R : L + 1), per = cdiv(cols, 256);
+  if (tiles * (per < 8 ? 8 : per) > 0x7fffffff)
+    return fail(NF4MOE_ERR_UNSUPPORTED, "R=%d rows of %d columns are too many for one call", R, cols);
   if (x_rows < 1 || (!x_row_of && x_rows < R))
     return fail(NF4MOE_ERR_INVALID_ARG, "x_rows=%d too small for R=%d%s", x_rows, R, x_row_of ? "" : " without a gather");
   if (!ids) return fail(NF4MOE_ERR_INVALID_ARG, "ids is NULL");
@@ -299,7 +304,7 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   if (st != NF4MOE_OK) return st;
   if (!dt_ok(dtype)) return fail(NF4MOE_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
   if (R == 0) return NF4MOE_OK;
-  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L)) != NF4MOE_OK) return st;
+  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, ad->N)) != NF4MOE_OK) return st;
   if (!x || !out) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(x, 2) || !aligned(base, dt_bytes(dtype)) || !aligned(out, dt_bytes(dtype)) || !aligned(t, 16))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
@@ -318,10 +323,8 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
   hipError_t e = plan ? hipSuccess : launch_adapter_plan(ids, R, ad->L, p, s);
   if (e != hipSuccess) return hip_status(e, "adapter plan launch");
-  float *low = t ? t : c.t;
-  e = launch_adapter_shrink({p, x, x_row_of, x_rows, ad->A, nullptr, ad->K, ad->rank, low}, s);
-  if (e != hipSuccess) return hip_status(e, "adapter shrink launch");
-  return hip_status(launch_adapter_expand({p, low, ad->B, ad->scale, ad->N, ad->rank, base, out, bf}, s), "adapter expand launch");
+  return hip_status(launch_adapter_low_rank({p, ids, R, ad->L, x, x_row_of, x_rows, ad->A, ad->B, ad->scale, ad->K, ad->N, ad->rank,
+                                             t, false, base, out, bf, c.slices, c.parts}, s), "adapter launch");
 }
 
 nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint16_t *dy, nf4moe_src_t x_src, const void *x,
@@ -344,7 +347,7 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
     if (e == hipSuccess && dB) e = launch_fill_f32_zero(dB, (int64_t)ad->L * ad->rank * ad->N, s);
     return hip_status(e, "fill launch");
   }
-  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L)) != NF4MOE_OK) return st;
+  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, ad->K)) != NF4MOE_OK) return st;
   if (!dy || (dA && (!x || (held && !x_scale))) || (dB && !t)) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(dy, 2) || !aligned(x, held ? 1 : 2) || !aligned(t, 16) || !aligned(dx_base, dt_bytes(dx_dtype)) ||
       !aligned(dx, dt_bytes(dx_dtype)))
@@ -359,17 +362,15 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
   if (!plan && (e = launch_adapter_plan(ids, R, ad->L, p, s)) != hipSuccess) return hip_status(e, "adapter plan launch");
   if (dx || dA) {
-    // u = s B^T dy: the shrink with B as [L, rank, N]
+    // u = s B^T dy and dx = dx_base + A^T u: the forward's kernel on B as [L, rank, N]
+    // and A as [L, K, rank]
     e = launch_transpose_bf16(ad->B, c.Bt, ad->L, ad->N, ad->rank, s);
-    if (e == hipSuccess) e = launch_adapter_shrink({p, dy, nullptr, R, c.Bt, ad->scale, ad->N, ad->rank, c.u}, s);
-    if (e != hipSuccess) return hip_status(e, "adapter backward shrink launch");
-  }
-  if (dx) {
-    // dx = dx_base + A^T u: the expand with A as [L, K, rank]
-    e = launch_transpose_bf16(ad->A, c.At, ad->L, ad->rank, ad->K, s);
+    if (e == hipSuccess && dx) e = launch_transpose_bf16(ad->A, c.At, ad->L, ad->rank, ad->K, s);
     if (e == hipSuccess)
-      e = launch_adapter_expand({p, c.u, c.At, nullptr, ad->K, ad->rank, dx_base, dx, dx_dtype == NF4MOE_DT_BF16}, s);
-    if (e != hipSuccess) return hip_status(e, "adapter backward expand launch");
+      e = launch_adapter_low_rank({p, ids, R, ad->L, dy, nullptr, R, c.Bt, c.At, ad->scale, ad->N, ad->K, ad->rank,
+                                   dA ? c.u : nullptr, true, dx_base, dx, dx_dtype == NF4MOE_DT_BF16, c.slices,
+                                   dx ? c.parts : nullptr}, s);
+    if (e != hipSuccess) return hip_status(e, "adapter backward launch");
   }
   if (dA) {
     e = launch_adapter_rowgrad({p, c.u, x, x_scale, x_src, x_row_of, x_rows, nullptr, ad->L, ad->K, ad->rank, false, dA, c.partial}, s);

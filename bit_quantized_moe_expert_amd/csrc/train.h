@@ -87,32 +87,31 @@ int adapter_chunk_rows(int R);
 size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p);   // bytes
 hipError_t launch_adapter_plan(const int32_t *ids, int R, int L, const AdapterPlan &p, hipStream_t s);
 
-// out[row][j] = m_l sum_k x[row'][k] W_l[j][k] for the rows of adapter l (W [L, rank, K]
-// bf16); zeros for rows without one. m: scale [L] or null; row' by row_of.
-struct ShrinkArgs {
+// v[row][j] = sum_k x[row'][k] W1_l[j][k] for the rows of adapter l (W1 [L, rank, K]
+// bf16), row' by row_of, and out[row][c] = base[row][c] + sum_j (m_l v[row][j])
+// W2_l[c][j] (W2 [L, N, rank] bf16). low (optional): v, or m_l v with low_scaled, by
+// row; zeros for rows without an adapter. m: scale [L] or null. out null: low alone.
+struct LowRankArgs {
   AdapterPlan plan;
+  const int32_t *ids;
+  int R, L;
   const uint16_t *x;
   const int32_t *row_of;
   int x_rows;
-  const uint16_t *W;
+  const uint16_t *W1, *W2;
   const float *scale;
-  int K, rank;
-  float *out;
-};
-hipError_t launch_adapter_shrink(const ShrinkArgs &a, hipStream_t s);
-
-// out[row][n] = base[row][n] + m_l sum_j t[row][j] W_l[n][j] (W [L, N, rank] bf16).
-struct ExpandArgs {
-  AdapterPlan plan;
-  const float *t;
-  const uint16_t *W;
-  const float *scale;
-  int N, rank;
+  int K, N, rank;
+  float *low;
+  bool low_scaled;
   const void *base;    // or null: zeros
   void *out;
   bool bf16;           // base and out
+  float *partial;      // scratch: [adapter_slices(R, K)][R][rank]
+  uint16_t *parts;     // scratch: adapter_parts_elems(R, rank) (null without out)
 };
-hipError_t launch_adapter_expand(const ExpandArgs &a, hipStream_t s);
+int adapter_slices(int R, int K);
+size_t adapter_parts_elems(int R, int rank);
+hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s);
 
 // out_l[j][c] (or [c][j], transposed) = m_l sum over the rows of l of p[row][j] v[row'][c].
 struct RowGradArgs {
