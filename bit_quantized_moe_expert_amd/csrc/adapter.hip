@@ -63,9 +63,7 @@ int plan_rows(int R, int L) {
 
 __device__ inline int bin_of(int id, int L) { return id < 0 || id >= L ? L : id; }
 
-__global__ __launch_bounds__(kPlanThreads) void k_plan_hist(const int32_t *__restrict__ ids, int R, int L, int per,
-                                                            int32_t *__restrict__ hist) {
-  __shared__ int32_t cnt[kMaxAdapters + 1];
+__device__ inline void plan_hist(const int32_t *__restrict__ ids, int R, int L, int per, int32_t *__restrict__ hist, int32_t *cnt) {
   for (int b = threadIdx.x; b <= L; b += kPlanThreads) cnt[b] = 0;
   __syncthreads();
   const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
@@ -74,130 +72,182 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_hist(const int32_t *__res
   for (int b = threadIdx.x; b <= L; b += kPlanThreads) hist[(int64_t)blockIdx.x * (L + 1) + b] = cnt[b];
 }
 
-// Exclusive prefix of v over the workgroup's threads in order; total in *sum.
-__device__ inline int32_t block_prefix(int32_t v, int32_t *wsum, int32_t *sum) {
+// Turned copies of the adapters' weights for the backward: [L][P][Q] -> [L][Q][P],
+// in pieces of pt x qt (multiples of 8, at most 8192 elements): 16-byte loads along
+// Q, 16-byte stores along P.
+struct TurnArgs {
+  const uint16_t *in;
+  uint16_t *out;
+  int P, Q, pt, qt, np, nq;  // np x nq pieces per adapter
+};
+constexpr int kTurnElems = 8192;
+__device__ inline void turn_piece(const TurnArgs &a, int64_t piece, uint16_t *tile) {
+  const int64_t base = piece / (a.np * a.nq) * a.P * a.Q;
+  const int rest = (int)(piece % (a.np * a.nq));
+  const int p0 = rest / a.nq * a.pt, q0 = rest % a.nq * a.qt;
+  const int stride = a.pt + 8;
+  const int q8 = a.qt / 8, p8 = a.pt / 8;
+  for (int i = threadIdx.x; i < a.pt * q8; i += kPlanThreads) {
+    const int p = i / q8, q = 8 * (i % q8);
+    if (p0 + p >= a.P || q0 + q >= a.Q) continue;
+    const uint4 v = load16(a.in + base + (int64_t)(p0 + p) * a.Q + q0 + q);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) tile[(q + k) * stride + p] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.qt * p8; i += kPlanThreads) {
+    const int q = i / p8, p = 8 * (i % p8);
+    if (p0 + p >= a.P || q0 + q >= a.Q) continue;
+    store16(a.out + base + (int64_t)(q0 + q) * a.P + p0 + p, *reinterpret_cast<const uint4 *>(tile + q * stride + p));
+  }
+}
+
+// What the later launches need and what does not depend on anything: the row
+// counters per plan workgroup, and the backward's turned weights (0, 1 or 2 arrays).
+__global__ __launch_bounds__(kPlanThreads) void k_prepare(const int32_t *__restrict__ ids, int R, int L, int per, int hists,
+                                                          int32_t *__restrict__ hist, TurnArgs t0, TurnArgs t1, int64_t n0) {
+  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
+  if ((int)blockIdx.x < hists) {
+    plan_hist(ids, R, L, per, hist, reinterpret_cast<int32_t *>(lds));
+    return;
+  }
+  const int64_t piece = (int64_t)blockIdx.x - hists;
+  if (piece < n0) turn_piece(t0, piece, lds);
+  else turn_piece(t1, piece - n0, lds);
+}
+
+// Exclusive prefixes of four counts over the workgroup's threads in order; totals in *sum.
+__device__ inline int4 block_prefix4(int4 v, int4 *wsum, int4 *sum) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int32_t x = v;
+  int4 x = v;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int32_t y = __shfl_up(x, d, kWave);
-    if (lane >= d) x += y;
+    const int4 y = make_int4(__shfl_up(x.x, d, kWave), __shfl_up(x.y, d, kWave), __shfl_up(x.z, d, kWave), __shfl_up(x.w, d, kWave));
+    if (lane >= d) x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
   }
   if (lane == 63) wsum[wave] = x;
   __syncthreads();
-  int32_t before = 0, all = 0;
+  int4 before = make_int4(0, 0, 0, 0), all = make_int4(0, 0, 0, 0);
+#pragma unroll
   for (int w = 0; w < kPlanThreads / 64; ++w) {
-    const int32_t s = wsum[w];
-    if (w < wave) before += s;
-    all += s;
+    const int4 s = wsum[w];
+    if (w < wave) before.x += s.x, before.y += s.y, before.z += s.z, before.w += s.w;
+    all.x += s.x, all.y += s.y, all.z += s.z, all.w += s.w;
   }
-  __syncthreads();
   *sum = all;
-  return before + x - v;
+  return make_int4(before.x + x.x - v.x, before.y + x.y - v.y, before.z + x.z - v.z, before.w + x.w - v.w);
 }
 
 // One workgroup per `per` rows. Each finds, for every bin, where its own rows of
 // that bin begin (all counters of the earlier workgroups and bins), then places
-// its rows in order, 1024 at a time: ranks inside a wave by ballots, and one
-// turn per wave for the running counters, so the order is stable. Workgroup 0
-// also writes the tile and chunk tables.
+// its rows in order, 1024 at a time: ranks inside a wave by ballots, then the
+// waves' counts of each bin in wave order, so the order is stable. Workgroup 0 also
+// writes the tile and chunk tables.
+constexpr int kWaveBins = 1024;  // up to so many bins the waves' counts have a place each in LDS
 __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__restrict__ ids, int R, int L, int per,
                                                                int groups, int chunk_rows, AdapterPlan p) {
-  __shared__ int32_t next[kMaxAdapters + 1];
-  __shared__ int32_t wsum[kPlanThreads / 64];
+  constexpr int W = kPlanThreads / 64;
+  __shared__ int32_t next[kMaxAdapters + 1], tot[kMaxAdapters + 1];
+  __shared__ uint16_t wcnt[W][kWaveBins];
+  __shared__ int4 wsum[W];
   const int tid = threadIdx.x, nb = L + 1;
-  const int seg = (nb + kPlanThreads - 1) / kPlanThreads, b0 = tid * seg, b1 = min(nb, b0 + seg);  // this thread's bins
-  constexpr int kSeg = (kMaxAdapters + 1 + kPlanThreads - 1) / kPlanThreads;
-  int32_t total[kSeg], mine[kSeg];
+  const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
+  int b = r0 + tid < r1 ? bin_of(ids[r0 + tid], L) : -1;
+  for (int i = tid; i < nb; i += kPlanThreads) next[i] = tot[i] = 0;
+  __syncthreads();
   if (groups == 1) {
-    for (int b = tid; b < nb; b += kPlanThreads) next[b] = 0;
-    __syncthreads();
-    for (int r = tid; r < R; r += kPlanThreads) atomicAdd(&next[bin_of(ids[r], L)], 1);
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < kSeg; ++i) {
-    total[i] = mine[i] = 0;
-    if (b0 + i >= b1) continue;
-    if (groups == 1) {
-      total[i] = next[b0 + i];
-    } else {
-      for (int g = 0; g < groups; ++g) {
-        const int32_t c = p.hist[(int64_t)g * nb + b0 + i];
-        total[i] += c;
-        if (g < (int)blockIdx.x) mine[i] += c;
-      }
-    }
-  }
-  int32_t rows = 0, sum;
-#pragma unroll
-  for (int i = 0; i < kSeg; ++i) rows += total[i];
-  int32_t off = block_prefix(rows, wsum, &sum);  // (its barriers also end the reads of next above)
-  int32_t first[kSeg];
-#pragma unroll
-  for (int i = 0; i < kSeg; ++i) {
-    first[i] = off;
-    if (b0 + i < b1) next[b0 + i] = off + mine[i];
-    off += total[i];
-  }
-  if (blockIdx.x == 0) {
-    int32_t nt = 0, nc = 0, ns = 0;
-#pragma unroll
-    for (int i = 0; i < kSeg; ++i) {
-      nt += (total[i] + kAdTile - 1) / kAdTile;
-      const int32_t c = b0 + i < L ? (total[i] + chunk_rows - 1) / chunk_rows : 0;
-      nc += c;
-      ns += c > 1 ? c : 0;
-    }
-    int32_t t_all, c_all, s_all;
-    int32_t t = block_prefix(nt, wsum, &t_all);
-    int32_t c = block_prefix(nc, wsum, &c_all);
-    int32_t s = block_prefix(ns, wsum, &s_all);
-    if (tid == 0) {
-      p.counts[0] = t_all;
-      p.counts[1] = c_all;
-    }
-#pragma unroll
-    for (int i = 0; i < kSeg; ++i) {
-      const int b = b0 + i;
-      if (b >= b1) continue;
-      for (int32_t r = 0; r < total[i]; r += kAdTile)
-        p.tiles[t++] = make_int4(b < L ? b : -1, first[i] + r, min(kAdTile, total[i] - r), 0);
-      if (b >= L) continue;
-      const int32_t n = (total[i] + chunk_rows - 1) / chunk_rows;
-      p.chunks_of[b] = make_int2(n, s);
-      for (int32_t k = 0; k < n; ++k)
-        p.chunks[c++] = make_int4(b, first[i] + k * chunk_rows, min(chunk_rows, total[i] - k * chunk_rows), n > 1 ? s + k : -1);
-      if (n > 1) s += n;
+    if (b >= 0) atomicAdd(&tot[b], 1);
+    for (int r = r0 + kPlanThreads + tid; r < r1; r += kPlanThreads) atomicAdd(&tot[bin_of(ids[r], L)], 1);
+  } else {
+    for (int i = tid; i < nb * groups; i += kPlanThreads) {
+      const int32_t c = p.hist[i];
+      if (c == 0) continue;
+      const int g = i / nb, bin = i % nb;
+      atomicAdd(&tot[bin], c);
+      if (g < (int)blockIdx.x) atomicAdd(&next[bin], c);
     }
   }
   __syncthreads();
+  const int seg = (nb + kPlanThreads - 1) / kPlanThreads, b0 = tid * seg, b1 = min(nb, b0 + seg);  // this thread's bins
+  int4 sums = make_int4(0, 0, 0, 0), all;  // rows, tiles, chunks, slots
+  for (int i = b0; i < b1; ++i) {
+    const int32_t n = tot[i];
+    const int32_t c = i < L ? (n + chunk_rows - 1) / chunk_rows : 0;
+    sums.x += n;
+    sums.y += (n + kAdTile - 1) / kAdTile;
+    sums.z += c;
+    sums.w += c > 1 ? c : 0;
+  }
+  int4 at = block_prefix4(sums, wsum, &all);
+  if (blockIdx.x == 0 && tid == 0) {
+    p.counts[0] = all.y;
+    p.counts[1] = all.z;
+  }
+  for (int i = b0; i < b1; ++i) {
+    const int32_t n = tot[i];
+    next[i] += at.x;
+    if (blockIdx.x == 0) {
+      for (int32_t r = 0; r < n; r += kAdTile) p.tiles[at.y++] = make_int4(i < L ? i : -1, at.x + r, min(kAdTile, n - r), 0);
+      if (i < L) {
+        const int32_t c = (n + chunk_rows - 1) / chunk_rows;
+        p.chunks_of[i] = make_int2(c, at.w);
+        for (int32_t k = 0; k < c; ++k)
+          p.chunks[at.z++] = make_int4(i, at.x + k * chunk_rows, min(chunk_rows, n - k * chunk_rows), c > 1 ? at.w + k : -1);
+        if (c > 1) at.w += c;
+      }
+    }
+    at.x += n;
+  }
+  __syncthreads();
   const int lane = tid & 63, wave = tid >> 6;
-  const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
   for (int base = r0; base < r1; base += kPlanThreads) {
     const int r = base + tid;
     const bool live = r < r1;
-    const int b = live ? bin_of(ids[r], L) : -1;
+    if (base != r0) b = live ? bin_of(ids[r], L) : -1;
+    if (nb <= kWaveBins) {
+      for (int i = tid; i < W * nb; i += kPlanThreads) wcnt[i / nb][i % nb] = 0;
+      __syncthreads();
+    }
     uint64_t todo = __ballot(live), same = 0;
     while (todo) {
       const int lead = __builtin_ctzll(todo);
-      const int lb = __shfl(b, lead, kWave);
+      const int lb = __builtin_amdgcn_readlane(b, lead);
       const uint64_t m = __ballot(live && b == lb);
       if (b == lb) same = m;
       todo &= ~m;
     }
     const int rank = __popcll(same & lanemask_lt());
     const int lead = same ? __builtin_ctzll(same) : 0;
-    int32_t at = 0;
-    for (int w = 0; w < kPlanThreads / 64; ++w) {
-      if (wave == w && live && lane == lead) {
-        at = next[b];
-        next[b] = at + __popcll(same);
+    int32_t first = 0;
+    if (nb <= kWaveBins) {
+      if (live && lane == lead) wcnt[wave][b] = (uint16_t)__popcll(same);
+      __syncthreads();
+      for (int i = tid; i < nb; i += kPlanThreads) {  // counts to prefixes, in wave order
+        uint32_t run = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const uint32_t c = wcnt[w][i];
+          wcnt[w][i] = (uint16_t)run;
+          run += c;
+        }
+        tot[i] = next[i];       // where this round's rows of the bin begin
+        next[i] += (int32_t)run;
       }
       __syncthreads();
+      if (live) first = tot[b] + wcnt[wave][b];
+      __syncthreads();          // both are written again in the next round
+    } else {
+      for (int w = 0; w < W; ++w) {
+        if (wave == w && live && lane == lead) {
+          first = next[b];
+          next[b] = first + __popcll(same);
+        }
+        __syncthreads();
+      }
+      first = __shfl(first, lead, kWave);
     }
-    at = __shfl(at, lead, kWave);
-    if (live) p.order[at + rank] = r;
+    if (live) p.order[first + rank] = r;
   }
 }
 
@@ -468,35 +518,30 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
 // Sums over rows: the contraction runs along the rows, across the storage order of
 // both operands. A lane loads 8 neighbouring columns of 8 rows and turns the 8 x 8
 // block in registers (one v_perm_b32 per pair of values), which gives it, for each
-// of its 8 columns, 8 consecutive rows: the matrix operand, with no LDS. 32 rows and
-// 128 columns a wave and step. p's rows are split into three bf16 parts in
-// registers. An adapter with one chunk is written straight out; the chunks of
-// others go to partial sums that k_rowgrad_join adds in order.
+// of its 8 columns, 8 consecutive rows: the matrix operand, with no LDS. p's rows
+// are split into three bf16 parts in registers. One workgroup per chunk of rows and
+// 128 columns, its four waves taking every fourth step of 32 rows; their sums are
+// added in order through LDS, from which they leave in either layout. An adapter
+// with one chunk is written straight out; the chunks of others go to partial sums
+// that k_rowgrad_join adds in order. dA and dB run in one launch.
+constexpr int kGradCols = 128;
+
 template <int SRC, int RT>
-__global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p) {
-  if ((int)blockIdx.x >= p.plan.counts[1]) return;
-  const int4 chunk = p.plan.chunks[blockIdx.x];
-  const int l = chunk.x, n = chunk.z;
-  const int32_t *order = p.plan.order + chunk.y;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+__device__ inline void rowgrad_body(const RowGradOne &p, const int4 chunk, int cw, int j0, int rank, const int32_t *prow,
+                                    const int32_t *vrow, float (*tile)[kGradCols + 4]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
-  const int cw = blockIdx.y * 512 + wave * 128;
-  if (cw >= p.C) return;
-  const int j0 = blockIdx.z * (16 * RT);
+  const int l = chunk.x, n = chunk.z;
   const int c = min(cw + 8 * l16, p.C - 8);  // past the end: a valid place, not stored
   f32x4_t acc[RT][8] = {};
-  for (int r0 = 0; r0 < n; r0 += 32) {
-    int32_t row[8];
+  for (int r0 = 32 * wave; r0 < n; r0 += 128) {
     uint32_t blk[4][8];  // rows (2 i, 2 i + 1) of column k as one word: [i][k]
     uint4 raw[8];
     uint32_t sc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) row[i] = order[min(r0 + 8 * q + i, n - 1)];
+    const bool whole = r0 + 32 <= n;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      int r = row[i];
-      if (p.row_of) r = min(max(p.row_of[r], 0), p.v_rows - 1);
-      const int64_t at = (int64_t)r * p.C + c;
+      const int64_t at = (int64_t)vrow[min(r0 + 8 * q + i, n - 1)] * p.C + c;
       if constexpr (SRC == SRC_BF16) {
         raw[i] = load16(reinterpret_cast<const uint16_t *>(p.v) + at);
       } else {
@@ -505,24 +550,26 @@ __global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p) {
         sc[i] = p.v_scale[at >> 5];
       }
     }
-    if (r0 + 32 > n) {  // places past the chunk hold zeros in both operands (0 x infinity is not 0)
+    float pv[RT][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float *src = p.p + (int64_t)prow[min(r0 + 8 * q + i, n - 1)] * rank;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) pv[t][i] = src[min(j0 + 16 * t + l16, rank - 1)];
+    }
+    if (!whole) {  // places past the chunk hold zeros in both operands (0 x infinity is not 0)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (r0 + 8 * q + i >= n) {
           raw[i] = make_uint4(0, 0, 0, 0);
           sc[i] = 0;
+#pragma unroll
+          for (int t = 0; t < RT; ++t) pv[t][i] = 0.0f;
         }
     }
     uint4 a[RT][3];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const int j = j0 + 16 * t + l16;
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = r0 + 8 * q + i < n && j < p.rank ? p.p[(int64_t)row[i] * p.rank + j] : 0.0f;
-      split3(v, a[t][0], a[t][1], a[t][2]);
-    }
+    for (int t = 0; t < RT; ++t) split3(pv[t], a[t][0], a[t][1], a[t][2]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (SRC == SRC_BF16) {
@@ -552,56 +599,82 @@ __global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p) {
     }
   }
   // lane: columns cw + 8 l16 + k, ranks j0 + 16 t + 4 q ..
-  if (cw + 8 * l16 >= p.C) return;
-  const int64_t size = (int64_t)p.rank * p.C;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float *d = &tile[16 * t + 4 * q + i][8 * l16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f32x4_t v = {acc[t][4 * h][i], acc[t][4 * h + 1][i], acc[t][4 * h + 2][i], acc[t][4 * h + 3][i]};
+            f32x4_t *e = reinterpret_cast<f32x4_t *>(d + 4 * h);
+            *e = w == 0 ? v : *e + v;
+          }
+        }
+    }
+    lds_barrier();
+  }
+  const int64_t size = (int64_t)rank * p.C;
   float *out = chunk.w < 0 ? p.out + l * size : p.partial + chunk.w * size;
   const float m = p.scale ? p.scale[l] : 1.0f;
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int j = j0 + 16 * t + 4 * q;
-    if (j >= p.rank) continue;
-    if (p.transposed) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) *reinterpret_cast<f32x4_t *>(out + (int64_t)(c + k) * p.rank + j) = acc[t][k] * m;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = acc[t][k][i] * m;
-        store_elems8<false>(out, (int64_t)(j + i) * p.C + c, v);
-      }
+  const int cols = min(kGradCols, p.C - cw), ranks = min(16 * RT, rank - j0);  // multiples of 8
+  if (p.transposed) {
+    const int r4 = ranks / 4;
+    for (int i = tid; i < cols * r4; i += 256) {
+      const int cc = i / r4, j = 4 * (i % r4);
+      const f32x4_t v = {tile[j][cc], tile[j + 1][cc], tile[j + 2][cc], tile[j + 3][cc]};
+      *reinterpret_cast<f32x4_t *>(out + (int64_t)(cw + cc) * rank + j0 + j) = v * m;
+    }
+  } else {
+    const int c4 = cols / 4;
+    for (int i = tid; i < ranks * c4; i += 256) {
+      const int j = i / c4, cc = 4 * (i % c4);
+      *reinterpret_cast<f32x4_t *>(out + (int64_t)(j0 + j) * p.C + cw + cc) = *reinterpret_cast<const f32x4_t *>(&tile[j][cc]) * m;
     }
   }
 }
 
+template <int SRC, int RT>
+__global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p, int na, int nb) {
+  __shared__ __attribute__((aligned(16))) float tile[16 * RT][kGradCols + 4];
+  __shared__ int32_t prow[kMaxChunk], vrow[kMaxChunk];
+  const int per = na + nb, ci = blockIdx.x / per, block = blockIdx.x % per;
+  if (ci >= p.plan.counts[1]) return;
+  const int4 chunk = p.plan.chunks[ci];
+  const bool first = block < na;
+  const int32_t *row_of = first ? p.a.row_of : p.b.row_of;
+  const int last = (first ? p.a.v_rows : p.b.v_rows) - 1;
+  for (int i = threadIdx.x; i < chunk.z; i += 256) {
+    const int r = p.plan.order[chunk.y + i];
+    prow[i] = r;
+    vrow[i] = row_of ? min(max(row_of[r], 0), last) : r;
+  }
+  lds_barrier();
+  const int j0 = blockIdx.y * (16 * RT);
+  if (first) rowgrad_body<SRC, RT>(p.a, chunk, block * kGradCols, j0, p.rank, prow, vrow, tile);
+  else rowgrad_body<SRC_BF16, RT>(p.b, chunk, (block - na) * kGradCols, j0, p.rank, prow, vrow, tile);
+}
+
 // The chunks of an adapter, added in order; zeros for an adapter without rows.
-__global__ __launch_bounds__(256) void k_rowgrad_join(const int2 *__restrict__ chunks_of, const float *__restrict__ partial,
-                                                      int64_t size, float *__restrict__ out) {
-  const int2 c = chunks_of[blockIdx.y];
+__global__ __launch_bounds__(256) void k_rowgrad_join(RowGradArgs p, int64_t sa, int64_t sb) {
+  const int2 c = p.plan.chunks_of[blockIdx.y];
   if (c.x == 1) return;
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= size) return;
+  int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= sa + sb) return;
+  const bool first = i < sa;
+  const int64_t size = first ? sa : sb;
+  if (!first) i -= sa;
+  const float *partial = (first ? p.a.partial : p.b.partial) + c.y * size + i;
   f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < c.x; ++k) s += *reinterpret_cast<const f32x4_t *>(partial + (c.y + k) * size + i);
-  *reinterpret_cast<f32x4_t *>(out + blockIdx.y * size + i) = s;
+  for (int k = 0; k < c.x; ++k) s += *reinterpret_cast<const f32x4_t *>(partial + k * size);
+  *reinterpret_cast<f32x4_t *>((first ? p.a.out : p.b.out) + blockIdx.y * size + i) = s;
 }
 
 __global__ __launch_bounds__(256) void k_zero_f32(float *p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0.0f;
-}
-
-__global__ __launch_bounds__(256) void k_transpose_bf16(const uint16_t *__restrict__ in, uint16_t *__restrict__ out, int P,
-                                                        int Q) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t base = (int64_t)blockIdx.z * P * Q;
-  const int p0 = blockIdx.y * 64, q0 = blockIdx.x * 64;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += 4)
-    if (p0 + i < P && q0 + x < Q) tile[i][x] = in[base + (int64_t)(p0 + i) * Q + q0 + x];
-  __syncthreads();
-  for (int i = y; i < 64; i += 4)
-    if (q0 + i < Q && p0 + x < P) out[base + (int64_t)(q0 + i) * P + p0 + x] = tile[x][i];
 }
 
 // ------------------------------------------------------------------ few rows
@@ -664,10 +737,10 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterRowsArgs p) {
 
 }  // namespace
 
-// Rows of a gradient chunk: about 64 chunks' worth of rows, 64 to 2048.
+// Rows of a gradient chunk: about 32 chunks' worth of rows, 128 to kMaxChunk.
 int adapter_chunk_rows(int R) {
-  const int64_t c = cdiv(cdiv(R, 64), kAdTile) * kAdTile;
-  return (int)(c < kAdTile ? kAdTile : c > 2048 ? 2048 : c);
+  const int64_t c = cdiv(cdiv(R, 32), 64) * 64;
+  return (int)(c < 128 ? 128 : c > kMaxChunk ? kMaxChunk : c);
 }
 
 size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p) {
@@ -694,11 +767,41 @@ size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p) {
   return off;
 }
 
-hipError_t launch_adapter_plan(const int32_t *ids, int R, int L, const AdapterPlan &p, hipStream_t s) {
-  const int per = plan_rows(R, L);
-  const int groups = (int)cdiv(R, per);
-  if (groups > 1) hipLaunchKernelGGL(k_plan_hist, dim3(groups), dim3(kPlanThreads), 0, s, ids, R, L, per, p.hist);
-  hipLaunchKernelGGL(k_plan_scatter, dim3(groups), dim3(kPlanThreads), 0, s, ids, R, L, per, groups, adapter_chunk_rows(R), p);
+static TurnArgs turn_args(const uint16_t *in, uint16_t *out, int P, int Q, bool p_is_rank) {
+  TurnArgs t = {in, out, P, Q, P, Q, 1, 1};
+  if (p_is_rank) t.qt = (int)(kTurnElems / P / 8 * 8);
+  else t.pt = (int)(kTurnElems / Q / 8 * 8);
+  t.np = (int)cdiv(P, t.pt);
+  t.nq = (int)cdiv(Q, t.qt);
+  return t;
+}
+
+hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
+  const int per = plan_rows(a.R, a.L);
+  const int groups = a.ids ? (int)cdiv(a.R, per) : 0, hists = groups > 1 ? groups : 0;
+  TurnArgs t0 = {}, t1 = {};
+  int64_t n0 = 0, n1 = 0;
+  size_t lds = hists ? sizeof(int32_t) * (a.L + 1) : 0;
+  auto need = [&](const TurnArgs &t) {
+    const size_t b = (size_t)t.qt * (t.pt + 8) * sizeof(uint16_t);  // at most 32 KB (rank 8)
+    if (b > lds) lds = b;
+  };
+  if (a.Bt) {
+    t0 = turn_args(a.B, a.Bt, a.N, a.rank, false);
+    n0 = (int64_t)a.L * t0.np * t0.nq;
+    need(t0);
+  }
+  if (a.At) {
+    t1 = turn_args(a.A, a.At, a.rank, a.K, true);
+    n1 = (int64_t)a.L * t1.np * t1.nq;
+    need(t1);
+  }
+  if (hists + n0 + n1 > 0)
+    hipLaunchKernelGGL(k_prepare, dim3((unsigned)(hists + n0 + n1)), dim3(kPlanThreads), lds, s, a.ids, a.R, a.L, per, hists,
+                       a.plan.hist, t0, t1, n0);
+  if (groups > 0)
+    hipLaunchKernelGGL(k_plan_scatter, dim3(groups), dim3(kPlanThreads), 0, s, a.ids, a.R, a.L, per, groups,
+                       adapter_chunk_rows(a.R), a.plan);
   return hipGetLastError();
 }
 
@@ -741,31 +844,25 @@ hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
 template <int SRC>
 static void rowgrad_src(const RowGradArgs &a, hipStream_t s) {
   const dim3 block(256);
-  const unsigned gx = (unsigned)a.plan.max_chunks, gy = (unsigned)cdiv(a.C, 512);
-  if (a.rank <= 16) hipLaunchKernelGGL((k_rowgrad<SRC, 1>), dim3(gx, gy, 1), block, 0, s, a);
-  else if (a.rank <= 32) hipLaunchKernelGGL((k_rowgrad<SRC, 2>), dim3(gx, gy, 1), block, 0, s, a);
-  else hipLaunchKernelGGL((k_rowgrad<SRC, 4>), dim3(gx, gy, (unsigned)cdiv(a.rank, 64)), block, 0, s, a);
+  const int na = a.a.out ? (int)cdiv(a.a.C, kGradCols) : 0, nb = a.b.out ? (int)cdiv(a.b.C, kGradCols) : 0;
+  const unsigned gx = (unsigned)((int64_t)a.plan.max_chunks * (na + nb));
+  if (a.rank <= 16) hipLaunchKernelGGL((k_rowgrad<SRC, 1>), dim3(gx), block, 0, s, a, na, nb);
+  else if (a.rank <= 32) hipLaunchKernelGGL((k_rowgrad<SRC, 2>), dim3(gx), block, 0, s, a, na, nb);
+  else hipLaunchKernelGGL((k_rowgrad<SRC, 4>), dim3(gx, (unsigned)cdiv(a.rank, 64)), block, 0, s, a, na, nb);
 }
 
 hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s) {
   if (a.src == SRC_BF16) rowgrad_src<SRC_BF16>(a, s);
   else if (a.src == SRC_MXINT8) rowgrad_src<SRC_MXINT8>(a, s);
   else rowgrad_src<SRC_MXFP8>(a, s);
-  const int64_t size = (int64_t)a.rank * a.C;  // a multiple of 64
-  hipLaunchKernelGGL(k_rowgrad_join, dim3((unsigned)cdiv(size, 1024), (unsigned)a.L), dim3(256), 0, s, a.plan.chunks_of,
-                     a.partial, size, a.out);
+  const int64_t sa = a.a.out ? (int64_t)a.rank * a.a.C : 0, sb = a.b.out ? (int64_t)a.rank * a.b.C : 0;  // multiples of 64
+  hipLaunchKernelGGL(k_rowgrad_join, dim3((unsigned)cdiv(sa + sb, 1024), (unsigned)a.L), dim3(256), 0, s, a, sa, sb);
   return hipGetLastError();
 }
 
 hipError_t launch_fill_f32_zero(float *p, int64_t n, hipStream_t s) {
   const int64_t g = cdiv(n, 256);
   hipLaunchKernelGGL(k_zero_f32, dim3((unsigned)(g < 4096 ? g : 4096)), dim3(256), 0, s, p, n);
-  return hipGetLastError();
-}
-
-hipError_t launch_transpose_bf16(const uint16_t *in, uint16_t *out, int L, int P, int Q, hipStream_t s) {
-  hipLaunchKernelGGL(k_transpose_bf16, dim3((unsigned)cdiv(Q, 64), (unsigned)cdiv(P, 64), (unsigned)L), dim3(256), 0, s, in,
-                     out, P, Q);
   return hipGetLastError();
 }
 

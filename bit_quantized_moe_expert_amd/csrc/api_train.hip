@@ -102,7 +102,7 @@ struct AdapterCarve {
   uint16_t *parts;              // the low-rank product for the second one
   float *u;                     // backward: [R, rank]
   uint16_t *At, *Bt;            // [L, K, rank], [L, rank, N]
-  float *partial;
+  float *partial_a, *partial_b;
   size_t bytes;
 };
 
@@ -119,7 +119,8 @@ AdapterCarve carve_adapter(void *ws, const nf4moe_adapters_t &a, int R, bool bac
     c.u = b.take<float>((size_t)R * a.rank);
     c.At = b.take<uint16_t>((size_t)a.L * a.K * a.rank);
     c.Bt = b.take<uint16_t>((size_t)a.L * a.N * a.rank);
-    c.partial = b.take<float>((size_t)lay.max_slots * a.rank * (a.K > a.N ? a.K : a.N));
+    c.partial_a = b.take<float>((size_t)lay.max_slots * a.rank * a.K);
+    c.partial_b = b.take<float>((size_t)lay.max_slots * a.rank * a.N);
   }
   c.bytes = b.off;
   return c;
@@ -266,7 +267,7 @@ nf4moe_status_t nf4moe_adapter_plan(const int32_t *ids, int32_t R, int32_t L, vo
   if (!aligned(plan, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "plan must be 256-byte aligned");
   AdapterPlan p;
   adapter_plan_layout(R, L, plan, &p);
-  return hip_status(launch_adapter_plan(ids, R, L, p, (hipStream_t)stream), "adapter plan launch");
+  return hip_status(launch_adapter_prepare({p, ids, R, L, 0, 0, 0, nullptr, nullptr, nullptr, nullptr}, (hipStream_t)stream), "adapter plan launch");
 }
 
 size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, int32_t backward) {
@@ -277,11 +278,11 @@ size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, in
   return carve_adapter(nullptr, *ad, R, backward != 0).bytes;
 }
 
-// Rows, gather, ids and plan, as both directions take them; `cols` is the widest
-// output (the last kernel runs a workgroup per 64 rows and 256 columns).
+// Rows, gather, ids and plan, as both directions take them; `cols` is the width of the
+// output (grids reach a workgroup per 64 rows and 128 columns).
 static nf4moe_status_t check_adapter_rows(int32_t R, int32_t x_rows, const int32_t *x_row_of, const int32_t *ids,
                                           const void *plan, size_t plan_bytes, int32_t L, int32_t cols) {
-  const int64_t tiles = cdiv(R, kAdTile) + (R < L + 1 ? R : L + 1), per = cdiv(cols, 256);
+  const int64_t tiles = cdiv(R, kAdTile) + (R < L + 1 ? R : L + 1), per = cdiv(cols, 128);
   if (tiles * (per < 8 ? 8 : per) > 0x7fffffff)
     return fail(NF4MOE_ERR_UNSUPPORTED, "R=%d rows of %d columns are too many for one call", R, cols);
   if (x_rows < 1 || (!x_row_of && x_rows < R))
@@ -321,7 +322,7 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   const AdapterCarve c = carve_adapter(ws, *ad, R, false);
   AdapterPlan p;
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
-  hipError_t e = plan ? hipSuccess : launch_adapter_plan(ids, R, ad->L, p, s);
+  hipError_t e = plan ? hipSuccess : launch_adapter_prepare({p, ids, R, ad->L, 0, 0, 0, nullptr, nullptr, nullptr, nullptr}, s);
   if (e != hipSuccess) return hip_status(e, "adapter plan launch");
   return hip_status(launch_adapter_low_rank({p, ids, R, ad->L, x, x_row_of, x_rows, ad->A, ad->B, ad->scale, ad->K, ad->N, ad->rank,
                                              t, false, base, out, bf, c.slices, c.parts}, s), "adapter launch");
@@ -347,7 +348,7 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
     if (e == hipSuccess && dB) e = launch_fill_f32_zero(dB, (int64_t)ad->L * ad->rank * ad->N, s);
     return hip_status(e, "fill launch");
   }
-  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, ad->K)) != NF4MOE_OK) return st;
+  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, ad->K + ad->N)) != NF4MOE_OK) return st;
   if (!dy || (dA && (!x || (held && !x_scale))) || (dB && !t)) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(dy, 2) || !aligned(x, held ? 1 : 2) || !aligned(t, 16) || !aligned(dx_base, dt_bytes(dx_dtype)) ||
       !aligned(dx, dt_bytes(dx_dtype)))
@@ -360,25 +361,23 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
   const AdapterCarve c = carve_adapter(ws, *ad, R, true);
   AdapterPlan p;
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
-  if (!plan && (e = launch_adapter_plan(ids, R, ad->L, p, s)) != hipSuccess) return hip_status(e, "adapter plan launch");
+  // u = s B^T dy and dx = dx_base + A^T u: the forward's kernels on B as [L, rank, N]
+  // and A as [L, K, rank]
+  e = launch_adapter_prepare({p, plan ? nullptr : ids, R, ad->L, ad->K, ad->N, ad->rank, ad->A, ad->B, dx ? c.At : nullptr,
+                              dx || dA ? c.Bt : nullptr}, s);
+  if (e != hipSuccess) return hip_status(e, "adapter prepare launch");
   if (dx || dA) {
-    // u = s B^T dy and dx = dx_base + A^T u: the forward's kernel on B as [L, rank, N]
-    // and A as [L, K, rank]
-    e = launch_transpose_bf16(ad->B, c.Bt, ad->L, ad->N, ad->rank, s);
-    if (e == hipSuccess && dx) e = launch_transpose_bf16(ad->A, c.At, ad->L, ad->rank, ad->K, s);
-    if (e == hipSuccess)
-      e = launch_adapter_low_rank({p, ids, R, ad->L, dy, nullptr, R, c.Bt, c.At, ad->scale, ad->N, ad->K, ad->rank,
-                                   dA ? c.u : nullptr, true, dx_base, dx, dx_dtype == NF4MOE_DT_BF16, c.slices,
-                                   dx ? c.parts : nullptr}, s);
+    e = launch_adapter_low_rank({p, ids, R, ad->L, dy, nullptr, R, c.Bt, c.At, ad->scale, ad->N, ad->K, ad->rank,
+                                 dA ? c.u : nullptr, true, dx_base, dx, dx_dtype == NF4MOE_DT_BF16, c.slices,
+                                 dx ? c.parts : nullptr}, s);
     if (e != hipSuccess) return hip_status(e, "adapter backward launch");
   }
-  if (dA) {
-    e = launch_adapter_rowgrad({p, c.u, x, x_scale, x_src, x_row_of, x_rows, nullptr, ad->L, ad->K, ad->rank, false, dA, c.partial}, s);
-    if (e != hipSuccess) return hip_status(e, "adapter dA launch");
-  }
-  if (dB) {
-    e = launch_adapter_rowgrad({p, t, dy, nullptr, SRC_BF16, nullptr, R, ad->scale, ad->L, ad->N, ad->rank, true, dB, c.partial}, s);
-    if (e != hipSuccess) return hip_status(e, "adapter dB launch");
+  if (dA || dB) {
+    RowGradArgs g = {p, ad->L, ad->rank, x_src, {}, {}};
+    g.a = {c.u, x, x_scale, x_row_of, x_rows, nullptr, ad->K, false, dA, c.partial_a};
+    g.b = {t, dy, nullptr, nullptr, R, ad->scale, ad->N, true, dB, c.partial_b};
+    e = launch_adapter_rowgrad(g, s);
+    if (e != hipSuccess) return hip_status(e, "adapter weight gradient launch");
   }
   return NF4MOE_OK;
 }

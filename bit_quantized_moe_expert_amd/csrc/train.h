@@ -74,6 +74,7 @@ constexpr int kNormMaxH = 16384;
 constexpr int kMaxAdapters = 4096;
 constexpr int kMaxRank = 128;
 constexpr int kAdTile = 64;
+constexpr int kMaxChunk = 2048;
 struct AdapterPlan {
   int32_t *order;      // [R] row of each place in grouped order
   int32_t *counts;     // [0] tiles, [1] chunks
@@ -85,7 +86,16 @@ struct AdapterPlan {
 };
 int adapter_chunk_rows(int R);
 size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p);   // bytes
-hipError_t launch_adapter_plan(const int32_t *ids, int R, int L, const AdapterPlan &p, hipStream_t s);
+// The plan (with ids), and the backward's turned weights: Bt [L, rank, N] and At [L,
+// K, rank], each where given.
+struct PrepareArgs {
+  AdapterPlan plan;
+  const int32_t *ids;  // or null: no plan to make
+  int R, L, K, N, rank;
+  const uint16_t *A, *B;
+  uint16_t *At, *Bt;
+};
+hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s);
 
 // v[row][j] = sum_k x[row'][k] W1_l[j][k] for the rows of adapter l (W1 [L, rank, K]
 // bf16), row' by row_of, and out[row][c] = base[row][c] + sum_j (m_l v[row][j])
@@ -113,25 +123,26 @@ int adapter_slices(int R, int K);
 size_t adapter_parts_elems(int R, int rank);
 hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s);
 
-// out_l[j][c] (or [c][j], transposed) = m_l sum over the rows of l of p[row][j] v[row'][c].
-struct RowGradArgs {
-  AdapterPlan plan;
+// Per adapter l, out_l[j][c] (or [c][j], transposed) = m_l sum over the rows of l of
+// p[row][j] v[row'][c]; a: v by src, b: v bf16. Each where out is given.
+struct RowGradOne {
   const float *p;      // [R, rank]
-  const void *v;       // [*, C] by src
+  const void *v;       // [v_rows, C]
   const uint8_t *v_scale;
-  int src;
   const int32_t *row_of;
   int v_rows;
   const float *scale;
-  int L, C, rank;
+  int C;
   bool transposed;     // out [L, C, rank]
-  float *out, *partial;
+  float *out, *partial;   // partial: [max_slots][rank * C]
+};
+struct RowGradArgs {
+  AdapterPlan plan;
+  int L, rank, src;
+  RowGradOne a, b;
 };
 hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s);
 hipError_t launch_fill_f32_zero(float *p, int64_t n, hipStream_t s);
-
-// [L][P][Q] -> [L][Q][P], bf16.
-hipError_t launch_transpose_bf16(const uint16_t *in, uint16_t *out, int L, int P, int Q, hipStream_t s);
 
 // The forward of few rows in one launch, without a plan.
 struct AdapterRowsArgs {
