@@ -63,58 +63,68 @@ int plan_rows(int R, int L) {
 
 __device__ inline int bin_of(int id, int L) { return id < 0 || id >= L ? L : id; }
 
+constexpr int kPrepareThreads = 256;
 __device__ inline void plan_hist(const int32_t *__restrict__ ids, int R, int L, int per, int32_t *__restrict__ hist, int32_t *cnt) {
-  for (int b = threadIdx.x; b <= L; b += kPlanThreads) cnt[b] = 0;
+  for (int b = threadIdx.x; b <= L; b += kPrepareThreads) cnt[b] = 0;
   __syncthreads();
   const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
-  for (int r = r0 + (int)threadIdx.x; r < r1; r += kPlanThreads) atomicAdd(&cnt[bin_of(ids[r], L)], 1);
+  for (int r = r0 + (int)threadIdx.x; r < r1; r += kPrepareThreads) atomicAdd(&cnt[bin_of(ids[r], L)], 1);
   __syncthreads();
-  for (int b = threadIdx.x; b <= L; b += kPlanThreads) hist[(int64_t)blockIdx.x * (L + 1) + b] = cnt[b];
+  for (int b = threadIdx.x; b <= L; b += kPrepareThreads) hist[(int64_t)blockIdx.x * (L + 1) + b] = cnt[b];
 }
 
-// Turned copies of the adapters' weights for the backward: [L][P][Q] -> [L][Q][P],
-// in pieces of pt x qt (multiples of 8, at most 8192 elements): 16-byte loads along
-// Q, 16-byte stores along P.
+// Turned copies of the adapters' weights for the backward: [L][P][Q] -> [L][Q][P]. A
+// thread turns 8 x 8 values in registers: 16-byte loads along Q, 16-byte stores
+// along P, the rank's dimension fastest over the lanes.
 struct TurnArgs {
   const uint16_t *in;
   uint16_t *out;
-  int P, Q, pt, qt, np, nq;  // np x nq pieces per adapter
+  int P, Q;
+  bool p_is_rank;
 };
-constexpr int kTurnElems = 8192;
-__device__ inline void turn_piece(const TurnArgs &a, int64_t piece, uint16_t *tile) {
-  const int64_t base = piece / (a.np * a.nq) * a.P * a.Q;
-  const int rest = (int)(piece % (a.np * a.nq));
-  const int p0 = rest / a.nq * a.pt, q0 = rest % a.nq * a.qt;
-  const int stride = a.pt + 8;
-  const int q8 = a.qt / 8, p8 = a.pt / 8;
-  for (int i = threadIdx.x; i < a.pt * q8; i += kPlanThreads) {
-    const int p = i / q8, q = 8 * (i % q8);
-    if (p0 + p >= a.P || q0 + q >= a.Q) continue;
-    const uint4 v = load16(a.in + base + (int64_t)(p0 + p) * a.Q + q0 + q);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Rows (2 i, 2 i + 1) of column k of an 8 x 8 block of 16-bit values as one word.
+__device__ inline void turn_8x8(const uint4 (&row)[8], uint32_t (&blk)[4][8]) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) tile[(q + k) * stride + p] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u[4] = {row[2 * i].x, row[2 * i].y, row[2 * i].z, row[2 * i].w};
+    const uint32_t w[4] = {row[2 * i + 1].x, row[2 * i + 1].y, row[2 * i + 1].z, row[2 * i + 1].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      blk[i][2 * k] = __builtin_amdgcn_perm(w[k], u[k], 0x05040100u);
+      blk[i][2 * k + 1] = __builtin_amdgcn_perm(w[k], u[k], 0x07060302u);
+    }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.qt * p8; i += kPlanThreads) {
-    const int q = i / p8, p = 8 * (i % p8);
-    if (p0 + p >= a.P || q0 + q >= a.Q) continue;
-    store16(a.out + base + (int64_t)(q0 + q) * a.P + p0 + p, *reinterpret_cast<const uint4 *>(tile + q * stride + p));
-  }
+}
+__device__ inline void turn_block(const TurnArgs &a, int l, int block) {
+  const int p8 = a.P / 8, q8 = a.Q / 8;
+  const int i = block * kPrepareThreads + (int)threadIdx.x;
+  if (i >= p8 * q8) return;
+  const int p = 8 * (a.p_is_rank ? i % p8 : i / q8), q = 8 * (a.p_is_rank ? i / p8 : i % q8);
+  const int64_t base = (int64_t)l * a.P * a.Q;
+  uint4 row[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) row[k] = load16(a.in + base + (int64_t)(p + k) * a.Q + q);
+  uint32_t blk[4][8];
+  turn_8x8(row, blk);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    store16(a.out + base + (int64_t)(q + k) * a.P + p, make_uint4(blk[0][k], blk[1][k], blk[2][k], blk[3][k]));
 }
 
 // What the later launches need and what does not depend on anything: the row
 // counters per plan workgroup, and the backward's turned weights (0, 1 or 2 arrays).
-__global__ __launch_bounds__(kPlanThreads) void k_prepare(const int32_t *__restrict__ ids, int R, int L, int per, int hists,
-                                                          int32_t *__restrict__ hist, TurnArgs t0, TurnArgs t1, int64_t n0) {
-  extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
-  if ((int)blockIdx.x < hists) {
-    plan_hist(ids, R, L, per, hist, reinterpret_cast<int32_t *>(lds));
+__global__ __launch_bounds__(kPrepareThreads) void k_prepare(const int32_t *__restrict__ ids, int R, int L, int per, int hists,
+                                                          int32_t *__restrict__ hist, TurnArgs t0, TurnArgs t1, int b0, int b1) {
+  extern __shared__ int32_t cnt[];
+  int i = (int)blockIdx.x;
+  if (i < hists) {
+    plan_hist(ids, R, L, per, hist, cnt);
     return;
   }
-  const int64_t piece = (int64_t)blockIdx.x - hists;
-  if (piece < n0) turn_piece(t0, piece, lds);
-  else turn_piece(t1, piece - n0, lds);
+  i -= hists;  // per adapter b0 blocks of the first array, then b1 of the second
+  const int l = i / (b0 + b1), block = i % (b0 + b1);
+  if (block < b0) turn_block(t0, l, block);
+  else turn_block(t1, l, block - b0);
 }
 
 // Exclusive prefixes of four counts over the workgroup's threads in order; totals in *sum.
@@ -173,7 +183,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
   int4 sums = make_int4(0, 0, 0, 0), all;  // rows, tiles, chunks, slots
   for (int i = b0; i < b1; ++i) {
     const int32_t n = tot[i];
-    const int32_t c = i < L ? (n + chunk_rows - 1) / chunk_rows : 0;
+    const int32_t c = i < L ? max(1, (n + chunk_rows - 1) / chunk_rows) : 0;
     sums.x += n;
     sums.y += (n + kAdTile - 1) / kAdTile;
     sums.z += c;
@@ -190,7 +200,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
     if (blockIdx.x == 0) {
       for (int32_t r = 0; r < n; r += kAdTile) p.tiles[at.y++] = make_int4(i < L ? i : -1, at.x + r, min(kAdTile, n - r), 0);
       if (i < L) {
-        const int32_t c = (n + chunk_rows - 1) / chunk_rows;
+        const int32_t c = max(1, (n + chunk_rows - 1) / chunk_rows);  // one of no rows where there are none
         p.chunks_of[i] = make_int2(c, at.w);
         for (int32_t k = 0; k < c; ++k)
           p.chunks[at.z++] = make_int4(i, at.x + k * chunk_rows, min(chunk_rows, n - k * chunk_rows), c > 1 ? at.w + k : -1);
@@ -250,6 +260,39 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
     if (live) p.order[first + rank] = r;
   }
 }
+
+// ------------------------------------------------------------------ low-rank values
+// How the second product takes the low-rank values: `steps` matrix instructions of
+// 32 places a row and 16 columns. The places hold the three bf16 parts of the
+// scaled values: for rank 8 all three parts in one step (PACK 1), for rank 16 two
+// and then the third (PACK 2), else 32 ranks of one part a step, the parts of a
+// block of 32 ranks following each other (PACK 0). Other places hold zeros.
+__host__ __device__ inline int part_pack(int rank) { return rank == 8 ? 1 : rank == 16 ? 2 : 0; }
+__host__ __device__ inline int part_steps(int rank) { return rank <= 16 ? rank / 8 : 3 * ((rank + 31) / 32); }
+__device__ inline int part_place(int pack, int r8, int part) {  // place of ranks 8 r8 .. of one part in a row
+  return pack == 1 ? 8 * part : pack == 2 ? 16 * part + 8 * r8 : 96 * (r8 >> 2) + 32 * part + 8 * (r8 & 3);
+}
+
+// The low-rank values v of ranks 8 r8 .. of one row, where they go: low by row, and
+// the scaled values' parts in grouped order.
+__device__ inline void put_low(const LowRankArgs &p, int place, int row, int r8, const float (&v)[8], float m) {
+  const int pack = part_pack(p.rank);
+  float sv[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sv[k] = v[k] * m;
+  if (p.low && 8 * r8 < p.rank) store_elems8<false>(p.low, (int64_t)row * p.rank + 8 * r8, p.low_scaled ? sv : v);
+  if (!p.parts) return;
+  uint4 hi, mid, lo;
+  split3(sv, hi, mid, lo);
+  uint16_t *d = p.parts + (int64_t)place * (32 * part_steps(p.rank));
+  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 0)) = hi;
+  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 1)) = mid;
+  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 2)) = lo;
+  if (pack && r8 == 0)
+    for (int c = 24 * pack; c < 32 * pack; c += 8) *reinterpret_cast<uint4 *>(d + c) = make_uint4(0, 0, 0, 0);
+}
+// Groups of 8 ranks of a row, with the empty ones of the last block of 32.
+__host__ __device__ inline int low_groups(int rank) { return part_pack(rank) ? rank / 8 : (rank + 31) / 32 * 4; }
 
 // ------------------------------------------------------------------ shrink
 // K is taken in slices, one workgroup per tile and slice, and the workgroups of a
@@ -312,10 +355,18 @@ __global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int s
   if (ti >= p.plan.counts[0]) return;
   const int4 tile = p.plan.tiles[ti];
   const int l = tile.x, n = tile.z, rank = p.rank;
-  if (l < 0) return;
   const int32_t *order = p.plan.order + tile.y;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
+  const int nr8 = rank / 8, g8 = low_groups(rank);
+  if (l < 0) {  // rows without an adapter: low is 0, and the parts are not read
+    if (slices == 1 && p.low)
+      for (int i = tid; i < n * nr8; i += 256) {
+        const float z[8] = {};
+        store_elems8<false>(p.low, (int64_t)order[i / nr8] * rank + 8 * (i % nr8), z);
+      }
+    return;
+  }
   const int k = si * slice + 64 * wave, k1 = min(p.K, (si + 1) * slice);
   f32x4_t acc[4][RT] = {};
   if (n <= 16) shrink_rows<RT, 1>(p, order, n, l, k, k1, acc);
@@ -335,6 +386,24 @@ __global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int s
     }
     lds_barrier();
   }
+  if (slices == 1) {  // nothing to join
+    const float m = p.scale ? p.scale[l] : 1.0f;
+    for (int i = tid; i < n * g8; i += 256) {
+      const int row = i / g8, r8 = i % g8;
+      float v[8] = {};
+      if (r8 < nr8) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float u = red[0][row][8 * r8 + c];
+#pragma unroll
+          for (int w = 1; w < SL; ++w) u += red[w][row][8 * r8 + c];
+          v[c] = u;
+        }
+      }
+      put_low(p, tile.y + row, order[row], r8, v, m);
+    }
+    return;
+  }
   float *out = p.partial + ((int64_t)si * p.R + tile.y) * rank;
   const int r4 = rank / 4;
   for (int i = tid; i < n * r4; i += 256) {
@@ -345,21 +414,10 @@ __global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int s
   }
 }
 
-// How the second product takes the low-rank values: `steps` matrix instructions of
-// 32 places a row and 16 columns. The places hold the three bf16 parts of the
-// scaled values: for rank 8 all three parts in one step (PACK 1), for rank 16 two
-// and then the third (PACK 2), else 32 ranks of one part a step, the parts of a
-// block of 32 ranks following each other (PACK 0). Other places hold zeros.
-__host__ __device__ inline int part_pack(int rank) { return rank == 8 ? 1 : rank == 16 ? 2 : 0; }
-__host__ __device__ inline int part_steps(int rank) { return rank <= 16 ? rank / 8 : 3 * ((rank + 31) / 32); }
-__device__ inline int part_place(int pack, int r8, int part) {  // place of ranks 8 r8 .. of one part in a row
-  return pack == 1 ? 8 * part : pack == 2 ? 16 * part + 8 * r8 : 96 * (r8 >> 2) + 32 * part + 8 * (r8 & 3);
-}
-
 // The slices' sums, added in order, for 8 ranks of one place a thread: out by row,
 // and the scaled value's parts in grouped order.
 __global__ __launch_bounds__(256) void k_shrink_join(LowRankArgs p, int slices, int L, const int32_t *__restrict__ ids) {
-  const int pack = part_pack(p.rank), nr8 = p.rank / 8, g8 = pack ? nr8 : (nr8 + 3) / 4 * 4;
+  const int nr8 = p.rank / 8, g8 = low_groups(p.rank);
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int place = (int)(i / g8), r8 = (int)(i % g8);
   if (place >= p.R) return;
@@ -373,20 +431,7 @@ __global__ __launch_bounds__(256) void k_shrink_join(LowRankArgs p, int slices, 
       for (int k = 0; k < 8; ++k) v[k] += u[k];
     }
   }
-  const float m = p.scale && l < L ? p.scale[l] : 1.0f;
-  float sv[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) sv[k] = v[k] * m;
-  if (p.low && r8 < nr8) store_elems8<false>(p.low, (int64_t)row * p.rank + 8 * r8, p.low_scaled ? sv : v);
-  if (!p.parts) return;
-  uint4 hi, mid, lo;
-  split3(sv, hi, mid, lo);
-  uint16_t *d = p.parts + (int64_t)place * (32 * part_steps(p.rank));
-  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 0)) = hi;
-  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 1)) = mid;
-  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 2)) = lo;
-  if (pack && r8 == 0)
-    for (int c = 24 * pack; c < 32 * pack; c += 8) *reinterpret_cast<uint4 *>(d + c) = make_uint4(0, 0, 0, 0);
+  put_low(p, place, row, r8, v, p.scale && l < L ? p.scale[l] : 1.0f);
 }
 
 // ------------------------------------------------------------------ expand
@@ -522,8 +567,8 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
 // are split into three bf16 parts in registers. One workgroup per chunk of rows and
 // 128 columns, its four waves taking every fourth step of 32 rows; their sums are
 // added in order through LDS, from which they leave in either layout. An adapter
-// with one chunk is written straight out; the chunks of others go to partial sums
-// that k_rowgrad_join adds in order. dA and dB run in one launch.
+// with one chunk (of no rows: zeros) is written straight out; the chunks of others go
+// to partial sums that k_rowgrad_join adds in order. dA and dB run in one launch.
 constexpr int kGradCols = 128;
 
 template <int SRC, int RT>
@@ -570,17 +615,11 @@ __device__ inline void rowgrad_body(const RowGradOne &p, const int4 chunk, int c
     uint4 a[RT][3];
 #pragma unroll
     for (int t = 0; t < RT; ++t) split3(pv[t], a[t][0], a[t][1], a[t][2]);
+    if constexpr (SRC == SRC_BF16) {
+      turn_8x8(raw, blk);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (SRC == SRC_BF16) {
-        const uint32_t u[4] = {raw[2 * i].x, raw[2 * i].y, raw[2 * i].z, raw[2 * i].w};
-        const uint32_t w[4] = {raw[2 * i + 1].x, raw[2 * i + 1].y, raw[2 * i + 1].z, raw[2 * i + 1].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          blk[i][2 * k] = __builtin_amdgcn_perm(w[k], u[k], 0x05040100u);
-          blk[i][2 * k + 1] = __builtin_amdgcn_perm(w[k], u[k], 0x07060302u);
-        }
-      } else {
+      for (int i = 0; i < 4; ++i) {
         constexpr int F = SRC - SRC_MXINT8;
         float x[8], y[8];
         ckpt8_decode8<F>(make_uint2(raw[2 * i].x, raw[2 * i].y), sc[2 * i], x);
@@ -658,10 +697,10 @@ __global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p, int na, int nb) 
   else rowgrad_body<SRC_BF16, RT>(p.b, chunk, (block - na) * kGradCols, j0, p.rank, prow, vrow, tile);
 }
 
-// The chunks of an adapter, added in order; zeros for an adapter without rows.
+// The chunks of an adapter that has several, added in order.
 __global__ __launch_bounds__(256) void k_rowgrad_join(RowGradArgs p, int64_t sa, int64_t sb) {
   const int2 c = p.plan.chunks_of[blockIdx.y];
-  if (c.x == 1) return;
+  if (c.x <= 1) return;
   int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= sa + sb) return;
   const bool first = i < sa;
@@ -678,33 +717,30 @@ __global__ __launch_bounds__(256) void k_zero_f32(float *p, int64_t n) {
 }
 
 // ------------------------------------------------------------------ few rows
-// One launch, no plan: a workgroup per row and 256 columns. Its four waves take
-// the ranks in turn (a dot product over K each), then every thread one column.
-// Each workgroup of a row repeats the row's shrink: A_l comes from L2 after the
-// first, and a second launch would cost more.
-template <bool BF>
-__global__ __launch_bounds__(256) void k_adapter_rows(AdapterRowsArgs p) {
+// One launch, no plan: a workgroup per row and share of the columns. Its W waves
+// take the ranks in turn (a dot product over K each, two at a time), then every
+// thread its columns. The workgroups of a row repeat its first product: A_l comes
+// from L2 after the first, and a second launch would cost more.
+template <bool BF, int W>
+__global__ __launch_bounds__(64 * W) void k_adapter_rows(AdapterRowsArgs p, int csplit) {
   __shared__ float ts[kMaxRank];
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = blockIdx.x / csplit, cs = blockIdx.x % csplit, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l = p.ids[r], rank = p.rank;
   const bool has = l >= 0 && l < p.L;
-  const int c = blockIdx.y * 256 + tid;
-  const int64_t at = (int64_t)r * p.N + c;
-  float b = 0.0f;
-  if (p.base && c < p.N)
-    b = BF ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p.base)[at]) : reinterpret_cast<const float *>(p.base)[at];
   if (has) {
     int xr = r;
     if (p.row_of) xr = min(max(p.row_of[r], 0), p.x_rows - 1);
     const uint16_t *x = p.x + (int64_t)xr * p.K;
     const uint16_t *A = p.A + (int64_t)l * rank * p.K;
-    for (int j = wave; j < rank; j += 8) {  // two ranks at a time: j and j + 4 (rank is a multiple of 8)
+    for (int j = wave; j < rank; j += 2 * W) {  // ranks j and j + W
+      const int j1 = min(j + W, rank - 1);
       float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 4
       for (int k = 8 * lane; k < p.K; k += 512) {
         float xv[8], a0[8], a1[8];
         load_elems8<true>(x, k, xv);
         load_elems8<true>(A, (int64_t)j * p.K + k, a0);
-        load_elems8<true>(A, (int64_t)(j + 4) * p.K + k, a1);
+        load_elems8<true>(A, (int64_t)j1 * p.K + k, a1);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           s0 += xv[i] * a0[i];
@@ -713,26 +749,37 @@ __global__ __launch_bounds__(256) void k_adapter_rows(AdapterRowsArgs p) {
       }
       s0 = wave_sum(s0);
       s1 = wave_sum(s1);
-      if (lane == 0) ts[j] = s0, ts[j + 4] = s1;
+      if (lane == 0) {
+        ts[j] = s0;
+        if (j + W < rank) ts[j + W] = s1;
+      }
     }
   }
   lds_barrier();
-  if (p.t && blockIdx.y == 0)
-    for (int j = tid; j < rank; j += 256) p.t[(int64_t)r * rank + j] = has ? ts[j] : 0.0f;
-  if (c >= p.N) return;
-  if (has) {
-    const uint16_t *w = p.B + ((int64_t)l * p.N + c) * rank;
-    float s = 0.0f;
-    for (int j = 0; j < rank; j += 8) {
-      float v[8];
-      load_elems8<true>(w, j, v);
+  if (p.t && cs == 0)
+    for (int j = tid; j < rank; j += 64 * W) p.t[(int64_t)r * rank + j] = has ? ts[j] : 0.0f;
+  const float m = has && p.scale ? p.scale[l] : 1.0f;
+  const int blocks = (p.N + 255) / 256;
+  const int c1 = min(p.N, 256 * (int)((int64_t)blocks * (cs + 1) / csplit));
+  for (int c = 256 * (int)((int64_t)blocks * cs / csplit) + tid; c < c1; c += 64 * W) {
+    const int64_t at = (int64_t)r * p.N + c;
+    float b = 0.0f;
+    if (p.base) b = BF ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p.base)[at]) : reinterpret_cast<const float *>(p.base)[at];
+    if (has) {
+      const uint16_t *w = p.B + ((int64_t)l * p.N + c) * rank;
+      float s = 0.0f;
+#pragma unroll 2
+      for (int j = 0; j < rank; j += 8) {
+        float v[8];
+        load_elems8<true>(w, j, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i] * ts[j + i];
+        for (int i = 0; i < 8; ++i) s += v[i] * ts[j + i];
+      }
+      b += m * s;
     }
-    b += p.scale ? p.scale[l] * s : s;
+    if (BF) reinterpret_cast<uint16_t *>(p.out)[at] = (uint16_t)f32_to_bf16_rne(b);
+    else reinterpret_cast<float *>(p.out)[at] = b;
   }
-  if (BF) reinterpret_cast<uint16_t *>(p.out)[at] = (uint16_t)f32_to_bf16_rne(b);
-  else reinterpret_cast<float *>(p.out)[at] = b;
 }
 
 }  // namespace
@@ -748,7 +795,7 @@ size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p) {
   const int64_t ch = adapter_chunk_rows(R);
   AdapterPlan q;
   q.max_tiles = (int)cdiv(R, kAdTile) + bins;
-  q.max_chunks = (int)cdiv(R, ch) + bins;
+  q.max_chunks = (int)cdiv(R, ch) + L;
   // an adapter of n > 1 chunks has more than (n - 1) ch rows, so n <= 2 rows / ch
   q.max_slots = (int)(2 * cdiv(R, ch));
   size_t off = 0;
@@ -767,38 +814,16 @@ size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p) {
   return off;
 }
 
-static TurnArgs turn_args(const uint16_t *in, uint16_t *out, int P, int Q, bool p_is_rank) {
-  TurnArgs t = {in, out, P, Q, P, Q, 1, 1};
-  if (p_is_rank) t.qt = (int)(kTurnElems / P / 8 * 8);
-  else t.pt = (int)(kTurnElems / Q / 8 * 8);
-  t.np = (int)cdiv(P, t.pt);
-  t.nq = (int)cdiv(Q, t.qt);
-  return t;
-}
-
 hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
   const int per = plan_rows(a.R, a.L);
   const int groups = a.ids ? (int)cdiv(a.R, per) : 0, hists = groups > 1 ? groups : 0;
-  TurnArgs t0 = {}, t1 = {};
-  int64_t n0 = 0, n1 = 0;
-  size_t lds = hists ? sizeof(int32_t) * (a.L + 1) : 0;
-  auto need = [&](const TurnArgs &t) {
-    const size_t b = (size_t)t.qt * (t.pt + 8) * sizeof(uint16_t);  // at most 32 KB (rank 8)
-    if (b > lds) lds = b;
-  };
-  if (a.Bt) {
-    t0 = turn_args(a.B, a.Bt, a.N, a.rank, false);
-    n0 = (int64_t)a.L * t0.np * t0.nq;
-    need(t0);
-  }
-  if (a.At) {
-    t1 = turn_args(a.A, a.At, a.rank, a.K, true);
-    n1 = (int64_t)a.L * t1.np * t1.nq;
-    need(t1);
-  }
-  if (hists + n0 + n1 > 0)
-    hipLaunchKernelGGL(k_prepare, dim3((unsigned)(hists + n0 + n1)), dim3(kPlanThreads), lds, s, a.ids, a.R, a.L, per, hists,
-                       a.plan.hist, t0, t1, n0);
+  const TurnArgs t0 = {a.B, a.Bt, a.N, a.rank, false}, t1 = {a.A, a.At, a.rank, a.K, true};
+  const int b0 = a.Bt ? (int)cdiv((int64_t)a.N * a.rank / 64, kPrepareThreads) : 0;
+  const int b1 = a.At ? (int)cdiv((int64_t)a.K * a.rank / 64, kPrepareThreads) : 0;
+  const unsigned grid = (unsigned)(hists + a.L * (b0 + b1));
+  if (grid > 0)
+    hipLaunchKernelGGL(k_prepare, dim3(grid), dim3(kPrepareThreads), hists ? sizeof(int32_t) * (a.L + 1) : 0, s, a.ids, a.R, a.L,
+                       per, hists, a.plan.hist, t0, t1, b0, b1);
   if (groups > 0)
     hipLaunchKernelGGL(k_plan_scatter, dim3(groups), dim3(kPlanThreads), 0, s, a.ids, a.R, a.L, per, groups,
                        adapter_chunk_rows(a.R), a.plan);
@@ -808,8 +833,10 @@ hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
 // Slices of K, each a multiple of 64 and at least kSliceMin wide: up to 8 where
 // there are few tiles to fill the chip with, else up to 4 (1003 rows of rank 32, K =
 // 1440: 5.1 us with 8, 5.9 with 4, 10.2 with 1; 32768 rows of rank 16, K = 2048,
-// product and join: 37.3, 33.7 and 38.4 us).
+// product and join: 37.3, 33.7 and 38.4 us). A narrow K is one slice and needs no
+// join.
 static int slice_width(int R, int K) {
+  if (K <= 512) return 512;
   const int w = (int)cdiv(cdiv(K, R < 4096 ? 8 : 4), 64) * 64;
   return w < kSliceMin ? kSliceMin : w;
 }
@@ -823,8 +850,10 @@ hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
   else if (a.rank <= 32) hipLaunchKernelGGL(k_shrink<2>, grid, block, 0, s, a, slices, slice);
   else if (a.rank <= 64) hipLaunchKernelGGL(k_shrink<4>, grid, block, 0, s, a, slices, slice);
   else hipLaunchKernelGGL(k_shrink<8>, grid, block, 0, s, a, slices, slice);
-  const int64_t items = (int64_t)a.R * (pack ? a.rank / 8 : cdiv(a.rank, 32) * 4);
-  hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices, a.L, a.ids);
+  if (slices > 1) {
+    const int64_t items = (int64_t)a.R * low_groups(a.rank);
+    hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices, a.L, a.ids);
+  }
   if (!a.out) return hipGetLastError();
   const int blocks = (int)cdiv(a.N, 128);
   const dim3 eg((unsigned)(a.plan.max_tiles * blocks));
@@ -856,7 +885,8 @@ hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s) {
   else if (a.src == SRC_MXINT8) rowgrad_src<SRC_MXINT8>(a, s);
   else rowgrad_src<SRC_MXFP8>(a, s);
   const int64_t sa = a.a.out ? (int64_t)a.rank * a.a.C : 0, sb = a.b.out ? (int64_t)a.rank * a.b.C : 0;  // multiples of 64
-  hipLaunchKernelGGL(k_rowgrad_join, dim3((unsigned)cdiv(sa + sb, 1024), (unsigned)a.L), dim3(256), 0, s, a, sa, sb);
+  if (a.R > adapter_chunk_rows(a.R))  // else no adapter has two chunks
+    hipLaunchKernelGGL(k_rowgrad_join, dim3((unsigned)cdiv(sa + sb, 1024), (unsigned)a.L), dim3(256), 0, s, a, sa, sb);
   return hipGetLastError();
 }
 
@@ -866,13 +896,34 @@ hipError_t launch_fill_f32_zero(float *p, int64_t n, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Up to 32 rows and 64 KB of A per workgroup and row.
-bool adapter_rows_supported(int R, int K, int rank) { return R <= 32 && (int64_t)K * rank <= 65536; }
+// Shares of a row's columns in the one-launch form: until there are two workgroups
+// per CU, and no fewer than 256 columns each.
+static int rows_csplit(int R, int N) {
+  const int64_t most = cdiv(N, 256), want = cdiv(512, R);
+  return (int)(want < most ? want : most);
+}
+
+// Where the one-launch form runs: while at most 1 MB of A and B passes through one
+// CU. Both forms, a pass in us on K = N = 2048: rank 16, 1024 / 2048 rows 13 / 22
+// against 24 / 30 for the grouped kernels; rank 64, 256 / 512 rows 20 / 29 against 24
+// / 25; and 2360 x 584, rank 128: 128 / 512 rows 29 / 35 against 30 / 34.
+bool adapter_rows_supported(int R, int K, int N, int rank) {
+  const int cs = rows_csplit(R, N);
+  const int64_t bytes = cdiv((int64_t)R * cs, 256) * 2 * rank * ((int64_t)K + cdiv(N, cs));  // of A and B through one CU
+  return bytes <= 1 << 20;
+}
 
 hipError_t launch_adapter_rows(const AdapterRowsArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)a.R, (unsigned)cdiv(a.N, 256)), block(256);
-  if (a.bf16) hipLaunchKernelGGL(k_adapter_rows<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_adapter_rows<false>, grid, block, 0, s, a);
+  const int cs = rows_csplit(a.R, a.N);
+  const dim3 grid((unsigned)(a.R * cs));
+  // 16 waves where a CU has no second workgroup anyway and the ranks feed them
+  if (a.R * cs <= 256 && a.rank >= 32) {
+    if (a.bf16) hipLaunchKernelGGL((k_adapter_rows<true, 16>), grid, dim3(1024), 0, s, a, cs);
+    else hipLaunchKernelGGL((k_adapter_rows<false, 16>), grid, dim3(1024), 0, s, a, cs);
+  } else {
+    if (a.bf16) hipLaunchKernelGGL((k_adapter_rows<true, 4>), grid, dim3(256), 0, s, a, cs);
+    else hipLaunchKernelGGL((k_adapter_rows<false, 4>), grid, dim3(256), 0, s, a, cs);
+  }
   return hipGetLastError();
 }
 

@@ -274,7 +274,7 @@ size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, in
   if (!ad || R < 1 || R > (1 << 30) || ad->L < 1 || ad->L > kMaxAdapters || ad->rank < 8 || ad->rank > kMaxRank ||
       ad->K < 8 || ad->N < 8)
     return 0;
-  if (!backward && adapter_rows_supported(R, ad->K, ad->rank)) return 0;
+  if (!backward && adapter_rows_supported(R, ad->K, ad->N, ad->rank)) return 0;
   return carve_adapter(nullptr, *ad, R, backward != 0).bytes;
 }
 
@@ -311,7 +311,7 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
   hipStream_t s = (hipStream_t)stream;
   const bool bf = dtype == NF4MOE_DT_BF16;
-  if (adapter_rows_supported(R, ad->K, ad->rank)) {
+  if (adapter_rows_supported(R, ad->K, ad->N, ad->rank)) {
     AdapterRowsArgs a = {x, x_row_of, ids, x_rows, R, ad->L, ad->K, ad->N, ad->rank, ad->A, ad->B, ad->scale, base, out, bf, t};
     return hip_status(launch_adapter_rows(a, s), "adapter launch");
   }
@@ -373,7 +373,7 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
     if (e != hipSuccess) return hip_status(e, "adapter backward launch");
   }
   if (dA || dB) {
-    RowGradArgs g = {p, ad->L, ad->rank, x_src, {}, {}};
+    RowGradArgs g = {p, R, ad->L, ad->rank, x_src, {}, {}};
     g.a = {c.u, x, x_scale, x_row_of, x_rows, nullptr, ad->K, false, dA, c.partial_a};
     g.b = {t, dy, nullptr, nullptr, R, ad->scale, ad->N, true, dB, c.partial_b};
     e = launch_adapter_rowgrad(g, s);

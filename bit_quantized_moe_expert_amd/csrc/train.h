@@ -78,7 +78,7 @@ constexpr int kMaxChunk = 2048;
 struct AdapterPlan {
   int32_t *order;      // [R] row of each place in grouped order
   int32_t *counts;     // [0] tiles, [1] chunks
-  int2 *chunks_of;     // [L] (chunks of the adapter, first partial slot)
+  int2 *chunks_of;     // [L] (chunks of the adapter, at least 1; first partial slot)
   int4 *tiles;         // (adapter or -1, first place, rows, 0)
   int4 *chunks;        // (adapter, first place, rows, partial slot or -1 when the adapter has one chunk)
   int32_t *hist;       // scratch
@@ -138,7 +138,7 @@ struct RowGradOne {
 };
 struct RowGradArgs {
   AdapterPlan plan;
-  int L, rank, src;
+  int R, L, rank, src;
   RowGradOne a, b;
 };
 hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s);
@@ -156,7 +156,7 @@ struct AdapterRowsArgs {
   bool bf16;
   float *t;            // or null
 };
-bool adapter_rows_supported(int R, int K, int rank);
+bool adapter_rows_supported(int R, int K, int N, int rank);
 hipError_t launch_adapter_rows(const AdapterRowsArgs &a, hipStream_t s);
 
 }  // namespace nf4moe

@@ -52,7 +52,14 @@ CASES = [("mixed", 1, 1, 8, 8, 8, "bf16"), ("mixed", 7, 3, 64, 40, 16, "f32"), (
          ("mixed", 200, 3, 2880, 96, 128, "bf16"), ("none", 9, 2, 64, 64, 16, "bf16"), ("experts", 2500, 4, 64, 96, 40, "f32")]
 
 
-@pytest.mark.parametrize("rows,Rn,L,K,N,rank,dt", CASES)
+# enough rows for the grouped kernels (the smaller forward calls run in one launch; every backward groups)
+GROUPED = [("mixed", 25000, 9, 512, 264, 8, "f32"), ("experts", 9000, 16, 768, 512, 16, "bf16"),
+           ("mixed", 5000, 40, 1032, 320, 24, "bf16"), ("one", 2100, 1, 520, 512, 64, "f32"),
+           ("mixed", 2600, 300, 520, 264, 72, "bf16"), ("mixed", 700, 3, 2880, 96, 128, "bf16"),
+           ("none", 25001, 2, 512, 264, 8, "bf16"), ("mixed", 40000, 50, 104, 520, 32, "f32")]
+
+
+@pytest.mark.parametrize("rows,Rn,L,K,N,rank,dt", CASES + GROUPED)
 def test_forward(rows, Rn, L, K, N, rank, dt):
     v = make(rows, Rn, L, K, N, rank, dt, Rn + K)
     n = {k: to_np(t) for k, t in v.items()}
@@ -132,8 +139,8 @@ def test_grouping_of_many_rows_and_adapters(Rn, L):
 
 def test_nonfinite_rows_stay_their_own():
     """A NaN or an infinity in one row's x reaches that row's output and its own adapter's gradients only."""
-    for Rn in (20, 200):
-        v = make("mixed", Rn, 4, 64, 64, 16, "bf16", 5)
+    for Rn in (20, 8000):       # in one launch, and grouped
+        v = make("mixed", Rn, 4, 512, 1024, 16, "bf16", 5)
         v["ids"][:] = torch.arange(Rn, device=DEV) % 4
         v["x"][6, 3] = float("nan")        # adapter 2
         v["x"][Rn - 1, 5] = float("inf")   # adapter 3, the last place of its tile
@@ -149,20 +156,24 @@ def test_nonfinite_rows_stay_their_own():
         assert torch.isfinite(g["dA"][3][:, 6:]).all() and not torch.isfinite(g["dA"][3][:, 5]).any()
         assert [bool(torch.isfinite(g["dB"][l]).all()) for l in range(4)] == [True, True, False, False]
     # an infinite weight of one adapter stays with that adapter
-    v = make("mixed", 200, 3, 64, 64, 24, "bf16", 6)
+    v = make("mixed", 8000, 3, 512, 1024, 24, "bf16", 6)
     v["B"][1, 7, 23] = float("inf")
     out = M.adapter_forward(v["x"], v["A"], v["B"], v["ids"], base=v["base"])
     assert torch.isfinite(out[v["ids"] != 1]).all() and torch.isfinite(out[:, :7]).all() and torch.isfinite(out[:, 8:]).all()
 
 
 def test_gather_indices_are_clamped():
-    v = make("experts", 100, 4, 64, 64, 16, "bf16", 8)
+    for Rn in (100, 9000):
+        _gather_clamped(make("experts", Rn, 4, 512, 1024, 16, "bf16", 8))
+
+
+def _gather_clamped(v):
     ok = M.adapter_forward(v["x"], v["A"], v["B"], v["ids"], x_row_of=v["row_of"])
     T = v["x"].shape[0]
     wild = v["row_of"].clone()
     wild[3], wild[50] = -5, T + 1000
     got = M.adapter_forward(v["x"], v["A"], v["B"], v["ids"], x_row_of=wild)
-    same = torch.ones(100, dtype=torch.bool, device=DEV)
+    same = torch.ones(len(wild), dtype=torch.bool, device=DEV)
     same[[3, 50]] = False
     assert torch.equal(got[same], ok[same])
 
@@ -178,14 +189,14 @@ def test_empty():
 
 
 def test_misaligned_views():
-    v = make("mixed", 150, 5, 72, 88, 24, "bf16", 11)
+    v = make("mixed", 4000, 5, 1032, 520, 24, "bf16", 11)
 
     def off(t):
         buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
         buf[1:] = t.reshape(-1)
         return buf[1:].view(t.shape)
     o = {k: off(t) if t is not None and t.dtype == torch.bfloat16 else t for k, t in v.items()}
-    for k in (150, 20):     # the grouped kernels and the one for few rows
+    for k in (4000, 20):    # the grouped kernels and the one for few rows
         a = M.adapter_forward(v["x"][:k], v["A"], v["B"], v["ids"][:k], base=v["base"][:k])
         b = M.adapter_forward(o["x"][:k], o["A"], o["B"], o["ids"][:k], base=o["base"][:k])
         assert torch.equal(a, b)
@@ -196,8 +207,8 @@ def test_misaligned_views():
 
 
 def test_captured_and_replayed():
-    v = make("experts", 700, 9, 256, 320, 16, "bf16", 12)
-    few = make("mixed", 6, 9, 256, 320, 16, "bf16", 13)
+    v = make("experts", 7000, 9, 1024, 320, 16, "bf16", 12)
+    few = make("mixed", 6, 9, 1024, 320, 16, "bf16", 13)
 
     def step():
         out, t = M.adapter_forward(v["x"], v["A"], v["B"], v["ids"], base=v["base"], scale=v["scale"], x_row_of=v["row_of"],
@@ -219,7 +230,7 @@ def test_captured_and_replayed():
         graphs.append((g, out))
     for k in range(4):
         v["x"].copy_(torch.randn_like(v["x"]))
-        v["ids"].copy_(torch.randint(-1, 9, (700,), device=DEV).int())      # other groups, other tables
+        v["ids"].copy_(torch.randint(-1, 9, (7000,), device=DEV).int())      # other groups, other tables
         few["ids"].copy_(torch.randint(-1, 9, (6,), device=DEV).int())
         torch.cuda.synchronize()
         streams = [torch.cuda.Stream() for _ in graphs]
@@ -234,7 +245,7 @@ def test_captured_and_replayed():
 
 
 def test_two_streams_at_once():
-    vs = [make("mixed", 3000, 12, 512, 512, 16, "bf16", 20 + i) for i in range(2)]
+    vs = [make("mixed", 12000, 12, 512, 512, 16, "bf16", 20 + i) for i in range(2)]
 
     def step(v):
         out, t = M.adapter_forward(v["x"], v["A"], v["B"], v["ids"], base=v["base"], return_t=True)

@@ -223,26 +223,28 @@ def test_adapter_validation():
     st, a = desc()
     assert L.nf4moe_adapter_plan_bytes(0, 4) == 0 and L.nf4moe_adapter_plan_bytes(8, 0) == 0
     assert L.nf4moe_adapter_plan_bytes(8, 4097) == 0 and L.nf4moe_adapter_plan_bytes(8, 4096) > 0
-    pb, wf, wb = (L.nf4moe_adapter_plan_bytes(100, 4), L.nf4moe_adapter_workspace_bytes(a, 100, 0),
-                  L.nf4moe_adapter_workspace_bytes(a, 100, 1))
-    assert pb > 0 and wf >= pb and wb > wf - 100 * 64
+    n = 200000          # enough rows for the grouped kernels
+    pb, wf, wb = (L.nf4moe_adapter_plan_bytes(n, 4), L.nf4moe_adapter_workspace_bytes(a, n, 0),
+                  L.nf4moe_adapter_workspace_bytes(a, n, 1))
+    assert pb > 0 and wf >= pb and wb > wf
+    assert L.nf4moe_adapter_workspace_bytes(a, 8, 0) == 0 and L.nf4moe_adapter_workspace_bytes(a, 8, 1) > 0
     assert L.nf4moe_adapter_workspace_bytes(a, 0, 0) == 0 and L.nf4moe_adapter_workspace_bytes(None, 8, 0) == 0
     plan = L.nf4moe_adapter_plan
-    assert plan(FAKE, 100, 0, FAKE, pb, None) == INVALID and plan(FAKE, 100, 4097, FAKE, pb, None) == INVALID
-    assert plan(FAKE, -1, 4, FAKE, pb, None) == INVALID and plan(None, 100, 4, FAKE, pb, None) == INVALID
-    assert plan(FAKE + 2, 100, 4, FAKE, pb, None) == INVALID and plan(FAKE, 100, 4, FAKE + 16, pb, None) == INVALID
-    assert plan(FAKE, 100, 4, None, pb, None) == WORKSPACE and plan(FAKE, 100, 4, FAKE, pb - 1, None) == WORKSPACE
+    assert plan(FAKE, n, 0, FAKE, pb, None) == INVALID and plan(FAKE, n, 4097, FAKE, pb, None) == INVALID
+    assert plan(FAKE, -1, 4, FAKE, pb, None) == INVALID and plan(None, n, 4, FAKE, pb, None) == INVALID
+    assert plan(FAKE + 2, n, 4, FAKE, pb, None) == INVALID and plan(FAKE, n, 4, FAKE + 16, pb, None) == INVALID
+    assert plan(FAKE, n, 4, None, pb, None) == WORKSPACE and plan(FAKE, n, 4, FAKE, pb - 1, None) == WORKSPACE
     assert plan(None, 0, 4, None, 0, None) == OK
 
     names = ["x", "x_rows", "row_of", "ids", "plan", "pb", "R", "base", "out", "dt", "t", "ws", "wsb"]
-    dflt = dict(x=FAKE, x_rows=100, row_of=None, ids=FAKE, plan=None, pb=0, R=100, base=FAKE, out=FAKE, dt=1, t=None,
+    dflt = dict(x=FAKE, x_rows=n, row_of=None, ids=FAKE, plan=None, pb=0, R=n, base=FAKE, out=FAKE, dt=1, t=None,
                 ws=FAKE, wsb=wf)
 
     def fwd(d=None, **kw):
         keep = d or desc()
         return L.nf4moe_adapter_forward(keep[1], *[dict(dflt, **kw)[n] for n in names], None)
     bnames = ["dy", "src", "x", "xs", "x_rows", "row_of", "t", "ids", "plan", "pb", "R", "dxb", "dx", "dt", "dA", "dB", "ws", "wsb"]
-    bdflt = dict(dy=FAKE, src=1, x=FAKE, xs=None, x_rows=100, row_of=None, t=FAKE, ids=FAKE, plan=None, pb=0, R=100, dxb=None,
+    bdflt = dict(dy=FAKE, src=1, x=FAKE, xs=None, x_rows=n, row_of=None, t=FAKE, ids=FAKE, plan=None, pb=0, R=n, dxb=None,
                  dx=FAKE, dt=1, dA=FAKE, dB=FAKE, ws=FAKE, wsb=wb)
 
     def bwd(d=None, **kw):
@@ -254,7 +256,7 @@ def test_adapter_validation():
             assert call(desc(**bad)) == INVALID, bad
         assert call(R=-1) == INVALID and call(R=(1 << 30) + 1) == INVALID
         assert call(dt=2) == INVALID and call(ids=None) == INVALID and call(ids=ODD) == INVALID
-        assert call(x_rows=99) == INVALID and call(x_rows=0, row_of=FAKE) == INVALID and call(row_of=ODD) == INVALID
+        assert call(x_rows=n - 1) == INVALID and call(x_rows=0, row_of=FAKE) == INVALID and call(row_of=ODD) == INVALID
         assert call(plan=FAKE, pb=pb - 1) == WORKSPACE and call(plan=FAKE + 16, pb=pb) == INVALID
         assert call(ws=None) == WORKSPACE and call(wsb=10) == WORKSPACE and call(ws=FAKE + 16) == INVALID
         assert call(t=FAKE + 4) == INVALID and call(x=ODD) == INVALID
