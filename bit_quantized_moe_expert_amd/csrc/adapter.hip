@@ -159,8 +159,13 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
                                                                int groups, int chunk_rows, AdapterPlan p) {
   constexpr int W = kPlanThreads / 64;
   __shared__ int32_t next[kMaxAdapters + 1], tot[kMaxAdapters + 1];
-  __shared__ uint16_t wcnt[W][kWaveBins];
+  __shared__ union {
+    uint16_t count[W][kWaveBins];
+    int32_t bins[2][kMaxAdapters + 1];
+  } u;
   __shared__ int4 wsum[W];
+  auto &wcnt = u.count;
+  int32_t *bin_tile = u.bins[0], *bin_row = u.bins[1];  // each bin's first tile and first place
   const int tid = threadIdx.x, nb = L + 1;
   const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
   int b = r0 + tid < r1 ? bin_of(ids[r0 + tid], L) : -1;
@@ -197,8 +202,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
   for (int i = b0; i < b1; ++i) {
     const int32_t n = tot[i];
     next[i] += at.x;
+    bin_tile[i] = at.y;
+    bin_row[i] = at.x;
+    at.y += (n + kAdTile - 1) / kAdTile;
     if (blockIdx.x == 0) {
-      for (int32_t r = 0; r < n; r += kAdTile) p.tiles[at.y++] = make_int4(i < L ? i : -1, at.x + r, min(kAdTile, n - r), 0);
       if (i < L) {
         const int32_t c = max(1, (n + chunk_rows - 1) / chunk_rows);  // one of no rows where there are none
         p.chunks_of[i] = make_int2(c, at.w);
@@ -210,6 +217,19 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
     at.x += n;
   }
   __syncthreads();
+  // the tile table, every workgroup its share: a tile's bin is the last that begins
+  // at or before it (a bin of no rows begins where the next one does)
+  for (int i = (int)blockIdx.x * kPlanThreads + tid; i < all.y; i += groups * kPlanThreads) {
+    int lo = 0, hi = nb;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (bin_tile[mid] <= i) lo = mid;
+      else hi = mid;
+    }
+    const int32_t r = (i - bin_tile[lo]) * kAdTile;
+    p.tiles[i] = make_int4(lo < L ? lo : -1, bin_row[lo] + r, min(kAdTile, tot[lo] - r), 0);
+  }
+  __syncthreads();  // bin_tile and bin_row end here
   const int lane = tid & 63, wave = tid >> 6;
   for (int base = r0; base < r1; base += kPlanThreads) {
     const int r = base + tid;
@@ -457,7 +477,7 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
   for (int s = 0; s < 2; ++s) rows[s] = order[min(r0 + 16 * s + l16, n - 1)];
   const uint16_t *trow[2], *wrow[4];
   const int width = 32 * part_steps(rank);
-  uint4 w[4], t[PACK ? PACK : 1][2];
+  uint4 w[4], t[PACK ? PACK : 3][2];
   // the weights of the ranks that this lane's 8 places of block o hold; places of no part meet zeros
   auto load_w = [&](int o) {
     const int r8 = PACK == 1 ? 0 : PACK == 2 ? (q & 1) : 4 * o + q;
@@ -474,12 +494,10 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
       wrow[j] = p.W2 + ((int64_t)l * p.N + min(c0 + c, p.N - 1)) * rank;
     }
     load_w(0);
-    if constexpr (PACK != 0) {
 #pragma unroll
-      for (int o = 0; o < PACK; ++o)
+    for (int o = 0; o < (PACK ? PACK : 3); ++o)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) t[o][s] = *reinterpret_cast<const uint4 *>(trow[s] + 32 * o);
-    }
+      for (int s = 0; s < 2; ++s) t[o][s] = *reinterpret_cast<const uint4 *>(trow[s] + 32 * o);
   }
   // base of this lane's rows 16 s + l16, in flight during the product (rows and
   // columns past the end read the last ones and are not stored)
@@ -517,18 +535,21 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
       }
     } else {
       for (int o = 0; o < (nr8 + 3) / 4; ++o) {
-        if (o > 0) load_w(o);
+        if (o > 0) {
+          load_w(o);
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
+          for (int part = 0; part < 3; ++part)
 #pragma unroll
-          for (int s = 0; s < 2; ++s) t[0][s] = *reinterpret_cast<const uint4 *>(trow[s] + 96 * o + 32 * part);
+            for (int s = 0; s < 2; ++s) t[part][s] = *reinterpret_cast<const uint4 *>(trow[s] + 96 * o + 32 * part);
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             if (r0 + 16 * s >= n) break;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t[0][s], acc[s][j]);
+            for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t[part][s], acc[s][j]);
           }
-        }
       }
     }
   }
