@@ -455,12 +455,14 @@ __global__ __launch_bounds__(256) void k_shrink_join(LowRankArgs p, int slices, 
 }
 
 // ------------------------------------------------------------------ expand
-// One workgroup per tile and 256 columns, 64 columns a wave; no LDS and no
-// barrier. The product is taken transposed (columns as the matrix rows), so a lane
-// ends with neighbouring columns of one row: 8 (bf16, by pairing two column blocks)
-// or 4 (fp32), 64 contiguous bytes of a row per access, and base, product and out
-// meet in registers. The low-rank values come ready for the matrix instructions.
-template <int PACK, bool BF>
+// One workgroup per tile and CB x 128 columns, a wave 32 rows and CB blocks of 64
+// columns; no LDS and no barrier. The product is taken transposed (columns as the
+// matrix rows), so a lane ends with neighbouring columns of one row: 8 (bf16, by
+// pairing two column blocks) or 4 (fp32), 64 contiguous bytes of a row per access,
+// and base, product and out meet in registers. The low-rank values come ready for the
+// matrix instructions. Bound by HBM: without the product (rows that have no adapter)
+// the same accesses of 32768 x 2048 bf16 take 54 us, 5.0 TB/s; with it 62 us.
+template <int PACK, bool BF, int CB>
 __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
   const int ti = blockIdx.x / blocks;  // a tile's column blocks follow each other: whole rows are in flight together
   if (ti >= p.plan.counts[0]) return;
@@ -469,112 +471,123 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
   if (l < 0 && p.base == p.out) return;  // nothing to add
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, q = lane >> 4;
-  const int c0 = (int)(blockIdx.x % blocks) * 128 + (wave >> 1) * 64, r0 = (wave & 1) * 32;
-  if (r0 >= n) return;
-  const int32_t *order = p.plan.order + tile.y;
+  const int c0 = (int)(blockIdx.x % blocks) * (128 * CB) + (wave >> 1) * (64 * CB), r0 = (wave & 1) * 32;
+  if (r0 >= n || c0 >= p.N) return;
+  const int32_t *order = p.plan.order + tile.y + r0;
+  const int rn = min(32, n - r0);
   int rows[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) rows[s] = order[min(r0 + 16 * s + l16, n - 1)];
-  const uint16_t *trow[2], *wrow[4];
+  for (int s = 0; s < 2; ++s) rows[s] = order[min(16 * s + l16, rn - 1)];
+  const uint16_t *trow[2], *wrow[CB][4];
   const int width = 32 * part_steps(rank);
-  uint4 w[4], t[PACK ? PACK : 3][2];
+  constexpr int NT = PACK ? PACK : 3, BH = BF ? 2 : 4;
+  uint4 t[NT][2];
+  struct Block {
+    uint4 base[2][BH], w[4];
+  } blk[CB];
+  auto load_t = [&](int o) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) t[k][s] = *reinterpret_cast<const uint4 *>(trow[s] + 96 * o + 32 * k);
+  };
   // the weights of the ranks that this lane's 8 places of block o hold; places of no part meet zeros
-  auto load_w = [&](int o) {
+  auto load_w = [&](int i, int o) {
     const int r8 = PACK == 1 ? 0 : PACK == 2 ? (q & 1) : 4 * o + q;
     const bool ok = PACK == 1 ? q < 3 : PACK == 2 ? true : r8 < nr8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = ok ? load16(wrow[j] + 8 * r8) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < 4; ++j) blk[i].w[j] = ok ? load16(wrow[i][j] + 8 * r8) : make_uint4(0, 0, 0, 0);
   };
   if (l >= 0) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) trow[s] = p.parts + (int64_t)(tile.y + min(r0 + 16 * s + l16, n - 1)) * width + 8 * q;
+    for (int s = 0; s < 2; ++s) trow[s] = p.parts + (int64_t)(tile.y + r0 + min(16 * s + l16, rn - 1)) * width + 8 * q;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = BF ? 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3) : 16 * j + l16;
-      wrow[j] = p.W2 + ((int64_t)l * p.N + min(c0 + c, p.N - 1)) * rank;
+    for (int i = 0; i < CB; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + 64 * i + (BF ? 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3) : 16 * j + l16);
+        wrow[i][j] = p.W2 + ((int64_t)l * p.N + min(c, p.N - 1)) * rank;
+      }
+      load_w(i, 0);
     }
-    load_w(0);
-#pragma unroll
-    for (int o = 0; o < (PACK ? PACK : 3); ++o)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) t[o][s] = *reinterpret_cast<const uint4 *>(trow[s] + 32 * o);
+    load_t(0);
   }
   // base of this lane's rows 16 s + l16, in flight during the product (rows and
   // columns past the end read the last ones and are not stored)
-  constexpr int BH = BF ? 2 : 4;
-  uint4 base[2][BH];
   if (p.base) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < CB; ++i)
 #pragma unroll
-      for (int h = 0; h < BH; ++h) {
-        const int64_t at = (int64_t)rows[s] * p.N + min(BF ? c0 + 32 * h + 8 * q : c0 + 16 * h + 4 * q, p.N - (BF ? 8 : 4));
-        base[s][h] = BF ? load16(reinterpret_cast<const uint16_t *>(p.base) + at) : load16(reinterpret_cast<const float *>(p.base) + at);
-      }
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int h = 0; h < BH; ++h) {
+          const int64_t at = (int64_t)rows[s] * p.N + min(c0 + 64 * i + (BF ? 32 * h + 8 * q : 16 * h + 4 * q), p.N - (BF ? 8 : 4));
+          blk[i].base[s][h] = BF ? load16(reinterpret_cast<const uint16_t *>(p.base) + at) : load16(reinterpret_cast<const float *>(p.base) + at);
+        }
   } else {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < CB; ++i)
 #pragma unroll
-      for (int h = 0; h < BH; ++h) base[s][h] = make_uint4(0, 0, 0, 0);
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int h = 0; h < BH; ++h) blk[i].base[s][h] = make_uint4(0, 0, 0, 0);
   }
-  f32x4_t acc[2][4] = {};  // [16 rows][16 columns]
-  if (l >= 0) {
-    if constexpr (PACK != 0) {
 #pragma unroll
-      for (int o = 0; o < PACK; ++o) {
-        if (o == 1 && q >= 2) {  // the third part and 16 empty places; the other weights are the first step's
+  for (int i = 0; i < CB; ++i) {
+    Block &u = blk[i];
+    const int cb = c0 + 64 * i;
+    if (cb >= p.N) break;
+    f32x4_t acc[2][4] = {};  // [16 rows][16 columns]
+    if (l >= 0) {
+      if constexpr (PACK != 0) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = make_uint4(0, 0, 0, 0);
+        for (int o = 0; o < PACK; ++o) {
+          if (o == 1 && q >= 2) {  // the third part and 16 empty places; the other weights are the first step's
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u.w[j] = make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(u.w[j], t[o][s], acc[s][j]);
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (r0 + 16 * s >= n) break;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t[o][s], acc[s][j]);
-        }
-      }
-    } else {
-      for (int o = 0; o < (nr8 + 3) / 4; ++o) {
-        if (o > 0) {
-          load_w(o);
+      } else {
+        const int nb = (nr8 + 3) / 4;
+        for (int o = 0; o < nb; ++o) {
+          if (o > 0) load_w(i, o);
+          if (nb > 1 && (o > 0 || i > 0)) load_t(o);
 #pragma unroll
           for (int part = 0; part < 3; ++part)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) t[part][s] = *reinterpret_cast<const uint4 *>(trow[s] + 96 * o + 32 * part);
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(u.w[j], t[part][s], acc[s][j]);
         }
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (r0 + 16 * s >= n) break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(w[j], t[part][s], acc[s][j]);
-          }
       }
     }
-  }
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (r0 + 16 * s + l16 >= n) continue;
-    const int64_t at = (int64_t)rows[s] * p.N;
+    for (int s = 0; s < 2; ++s) {
+      if (16 * s + l16 >= rn) continue;
+      const int64_t at = (int64_t)rows[s] * p.N;
 #pragma unroll
-    for (int h = 0; h < BH; ++h) {
-      const int c = c0 + (BF ? 32 * h + 8 * q : 16 * h + 4 * q);
-      if (c >= p.N) continue;
-      if constexpr (BF) {
-        float v[8];
-        unpack_bf16x8(base[s][h], v);
+      for (int h = 0; h < BH; ++h) {
+        const int c = cb + (BF ? 32 * h + 8 * q : 16 * h + 4 * q);
+        if (c >= p.N) continue;
+        if constexpr (BF) {
+          float v[8];
+          unpack_bf16x8(u.base[s][h], v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] += acc[s][2 * h][k];
-          v[4 + k] += acc[s][2 * h + 1][k];
+          for (int k = 0; k < 4; ++k) {
+            v[k] += acc[s][2 * h][k];
+            v[4 + k] += acc[s][2 * h + 1][k];
+          }
+          store_elems8<true>(p.out, at + c, v);
+        } else {
+          const uint4 b = u.base[s][h];
+          store16(reinterpret_cast<float *>(p.out) + at + c,
+                  make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[s][h][0]), __float_as_uint(__uint_as_float(b.y) + acc[s][h][1]),
+                             __float_as_uint(__uint_as_float(b.z) + acc[s][h][2]), __float_as_uint(__uint_as_float(b.w) + acc[s][h][3])));
         }
-        store_elems8<true>(p.out, at + c, v);
-      } else {
-        const uint4 b = base[s][h];
-        store16(reinterpret_cast<float *>(p.out) + at + c,
-                make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[s][h][0]), __float_as_uint(__uint_as_float(b.y) + acc[s][h][1]),
-                           __float_as_uint(__uint_as_float(b.z) + acc[s][h][2]), __float_as_uint(__uint_as_float(b.w) + acc[s][h][3])));
       }
     }
   }
@@ -864,6 +877,24 @@ static int slice_width(int R, int K) {
 int adapter_slices(int R, int K) { return (int)cdiv(K, slice_width(R, K)); }
 size_t adapter_parts_elems(int R, int rank) { return (size_t)R * 32 * part_steps(rank); }
 
+template <int PACK, bool BF, int CB>
+static void expand_one(const LowRankArgs &a, hipStream_t s) {
+  const int blocks = (int)cdiv(a.N, 128 * CB);
+  hipLaunchKernelGGL((k_expand<PACK, BF, CB>), dim3((unsigned)(a.plan.max_tiles * blocks)), dim3(256), 0, s, a, blocks);
+}
+template <int PACK>
+static void expand_pack(const LowRankArgs &a, hipStream_t s) {
+  // Two blocks of 64 columns a wave, one after the other on the same low-rank values,
+  // for many rows; else one, and more workgroups. us, two against one: 32768 rows of
+  // rank 16, N = 2048 bf16 61.6 / 72.4, fp32 107.5 / 118.7; 16384 rows 33.0 / 37.6, fp32
+  // 58.5 / 58.9; 12867 rows of rank 64 52.6 / 51.4; 4099 rows, N = 2880 fp32 29.7 / 26.5.
+  const bool wide = a.R >= 16384;
+  if (a.bf16 && wide) expand_one<PACK, true, 2>(a, s);
+  else if (a.bf16) expand_one<PACK, true, 1>(a, s);
+  else if (wide) expand_one<PACK, false, 2>(a, s);
+  else expand_one<PACK, false, 1>(a, s);
+}
+
 hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
   const int slice = slice_width(a.R, a.K), slices = adapter_slices(a.R, a.K), pack = part_pack(a.rank);
   const dim3 grid((unsigned)(a.plan.max_tiles * slices)), block(256);
@@ -876,18 +907,9 @@ hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
     hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices, a.L, a.ids);
   }
   if (!a.out) return hipGetLastError();
-  const int blocks = (int)cdiv(a.N, 128);
-  const dim3 eg((unsigned)(a.plan.max_tiles * blocks));
-  if (pack == 1) {
-    if (a.bf16) hipLaunchKernelGGL((k_expand<1, true>), eg, block, 0, s, a, blocks);
-    else hipLaunchKernelGGL((k_expand<1, false>), eg, block, 0, s, a, blocks);
-  } else if (pack == 2) {
-    if (a.bf16) hipLaunchKernelGGL((k_expand<2, true>), eg, block, 0, s, a, blocks);
-    else hipLaunchKernelGGL((k_expand<2, false>), eg, block, 0, s, a, blocks);
-  } else {
-    if (a.bf16) hipLaunchKernelGGL((k_expand<0, true>), eg, block, 0, s, a, blocks);
-    else hipLaunchKernelGGL((k_expand<0, false>), eg, block, 0, s, a, blocks);
-  }
+  if (pack == 1) expand_pack<1>(a, s);
+  else if (pack == 2) expand_pack<2>(a, s);
+  else expand_pack<0>(a, s);
   return hipGetLastError();
 }
 
