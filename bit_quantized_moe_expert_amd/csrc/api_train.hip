@@ -207,7 +207,7 @@ nf4moe_status_t nf4moe_block_norm_forward(const nf4moe_block_norm_t *norm, const
 
 size_t nf4moe_block_norm_workspace_bytes(int32_t H, int64_t T) {
   if (H < 1 || H > kNormMaxH || T < 1 || T > 0x7fffffff) return 0;
-  return align_up((size_t)norm_backward_groups(T, H) * 3 * H * sizeof(float));
+  return align_up((size_t)norm_backward_groups(T, H) * 2 * H * sizeof(float));
 }
 
 nf4moe_status_t nf4moe_block_norm_backward(const nf4moe_block_norm_t *norm, const void *dx_new, const uint16_t *dy,

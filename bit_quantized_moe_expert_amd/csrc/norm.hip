@@ -10,7 +10,9 @@
 //   dz = alpha phi g;  dgate = alpha phi' g z (summed to the gate's shape)
 //   df = rstd_f (dz w_post - n_f mean(dz w_post n_f));  dw_post = sum_t dz n_f
 // Everything is fp32 in registers between the loads and the stores; each output
-// is rounded once. Both directions are bound by memory traffic.
+// is rounded once. Both directions are bound by memory traffic: the forward of 8190 x
+// 2880 (fp32 stream) runs at 5.2 TB/s, the backward of 8192 x 2048 bf16 at 4.2 TB/s
+// with its column sums (latency of a row's two dependent sums).
 //
 // A row is held by TPR threads, 8 NC values each, so its reductions are a wave
 // sum (TPR = 64) or wave sums joined through LDS. Rows of any width: the last
@@ -22,6 +24,7 @@
 namespace nf4moe {
 
 namespace {
+
 
 // Elements i .. i + 7 of a row of H, zeros past the end.
 template <bool BF>
@@ -60,6 +63,20 @@ __device__ inline float gate_phi(int fn, float v) {
 }
 __device__ inline float gate_slope(int fn, float phi) { return fn == 1 ? phi * (1.0f - phi) : fn == 2 ? 1.0f - phi * phi : 1.0f; }
 
+// phi of 8 gate values; the function is chosen once, outside the loop over them.
+__device__ inline void gate_phi8(int fn, const float (&v)[8], float (&phi)[8]) {
+  if (fn == 1) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) phi[j] = gate_phi(1, v[j]);
+  } else if (fn == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) phi[j] = gate_phi(2, v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) phi[j] = v[j];
+  }
+}
+
 __device__ inline float gate_scalar(const NormArgs &p, int64_t i) {
   return p.gate_bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p.gate)[i]) : reinterpret_cast<const float *>(p.gate)[i];
 }
@@ -68,8 +85,10 @@ __device__ inline void gate_row8(const NormArgs &p, int64_t base, int i, float (
   else load_row8<false>(p.gate, base, i, p.H, v);
 }
 
-// Sum over the TPR threads of a row (NV values at once); red has a place per
-// wave and value. TPR > 64: two barriers, taken by every thread of the workgroup.
+// Sum over the TPR threads of a row (NV values at once); red has a place per wave and
+// value. TPR > 64: one barrier, taken by every thread of the workgroup. Consecutive
+// sums use different places (a thread that writes them again has passed another
+// sum's barrier, and so has every reader).
 template <int TPR, int NV>
 __device__ inline void row_sum(float (&v)[NV], float *red) {
 #pragma unroll
@@ -90,14 +109,48 @@ __device__ inline void row_sum(float (&v)[NV], float *red) {
       for (int w = 0; w < W; ++w) s += red[(first + w) * NV + k];
       v[k] = s;
     }
-    lds_barrier();  // red may be written again
+  }
+}
+
+// Eight elements as they lie in memory: loads first, arithmetic later.
+template <bool BF>
+struct Raw8 {
+  uint4 v[BF ? 1 : 2];
+};
+template <bool BF>
+__device__ inline Raw8<BF> load_raw8(const void *p, int64_t base, int i, int H) {
+  Raw8<BF> r;
+  const char *at = reinterpret_cast<const char *>(p) + (base + i) * (BF ? 2 : 4);
+  if (i + 8 <= H) {
+    r.v[0] = load16(at);
+    if constexpr (!BF) r.v[1] = load16(at + 16);
+  } else {
+    float f[8];
+    load_row8<BF>(p, base, i, H, f);
+    if constexpr (BF) {
+      r.v[0] = pack_bf16x8(f);
+    } else {
+      r.v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+      r.v[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+    }
+  }
+  return r;
+}
+template <bool BF>
+__device__ inline void unpack_raw8(const Raw8<BF> &r, float (&v)[8]) {
+  if constexpr (BF) {
+    unpack_bf16x8(r.v[0], v);
+  } else {
+    const uint4 a = r.v[0], b = r.v[1];
+    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+    v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
   }
 }
 
 template <bool XBF, int TPR, int NC>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
-  __shared__ float red[THREADS / 64];
+  __shared__ float red[2][THREADS / 64];
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   // Rows past the end (TPR = 64 only: no barriers there) leave; else ROWS = 1 or
@@ -124,7 +177,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss[0] += f[c][j] * f[c][j];
-      row_sum<TPR, 1>(ss, red);
+      row_sum<TPR, 1>(ss, red[0]);
       rs = 1.0f / sqrtf(ss[0] / (float)H + p.eps);
       if (t == 0 && live) p.rstd_post[row] = rs;
     }
@@ -136,12 +189,19 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
       if (i < H) {
         float w[8], g[8];
         if (p.w_post) load_row8<false>(p.w_post, 0, i, H, w);
-        if (p.gate_kind & 1) gate_row8(p, p.gate_kind == 3 ? base : 0, i, g);
+        if (p.w_post) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[c][j] *= rs * w[j];
+        }
+        if (p.gate_kind & 1) {
+          gate_row8(p, p.gate_kind == 3 ? base : 0, i, g);
+          gate_phi8(p.gate_fn, g, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[c][j] *= w[j];
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float z = p.w_post ? f[c][j] * rs * w[j] : f[c][j];
-          const float k = (p.gate_kind & 1) ? m * gate_phi(p.gate_fn, g[j]) : m;
-          x[c][j] += k * z;
+          x[c][j] += m * f[c][j];
           if (XBF) x[c][j] = bf16_to_f32(f32_to_bf16_rne(x[c][j]));
         }
         if (live) store_row8<XBF>(p.x_new, base, i, H, x[c]);
@@ -154,7 +214,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss[0] += x[c][j] * x[c][j];
-    row_sum<TPR, 1>(ss, red);
+    row_sum<TPR, 1>(ss, red[1]);
     const float rs = 1.0f / sqrtf(ss[0] / (float)H + p.eps);
     if (t == 0 && live) p.rstd_pre[row] = rs;
 #pragma unroll
@@ -171,64 +231,122 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
   }
 }
 
-// Rows are dealt to a fixed number of workgroups (a function of T and H), each
-// row slot of a workgroup keeps its columns' sums for dw_pre, dw_post and a
-// per-channel dgate in registers, the slots are added in order through LDS, and
-// k_norm_colsum adds the workgroups in order: the same bits on every run.
+// Rows are dealt to a fixed number of workgroups (a function of T and H). Each row
+// slot of a workgroup keeps two sums per column in registers: dy n_x for dw_pre, and
+// the one that dw_post and a per-channel dgate both are multiples of, sum_t g n_f
+// (without the gate's factor where that is a channel's constant). The slots are added
+// in order through LDS and k_norm_colsum adds the workgroups in order: the same bits
+// on every run.
+// Two workgroups of 512 threads a CU where a row's threads fit (8192 x 2048 bf16: 48
+// us; one of 1024: 49; one of 768 that asks for the next row early: 51; four of 256:
+// 57, whose partial sums cost most).
+__host__ __device__ constexpr int back_threads(int tpr) { return tpr <= 512 ? 512 : 1024; }
+
 template <bool XBF, int TPR, int NC>
-__global__ __launch_bounds__(1024) void k_norm_backward(NormArgs p) {
-  constexpr int SLOTS = 1024 / TPR;
-  __shared__ float red[2 * 16];
-  extern __shared__ float slot_sum[];  // [3][H] (SLOTS > 1: at most 48 KB)
-  const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+__global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p) {
+  constexpr int THREADS = back_threads(TPR), SLOTS = THREADS / TPR;
+  // the first sum's places and the second's, in turn for even and odd rounds (a
+  // round may have one sum only)
+  __shared__ float red[2][2 * 16];
+  int turn = 0;
+  extern __shared__ float slot_sum[];  // [2][H] (SLOTS > 1: at most 32 KB)
+  const int t = threadIdx.x % TPR, slot = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
   const int H = p.H;
-  float a_pre[NC][8] = {}, a_post[NC][8] = {}, a_gate[NC][8] = {};
   const float invH = 1.0f / (float)H;
+  // w_pre, and w_post times a per-channel gate's phi, are kept in LDS as each thread
+  // reads them (NC = 1)
+  constexpr bool KEEP = NC == 1;
+  __shared__ float4 kept[KEEP ? 2 : 1][2][KEEP ? TPR : 1];
+  auto first_weights = [&](int i, float (&w)[8]) { load_row8<false>(p.w_pre, 0, i, H, w); };
+  auto second_weights = [&](int i, float (&w)[8]) {
+    if (p.w_post) {
+      load_row8<false>(p.w_post, 0, i, H, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+    }
+    if (p.gate_kind == 1) {
+      float v[8], phi[8];
+      gate_row8(p, 0, i, v);
+      gate_phi8(p.gate_fn, v, phi);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] *= phi[j];
+    }
+  };
+  auto keep = [&](int which, const float (&w)[8]) {
+    kept[which][0][t] = make_float4(w[0], w[1], w[2], w[3]);
+    kept[which][1][t] = make_float4(w[4], w[5], w[6], w[7]);
+  };
+  auto kept8 = [&](int which, float (&w)[8]) {
+    const float4 a = kept[which][0][t], b = kept[which][1][t];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  };
+  if (KEEP) {
+    if (slot == 0 && 8 * t < H) {
+      float w[8];
+      if (p.w_pre) {
+        first_weights(8 * t, w);
+        keep(0, w);
+      }
+      if (p.f) {
+        second_weights(8 * t, w);
+        keep(1, w);
+      }
+    }
+    lds_barrier();
+  }
+  float a_pre[NC][8] = {}, a_post[NC][8] = {};
   // every thread runs the same number of rounds: row_sum's barriers need them all
   for (int64_t r0 = (int64_t)blockIdx.x * SLOTS; r0 < p.T; r0 += (int64_t)gridDim.x * SLOTS) {
     const int64_t row = r0 + slot;
     const bool live = row < p.T;
     const int64_t base = (live ? row : 0) * H;
-    float g[NC][8], f[NC][8];
+    turn ^= 1;
+    // all that the row reads is asked for together
+    Raw8<XBF> rg[NC] = {}, rx[NC] = {};
+    Raw8<true> rf[NC] = {}, ry[NC] = {};
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = 8 * (t + c * TPR);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[c][j] = f[c][j] = 0.0f;
-      if (i < H && live) {
-        if (p.dx_new) load_row8<XBF>(p.dx_new, base, i, H, g[c]);
-        if (p.f) load_row8<true>(p.f, base, i, H, f[c]);
+      if (i >= H || !live) continue;
+      if (p.w_pre) {
+        ry[c] = load_raw8<true>(p.dy, base, i, H);
+        rx[c] = load_raw8<XBF>(p.x, base, i, H);
       }
+      if (p.dx_new) rg[c] = load_raw8<XBF>(p.dx_new, base, i, H);
+      if (p.f) rf[c] = load_raw8<true>(p.f, base, i, H);
     }
+    float g[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) unpack_raw8<XBF>(rg[c], g[c]);
     if (p.w_pre) {
-      float dy[NC][8], n[NC][8];
+      float a[NC][8], n[NC][8];
       float s[1] = {0.0f};
       const float rs = live ? p.rstd_pre[row] : 0.0f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = 8 * (t + c * TPR);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dy[c][j] = n[c][j] = 0.0f;
-        if (i < H && live) {
+        unpack_raw8<true>(ry[c], a[c]);
+        unpack_raw8<XBF>(rx[c], n[c]);
+        if (i < H) {
           float w[8];
-          load_row8<true>(p.dy, base, i, H, dy[c]);
-          load_row8<XBF>(p.x, base, i, H, n[c]);
-          load_row8<false>(p.w_pre, 0, i, H, w);
+          if (KEEP) kept8(0, w);
+          else first_weights(i, w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             n[c][j] *= rs;
-            a_pre[c][j] += dy[c][j] * n[c][j];
-            dy[c][j] *= w[j];
-            s[0] += dy[c][j] * n[c][j];
+            a_pre[c][j] += a[c][j] * n[c][j];
+            a[c][j] *= w[j];
+            s[0] += a[c][j] * n[c][j];
           }
         }
       }
-      row_sum<TPR, 1>(s, red);
+      row_sum<TPR, 1>(s, red[turn]);
       const float mean = s[0] * invH;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[c][j] += rs * (dy[c][j] - n[c][j] * mean);
+        for (int j = 0; j < 8; ++j) g[c][j] += rs * (a[c][j] - n[c][j] * mean);
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -236,52 +354,57 @@ __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs p) {
       if (i < H && live) store_row8<XBF>(p.dx, base, i, H, g[c]);
     }
     if (p.f) {
-      // f becomes n_f (or stays f), g becomes dz * w_post (or dz)
+      // f becomes n_f (or stays f), g becomes the gradient of n_f up to the factor m
       const float rs = p.w_post ? (live ? p.rstd_post[row] : 0.0f) : 1.0f;
-      const float raw = p.gate_kind == 2 ? gate_phi(p.gate_fn, gate_scalar(p, live ? row : 0)) : 1.0f;
-      float s[2] = {0.0f, 0.0f};
+      const float phi = p.gate_kind == 2 ? gate_phi(p.gate_fn, gate_scalar(p, live ? row : 0)) : 1.0f;
+      const float m = p.alpha * phi;
+      float f[NC][8];
+      float s[1] = {0.0f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = 8 * (t + c * TPR);
-        if (i < H && live) {
-          float w[8], v[8], dg[8];
-          if (p.w_post) load_row8<false>(p.w_post, 0, i, H, w);
-          if (p.gate_kind & 1) gate_row8(p, p.gate_kind == 3 ? base : 0, i, v);
+        unpack_raw8<true>(rf[c], f[c]);
+        if (i < H) {
+          float w[8];
+          if (KEEP) kept8(1, w);
+          else second_weights(i, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[c][j] *= rs;
+          if (p.gate_kind == 3) {
+            float v[8], q[8], dg[8];
+            gate_row8(p, base, i, v);
+            gate_phi8(p.gate_fn, v, q);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dg[j] = p.alpha * gate_slope(p.gate_fn, q[j]) * g[c][j] * f[c][j] * w[j];
+            if (live) store_row8<false>(p.dgate, base, i, H, dg);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[c][j] *= q[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a_post[c][j] += (p.gate_kind == 2 ? phi * g[c][j] : g[c][j]) * f[c][j];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float n = f[c][j] * rs, wj = p.w_post ? w[j] : 1.0f;
-            const float phi = (p.gate_kind & 1) ? gate_phi(p.gate_fn, v[j]) : raw;
-            const float gz = p.alpha * g[c][j] * n * wj;  // alpha g z
-            dg[j] = gz * gate_slope(p.gate_fn, phi);
-            if (p.gate_kind == 1) a_gate[c][j] += dg[j];
-            s[1] += gz;
-            const float dz = p.alpha * phi * g[c][j];
-            if (p.w_post) a_post[c][j] += dz * n;
-            f[c][j] = n;
-            g[c][j] = dz * wj;
-            s[0] += g[c][j] * n;
+            g[c][j] *= w[j];
+            s[0] += g[c][j] * f[c][j];
           }
-          if (p.gate_kind == 3) store_row8<false>(p.dgate, base, i, H, dg);
         }
       }
-      row_sum<TPR, 2>(s, red);
-      if (p.gate_kind == 2 && t == 0 && live) p.dgate[row] = s[1] * gate_slope(p.gate_fn, raw);
-      const float mean = s[0] * invH;
+      row_sum<TPR, 1>(s, red[turn] + 16);
+      if (p.gate_kind == 2 && t == 0 && live) p.dgate[row] = p.alpha * s[0] * gate_slope(p.gate_fn, phi);
+      const float mean = p.w_post ? s[0] * invH : 0.0f, mr = m * rs;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = 8 * (t + c * TPR);
         if (i < H && live) {
-          if (p.w_post) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) g[c][j] = rs * (g[c][j] - f[c][j] * mean);
-          }
+          for (int j = 0; j < 8; ++j) g[c][j] = mr * (g[c][j] - f[c][j] * mean);
           store_row8<true>(p.df, base, i, H, g[c]);
         }
       }
     }
   }
   // join the slots, then one partial per workgroup
-  float *out = p.partial + (int64_t)blockIdx.x * 3 * H;
+  float *out = p.partial + (int64_t)blockIdx.x * 2 * H;
   for (int s = 0; s < SLOTS; ++s) {
     if (slot == s) {
       float *dst = SLOTS == 1 ? out : slot_sum;
@@ -291,17 +414,15 @@ __global__ __launch_bounds__(1024) void k_norm_backward(NormArgs p) {
         for (int j = 0; j < 8; ++j) {
           const int i = 8 * (t + c * TPR) + j;
           if (i >= H) continue;
-          const bool first = s == 0;
-          dst[i] = first ? a_pre[c][j] : dst[i] + a_pre[c][j];
-          dst[H + i] = first ? a_post[c][j] : dst[H + i] + a_post[c][j];
-          dst[2 * H + i] = first ? a_gate[c][j] : dst[2 * H + i] + a_gate[c][j];
+          dst[i] = s == 0 ? a_pre[c][j] : dst[i] + a_pre[c][j];
+          dst[H + i] = s == 0 ? a_post[c][j] : dst[H + i] + a_post[c][j];
         }
       }
     }
     if (SLOTS > 1) lds_barrier();
   }
   if (SLOTS > 1)
-    for (int i = threadIdx.x; i < 3 * H; i += 1024) out[i] = slot_sum[i];
+    for (int i = threadIdx.x; i < 2 * H; i += THREADS) out[i] = slot_sum[i];
 }
 
 // dw_pre, dw_post and dgate [H] from the workgroups' partial sums: 64 columns a
@@ -311,16 +432,27 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(NormArgs p) {
   __shared__ float part[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = (int)blockIdx.x * 64 + lane, which = blockIdx.y;
-  float *out = which == 0 ? p.dw_pre : which == 1 ? p.dw_post : (p.gate_kind == 1 ? p.dgate : nullptr);
-  if (!out) return;  // the whole workgroup
+  if (which == 0 ? !p.dw_pre : !(p.dw_post || p.gate_kind == 1)) return;  // the whole workgroup
   float s = 0.0f;
-  if (col < p.H)
-    for (int g = wave; g < p.groups; g += 16) s += p.partial[((int64_t)g * 3 + which) * p.H + col];
+  if (col < p.H) {
+#pragma unroll 8
+    for (int g = wave; g < p.groups; g += 16) s += p.partial[((int64_t)g * 2 + which) * p.H + col];
+  }
   part[wave][lane] = s;
   lds_barrier();
   if (wave != 0 || col >= p.H) return;
   for (int w = 1; w < 16; ++w) s += part[w][lane];
-  out[col] = s;
+  if (which == 0) {
+    p.dw_pre[col] = s;
+    return;
+  }
+  s *= p.alpha;
+  float phi = 1.0f;
+  if (p.gate_kind == 1) {
+    phi = gate_phi(p.gate_fn, gate_scalar(p, col));
+    p.dgate[col] = gate_slope(p.gate_fn, phi) * (p.w_post ? p.w_post[col] * s : s);
+  }
+  if (p.dw_post) p.dw_post[col] = phi * s;
 }
 
 template <bool XBF>
@@ -338,12 +470,13 @@ hipError_t norm_forward_t(const NormArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-int norm_slots(int H) { return H <= 512 ? 16 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1; }
+int norm_tpr(int H) { return H <= 512 ? 64 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024; }
+int norm_slots(int H) { return back_threads(norm_tpr(H)) / norm_tpr(H); }
 
 template <bool XBF>
 hipError_t norm_backward_t(const NormArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)a.groups), block(1024);
-  const size_t lds = norm_slots(a.H) > 1 ? (size_t)3 * a.H * sizeof(float) : 0;
+  const dim3 grid((unsigned)a.groups), block(back_threads(norm_tpr(a.H)));
+  const size_t lds = norm_slots(a.H) > 1 ? (size_t)2 * a.H * sizeof(float) : 0;
   if (a.H <= 512) hipLaunchKernelGGL((k_norm_backward<XBF, 64, 1>), grid, block, lds, s, a);
   else if (a.H <= 2048) hipLaunchKernelGGL((k_norm_backward<XBF, 256, 1>), grid, block, lds, s, a);
   else if (a.H <= 4096) hipLaunchKernelGGL((k_norm_backward<XBF, 512, 1>), grid, block, lds, s, a);
@@ -352,7 +485,7 @@ hipError_t norm_backward_t(const NormArgs &a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.dw_pre || a.dw_post || (a.dgate && a.gate_kind == 1)) {
-    hipLaunchKernelGGL(k_norm_colsum, dim3((unsigned)cdiv(a.H, 64), 3), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(k_norm_colsum, dim3((unsigned)cdiv(a.H, 64), 2), dim3(1024), 0, s, a);
     e = hipGetLastError();
   }
   return e;
@@ -360,11 +493,10 @@ hipError_t norm_backward_t(const NormArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups of the backward: one per CU (1024 threads each), fewer where there
-// are fewer rows.
+// Workgroups of the backward: 1024 threads a CU, fewer where there are fewer rows.
 int norm_backward_groups(int64_t T, int H) {
-  const int64_t need = cdiv(T, norm_slots(H));
-  return (int)(need < 256 ? need : 256);
+  const int64_t need = cdiv(T, norm_slots(H)), most = 256 * 1024 / back_threads(norm_tpr(H));
+  return (int)(need < most ? need : most);
 }
 
 hipError_t launch_norm_forward(const NormArgs &a, hipStream_t s) {

@@ -61,7 +61,7 @@ struct NormArgs {
   uint16_t *df;              // bf16 or null
   float *dgate;              // fp32: [H], [T] or [T, H]
   float *dw_post, *dw_pre;   // [H]
-  float *partial;            // [groups][3][H]
+  float *partial;            // [groups][2][H]
   int groups;
 };
 hipError_t launch_norm_forward(const NormArgs &a, hipStream_t s);
