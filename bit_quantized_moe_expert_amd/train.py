@@ -10,7 +10,7 @@ the rest by the library.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -41,9 +41,11 @@ def _arg(t, name, shape, dtype, index):
     once shapes and types are known to be right)."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == index
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     M._shape(t, name, tuple(shape))
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -83,6 +85,16 @@ def _run(index, fn, *args):
 
 def _p(t):
     return None if t is None else t.data_ptr()
+
+
+def _scratch(like, nbytes):
+    """(tensor, address, size) of a 256-byte aligned workspace on like's device."""
+    ws = like.new_empty(nbytes, dtype=_U8)
+    ptr = ws.data_ptr()
+    if ptr & 255:  # the caching allocator's blocks are aligned further; another allocator's need not be
+        ws = like.new_empty(nbytes + 256, dtype=_U8)
+        ptr = (ws.data_ptr() + 255) & ~255
+    return ws, ptr, nbytes
 
 
 @dataclass
@@ -185,12 +197,18 @@ def glu_backward(dh, gu, glu: int = 0, alpha: float = 0.0, limit: float = 0.0, i
     return out
 
 
-class _BlockNorm(ctypes.Structure):
-    """Mirror of nf4moe_block_norm_t."""
-    _fields_ = [("H", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("w_post", ctypes.c_void_p),
-                ("w_pre", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_kind", ctypes.c_int32),
-                ("gate_dtype", ctypes.c_int32), ("gate_fn", ctypes.c_int32), ("alpha", ctypes.c_float),
-                ("eps", ctypes.c_float)]
+# The C descriptors as packed bytes (which a c_void_p argument passes by address):
+# nf4moe_block_norm_t (H, x_dtype, w_post, w_pre, gate, gate_kind, gate_dtype, gate_fn,
+# alpha, eps) and nf4moe_adapters_t (L, rank, K, N, A, B, scale).
+_BLOCK_NORM = struct.Struct("@2i3P3i2f0P")
+_ADAPTERS = struct.Struct("@4i3P")
+
+
+def _i32(v, name):
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name}={v} does not fit 32 bits")
+    return v
 
 
 def _norm_struct(x, f, w_post, w_pre, gate, gate_fn, alpha, eps):
@@ -207,8 +225,8 @@ def _norm_struct(x, f, w_post, w_pre, gate, gate_fn, alpha, eps):
         gdt = _dt(gate, "gate")
         gp = _arg(gate, "gate", gate.shape, gate.dtype, i)
     fp = _arg(f, "f", x.shape, _BF16, i)
-    st = _BlockNorm(H, dt, _arg(w_post, "w_post", (H,), _F32, i), _arg(w_pre, "w_pre", (H,), _F32, i), gp, kind, gdt,
-                    gate_fn, alpha, eps)
+    st = _BLOCK_NORM.pack(_i32(H, "H"), dt, _arg(w_post, "w_post", (H,), _F32, i) or 0, _arg(w_pre, "w_pre", (H,), _F32, i) or 0,
+                          gp or 0, kind, gdt, _i32(gate_fn, "gate_fn"), alpha, eps)
     return st, _arg(x, "x", x.shape, x.dtype, i), fp, T, H, i
 
 
@@ -230,10 +248,10 @@ def block_norm_forward(x, f=None, *, w_post=None, w_pre=None, gate=None, gate_fn
         if out is None:
             out = torch.empty_like(x)
         np_ = _arg(out, "out", x.shape, x.dtype, i)
-    y = x.new_empty((T, H), dtype=_BF16) if w_pre is not None else None
+    y = None if w_pre is None else torch.empty_like(x) if x.dtype is _BF16 else x.new_empty((T, H), dtype=_BF16)
     rp = x.new_empty((T,), dtype=_F32) if w_post is not None else None
     r = x.new_empty((T,), dtype=_F32) if w_pre is not None else None
-    _run(i, M.lib().nf4moe_block_norm_forward, ctypes.addressof(st), xp, fp, T, np_, _p(y), _p(rp), _p(r))
+    _run(i, M.lib().nf4moe_block_norm_forward, st, xp, fp, T, np_, _p(y), _p(rp), _p(r))
     return dict(x=x if f is None else out, y=y, rstd_post=rp, rstd_pre=r)
 
 
@@ -264,16 +282,10 @@ def block_norm_backward(dx_new, dy, x_new, f=None, *, rstd_post=None, rstd_pre=N
     if w_pre is not None:
         out["dw_pre"] = torch.empty_like(w_pre)
     L = M.lib()
-    ws, wsp, nb = M._workspace(L.nf4moe_block_norm_workspace_bytes(H, T), x_new.device)
-    _run(i, L.nf4moe_block_norm_backward, ctypes.addressof(st), dxp, dyp, xp, fp, rp, r, T, out["dx"].data_ptr(),
+    ws, wsp, nb = _scratch(x_new, L.nf4moe_block_norm_workspace_bytes(H, T))
+    _run(i, L.nf4moe_block_norm_backward, st, dxp, dyp, xp, fp, rp, r, T, out["dx"].data_ptr(),
          _p(out.get("df")), _p(out.get("dgate")), _p(out.get("dw_post")), _p(out.get("dw_pre")), wsp, nb)
     return out
-
-
-class _Adapters(ctypes.Structure):
-    """Mirror of nf4moe_adapters_t."""
-    _fields_ = [("L", ctypes.c_int32), ("rank", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
-                ("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 @dataclass
@@ -293,16 +305,16 @@ def adapter_plan(ids, num_adapters: int) -> AdapterPlan:
     (R,), i = _dims(ids, "ids", 1), ids.get_device()
     ip = _arg(ids, "ids", (R,), _I32, i)
     L = M.lib()
-    ws, wsp, nb = M._workspace(L.nf4moe_adapter_plan_bytes(R, num_adapters), ids.device)
+    ws, wsp, nb = _scratch(ids, L.nf4moe_adapter_plan_bytes(R, num_adapters))
     _run(i, L.nf4moe_adapter_plan, ip, R, num_adapters, wsp, nb)
-    return AdapterPlan(ws, wsp.value, nb, R, num_adapters)
+    return AdapterPlan(ws, wsp, nb, R, num_adapters)
 
 
 def _adapter_struct(A, B, ids, scale, plan, x_row_of, i):
     """The descriptor, (R, K, N, rank, L), and the addresses of ids, the gather, the plan and its size."""
     (L, rank, K), (R,), N = _dims(A, "A", 3), _dims(ids, "ids", 1), _dims(B, "B", 3)[1]
-    st = _Adapters(L, rank, K, N, _arg(A, "A", A.shape, _BF16, i), _arg(B, "B", (L, N, rank), _BF16, i),
-                   _arg(scale, "scale", (L,), _F32, i))
+    st = _ADAPTERS.pack(_i32(L, "L"), _i32(rank, "rank"), _i32(K, "K"), _i32(N, "N"), _arg(A, "A", A.shape, _BF16, i),
+                        _arg(B, "B", (L, N, rank), _BF16, i), _arg(scale, "scale", (L,), _F32, i) or 0)
     rows = (_arg(x_row_of, "x_row_of", (R,), _I32, i), _arg(ids, "ids", (R,), _I32, i))
     if plan is None:
         return st, (R, K, N, rank, L), rows, (None, 0)
@@ -349,9 +361,9 @@ def adapter_forward(x, A, B, ids, *, base=None, scale=None, x_row_of=None, out=N
         out = x.new_empty((R, N), dtype=dtype)
     op = _arg(out, "out", (R, N), dtype, i)
     t = x.new_empty((R, rank), dtype=_F32) if return_t else None
-    lib, sp = M.lib(), ctypes.addressof(st)
+    lib, sp = M.lib(), st
     nb = lib.nf4moe_adapter_workspace_bytes(sp, R, 0)
-    ws, wsp, nb = M._workspace(nb, x.device) if nb else (None, None, 0)
+    ws, wsp, nb = _scratch(x, nb) if nb else (None, None, 0)
     _run(i, lib.nf4moe_adapter_forward, sp, xp, rows, rp, ip, pp, pn, R, bp, op, dt, _p(t), wsp, nb)
     return (out, t) if return_t else out
 
@@ -395,8 +407,8 @@ def adapter_backward(dy, x, t, A, B, ids, *, scale=None, x_row_of=None, dx_base=
         out["dA"] = dy.new_empty((L, rank, K), dtype=_F32)
     if "dB" in need:
         out["dB"] = dy.new_empty((L, N, rank), dtype=_F32)
-    lib, sp = M.lib(), ctypes.addressof(st)
-    ws, wsp, nb = M._workspace(lib.nf4moe_adapter_workspace_bytes(sp, R, 1), dy.device)
+    lib, sp = M.lib(), st
+    ws, wsp, nb = _scratch(dy, lib.nf4moe_adapter_workspace_bytes(sp, R, 1))
     _run(i, lib.nf4moe_adapter_backward, sp, dyp, src, xp, xs, max(rows, 1), rp, tp, ip, pp, pn, R, bp, _p(out.get("dx")), dt,
          _p(out.get("dA")), _p(out.get("dB")), wsp, nb)
     return out

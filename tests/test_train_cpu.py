@@ -171,11 +171,9 @@ def test_glu_validation():
 
 
 def _norm(H=64, x_dtype=1, w_post=FAKE, w_pre=FAKE, gate=None, kind=0, gdt=0, fn=0, alpha=1.0, eps=1e-6):
-    import ctypes
-
     from bit_quantized_moe_expert_amd import train
-    st = train._BlockNorm(H, x_dtype, w_post, w_pre, gate, kind, gdt, fn, alpha, eps)
-    return st, ctypes.addressof(st)
+    st = train._BLOCK_NORM.pack(H, x_dtype, w_post or 0, w_pre or 0, gate or 0, kind, gdt, fn, alpha, eps)
+    return st, st
 
 
 def test_block_norm_validation():
@@ -213,13 +211,11 @@ def test_block_norm_validation():
 
 
 def test_adapter_validation():
-    import ctypes
-
     from bit_quantized_moe_expert_amd import train
 
     def desc(L_=4, rank=16, K=64, N=64, A=FAKE, B=FAKE, scale=None):
-        st = train._Adapters(L_, rank, K, N, A, B, scale)
-        return st, ctypes.addressof(st)
+        st = train._ADAPTERS.pack(L_, rank, K, N, A or 0, B or 0, scale or 0)
+        return st, st
     st, a = desc()
     assert L.nf4moe_adapter_plan_bytes(0, 4) == 0 and L.nf4moe_adapter_plan_bytes(8, 0) == 0
     assert L.nf4moe_adapter_plan_bytes(8, 4097) == 0 and L.nf4moe_adapter_plan_bytes(8, 4096) > 0
