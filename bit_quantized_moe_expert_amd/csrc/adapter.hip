@@ -320,12 +320,11 @@ __host__ __device__ inline int low_groups(int rank) { return part_pack(rank) ? r
 // gathered x (each token's row is read by every expert that it was routed to) and
 // of all adapters then stay in that XCD's L2 (4 slices: a pair of XCDs a slice). Few
 // rows still make many workgroups.
-// Inside, the four waves take every fourth 64-wide step of the slice for all the
-// tile's rows, so each adapter row is read once per workgroup; a row's step is one
+// Inside, the W waves take every W-th 64-wide step of the slice for all the tile's rows, so each adapter row is read once per workgroup; a row's step is one
 // whole 128-byte line, taken as two 64-byte halves.
 constexpr int kSliceMin = 256;   // no slice is narrower
 
-template <int RT, int NS>
+template <int RT, int NS, int W>
 __device__ inline void shrink_rows(const LowRankArgs &p, const int32_t *order, int n, int l, int k, int k1, f32x4_t (&acc)[4][RT]) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const uint16_t *xrow[NS], *wrow[RT];
@@ -342,7 +341,7 @@ __device__ inline void shrink_rows(const LowRankArgs &p, const int32_t *order, i
   for (int s = 0; s < NS; ++s) xrow[s] = p.x + (int64_t)r[s] * p.K;
 #pragma unroll
   for (int j = 0; j < RT; ++j) wrow[j] = p.W1 + ((int64_t)l * p.rank + min(16 * j + l16, p.rank - 1)) * p.K;
-  for (; k < k1; k += 256) {
+  for (; k < k1; k += 64 * W) {
     // Every load is made (places past the slice read its last ones, against zero
     // weights): no branch splits a step's loads.
     uint4 x[NS][2], w[RT][2];
@@ -367,8 +366,8 @@ __device__ inline void shrink_rows(const LowRankArgs &p, const int32_t *order, i
   }
 }
 
-template <int RT>
-__global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int slice) {
+template <int RT, int W>
+__global__ __launch_bounds__(64 * W) void k_shrink(LowRankArgs p, int slices, int slice) {
   constexpr int kPad = RT * 16 + 4, SL = RT <= 2 ? 4 : RT == 4 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) float red[SL][kAdTile][kPad];
   const int si = blockIdx.x % slices, ti = blockIdx.x / slices;
@@ -381,7 +380,7 @@ __global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int s
   const int nr8 = rank / 8, g8 = low_groups(rank);
   if (l < 0) {  // rows without an adapter: low is 0, and the parts are not read
     if (slices == 1 && p.low)
-      for (int i = tid; i < n * nr8; i += 256) {
+      for (int i = tid; i < n * nr8; i += 64 * W) {
         const float z[8] = {};
         store_elems8<false>(p.low, (int64_t)order[i / nr8] * rank + 8 * (i % nr8), z);
       }
@@ -389,12 +388,12 @@ __global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int s
   }
   const int k = si * slice + 64 * wave, k1 = min(p.K, (si + 1) * slice);
   f32x4_t acc[4][RT] = {};
-  if (n <= 16) shrink_rows<RT, 1>(p, order, n, l, k, k1, acc);
-  else if (n <= 32) shrink_rows<RT, 2>(p, order, n, l, k, k1, acc);
-  else shrink_rows<RT, 4>(p, order, n, l, k, k1, acc);
+  if (n <= 16) shrink_rows<RT, 1, W>(p, order, n, l, k, k1, acc);
+  else if (n <= 32) shrink_rows<RT, 2, W>(p, order, n, l, k, k1, acc);
+  else shrink_rows<RT, 4, W>(p, order, n, l, k, k1, acc);
   // lane: row 16 s + l16, ranks 16 j + 4 q ..; the waves' sums in a fixed order, SL of them at a time
 #pragma unroll
-  for (int turn = 0; turn < 4 / SL; ++turn) {
+  for (int turn = 0; turn < W / SL; ++turn) {
     if (wave / SL == turn) {
 #pragma unroll
       for (int s = 0; s < 4; ++s)
@@ -408,7 +407,7 @@ __global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int s
   }
   if (slices == 1) {  // nothing to join
     const float m = p.scale ? p.scale[l] : 1.0f;
-    for (int i = tid; i < n * g8; i += 256) {
+    for (int i = tid; i < n * g8; i += 64 * W) {
       const int row = i / g8, r8 = i % g8;
       float v[8] = {};
       if (r8 < nr8) {
@@ -426,7 +425,7 @@ __global__ __launch_bounds__(256) void k_shrink(LowRankArgs p, int slices, int s
   }
   float *out = p.partial + ((int64_t)si * p.R + tile.y) * rank;
   const int r4 = rank / 4;
-  for (int i = tid; i < n * r4; i += 256) {
+  for (int i = tid; i < n * r4; i += 64 * W) {
     f32x4_t v = *reinterpret_cast<const f32x4_t *>(&red[0][i / r4][4 * (i % r4)]);
 #pragma unroll
     for (int w = 1; w < SL; ++w) v += *reinterpret_cast<const f32x4_t *>(&red[w][i / r4][4 * (i % r4)]);
@@ -864,17 +863,19 @@ hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Slices of K, each a multiple of 64 and at least kSliceMin wide: up to 8 where
-// there are few tiles to fill the chip with, else up to 4 (1003 rows of rank 32, K =
-// 1440: 5.1 us with 8, 5.9 with 4, 10.2 with 1; 32768 rows of rank 16, K = 2048,
-// product and join: 37.3, 33.7 and 38.4 us). A narrow K is one slice and needs no
-// join.
-static int slice_width(int R, int K) {
-  if (K <= 512) return 512;
+// Slices of K, each a multiple of 64 and at least kSliceMin wide: up to 8 where there
+// are few tiles to fill the chip with, else up to 4 (32768 rows of rank 16, K = 2048,
+// product and join: 37.3 us with 8, 33.7 with 4, 38.4 with 1; 4099 rows of rank 64, K =
+// 2880: 17.3 with 4, 32.3 with 1). A narrow K, or few rows of a low rank with 16 waves
+// a workgroup, is one slice and needs no join (a backward of 168 rows of rank 16, 2784 x
+// 2744: 40 against 43 us a pass; of 979 rows of rank 8, 992 x 864: 36 against 40).
+static bool one_slice(int R, int K, int rank) { return K <= 512 || (rank <= 32 && R < 4096); }
+static int slice_width(int R, int K, int rank) {
+  if (one_slice(R, K, rank)) return (int)cdiv(K, 64) * 64;
   const int w = (int)cdiv(cdiv(K, R < 4096 ? 8 : 4), 64) * 64;
   return w < kSliceMin ? kSliceMin : w;
 }
-int adapter_slices(int R, int K) { return (int)cdiv(K, slice_width(R, K)); }
+int adapter_slices(int R, int K, int rank) { return (int)cdiv(K, slice_width(R, K, rank)); }
 size_t adapter_parts_elems(int R, int rank) { return (size_t)R * 32 * part_steps(rank); }
 
 template <int PACK, bool BF, int CB>
@@ -896,12 +897,15 @@ static void expand_pack(const LowRankArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
-  const int slice = slice_width(a.R, a.K), slices = adapter_slices(a.R, a.K), pack = part_pack(a.rank);
+  const int slice = slice_width(a.R, a.K, a.rank), slices = adapter_slices(a.R, a.K, a.rank), pack = part_pack(a.rank);
   const dim3 grid((unsigned)(a.plan.max_tiles * slices)), block(256);
-  if (a.rank <= 16) hipLaunchKernelGGL(k_shrink<1>, grid, block, 0, s, a, slices, slice);
-  else if (a.rank <= 32) hipLaunchKernelGGL(k_shrink<2>, grid, block, 0, s, a, slices, slice);
-  else if (a.rank <= 64) hipLaunchKernelGGL(k_shrink<4>, grid, block, 0, s, a, slices, slice);
-  else hipLaunchKernelGGL(k_shrink<8>, grid, block, 0, s, a, slices, slice);
+  const bool deep = slices == 1 && a.K > 512;  // (rank at most 32)
+  if (a.rank <= 16 && deep) hipLaunchKernelGGL((k_shrink<1, 16>), grid, dim3(1024), 0, s, a, slices, slice);
+  else if (a.rank <= 32 && deep) hipLaunchKernelGGL((k_shrink<2, 16>), grid, dim3(1024), 0, s, a, slices, slice);
+  else if (a.rank <= 16) hipLaunchKernelGGL((k_shrink<1, 4>), grid, block, 0, s, a, slices, slice);
+  else if (a.rank <= 32) hipLaunchKernelGGL((k_shrink<2, 4>), grid, block, 0, s, a, slices, slice);
+  else if (a.rank <= 64) hipLaunchKernelGGL((k_shrink<4, 4>), grid, block, 0, s, a, slices, slice);
+  else hipLaunchKernelGGL((k_shrink<8, 4>), grid, block, 0, s, a, slices, slice);
   if (slices > 1) {
     const int64_t items = (int64_t)a.R * low_groups(a.rank);
     hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices, a.L, a.ids);

@@ -113,7 +113,7 @@ AdapterCarve carve_adapter(void *ws, const nf4moe_adapters_t &a, int R, bool bac
   Bump b{(char *)ws};
   AdapterPlan lay;
   c.plan = b.take<char>(adapter_plan_layout(R, a.L, nullptr, &lay));
-  c.slices = b.take<float>((size_t)adapter_slices(R, backward ? a.N : a.K) * R * a.rank);
+  c.slices = b.take<float>((size_t)adapter_slices(R, backward ? a.N : a.K, a.rank) * R * a.rank);
   c.parts = b.take<uint16_t>(adapter_parts_elems(R, a.rank));
   if (backward) {
     c.u = b.take<float>((size_t)R * a.rank);

@@ -116,10 +116,10 @@ struct LowRankArgs {
   const void *base;    // or null: zeros
   void *out;
   bool bf16;           // base and out
-  float *partial;      // scratch: [adapter_slices(R, K)][R][rank]
+  float *partial;      // scratch: [adapter_slices(R, K, rank)][R][rank]
   uint16_t *parts;     // scratch: adapter_parts_elems(R, rank) (null without out)
 };
-int adapter_slices(int R, int K);
+int adapter_slices(int R, int K, int rank);
 size_t adapter_parts_elems(int R, int rank);
 hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s);
 
