@@ -282,34 +282,67 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
 }
 
 // ------------------------------------------------------------------ low-rank values
+// The vector memory unit takes the 16-byte accesses of four neighbouring lanes in
+// one cycle where they are neighbours in memory, and in four where they are not (a
+// matrix operand's neighbouring lanes are neighbouring ROWS: counted, 54 cache
+// accesses per load instruction instead of 16, which bound the kernels). So a quad of
+// lanes reads 64 contiguous bytes of one row per instruction, of its four rows in
+// turn, and this turns the 4 x 4 pieces: in, register c of lane j is piece j of row c;
+// out, register m of lane j is piece m of row j. Its own inverse.
+template <int CTRL>
+__device__ inline uint32_t dpp_u32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ inline void swap_pieces(uint4 &lo, uint4 &hi, bool upper) {
+  uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t fb = dpp_u32<CTRL>(b[i]), fa = dpp_u32<CTRL>(a[i]);
+    const uint32_t na = upper ? fb : a[i], nb = upper ? b[i] : fa;
+    a[i] = na;
+    b[i] = nb;
+  }
+  lo = make_uint4(a[0], a[1], a[2], a[3]);
+  hi = make_uint4(b[0], b[1], b[2], b[3]);
+}
+__device__ inline void turn_quad(uint4 (&v)[4]) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+  swap_pieces<0xB1>(v[0], v[1], odd);   // quad_perm [1,0,3,2]
+  swap_pieces<0xB1>(v[2], v[3], odd);
+  swap_pieces<0x4E>(v[0], v[2], high);  // quad_perm [2,3,0,1]
+  swap_pieces<0x4E>(v[1], v[3], high);
+}
+
 // How the second product takes the low-rank values: `steps` matrix instructions of
 // 32 places a row and 16 columns. The places hold the three bf16 parts of the
 // scaled values: for rank 8 all three parts in one step (PACK 1), for rank 16 two
 // and then the third (PACK 2), else 32 ranks of one part a step, the parts of a
-// block of 32 ranks following each other (PACK 0). Other places hold zeros.
+// block of 32 ranks following each other (PACK 0). Other places hold zeros. In memory
+// they lie as the instructions take them, [tile of 64 rows][16 rows][step][lane].
 __host__ __device__ inline int part_pack(int rank) { return rank == 8 ? 1 : rank == 16 ? 2 : 0; }
 __host__ __device__ inline int part_steps(int rank) { return rank <= 16 ? rank / 8 : 3 * ((rank + 31) / 32); }
-__device__ inline int part_place(int pack, int r8, int part) {  // place of ranks 8 r8 .. of one part in a row
-  return pack == 1 ? 8 * part : pack == 2 ? 16 * part + 8 * r8 : 96 * (r8 >> 2) + 32 * part + 8 * (r8 & 3);
-}
 
-// The low-rank values v of ranks 8 r8 .. of one row, where they go: low by row, and
-// the scaled values' parts in grouped order.
-__device__ inline void put_low(const LowRankArgs &p, int place, int row, int r8, const float (&v)[8], float m) {
-  const int pack = part_pack(p.rank);
+// The low-rank values v of ranks 8 r8 .. of row i of a tile, where they go: low by
+// row, and the scaled values' parts.
+__device__ inline void put_low(const LowRankArgs &p, int tile, int i, int row, int r8, const float (&v)[8], float m) {
+  const int pack = part_pack(p.rank), steps = part_steps(p.rank);
   float sv[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) sv[k] = v[k] * m;
   if (p.low && 8 * r8 < p.rank) store_elems8<false>(p.low, (int64_t)row * p.rank + 8 * r8, p.low_scaled ? sv : v);
   if (!p.parts) return;
-  uint4 hi, mid, lo;
-  split3(sv, hi, mid, lo);
-  uint16_t *d = p.parts + (int64_t)place * (32 * part_steps(p.rank));
-  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 0)) = hi;
-  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 1)) = mid;
-  *reinterpret_cast<uint4 *>(d + part_place(pack, r8, 2)) = lo;
+  uint4 q[3];
+  split3(sv, q[0], q[1], q[2]);
+  uint4 *d = reinterpret_cast<uint4 *>(p.parts) + ((int64_t)tile * 4 + (i >> 4)) * steps * 64 + (i & 15);
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    const int g = pack == 1 ? part : 2 * part + r8;  // PACK 1 and 2: groups of 8 places one after the other
+    const int step = pack ? g >> 2 : 3 * (r8 >> 2) + part, lane = 16 * (pack ? g & 3 : r8 & 3);
+    d[step * 64 + lane] = q[part];
+  }
   if (pack && r8 == 0)
-    for (int c = 24 * pack; c < 32 * pack; c += 8) *reinterpret_cast<uint4 *>(d + c) = make_uint4(0, 0, 0, 0);
+    for (int g = 3 * pack; g < 4 * pack; ++g) d[(g >> 2) * 64 + 16 * (g & 3)] = make_uint4(0, 0, 0, 0);
 }
 // Groups of 8 ranks of a row, with the empty ones of the last block of 32.
 __host__ __device__ inline int low_groups(int rank) { return part_pack(rank) ? rank / 8 : (rank + 31) / 32 * 4; }
@@ -320,48 +353,56 @@ __host__ __device__ inline int low_groups(int rank) { return part_pack(rank) ? r
 // gathered x (each token's row is read by every expert that it was routed to) and
 // of all adapters then stay in that XCD's L2 (4 slices: a pair of XCDs a slice). Few
 // rows still make many workgroups.
-// Inside, the W waves take every W-th 64-wide step of the slice for all the tile's rows, so each adapter row is read once per workgroup; a row's step is one
-// whole 128-byte line, taken as two 64-byte halves.
-constexpr int kSliceMin = 256;   // no slice is narrower
+// Inside, the W waves take every W-th 128-wide step of the slice for all the tile's
+// rows, so each adapter row is read once per workgroup. Four waves, for many rows:
+// eight take 31.4 against 27.1 us for 32768 gathered rows of rank 16, 89.7 / 57.1 of 64. A quad reads 64 bytes of one
+// row, the four quads of a row 256.
+constexpr int kSliceMin = 256;  // no slice is narrower
 
 template <int RT, int NS, int W>
 __device__ inline void shrink_rows(const LowRankArgs &p, const int32_t *order, int n, int l, int k, int k1, f32x4_t (&acc)[4][RT]) {
-  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-  const uint16_t *xrow[NS], *wrow[RT];
-  int r[NS];
+  const int lane = threadIdx.x & 63, q = lane >> 4, first = 4 * ((lane >> 2) & 3);  // this quad's rows: first + c
+  int r[NS][4];
 #pragma unroll
-  for (int s = 0; s < NS; ++s) r[s] = order[min(16 * s + l16, n - 1)];
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r[s][c] = order[min(16 * s + first + c, n - 1)];
   if (p.row_of) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) r[s] = p.row_of[r[s]];
+    for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int s = 0; s < NS; ++s) r[s] = min(max(r[s], 0), p.x_rows - 1);
+      for (int c = 0; c < 4; ++c) r[s][c] = p.row_of[r[s][c]];
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) r[s][c] = min(max(r[s][c], 0), p.x_rows - 1);
   }
-#pragma unroll
-  for (int s = 0; s < NS; ++s) xrow[s] = p.x + (int64_t)r[s] * p.K;
-#pragma unroll
-  for (int j = 0; j < RT; ++j) wrow[j] = p.W1 + ((int64_t)l * p.rank + min(16 * j + l16, p.rank - 1)) * p.K;
-  for (; k < k1; k += 64 * W) {
+  const uint16_t *w0 = p.W1 + (int64_t)l * p.rank * p.K;
+  for (; k < k1; k += 128 * W) {
     // Every load is made (places past the slice read its last ones, against zero
     // weights): no branch splits a step's loads.
-    uint4 x[NS][2], w[RT][2];
+    const int kl = k + 32 * q + 8 * (lane & 3), kc = min(kl, k1 - 8);
+    uint4 x[NS][4], w[RT][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int kc = min(k + 32 * h + 8 * q, k1 - 8);
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) w[j][h] = load16(wrow[j] + kc);
+      for (int c = 0; c < 4; ++c) w[j][c] = load16(w0 + (int64_t)min(16 * j + first + c, p.rank - 1) * p.K + kc);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) x[s][h] = load16(xrow[s] + kc);
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[s][c] = load16(p.x + (int64_t)r[s][c] * p.K + kc);
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      if (kl >= k1) w[j][0] = w[j][1] = w[j][2] = w[j][3] = make_uint4(0, 0, 0, 0);
+      turn_quad(w[j]);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool ok = k + 32 * h + 8 * q < k1;
+    for (int s = 0; s < NS; ++s) {
+      turn_quad(x[s]);
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const uint4 wv = ok ? w[j][h] : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < RT; ++j)
 #pragma unroll
-        for (int s = 0; s < NS; ++s) acc[s][j] = mfma16(wv, x[s][h], acc[s][j]);
-      }
+        for (int c = 0; c < 4; ++c) acc[s][j] = mfma16(w[j][c], x[s][c], acc[s][j]);
     }
   }
 }
@@ -386,7 +427,7 @@ __global__ __launch_bounds__(64 * W) void k_shrink(LowRankArgs p, int slices, in
       }
     return;
   }
-  const int k = si * slice + 64 * wave, k1 = min(p.K, (si + 1) * slice);
+  const int k = si * slice + 128 * wave, k1 = min(p.K, (si + 1) * slice);
   f32x4_t acc[4][RT] = {};
   if (n <= 16) shrink_rows<RT, 1, W>(p, order, n, l, k, k1, acc);
   else if (n <= 32) shrink_rows<RT, 2, W>(p, order, n, l, k, k1, acc);
@@ -419,7 +460,7 @@ __global__ __launch_bounds__(64 * W) void k_shrink(LowRankArgs p, int slices, in
           v[c] = u;
         }
       }
-      put_low(p, tile.y + row, order[row], r8, v, m);
+      put_low(p, ti, row, order[row], r8, v, m);
     }
     return;
   }
@@ -433,16 +474,17 @@ __global__ __launch_bounds__(64 * W) void k_shrink(LowRankArgs p, int slices, in
   }
 }
 
-// The slices' sums, added in order, for 8 ranks of one place a thread: out by row,
-// and the scaled value's parts in grouped order.
-__global__ __launch_bounds__(256) void k_shrink_join(LowRankArgs p, int slices, int L, const int32_t *__restrict__ ids) {
+// The slices' sums, added in order, for 8 ranks of one row of a tile a thread.
+__global__ __launch_bounds__(256) void k_shrink_join(LowRankArgs p, int slices) {
   const int nr8 = p.rank / 8, g8 = low_groups(p.rank);
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int place = (int)(i / g8), r8 = (int)(i % g8);
-  if (place >= p.R) return;
-  const int row = p.plan.order[place], l = bin_of(ids[row], L);
+  const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int ti = (int)(item / (kAdTile * g8)), i = (int)(item % (kAdTile * g8)) / g8, r8 = (int)(item % g8);
+  if (ti >= p.plan.counts[0]) return;
+  const int4 tile = p.plan.tiles[ti];
+  if (i >= tile.z) return;
+  const int l = tile.x, place = tile.y + i;
   float v[8] = {};
-  if (l < L && r8 < nr8) {
+  if (l >= 0 && r8 < nr8) {
     for (int s = 0; s < slices; ++s) {
       float u[8];
       load_elems8<false>(p.partial, ((int64_t)s * p.R + place) * p.rank + 8 * r8, u);
@@ -450,143 +492,144 @@ __global__ __launch_bounds__(256) void k_shrink_join(LowRankArgs p, int slices, 
       for (int k = 0; k < 8; ++k) v[k] += u[k];
     }
   }
-  put_low(p, place, row, r8, v, p.scale && l < L ? p.scale[l] : 1.0f);
+  put_low(p, ti, i, p.plan.order[place], r8, v, p.scale && l >= 0 ? p.scale[l] : 1.0f);
 }
 
 // ------------------------------------------------------------------ expand
-// One workgroup per tile and CB x 128 columns, a wave 32 rows and CB blocks of 64
-// columns; no LDS and no barrier. The product is taken transposed (columns as the
-// matrix rows), so a lane ends with neighbouring columns of one row: 8 (bf16, by
-// pairing two column blocks) or 4 (fp32), 64 contiguous bytes of a row per access,
-// and base, product and out meet in registers. The low-rank values come ready for the
-// matrix instructions. Bound by HBM: without the product (rows that have no adapter)
-// the same accesses of 32768 x 2048 bf16 take 54 us, 5.0 TB/s; with it 62 us.
-template <int PACK, bool BF, int CB>
+// A wave takes S blocks of 16 rows and 128 columns, a workgroup of four waves a tile
+// of 64 rows and S x 128 columns; no LDS and no barrier. The product is taken
+// transposed (columns as the matrix rows), so a lane ends with whole 16-byte pieces of
+// one row's columns: pieces m = 0 .. 3 of the 128 (bf16) or twice 64 (fp32) columns,
+// 4 q + m of 16. base comes and out goes by turn_quad, 256 contiguous bytes of a row
+// per instruction, and the three meet in registers. Bound by HBM: without the product
+// (rows that have no adapter) the accesses of 32768 x 2048 bf16 take 54 us, 5.0 TB/s.
+template <int PACK, bool BF, int S>
 __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
   const int ti = blockIdx.x / blocks;  // a tile's column blocks follow each other: whole rows are in flight together
   if (ti >= p.plan.counts[0]) return;
   const int4 tile = p.plan.tiles[ti];
-  const int l = tile.x, n = tile.z, rank = p.rank, nr8 = rank / 8;
+  const int l = tile.x, rank = p.rank, nr8 = rank / 8;
   if (l < 0 && p.base == p.out) return;  // nothing to add
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, q = lane >> 4;
-  const int c0 = (int)(blockIdx.x % blocks) * (128 * CB) + (wave >> 1) * (64 * CB), r0 = (wave & 1) * 32;
-  if (r0 >= n || c0 >= p.N) return;
+  const int l16 = lane & 15, q = lane >> 4, first = 4 * ((lane >> 2) & 3);
+  constexpr int WR = 4 / S;  // waves along the rows; the others along the columns
+  const int c0 = ((int)(blockIdx.x % blocks) * S + wave / WR) * 128, r0 = (wave % WR) * 16 * S;
+  const int n = tile.z - r0;
+  if (n <= 0 || c0 >= p.N) return;
   const int32_t *order = p.plan.order + tile.y + r0;
-  const int rn = min(32, n - r0);
-  int rows[2];
+  int rows[S][4];  // this quad's rows: 16 s + first + c
 #pragma unroll
-  for (int s = 0; s < 2; ++s) rows[s] = order[min(16 * s + l16, rn - 1)];
-  const uint16_t *trow[2], *wrow[CB][4];
-  const int width = 32 * part_steps(rank);
-  constexpr int NT = PACK ? PACK : 3, BH = BF ? 2 : 4;
-  uint4 t[NT][2];
-  struct Block {
-    uint4 base[2][BH], w[4];
-  } blk[CB];
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) rows[s][c] = order[min(16 * s + first + c, n - 1)];
+  constexpr int NT = PACK ? PACK : 3, NB = BF ? 1 : 2, TPB = BF ? 8 : 4, E = BF ? 8 : 4;  // blocks, column tiles a block, values a piece
+  const int steps = part_steps(rank);
+  const uint4 *trow = reinterpret_cast<const uint4 *>(p.parts) + ((int64_t)ti * 4 + r0 / 16) * steps * 64 + lane;
+  uint4 w[8], t[NT][S];
   auto load_t = [&](int o) {
 #pragma unroll
     for (int k = 0; k < NT; ++k)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) t[k][s] = *reinterpret_cast<const uint4 *>(trow[s] + 96 * o + 32 * k);
+      for (int s = 0; s < S; ++s) t[k][s] = trow[(s * steps + 3 * o + k) * 64];
   };
   // the weights of the ranks that this lane's 8 places of block o hold; places of no part meet zeros
-  auto load_w = [&](int i, int o) {
+  auto load_w = [&](int o) {
     const int r8 = PACK == 1 ? 0 : PACK == 2 ? (q & 1) : 4 * o + q;
     const bool ok = PACK == 1 ? q < 3 : PACK == 2 ? true : r8 < nr8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) blk[i].w[j] = ok ? load16(wrow[i][j] + 8 * r8) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < 8; ++j) {
+      const int c = BF ? 32 * (l16 >> 2) + 4 * j + (l16 & 3) : 64 * (j >> 2) + 16 * (l16 >> 2) + 4 * (j & 3) + (l16 & 3);
+      const uint4 v = load16(p.W2 + ((int64_t)l * p.N + min(c0 + c, p.N - 1)) * rank + (ok ? 8 * r8 : 0));
+      w[j] = ok ? v : make_uint4(0, 0, 0, 0);
+    }
   };
   if (l >= 0) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) trow[s] = p.parts + (int64_t)(tile.y + r0 + min(16 * s + l16, rn - 1)) * width + 8 * q;
-#pragma unroll
-    for (int i = 0; i < CB; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 64 * i + (BF ? 32 * (j >> 1) + 8 * (l16 >> 2) + 4 * (j & 1) + (l16 & 3) : 16 * j + l16);
-        wrow[i][j] = p.W2 + ((int64_t)l * p.N + min(c, p.N - 1)) * rank;
-      }
-      load_w(i, 0);
-    }
+    load_w(0);
     load_t(0);
   }
-  // base of this lane's rows 16 s + l16, in flight during the product (rows and
-  // columns past the end read the last ones and are not stored)
+  // base, in flight during the product (rows and columns past the end read the last
+  // ones and are not stored)
+  const int cq = c0 + 4 * E * q + E * (lane & 3);  // this lane's piece, of block 0
+  uint4 base[S][NB][4];
   if (p.base) {
 #pragma unroll
-    for (int i = 0; i < CB; ++i)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int h = 0; h < BH; ++h) {
-          const int64_t at = (int64_t)rows[s] * p.N + min(c0 + 64 * i + (BF ? 32 * h + 8 * q : 16 * h + 4 * q), p.N - (BF ? 8 : 4));
-          blk[i].base[s][h] = BF ? load16(reinterpret_cast<const uint16_t *>(p.base) + at) : load16(reinterpret_cast<const float *>(p.base) + at);
+        for (int c = 0; c < 4; ++c) {
+          const int64_t at = (int64_t)rows[s][c] * p.N + min(cq + 64 * b, p.N - E);
+          base[s][b][c] = BF ? load16(reinterpret_cast<const uint16_t *>(p.base) + at) : load16(reinterpret_cast<const float *>(p.base) + at);
         }
   } else {
 #pragma unroll
-    for (int i = 0; i < CB; ++i)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int h = 0; h < BH; ++h) blk[i].base[s][h] = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 4; ++c) base[s][b][c] = make_uint4(0, 0, 0, 0);
   }
+  f32x4_t acc[S][8] = {};  // [16 rows][16 columns]
+  if (l >= 0) {
+    if constexpr (PACK != 0) {
 #pragma unroll
-  for (int i = 0; i < CB; ++i) {
-    Block &u = blk[i];
-    const int cb = c0 + 64 * i;
-    if (cb >= p.N) break;
-    f32x4_t acc[2][4] = {};  // [16 rows][16 columns]
-    if (l >= 0) {
-      if constexpr (PACK != 0) {
+      for (int o = 0; o < PACK; ++o) {
+        if (o == 1 && q >= 2) {  // the third part and 16 empty places; the other weights are the first step's
 #pragma unroll
-        for (int o = 0; o < PACK; ++o) {
-          if (o == 1 && q >= 2) {  // the third part and 16 empty places; the other weights are the first step's
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u.w[j] = make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(u.w[j], t[o][s], acc[s][j]);
+          for (int j = 0; j < 8; ++j) w[j] = make_uint4(0, 0, 0, 0);
         }
-      } else {
-        const int nb = (nr8 + 3) / 4;
-        for (int o = 0; o < nb; ++o) {
-          if (o > 0) load_w(i, o);
-          if (nb > 1 && (o > 0 || i > 0)) load_t(o);
 #pragma unroll
-          for (int part = 0; part < 3; ++part)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[s][j] = mfma16(u.w[j], t[part][s], acc[s][j]);
+          for (int j = 0; j < 8; ++j) acc[s][j] = mfma16(w[j], t[o][s], acc[s][j]);
+      }
+    } else {
+      for (int o = 0; o < (nr8 + 3) / 4; ++o) {
+        if (o > 0) {
+          load_w(o);
+          load_t(o);
         }
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[s][j] = mfma16(w[j], t[part][s], acc[s][j]);
       }
     }
+  }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (16 * s + l16 >= rn) continue;
-      const int64_t at = (int64_t)rows[s] * p.N;
+  for (int s = 0; s < S; ++s) {
+    if (16 * s >= n) break;
 #pragma unroll
-      for (int h = 0; h < BH; ++h) {
-        const int c = cb + (BF ? 32 * h + 8 * q : 16 * h + 4 * q);
-        if (c >= p.N) continue;
+    for (int b = 0; b < NB; ++b) {
+      uint4 (&v)[4] = base[s][b];
+      turn_quad(v);  // pieces m = 0 .. 3 of row 16 s + l16
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
         if constexpr (BF) {
-          float v[8];
-          unpack_bf16x8(u.base[s][h], v);
+          float f[8];
+          unpack_bf16x8(v[m], f);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            v[k] += acc[s][2 * h][k];
-            v[4 + k] += acc[s][2 * h + 1][k];
+            f[k] += acc[s][2 * m][k];
+            f[4 + k] += acc[s][2 * m + 1][k];
           }
-          store_elems8<true>(p.out, at + c, v);
+          v[m] = pack_bf16x8(f);
         } else {
-          const uint4 b = u.base[s][h];
-          store16(reinterpret_cast<float *>(p.out) + at + c,
-                  make_uint4(__float_as_uint(__uint_as_float(b.x) + acc[s][h][0]), __float_as_uint(__uint_as_float(b.y) + acc[s][h][1]),
-                             __float_as_uint(__uint_as_float(b.z) + acc[s][h][2]), __float_as_uint(__uint_as_float(b.w) + acc[s][h][3])));
+          const f32x4_t a = acc[s][TPB * b + m];
+          v[m] = make_uint4(__float_as_uint(__uint_as_float(v[m].x) + a[0]), __float_as_uint(__uint_as_float(v[m].y) + a[1]),
+                            __float_as_uint(__uint_as_float(v[m].z) + a[2]), __float_as_uint(__uint_as_float(v[m].w) + a[3]));
         }
+      }
+      turn_quad(v);
+      const int c1 = cq + 64 * b;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (16 * s + first + c >= n || c1 >= p.N) continue;
+        const int64_t at = (int64_t)rows[s][c] * p.N + c1;
+        if constexpr (BF) store16(reinterpret_cast<uint16_t *>(p.out) + at, v[c]);
+        else store16(reinterpret_cast<float *>(p.out) + at, v[c]);
       }
     }
   }
@@ -863,57 +906,60 @@ hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Slices of K, each a multiple of 64 and at least kSliceMin wide: up to 8 where there
-// are few tiles to fill the chip with, else up to 4 (32768 rows of rank 16, K = 2048,
-// product and join: 37.3 us with 8, 33.7 with 4, 38.4 with 1; 4099 rows of rank 64, K =
-// 2880: 17.3 with 4, 32.3 with 1). A narrow K, or few rows of a low rank with 16 waves
-// a workgroup, is one slice and needs no join (a backward of 168 rows of rank 16, 2784 x
-// 2744: 40 against 43 us a pass; of 979 rows of rank 8, 992 x 864: 36 against 40).
-static bool one_slice(int R, int K, int rank) { return K <= 512 || (rank <= 32 && R < 4096); }
+// Slices of K, each a multiple of 128 and at least kSliceMin wide. A slice more is
+// more workgroups, and more to join. us, product + join, for 1 / 2 / 4 / 8 slices:
+//   640 rows, rank 32, K 4096       19.6 / 16.3 / 12.7 / 11.6
+//   2048 rows, rank 64, K 4096      27.6 / 20.8 / 17.2 / 19.5
+//   4099 rows, rank 64, K 2880      22.5 / 20.1 / 23.3 / 24.4
+//   8192 rows, rank 16, K 2048      13.4 / 16.6 / 16.6 / 17.5
+//   12867 rows, rank 64, K 1568     19.6 / 26.9 / 33.2 / 40.6
+//   16384 rows, rank 64, K 4096     67.1 / 63.7 / 59.7 / 71.2   (more tiles than run at once)
+//   32768 rows, rank 64, K 2048     57.1 / 61.2 / 72.4 / 114
+//   32768 rows, rank 16, K 2048     44.1 / 42.0 / 40.3 / 43.3
+// Few rows of a low rank take one slice with 8 waves a workgroup, without a join,
+// while K is not too long for it (640 rows, rank 32, K 4096 17.0 us, 2048 rows, rank 16
+// 13.8): 1003 rows, rank 32, K 1440 10.3 us against 6.2 + 5.1 and a launch, a backward
+// of 168 rows, rank 16, 2784 x 2744 40 us against 43.
+static bool deep_slice(int R, int K, int rank) { return R < 4096 && rank <= 32 && K > 512 && K < 3000; }
 static int slice_width(int R, int K, int rank) {
-  if (one_slice(R, K, rank)) return (int)cdiv(K, 64) * 64;
-  const int w = (int)cdiv(cdiv(K, R < 4096 ? 8 : 4), 64) * 64;
+  const int most = R < 8192 ? 4 : R < 16384 ? 1 : rank <= 16 ? 4 : 2;
+  const int w = (int)cdiv(cdiv(K, K <= 512 || deep_slice(R, K, rank) ? 1 : most), 128) * 128;
   return w < kSliceMin ? kSliceMin : w;
 }
 int adapter_slices(int R, int K, int rank) { return (int)cdiv(K, slice_width(R, K, rank)); }
-size_t adapter_parts_elems(int R, int rank) { return (size_t)R * 32 * part_steps(rank); }
+size_t adapter_parts_elems(int tiles, int rank) { return (size_t)tiles * kAdTile * 32 * part_steps(rank); }
 
-template <int PACK, bool BF, int CB>
+template <int PACK, int S>
 static void expand_one(const LowRankArgs &a, hipStream_t s) {
-  const int blocks = (int)cdiv(a.N, 128 * CB);
-  hipLaunchKernelGGL((k_expand<PACK, BF, CB>), dim3((unsigned)(a.plan.max_tiles * blocks)), dim3(256), 0, s, a, blocks);
-}
-template <int PACK>
-static void expand_pack(const LowRankArgs &a, hipStream_t s) {
-  // Two blocks of 64 columns a wave, one after the other on the same low-rank values,
-  // for many rows; else one, and more workgroups. us, two against one: 32768 rows of
-  // rank 16, N = 2048 bf16 61.6 / 72.4, fp32 107.5 / 118.7; 16384 rows 33.0 / 37.6, fp32
-  // 58.5 / 58.9; 12867 rows of rank 64 52.6 / 51.4; 4099 rows, N = 2880 fp32 29.7 / 26.5.
-  const bool wide = a.R >= 16384;
-  if (a.bf16 && wide) expand_one<PACK, true, 2>(a, s);
-  else if (a.bf16) expand_one<PACK, true, 1>(a, s);
-  else if (wide) expand_one<PACK, false, 2>(a, s);
-  else expand_one<PACK, false, 1>(a, s);
+  const int blocks = (int)cdiv(a.N, 128 * S);
+  const dim3 grid((unsigned)(a.plan.max_tiles * blocks));
+  if (a.bf16) hipLaunchKernelGGL((k_expand<PACK, true, S>), grid, dim3(256), 0, s, a, blocks);
+  else hipLaunchKernelGGL((k_expand<PACK, false, S>), grid, dim3(256), 0, s, a, blocks);
 }
 
 hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
   const int slice = slice_width(a.R, a.K, a.rank), slices = adapter_slices(a.R, a.K, a.rank), pack = part_pack(a.rank);
   const dim3 grid((unsigned)(a.plan.max_tiles * slices)), block(256);
-  const bool deep = slices == 1 && a.K > 512;  // (rank at most 32)
-  if (a.rank <= 16 && deep) hipLaunchKernelGGL((k_shrink<1, 16>), grid, dim3(1024), 0, s, a, slices, slice);
-  else if (a.rank <= 32 && deep) hipLaunchKernelGGL((k_shrink<2, 16>), grid, dim3(1024), 0, s, a, slices, slice);
+  const bool deep = deep_slice(a.R, a.K, a.rank);
+  if (a.rank <= 16 && deep) hipLaunchKernelGGL((k_shrink<1, 8>), grid, dim3(512), 0, s, a, slices, slice);
   else if (a.rank <= 16) hipLaunchKernelGGL((k_shrink<1, 4>), grid, block, 0, s, a, slices, slice);
+  else if (a.rank <= 32 && deep) hipLaunchKernelGGL((k_shrink<2, 8>), grid, dim3(512), 0, s, a, slices, slice);
   else if (a.rank <= 32) hipLaunchKernelGGL((k_shrink<2, 4>), grid, block, 0, s, a, slices, slice);
   else if (a.rank <= 64) hipLaunchKernelGGL((k_shrink<4, 4>), grid, block, 0, s, a, slices, slice);
   else hipLaunchKernelGGL((k_shrink<8, 4>), grid, block, 0, s, a, slices, slice);
   if (slices > 1) {
-    const int64_t items = (int64_t)a.R * low_groups(a.rank);
-    hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices, a.L, a.ids);
+    const int64_t items = (int64_t)a.plan.max_tiles * kAdTile * low_groups(a.rank);
+    hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices);
   }
   if (!a.out) return hipGetLastError();
-  if (pack == 1) expand_pack<1>(a, s);
-  else if (pack == 2) expand_pack<2>(a, s);
-  else expand_pack<0>(a, s);
+  // Two blocks of 16 rows a wave for a high rank, whose weights are then read half as
+  // often, unless the workgroups get few. us, one block against two: rank 128, 8192
+  // rows, N = 4096 91.8 / 79.6; rank 64, 12867 rows, N = 2048 47.2 / 42.4, 2048 rows
+  // 12.0 / 11.8; rank 32, 8192 rows 17.9 / 18.9; rank 16, 32768 rows 52.2 / 53.9.
+  if (pack == 1) expand_one<1, 1>(a, s);
+  else if (pack == 2) expand_one<2, 1>(a, s);
+  else if (a.rank > 32 && a.R >= 4096) expand_one<0, 2>(a, s);
+  else expand_one<0, 1>(a, s);
   return hipGetLastError();
 }
 

@@ -114,7 +114,7 @@ AdapterCarve carve_adapter(void *ws, const nf4moe_adapters_t &a, int R, bool bac
   AdapterPlan lay;
   c.plan = b.take<char>(adapter_plan_layout(R, a.L, nullptr, &lay));
   c.slices = b.take<float>((size_t)adapter_slices(R, backward ? a.N : a.K, a.rank) * R * a.rank);
-  c.parts = b.take<uint16_t>(adapter_parts_elems(R, a.rank));
+  c.parts = b.take<uint16_t>(adapter_parts_elems(lay.max_tiles, a.rank));
   if (backward) {
     c.u = b.take<float>((size_t)R * a.rank);
     c.At = b.take<uint16_t>((size_t)a.L * a.K * a.rank);
@@ -324,7 +324,7 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
   hipError_t e = plan ? hipSuccess : launch_adapter_prepare({p, ids, R, ad->L, 0, 0, 0, nullptr, nullptr, nullptr, nullptr}, s);
   if (e != hipSuccess) return hip_status(e, "adapter plan launch");
-  return hip_status(launch_adapter_low_rank({p, ids, R, ad->L, x, x_row_of, x_rows, ad->A, ad->B, ad->scale, ad->K, ad->N, ad->rank,
+  return hip_status(launch_adapter_low_rank({p, R, x, x_row_of, x_rows, ad->A, ad->B, ad->scale, ad->K, ad->N, ad->rank,
                                              t, false, base, out, bf, c.slices, c.parts}, s), "adapter launch");
 }
 
@@ -367,7 +367,7 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
                               dx || dA ? c.Bt : nullptr}, s);
   if (e != hipSuccess) return hip_status(e, "adapter prepare launch");
   if (dx || dA) {
-    e = launch_adapter_low_rank({p, ids, R, ad->L, dy, nullptr, R, c.Bt, c.At, ad->scale, ad->N, ad->K, ad->rank,
+    e = launch_adapter_low_rank({p, R, dy, nullptr, R, c.Bt, c.At, ad->scale, ad->N, ad->K, ad->rank,
                                  dA ? c.u : nullptr, true, dx_base, dx, dx_dtype == NF4MOE_DT_BF16, c.slices,
                                  dx ? c.parts : nullptr}, s);
     if (e != hipSuccess) return hip_status(e, "adapter backward launch");

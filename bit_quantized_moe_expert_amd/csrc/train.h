@@ -103,8 +103,7 @@ hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s);
 // row; zeros for rows without an adapter. m: scale [L] or null. out null: low alone.
 struct LowRankArgs {
   AdapterPlan plan;
-  const int32_t *ids;
-  int R, L;
+  int R;
   const uint16_t *x;
   const int32_t *row_of;
   int x_rows;
@@ -117,10 +116,10 @@ struct LowRankArgs {
   void *out;
   bool bf16;           // base and out
   float *partial;      // scratch: [adapter_slices(R, K, rank)][R][rank]
-  uint16_t *parts;     // scratch: adapter_parts_elems(R, rank) (null without out)
+  uint16_t *parts;     // scratch: adapter_parts_elems(max_tiles, rank) (null without out)
 };
 int adapter_slices(int R, int K, int rank);
-size_t adapter_parts_elems(int R, int rank);
+size_t adapter_parts_elems(int tiles, int rank);
 hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s);
 
 // Per adapter l, out_l[j][c] (or [c][j], transposed) = m_l sum over the rows of l of
