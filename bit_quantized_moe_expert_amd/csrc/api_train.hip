@@ -17,6 +17,12 @@ bool dt_ok(int dt) { return dt == NF4MOE_DT_F32 || dt == NF4MOE_DT_BF16; }
 size_t dt_bytes(int dt) { return dt == NF4MOE_DT_BF16 ? 2 : 4; }
 bool ck_ok(int f) { return f == NF4MOE_CKPT_MXINT8 || f == NF4MOE_CKPT_MXFP8; }
 
+// Whether two arrays share a byte (absent ones share none).
+bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+  const uint64_t p = (uint64_t)a, q = (uint64_t)b;
+  return p && q && na && nb && p < q + nb && q < p + na;
+}
+
 nf4moe_status_t check_ckpt8(int32_t fmt, const void *dense, nf4moe_dtype_t dt, int64_t rows, int64_t K,
                             const void *codes, const void *scale) {
   if (!ck_ok(fmt)) return fail(NF4MOE_ERR_INVALID_ARG, "unknown checkpoint format %d", (int)fmt);
@@ -200,6 +206,9 @@ nf4moe_status_t nf4moe_block_norm_forward(const nf4moe_block_norm_t *norm, const
   if (!aligned(x, dt_bytes(n.x_dtype)) || !aligned(x_new, dt_bytes(n.x_dtype)) || !aligned(f, 2) || !aligned(y, 2) ||
       !aligned(rstd_post, 4) || !aligned(rstd_pre, 4))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  const uint64_t bytes = (uint64_t)T * n.H * dt_bytes(n.x_dtype);
+  if (f && ((x_new != x && overlap(x_new, bytes, x, bytes)) || overlap(x_new, bytes, f, (uint64_t)T * n.H * 2)))
+    return fail(NF4MOE_ERR_INVALID_ARG, "x_new overlaps an input (it may only be x itself)");
   NormArgs a = norm_args(n, T);
   a.x = x, a.f = f, a.x_new = x_new, a.y = y, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
   return hip_status(launch_norm_forward(a, (hipStream_t)stream), "norm launch");
@@ -278,12 +287,13 @@ size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, in
   return carve_adapter(nullptr, *ad, R, backward != 0).bytes;
 }
 
-// Rows, gather, ids and plan, as both directions take them; `cols` is the width of the
-// output (grids reach a workgroup per 64 rows and 128 columns).
+// Rows, gather, ids and plan, as both directions take them; `cols` is the width that
+// is written, dA's and dB's included. Grids reach a workgroup of 256 threads per 64
+// rows, or per adapter, and 128 columns; a dispatch holds less than 2^32 threads.
 static nf4moe_status_t check_adapter_rows(int32_t R, int32_t x_rows, const int32_t *x_row_of, const int32_t *ids,
-                                          const void *plan, size_t plan_bytes, int32_t L, int32_t cols) {
-  const int64_t tiles = cdiv(R, kAdTile) + (R < L + 1 ? R : L + 1), per = cdiv(cols, 128);
-  if (tiles * (per < 8 ? 8 : per) > 0x7fffffff)
+                                          const void *plan, size_t plan_bytes, int32_t L, int64_t cols, bool sums) {
+  const int64_t tiles = cdiv(R, kAdTile) + (R < L + 1 && !sums ? R : L + 1), per = cdiv(cols, 128) + 1;
+  if (tiles * (per < 8 ? 8 : per) >= 1 << 24)
     return fail(NF4MOE_ERR_UNSUPPORTED, "R=%d rows of %d columns are too many for one call", R, cols);
   if (x_rows < 1 || (!x_row_of && x_rows < R))
     return fail(NF4MOE_ERR_INVALID_ARG, "x_rows=%d too small for R=%d%s", x_rows, R, x_row_of ? "" : " without a gather");
@@ -305,20 +315,25 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   if (st != NF4MOE_OK) return st;
   if (!dt_ok(dtype)) return fail(NF4MOE_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
   if (R == 0) return NF4MOE_OK;
-  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, ad->N)) != NF4MOE_OK) return st;
+  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, ad->N, false)) != NF4MOE_OK) return st;
   if (!x || !out) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(x, 2) || !aligned(base, dt_bytes(dtype)) || !aligned(out, dt_bytes(dtype)) || !aligned(t, 16))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
   hipStream_t s = (hipStream_t)stream;
   const bool bf = dtype == NF4MOE_DT_BF16;
-  if (adapter_rows_supported(R, ad->K, ad->N, ad->rank)) {
+  const bool one_launch = adapter_rows_supported(R, ad->K, ad->N, ad->rank);
+  if (!one_launch) {
+    const size_t need = carve_adapter(nullptr, *ad, R, false).bytes;
+    if (!ws || ws_bytes < need) return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need);
+    if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
+  const uint64_t ob = (uint64_t)R * ad->N * dt_bytes(dtype);
+  if (overlap(out, ob, x, (uint64_t)x_rows * ad->K * 2) || (out != base && overlap(out, ob, base, ob)))
+    return fail(NF4MOE_ERR_INVALID_ARG, "out overlaps x or base (it may only be base itself)");
+  if (one_launch) {
     AdapterRowsArgs a = {x, x_row_of, ids, x_rows, R, ad->L, ad->K, ad->N, ad->rank, ad->A, ad->B, ad->scale, base, out, bf, t};
     return hip_status(launch_adapter_rows(a, s), "adapter launch");
   }
-  const AdapterCarve need = carve_adapter(nullptr, *ad, R, false);
-  if (!ws || ws_bytes < need.bytes)
-    return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need.bytes);
-  if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   const AdapterCarve c = carve_adapter(ws, *ad, R, false);
   AdapterPlan p;
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
@@ -348,7 +363,7 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
     if (e == hipSuccess && dB) e = launch_fill_f32_zero(dB, (int64_t)ad->L * ad->rank * ad->N, s);
     return hip_status(e, "fill launch");
   }
-  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, ad->K + ad->N)) != NF4MOE_OK) return st;
+  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, (int64_t)ad->K + ad->N, dA || dB)) != NF4MOE_OK) return st;
   if (!dy || (dA && (!x || (held && !x_scale))) || (dB && !t)) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(dy, 2) || !aligned(x, held ? 1 : 2) || !aligned(t, 16) || !aligned(dx_base, dt_bytes(dx_dtype)) ||
       !aligned(dx, dt_bytes(dx_dtype)))
@@ -357,6 +372,10 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
   if (!ws || ws_bytes < need.bytes)
     return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need.bytes);
   if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const uint64_t xb = (uint64_t)R * ad->K * dt_bytes(dx_dtype);
+  if (overlap(dx, xb, dy, (uint64_t)R * ad->N * 2) || (dx != dx_base && overlap(dx, xb, dx_base, xb)) ||
+      (dA && overlap(dx, xb, x, (uint64_t)x_rows * ad->K * (held ? 1 : 2))))
+    return fail(NF4MOE_ERR_INVALID_ARG, "dx overlaps dy, x or dx_base (it may only be dx_base itself)");
   if (!dx && !dA && !dB) return NF4MOE_OK;
   const AdapterCarve c = carve_adapter(ws, *ad, R, true);
   AdapterPlan p;

@@ -29,15 +29,6 @@ __device__ inline void store16(void *p, uint4 v) {
   u32x4_any u = {v.x, v.y, v.z, v.w};
   *reinterpret_cast<u32x4_any *>(p) = u;
 }
-// A store that is not read again soon: it leaves the caches to the reads.
-__device__ inline void store16_stream(void *p, uint4 v) {
-  u32x4_any u = {v.x, v.y, v.z, v.w};
-  __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any *>(p));
-}
-__device__ inline uint4 load16_stream(const void *p) {
-  const u32x4_any v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
 __device__ inline uint2 load8(const void *p) {
   const u32x2_any v = *reinterpret_cast<const u32x2_any *>(p);
   return make_uint2(v.x, v.y);

@@ -239,10 +239,33 @@ static void glu_forward_f(const GluArgs &a, dim3 grid, hipStream_t s) {
   else hipLaunchKernelGGL((k_glu_forward<BF, CK_MXFP8>), grid, dim3(256), 0, s, a);
 }
 
+// Calls of many rows go in pieces of whole rows, for the same reason.
+static int64_t glu_rows(int I) {
+  const int64_t rows = kPiece8 / (I / 8), most = int64_t(1) << 22;
+  return rows < most ? rows : most;
+}
+static GluArgs glu_piece(const GluArgs &a, int64_t r0) {
+  GluArgs p = a;
+  const int64_t n = r0 * a.I, n2 = 2 * n, left = a.R - r0, most = glu_rows(a.I);
+  p.R = left < most ? left : most;
+  p.gu = (const char *)a.gu + n2 * (a.src == SRC_F32 ? 4 : a.src == SRC_BF16 ? 2 : 1);
+  if (a.gu_scale) p.gu_scale = a.gu_scale + n2 / 32;
+  if (a.codes) p.codes = a.codes + n2, p.scale = a.scale + n2 / 32;
+  if (a.h) p.h = a.h + n;
+  if (a.dh) p.dh = (const char *)a.dh + n * (a.dh_bf16 ? 2 : 4);
+  if (a.row_w) p.row_w = a.row_w + r0;
+  if (a.dgu) p.dgu = a.dgu + n2;
+  if (a.drow) p.drow = a.drow + r0;
+  return p;
+}
+
 hipError_t launch_glu_forward(const GluArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)cdiv(a.R * (a.I / 8), 256));
-  if (a.src == SRC_BF16) glu_forward_f<true>(a, grid, s);
-  else glu_forward_f<false>(a, grid, s);
+  for (int64_t r0 = 0; r0 < a.R; r0 += glu_rows(a.I)) {
+    const GluArgs p = glu_piece(a, r0);
+    const dim3 grid((unsigned)cdiv(p.R * (p.I / 8), 256));
+    if (p.src == SRC_BF16) glu_forward_f<true>(p, grid, s);
+    else glu_forward_f<false>(p, grid, s);
+  }
   return hipGetLastError();
 }
 
@@ -262,10 +285,13 @@ hipError_t launch_glu_backward(const GluArgs &a, hipStream_t s) {
   // wave a row against four: I = 2880, 8192 rows 43.7 / 38.6, 64 rows 7.4 / 4.3; I = 1024,
   // 256 rows 4.2 / 3.6, 2048 rows 7.2 / 8.0; I = 768, 16384 rows 23.1 / 27.1.
   const bool wide = a.I > 1536 || a.R <= 512;
-  if (wide && a.dh_bf16) glu_backward_d<true, 4>(a, s);
-  else if (wide) glu_backward_d<false, 4>(a, s);
-  else if (a.dh_bf16) glu_backward_d<true, 1>(a, s);
-  else glu_backward_d<false, 1>(a, s);
+  for (int64_t r0 = 0; r0 < a.R; r0 += glu_rows(a.I)) {
+    const GluArgs p = glu_piece(a, r0);
+    if (wide && p.dh_bf16) glu_backward_d<true, 4>(p, s);
+    else if (wide) glu_backward_d<false, 4>(p, s);
+    else if (p.dh_bf16) glu_backward_d<true, 1>(p, s);
+    else glu_backward_d<false, 1>(p, s);
+  }
   return hipGetLastError();
 }
 

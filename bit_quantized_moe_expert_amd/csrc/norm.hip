@@ -25,7 +25,6 @@ namespace nf4moe {
 
 namespace {
 
-
 // Elements i .. i + 7 of a row of H, zeros past the end.
 template <bool BF>
 __device__ inline void load_row8(const void *p, int64_t base, int i, int H, float (&v)[8]) {
@@ -153,8 +152,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
   __shared__ float red[2][THREADS / 64];
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-  // Rows past the end (TPR = 64 only: no barriers there) leave; else ROWS = 1 or
-  // all threads of the workgroup stay for the barriers.
+  // Rows past the end (TPR = 64) read row 0 and store nothing.
   const bool live = row < p.T;
   const int64_t base = (live ? row : 0) * p.H;
   const int H = p.H;
@@ -499,8 +497,23 @@ int norm_backward_groups(int64_t T, int H) {
   return (int)(need < most ? need : most);
 }
 
+// Many rows go in pieces, each well inside a dispatch's 2^32 threads.
 hipError_t launch_norm_forward(const NormArgs &a, hipStream_t s) {
-  return a.x_bf16 ? norm_forward_t<true>(a, s) : norm_forward_t<false>(a, s);
+  constexpr int64_t kPiece = 1 << 21;
+  for (int64_t r0 = 0; r0 < a.T; r0 += kPiece) {
+    NormArgs p = a;
+    const int64_t n = r0 * a.H, xb = a.x_bf16 ? 2 : 4, gb = a.gate_bf16 ? 2 : 4;
+    p.T = a.T - r0 < kPiece ? a.T - r0 : kPiece;
+    p.x = (const char *)a.x + n * xb;
+    if (a.f) p.f = a.f + n, p.x_new = (char *)a.x_new + n * xb;
+    if (a.y) p.y = a.y + n;
+    if (a.gate_kind >= 2) p.gate = (const char *)a.gate + (a.gate_kind == 3 ? n : r0) * gb;
+    if (a.rstd_post) p.rstd_post = a.rstd_post + r0;
+    if (a.rstd_pre) p.rstd_pre = a.rstd_pre + r0;
+    const hipError_t e = a.x_bf16 ? norm_forward_t<true>(p, s) : norm_forward_t<false>(p, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_norm_backward(const NormArgs &a, hipStream_t s) {

@@ -156,7 +156,7 @@ def glu_forward(gu, glu: int = 0, alpha: float = 0.0, limit: float = 0.0, interl
     (CKPT_MXINT8 or CKPT_MXFP8) the same pass saves gu in 8 bits: (h, Ckpt8).
     glu, alpha, limit, interleaved as in MoELayer."""
     R, cols = _dims(gu, "gu", 2)
-    dt, I, i = _dt(gu, "gu"), _glu_width(cols), gu.get_device()
+    dt, I, i = _dt(gu, "gu"), _i32(_glu_width(cols), "I"), gu.get_device()
     if ckpt not in (None, CKPT_MXINT8, CKPT_MXFP8):
         raise ValueError(f"unknown checkpoint format {ckpt}")
     gp = _arg(gu, "gu", gu.shape, gu.dtype, i)
@@ -177,7 +177,7 @@ def glu_backward(dh, gu, glu: int = 0, alpha: float = 0.0, limit: float = 0.0, i
     [R, 2I]; h bf16 [R, I] recomputed (need_h); drow_w fp32 [R] (with row_w)."""
     R, I = _dims(dh, "dh", 2)
     ddt, i = _dt(dh, "dh"), dh.get_device()
-    _glu_width(2 * I)
+    _glu_width(2 * _i32(I, "I"))
     if isinstance(gu, Ckpt8):
         gp, sp = gu.args("gu", (R, 2 * I), i)
         src = _SRC[gu.fmt]
@@ -303,6 +303,7 @@ def adapter_plan(ids, num_adapters: int) -> AdapterPlan:
     """Group the rows of ids int32 [R] by adapter once, for several calls on the same
     batch (adapter_forward and adapter_backward otherwise do it in each call)."""
     (R,), i = _dims(ids, "ids", 1), ids.get_device()
+    _i32(R, "rows"), _i32(num_adapters, "num_adapters")
     ip = _arg(ids, "ids", (R,), _I32, i)
     L = M.lib()
     ws, wsp, nb = _scratch(ids, L.nf4moe_adapter_plan_bytes(R, num_adapters))
@@ -313,6 +314,7 @@ def adapter_plan(ids, num_adapters: int) -> AdapterPlan:
 def _adapter_struct(A, B, ids, scale, plan, x_row_of, i):
     """The descriptor, (R, K, N, rank, L), and the addresses of ids, the gather, the plan and its size."""
     (L, rank, K), (R,), N = _dims(A, "A", 3), _dims(ids, "ids", 1), _dims(B, "B", 3)[1]
+    _i32(R, "rows")
     st = _ADAPTERS.pack(_i32(L, "L"), _i32(rank, "rank"), _i32(K, "K"), _i32(N, "N"), _arg(A, "A", A.shape, _BF16, i),
                         _arg(B, "B", (L, N, rank), _BF16, i), _arg(scale, "scale", (L,), _F32, i) or 0)
     rows = (_arg(x_row_of, "x_row_of", (R,), _I32, i), _arg(ids, "ids", (R,), _I32, i))
@@ -326,6 +328,7 @@ def _adapter_struct(A, B, ids, scale, plan, x_row_of, i):
 
 
 def _gathered(x_row_of, R, rows):
+    _i32(rows, "rows of x")
     if x_row_of is None and rows != R:
         raise ValueError(f"x has {rows} rows, expected {R} (or an x_row_of gather)")
 

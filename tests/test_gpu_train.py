@@ -337,3 +337,28 @@ def test_rows_behind_the_last_are_left_alone():
     assert (h[Rn:] == 7.0).all() and (codes[Rn:] == 0xAB).all() and (scale[Rn:] == 0xAB).all()
     assert (q[Rn:] == 0xAB).all() and (qs[Rn:] == 0xAB).all()
     assert not (h[:Rn] == 7.0).all()
+
+
+def test_rows_past_one_launch():
+    """More rows than one launch takes: every piece's rows, and nothing between them, against the same rows alone."""
+    T, H, I = (1 << 22) + 5, 8, 32
+    g = torch.Generator(device=DEV).manual_seed(4)
+    rn = lambda *s, dt=torch.bfloat16: torch.randn(*s, generator=g, device=DEV).to(dt)  # noqa: E731
+    cuts = [(0, 4), ((1 << 21) - 3, (1 << 21) + 3), ((1 << 22) - 3, T)]
+    x, f, gate = rn(T, H), rn(T, H), rn(T, 1, dt=torch.float32)
+    w = dict(w_post=rn(H, dt=torch.float32), w_pre=rn(H, dt=torch.float32), gate_fn=M.GATE_TANH)
+    for gt in (gate, rn(T, H)):
+        a = M.block_norm_forward(x, f, gate=gt, **w)
+        for lo, hi in cuts:
+            b = M.block_norm_forward(x[lo:hi].clone(), f[lo:hi].clone(), gate=gt[lo:hi].clone(), **w)
+            assert all(torch.equal(a[k][lo:hi], b[k]) for k in a), (lo, hi)
+    del x, f, gate, gt, a, b
+    gu, dh, rw = rn(T, 2 * I), rn(T, I), rn(T, dt=torch.float32)
+    h, ck = M.glu_forward(gu, ckpt=M.CKPT_MXFP8)
+    a = M.glu_backward(dh, ck, row_w=rw)
+    for lo, hi in cuts:
+        b, c = M.glu_forward(gu[lo:hi].clone(), ckpt=M.CKPT_MXFP8)
+        assert torch.equal(b, h[lo:hi]) and torch.equal(c.codes, ck.codes[lo:hi]) and torch.equal(c.scale, ck.scale[lo:hi])
+        d = M.glu_backward(dh[lo:hi].clone(), c, row_w=rw[lo:hi].clone())
+        # drow_w: one wave a row against four for so few; 32 columns lie in one wave either way, the rest adds zeros
+        assert all(torch.equal(a[k][lo:hi], d[k]) for k in a), (lo, hi)

@@ -267,6 +267,70 @@ def test_adapter_validation():
     assert bwd(R=0, dA=None, dB=None) == OK
 
 
+@pytest.mark.parametrize("n", [4, 200000])          # the one-launch form and the grouped kernels
+def test_adapter_refuses_overlapping_outputs(n):
+    """An output over an input that other rows still read; the exceptions are base and dx_base themselves."""
+    from bit_quantized_moe_expert_amd import train
+    K = N = 64
+    desc = train._ADAPTERS.pack(4, 16, K, N, FAKE, FAKE, 0)
+    big, far, bytes_ = 1 << 40, 1 << 41, n * N * 2
+    wf, wb = L.nf4moe_adapter_workspace_bytes(desc, n, 0), L.nf4moe_adapter_workspace_bytes(desc, n, 1)
+
+    def fwd(x, base, out):
+        return L.nf4moe_adapter_forward(desc, x, n, None, FAKE, None, 0, n, base, out, 1, None, FAKE, wf, None)
+
+    def bwd(dy, x, dxb, dx):
+        return L.nf4moe_adapter_backward(desc, dy, 1, x, None, n, None, FAKE, FAKE, None, 0, n, dxb, dx, 1, FAKE, FAKE, FAKE, wb,
+                                         None)
+    for d in (0, 2, bytes_ - 2, 2 - bytes_):
+        assert fwd(big, None, big + d) == INVALID and fwd(big, big, big) == INVALID
+        assert bwd(big, far, None, big + d) == INVALID and bwd(far, big, None, big + d) == INVALID
+        if d:
+            assert fwd(far, big, big + d) == INVALID and bwd(far, 1 << 42, big, big + d) == INVALID
+    assert "overlaps" in L.nf4moe_last_error().decode()
+
+
+def test_block_norm_refuses_overlapping_outputs():
+    big, far = 1 << 40, 1 << 41
+    st, a = _norm()
+    fw = lambda x, f, out: L.nf4moe_block_norm_forward(a, x, f, 4, out, FAKE, FAKE, FAKE, None)  # noqa: E731
+    for d in (2, 4 * 64 * 2 - 2, 2 - 4 * 64 * 2):
+        assert fw(big, far, big + d) == INVALID and fw(far, big, big + d) == INVALID
+    assert fw(far, big, big) == INVALID
+
+
+def test_adapter_refuses_more_than_a_dispatch():
+    """Grids past 2^32 threads are refused before anything runs."""
+    from bit_quantized_moe_expert_amd import train
+    n = 1 << 30
+    desc = train._ADAPTERS.pack(4, 16, 64, 1 << 14, FAKE, FAKE, 0)
+    assert L.nf4moe_adapter_forward(desc, FAKE, n, None, FAKE, None, 0, n, None, FAKE, 1, None, FAKE, 0, None) == UNSUPPORTED
+    wide = train._ADAPTERS.pack(4096, 8, 1 << 18, 1 << 18, FAKE, FAKE, 0)     # dA and dB of many adapters, one row
+    assert L.nf4moe_adapter_backward(wide, FAKE, 1, FAKE, None, 1, None, FAKE, FAKE, None, 0, 1, None, None, 1, FAKE, FAKE, FAKE, 0,
+                                     None) == UNSUPPORTED
+    assert L.nf4moe_adapter_backward(wide, FAKE, 1, FAKE, None, 1, None, FAKE, FAKE, None, 0, 1, None, FAKE, 1, None, None, FAKE, 0,
+                                     None) == WORKSPACE
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """Row counts that a 32-bit argument cannot hold are refused, not cut."""
+    meta = dict(device="meta")
+    A, B = torch.empty(2, 8, 64, dtype=torch.bfloat16, **meta), torch.empty(2, 64, 8, dtype=torch.bfloat16, **meta)
+    rows = (1 << 32) + 4
+    x, ids = torch.empty(rows, 64, dtype=torch.bfloat16, **meta), torch.empty(rows, dtype=torch.int32, **meta)
+    few = torch.empty(4, dtype=torch.int32, **meta)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkg.adapter_forward(x, A, B, ids)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkg.adapter_forward(x, A, B, few, x_row_of=few)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkg.adapter_plan(ids, 2)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkg.adapter_plan(few, rows)
+    with pytest.raises(ValueError, match="32 bits"):
+        pkg.glu_forward(torch.empty(2, 1 << 33, dtype=torch.bfloat16, **meta))
+
+
 # ------------------------------------------------------------------ refusals of the binding
 def test_binding_refuses_before_the_device():
     M = pkg
