@@ -153,10 +153,16 @@ __device__ inline int4 block_prefix4(int4 v, int4 *wsum, int4 *sum) {
 // that bin begin (all counters of the earlier workgroups and bins), then places
 // its rows in order, 1024 at a time: ranks inside a wave by ballots, then the
 // waves' counts of each bin in wave order, so the order is stable. Workgroup 0 also
-// writes the tile and chunk tables.
+// writes the chunk table; all share the tile table. Bound by the latency of a chain of
+// barriers, 6 to 10 us up to 32768 rows of 64 adapters, not by bytes.
+//
+// The counters come from k_prepare, or every workgroup counts all rows itself where
+// that spares the launch. us, two launches against one: 4099 rows of 6 adapters 2.4 +
+// 5.9 / 7.8, 8192 of 64 2.4 + 10.2 / 12.7, 16384 of 64 2.1 + 10.3 / 15.9.
+constexpr int kSelfCount = 8192;
 constexpr int kWaveBins = 1024;  // up to so many bins the waves' counts have a place each in LDS
 __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__restrict__ ids, int R, int L, int per,
-                                                               int groups, int chunk_rows, AdapterPlan p) {
+                                                               int groups, bool self_count, int chunk_rows, AdapterPlan p) {
   constexpr int W = kPlanThreads / 64;
   __shared__ int32_t next[kMaxAdapters + 1], tot[kMaxAdapters + 1];
   __shared__ union {
@@ -171,9 +177,31 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
   int b = r0 + tid < r1 ? bin_of(ids[r0 + tid], L) : -1;
   for (int i = tid; i < nb; i += kPlanThreads) next[i] = tot[i] = 0;
   __syncthreads();
-  if (groups == 1) {
-    if (b >= 0) atomicAdd(&tot[b], 1);
-    for (int r = r0 + kPlanThreads + tid; r < r1; r += kPlanThreads) atomicAdd(&tot[bin_of(ids[r], L)], 1);
+  if (self_count) {
+    // a wave's rows of its first lane's bin as one addition: neighbours often share one
+    auto count = [&](int bin, int32_t *cnt) {
+      const int lead = __builtin_amdgcn_readfirstlane(bin);
+      const uint64_t same = __ballot(bin == lead);
+      if (bin != lead) {
+        if (bin >= 0) atomicAdd(&cnt[bin], 1);
+      } else if (lead >= 0 && (threadIdx.x & 63) == (unsigned)__builtin_ctzll(same)) {
+        atomicAdd(&cnt[lead], __popcll(same));
+      }
+    };
+    for (int base = 0; base < R; base += 4 * kPlanThreads) {
+      int bin[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = base + k * kPlanThreads + tid;
+        bin[k] = r < R ? bin_of(ids[r], L) : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = base + k * kPlanThreads;  // `per` is a multiple of kPlanThreads: all of these rows are before r0, or none
+        if (at < R) count(bin[k], tot);
+        if (at < r0) count(bin[k], next);
+      }
+    }
   } else {
     for (int i = tid; i < nb * groups; i += kPlanThreads) {
       const int32_t c = p.hist[i];
@@ -354,9 +382,11 @@ __host__ __device__ inline int low_groups(int rank) { return part_pack(rank) ? r
 // of all adapters then stay in that XCD's L2 (4 slices: a pair of XCDs a slice). Few
 // rows still make many workgroups.
 // Inside, the W waves take every W-th 128-wide step of the slice for all the tile's
-// rows, so each adapter row is read once per workgroup. Four waves, for many rows:
-// eight take 31.4 against 27.1 us for 32768 gathered rows of rank 16, 89.7 / 57.1 of 64. A quad reads 64 bytes of one
-// row, the four quads of a row 256.
+// rows, so each adapter row is read once per workgroup. A quad reads 64 bytes of one
+// row, the four quads of a row 256. Four waves where there are many rows: eight take
+// 31.4 us against 27.1 for 32768 gathered rows of rank 16, 89.7 against 57.1 of rank 64.
+// Bound by the loads of x: 32768 contiguous rows of 2048 (134 MB) take 32 us, 4.2 TB/s,
+// a plain read of them 24; 4096 rows gathered 8 times each 21.4 us, 6.3 TB/s out of L2.
 constexpr int kSliceMin = 256;  // no slice is narrower
 
 template <int RT, int NS, int W>
@@ -644,7 +674,10 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
 // 128 columns, its four waves taking every fourth step of 32 rows; their sums are
 // added in order through LDS, from which they leave in either layout. An adapter
 // with one chunk (of no rows: zeros) is written straight out; the chunks of others go
-// to partial sums that k_rowgrad_join adds in order. dA and dB run in one launch.
+// to partial sums that k_rowgrad_join adds in order. dA and dB run in one launch: dB
+// waits for dy while dA, from an 8-bit x that the caches hold, decodes and turns; apart,
+// one after the other, they take 64 us instead of 55 (32768 rows of rank 16, 2048 x
+// 2048, dy 134 MB read once; twice the 24 us of a plain read, vector instructions 20).
 constexpr int kGradCols = 128;
 
 template <int SRC, int RT>
@@ -796,7 +829,9 @@ __global__ __launch_bounds__(256) void k_zero_f32(float *p, int64_t n) {
 // One launch, no plan: a workgroup per row and share of the columns. Its W waves
 // take the ranks in turn (a dot product over K each, two at a time), then every
 // thread its columns. The workgroups of a row repeat its first product: A_l comes
-// from L2 after the first, and a second launch would cost more.
+// from L2 after the first, and a second launch would cost more. Bound by the latency of
+// the two dependent products: 64 rows of rank 16 on 2048 x 2048 take 4 us, and a call
+// 11, most of it the host's.
 template <bool BF, int W>
 __global__ __launch_bounds__(64 * W) void k_adapter_rows(AdapterRowsArgs p, int csplit) {
   __shared__ float ts[kMaxRank];
@@ -892,17 +927,19 @@ size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p) {
 
 hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
   const int per = plan_rows(a.R, a.L);
-  const int groups = a.ids ? (int)cdiv(a.R, per) : 0, hists = groups > 1 ? groups : 0;
+  const int groups = a.ids ? (int)cdiv(a.R, per) : 0;
   const TurnArgs t0 = {a.B, a.Bt, a.N, a.rank, false}, t1 = {a.A, a.At, a.rank, a.K, true};
   const int b0 = a.Bt ? (int)cdiv((int64_t)a.N * a.rank / 64, kPrepareThreads) : 0;
   const int b1 = a.At ? (int)cdiv((int64_t)a.K * a.rank / 64, kPrepareThreads) : 0;
+  // a launch for the counters alone is spared for few rows
+  const int hists = groups > 1 && (a.R > kSelfCount || b0 + b1 > 0) ? groups : 0;
   const unsigned grid = (unsigned)(hists + a.L * (b0 + b1));
   if (grid > 0)
     hipLaunchKernelGGL(k_prepare, dim3(grid), dim3(kPrepareThreads), hists ? sizeof(int32_t) * (a.L + 1) : 0, s, a.ids, a.R, a.L,
                        per, hists, a.plan.hist, t0, t1, b0, b1);
   if (groups > 0)
     hipLaunchKernelGGL(k_plan_scatter, dim3(groups), dim3(kPlanThreads), 0, s, a.ids, a.R, a.L, per, groups,
-                       adapter_chunk_rows(a.R), a.plan);
+                       hists == 0, adapter_chunk_rows(a.R), a.plan);
   return hipGetLastError();
 }
 
@@ -997,9 +1034,9 @@ static int rows_csplit(int R, int N) {
 }
 
 // Where the one-launch form runs: while at most 1 MB of A and B passes through one
-// CU. Both forms, a pass in us on K = N = 2048: rank 16, 1024 / 2048 rows 13 / 22
-// against 24 / 30 for the grouped kernels; rank 64, 256 / 512 rows 20 / 29 against 24
-// / 25; and 2360 x 584, rank 128: 128 / 512 rows 29 / 35 against 30 / 34.
+// CU. Both forms, a pass in us on K = N = 2048: rank 16, 1024 / 2048 rows 14 / 23
+// against 23 / 27 for the grouped kernels; rank 64, 256 / 512 rows 21 / 29 against 25
+// / 27; and 2880 x 2880, rank 32: 256 / 1024 rows 17 / 29 against 22 / 27.
 bool adapter_rows_supported(int R, int K, int N, int rank) {
   const int cs = rows_csplit(R, N);
   const int64_t bytes = cdiv((int64_t)R * cs, 256) * 2 * rank * ((int64_t)K + cdiv(N, cs));  // of A and B through one CU

@@ -2,7 +2,8 @@
 // that writes and reads them.
 //
 // All of it is bound by memory traffic: every element is read once, worked on in
-// registers and written once, 8 elements a thread (16-byte accesses of bf16).
+// registers and written once, 8 elements a thread (16-byte accesses of bf16), at the
+// rate of a plain copy or better: see each kernel.
 #include "ckpt8.h"
 #include "internal.h"
 #include "train.h"
