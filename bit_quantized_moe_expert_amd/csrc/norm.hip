@@ -11,8 +11,9 @@
 //   df = rstd_f (dz w_post - n_f mean(dz w_post n_f));  dw_post = sum_t dz n_f
 // Everything is fp32 in registers between the loads and the stores; each output
 // is rounded once. Both directions are bound by memory traffic: the forward of 8190 x
-// 2880 (fp32 stream) runs at 5.2 TB/s, the backward of 8192 x 2048 bf16 at 4.2 TB/s
-// with its column sums (latency of a row's two dependent sums).
+// 2880 (fp32 stream, 283 MB) takes 53.5 us, 5.3 TB/s, the backward of 8192 x 2048 bf16
+// (201 MB) 43.4 us and 5.0 for the joined column sums, 4.2 TB/s: a row's two sums wait
+// for each other.
 //
 // A row is held by TPR threads, 8 NC values each, so its reductions are a wave
 // sum (TPR = 64) or wave sums joined through LDS. Rows of any width: the last
