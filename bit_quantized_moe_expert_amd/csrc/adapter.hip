@@ -676,8 +676,9 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
 // with one chunk (of no rows: zeros) is written straight out; the chunks of others go
 // to partial sums that k_rowgrad_join adds in order. dA and dB run in one launch: dB
 // waits for dy while dA, from an 8-bit x that the caches hold, decodes and turns; apart,
-// one after the other, they take 64 us instead of 55 (32768 rows of rank 16, 2048 x
-// 2048, dy 134 MB read once; twice the 24 us of a plain read, vector instructions 20).
+// one after the other, they take 64 us instead of 56 (32768 rows of rank 16, 2048 x
+// 2048, dy 134 MB read once; vector instructions 20 us). Run right after the product
+// that reads dy too, before the expansion: 49 us, the caches still hold a part of dy.
 constexpr int kGradCols = 128;
 
 template <int SRC, int RT>
@@ -974,8 +975,8 @@ static void expand_one(const LowRankArgs &a, hipStream_t s) {
   else hipLaunchKernelGGL((k_expand<PACK, false, S>), grid, dim3(256), 0, s, a, blocks);
 }
 
-hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
-  const int slice = slice_width(a.R, a.K, a.rank), slices = adapter_slices(a.R, a.K, a.rank), pack = part_pack(a.rank);
+hipError_t launch_adapter_shrink(const LowRankArgs &a, hipStream_t s) {
+  const int slice = slice_width(a.R, a.K, a.rank), slices = adapter_slices(a.R, a.K, a.rank);
   const dim3 grid((unsigned)(a.plan.max_tiles * slices)), block(256);
   const bool deep = deep_slice(a.R, a.K, a.rank);
   if (a.rank <= 16 && deep) hipLaunchKernelGGL((k_shrink<1, 8>), grid, dim3(512), 0, s, a, slices, slice);
@@ -988,7 +989,11 @@ hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s) {
     const int64_t items = (int64_t)a.plan.max_tiles * kAdTile * low_groups(a.rank);
     hipLaunchKernelGGL(k_shrink_join, dim3((unsigned)cdiv(items, 256)), block, 0, s, a, slices);
   }
-  if (!a.out) return hipGetLastError();
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_expand(const LowRankArgs &a, hipStream_t s) {
+  const int pack = part_pack(a.rank);
   // Two blocks of 16 rows a wave for a high rank, whose weights are then read half as
   // often, unless the workgroups get few. us, one block against two: rank 128, 8192
   // rows, N = 4096 91.8 / 79.6; rank 64, 12867 rows, N = 2048 47.2 / 42.4, 2048 rows

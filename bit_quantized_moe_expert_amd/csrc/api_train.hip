@@ -339,8 +339,10 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);
   hipError_t e = plan ? hipSuccess : launch_adapter_prepare({p, ids, R, ad->L, 0, 0, 0, nullptr, nullptr, nullptr, nullptr}, s);
   if (e != hipSuccess) return hip_status(e, "adapter plan launch");
-  return hip_status(launch_adapter_low_rank({p, R, x, x_row_of, x_rows, ad->A, ad->B, ad->scale, ad->K, ad->N, ad->rank,
-                                             t, false, base, out, bf, c.slices, c.parts}, s), "adapter launch");
+  const LowRankArgs a = {p, R, x, x_row_of, x_rows, ad->A, ad->B, ad->scale, ad->K, ad->N, ad->rank,
+                         t, false, base, out, bf, c.slices, c.parts};
+  e = launch_adapter_shrink(a, s);
+  return hip_status(e != hipSuccess ? e : launch_adapter_expand(a, s), "adapter launch");
 }
 
 nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint16_t *dy, nf4moe_src_t x_src, const void *x,
@@ -385,10 +387,10 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
   e = launch_adapter_prepare({p, plan ? nullptr : ids, R, ad->L, ad->K, ad->N, ad->rank, ad->A, ad->B, dx ? c.At : nullptr,
                               dx || dA ? c.Bt : nullptr}, s);
   if (e != hipSuccess) return hip_status(e, "adapter prepare launch");
+  const LowRankArgs a = {p, R, dy, nullptr, R, c.Bt, c.At, ad->scale, ad->N, ad->K, ad->rank, dA ? c.u : nullptr, true,
+                         dx_base, dx, dx_dtype == NF4MOE_DT_BF16, c.slices, dx ? c.parts : nullptr};
   if (dx || dA) {
-    e = launch_adapter_low_rank({p, R, dy, nullptr, R, c.Bt, c.At, ad->scale, ad->N, ad->K, ad->rank,
-                                 dA ? c.u : nullptr, true, dx_base, dx, dx_dtype == NF4MOE_DT_BF16, c.slices,
-                                 dx ? c.parts : nullptr}, s);
+    e = launch_adapter_shrink(a, s);
     if (e != hipSuccess) return hip_status(e, "adapter backward launch");
   }
   if (dA || dB) {
@@ -398,7 +400,8 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
     e = launch_adapter_rowgrad(g, s);
     if (e != hipSuccess) return hip_status(e, "adapter weight gradient launch");
   }
-  return NF4MOE_OK;
+  // after dB, which finds dy (up to the last-level cache's size) where u's product left it
+  return dx ? hip_status(launch_adapter_expand(a, s), "adapter backward launch") : NF4MOE_OK;
 }
 
 }  // extern "C"

@@ -100,7 +100,8 @@ hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s);
 // v[row][j] = sum_k x[row'][k] W1_l[j][k] for the rows of adapter l (W1 [L, rank, K]
 // bf16), row' by row_of, and out[row][c] = base[row][c] + sum_j (m_l v[row][j])
 // W2_l[c][j] (W2 [L, N, rank] bf16). low (optional): v, or m_l v with low_scaled, by
-// row; zeros for rows without an adapter. m: scale [L] or null. out null: low alone.
+// row; zeros for rows without an adapter. m: scale [L] or null. The first launch makes
+// v, the second out of it (out null: low alone, no second launch).
 struct LowRankArgs {
   AdapterPlan plan;
   int R;
@@ -120,7 +121,8 @@ struct LowRankArgs {
 };
 int adapter_slices(int R, int K, int rank);
 size_t adapter_parts_elems(int tiles, int rank);
-hipError_t launch_adapter_low_rank(const LowRankArgs &a, hipStream_t s);
+hipError_t launch_adapter_shrink(const LowRankArgs &a, hipStream_t s);
+hipError_t launch_adapter_expand(const LowRankArgs &a, hipStream_t s);
 
 // Per adapter l, out_l[j][c] (or [c][j], transposed) = m_l sum over the rows of l of
 // p[row][j] v[row'][c]; a: v by src, b: v bf16. Each where out is given.
