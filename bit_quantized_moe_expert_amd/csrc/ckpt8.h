@@ -29,6 +29,15 @@ __device__ inline void store16(void *p, uint4 v) {
   u32x4_any u = {v.x, v.y, v.z, v.w};
   *reinterpret_cast<u32x4_any *>(p) = u;
 }
+// ... past the caches, for long arrays that are read or written once.
+__device__ inline void store16_nt(void *p, uint4 v) {
+  u32x4_any u = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any *>(p));
+}
+__device__ inline uint4 load16_nt(const void *p) {
+  const u32x4_any v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
 __device__ inline uint2 load8(const void *p) {
   const u32x2_any v = *reinterpret_cast<const u32x2_any *>(p);
   return make_uint2(v.x, v.y);
@@ -52,13 +61,14 @@ __device__ inline uint4 pack_bf16x8(const float (&v)[8]) {
 }
 
 // Eight consecutive elements at index i of a bf16 (BF = true) or fp32 array.
-template <bool BF>
+template <bool BF, bool NT = false>
 __device__ inline void load_elems8(const void *p, int64_t i, float (&v)[8]) {
   if constexpr (BF) {
-    unpack_bf16x8(load16(reinterpret_cast<const uint16_t *>(p) + i), v);
+    const uint16_t *h = reinterpret_cast<const uint16_t *>(p) + i;
+    unpack_bf16x8(NT ? load16_nt(h) : load16(h), v);
   } else {
     const float *f = reinterpret_cast<const float *>(p) + i;
-    const uint4 a = load16(f), b = load16(f + 4);
+    const uint4 a = NT ? load16_nt(f) : load16(f), b = NT ? load16_nt(f + 4) : load16(f + 4);
     v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
     v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
   }
