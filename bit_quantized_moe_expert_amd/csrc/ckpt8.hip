@@ -75,7 +75,10 @@ __device__ inline float clamp_up(float u, float limit) { return u > limit ? limi
 // thread per 8 columns of a row: the flat index splits into (row, column) by the
 // workgroup's first index, once per workgroup. A block of 32 values is 4 threads
 // of one half, or 2 threads of interleaved pairs. 32768 x 1024 pairs of bf16 with the
-// save: 270 MB in 53 us, 5.1 TB/s.
+// save: 270 MB in 49 us, 5.5 TB/s. gu is read past the caches, which keep room for h and
+// the save: between a kernel that makes gu and one that reads h, us for the three, 129
+// -> 114; 8192 x 2880 86 -> 80, 2048 x 2880 the same 24. (Storing past them too gains 4 us
+// more there, and costs 8 where the save is read back soon.)
 template <bool BF, int FMT>
 __global__ __launch_bounds__(256) void k_glu_forward(GluArgs p) {
   const uint32_t I8 = (uint32_t)p.I / 8;
@@ -86,8 +89,8 @@ __global__ __launch_bounds__(256) void k_glu_forward(GluArgs p) {
   const int c = 8 * (int)(off % I8);
   const int64_t base = row * 2 * p.I;
   float a[8], b[8];        // the two 8-element pieces as they lie in memory
-  load_elems8<BF>(p.gu, base + (p.inter ? 2 * c : c), a);
-  load_elems8<BF>(p.gu, base + (p.inter ? 2 * c + 8 : p.I + c), b);
+  load_elems8<BF, true>(p.gu, base + (p.inter ? 2 * c : c), a);
+  load_elems8<BF, true>(p.gu, base + (p.inter ? 2 * c + 8 : p.I + c), b);
   float h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
