@@ -42,6 +42,8 @@ __device__ inline uint2 load8(const void *p) {
   const u32x2_any v = *reinterpret_cast<const u32x2_any *>(p);
   return make_uint2(v.x, v.y);
 }
+typedef uint32_t u32_any __attribute__((aligned(1)));
+__device__ inline void store4(void *p, uint32_t v) { *reinterpret_cast<u32_any *>(p) = v; }
 __device__ inline void store8(void *p, uint2 v) {
   u32x2_any u = {v.x, v.y};
   *reinterpret_cast<u32x2_any *>(p) = u;

@@ -26,32 +26,97 @@ namespace nf4moe {
 
 namespace {
 
-// Elements i .. i + 7 of a row of H, zeros past the end.
+// Eight elements as they lie in memory: loads first, arithmetic later. ODD: H % 8 != 0,
+// a row's last piece is partial; then its lane reads the row's last eight elements, which
+// are all there, and unpack_raw8 moves its own ones down and zeros in behind them. One
+// load for every lane, no branch between loads, nothing read past the row; a load per
+// element in that lane made the kernels twice as long (7954 rows of 118 bf16, backward:
+// 23 us against 13.5 for 120 columns).
 template <bool BF>
-__device__ inline void load_row8(const void *p, int64_t base, int i, int H, float (&v)[8]) {
-  if (i + 8 <= H) {
-    load_elems8<BF>(p, base + i, v);
+struct Raw8 {
+  uint4 v[BF ? 1 : 2];
+};
+template <bool BF, bool ODD>
+__device__ inline Raw8<BF> load_raw8(const void *p, int64_t base, int i, int H) {
+  Raw8<BF> r;
+  if (!ODD || H >= 8) {
+    const char *at = reinterpret_cast<const char *>(p) + (base + (ODD ? min(i, H - 8) : i)) * (BF ? 2 : 4);
+    r.v[0] = load16(at);
+    if constexpr (!BF) r.v[1] = load16(at + 16);
   } else {
+    uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      v[j] = 0.0f;
-      if (i + j < H)
-        v[j] = BF ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p)[base + i + j])
-                  : reinterpret_cast<const float *>(p)[base + i + j];
+      const int64_t at = base + min(j, H - 1);  // (i is 0)
+      w[j] = BF ? (uint32_t)reinterpret_cast<const uint16_t *>(p)[at] : reinterpret_cast<const uint32_t *>(p)[at];
+      w[j] = j < H ? w[j] : 0u;
+    }
+    if constexpr (BF) {
+      r.v[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    } else {
+      r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      r.v[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
   }
+  return r;
 }
-template <bool BF>
-__device__ inline void store_row8(void *p, int64_t base, int i, int H, const float (&v)[8]) {
-  if (i + 8 <= H) {
-    store_elems8<BF>(p, base + i, v);
-  } else {
+template <int N>
+__device__ inline void move_down(uint32_t (&w)[N], int by, bool yes) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j < H) {
-        if (BF) reinterpret_cast<uint16_t *>(p)[base + i + j] = (uint16_t)f32_to_bf16_rne(v[j]);
-        else reinterpret_cast<float *>(p)[base + i + j] = v[j];
-      }
+  for (int k = 0; k < N; ++k) w[k] = yes ? (k + by < N ? w[k + by] : 0u) : w[k];
+}
+template <bool BF, bool ODD>
+__device__ inline void unpack_raw8(const Raw8<BF> &r, int i, int H, float (&v)[8]) {
+  const int down = ODD && H >= 8 ? max(i - (H - 8), 0) : 0;  // places that the piece began too early
+  if constexpr (BF) {
+    uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+    if constexpr (ODD) {
+      move_down(w, 2, down & 4);
+      move_down(w, 1, down & 2);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = down & 1 ? __builtin_amdgcn_alignbit(k < 3 ? w[k + 1] : 0u, w[k], 16) : w[k];
+    }
+    unpack_bf16x8(make_uint4(w[0], w[1], w[2], w[3]), v);
+  } else {
+    uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+    if constexpr (ODD) {
+      move_down(w, 4, down & 4);
+      move_down(w, 2, down & 2);
+      move_down(w, 1, down & 1);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+  }
+}
+// Elements i .. i + 7 of a row of H (i < H), zeros past the end, and back.
+template <bool BF, bool ODD>
+__device__ inline void load_row8(const void *p, int64_t base, int i, int H, float (&v)[8]) {
+  unpack_raw8<BF, ODD>(load_raw8<BF, ODD>(p, base, i, H), i, H, v);
+}
+template <bool BF, bool ODD>
+__device__ inline void store_row8(void *p, int64_t base, int i, int H, const float (&v)[8]) {
+  if (!ODD || i + 8 <= H) {
+    store_elems8<BF>(p, base + i, v);
+    return;
+  }
+  // the partial piece: 4 elements, then 2, then 1, those that its length has
+  const int n = H & 7;
+  const uint32_t four = n & 4 ? ~0u : 0u, two = n & 2 ? ~0u : 0u;
+  auto pick = [](uint32_t m, uint32_t a, uint32_t b) { return (m & a) | (~m & b); };
+  if constexpr (BF) {
+    uint16_t *at = reinterpret_cast<uint16_t *>(p) + base + i;
+    const uint4 w = pack_bf16x8(v);
+    if (n & 4) store8(at, make_uint2(w.x, w.y));
+    if (n & 2) store4(at + (n & 4), pick(four, w.z, w.x));
+    if (n & 1) at[n & 6] = (uint16_t)pick(two, pick(four, w.w, w.y), pick(four, w.z, w.x));
+  } else {
+    uint32_t *at = reinterpret_cast<uint32_t *>(p) + base + i;
+    uint32_t w[7];
+#pragma unroll
+    for (int k = 0; k < 7; ++k) w[k] = __float_as_uint(v[k]);
+    if (n & 4) store16(at, make_uint4(w[0], w[1], w[2], w[3]));
+    if (n & 2) store8(at + (n & 4), make_uint2(pick(four, w[4], w[0]), pick(four, w[5], w[1])));
+    if (n & 1) at[n & 6] = pick(two, pick(four, w[6], w[2]), pick(four, w[4], w[0]));
   }
 }
 
@@ -80,9 +145,10 @@ __device__ inline void gate_phi8(int fn, const float (&v)[8], float (&phi)[8]) {
 __device__ inline float gate_scalar(const NormArgs &p, int64_t i) {
   return p.gate_bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p.gate)[i]) : reinterpret_cast<const float *>(p.gate)[i];
 }
+template <bool ODD>
 __device__ inline void gate_row8(const NormArgs &p, int64_t base, int i, float (&v)[8]) {
-  if (p.gate_bf16) load_row8<true>(p.gate, base, i, p.H, v);
-  else load_row8<false>(p.gate, base, i, p.H, v);
+  if (p.gate_bf16) load_row8<true, ODD>(p.gate, base, i, p.H, v);
+  else load_row8<false, ODD>(p.gate, base, i, p.H, v);
 }
 
 // Sum over the TPR threads of a row (NV values at once); red has a place per wave and
@@ -112,42 +178,7 @@ __device__ inline void row_sum(float (&v)[NV], float *red) {
   }
 }
 
-// Eight elements as they lie in memory: loads first, arithmetic later.
-template <bool BF>
-struct Raw8 {
-  uint4 v[BF ? 1 : 2];
-};
-template <bool BF>
-__device__ inline Raw8<BF> load_raw8(const void *p, int64_t base, int i, int H) {
-  Raw8<BF> r;
-  const char *at = reinterpret_cast<const char *>(p) + (base + i) * (BF ? 2 : 4);
-  if (i + 8 <= H) {
-    r.v[0] = load16(at);
-    if constexpr (!BF) r.v[1] = load16(at + 16);
-  } else {
-    float f[8];
-    load_row8<BF>(p, base, i, H, f);
-    if constexpr (BF) {
-      r.v[0] = pack_bf16x8(f);
-    } else {
-      r.v[0] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-      r.v[1] = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
-    }
-  }
-  return r;
-}
-template <bool BF>
-__device__ inline void unpack_raw8(const Raw8<BF> &r, float (&v)[8]) {
-  if constexpr (BF) {
-    unpack_bf16x8(r.v[0], v);
-  } else {
-    const uint4 a = r.v[0], b = r.v[1];
-    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-  }
-}
-
-template <bool XBF, int TPR, int NC>
+template <bool XBF, int TPR, int NC, bool ODD>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs p) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
   __shared__ float red[2][THREADS / 64];
@@ -157,16 +188,20 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
   const bool live = row < p.T;
   const int64_t base = (live ? row : 0) * p.H;
   const int H = p.H;
-  float x[NC][8], f[NC][8];
+  Raw8<XBF> rx[NC] = {};
+  Raw8<true> rf[NC] = {};
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int i = 8 * (t + c * TPR);
+    if (i >= H) continue;
+    rx[c] = load_raw8<XBF, ODD>(p.x, base, i, H);
+    if (p.f) rf[c] = load_raw8<true, ODD>(p.f, base, i, H);
+  }
+  float x[NC][8], f[NC][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[c][j] = f[c][j] = 0.0f;
-    if (i < H) {
-      load_row8<XBF>(p.x, base, i, H, x[c]);
-      if (p.f) load_row8<true>(p.f, base, i, H, f[c]);
-    }
+  for (int c = 0; c < NC; ++c) {
+    unpack_raw8<XBF, ODD>(rx[c], 8 * (t + c * TPR), H, x[c]);
+    unpack_raw8<true, ODD>(rf[c], 8 * (t + c * TPR), H, f[c]);
   }
   if (p.f) {
     float rs = 1.0f;
@@ -187,13 +222,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
       const int i = 8 * (t + c * TPR);
       if (i < H) {
         float w[8], g[8];
-        if (p.w_post) load_row8<false>(p.w_post, 0, i, H, w);
+        if (p.w_post) load_row8<false, ODD>(p.w_post, 0, i, H, w);
         if (p.w_post) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[c][j] *= rs * w[j];
         }
         if (p.gate_kind & 1) {
-          gate_row8(p, p.gate_kind == 3 ? base : 0, i, g);
+          gate_row8<ODD>(p, p.gate_kind == 3 ? base : 0, i, g);
           gate_phi8(p.gate_fn, g, w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[c][j] *= w[j];
@@ -203,7 +238,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
           x[c][j] += m * f[c][j];
           if (XBF) x[c][j] = bf16_to_f32(f32_to_bf16_rne(x[c][j]));
         }
-        if (live) store_row8<XBF>(p.x_new, base, i, H, x[c]);
+        if (live) store_row8<XBF, ODD>(p.x_new, base, i, H, x[c]);
       }
     }
   }
@@ -221,10 +256,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
       const int i = 8 * (t + c * TPR);
       if (i < H) {
         float w[8], y[8];
-        load_row8<false>(p.w_pre, 0, i, H, w);
+        load_row8<false, ODD>(p.w_pre, 0, i, H, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = x[c][j] * rs * w[j];
-        if (live) store_row8<true>(p.y, base, i, H, y);
+        if (live) store_row8<true, ODD>(p.y, base, i, H, y);
       }
     }
   }
@@ -241,7 +276,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_forward(NormArgs
 // 57, whose partial sums cost most).
 __host__ __device__ constexpr int back_threads(int tpr) { return tpr <= 512 ? 512 : 1024; }
 
-template <bool XBF, int TPR, int NC>
+template <bool XBF, int TPR, int NC, bool ODD>
 __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p) {
   constexpr int THREADS = back_threads(TPR), SLOTS = THREADS / TPR;
   // the first sum's places and the second's, in turn for even and odd rounds (a
@@ -256,17 +291,17 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
   // reads them (NC = 1)
   constexpr bool KEEP = NC == 1;
   __shared__ float4 kept[KEEP ? 2 : 1][2][KEEP ? TPR : 1];
-  auto first_weights = [&](int i, float (&w)[8]) { load_row8<false>(p.w_pre, 0, i, H, w); };
+  auto first_weights = [&](int i, float (&w)[8]) { load_row8<false, ODD>(p.w_pre, 0, i, H, w); };
   auto second_weights = [&](int i, float (&w)[8]) {
     if (p.w_post) {
-      load_row8<false>(p.w_post, 0, i, H, w);
+      load_row8<false, ODD>(p.w_post, 0, i, H, w);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 1.0f;
     }
     if (p.gate_kind == 1) {
       float v[8], phi[8];
-      gate_row8(p, 0, i, v);
+      gate_row8<ODD>(p, 0, i, v);
       gate_phi8(p.gate_fn, v, phi);
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] *= phi[j];
@@ -309,15 +344,15 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
       const int i = 8 * (t + c * TPR);
       if (i >= H || !live) continue;
       if (p.w_pre) {
-        ry[c] = load_raw8<true>(p.dy, base, i, H);
-        rx[c] = load_raw8<XBF>(p.x, base, i, H);
+        ry[c] = load_raw8<true, ODD>(p.dy, base, i, H);
+        rx[c] = load_raw8<XBF, ODD>(p.x, base, i, H);
       }
-      if (p.dx_new) rg[c] = load_raw8<XBF>(p.dx_new, base, i, H);
-      if (p.f) rf[c] = load_raw8<true>(p.f, base, i, H);
+      if (p.dx_new) rg[c] = load_raw8<XBF, ODD>(p.dx_new, base, i, H);
+      if (p.f) rf[c] = load_raw8<true, ODD>(p.f, base, i, H);
     }
     float g[NC][8];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) unpack_raw8<XBF>(rg[c], g[c]);
+    for (int c = 0; c < NC; ++c) unpack_raw8<XBF, ODD>(rg[c], 8 * (t + c * TPR), H, g[c]);
     if (p.w_pre) {
       float a[NC][8], n[NC][8];
       float s[1] = {0.0f};
@@ -325,8 +360,8 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = 8 * (t + c * TPR);
-        unpack_raw8<true>(ry[c], a[c]);
-        unpack_raw8<XBF>(rx[c], n[c]);
+        unpack_raw8<true, ODD>(ry[c], i, H, a[c]);
+        unpack_raw8<XBF, ODD>(rx[c], i, H, n[c]);
         if (i < H) {
           float w[8];
           if (KEEP) kept8(0, w);
@@ -350,7 +385,7 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = 8 * (t + c * TPR);
-      if (i < H && live) store_row8<XBF>(p.dx, base, i, H, g[c]);
+      if (i < H && live) store_row8<XBF, ODD>(p.dx, base, i, H, g[c]);
     }
     if (p.f) {
       // f becomes n_f (or stays f), g becomes the gradient of n_f up to the factor m
@@ -362,7 +397,7 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = 8 * (t + c * TPR);
-        unpack_raw8<true>(rf[c], f[c]);
+        unpack_raw8<true, ODD>(rf[c], i, H, f[c]);
         if (i < H) {
           float w[8];
           if (KEEP) kept8(1, w);
@@ -371,11 +406,11 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
           for (int j = 0; j < 8; ++j) f[c][j] *= rs;
           if (p.gate_kind == 3) {
             float v[8], q[8], dg[8];
-            gate_row8(p, base, i, v);
+            gate_row8<ODD>(p, base, i, v);
             gate_phi8(p.gate_fn, v, q);
 #pragma unroll
             for (int j = 0; j < 8; ++j) dg[j] = p.alpha * gate_slope(p.gate_fn, q[j]) * g[c][j] * f[c][j] * w[j];
-            if (live) store_row8<false>(p.dgate, base, i, H, dg);
+            if (live) store_row8<false, ODD>(p.dgate, base, i, H, dg);
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[c][j] *= q[j];
           }
@@ -397,7 +432,7 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
         if (i < H && live) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[c][j] = mr * (g[c][j] - f[c][j] * mean);
-          store_row8<true>(p.df, base, i, H, g[c]);
+          store_row8<true, ODD>(p.df, base, i, H, g[c]);
         }
       }
     }
@@ -454,33 +489,33 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(NormArgs p) {
   if (p.dw_post) p.dw_post[col] = phi * s;
 }
 
-template <bool XBF>
+template <bool XBF, bool ODD>
 hipError_t norm_forward_t(const NormArgs &a, hipStream_t s) {
   if (a.H <= 512)
-    hipLaunchKernelGGL((k_norm_forward<XBF, 64, 1>), dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_norm_forward<XBF, 64, 1, ODD>), dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a);
   else if (a.H <= 2048)
-    hipLaunchKernelGGL((k_norm_forward<XBF, 256, 1>), dim3((unsigned)a.T), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_norm_forward<XBF, 256, 1, ODD>), dim3((unsigned)a.T), dim3(256), 0, s, a);
   else if (a.H <= 4096)
-    hipLaunchKernelGGL((k_norm_forward<XBF, 512, 1>), dim3((unsigned)a.T), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((k_norm_forward<XBF, 512, 1, ODD>), dim3((unsigned)a.T), dim3(512), 0, s, a);
   else if (a.H <= 8192)
-    hipLaunchKernelGGL((k_norm_forward<XBF, 1024, 1>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((k_norm_forward<XBF, 1024, 1, ODD>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
   else
-    hipLaunchKernelGGL((k_norm_forward<XBF, 1024, 2>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL((k_norm_forward<XBF, 1024, 2, ODD>), dim3((unsigned)a.T), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 
 int norm_tpr(int H) { return H <= 512 ? 64 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024; }
 int norm_slots(int H) { return back_threads(norm_tpr(H)) / norm_tpr(H); }
 
-template <bool XBF>
+template <bool XBF, bool ODD>
 hipError_t norm_backward_t(const NormArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)a.groups), block(back_threads(norm_tpr(a.H)));
   const size_t lds = norm_slots(a.H) > 1 ? (size_t)2 * a.H * sizeof(float) : 0;
-  if (a.H <= 512) hipLaunchKernelGGL((k_norm_backward<XBF, 64, 1>), grid, block, lds, s, a);
-  else if (a.H <= 2048) hipLaunchKernelGGL((k_norm_backward<XBF, 256, 1>), grid, block, lds, s, a);
-  else if (a.H <= 4096) hipLaunchKernelGGL((k_norm_backward<XBF, 512, 1>), grid, block, lds, s, a);
-  else if (a.H <= 8192) hipLaunchKernelGGL((k_norm_backward<XBF, 1024, 1>), grid, block, lds, s, a);
-  else hipLaunchKernelGGL((k_norm_backward<XBF, 1024, 2>), grid, block, lds, s, a);
+  if (a.H <= 512) hipLaunchKernelGGL((k_norm_backward<XBF, 64, 1, ODD>), grid, block, lds, s, a);
+  else if (a.H <= 2048) hipLaunchKernelGGL((k_norm_backward<XBF, 256, 1, ODD>), grid, block, lds, s, a);
+  else if (a.H <= 4096) hipLaunchKernelGGL((k_norm_backward<XBF, 512, 1, ODD>), grid, block, lds, s, a);
+  else if (a.H <= 8192) hipLaunchKernelGGL((k_norm_backward<XBF, 1024, 1, ODD>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((k_norm_backward<XBF, 1024, 2, ODD>), grid, block, lds, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.dw_pre || a.dw_post || (a.dgate && a.gate_kind == 1)) {
@@ -511,14 +546,16 @@ hipError_t launch_norm_forward(const NormArgs &a, hipStream_t s) {
     if (a.gate_kind >= 2) p.gate = (const char *)a.gate + (a.gate_kind == 3 ? n : r0) * gb;
     if (a.rstd_post) p.rstd_post = a.rstd_post + r0;
     if (a.rstd_pre) p.rstd_pre = a.rstd_pre + r0;
-    const hipError_t e = a.x_bf16 ? norm_forward_t<true>(p, s) : norm_forward_t<false>(p, s);
+    const hipError_t e = a.H % 8 ? (a.x_bf16 ? norm_forward_t<true, true>(p, s) : norm_forward_t<false, true>(p, s))
+                                 : (a.x_bf16 ? norm_forward_t<true, false>(p, s) : norm_forward_t<false, false>(p, s));
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
 hipError_t launch_norm_backward(const NormArgs &a, hipStream_t s) {
-  return a.x_bf16 ? norm_backward_t<true>(a, s) : norm_backward_t<false>(a, s);
+  if (a.H % 8) return a.x_bf16 ? norm_backward_t<true, true>(a, s) : norm_backward_t<false, true>(a, s);
+  return a.x_bf16 ? norm_backward_t<true, false>(a, s) : norm_backward_t<false, false>(a, s);
 }
 
 }  // namespace nf4moe

@@ -318,6 +318,31 @@ def test_two_streams_at_once():
         assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
 
 
+@pytest.mark.parametrize("H", [2, 3, 4, 5, 6, 8, 9, 10, 11, 12, 13, 14, 15, 521, 2052, 4094, 8198])
+@pytest.mark.parametrize("xdt,gdt", [("bf16", "f32"), ("f32", "bf16")])
+def test_block_norm_every_length_of_a_last_piece(H, xdt, gdt):
+    test_block_norm_forward_and_backward(9, H, xdt, True, True, "full", gdt, 1)
+
+
+def test_block_norm_neighbours_of_a_last_piece():
+    """A row's partial piece is read with the values before it: those, not finite, stay out of it, and no row reaches another."""
+    T, H = 6, 21
+    v = norm_inputs(T, H, "bf16", True, True, "none", "f32", 3)
+    w = dict(w_post=v["w_post"], w_pre=v["w_pre"])
+    want = M.block_norm_forward(v["x"], v["f"], **w)
+    bad = v["f"].clone()
+    bad[2, 15] = float("nan")
+    bad[3, 13] = float("inf")
+    got = M.block_norm_forward(v["x"], bad, **w)
+    keep = [0, 1, 4, 5]
+    assert all(torch.equal(got[k][keep], want[k][keep]) for k in want)
+    w1 = dict(w_pre=v["w_pre"])                 # without the post norm each value of f reaches its own place of x' only
+    a, b = M.block_norm_forward(v["x"], v["f"], **w1), M.block_norm_forward(v["x"], bad, **w1)
+    same = torch.ones(T, H, dtype=torch.bool, device=DEV)
+    same[2, 15] = same[3, 13] = False
+    assert torch.equal(a["x"][same], b["x"][same]) and not torch.isfinite(b["x"][~same]).any()
+
+
 def test_rows_behind_the_last_are_left_alone():
     """Through the C ABI with room behind each output: nothing past the last row is written."""
     Rn, I = 5, 64
