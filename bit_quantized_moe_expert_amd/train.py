@@ -87,6 +87,10 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# A new tensor of a checked (so contiguous) one's shape; 0.5 us sooner than new_empty.
+_like = torch.empty_like
+
+
 def _scratch(like, nbytes):
     """(tensor, address, size) of a 256-byte aligned workspace on like's device."""
     ws = like.new_empty(nbytes, dtype=_U8)
@@ -126,7 +130,7 @@ def ckpt8_quantize(x, fmt: int = CKPT_MXINT8) -> Ckpt8:
     if fmt not in (CKPT_MXINT8, CKPT_MXFP8):
         raise ValueError(f"unknown checkpoint format {fmt}")
     xp, K = _arg(x, "x", shape, x.dtype, i), shape[-1]
-    codes = x.new_empty(shape, dtype=_U8)
+    codes = _like(x, dtype=_U8)
     scale = x.new_empty((*shape[:-1], K // 32), dtype=_U8)
     _run(i, M.lib().nf4moe_ckpt8_quantize, fmt, xp, dt, x.numel() // K, K, codes.data_ptr(), scale.data_ptr())
     return Ckpt8(codes, scale, fmt)
@@ -140,7 +144,7 @@ def ckpt8_dequantize(ck: Ckpt8, dtype=_BF16):
     shape, i = ck.codes.shape, ck.codes.get_device()
     cp, sp = ck.args("checkpoint", shape, i)
     K = shape[-1]
-    out = ck.codes.new_empty(shape, dtype=dtype)
+    out = _like(ck.codes, dtype=dtype)
     _run(i, M.lib().nf4moe_ckpt8_dequantize, ck.fmt, cp, sp, out.numel() // K, K, out.data_ptr(), dt)
     return out
 
@@ -164,7 +168,7 @@ def glu_forward(gu, glu: int = 0, alpha: float = 0.0, limit: float = 0.0, interl
     if ckpt is None:
         _run(i, M.lib().nf4moe_glu_forward, gp, dt, R, I, glu, alpha, limit, interleaved, h.data_ptr(), 0, None, None)
         return h
-    ck = Ckpt8(gu.new_empty((R, cols), dtype=_U8), gu.new_empty((R, cols // 32), dtype=_U8), ckpt)
+    ck = Ckpt8(_like(gu, dtype=_U8), gu.new_empty((R, cols // 32), dtype=_U8), ckpt)
     _run(i, M.lib().nf4moe_glu_forward, gp, dt, R, I, glu, alpha, limit, interleaved, h.data_ptr(), ckpt,
          ck.codes.data_ptr(), ck.scale.data_ptr())
     return h, ck
@@ -187,11 +191,11 @@ def glu_backward(dh, gu, glu: int = 0, alpha: float = 0.0, limit: float = 0.0, i
         gp = _arg(gu, "gu", (R, 2 * I), gu.dtype, i)
     wp = _arg(row_w, "row_w", (R,), _F32, i)
     dp = _arg(dh, "dh", dh.shape, dh.dtype, i)
-    out = dict(dgu=dh.new_empty((R, 2 * I), dtype=_BF16))
+    out = dict(dgu=_like(gu.codes if isinstance(gu, Ckpt8) else gu, dtype=_BF16))
     if need_h:
-        out["h"] = dh.new_empty((R, I), dtype=_BF16)
+        out["h"] = _like(dh, dtype=_BF16)
     if row_w is not None:
-        out["drow_w"] = torch.empty_like(row_w)
+        out["drow_w"] = _like(row_w)
     _run(i, M.lib().nf4moe_glu_backward, dp, ddt, src, gp, sp, R, I, glu, alpha, limit, interleaved, wp,
          out["dgu"].data_ptr(), _p(out.get("h")), _p(out.get("drow_w")))
     return out
@@ -246,11 +250,11 @@ def block_norm_forward(x, f=None, *, w_post=None, w_pre=None, gate=None, gate_fn
         np_ = None
     else:
         if out is None:
-            out = torch.empty_like(x)
+            out = _like(x)
         np_ = _arg(out, "out", x.shape, x.dtype, i)
-    y = None if w_pre is None else torch.empty_like(x) if x.dtype is _BF16 else x.new_empty((T, H), dtype=_BF16)
+    y = None if w_pre is None else _like(x, dtype=_BF16)
     rp = x.new_empty((T,), dtype=_F32) if w_post is not None else None
-    r = x.new_empty((T,), dtype=_F32) if w_pre is not None else None
+    r = None if w_pre is None else x.new_empty((T,), dtype=_F32) if rp is None else _like(rp)
     _run(i, M.lib().nf4moe_block_norm_forward, st, xp, fp, T, np_, _p(y), _p(rp), _p(r))
     return dict(x=x if f is None else out, y=y, rstd_post=rp, rstd_pre=r)
 
@@ -272,15 +276,15 @@ def block_norm_backward(dx_new, dy, x_new, f=None, *, rstd_post=None, rstd_pre=N
     dyp = _arg(dy, "dy", x_new.shape, _BF16, i)
     rp = None if w_post is None else _arg(rstd_post, "rstd_post", (T,), _F32, i)
     r = None if w_pre is None else _arg(rstd_pre, "rstd_pre", (T,), _F32, i)
-    out = dict(dx=torch.empty_like(x_new))
+    out = dict(dx=_like(x_new))
     if f is not None:
-        out["df"] = torch.empty_like(f)
+        out["df"] = _like(f)
     if gate is not None:
-        out["dgate"] = x_new.new_empty(gate.shape, dtype=_F32)
+        out["dgate"] = _like(gate, dtype=_F32)
     if w_post is not None:
-        out["dw_post"] = torch.empty_like(w_post)
+        out["dw_post"] = _like(w_post)
     if w_pre is not None:
-        out["dw_pre"] = torch.empty_like(w_pre)
+        out["dw_pre"] = _like(w_pre)
     L = M.lib()
     ws, wsp, nb = _scratch(x_new, L.nf4moe_block_norm_workspace_bytes(H, T))
     _run(i, L.nf4moe_block_norm_backward, st, dxp, dyp, xp, fp, rp, r, T, out["dx"].data_ptr(),
@@ -361,7 +365,7 @@ def adapter_forward(x, A, B, ids, *, base=None, scale=None, x_row_of=None, out=N
     _gathered(x_row_of, R, rows)
     bp = _arg(base, "base", (R, N), dtype, i)
     if out is None:
-        out = x.new_empty((R, N), dtype=dtype)
+        out = x.new_empty((R, N), dtype=dtype) if base is None else _like(base)
     op = _arg(out, "out", (R, N), dtype, i)
     t = x.new_empty((R, rank), dtype=_F32) if return_t else None
     lib, sp = M.lib(), st
@@ -404,12 +408,12 @@ def adapter_backward(dy, x, t, A, B, ids, *, scale=None, x_row_of=None, dx_base=
     bp = _arg(dx_base, "dx_base", (R, K), dtype, i)
     out = {}
     if "dx" in need:
-        out["dx"] = dy.new_empty((R, K), dtype=dtype) if dx is None else dx
+        out["dx"] = dx if dx is not None else dy.new_empty((R, K), dtype=dtype) if dx_base is None else _like(dx_base)
         _arg(out["dx"], "dx", (R, K), dtype, i)
     if "dA" in need:
-        out["dA"] = dy.new_empty((L, rank, K), dtype=_F32)
+        out["dA"] = _like(A, dtype=_F32)
     if "dB" in need:
-        out["dB"] = dy.new_empty((L, N, rank), dtype=_F32)
+        out["dB"] = _like(B, dtype=_F32)
     lib, sp = M.lib(), st
     ws, wsp, nb = _scratch(dy, lib.nf4moe_adapter_workspace_bytes(sp, R, 1))
     _run(i, lib.nf4moe_adapter_backward, sp, dyp, src, xp, xs, max(rows, 1), rp, tp, ip, pp, pn, R, bp, _p(out.get("dx")), dt,
