@@ -385,8 +385,8 @@ __host__ __device__ inline int low_groups(int rank) { return part_pack(rank) ? r
 // rows, so each adapter row is read once per workgroup. A quad reads 64 bytes of one
 // row, the four quads of a row 256. Four waves where there are many rows: eight take
 // 31.4 us against 27.1 for 32768 gathered rows of rank 16, 89.7 against 57.1 of rank 64.
-// Bound by the loads of x: 32768 contiguous rows of 2048 (134 MB) take 32 us, 4.2 TB/s,
-// a plain read of them 24; 4096 rows gathered 8 times each 21.4 us, 6.3 TB/s out of L2.
+// Bound by the loads of x: 32768 contiguous rows of 2048 (134 MB) take 30 us, 4.5 TB/s,
+// a plain read of them 24; 4096 rows gathered 8 times each 19.4 us, 6.9 TB/s out of L2.
 constexpr int kSliceMin = 256;  // no slice is narrower
 
 template <int RT, int NS, int W>

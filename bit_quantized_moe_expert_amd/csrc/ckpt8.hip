@@ -75,7 +75,7 @@ __device__ inline float clamp_up(float u, float limit) { return u > limit ? limi
 // thread per 8 columns of a row: the flat index splits into (row, column) by the
 // workgroup's first index, once per workgroup. A block of 32 values is 4 threads
 // of one half, or 2 threads of interleaved pairs. 32768 x 1024 pairs of bf16 with the
-// save: 270 MB in 49 us, 5.5 TB/s. gu is read past the caches, which keep room for h and
+// save: 270 MB in 42 us, 6.4 TB/s (in part the last-level cache). gu is read past the caches, which keep room for h and
 // the save: between a kernel that makes gu and one that reads h, us for the three, 129
 // -> 114; 8192 x 2880 86 -> 80, 2048 x 2880 the same 24. (Storing past them too gains 4 us
 // more there, and costs 8 where the save is read back soon.)

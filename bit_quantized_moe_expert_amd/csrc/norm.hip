@@ -11,7 +11,7 @@
 //   df = rstd_f (dz w_post - n_f mean(dz w_post n_f));  dw_post = sum_t dz n_f
 // Everything is fp32 in registers between the loads and the stores; each output
 // is rounded once. Both directions are bound by memory traffic: the forward of 8190 x
-// 2880 (fp32 stream, 283 MB) takes 53.5 us, 5.3 TB/s, the backward of 8192 x 2048 bf16
+// 2880 (fp32 stream, 283 MB) takes 52.4 us, 5.4 TB/s, the backward of 8192 x 2048 bf16
 // (201 MB) 43.4 us and 5.0 for the joined column sums, 4.2 TB/s: a row's two sums wait
 // for each other.
 //
