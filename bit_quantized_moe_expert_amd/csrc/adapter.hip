@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
           wcnt[w][i] = (uint16_t)run;
           run += c;
         }
-        tot[i] = next[i];       // where this round's rows of the bin begin
+        tot[i] = next[i];       // where these rows of the bin begin
         next[i] += (int32_t)run;
       }
       __syncthreads();

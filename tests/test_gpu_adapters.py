@@ -115,6 +115,24 @@ def test_backward(rows, Rn, L, K, N, rank, dt, src):
         assert set(one) == set(need) and torch.equal(one[need[0]], got[need[0]])
 
 
+# every number of K slices, both heights of an expansion block, several chunks of an adapter
+LARGE = [("mixed", 9000, 9, 1032, 264, 48, "bf16"), ("experts", 17000, 12, 776, 280, 40, "f32"),
+         ("one", 16500, 3, 1544, 136, 16, "bf16"), ("mixed", 4100, 5, 3208, 264, 32, "f32"),
+         ("mixed", 1300, 3, 3208, 520, 8, "bf16"), ("mixed", 5000, 7, 1032, 2056, 64, "bf16"),
+         ("experts", 8200, 6, 640, 136, 128, "f32"), ("one", 20000, 2, 520, 392, 24, "bf16")]
+
+
+@pytest.mark.parametrize("rows,Rn,L,K,N,rank,dt", LARGE)
+def test_forward_of_many_rows(rows, Rn, L, K, N, rank, dt):
+    test_forward(rows, Rn, L, K, N, rank, dt)
+
+
+@pytest.mark.parametrize("src", ["bf16", M.CKPT_MXINT8, M.CKPT_MXFP8])
+@pytest.mark.parametrize("rows,Rn,L,K,N,rank,dt", LARGE)
+def test_backward_of_many_rows(rows, Rn, L, K, N, rank, dt, src):
+    test_backward(rows, Rn, L, K, N, rank, dt, src)
+
+
 @pytest.mark.parametrize("Rn,L", [(1500, 7), (5000, 4096), (70000, 900), (70000, 4096)])
 def test_grouping_of_many_rows_and_adapters(Rn, L):
     """Every row meets its own adapter, and sums over rows see each row once."""
