@@ -684,9 +684,9 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
 // are split into three bf16 parts in registers. One workgroup per chunk of rows and
 // 128 columns, its four waves taking every fourth step of 32 rows; their sums are
 // added in order through LDS, from which they leave in either layout. An adapter
-// with one chunk (of no rows: zeros) is written straight out; the chunks of others go
-// to partial sums that k_rowgrad_join adds in order. dA and dB run in one launch: dB
-// waits for dy while dA, from an 8-bit x that the caches hold, decodes and turns; apart,
+// with one chunk (of no rows: zeros), or so few that one workgroup takes all, is written
+// straight out; the chunks of others go to partial sums that k_rowgrad_join adds in
+// order. dA and dB run in one launch: dB waits for dy while dA, from an 8-bit x that the caches hold, decodes and turns; apart,
 // one after the other, they take 64 us instead of 56 (32768 rows of rank 16, 2048 x
 // 2048, dy 134 MB read once; vector instructions 20 us). Run right after the product
 // that reads dy too, before the expansion: 49 us, the caches still hold a part of dy.
@@ -803,7 +803,15 @@ __global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p, int na, int nb) 
   __shared__ int32_t prow[kMaxChunk], vrow[kMaxChunk];
   const int per = na + nb, ci = blockIdx.x / per, block = blockIdx.x % per;
   if (ci >= p.plan.counts[1]) return;
-  const int4 chunk = p.plan.chunks[ci];
+  int4 chunk = p.plan.chunks[ci];
+  if (p.merge > 1 && chunk.w >= 0) {  // the first of `merge` chunks takes them all
+    const int2 of = p.plan.chunks_of[chunk.x];
+    const int k = chunk.w - of.y;
+    if (k % p.merge) return;
+    const int4 end = p.plan.chunks[ci + min(p.merge, of.x - k) - 1];
+    chunk.z = end.y + end.z - chunk.y;
+    if (of.x <= p.merge) chunk.w = -1;
+  }
   const bool first = block < na;
   const int32_t *row_of = first ? p.a.row_of : p.b.row_of;
   const int last = (first ? p.a.v_rows : p.b.v_rows) - 1;
@@ -821,7 +829,7 @@ __global__ __launch_bounds__(256) void k_rowgrad(RowGradArgs p, int na, int nb) 
 // The chunks of an adapter that has several, added in order.
 __global__ __launch_bounds__(256) void k_rowgrad_join(RowGradArgs p, int64_t sa, int64_t sb) {
   const int2 c = p.plan.chunks_of[blockIdx.y];
-  if (c.x <= 1) return;
+  if (c.x <= p.merge) return;
   int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= sa + sb) return;
   const bool first = i < sa;
@@ -829,7 +837,7 @@ __global__ __launch_bounds__(256) void k_rowgrad_join(RowGradArgs p, int64_t sa,
   if (!first) i -= sa;
   const float *partial = (first ? p.a.partial : p.b.partial) + c.y * size + i;
   f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < c.x; ++k) s += *reinterpret_cast<const f32x4_t *>(partial + k * size);
+  for (int k = 0; k < c.x; k += p.merge) s += *reinterpret_cast<const f32x4_t *>(partial + k * size);
   *reinterpret_cast<f32x4_t *>((first ? p.a.out : p.b.out) + blockIdx.y * size + i) = s;
 }
 
@@ -1026,12 +1034,24 @@ static void rowgrad_src(const RowGradArgs &a, hipStream_t s) {
   else hipLaunchKernelGGL((k_rowgrad<SRC, 4>), dim3(gx, (unsigned)cdiv(a.rank, 64)), block, 0, s, a, na, nb);
 }
 
-hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s) {
+hipError_t launch_adapter_rowgrad(const RowGradArgs &args, hipStream_t s) {
+  // A chunk's partial sums are rank x 128 fp32 a workgroup, as many bytes as its rows of
+  // a high rank: then more chunks to a workgroup, and where all of them fit no join. us, dA
+  // and dB with the join, for 1 / 2 / 4 / 8 chunks:
+  //   1003 rows of 5 adapters, 2880 x 1440, rank 16   9.9 / 9.0 / 8.9 / 7.5, rank 128 31.7 / 22.4 / 22.5 / 18.3
+  //   4096 rows of 8, 2048 x 2048, rank 16 16.7 / 17.1 / 17.5 / 17.5, 32 24.3 / 20.2 / 21.8 / 21.3,
+  //                                rank 64 44.1 / 35.3 / 28.6 / 29.9, 128 73.3 / 55.8 / 46.2 / 33.7
+  //   12288 rows of 8, rank 32 37.0 / 36.5 / 49.3 / 43.5, 64 60.9 / 52.0 / 57.4 / 56.7, 128 108 / 92.7 / 83.5 / 90.3
+  //   32768 rows of 4 (chunks of 1024), rank 32 71.0 / 74.9, 64 101.5 / 90.9, 128 193 / 172
+  RowGradArgs a = args;
+  const int rows = adapter_chunk_rows(a.R);
+  a.merge = a.R <= 8 * rows ? 8 : a.rank <= 16 ? 1 : a.rank <= 32 ? (a.R < 8192 ? 2 : 1) : 4;
+  while (a.merge * rows > kMaxChunk) a.merge /= 2;
   if (a.src == SRC_BF16) rowgrad_src<SRC_BF16>(a, s);
   else if (a.src == SRC_MXINT8) rowgrad_src<SRC_MXINT8>(a, s);
   else rowgrad_src<SRC_MXFP8>(a, s);
   const int64_t sa = a.a.out ? (int64_t)a.rank * a.a.C : 0, sb = a.b.out ? (int64_t)a.rank * a.b.C : 0;  // multiples of 64
-  if (a.R > adapter_chunk_rows(a.R))  // else no adapter has two chunks
+  if (a.R > a.merge * rows)  // else no adapter has partial sums
     hipLaunchKernelGGL(k_rowgrad_join, dim3((unsigned)cdiv(sa + sb, 1024), (unsigned)a.L), dim3(256), 0, s, a, sa, sb);
   return hipGetLastError();
 }

@@ -141,6 +141,7 @@ struct RowGradArgs {
   AdapterPlan plan;
   int R, L, rank, src;
   RowGradOne a, b;
+  int merge;           // chunks of an adapter that a workgroup takes together (set by the launch)
 };
 hipError_t launch_adapter_rowgrad(const RowGradArgs &a, hipStream_t s);
 hipError_t launch_fill_f32_zero(float *p, int64_t n, hipStream_t s);
