@@ -64,7 +64,10 @@ int plan_rows(int R, int L) {
 __device__ inline int bin_of(int id, int L) { return id < 0 || id >= L ? L : id; }
 
 constexpr int kPrepareThreads = 256;
-__device__ inline void plan_hist(const int32_t *__restrict__ ids, int R, int L, int per, int32_t *__restrict__ hist, int32_t *cnt) {
+// The row counters of every bin per plan workgroup.
+__global__ __launch_bounds__(kPrepareThreads) void k_plan_hist(const int32_t *__restrict__ ids, int R, int L, int per,
+                                                               int32_t *__restrict__ hist) {
+  extern __shared__ int32_t cnt[];
   for (int b = threadIdx.x; b <= L; b += kPrepareThreads) cnt[b] = 0;
   __syncthreads();
   const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
@@ -95,9 +98,10 @@ __device__ inline void turn_8x8(const uint4 (&row)[8], uint32_t (&blk)[4][8]) {
     }
   }
 }
+template <int THREADS>
 __device__ inline void turn_block(const TurnArgs &a, int l, int block) {
   const int p8 = a.P / 8, q8 = a.Q / 8;
-  const int i = block * kPrepareThreads + (int)threadIdx.x;
+  const int i = block * THREADS + (int)threadIdx.x;
   if (i >= p8 * q8) return;
   const int p = 8 * (a.p_is_rank ? i % p8 : i / q8), q = 8 * (a.p_is_rank ? i / p8 : i % q8);
   const int64_t base = (int64_t)l * a.P * a.Q;
@@ -111,21 +115,20 @@ __device__ inline void turn_block(const TurnArgs &a, int l, int block) {
     store16(a.out + base + (int64_t)(q + k) * a.P + p, make_uint4(blk[0][k], blk[1][k], blk[2][k], blk[3][k]));
 }
 
-// What the later launches need and what does not depend on anything: the row
-// counters per plan workgroup, and the backward's turned weights (0, 1 or 2 arrays).
-__global__ __launch_bounds__(kPrepareThreads) void k_prepare(const int32_t *__restrict__ ids, int R, int L, int per, int hists,
-                                                          int32_t *__restrict__ hist, TurnArgs t0, TurnArgs t1, int b0, int b1) {
-  extern __shared__ int32_t cnt[];
-  int i = (int)blockIdx.x;
-  if (i < hists) {
-    plan_hist(ids, R, L, per, hist, cnt);
-    return;
-  }
-  i -= hists;  // per adapter b0 blocks of the first array, then b1 of the second
-  const int l = i / (b0 + b1), block = i % (b0 + b1);
-  if (block < b0) turn_block(t0, l, block);
-  else turn_block(t1, l, block - b0);
+// Block i of the turned copies: per adapter b0 blocks of the first array, then b1 of the
+// second (0 where there is none).
+struct TurnPair {
+  TurnArgs t0, t1;
+  int b0, b1;
+};
+template <int THREADS>
+__device__ inline void turn_blocks(const TurnPair &t, int i) {
+  const int l = i / (t.b0 + t.b1), block = i % (t.b0 + t.b1);
+  if (block < t.b0) turn_block<THREADS>(t.t0, l, block);
+  else turn_block<THREADS>(t.t1, l, block - t.b0);
 }
+
+__global__ __launch_bounds__(kPrepareThreads) void k_turn(TurnPair turn) { turn_blocks<kPrepareThreads>(turn, (int)blockIdx.x); }
 
 // Exclusive prefixes of four counts over the workgroup's threads in order; totals in *sum.
 __device__ inline int4 block_prefix4(int4 v, int4 *wsum, int4 *sum) {
@@ -156,13 +159,15 @@ __device__ inline int4 block_prefix4(int4 v, int4 *wsum, int4 *sum) {
 // writes the chunk table; all share the tile table. Bound by the latency of a chain of
 // barriers, 6 to 10 us up to 32768 rows of 64 adapters, not by bytes.
 //
-// The counters come from k_prepare, or every workgroup counts all rows itself where
-// that spares the launch. us, two launches against one: 4099 rows of 6 adapters 2.4 +
-// 5.9 / 7.8, 8192 of 64 2.4 + 10.2 / 12.7, 16384 of 64 2.1 + 10.3 / 15.9.
+// The counters come from k_plan_hist, or for few rows every workgroup counts all of them
+// itself. Workgroups behind these turn the backward's weights, which nothing waits for. us, two launches
+// against one: 4099 rows of 6 adapters 2.4 + 5.9 / 7.8, 8192 of 64 2.4 + 10.2 / 12.7,
+// 16384 of 64 2.1 + 10.3 / 15.9.
 constexpr int kSelfCount = 8192;
 constexpr int kWaveBins = 1024;  // up to so many bins the waves' counts have a place each in LDS
 __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__restrict__ ids, int R, int L, int per,
-                                                               int groups, bool self_count, int chunk_rows, AdapterPlan p) {
+                                                               int groups, bool self_count, int chunk_rows, AdapterPlan p,
+                                                               TurnPair turn) {
   constexpr int W = kPlanThreads / 64;
   __shared__ int32_t next[kMaxAdapters + 1], tot[kMaxAdapters + 1];
   __shared__ union {
@@ -172,6 +177,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_plan_scatter(const int32_t *__
   __shared__ int4 wsum[W];
   auto &wcnt = u.count;
   int32_t *bin_tile = u.bins[0], *bin_row = u.bins[1];  // each bin's first tile and first place
+  if ((int)blockIdx.x >= groups) {
+    turn_blocks<kPlanThreads>(turn, (int)blockIdx.x - groups);
+    return;
+  }
   const int tid = threadIdx.x, nb = L + 1;
   const int r0 = blockIdx.x * per, r1 = min(R, r0 + per);
   int b = r0 + tid < r1 ? bin_of(ids[r0 + tid], L) : -1;
@@ -948,18 +957,19 @@ size_t adapter_plan_layout(int R, int L, void *base, AdapterPlan *p) {
 hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
   const int per = plan_rows(a.R, a.L);
   const int groups = a.ids ? (int)cdiv(a.R, per) : 0;
-  const TurnArgs t0 = {a.B, a.Bt, a.N, a.rank, false}, t1 = {a.A, a.At, a.rank, a.K, true};
-  const int b0 = a.Bt ? (int)cdiv((int64_t)a.N * a.rank / 64, kPrepareThreads) : 0;
-  const int b1 = a.At ? (int)cdiv((int64_t)a.K * a.rank / 64, kPrepareThreads) : 0;
-  // a launch for the counters alone is spared for few rows
-  const int hists = groups > 1 && (a.R > kSelfCount || b0 + b1 > 0) ? groups : 0;
-  const unsigned grid = (unsigned)(hists + a.L * (b0 + b1));
-  if (grid > 0)
-    hipLaunchKernelGGL(k_prepare, dim3(grid), dim3(kPrepareThreads), hists ? sizeof(int32_t) * (a.L + 1) : 0, s, a.ids, a.R, a.L,
-                       per, hists, a.plan.hist, t0, t1, b0, b1);
-  if (groups > 0)
-    hipLaunchKernelGGL(k_plan_scatter, dim3(groups), dim3(kPlanThreads), 0, s, a.ids, a.R, a.L, per, groups,
-                       hists == 0, adapter_chunk_rows(a.R), a.plan);
+  const bool self = a.R <= kSelfCount;
+  const int threads = groups ? kPlanThreads : kPrepareThreads;  // the weights are turned beside the grouping, or alone
+  const TurnPair turn = {{a.B, a.Bt, a.N, a.rank, false}, {a.A, a.At, a.rank, a.K, true},
+                         a.Bt ? (int)cdiv((int64_t)a.N * a.rank / 64, threads) : 0,
+                         a.At ? (int)cdiv((int64_t)a.K * a.rank / 64, threads) : 0};
+  const unsigned turns = (unsigned)(a.L * (turn.b0 + turn.b1));
+  if (groups == 0 && turns > 0) hipLaunchKernelGGL(k_turn, dim3(turns), dim3(kPrepareThreads), 0, s, turn);
+  if (groups == 0) return hipGetLastError();
+  if (!self)
+    hipLaunchKernelGGL(k_plan_hist, dim3(groups), dim3(kPrepareThreads), sizeof(int32_t) * (a.L + 1), s, a.ids, a.R, a.L, per,
+                       a.plan.hist);
+  hipLaunchKernelGGL(k_plan_scatter, dim3(groups + turns), dim3(kPlanThreads), 0, s, a.ids, a.R, a.L, per, groups, self,
+                     adapter_chunk_rows(a.R), a.plan, turn);
   return hipGetLastError();
 }
 
