@@ -973,23 +973,26 @@ hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Slices of K, each a multiple of 128 and at least kSliceMin wide. A slice more is
-// more workgroups, and more to join. us, product + join, for 1 / 2 / 4 / 8 slices:
-//   640 rows, rank 32, K 4096       19.6 / 16.3 / 12.7 / 11.6
-//   2048 rows, rank 64, K 4096      27.6 / 20.8 / 17.2 / 19.5
-//   4099 rows, rank 64, K 2880      22.5 / 20.1 / 23.3 / 24.4
-//   8192 rows, rank 16, K 2048      13.4 / 16.6 / 16.6 / 17.5
-//   12867 rows, rank 64, K 1568     19.6 / 26.9 / 33.2 / 40.6
-//   16384 rows, rank 64, K 4096     67.1 / 63.7 / 59.7 / 71.2   (more tiles than run at once)
-//   32768 rows, rank 64, K 2048     57.1 / 61.2 / 72.4 / 114
-//   32768 rows, rank 16, K 2048     44.1 / 42.0 / 40.3 / 43.3
+// Slices of K, each a multiple of 128 and at least kSliceMin wide: up to 4, as many as
+// the CUs take at once, a workgroup of 64 rows each; where one slice is more than that,
+// slices against the tail of the last round. us, product + join, for 1 / 2 / 3 / 4 / 8:
+//   640 rows, rank 32, K 4096       19.6 / 16.3 /      / 12.7 / 11.6
+//   2000 rows, rank 64, K 2880           / 18.1 / 16.6 / 15.1
+//   4099 rows, rank 64, K 2880      22.5 / 19.4 / 18.1 / 23.2 / 24.4
+//   6500 rows, rank 64, K 2880           / 19.6 / 26.0 / 24.3
+//   8192 rows, rank 16, K 2048      13.4 / 16.6 /      / 16.6 / 17.5
+//   12867 rows, rank 64, K 1568     19.6 / 26.9 /      / 33.2 / 40.6
+//   16384 rows, rank 64, K 4096     67.1 / 63.7 /      / 59.7 / 71.2
+//   32768 rows, rank 64, K 2048     57.1 / 61.2 /      / 72.4 / 114
+//   32768 rows, rank 16, K 2048     44.1 / 42.0 /      / 40.3 / 43.3
 // Few rows of a low rank take one slice with 8 waves a workgroup, without a join,
 // while K is not too long for it (640 rows, rank 32, K 4096 17.0 us, 2048 rows, rank 16
 // 13.8): 1003 rows, rank 32, K 1440 10.3 us against 6.2 + 5.1 and a launch, a backward
 // of 168 rows, rank 16, 2784 x 2744 40 us against 43.
 static bool deep_slice(int R, int K, int rank) { return R < 4096 && rank <= 32 && K > 512 && K < 3000; }
 static int slice_width(int R, int K, int rank) {
-  const int most = R < 8192 ? 4 : R < 16384 ? 1 : rank <= 16 ? 4 : 2;
+  const int fit = (256 * kAdTile - 1) / R;  // an adapter more makes a tile more
+  const int most = fit > 0 ? (fit < 4 ? fit : 4) : rank <= 16 ? 4 : 2;
   const int w = (int)cdiv(cdiv(K, K <= 512 || deep_slice(R, K, rank) ? 1 : most), 128) * 128;
   return w < kSliceMin ? kSliceMin : w;
 }
