@@ -40,6 +40,8 @@ nf4moe_status_t check_ckpt8(int32_t fmt, const void *dense, nf4moe_dtype_t dt, i
 nf4moe_status_t check_glu(int64_t R, int32_t I, int32_t glu, float alpha, float limit, int32_t inter) {
   if (R < 0) return fail(NF4MOE_ERR_INVALID_ARG, "R=%lld < 0", (long long)R);
   if (I <= 0 || I % 32) return fail(NF4MOE_ERR_INVALID_ARG, "I=%d must be a positive multiple of 32", I);
+  // the kernels count the 2 I columns of a row in 32 bits, up to 2 I - 8 and 8 values from there
+  if (I > 1 << 30) return fail(NF4MOE_ERR_UNSUPPORTED, "I=%d past 2^30", I);
   if (R > ((int64_t)1 << 36) / I) return fail(NF4MOE_ERR_UNSUPPORTED, "R * I too large");
   if (glu != NF4MOE_GLU_SWIGLU && glu != NF4MOE_GLU_CLAMPED) return fail(NF4MOE_ERR_INVALID_ARG, "unknown glu %d", glu);
   if (glu == NF4MOE_GLU_CLAMPED && !(alpha > 0.0f && alpha < 1e30f && limit > 0.0f && limit < 1e30f))

@@ -371,7 +371,8 @@ nf4moe_status_t nf4moe_ckpt8_dequantize(nf4moe_ckpt8_t fmt, const uint8_t *codes
  * product gu [R, 2I] (fp32 or bf16; gate and up in halves, or interleaved as in
  * nf4moe_layer_t), bf16 RNE [R, I]. With codes / scale the same pass also writes
  * gu's 8-bit checkpoint ([R, 2I] and [R, 2I/32], format ckpt); both NULL saves
- * nothing. I % 32 == 0. R == 0 is a no-op. Errors: INVALID_ARG. */
+ * nothing. I % 32 == 0. R == 0 is a no-op. Errors: INVALID_ARG; UNSUPPORTED for I
+ * past 2^30 or R * I past 2^36. */
 nf4moe_status_t nf4moe_glu_forward(const void *gu, nf4moe_dtype_t gu_dtype, int64_t R, int32_t I, int32_t glu,
                                    float glu_alpha, float glu_limit, int32_t glu_interleaved, uint16_t *h,
                                    nf4moe_ckpt8_t ckpt, uint8_t *codes, uint8_t *scale, void *stream);
@@ -385,7 +386,7 @@ nf4moe_status_t nf4moe_glu_forward(const void *gu, nf4moe_dtype_t gu_dtype, int6
  *   h      bf16 [R, I]    the activation recomputed (optional)
  *   drow_w fp32 [R]       sum_c dh[r, c] * h[r, c], the gradient of row_w (optional)
  * The clamped form's gradient is that of the unclamped side at the limit itself.
- * Errors: INVALID_ARG. */
+ * Errors: INVALID_ARG, UNSUPPORTED as for the forward. */
 nf4moe_status_t nf4moe_glu_backward(const void *dh, nf4moe_dtype_t dh_dtype, nf4moe_src_t gu_src, const void *gu,
                                     const uint8_t *gu_scale, int64_t R, int32_t I, int32_t glu, float glu_alpha,
                                     float glu_limit, int32_t glu_interleaved, const float *row_w, uint16_t *dgu,

@@ -1,0 +1,35 @@
+"""Refusals of the fine-tuning operators at the edges of their sizes and arguments,
+without a GPU: addresses are made up and never dereferenced, every refused call
+returns before anything is enqueued."""
+import os
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pkg = pytest.importorskip("bit_quantized_moe_expert_amd")
+if not os.path.exists(pkg.LIB_PATH):
+    pytest.skip("libnf4moe.so not built", allow_module_level=True)
+
+L = pkg.lib()
+OK, INVALID, UNSUPPORTED, WORKSPACE, HIP = 0, 1, 2, 3, 4
+FAKE = 0x10000
+
+
+def far(i):
+    """Made-up addresses 8 TB apart."""
+    return (i + 1) << 43
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses, which a GPU would dereference")
+@pytest.mark.parametrize("glu,alpha,limit", [(0, 0.0, 0.0), (1, 1.702, 7.0)])
+def test_glu_refuses_rows_whose_columns_pass_32_bits(glu, alpha, limit):
+    """Columns of a row of gu are counted in 32 bits: 2 I is at most 2^31."""
+    for inter in (0, 1):
+        for wide in ((1 << 30) + 32, (1 << 31) - 32):
+            assert L.nf4moe_glu_forward(far(0), 1, 1, wide, glu, alpha, limit, inter, far(1), 0, None, None, None) == UNSUPPORTED
+            assert L.nf4moe_glu_forward(far(0), 0, 3, wide, glu, alpha, limit, inter, far(1), 1, far(2), far(3), None) == UNSUPPORTED
+            for src in range(4):
+                assert L.nf4moe_glu_backward(far(0), 1, src, far(1), far(2), 1, wide, glu, alpha, limit, inter, None, far(3),
+                                             far(4), None, None) == UNSUPPORTED
+        # the widest row is taken: without a device its launch fails
+        assert L.nf4moe_glu_forward(far(0), 1, 1, 1 << 30, glu, alpha, limit, inter, far(1), 0, None, None, None) == HIP
