@@ -548,7 +548,21 @@ def moe_forward(layer: MoELayer, x, return_routing: bool = False):
     return out, ids, w
 
 
-# fine-tuning and multi-adapter serving around the frozen 4-bit layer
-from .train import (CKPT_MXFP8, CKPT_MXINT8, GATE_IDENTITY, GATE_SIGMOID, GATE_TANH, AdapterPlan,  # noqa: E402
-                    Ckpt8, adapter_backward, adapter_forward, adapter_plan, block_norm_backward,
-                    block_norm_forward, ckpt8_dequantize, ckpt8_quantize, glu_backward, glu_forward)
+# Fine-tuning and multi-adapter serving around the frozen 4-bit layer: train.py's names,
+# loaded when one is first used, so that this package (and its build) imports without torch.
+_TRAIN = ("CKPT_MXFP8", "CKPT_MXINT8", "GATE_IDENTITY", "GATE_SIGMOID", "GATE_TANH", "AdapterPlan", "Ckpt8",
+          "adapter_backward", "adapter_forward", "adapter_plan", "block_norm_backward", "block_norm_forward",
+          "ckpt8_dequantize", "ckpt8_quantize", "glu_backward", "glu_forward")
+
+
+def __getattr__(name):
+    if name != "train" and name not in _TRAIN:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    train = importlib.import_module(".train", __name__)
+    globals().update({n: getattr(train, n) for n in _TRAIN})
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_TRAIN})

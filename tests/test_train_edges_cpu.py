@@ -33,3 +33,20 @@ def test_glu_refuses_rows_whose_columns_pass_32_bits(glu, alpha, limit):
                                              far(4), None, None) == UNSUPPORTED
         # the widest row is taken: without a device its launch fails
         assert L.nf4moe_glu_forward(far(0), 1, 1, 1 << 30, glu, alpha, limit, inter, far(1), 0, None, None, None) == HIP
+
+
+def test_package_imports_without_torch():
+    """Constants, the library's path and the build are there without torch, as before; the operators come with it."""
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(pkg.__file__)))
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import bit_quantized_moe_expert_amd as M, bit_quantized_moe_expert_amd.build as b\n"
+            "assert M.FMT_MXFP4 == 1 and M.LIB_PATH and b.sources() and 'adapter_forward' in dir(M)\n"
+            "assert not hasattr(M, 'no_such_name')\n")
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=120)
+    code = ("import sys, bit_quantized_moe_expert_amd as M\n"
+            "assert 'torch' not in sys.modules\n"
+            "from bit_quantized_moe_expert_amd import Ckpt8, adapter_forward\n"
+            "assert M.adapter_forward is adapter_forward is M.train.adapter_forward and M.CKPT_MXFP8 == 1\n")
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
