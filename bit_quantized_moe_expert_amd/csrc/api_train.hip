@@ -367,7 +367,8 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
     if (e == hipSuccess && dB) e = launch_fill_f32_zero(dB, (int64_t)ad->L * ad->rank * ad->N, s);
     return hip_status(e, "fill launch");
   }
-  if ((st = check_adapter_rows(R, x_rows, x_row_of, ids, plan, plan_bytes, ad->L, (int64_t)ad->K + ad->N, dA || dB)) != NF4MOE_OK) return st;
+  st = check_adapter_rows(R, dA ? x_rows : R, x_row_of, ids, plan, plan_bytes, ad->L, (int64_t)ad->K + ad->N, dA || dB);
+  if (st != NF4MOE_OK) return st;
   if (!dy || (dA && (!x || (held && !x_scale))) || (dB && !t)) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(dy, 2) || !aligned(x, held ? 1 : 2) || !aligned(t, 16) || !aligned(dx_base, dt_bytes(dx_dtype)) ||
       !aligned(dx, dt_bytes(dx_dtype)))

@@ -502,11 +502,11 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
  *   dA_l = sum_r u[r] x[x_row_of[r]]^T    fp32 [L, rank, K]
  *   dB_l = scale_l * sum_r dy[r] t[r]^T   fp32 [L, N, rank]
  * over the rows of adapter l, zeros for an adapter without rows; dx, dA and dB may
- * each be NULL. x is read for dA only: bf16, or an 8-bit checkpoint (x_src, with
- * x_scale; K % 32 == 0) decoded in registers. t is the forward's (for dB). The sums
- * over rows are added in a fixed order: the same bits on every run. dA and dB
- * 16-byte aligned. R == 0 writes zeros to dA and dB. Errors: INVALID_ARG,
- * WORKSPACE. */
+ * each be NULL. x (with x_rows) is read for dA only: bf16, or an 8-bit checkpoint
+ * (x_src, with x_scale; K % 32 == 0) decoded in registers. t is the forward's (for
+ * dB). The sums over rows are added in a fixed order: the same bits on every run. dA
+ * and dB 16-byte aligned. R == 0 writes zeros to dA and dB. Errors: INVALID_ARG,
+ * WORKSPACE, UNSUPPORTED where a launch would pass 2^32 threads. */
 nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint16_t *dy, nf4moe_src_t x_src, const void *x,
                                         const uint8_t *x_scale, int32_t x_rows, const int32_t *x_row_of, const float *t,
                                         const int32_t *ids, const void *plan, size_t plan_bytes, int32_t R,

@@ -50,3 +50,19 @@ def test_package_imports_without_torch():
             "from bit_quantized_moe_expert_amd import Ckpt8, adapter_forward\n"
             "assert M.adapter_forward is adapter_forward is M.train.adapter_forward and M.CKPT_MXFP8 == 1\n")
     subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
+
+
+def test_adapter_backward_without_dA_takes_no_x():
+    """x is read for dA only: dx and dB are made without its rows."""
+    from bit_quantized_moe_expert_amd import train
+    n = 100
+    desc = train._ADAPTERS.pack(4, 16, 64, 64, far(0), far(1), 0)
+    need = L.nf4moe_adapter_workspace_bytes(desc, n, 1)
+
+    def bwd(dA, ws_bytes, x=None, x_rows=0):
+        return L.nf4moe_adapter_backward(desc, far(2), 1, x, None, x_rows, None, far(3), far(4), None, 0, n, None, far(5), 1, dA,
+                                         far(6), far(7), ws_bytes, None)
+    assert bwd(None, need - 1) == WORKSPACE         # the next check after those of the rows
+    assert bwd(None, need - 1, x_rows=n - 1) == WORKSPACE
+    assert bwd(far(8), need, x=far(9), x_rows=n - 1) == INVALID
+    assert bwd(far(8), need, x=None, x_rows=n) == INVALID
