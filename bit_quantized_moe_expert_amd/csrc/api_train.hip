@@ -296,7 +296,7 @@ static nf4moe_status_t check_adapter_rows(int32_t R, int32_t x_rows, const int32
                                           const void *plan, size_t plan_bytes, int32_t L, int64_t cols, bool sums) {
   const int64_t tiles = cdiv(R, kAdTile) + (R < L + 1 && !sums ? R : L + 1), per = cdiv(cols, 128) + 1;
   if (tiles * (per < 8 ? 8 : per) >= 1 << 24)
-    return fail(NF4MOE_ERR_UNSUPPORTED, "R=%d rows of %d columns are too many for one call", R, cols);
+    return fail(NF4MOE_ERR_UNSUPPORTED, "R=%d rows of %lld columns are too many for one call", R, (long long)cols);
   if (x_rows < 1 || (!x_row_of && x_rows < R))
     return fail(NF4MOE_ERR_INVALID_ARG, "x_rows=%d too small for R=%d%s", x_rows, R, x_row_of ? "" : " without a gather");
   if (!ids) return fail(NF4MOE_ERR_INVALID_ARG, "ids is NULL");

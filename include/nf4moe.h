@@ -488,7 +488,8 @@ size_t nf4moe_adapter_workspace_bytes(const nf4moe_adapters_t *ad, int32_t R, in
  * t is summed in fp32 and enters the second product exactly; the output has one
  * rounding. R == 0 is a no-op. Calls that need no workspace (few rows for their
  * rank and widths) run in one launch and ignore the plan; results differ from the
- * grouped kernels' in summation order only. Errors: INVALID_ARG, WORKSPACE. */
+ * grouped kernels' in summation order only. Errors: INVALID_ARG, WORKSPACE,
+ * UNSUPPORTED where a launch would pass 2^32 threads. */
 nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16_t *x, int32_t x_rows,
                                        const int32_t *x_row_of, const int32_t *ids, const void *plan, size_t plan_bytes,
                                        int32_t R, const void *base, void *out, nf4moe_dtype_t dtype, float *t, void *ws,

@@ -66,3 +66,11 @@ def test_adapter_backward_without_dA_takes_no_x():
     assert bwd(None, need - 1, x_rows=n - 1) == WORKSPACE
     assert bwd(far(8), need, x=far(9), x_rows=n - 1) == INVALID
     assert bwd(far(8), need, x=None, x_rows=n) == INVALID
+
+
+def test_sources_compile_without_format_warnings():
+    """Error messages print each argument by its own type (printf formats, checked by the compiler)."""
+    import subprocess
+    from bit_quantized_moe_expert_amd import build
+    src = os.path.join(build.CSRC, "api_train.hip")
+    subprocess.run([build._hipcc(), *build.FLAGS, "--offload-host-only", "-Werror=format", "-fsyntax-only", src], check=True, timeout=300)
