@@ -3,6 +3,8 @@
 // is enqueued; on a non-OK status nothing was launched.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "../../include/nf4moe.h"
 #include "ckpt8.h"
 #include "internal.h"
@@ -17,11 +19,29 @@ bool dt_ok(int dt) { return dt == NF4MOE_DT_F32 || dt == NF4MOE_DT_BF16; }
 size_t dt_bytes(int dt) { return dt == NF4MOE_DT_BF16 ? 2 : 4; }
 bool ck_ok(int f) { return f == NF4MOE_CKPT_MXINT8 || f == NF4MOE_CKPT_MXFP8; }
 
-// Whether two arrays share a byte (absent ones share none).
-bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
-  const uint64_t p = (uint64_t)a, q = (uint64_t)b;
-  return p && q && na && nb && p < q + nb && q < p + na;
+// An array that a call writes or reads (absent: no address or no bytes).
+struct Span {
+  const char *name;
+  const void *p;
+  uint64_t n;
+};
+bool overlap(const Span &a, const Span &b) {
+  const uint64_t p = (uint64_t)a.p, q = (uint64_t)b.p;
+  return p && q && a.n && b.n && p < q + b.n && q < p + a.n;
 }
+
+// No output shares a byte with an input or with another output. An input that an output
+// may be is left out of `ins` by the caller where it is that very array (see but()).
+nf4moe_status_t check_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span *q = o + 1; q != outs.end(); ++q)
+      if (overlap(*o, *q)) return fail(NF4MOE_ERR_INVALID_ARG, "%s overlaps %s", o->name, q->name);
+    for (const Span &q : ins)
+      if (overlap(*o, q)) return fail(NF4MOE_ERR_INVALID_ARG, "%s overlaps %s", o->name, q.name);
+  }
+  return NF4MOE_OK;
+}
+Span but(Span in, const void *out) { return {in.name, in.p == out ? nullptr : in.p, in.n}; }
 
 nf4moe_status_t check_ckpt8(int32_t fmt, const void *dense, nf4moe_dtype_t dt, int64_t rows, int64_t K,
                             const void *codes, const void *scale) {
@@ -67,6 +87,12 @@ nf4moe_status_t check_norm(const nf4moe_block_norm_t *n, int64_t T) {
   if (!aligned(n->w_post, 4) || !aligned(n->w_pre, 4) || !aligned(n->gate, dt_bytes(n->gate_dtype)))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
   return NF4MOE_OK;
+}
+
+// Elements of a gate, and of its gradient.
+uint64_t gate_count(const nf4moe_block_norm_t &n, int64_t T) {
+  const uint64_t count[4] = {0, (uint64_t)n.H, (uint64_t)T, (uint64_t)T * n.H};
+  return count[n.gate_kind];
 }
 
 NormArgs norm_args(const nf4moe_block_norm_t &n, int64_t T) {
@@ -142,6 +168,9 @@ nf4moe_status_t nf4moe_ckpt8_quantize(nf4moe_ckpt8_t fmt, const void *x, nf4moe_
                                       uint8_t *codes, uint8_t *scale, void *stream) {
   const nf4moe_status_t st = check_ckpt8(fmt, x, x_dtype, rows, K, codes, scale);
   if (st != NF4MOE_OK || rows == 0) return st;
+  const uint64_t n = (uint64_t)rows * K;
+  const nf4moe_status_t apart = check_overlap({{"codes", codes, n}, {"scale", scale, n / 32}}, {{"x", x, n * dt_bytes(x_dtype)}});
+  if (apart != NF4MOE_OK) return apart;
   return hip_status(launch_ckpt8_quantize(fmt, x, x_dtype == NF4MOE_DT_BF16, rows * K, codes, scale, (hipStream_t)stream),
                     "checkpoint quantize launch");
 }
@@ -150,6 +179,9 @@ nf4moe_status_t nf4moe_ckpt8_dequantize(nf4moe_ckpt8_t fmt, const uint8_t *codes
                                         int64_t K, void *out, nf4moe_dtype_t out_dtype, void *stream) {
   const nf4moe_status_t st = check_ckpt8(fmt, out, out_dtype, rows, K, codes, scale);
   if (st != NF4MOE_OK || rows == 0) return st;
+  const uint64_t n = (uint64_t)rows * K;
+  const nf4moe_status_t apart = check_overlap({{"out", out, n * dt_bytes(out_dtype)}}, {{"codes", codes, n}, {"scale", scale, n / 32}});
+  if (apart != NF4MOE_OK) return apart;
   return hip_status(launch_ckpt8_dequantize(fmt, codes, scale, rows * K, out, out_dtype == NF4MOE_DT_BF16, (hipStream_t)stream),
                     "checkpoint dequantize launch");
 }
@@ -165,6 +197,10 @@ nf4moe_status_t nf4moe_glu_forward(const void *gu, nf4moe_dtype_t gu_dtype, int6
   if (R == 0) return NF4MOE_OK;
   if (!gu || !h) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(gu, dt_bytes(gu_dtype)) || !aligned(h, 2)) return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  const uint64_t n = (uint64_t)R * I;
+  const nf4moe_status_t apart = check_overlap({{"h", h, 2 * n}, {"codes", codes, 2 * n}, {"scale", scale, n / 16}},
+                                              {{"gu", gu, 2 * n * dt_bytes(gu_dtype)}});
+  if (apart != NF4MOE_OK) return apart;
   GluArgs a = {};
   a.R = R, a.I = I, a.glu = glu, a.inter = glu_interleaved, a.alpha = glu_alpha, a.limit = glu_limit;
   a.gu = gu, a.src = gu_dtype == NF4MOE_DT_BF16 ? SRC_BF16 : SRC_F32;
@@ -186,6 +222,12 @@ nf4moe_status_t nf4moe_glu_backward(const void *dh, nf4moe_dtype_t dh_dtype, nf4
   if (!aligned(dh, dt_bytes(dh_dtype)) || !aligned(gu, held ? 1 : gu_src == NF4MOE_SRC_F32 ? 4 : 2) || !aligned(dgu, 2) ||
       !aligned(h, 2) || !aligned(row_w, 4) || !aligned(drow_w, 4))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
+  const uint64_t n = (uint64_t)R * I;
+  const nf4moe_status_t apart = check_overlap(
+      {{"dgu", dgu, 4 * n}, {"h", h, 2 * n}, {"drow_w", drow_w, 4 * (uint64_t)R}},
+      {{"dh", dh, n * dt_bytes(dh_dtype)}, {"gu", gu, 2 * n * (held ? 1 : gu_src == NF4MOE_SRC_F32 ? 4 : 2)},
+       {"gu_scale", held ? gu_scale : nullptr, n / 16}, {"row_w", row_w, 4 * (uint64_t)R}});
+  if (apart != NF4MOE_OK) return apart;
   GluArgs a = {};
   a.R = R, a.I = I, a.glu = glu, a.inter = glu_interleaved, a.alpha = glu_alpha, a.limit = glu_limit;
   a.gu = gu, a.gu_scale = gu_scale, a.src = gu_src;
@@ -208,9 +250,13 @@ nf4moe_status_t nf4moe_block_norm_forward(const nf4moe_block_norm_t *norm, const
   if (!aligned(x, dt_bytes(n.x_dtype)) || !aligned(x_new, dt_bytes(n.x_dtype)) || !aligned(f, 2) || !aligned(y, 2) ||
       !aligned(rstd_post, 4) || !aligned(rstd_pre, 4))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
-  const uint64_t bytes = (uint64_t)T * n.H * dt_bytes(n.x_dtype);
-  if (f && ((x_new != x && overlap(x_new, bytes, x, bytes)) || overlap(x_new, bytes, f, (uint64_t)T * n.H * 2)))
-    return fail(NF4MOE_ERR_INVALID_ARG, "x_new overlaps an input (it may only be x itself)");
+  const uint64_t rows = (uint64_t)T, cells = rows * n.H, xb = cells * dt_bytes(n.x_dtype), wb = 4 * (uint64_t)n.H;
+  const nf4moe_status_t apart = check_overlap(
+      {{"x_new", f ? x_new : nullptr, xb}, {"y", n.w_pre ? y : nullptr, 2 * cells},
+       {"rstd_post", n.w_post ? rstd_post : nullptr, 4 * rows}, {"rstd_pre", n.w_pre ? rstd_pre : nullptr, 4 * rows}},
+      {but({"x", x, xb}, f ? x_new : nullptr), {"f", f, 2 * cells}, {"w_post", n.w_post, wb}, {"w_pre", n.w_pre, wb},
+       {"gate", n.gate, gate_count(n, T) * dt_bytes(n.gate_dtype)}});
+  if (apart != NF4MOE_OK) return apart;
   NormArgs a = norm_args(n, T);
   a.x = x, a.f = f, a.x_new = x_new, a.y = y, a.rstd_post = rstd_post, a.rstd_pre = rstd_pre;
   return hip_status(launch_norm_forward(a, (hipStream_t)stream), "norm launch");
@@ -254,6 +300,15 @@ nf4moe_status_t nf4moe_block_norm_backward(const nf4moe_block_norm_t *norm, cons
   const size_t need = nf4moe_block_norm_workspace_bytes(n.H, T);
   if (!ws || ws_bytes < need) return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need);
   if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const uint64_t rows = (uint64_t)T, cells = rows * n.H, xb = cells * xa, wb = 4 * (uint64_t)n.H;
+  const nf4moe_status_t apart = check_overlap(
+      {{"dx", dx, xb}, {"df", f ? df : nullptr, 2 * cells}, {"dgate", n.gate ? dgate : nullptr, 4 * gate_count(n, T)},
+       {"dw_post", n.w_post ? dw_post : nullptr, wb}, {"dw_pre", n.w_pre ? dw_pre : nullptr, wb}, {"workspace", ws, need}},
+      {{"dx_new", dx_new, xb}, {"dy", n.w_pre ? dy : nullptr, 2 * cells}, {"x_new", n.w_pre ? x_new : nullptr, xb},
+       {"f", f, 2 * cells}, {"rstd_post", n.w_post ? rstd_post : nullptr, 4 * rows},
+       {"rstd_pre", n.w_pre ? rstd_pre : nullptr, 4 * rows}, {"w_post", n.w_post, wb}, {"w_pre", n.w_pre, wb},
+       {"gate", n.gate, gate_count(n, T) * dt_bytes(n.gate_dtype)}});
+  if (apart != NF4MOE_OK) return apart;
   NormArgs a = norm_args(n, T);
   a.x = x_new, a.f = f, a.rstd_post = const_cast<float *>(rstd_post), a.rstd_pre = const_cast<float *>(rstd_pre);
   a.dx_new = dx_new, a.dy = dy, a.dx = dx, a.df = df, a.dgate = dgate;
@@ -276,6 +331,8 @@ nf4moe_status_t nf4moe_adapter_plan(const int32_t *ids, int32_t R, int32_t L, vo
   const size_t need = nf4moe_adapter_plan_bytes(R, L);
   if (!plan || plan_bytes < need) return fail(NF4MOE_ERR_WORKSPACE, "plan %zu bytes < %zu required", plan_bytes, need);
   if (!aligned(plan, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "plan must be 256-byte aligned");
+  const nf4moe_status_t apart = check_overlap({{"plan", plan, need}}, {{"ids", ids, 4 * (uint64_t)R}});
+  if (apart != NF4MOE_OK) return apart;
   AdapterPlan p;
   adapter_plan_layout(R, L, plan, &p);
   return hip_status(launch_adapter_prepare({p, ids, R, L, 0, 0, 0, nullptr, nullptr, nullptr, nullptr}, (hipStream_t)stream), "adapter plan launch");
@@ -324,14 +381,17 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   hipStream_t s = (hipStream_t)stream;
   const bool bf = dtype == NF4MOE_DT_BF16;
   const bool one_launch = adapter_rows_supported(R, ad->K, ad->N, ad->rank);
+  const size_t need = one_launch ? 0 : carve_adapter(nullptr, *ad, R, false).bytes;
   if (!one_launch) {
-    const size_t need = carve_adapter(nullptr, *ad, R, false).bytes;
     if (!ws || ws_bytes < need) return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need);
     if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   }
-  const uint64_t ob = (uint64_t)R * ad->N * dt_bytes(dtype);
-  if (overlap(out, ob, x, (uint64_t)x_rows * ad->K * 2) || (out != base && overlap(out, ob, base, ob)))
-    return fail(NF4MOE_ERR_INVALID_ARG, "out overlaps x or base (it may only be base itself)");
+  const uint64_t rows = (uint64_t)R, ob = rows * ad->N * dt_bytes(dtype), lr = (uint64_t)ad->L * ad->rank * 2;
+  st = check_overlap({{"out", out, ob}, {"t", t, 4 * rows * ad->rank}, {"workspace", ws, need}},
+                     {{"x", x, (uint64_t)x_rows * ad->K * 2}, {"x_row_of", x_row_of, 4 * rows}, {"ids", ids, 4 * rows},
+                      {"plan", plan, plan_bytes}, but({"base", base, ob}, out), {"A", ad->A, lr * ad->K}, {"B", ad->B, lr * ad->N},
+                      {"scale", ad->scale, 4 * (uint64_t)ad->L}});
+  if (st != NF4MOE_OK) return st;
   if (one_launch) {
     AdapterRowsArgs a = {x, x_row_of, ids, x_rows, R, ad->L, ad->K, ad->N, ad->rank, ad->A, ad->B, ad->scale, base, out, bf, t};
     return hip_status(launch_adapter_rows(a, s), "adapter launch");
@@ -377,11 +437,16 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
   if (!ws || ws_bytes < need.bytes)
     return fail(NF4MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", ws_bytes, need.bytes);
   if (!aligned(ws, 256)) return fail(NF4MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  const uint64_t xb = (uint64_t)R * ad->K * dt_bytes(dx_dtype);
-  if (overlap(dx, xb, dy, (uint64_t)R * ad->N * 2) || (dx != dx_base && overlap(dx, xb, dx_base, xb)) ||
-      (dA && overlap(dx, xb, x, (uint64_t)x_rows * ad->K * (held ? 1 : 2))))
-    return fail(NF4MOE_ERR_INVALID_ARG, "dx overlaps dy, x or dx_base (it may only be dx_base itself)");
   if (!dx && !dA && !dB) return NF4MOE_OK;
+  const uint64_t rows = (uint64_t)R, xb = rows * ad->K * dt_bytes(dx_dtype), lr = (uint64_t)ad->L * ad->rank * 2;
+  const uint64_t held_x = dA ? (uint64_t)x_rows * ad->K : 0;
+  st = check_overlap({{"dx", dx, xb}, {"dA", dA, 2 * lr * ad->K}, {"dB", dB, 2 * lr * ad->N}, {"workspace", ws, need.bytes}},
+                     {{"dy", dy, 2 * rows * ad->N}, {"x", x, held ? held_x : 2 * held_x},
+                      {"x_scale", held ? x_scale : nullptr, held_x / 32}, {"x_row_of", x_row_of, 4 * rows},
+                      {"t", dB ? t : nullptr, 4 * rows * ad->rank}, {"ids", ids, 4 * rows}, {"plan", plan, plan_bytes},
+                      but({"dx_base", dx ? dx_base : nullptr, xb}, dx), {"A", ad->A, lr * ad->K}, {"B", ad->B, lr * ad->N},
+                      {"scale", ad->scale, 4 * (uint64_t)ad->L}});
+  if (st != NF4MOE_OK) return st;
   const AdapterCarve c = carve_adapter(ws, *ad, R, true);
   AdapterPlan p;
   adapter_plan_layout(R, ad->L, plan ? const_cast<void *>(plan) : c.plan, &p);

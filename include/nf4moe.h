@@ -334,8 +334,8 @@ nf4moe_status_t nf4moe_moe_forward_profiled(const nf4moe_layer_t *layer, const u
  * Fine-tuning and multi-adapter serving around the frozen 4-bit layer. These
  * calls follow the same conventions (caller-owned device memory, checks before
  * anything is enqueued, one stream, no host synchronisation, capturable). An
- * output overlaps neither an input nor another output, except where a call says
- * that it may be one.
+ * output (or workspace) overlaps neither an input nor another output, except where
+ * a call says that it may be one: INVALID_ARG otherwise.
  *
  * 8-bit activation checkpoints. A tensor [rows, K] kept for the backward pass as
  * one byte per value and one e8m0 scale byte b per 32 consecutive k (multiplier

@@ -74,3 +74,104 @@ def test_sources_compile_without_format_warnings():
     from bit_quantized_moe_expert_amd import build
     src = os.path.join(build.CSRC, "api_train.hip")
     subprocess.run([build._hipcc(), *build.FLAGS, "--offload-host-only", "-Werror=format", "-fsyntax-only", src], check=True, timeout=300)
+
+
+# ------------------------------------------------------------------ arrays that share bytes
+def overlaps_refused(call, outs, ins, may_be=(), base=None):
+    """Every output laid over each input and each other output, by its last and its first
+    element: INVALID_ARG. may_be: (output, input) pairs that may be one array, not two in part."""
+    at = {n: far(i) for i, n in enumerate({**outs, **ins})}
+    size = {**outs, **ins}
+
+    def status(**over):
+        return call(**{**at, **over})
+    for o in outs:
+        for other in size:
+            if other == o or (other in outs and list(outs).index(other) < list(outs).index(o)):
+                continue
+            for shift in (size[other] - 256, 256 - size[o], 0):
+                if shift % 256 or (shift == 0 and (o, other) in may_be):
+                    continue
+                if shift and not -size[o] < shift < size[other]:
+                    continue
+                assert status(**{o: at[other] + shift}) == INVALID, (o, other, shift)
+                msg = L.nf4moe_last_error().decode()
+                assert "overlaps" in msg and o in msg.split() and other in msg.split(), msg
+    for o, other in may_be:
+        if not torch.cuda.is_available():
+            assert status(**{o: at[other]}) == HIP, (o, other)      # every check passed: no device to run on
+    if not torch.cuda.is_available():
+        assert status() == HIP
+        # side by side is not over one another
+        o, i = next(iter(outs)), next(iter(ins))
+        assert status(**{o: at[i] + size[i]}) == HIP and status(**{o: at[i] - size[o]}) == HIP
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_ckpt8_refuses_overlapping_outputs(fmt, dt):
+    rows, K = 64, 1024
+    dense, n = rows * K * (4 if dt == 0 else 2), rows * K
+    overlaps_refused(lambda x, codes, scale: L.nf4moe_ckpt8_quantize(fmt, x, dt, rows, K, codes, scale, None),
+                     dict(codes=n, scale=n // 32), dict(x=dense))
+    overlaps_refused(lambda out, codes, scale: L.nf4moe_ckpt8_dequantize(fmt, codes, scale, rows, K, out, dt, None),
+                     dict(out=dense), dict(codes=n, scale=n // 32))
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+def test_glu_refuses_overlapping_outputs(dt):
+    R, I = 256, 1024
+    e, n = (4 if dt == 0 else 2), 256 * 1024
+    overlaps_refused(lambda gu, h, codes, scale: L.nf4moe_glu_forward(gu, dt, R, I, 0, 0.0, 0.0, 0, h, 0, codes, scale, None),
+                     dict(h=2 * n, codes=2 * n, scale=n // 16), dict(gu=2 * n * e))
+    for src, width in ((0, 4), (1, 2), (2, 1), (3, 1)):
+        ins = dict(dh=n * e, gu=2 * n * width, row_w=4 * R, **(dict(gu_scale=n // 16) if src > 1 else {}))
+        overlaps_refused(lambda dh, gu, row_w, dgu, h, drow_w, gu_scale=None: L.nf4moe_glu_backward(  # noqa: E731
+            dh, dt, src, gu, gu_scale, R, I, 0, 0.0, 0.0, 0, row_w, dgu, h, drow_w, None),
+            dict(dgu=4 * n, h=2 * n, drow_w=4 * R), ins)
+
+
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("kind", [1, 2, 3])
+def test_block_norm_refuses_overlapping_arrays(dt, kind):
+    from bit_quantized_moe_expert_amd import train
+    T, H = 256, 1024
+    xb, hb, gate = T * H * (4 if dt == 0 else 2), T * H * 2, 4 * (0, H, T, T * H)[kind]
+
+    def desc(w_post, w_pre, g):
+        return train._BLOCK_NORM.pack(H, dt, w_post, w_pre, g, kind, 0, 0, 1.0, 1e-6)
+    w = dict(w_post=4 * H, w_pre=4 * H, gate=gate)
+    overlaps_refused(lambda x, f, w_post, w_pre, gate, x_new, y, rstd_post, rstd_pre: L.nf4moe_block_norm_forward(
+        desc(w_post, w_pre, gate), x, f, T, x_new, y, rstd_post, rstd_pre, None),
+        dict(x_new=xb, y=hb, rstd_post=4 * T, rstd_pre=4 * T), dict(x=xb, f=hb, **w), may_be=[("x_new", "x")])
+    need = L.nf4moe_block_norm_workspace_bytes(H, T)
+    overlaps_refused(lambda dx_new, dy, x_new, f, rstd_post, rstd_pre, w_post, w_pre, gate, dx, df, dgate, dw_post, dw_pre, workspace:
+                     L.nf4moe_block_norm_backward(desc(w_post, w_pre, gate), dx_new, dy, x_new, f, rstd_post, rstd_pre, T, dx, df,
+                                                  dgate, dw_post, dw_pre, workspace, need, None),
+                     dict(dx=xb, df=hb, dgate=gate, dw_post=4 * H, dw_pre=4 * H, workspace=need),
+                     dict(dx_new=xb, dy=hb, x_new=xb, f=hb, rstd_post=4 * T, rstd_pre=4 * T, **w))
+
+
+@pytest.mark.parametrize("R", [256, 65536])         # the one-launch form and the grouped kernels
+@pytest.mark.parametrize("dt", [0, 1])
+def test_adapters_refuse_overlapping_arrays(R, dt):
+    from bit_quantized_moe_expert_amd import train
+    Ln, rank, K, N, T = 64, 16, 128, 256, 128
+    e = 4 if dt == 0 else 2
+    d = lambda A, B, scale: train._ADAPTERS.pack(Ln, rank, K, N, A, B, scale)  # noqa: E731
+    w = dict(A=2 * Ln * rank * K, B=2 * Ln * rank * N, scale=4 * Ln)
+    pb = L.nf4moe_adapter_plan_bytes(R, Ln)
+    wf, wb = (L.nf4moe_adapter_workspace_bytes(d(far(0), far(1), 0), R, k) for k in (0, 1))
+    overlaps_refused(lambda ids, plan: L.nf4moe_adapter_plan(ids, R, Ln, plan, pb, None), dict(plan=pb), dict(ids=4 * R))
+    outs = dict(out=R * N * e, t=4 * R * rank, **(dict(workspace=wf) if wf else {}))
+    overlaps_refused(lambda x, x_row_of, ids, plan, base, A, B, scale, out, t, workspace=None: L.nf4moe_adapter_forward(
+        d(A, B, scale), x, T, x_row_of, ids, plan, pb, R, base, out, dt, t, workspace, wf, None),
+        outs, dict(x=2 * T * K, x_row_of=4 * R, ids=4 * R, plan=pb, base=R * N * e, **w), may_be=[("out", "base")])
+    for src, width in ((1, 2), (2, 1)):
+        more = dict(x_scale=T * K // 32) if src == 2 else {}
+        overlaps_refused(lambda dy, x, x_row_of, t, ids, plan, dx_base, A, B, scale, dx, dA, dB, workspace, x_scale=None:
+                         L.nf4moe_adapter_backward(d(A, B, scale), dy, src, x, x_scale, T, x_row_of, t, ids, plan, pb, R, dx_base, dx,
+                                                   dt, dA, dB, workspace, wb, None),
+                         dict(dx=R * K * e, dA=4 * Ln * rank * K, dB=4 * Ln * rank * N, workspace=wb),
+                         dict(dy=2 * R * N, x=width * T * K, x_row_of=4 * R, t=4 * R * rank, ids=4 * R, plan=pb,
+                              dx_base=R * K * e, **more, **w), may_be=[("dx", "dx_base")])
