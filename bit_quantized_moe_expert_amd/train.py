@@ -229,11 +229,8 @@ def _norm_struct(x, f, w_post, w_pre, gate, gate_fn, alpha, eps):
         gdt = _dt(gate, "gate")
         gp = _arg(gate, "gate", gate.shape, gate.dtype, i)
     fp = _arg(f, "f", x.shape, _BF16, i)
-    wp, wr = _arg(w_post, "w_post", (H,), _F32, i) or 0, _arg(w_pre, "w_pre", (H,), _F32, i) or 0
-    try:
-        st = _BLOCK_NORM.pack(_i32(H, "H"), dt, wp, wr, gp or 0, kind, gdt, _i32(gate_fn, "gate_fn"), alpha, eps)
-    except OverflowError:
-        raise ValueError(f"alpha={alpha} and eps={eps} must fit 32-bit floats") from None
+    st = _BLOCK_NORM.pack(_i32(H, "H"), dt, _arg(w_post, "w_post", (H,), _F32, i) or 0, _arg(w_pre, "w_pre", (H,), _F32, i) or 0,
+                          gp or 0, kind, gdt, _i32(gate_fn, "gate_fn"), alpha, eps)
     return st, _arg(x, "x", x.shape, x.dtype, i), fp, T, H, i
 
 

@@ -175,14 +175,3 @@ def test_adapters_refuse_overlapping_arrays(R, dt):
                          dict(dx=R * K * e, dA=4 * Ln * rank * K, dB=4 * Ln * rank * N, workspace=wb),
                          dict(dy=2 * R * N, x=width * T * K, x_row_of=4 * R, t=4 * R * rank, ids=4 * R, plan=pb,
                               dx_base=R * K * e, **more, **w), may_be=[("dx", "dx_base")])
-
-
-# ------------------------------------------------------------------ the binding's own refusals
-@pytest.mark.parametrize("kw", [dict(alpha=1e39), dict(alpha=-1e39), dict(eps=1e60)])
-def test_block_norm_refuses_scales_past_32_bit_floats(kw):
-    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.ones(64)
-    with pytest.raises(ValueError, match="32"):
-        pkg.block_norm_forward(x, x.clone(), w_pre=w, **kw)
-    if "alpha" in kw:
-        with pytest.raises(ValueError, match="32"):
-            pkg.block_norm_backward(x, x, x, x, w_pre=w, rstd_pre=torch.ones(4), **kw)
