@@ -788,7 +788,7 @@ __device__ inline void rowgrad_body(const RowGradOne &p, const int4 chunk, int c
   }
   const int64_t size = (int64_t)rank * p.C;
   float *out = chunk.w < 0 ? p.out + l * size : p.partial + chunk.w * size;
-  const float m = p.scale ? p.scale[l] : 1.0f;
+  const float m = p.scale && n > 0 ? p.scale[l] : 1.0f;  // no rows: zeros, whatever an unused slot's scale holds
   const int cols = min(kGradCols, p.C - cw), ranks = min(16 * RT, rank - j0);  // multiples of 8
   if (p.transposed) {
     const int r4 = ranks / 4;
