@@ -647,6 +647,11 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
             for (int j = 0; j < 8; ++j) acc[s][j] = mfma16(w[j], t[part][s], acc[s][j]);
       }
     }
+  } else {  // base's bits: x + -0 is x, where x + 0 turns a -0 into 0
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[s][j] = {-0.0f, -0.0f, -0.0f, -0.0f};
   }
 #pragma unroll
   for (int s = 0; s < S; ++s) {

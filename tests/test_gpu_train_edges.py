@@ -47,3 +47,27 @@ def test_gradients_of_an_adapter_without_rows_are_zero(Rn, rank, src, bad):
     for l in unused:
         assert torch.count_nonzero(got["dA"][l]) == 0 and torch.count_nonzero(got["dB"][l]) == 0
     assert torch.equal(M.adapter_forward(x, A, B, ids, scale=wild), M.adapter_forward(x, A, B, ids, scale=scale))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Rn,rank", [(9, 8), (30000, 8), (30000, 16), (12000, 24), (12000, 72)])
+def test_rows_without_an_adapter_take_base_as_it_is(Rn, rank, dtype):
+    """Its bits: a negative zero keeps its sign, in the one-launch form (9 rows) and in the grouped kernels."""
+    g = torch.Generator(device=DEV).manual_seed(Rn + rank)
+    Ln, K, N = 3, 520, 264
+    ids = torch.randint(-2, Ln + 2, (Rn,), generator=g, device=DEV).int()
+    ids[:3] = torch.tensor([-1, 0, Ln], device=DEV)
+    x = torch.randn(Rn, K, generator=g, device=DEV).to(BF16)
+    A = torch.randn(Ln, rank, K, generator=g, device=DEV).to(BF16)
+    B = torch.randn(Ln, N, rank, generator=g, device=DEV).to(BF16)
+    base = torch.randn(Rn, N, generator=g, device=DEV)
+    fi = torch.finfo(dtype)
+    base[:, :6] = torch.tensor([-0.0, 0.0, float("inf"), float("-inf"), fi.max, fi.tiny / 4], device=DEV)
+    base = base.to(dtype)
+    none = (ids < 0) | (ids >= Ln)
+    word = torch.int16 if dtype is BF16 else torch.int32
+    out = M.adapter_forward(x, A, B, ids, base=base)
+    assert torch.equal(out[none].view(word), base[none].view(word))
+    dx_base = base.repeat(1, 2)[:, :K].contiguous()
+    back = M.adapter_backward(torch.ones(Rn, N, device=DEV, dtype=BF16), None, None, A, B, ids, dx_base=dx_base, need=("dx",))
+    assert torch.equal(back["dx"][none].view(word), dx_base[none].view(word))
