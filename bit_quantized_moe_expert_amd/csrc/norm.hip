@@ -120,13 +120,21 @@ __device__ inline void store_row8(void *p, int64_t base, int i, int H, const flo
   }
 }
 
-// The gate's factor phi and its slope. tanh by the library function: 1 - 2 / (1 +
-// exp(2 v)) loses the small values, where a tanh gate starts.
+// The gate's factor phi and its slope at gate value v. tanh by the library function: 1 - 2 /
+// (1 + exp(2 v)) loses the small values, where a tanh gate starts. The slopes from v, not from
+// phi: where the gate saturates, 1 - phi (1 - phi^2) has lost its bits (sigma's was 0 from v = 17,
+// tanh's from |v| = 9 and 6 % off at 8). With e = exp(-|v|) (exp(-2 |v|)) they are e / (1 + e)^2
+// (four times that), which lose none.
 __device__ inline float gate_phi(int fn, float v) {
   if (fn == 1) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
   return fn == 2 ? tanhf(v) : v;
 }
-__device__ inline float gate_slope(int fn, float phi) { return fn == 1 ? phi * (1.0f - phi) : fn == 2 ? 1.0f - phi * phi : 1.0f; }
+__device__ inline float gate_slope(int fn, float v) {
+  if (fn == 0) return 1.0f;
+  const float e = __builtin_amdgcn_exp2f(fabsf(v) * (fn == 1 ? -1.44269504088896341f : -2.88539008177792681f));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  return (fn == 1 ? e : 4.0f * e) * r * r;
+}
 
 // phi of 8 gate values; the function is chosen once, outside the loop over them.
 __device__ inline void gate_phi8(int fn, const float (&v)[8], float (&phi)[8]) {
@@ -390,7 +398,8 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
     if (p.f) {
       // f becomes n_f (or stays f), g becomes the gradient of n_f up to the factor m
       const float rs = p.w_post ? (live ? p.rstd_post[row] : 0.0f) : 1.0f;
-      const float phi = p.gate_kind == 2 ? gate_phi(p.gate_fn, gate_scalar(p, live ? row : 0)) : 1.0f;
+      const float rg = p.gate_kind == 2 ? gate_scalar(p, live ? row : 0) : 0.0f;
+      const float phi = p.gate_kind == 2 ? gate_phi(p.gate_fn, rg) : 1.0f;
       const float m = p.alpha * phi;
       float f[NC][8];
       float s[1] = {0.0f};
@@ -405,11 +414,11 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[c][j] *= rs;
           if (p.gate_kind == 3) {
-            float v[8], q[8], dg[8];
-            gate_row8<ODD>(p, base, i, v);
-            gate_phi8(p.gate_fn, v, q);
+            float q[8], dg[8];
+            gate_row8<ODD>(p, base, i, q);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dg[j] = p.alpha * gate_slope(p.gate_fn, q[j]) * g[c][j] * f[c][j] * w[j];
+            for (int j = 0; j < 8; ++j) dg[j] = gate_slope(p.gate_fn, q[j]) * (p.alpha * g[c][j] * f[c][j] * w[j]);
+            gate_phi8(p.gate_fn, q, q);
             if (live) store_row8<false, ODD>(p.dgate, base, i, H, dg);
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[c][j] *= q[j];
@@ -424,7 +433,7 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
         }
       }
       row_sum<TPR, 1>(s, red[turn] + 16);
-      if (p.gate_kind == 2 && t == 0 && live) p.dgate[row] = p.alpha * s[0] * gate_slope(p.gate_fn, phi);
+      if (p.gate_kind == 2 && t == 0 && live) p.dgate[row] = p.alpha * s[0] * gate_slope(p.gate_fn, rg);
       const float mean = p.w_post ? s[0] * invH : 0.0f, mr = m * rs;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -483,8 +492,9 @@ __global__ __launch_bounds__(1024) void k_norm_colsum(NormArgs p) {
   s *= p.alpha;
   float phi = 1.0f;
   if (p.gate_kind == 1) {
-    phi = gate_phi(p.gate_fn, gate_scalar(p, col));
-    p.dgate[col] = gate_slope(p.gate_fn, phi) * (p.w_post ? p.w_post[col] * s : s);
+    const float v = gate_scalar(p, col);
+    phi = gate_phi(p.gate_fn, v);
+    p.dgate[col] = gate_slope(p.gate_fn, v) * (p.w_post ? p.w_post[col] * s : s);
   }
   if (p.dw_post) p.dw_post[col] = phi * s;
 }

@@ -71,3 +71,77 @@ def test_rows_without_an_adapter_take_base_as_it_is(Rn, rank, dtype):
     dx_base = base.repeat(1, 2)[:, :K].contiguous()
     back = M.adapter_backward(torch.ones(Rn, N, device=DEV, dtype=BF16), None, None, A, B, ids, dx_base=dx_base, need=("dx",))
     assert torch.equal(back["dx"][none].view(word), dx_base[none].view(word))
+
+
+# ------------------------------------------------------------------ gates on their tails
+TAILS = [0.0, 0.5, 2.5, 4.0, 6.0, 8.0, 10.0, 14.0, 17.0, 20.0, 40.0, 60.0, 80.0, 100.0, float("inf")]
+TAILS = np.array(TAILS + [-v for v in TAILS])
+
+
+def tail_phi(v, fn):
+    """phi and its slope in 64 bits without cancellation: sigma(v), sigma(v) sigma(-v); tanh(v), 4 sigma(2 v) sigma(-2 v)."""
+    s = R._sigma
+    return (s(v), s(v) * s(-v)) if fn == 1 else (np.tanh(v), 4 * s(2 * v) * s(-2 * v))
+
+
+def tail_error(v, fn):
+    """Relative error of phi, and of the slope, evaluated in fp32: a sigma of argument a is within (|a| + 8) 2^-23 of
+    itself (the exponent's argument is rounded, |a| 1.5 U, then exp2, one addition and a reciprocal, 5 U), the library's
+    tanh within 2 units in the last place; a slope is two sigmas and their product."""
+    a = np.minimum(np.abs(v) * (1 if fn == 1 else 2), 200.0)
+    return (a + 8) * 2 * U if fn == 1 else np.full_like(a, 4 * U), 2 * (a + 8) * 2 * U + 2 * U
+
+
+@pytest.mark.parametrize("fn", [M.GATE_SIGMOID, M.GATE_TANH])
+@pytest.mark.parametrize("kind", ["channel", "row", "full"])
+@pytest.mark.parametrize("post", [False, True])
+def test_gates_on_their_tails(fn, kind, post):
+    """x' and dgate where the gate saturates: phi to its last bits, and a slope that falls like exp(-|v|) (exp(-2 |v|)), not 0.
+
+    x = 0 and no pre norm, so x' = alpha phi z, and g = dx' as it is given. Below 2^-126 the hardware's exp2 and
+    reciprocal may give 0: 2^-126 of a sigma, 4 of them in tanh's slope, is allowed on top of the relative error."""
+    n = len(TAILS)
+    T, H = (n, 9) if kind == "row" else (5, 2 * n)
+    g = torch.Generator(device=DEV).manual_seed(7 * fn + post)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    v = dict(channel=np.tile(TAILS, 2), row=TAILS[:, None], full=np.tile(TAILS, (5, 2)))[kind]
+    gate = torch.from_numpy(v.astype(np.float32)).to(DEV)
+    x, f, dx = torch.zeros(T, H, device=DEV), rn(T, H).to(BF16), rn(T, H)
+    w_post = 1 + 0.2 * rn(H) if post else None
+    kw = dict(w_post=w_post, gate=gate, gate_fn=fn, alpha=0.625)
+    got = M.block_norm_forward(x, f, eps=1e-6, **kw)
+    back = M.block_norm_backward(dx, None, got["x"], f, rstd_post=got["rstd_post"], **kw)
+    v = to_np(gate)
+    phi, slope = tail_phi(v, fn)
+    ep, es = tail_error(v, fn)
+    z = to_np(f)
+    if post:
+        z = z * to_np(got["rstd_post"])[:, None] * to_np(w_post)
+    tiny = 2.0 ** -123
+    # two products of z (rstd, w_post), then phi and alpha: 4 U more
+    R.within(to_np(got["x"]), 0.625 * phi * z, 0.625 * np.abs(z) * (np.abs(phi) * (ep + 6 * U) + tiny), "x'")
+    term = 0.625 * to_np(dx) * z
+    ref, mag = slope * term, np.abs(slope * term) * (es + 8 * U) + np.abs(term) * tiny
+    if kind != "full":
+        axis = 0 if kind == "channel" else 1
+        keep = axis == 1
+        # the terms' sum in fp32: H = 9 or T = 5 of them, the lanes, slots and workgroups that hold none add zeros
+        ref, mag = ref.sum(axis, keepdims=keep), mag.sum(axis, keepdims=keep) + 16 * U * np.abs(slope * term).sum(axis, keepdims=keep)
+    R.within(to_np(back["dgate"]), ref, mag, "dgate")
+    if fn == M.GATE_TANH:                       # not lost: the slope at 10 is 8.2e-9
+        at = back["dgate"].cpu().numpy()[..., 6:7] if kind != "row" else back["dgate"].cpu().numpy()[6:7]
+        assert np.all(at != 0)
+
+
+def test_a_gate_that_is_not_a_number_stays_its_own():
+    T, H = 4, 24
+    f, dx = torch.randn(T, H, device=DEV).to(BF16), torch.randn(T, H, device=DEV)
+    for fn in (M.GATE_IDENTITY, M.GATE_SIGMOID, M.GATE_TANH):
+        gate = torch.randn(T, H, device=DEV)
+        gate[2, 5] = float("nan")
+        out = M.block_norm_forward(torch.zeros(T, H, device=DEV), f, gate=gate, gate_fn=fn)
+        back = M.block_norm_backward(dx, None, out["x"], f, gate=gate, gate_fn=fn)
+        one = torch.zeros(T, H, dtype=torch.bool, device=DEV)
+        one[2, 5] = True
+        assert torch.equal(torch.isnan(out["x"]), one) and torch.equal(torch.isnan(back["df"]), one)
+        assert torch.equal(torch.isnan(back["dgate"]), one if fn else torch.zeros_like(one))
