@@ -145,3 +145,28 @@ def test_a_gate_that_is_not_a_number_stays_its_own():
         one[2, 5] = True
         assert torch.equal(torch.isnan(out["x"]), one) and torch.equal(torch.isnan(back["df"]), one)
         assert torch.equal(torch.isnan(back["dgate"]), one if fn else torch.zeros_like(one))
+
+
+# ------------------------------------------------------------------ the widest rows of the gated activation
+@pytest.mark.parametrize("inter", [0, 1])
+def test_the_widest_row_of_the_gated_activation(inter):
+    """2^30 pairs in one row, a pattern of 2^16 repeated: every repeat gives what a row of one repeat gives."""
+    P, n = 1 << 16, 1 << 14
+    g = torch.Generator(device=DEV).manual_seed(3)
+    gu1, dh1 = torch.randn(1, 2 * P, generator=g, device=DEV).to(BF16), torch.randn(1, P, generator=g, device=DEV).to(BF16)
+    h1, ck1 = M.glu_forward(gu1, interleaved=inter, ckpt=M.CKPT_MXFP8)
+    b1 = M.glu_backward(dh1, ck1, interleaved=inter)
+    gu = gu1.repeat(1, n) if inter else torch.cat([gu1[:, :P].repeat(1, n), gu1[:, P:].repeat(1, n)], 1)
+    h, ck = M.glu_forward(gu, interleaved=inter, ckpt=M.CKPT_MXFP8)
+    del gu
+
+    def same(wide, one, halves):
+        if halves and not inter:            # gate columns, then up columns
+            k = one.shape[1] // 2
+            w = wide.view(2, n, k)
+            return all(bool((w[i] == one[0, i * k:(i + 1) * k]).all()) for i in range(2))
+        return bool((wide.view(n, -1) == one).all())
+    assert same(h, h1, False) and same(ck.codes, ck1.codes, True) and same(ck.scale, ck1.scale, True)
+    del h
+    b = M.glu_backward(dh1.repeat(1, n), ck, interleaved=inter)
+    assert same(b["dgu"], b1["dgu"], True) and same(b["h"], b1["h"], False)
