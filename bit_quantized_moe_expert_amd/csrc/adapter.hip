@@ -160,8 +160,8 @@ __device__ inline int4 block_prefix4(int4 v, int4 *wsum, int4 *sum) {
 // barriers, 6 to 10 us up to 32768 rows of 64 adapters, not by bytes.
 //
 // The counters come from k_plan_hist, or for few rows every workgroup counts all of them
-// itself. Workgroups behind these turn the backward's weights, which nothing waits for. us, two launches
-// against one: 4099 rows of 6 adapters 2.4 + 5.9 / 7.8, 8192 of 64 2.4 + 10.2 / 12.7,
+// itself. Workgroups behind these turn the backward's weights, those of all L adapters,
+// beside the grouping; the next launch waits for both. us, two launches against one: 4099 rows of 6 adapters 2.4 + 5.9 / 7.8, 8192 of 64 2.4 + 10.2 / 12.7,
 // 16384 of 64 2.1 + 10.3 / 15.9.
 constexpr int kSelfCount = 8192;
 constexpr int kWaveBins = 1024;  // up to so many bins the waves' counts have a place each in LDS
@@ -385,11 +385,11 @@ __device__ inline void put_low(const LowRankArgs &p, int tile, int i, int row, i
 __host__ __device__ inline int low_groups(int rank) { return part_pack(rank) ? rank / 8 : (rank + 31) / 32 * 4; }
 
 // ------------------------------------------------------------------ shrink
-// K is taken in slices, one workgroup per tile and slice, and the workgroups of a
-// slice on one XCD (workgroups go to the XCDs in turn): the slice's columns of a
-// gathered x (each token's row is read by every expert that it was routed to) and
-// of all adapters then stay in that XCD's L2 (4 slices: a pair of XCDs a slice). Few
-// rows still make many workgroups.
+// K is taken in slices, one workgroup per tile and slice, so that few rows still make
+// many workgroups. Workgroups go to the 8 XCDs in turn, so with 2 or 4 slices a slice's
+// workgroups share 4 or 2 XCDs, and its columns of a gathered x (each token's row is read
+// by every expert that it was routed to) and of all adapters stay in those XCDs' L2; with
+// 1 or 3 slices every XCD reads all columns.
 // Inside, the W waves take every W-th 128-wide step of the slice for all the tile's
 // rows, so each adapter row is read once per workgroup. A quad reads 64 bytes of one
 // row, the four quads of a row 256. Four waves where there are many rows: eight take
@@ -704,6 +704,9 @@ __global__ __launch_bounds__(256) void k_expand(LowRankArgs p, int blocks) {
 // one after the other, they take 64 us instead of 56 (32768 rows of rank 16, 2048 x
 // 2048, dy 134 MB read once; vector instructions 20 us). Run right after the product
 // that reads dy too, before the expansion: 49 us, the caches still hold a part of dy.
+// Ranks above 64 take two workgroups along y, which read and turn dy and x twice: a whole
+// backward of 32768 rows of rank 128 takes 378 us, of rank 64 224 (2048 x 2048). Above rank
+// 32 an MXFP8 x needs 262 registers, one wave a SIMD instead of two: rank 64 262 us.
 constexpr int kGradCols = 128;
 
 template <int SRC, int RT>
@@ -979,8 +982,12 @@ hipError_t launch_adapter_prepare(const PrepareArgs &a, hipStream_t s) {
 }
 
 // Slices of K, each a multiple of 128 and at least kSliceMin wide: up to 4, as many as
-// the CUs take at once, a workgroup of 64 rows each; where one slice is more than that,
-// slices against the tail of the last round. us, product + join, for 1 / 2 / 3 / 4 / 8:
+// make no more workgroups of 64 rows than there are CUs; where one slice already makes
+// more (from 16384 rows), 4 for ranks up to 16 and 2 above. Ranks above 32 hold one
+// workgroup a CU (their registers); lower ones two or three, and take the same rule.
+// The rule is not the fastest everywhere: from 16384 rows of rank 64, 1 slice was 4 us
+// faster than its 2 at K = 2048 and 4 slices 4 us faster at K = 4096. us, product +
+// join, for 1 / 2 / 3 / 4 / 8:
 //   640 rows, rank 32, K 4096       19.6 / 16.3 /      / 12.7 / 11.6
 //   2000 rows, rank 64, K 2880           / 18.1 / 16.6 / 15.1
 //   4099 rows, rank 64, K 2880      22.5 / 19.4 / 18.1 / 23.2 / 24.4
@@ -1034,7 +1041,8 @@ hipError_t launch_adapter_expand(const LowRankArgs &a, hipStream_t s) {
   // Two blocks of 16 rows a wave for a high rank, whose weights are then read half as
   // often, unless the workgroups get few. us, one block against two: rank 128, 8192
   // rows, N = 4096 91.8 / 79.6; rank 64, 12867 rows, N = 2048 47.2 / 42.4, 2048 rows
-  // 12.0 / 11.8; rank 32, 8192 rows 17.9 / 18.9; rank 16, 32768 rows 52.2 / 53.9.
+  // 12.0 / 11.8; rank 32, 8192 rows 17.9 / 18.9; rank 16, 32768 rows 52.2 / 53.9. (4096 rows
+  // lie between the measured 2048, where both are even, and 8192.)
   if (pack == 1) expand_one<1, 1>(a, s);
   else if (pack == 2) expand_one<2, 1>(a, s);
   else if (a.rank > 32 && a.R >= 4096) expand_one<0, 2>(a, s);
@@ -1061,6 +1069,8 @@ hipError_t launch_adapter_rowgrad(const RowGradArgs &args, hipStream_t s) {
   //                                rank 64 44.1 / 35.3 / 28.6 / 29.9, 128 73.3 / 55.8 / 46.2 / 33.7
   //   12288 rows of 8, rank 32 37.0 / 36.5 / 49.3 / 43.5, 64 60.9 / 52.0 / 57.4 / 56.7, 128 108 / 92.7 / 83.5 / 90.3
   //   32768 rows of 4 (chunks of 1024), rank 32 71.0 / 74.9, 64 101.5 / 90.9, 128 193 / 172
+  // 4 chunks above rank 32 is one number for all of these: 4096 rows of rank 128 would take
+  // 8 (33.7 against 46.2), 12288 of rank 64 2 (52.0 against 57.4).
   RowGradArgs a = args;
   const int rows = adapter_chunk_rows(a.R);
   a.merge = a.R <= 8 * rows ? 8 : a.rank <= 16 ? 1 : a.rank <= 32 ? (a.R < 8192 ? 2 : 1) : 4;
@@ -1090,7 +1100,8 @@ static int rows_csplit(int R, int N) {
 // Where the one-launch form runs: while at most 1 MB of A and B passes through one
 // CU. Both forms, a pass in us on K = N = 2048: rank 16, 1024 / 2048 rows 14 / 23
 // against 23 / 27 for the grouped kernels; rank 64, 256 / 512 rows 21 / 29 against 25
-// / 27; and 2880 x 2880, rank 32: 256 / 1024 rows 17 / 29 against 22 / 27.
+// / 27; and 2880 x 2880, rank 32: 256 / 1024 rows 17 / 29 against 22 / 27. (512 rows of
+// rank 64 lie on the limit and still run here, 2 us behind.)
 bool adapter_rows_supported(int R, int K, int N, int rank) {
   const int cs = rows_csplit(R, N);
   const int64_t bytes = cdiv((int64_t)R * cs, 256) * 2 * rank * ((int64_t)K + cdiv(N, cs));  // of A and B through one CU

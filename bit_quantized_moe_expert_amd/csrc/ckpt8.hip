@@ -126,7 +126,8 @@ __global__ __launch_bounds__(256) void k_glu_forward(GluArgs p) {
 // and drow = sum_c dh h, the gradient of the row's weight. gate and up come
 // from the 8-bit save (decoded here, never written out) or from bf16 / fp32.
 // WPR waves per row; drow is their sums added in a fixed order. 32768 x 1024 pairs from
-// 8 bits, h recomputed: 337 MB in 54 us, 6.3 TB/s.
+// 8 bits, h recomputed: 337 MB in 54 us, 6.3 TB/s right after the forward (in part the
+// last-level cache), 61 from other inputs; with fp32 dh 405 MB in 74, from bf16 gu 403 in 72.
 template <int SRC, bool DHBF, int WPR>
 __global__ __launch_bounds__(256) void k_glu_backward(GluArgs p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -291,7 +292,8 @@ static void glu_backward_d(const GluArgs &a, hipStream_t s) {
 hipError_t launch_glu_backward(const GluArgs &a, hipStream_t s) {
   // Four waves a row where a row feeds them, or few rows would leave CUs idle. us, one
   // wave a row against four: I = 2880, 8192 rows 43.7 / 38.6, 64 rows 7.4 / 4.3; I = 1024,
-  // 256 rows 4.2 / 3.6, 2048 rows 7.2 / 8.0; I = 768, 16384 rows 23.1 / 27.1.
+  // 256 rows 4.2 / 3.6, 2048 rows 7.2 / 8.0; I = 768, 16384 rows 23.1 / 27.1. (1536, three
+  // rounds of a wave, lies between the measured 1024 and 2880.)
   const bool wide = a.I > 1536 || a.R <= 512;
   for (int64_t r0 = 0; r0 < a.R; r0 += glu_rows(a.I)) {
     const GluArgs p = glu_piece(a, r0);

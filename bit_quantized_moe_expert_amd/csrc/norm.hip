@@ -13,7 +13,10 @@
 // is rounded once. Both directions are bound by memory traffic: the forward of 8190 x
 // 2880 (fp32 stream, 283 MB) takes 52.4 us, 5.4 TB/s, the backward of 8192 x 2048 bf16
 // (201 MB) 43.4 us and 5.0 for the joined column sums, 4.2 TB/s: a row's two sums wait
-// for each other.
+// for each other. Wider rows, bf16: 4096 x 4096 25.7 and 54.3 us, 4096 x 8192 51.5 and
+// 95.8, 2048 x 16384 50.9 and 119.8. Above 8192 columns a thread of the backward holds two
+// pieces, and its registers do not suffice: 8 to 92 of them go to memory (36 to 304 bytes a
+// lane, most where H % 8 != 0; 2048 x 16383 fp32 with a gate per element 319 us).
 //
 // A row is held by TPR threads, 8 NC values each, so its reductions are a wave
 // sum (TPR = 64) or wave sums joined through LDS. Rows of any width: the last
@@ -291,7 +294,7 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
   // round may have one sum only)
   __shared__ float red[2][2 * 16];
   int turn = 0;
-  extern __shared__ float slot_sum[];  // [2][H] (SLOTS > 1: at most 32 KB)
+  extern __shared__ float slot_sum[];  // [2][H] (SLOTS > 1, H <= 2048: at most 16 KB)
   const int t = threadIdx.x % TPR, slot = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
   const int H = p.H;
   const float invH = 1.0f / (float)H;

@@ -7,6 +7,10 @@ Like the rest of the binding this only marshals arguments; every step runs in th
 library's HIP kernels, on the current stream of the tensors' device. Tensors are
 contiguous CUDA tensors of one device; sizes, types and devices are checked here,
 the rest by the library.
+
+None of these calls is recorded by autograd: inputs that require grad are taken as
+values, outputs have no grad_fn, and each forward has a backward call of its own
+beside it, for a training loop or a torch.autograd.Function to call.
 """
 from __future__ import annotations
 
@@ -121,7 +125,8 @@ class Ckpt8:
 
 
 def ckpt8_quantize(x, fmt: int = CKPT_MXINT8) -> Ckpt8:
-    """fp32 or bf16 x [.., K] (K % 32 == 0) -> its 8-bit checkpoint."""
+    """fp32 or bf16 x [.., K] (K % 32 == 0) -> its 8-bit checkpoint. Not recorded by
+    autograd."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch tensor")
     dt, shape, i = _dt(x, "x"), x.shape, x.get_device()
@@ -137,7 +142,8 @@ def ckpt8_quantize(x, fmt: int = CKPT_MXINT8) -> Ckpt8:
 
 
 def ckpt8_dequantize(ck: Ckpt8, dtype=_BF16):
-    """The values an 8-bit checkpoint stands for, as dtype (bf16 by default, exact)."""
+    """The values an 8-bit checkpoint stands for, as dtype (bf16 by default, exact).
+    Not recorded by autograd."""
     dt = _out_dt(dtype)
     if not isinstance(ck.codes, torch.Tensor):
         raise TypeError("checkpoint codes must be a torch tensor")
@@ -158,7 +164,8 @@ def _glu_width(cols):
 def glu_forward(gu, glu: int = 0, alpha: float = 0.0, limit: float = 0.0, interleaved: int = 0, ckpt=None):
     """The gated activation of gu [R, 2I] (bf16 or fp32): h bf16 [R, I]. With ckpt
     (CKPT_MXINT8 or CKPT_MXFP8) the same pass saves gu in 8 bits: (h, Ckpt8).
-    glu, alpha, limit, interleaved as in MoELayer."""
+    glu, alpha, limit, interleaved as in MoELayer. Not recorded by autograd: the
+    gradient is glu_backward's."""
     R, cols = _dims(gu, "gu", 2)
     dt, I, i = _dt(gu, "gu"), _i32(_glu_width(cols), "I"), gu.get_device()
     if ckpt not in (None, CKPT_MXINT8, CKPT_MXFP8):
@@ -242,7 +249,8 @@ def block_norm_forward(x, f=None, *, w_post=None, w_pre=None, gate=None, gate_fn
     [H] (None: without that norm); gate fp32 or bf16, [H], [T, 1] or [T, H]; gate_fn
     GATE_IDENTITY, GATE_SIGMOID or GATE_TANH; out: where x' goes (may be x). Returns
     a dict: x (x', or x itself without f), y bf16, rstd_post, rstd_pre fp32 [T] (None
-    where there is no such norm); block_norm_backward takes them."""
+    where there is no such norm); block_norm_backward takes them. Not recorded by
+    autograd: the gradients are block_norm_backward's."""
     st, xp, fp, T, H, i = _norm_struct(x, f, w_post, w_pre, gate, gate_fn, alpha, eps)
     if f is None:
         if out is not None:
@@ -354,7 +362,8 @@ def adapter_forward(x, A, B, ids, *, base=None, scale=None, x_row_of=None, out=N
     id outside [0, L) means no adapter; scale fp32 [L] or None; base bf16 or fp32 [R,
     N], the shared projection's output, or None (zeros); out: where the result goes
     (may be base), else a new tensor of base's type or out_dtype. Returns out, or
-    (out, t) with t = A x fp32 [R, rank] for adapter_backward."""
+    (out, t) with t = A x fp32 [R, rank] for adapter_backward. Not recorded by autograd:
+    the gradients are adapter_backward's."""
     rows, _ = _dims(x, "x", 2)
     i = x.get_device()
     dtype = _one_dtype("base, out and out_dtype", out if out is None else out.dtype, base if base is None else base.dtype,
@@ -381,7 +390,8 @@ def adapter_backward(dy, x, t, A, B, ids, *, scale=None, x_row_of=None, dx_base=
     Ckpt8 of it (read in 8 bits; K % 32 == 0); t the forward's. Returns a dict of
     those in `need`: dx [R, K] = dx_base + A^T u per row (dx_base bf16 or fp32 or None;
     dx: where it goes, may be dx_base), dA fp32 [L, rank, K], dB fp32 [L, N, rank].
-    x may be None without dA, t without dB. The same bits on every run."""
+    x may be None without dA, t without dB. The weights of all L adapters are read, used
+    or not. The same bits on every run."""
     R, _ = _dims(dy, "dy", 2)
     i = dy.get_device()
     if not set(need) <= {"dx", "dA", "dB"}:

@@ -502,7 +502,8 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
  *                                      Per routed row, as nf4moe_grouped_dgrad
  *   dA_l = sum_r u[r] x[x_row_of[r]]^T    fp32 [L, rank, K]
  *   dB_l = scale_l * sum_r dy[r] t[r]^T   fp32 [L, N, rank]
- * over the rows of adapter l, zeros for an adapter without rows; dx, dA and dB may
+ * over the rows of adapter l, zeros for an adapter without rows whatever its scale; the
+ * weights of all L adapters are read, used or not (for dx, dA). dx, dA and dB may
  * each be NULL. x (with x_rows) is read for dA only: bf16, or an 8-bit checkpoint
  * (x_src, with x_scale; K % 32 == 0) decoded in registers. t is the forward's (for
  * dB). The sums over rows are added in a fixed order: the same bits on every run. dA
