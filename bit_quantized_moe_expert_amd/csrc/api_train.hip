@@ -389,7 +389,7 @@ nf4moe_status_t nf4moe_adapter_forward(const nf4moe_adapters_t *ad, const uint16
   const uint64_t rows = (uint64_t)R, ob = rows * ad->N * dt_bytes(dtype), lr = (uint64_t)ad->L * ad->rank * 2;
   st = check_overlap({{"out", out, ob}, {"t", t, 4 * rows * ad->rank}, {"workspace", ws, need}},
                      {{"x", x, (uint64_t)x_rows * ad->K * 2}, {"x_row_of", x_row_of, 4 * rows}, {"ids", ids, 4 * rows},
-                      {"plan", plan, plan_bytes}, but({"base", base, ob}, out), {"A", ad->A, lr * ad->K}, {"B", ad->B, lr * ad->N},
+                      {"plan", plan, nf4moe_adapter_plan_bytes(R, ad->L)}, but({"base", base, ob}, out), {"A", ad->A, lr * ad->K}, {"B", ad->B, lr * ad->N},
                       {"scale", ad->scale, 4 * (uint64_t)ad->L}});
   if (st != NF4MOE_OK) return st;
   if (one_launch) {
@@ -443,7 +443,7 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
   st = check_overlap({{"dx", dx, xb}, {"dA", dA, 2 * lr * ad->K}, {"dB", dB, 2 * lr * ad->N}, {"workspace", ws, need.bytes}},
                      {{"dy", dy, 2 * rows * ad->N}, {"x", x, held ? held_x : 2 * held_x},
                       {"x_scale", held ? x_scale : nullptr, held_x / 32}, {"x_row_of", x_row_of, 4 * rows},
-                      {"t", dB ? t : nullptr, 4 * rows * ad->rank}, {"ids", ids, 4 * rows}, {"plan", plan, plan_bytes},
+                      {"t", dB ? t : nullptr, 4 * rows * ad->rank}, {"ids", ids, 4 * rows}, {"plan", plan, nf4moe_adapter_plan_bytes(R, ad->L)},
                       but({"dx_base", dx ? dx_base : nullptr, xb}, dx), {"A", ad->A, lr * ad->K}, {"B", ad->B, lr * ad->N},
                       {"scale", ad->scale, 4 * (uint64_t)ad->L}});
   if (st != NF4MOE_OK) return st;

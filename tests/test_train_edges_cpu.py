@@ -175,3 +175,19 @@ def test_adapters_refuse_overlapping_arrays(R, dt):
                          dict(dx=R * K * e, dA=4 * Ln * rank * K, dB=4 * Ln * rank * N, workspace=wb),
                          dict(dy=2 * R * N, x=width * T * K, x_row_of=4 * R, t=4 * R * rank, ids=4 * R, plan=pb,
                               dx_base=R * K * e, **more, **w), may_be=[("dx", "dx_base")])
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses, which a GPU would dereference")
+@pytest.mark.parametrize("plan_bytes", [1 << 46, (1 << 64) - 1])
+def test_a_plan_counts_for_its_own_bytes_alone(plan_bytes):
+    """A caller may state any size from nf4moe_adapter_plan_bytes up: what lies behind the plan is free for outputs."""
+    from bit_quantized_moe_expert_amd import train
+    R, Ln = 65536, 64
+    d = train._ADAPTERS.pack(Ln, 16, 128, 256, far(0), far(1), 0)
+    wf, wb = (L.nf4moe_adapter_workspace_bytes(d, R, k) for k in (0, 1))
+    plan, behind = far(3), far(3) + L.nf4moe_adapter_plan_bytes(R, Ln)
+    assert L.nf4moe_adapter_forward(d, far(2), R, None, far(4), plan, plan_bytes, R, None, behind, 1, None, far(6), wf, None) == HIP
+    assert L.nf4moe_adapter_backward(d, far(2), 1, far(4), None, R, None, far(5), far(6), plan, plan_bytes, R, None, behind, 1,
+                                     far(8), far(9), far(10), wb, None) == HIP
+    assert L.nf4moe_adapter_forward(d, far(2), R, None, far(4), plan, plan_bytes, R, None, behind - 256, 1, None, far(6), wf,
+                                    None) == INVALID
