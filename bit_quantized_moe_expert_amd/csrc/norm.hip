@@ -420,7 +420,7 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_norm_backward(NormArgs p)
             float q[8], dg[8];
             gate_row8<ODD>(p, base, i, q);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dg[j] = gate_slope(p.gate_fn, q[j]) * (p.alpha * g[c][j] * f[c][j] * w[j]);
+            for (int j = 0; j < 8; ++j) dg[j] = p.alpha * gate_slope(p.gate_fn, q[j]) * g[c][j] * f[c][j] * w[j];
             gate_phi8(p.gate_fn, q, q);
             if (live) store_row8<false, ODD>(p.dgate, base, i, H, dg);
 #pragma unroll

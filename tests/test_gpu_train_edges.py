@@ -170,3 +170,15 @@ def test_the_widest_row_of_the_gated_activation(inter):
     del h
     b = M.glu_backward(dh1.repeat(1, n), ck, interleaved=inter)
     assert same(b["dgu"], b1["dgu"], True) and same(b["h"], b1["h"], False)
+
+
+def test_a_small_slope_meets_large_gradients():
+    """The slope enters its product first: a gradient that fits is not lost to an infinity on the way."""
+    T, H = 3, 16
+    f, dx = torch.full((T, H), 1e30, device=DEV).to(BF16), torch.full((T, H), 1e10, device=DEV)
+    gate = torch.full((T, H), 20.0, device=DEV)
+    gate[1] = -20.0
+    out = M.block_norm_forward(torch.zeros(T, H, device=DEV), f, gate=gate, gate_fn=M.GATE_TANH)
+    got = to_np(M.block_norm_backward(dx, None, out["x"], f, gate=gate, gate_fn=M.GATE_TANH)["dgate"])
+    ref = tail_phi(to_np(gate), 2)[1] * to_np(dx) * to_np(f)
+    R.within(got, ref, np.abs(ref) * (tail_error(to_np(gate), 2)[1] + 8 * U), "dgate")
