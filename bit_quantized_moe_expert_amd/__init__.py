@@ -96,6 +96,17 @@ def lib() -> ctypes.CDLL:
         "nf4moe_adapter_forward": [vp, vp, i32, vp, vp, vp, sz, i32, vp, vp, ctypes.c_int, vp, vp, sz, vp],
         "nf4moe_adapter_backward": [vp, vp, ctypes.c_int, vp, vp, i32, vp, vp, vp, vp, sz, i32, vp, vp,
                                     ctypes.c_int, vp, vp, vp, sz, vp],
+        "nf4moe_gated_ffn_forward": [vp, vp, i64, vp, vp],
+        "nf4moe_gated_ffn_workspace_bytes": [vp, i64],
+        "nf4moe_gated_ffn_backward": [vp, vp, vp, i64, vp, vp, vp, vp, sz, vp],
+        "nf4moe_vocab_workspace_bytes": [vp, i64, i32],
+        "nf4moe_vocab_ce_forward": [vp, vp, i64, vp, vp, vp, vp, sz, vp],
+        "nf4moe_vocab_ce_backward": [vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp],
+        "nf4moe_vocab_distill_forward": [vp, vp, i64, vp, vp, ctypes.c_int, i32, f32, vp, vp, vp, vp, vp, sz, vp],
+        "nf4moe_vocab_distill_backward": [vp, vp, vp, i64, vp, vp, vp, vp, i32, f32, vp, vp, vp, sz, vp],
+        "nf4moe_layer_norm_forward": [vp, vp, i64, vp, vp, vp, vp],
+        "nf4moe_layer_norm_workspace_bytes": [i32, i64],
+        "nf4moe_layer_norm_backward": [vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp],
         "nf4moe_codebook": [ctypes.c_int, ctypes.POINTER(ctypes.c_float)],
         "nf4moe_auto_path": [ctypes.c_int, i64, i64],
         "nf4moe_stream_read_sink_words": [i64, i32],
@@ -112,7 +123,8 @@ def lib() -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     for name in ("nf4moe_route_workspace_bytes", "nf4moe_gemm_workspace_bytes", "nf4moe_workspace_bytes",
                  "nf4moe_router_workspace_bytes", "nf4moe_block_norm_workspace_bytes",
-                 "nf4moe_adapter_plan_bytes", "nf4moe_adapter_workspace_bytes"):
+                 "nf4moe_adapter_plan_bytes", "nf4moe_adapter_workspace_bytes",
+                 "nf4moe_gated_ffn_workspace_bytes", "nf4moe_vocab_workspace_bytes", "nf4moe_layer_norm_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_size_t
     L.nf4moe_stream_read_sink_words.restype = ctypes.c_int64
     L.nf4moe_mfma_peak_flops.restype = ctypes.c_int64
@@ -548,21 +560,25 @@ def moe_forward(layer: MoELayer, x, return_routing: bool = False):
     return out, ids, w
 
 
-# Fine-tuning and multi-adapter serving around the frozen 4-bit layer: train.py's names,
-# loaded when one is first used, so that this package (and its build) imports without torch.
+# Fine-tuning and multi-adapter serving around the frozen 4-bit layer (train.py) and the dense
+# ends of a training step (dense.py): their names, loaded when one is first used, so that this
+# package (and its build) imports without torch.
 _TRAIN = ("CKPT_MXFP8", "CKPT_MXINT8", "GATE_IDENTITY", "GATE_SIGMOID", "GATE_TANH", "AdapterPlan", "Ckpt8",
           "adapter_backward", "adapter_forward", "adapter_plan", "block_norm_backward", "block_norm_forward",
           "ckpt8_dequantize", "ckpt8_quantize", "glu_backward", "glu_forward")
+_DENSE = ("gated_ffn_backward", "gated_ffn_forward", "layer_norm_backward", "layer_norm_forward", "vocab_ce_backward",
+          "vocab_ce_forward", "vocab_distill_backward", "vocab_distill_forward")
 
 
 def __getattr__(name):
-    if name != "train" and name not in _TRAIN:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    import importlib
-    train = importlib.import_module(".train", __name__)
-    globals().update({n: getattr(train, n) for n in _TRAIN})
-    return globals()[name]
+    for module, names in (("train", _TRAIN), ("dense", _DENSE)):
+        if name == module or name in names:
+            import importlib
+            m = importlib.import_module("." + module, __name__)
+            globals().update({n: getattr(m, n) for n in names})
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted({*globals(), *_TRAIN})
+    return sorted({*globals(), *_TRAIN, *_DENSE})

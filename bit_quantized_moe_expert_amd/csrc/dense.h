@@ -1,0 +1,92 @@
+// Host-side declarations of the dense operators' kernels (gated feed-forward, vocabulary
+// loss and distillation, layer norm).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace nf4moe {
+
+constexpr int kDenseMaxWidth = 1 << 20;   // H and I: 256 rows of it are below 2^31 bytes
+
+// out[m][n] = sum_k X(m, k) Y(n, k) in bf16, or in fp32 to `part` by slices of K (added to what is
+// there with `add`). X: element (m, k) at x[m * ldx + k], turned x[k * ldx + m]; Y turned:
+// y[k * ldy + n]. `live`: a bit for each k, zero where Y's row k counts as zeros (turned X).
+struct ProductArgs {
+  const uint16_t *x, *y;
+  int64_t ldx, ldy, M, N, K;
+  uint16_t *out;        // [M, N], or null
+  float *part;          // [slices][M][N]
+  bool add;
+  int slices;
+  const uint64_t *live;
+};
+// x as it lies or turned, y turned: the two products of a backward pass.
+hipError_t launch_product(const ProductArgs &a, bool x_turned, hipStream_t s);
+// Slices of K that fill the card for the product with x as it lies.
+int product_slices(int64_t M, int64_t N, int64_t K);
+// out bf16 [n] = the sum of the slices' parts, in order.
+hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s);
+
+struct FfnArgs {
+  int64_t T;
+  int H, I, glu, inter;
+  float alpha, limit;
+  const uint16_t *x, *w13;   // [T, H], [2I, H]
+  uint16_t *h;               // [T, I] (backward: optional)
+  const uint16_t *dh;        // [T, I]
+  uint16_t *dgu;             // [T, 2I] in w13's row order
+};
+hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s);
+hipError_t launch_ffn_dgu(const FfnArgs &a, hipStream_t s);
+
+constexpr int kMaxTeacher = 1024;
+// The vocabulary head: logits x W^T, by k_head_* kernels that never store them.
+struct HeadArgs {
+  int64_t T, V;
+  int H, k;                  // k: teacher entries a row (0: labels)
+  float tau;
+  const uint16_t *x, *w;     // [T, H], [V, H]
+  const int32_t *ids;        // [T] labels or [T, k]
+  // forward
+  const void *teacher;       // [T, k]
+  bool teacher_bf16;
+  float *loss, *lse;         // [T]
+  float *q, *logits;         // [T, k]
+  float2 *stats;             // [n tiles][T]: (maximum, sum) of a tile's columns
+  float *picked;             // [T] the label's logit
+  // backward
+  const float *dloss;        // [T]
+  int64_t v0, vn, vp;        // the piece of the vocabulary, and the row stride of P
+  uint16_t *P;               // [T, vp]
+  uint64_t *live;            // [T / 64]
+};
+int64_t head_stat_tiles(int64_t T, int64_t V);
+hipError_t launch_head_forward(const HeadArgs &a, hipStream_t s);
+hipError_t launch_head_live(const HeadArgs &a, hipStream_t s);
+hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s);
+int64_t head_piece(int64_t T, int64_t V);
+
+struct LayerNormArgs {
+  int64_t T;
+  int H;
+  bool x_bf16, y_bf16;
+  const void *x;
+  const float *w, *b;        // [H] or null
+  float eps;
+  void *y;                   // forward
+  float *mean, *rstd;        // [T], written by the forward, read by the backward
+  // backward
+  const void *dy;            // as y
+  const void *dx_base;       // as x, or null
+  void *dx;                  // as x, or null
+  float *dw, *db;            // [H] or null
+  float *partial;            // [groups][2][H]
+  int groups;
+};
+constexpr int kLayerNormMaxH = 16384;
+hipError_t launch_layer_norm_forward(const LayerNormArgs &a, hipStream_t s);
+hipError_t launch_layer_norm_backward(const LayerNormArgs &a, hipStream_t s);
+int layer_norm_groups(int64_t T, int H);
+
+}  // namespace nf4moe

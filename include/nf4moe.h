@@ -515,6 +515,118 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
                                         const void *dx_base, void *dx, nf4moe_dtype_t dx_dtype, float *dA, float *dB,
                                         void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The dense bf16 ends of a training step around the frozen layer: a gated feed-forward
+ * (a shared expert), the losses of a vocabulary head, layer norm. The conventions are
+ * those of the fine-tuning calls above. Matrices are bf16, contiguous and 16-byte aligned, their
+ * widths (H, I) multiples of 8 up to 2^20; products are summed in fp32, every output is
+ * rounded once; the gradient of a product (dgu, P below) is rounded to bf16 where it becomes
+ * an operand of the next. The same bits on every run. UNSUPPORTED past 2^22 tiles of 256 x
+ * 256 of one product, or 2^38 values.
+ *
+ * Gated feed-forward: g = x Wg^T, u = x Wu^T, h = the gated activation (nf4moe_glu_t) of g and u.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t H, I;
+  const uint16_t *w13;       /* bf16 [2I, H]: gate rows, then up rows; or interleaved */
+  int32_t glu;               /* nf4moe_glu_t                                        */
+  float glu_alpha, glu_limit;
+  int32_t glu_interleaved;   /* rows alternate gate, up (as in nf4moe_layer_t)      */
+} nf4moe_gated_ffn_t;
+
+/* nf4moe_gated_ffn_forward -- h bf16 [T, I] from x bf16 [T, H]. One launch, no workspace.
+ * T at most 2^30; T == 0 is a no-op. Errors: INVALID_ARG, UNSUPPORTED. */
+nf4moe_status_t nf4moe_gated_ffn_forward(const nf4moe_gated_ffn_t *ffn, const uint16_t *x, int64_t T, uint16_t *h,
+                                         void *stream);
+
+/* nf4moe_gated_ffn_workspace_bytes -- workspace of the backward (0 for T < 1 or invalid sizes). */
+size_t nf4moe_gated_ffn_workspace_bytes(const nf4moe_gated_ffn_t *ffn, int64_t T);
+
+/* nf4moe_gated_ffn_backward -- gradients for dh bf16 [T, I], g and u computed again:
+ *   dx   bf16 [T, H]    dgu W13           (NULL: not computed)
+ *   dw13 bf16 [2I, H]   dgu^T x, in w13's row order   (NULL: not computed)
+ *   h    bf16 [T, I]    the forward's output again (optional)
+ * The clamped form's gradient is that of the unclamped side at the limit itself. T == 0 writes
+ * zeros to dw13. Errors: INVALID_ARG (neither dx nor dw13 among them), WORKSPACE, UNSUPPORTED. */
+nf4moe_status_t nf4moe_gated_ffn_backward(const nf4moe_gated_ffn_t *ffn, const uint16_t *dh, const uint16_t *x, int64_t T,
+                                          uint16_t *dx, uint16_t *dw13, uint16_t *h, void *ws, size_t ws_bytes,
+                                          void *stream);
+
+/* The head of the losses below: logits l = x W^T [T, V], never stored. */
+typedef struct {
+  int32_t H;
+  int32_t V;                 /* 1..2^21                                             */
+  const uint16_t *w;         /* bf16 [V, H]                                         */
+} nf4moe_head_t;
+
+/* nf4moe_vocab_workspace_bytes -- workspace of the forward (backward = 0) or the backward (1) of
+ * either loss for T rows; 0 for T < 1 or invalid sizes. The backward's holds the gradient of
+ * one piece of the vocabulary at a time (at most 128 MB, or 256 columns). */
+size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_t backward);
+
+/* nf4moe_vocab_ce_forward -- softmax cross entropy: lse[t] = log sum_v exp(l[t, v]) and loss[t] =
+ * lse[t] - l[t, labels[t]], fp32 [T]; a label outside [0, V) (-100, say) means loss 0 and no
+ * gradient. T == 0 is a no-op. Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED.
+ *
+ * nf4moe_vocab_ce_backward -- for dloss fp32 [T] (the gradient of loss; not read where a row has no
+ * label) and the forward's lse, with P = dloss (softmax(l) - onehot(label)):
+ *   dx bf16 [T, H] = P W;  dw bf16 [V, H] = P^T x     (either may be NULL)
+ * A row without a label counts for nothing whatever its x holds. T == 0 writes zeros to dw. */
+nf4moe_status_t nf4moe_vocab_ce_forward(const nf4moe_head_t *head, const uint16_t *x, int64_t T, const int32_t *labels,
+                                        float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
+nf4moe_status_t nf4moe_vocab_ce_backward(const nf4moe_head_t *head, const float *dloss, const uint16_t *x, int64_t T,
+                                         const int32_t *labels, const float *lse, uint16_t *dx, uint16_t *dw, void *ws,
+                                         size_t ws_bytes, void *stream);
+
+/* nf4moe_vocab_distill_forward -- distillation from a teacher's top logits: ids int32 [T, k] and the
+ * teacher's logits for them (fp32 or bf16 [T, k], k 1..1024), temperature tau in 0.001..1000:
+ *   q      fp32 [T, k]  softmax over a row's entries of teacher / tau
+ *   logits fp32 [T, k]  the student's logits l[t, ids[t, j]]
+ *   lse    fp32 [T]     log sum_v exp(l[t, v] / tau)
+ *   loss   fp32 [T]     tau^2 sum_j q_j (log q_j - logits_j / tau + lse), tau^2 times the divergence of
+ *                       the student's whole softmax from the teacher's
+ * An entry with an id outside [0, V) counts for nothing, whatever its logit (q and logits 0). An id
+ * that a row names twice has the sum of both probabilities, in its first place. A row without an
+ * entry whose teacher logit is above -inf has loss 0, lse +inf and no gradient. T == 0 is a no-op.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED.
+ *
+ * nf4moe_vocab_distill_backward -- with the forward's q, logits and lse, P = dloss tau (softmax(l / tau)
+ * - q); dx, dw and the rest as in nf4moe_vocab_ce_backward. */
+nf4moe_status_t nf4moe_vocab_distill_forward(const nf4moe_head_t *head, const uint16_t *x, int64_t T, const int32_t *ids,
+                                             const void *teacher, nf4moe_dtype_t teacher_dtype, int32_t k,
+                                             float temperature, float *loss, float *lse, float *q, float *logits, void *ws,
+                                             size_t ws_bytes, void *stream);
+nf4moe_status_t nf4moe_vocab_distill_backward(const nf4moe_head_t *head, const float *dloss, const uint16_t *x, int64_t T,
+                                              const int32_t *ids, const float *q, const float *logits, const float *lse,
+                                              int32_t k, float temperature, uint16_t *dx, uint16_t *dw, void *ws,
+                                              size_t ws_bytes, void *stream);
+
+/* Layer norm: y = (x - mean) rstd w + b, rstd = 1 / sqrt(mean((x - mean)^2) + eps), fp32 in
+ * registers. Rows contiguous, H 1..16384, no alignment beyond the element's. */
+typedef struct {
+  int32_t H;
+  int32_t x_dtype;           /* nf4moe_dtype_t of x, dx_base, dx                    */
+  int32_t y_dtype;           /* ... of y, dy                                        */
+  const float *w, *b;        /* fp32 [H] or NULL (1, 0)                             */
+  float eps;                 /* finite, >= 0                                        */
+} nf4moe_layer_norm_t;
+
+/* nf4moe_layer_norm_forward -- x [T, H] -> y [T, H], mean and rstd fp32 [T] (which the backward
+ * reads). T == 0 is a no-op. Errors: INVALID_ARG. */
+nf4moe_status_t nf4moe_layer_norm_forward(const nf4moe_layer_norm_t *norm, const void *x, int64_t T, void *y, float *mean,
+                                          float *rstd, void *stream);
+
+/* nf4moe_layer_norm_workspace_bytes -- workspace of the backward (0 for T < 1). */
+size_t nf4moe_layer_norm_workspace_bytes(int32_t H, int64_t T);
+
+/* nf4moe_layer_norm_backward -- for dy [T, H], with n = (x - mean) rstd and a = dy w:
+ *   dx [T, H] = dx_base + rstd (a - mean(a) - n mean(a n))   (dx_base NULL: zero; may be dx)
+ *   dw fp32 [H] = sum_t dy n;  db fp32 [H] = sum_t dy
+ * dx, dw, db may each be NULL. T == 0 writes zeros to dw and db. Errors: INVALID_ARG, WORKSPACE. */
+nf4moe_status_t nf4moe_layer_norm_backward(const nf4moe_layer_norm_t *norm, const void *dy, const void *x, const float *mean,
+                                           const float *rstd, int64_t T, const void *dx_base, void *dx, float *dw, float *db,
+                                           void *ws, size_t ws_bytes, void *stream);
+
 /* nf4moe_stream_read -- a measurement aid, not part of the layer: one launch
  * that reads `bytes` bytes of `buf` (device, 16-byte aligned, bytes a positive
  * multiple of 16) once with 16-byte loads, loads_per_thread (1, 2, 4, 8 or 16)
