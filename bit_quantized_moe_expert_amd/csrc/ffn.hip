@@ -43,41 +43,38 @@ __global__ __launch_bounds__(T::THREADS) void k_ffn(FfnArgs p) {
   if (p.inter) t.y.template init_pair<G>(p.w13, p.w13 + p.H, 2 * (int64_t)p.H, c0, p.I);
   else t.y.template init_pair<G>(p.w13, p.w13 + (int64_t)p.I * p.H, p.H, c0, p.I);
   t.run(lds, 0, p.H, nullptr);
-  const int wn = T::wave_n(), g4 = 4 * (int)(threadIdx.x >> 5 & 1);
+  const int wn = T::wave_n(), g4 = 4 * (int)(threadIdx.x >> 4 & 3);
 #pragma unroll
   for (int mb = 0; mb < T::MB; ++mb) {
     const int r = T::row_of(mb);
     char *row = lds + r * T::PITCH;
 #pragma unroll
     for (int nb = 0; nb < G; ++nb) {
+      const int c = (wn * G + nb) * 16 + g4;   // column of the tile's HN
+      f32x4_t &gv = t.acc[nb][mb], &uv = t.acc[nb + G][mb];
+      if constexpr (!BACK) {
+        float h[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = (wn * G + nb) * 32 + 8 * q + g4;   // column of the tile's HN
-        f32x16_t &gv = t.acc[nb][mb], &uv = t.acc[nb + G][mb];
-        if constexpr (!BACK) {
-          float h[4];
+        for (int j = 0; j < 4; ++j) h[j] = glu_value(p.glu, p.alpha, p.limit, gv[j], uv[j]);
+        *reinterpret_cast<uint2 *>(row + 2 * c) = pack4(h[0], h[1], h[2], h[3]);
+      } else {
+        uint2 d = make_uint2(0, 0);
+        if (m0 + r < p.T && c0 + c < p.I) d = *reinterpret_cast<const uint2 *>(p.dh + (m0 + r) * p.I + c0 + c);
+        const float dh[4] = {bf16lo_to_f32(d.x), bf16hi_to_f32(d.x), bf16lo_to_f32(d.y), bf16hi_to_f32(d.y)};
+        float dg[4], du[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = glu_value(p.glu, p.alpha, p.limit, gv[4 * q + j], uv[4 * q + j]);
-          *reinterpret_cast<uint2 *>(row + 2 * c) = pack4(h[0], h[1], h[2], h[3]);
+        for (int j = 0; j < 4; ++j) {
+          float by_g, by_u;
+          // h takes g's place for the second pass
+          gv[j] = glu_slopes(p.glu, p.alpha, p.limit, gv[j], uv[j], by_g, by_u);
+          dg[j] = dh[j] * by_g, du[j] = dh[j] * by_u;
+        }
+        if (p.inter) {
+          *reinterpret_cast<uint2 *>(row + 4 * c) = pack4(dg[0], du[0], dg[1], du[1]);
+          *reinterpret_cast<uint2 *>(row + 4 * c + 8) = pack4(dg[2], du[2], dg[3], du[3]);
         } else {
-          uint2 d = make_uint2(0, 0);
-          if (m0 + r < p.T && c0 + c < p.I) d = *reinterpret_cast<const uint2 *>(p.dh + (m0 + r) * p.I + c0 + c);
-          const float dh[4] = {bf16lo_to_f32(d.x), bf16hi_to_f32(d.x), bf16lo_to_f32(d.y), bf16hi_to_f32(d.y)};
-          float dg[4], du[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float by_g, by_u;
-            // h takes g's place for the second pass
-            gv[4 * q + j] = glu_slopes(p.glu, p.alpha, p.limit, gv[4 * q + j], uv[4 * q + j], by_g, by_u);
-            dg[j] = dh[j] * by_g, du[j] = dh[j] * by_u;
-          }
-          if (p.inter) {
-            *reinterpret_cast<uint2 *>(row + 4 * c) = pack4(dg[0], du[0], dg[1], du[1]);
-            *reinterpret_cast<uint2 *>(row + 4 * c + 8) = pack4(dg[2], du[2], dg[3], du[3]);
-          } else {
-            *reinterpret_cast<uint2 *>(row + 2 * c) = pack4(dg[0], dg[1], dg[2], dg[3]);
-            *reinterpret_cast<uint2 *>(row + 2 * (HN + c)) = pack4(du[0], du[1], du[2], du[3]);
-          }
+          *reinterpret_cast<uint2 *>(row + 2 * c) = pack4(dg[0], dg[1], dg[2], dg[3]);
+          *reinterpret_cast<uint2 *>(row + 2 * (HN + c)) = pack4(du[0], du[1], du[2], du[3]);
         }
       }
     }
@@ -99,13 +96,10 @@ __global__ __launch_bounds__(T::THREADS) void k_ffn(FfnArgs p) {
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
-      for (int nb = 0; nb < G; ++nb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16_t &h = t.acc[nb][mb];
-          *reinterpret_cast<uint2 *>(lds + T::row_of(mb) * T::PITCH + 2 * ((wn * G + nb) * 32 + 8 * q + g4)) =
-              pack4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-        }
+      for (int nb = 0; nb < G; ++nb) {
+        const f32x4_t &h = t.acc[nb][mb];
+        *reinterpret_cast<uint2 *>(lds + T::row_of(mb) * T::PITCH + 2 * ((wn * G + nb) * 16 + g4)) = pack4(h[0], h[1], h[2], h[3]);
+      }
     lds_barrier();
     store_tile<T::BM, HN, T::THREADS>(lds, T::PITCH, p.h + m0 * p.I + c0, p.I, rows, cols);
   }
@@ -129,13 +123,10 @@ __global__ __launch_bounds__(T::THREADS) void k_product(ProductArgs p) {
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
-      for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16_t &v = t.acc[nb][mb];
-          *reinterpret_cast<uint2 *>(lds + T::row_of(mb) * T::PITCH + 2 * T::col_of(nb, q)) =
-              pack4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        }
+      for (int nb = 0; nb < T::NB; ++nb) {
+        const f32x4_t &v = t.acc[nb][mb];
+        *reinterpret_cast<uint2 *>(lds + T::row_of(mb) * T::PITCH + 2 * T::col_of(nb)) = pack4(v[0], v[1], v[2], v[3]);
+      }
     lds_barrier();
     store_tile<T::BM, T::BN, T::THREADS>(lds, T::PITCH, p.out + m0 * p.N + n0, p.N, p.M - m0, p.N - n0);
     return;
@@ -146,20 +137,18 @@ __global__ __launch_bounds__(T::THREADS) void k_product(ProductArgs p) {
     const int64_t m = m0 + T::row_of(mb);
     if (m >= p.M) continue;
 #pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t n = n0 + T::col_of(nb, q);
-        if (n >= p.N) continue;
-        float4 *at = reinterpret_cast<float4 *>(part + m * p.N + n);
-        const f32x16_t &v = t.acc[nb][mb];
-        float4 o = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        if (p.add) {
-          const float4 was = *at;
-          o = make_float4(was.x + o.x, was.y + o.y, was.z + o.z, was.w + o.w);
-        }
-        *at = o;
+    for (int nb = 0; nb < T::NB; ++nb) {
+      const int64_t n = n0 + T::col_of(nb);
+      if (n >= p.N) continue;
+      float4 *at = reinterpret_cast<float4 *>(part + m * p.N + n);
+      const f32x4_t &v = t.acc[nb][mb];
+      float4 o = make_float4(v[0], v[1], v[2], v[3]);
+      if (p.add) {
+        const float4 was = *at;
+        o = make_float4(was.x + o.x, was.y + o.y, was.z + o.z, was.w + o.w);
       }
+      *at = o;
+    }
   }
 }
 
@@ -182,13 +171,13 @@ template <bool BACK>
 hipError_t ffn(const FfnArgs &a, hipStream_t s) {
   auto tiles = [&](int bm, int hn) { return cdiv(a.T, bm) * cdiv(a.I, hn); };
   if (tiles(256, 128) >= 160) {
-    using T = GemmTile<2, 4, 4, 2, false, false, 2>;
+    using T = GemmTile<4, 8, 4, 2, false, false, 4>;
     hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(cdiv(a.T, 256), cdiv(a.I, 128))), dim3(T::THREADS), 0, s, a);
   } else if (tiles(128, 64) >= 160) {
-    using T = GemmTile<2, 2, 2, 2, false, false, 1>;
+    using T = GemmTile<4, 4, 2, 2, false, false, 2>;
     hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(cdiv(a.T, 128), cdiv(a.I, 64))), dim3(T::THREADS), 0, s, a);
   } else {
-    using T = GemmTile<1, 2, 2, 1, false, false, 1>;
+    using T = GemmTile<2, 4, 2, 1, false, false, 2>;
     hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(cdiv(a.T, 64), cdiv(a.I, 32))), dim3(T::THREADS), 0, s, a);
   }
   return hipGetLastError();
@@ -198,13 +187,13 @@ template <bool XT, bool MASK>
 hipError_t product(const ProductArgs &a, hipStream_t s) {
   auto tiles = [&](int bm, int bn) { return cdiv(a.M, bm) * cdiv(a.N, bn) * a.slices; };
   if (tiles(256, 256) >= 160) {
-    using T = GemmTile<2, 4, 4, 2, XT, true, 0, MASK>;
+    using T = GemmTile<4, 8, 4, 2, XT, true, 0, MASK>;
     hipLaunchKernelGGL((k_product<T>), dim3(gemm_grid(cdiv(a.M, 256), cdiv(a.N, 256)), a.slices), dim3(T::THREADS), 0, s, a);
   } else if (tiles(128, 128) >= 160) {
-    using T = GemmTile<2, 2, 2, 2, XT, true, 0, MASK>;
+    using T = GemmTile<4, 4, 2, 2, XT, true, 0, MASK>;
     hipLaunchKernelGGL((k_product<T>), dim3(gemm_grid(cdiv(a.M, 128), cdiv(a.N, 128)), a.slices), dim3(T::THREADS), 0, s, a);
   } else {
-    using T = GemmTile<1, 1, 2, 2, XT, true, 0, MASK>;
+    using T = GemmTile<2, 2, 2, 2, XT, true, 0, MASK>;
     hipLaunchKernelGGL((k_product<T>), dim3(gemm_grid(cdiv(a.M, 64), cdiv(a.N, 64)), a.slices), dim3(T::THREADS), 0, s, a);
   }
   return hipGetLastError();

@@ -32,10 +32,10 @@ __device__ inline void join_stats(float &m, float &s, float m2, float s2) {
   m = top;
 }
 
-// A wave's block row mb of logits (32 rows, 32 NB columns) as fp32 rows in its own part of LDS.
+// A wave's block row mb of logits (16 rows, 16 NB columns) as fp32 rows in its own part of LDS.
 template <class T>
 struct Staged {
-  static constexpr int PITCH = 32 * T::NB * 4 + 16, BYTES = 32 * PITCH;   // rows 4 banks apart
+  static constexpr int PITCH = 16 * T::NB * 4 + 16, BYTES = 16 * PITCH;   // rows 4 banks apart
   static constexpr int LDS = BYTES * T::WM * T::WN;
 };
 
@@ -69,8 +69,8 @@ __global__ __launch_bounds__(T::THREADS) void k_head_stats(HeadArgs p) {
 #pragma unroll
       for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool hit = want == T::col_of(nb, i >> 2) + (i & 3);
+        for (int i = 0; i < 4; ++i) {
+          const bool hit = want == T::col_of(nb) + i;
           got = hit ? t.acc[nb][mb][i] : got;
           here |= hit;
         }
@@ -79,17 +79,15 @@ __global__ __launch_bounds__(T::THREADS) void k_head_stats(HeadArgs p) {
       // rows of fp32 in the wave's own part of LDS; its lanes look the entries' ids through
       char *mine = lds + wave * Staged<T>::BYTES;
 #pragma unroll
-      for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16_t &v = t.acc[nb][mb];
-          *reinterpret_cast<float4 *>(mine + (lane & 31) * Staged<T>::PITCH + 4 * (nb * 32 + 8 * q + 4 * (lane >> 5))) =
-              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        }
+      for (int nb = 0; nb < T::NB; ++nb) {
+        const f32x4_t &v = t.acc[nb][mb];
+        *reinterpret_cast<float4 *>(mine + (lane & 15) * Staged<T>::PITCH + 4 * (nb * 16 + 4 * (lane >> 4))) =
+            make_float4(v[0], v[1], v[2], v[3]);
+      }
       lds_barrier();
-      const int64_t r0 = m0 + (T::wave_m() * T::MB + mb) * 32;
-      const int rows = (int)(p.T - r0 < 32 ? p.T - r0 : 32), first = wn * 32 * T::NB;
-      const int last = left < first + 32 * T::NB ? left : first + 32 * T::NB;
+      const int64_t r0 = m0 + (T::wave_m() * T::MB + mb) * 16;
+      const int rows = (int)(p.T - r0 < 16 ? p.T - r0 : 16), first = wn * 16 * T::NB;
+      const int last = left < first + 16 * T::NB ? left : first + 16 * T::NB;
       for (int e = lane; e < rows * p.k; e += 64) {
         const int64_t at = (int64_t)p.ids[r0 * p.k + e] - n0;
         if (at >= first && at < last)
@@ -101,8 +99,8 @@ __global__ __launch_bounds__(T::THREADS) void k_head_stats(HeadArgs p) {
 #pragma unroll
     for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float z = T::col_of(nb, i >> 2) + (i & 3) < left ? t.acc[nb][mb][i] * c : -__builtin_inff();
+      for (int i = 0; i < 4; ++i) {
+        const float z = T::col_of(nb) + i < left ? t.acc[nb][mb][i] * c : -__builtin_inff();
         t.acc[nb][mb][i] = z;
         m = fmaxf(m, z);
       }
@@ -111,15 +109,16 @@ __global__ __launch_bounds__(T::THREADS) void k_head_stats(HeadArgs p) {
 #pragma unroll
     for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s += __builtin_amdgcn_exp2f(t.acc[nb][mb][i] - top);
+      for (int i = 0; i < 4; ++i) s += __builtin_amdgcn_exp2f(t.acc[nb][mb][i] - top);
+    join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
+    join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
     ms[mb] = m, ss[mb] = s;
-    join_stats(ms[mb], ss[mb], __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
   }
   // the waves of a row, in order
   float2 *red = reinterpret_cast<float2 *>(lds);
 #pragma unroll
   for (int mb = 0; mb < T::MB; ++mb)
-    if (lane < 32) red[wn * T::BM + T::row_of(mb)] = make_float2(ms[mb], ss[mb]);
+    if (lane < 16) red[wn * T::BM + T::row_of(mb)] = make_float2(ms[mb], ss[mb]);
   lds_barrier();
   for (int r = threadIdx.x; r < T::BM; r += T::THREADS) {
     if (m0 + r >= p.T) continue;
@@ -266,19 +265,17 @@ __global__ __launch_bounds__(T::THREADS) void k_head_piece(HeadArgs p) {
     int64_t want = -1;
     if (!TEACH && on) want = (int64_t)p.ids[row] - p.v0 - n0;
 #pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb)
+    for (int nb = 0; nb < T::NB; ++nb) {
+      float v[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = T::col_of(nb, q) + j;
-          float d = __builtin_amdgcn_exp2f(t.acc[nb][mb][4 * q + j] * c - lse);
-          if (!TEACH) d -= want == n ? 1.0f : 0.0f;
-          v[j] = on && n < left ? coef * d : 0.0f;
-        }
-        *reinterpret_cast<uint2 *>(lds + r * T::PITCH + 2 * T::col_of(nb, q)) = pack4(v[0], v[1], v[2], v[3]);
+      for (int j = 0; j < 4; ++j) {
+        const int n = T::col_of(nb) + j;
+        float d = __builtin_amdgcn_exp2f(t.acc[nb][mb][j] * c - lse);
+        if (!TEACH) d -= want == n ? 1.0f : 0.0f;
+        v[j] = on && n < left ? coef * d : 0.0f;
       }
+      *reinterpret_cast<uint2 *>(lds + r * T::PITCH + 2 * T::col_of(nb)) = pack4(v[0], v[1], v[2], v[3]);
+    }
   }
   lds_barrier();
   if constexpr (TEACH) {   // the entries' places, from their logits in fp32
@@ -310,10 +307,10 @@ HeadTile head_tile(int64_t T, int64_t V) {
 
 template <class F>
 void by_head_tile(HeadTile t, F &&f) {
-  if (t.bm == 256) f(GemmTile<2, 4, 4, 2>());
-  else if (t.bm == 128) f(GemmTile<2, 2, 2, 2>());
-  else if (t.bm == 64) f(GemmTile<1, 1, 2, 2>());
-  else f(GemmTile<1, 1, 1, 2>());
+  if (t.bm == 256) f(GemmTile<4, 8, 4, 2>());
+  else if (t.bm == 128) f(GemmTile<4, 4, 2, 2>());
+  else if (t.bm == 64) f(GemmTile<2, 2, 2, 2>());
+  else f(GemmTile<2, 2, 1, 2>());
 }
 
 }  // namespace
