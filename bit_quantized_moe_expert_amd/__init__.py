@@ -99,7 +99,7 @@ def lib() -> ctypes.CDLL:
         "nf4moe_gated_ffn_forward": [vp, vp, i64, vp, vp],
         "nf4moe_gated_ffn_workspace_bytes": [vp, i64],
         "nf4moe_gated_ffn_backward": [vp, vp, vp, i64, vp, vp, vp, vp, sz, vp],
-        "nf4moe_vocab_workspace_bytes": [vp, i64, i32],
+        "nf4moe_vocab_workspace_bytes": [vp, i64, i32, i32],
         "nf4moe_vocab_ce_forward": [vp, vp, i64, vp, vp, vp, vp, sz, vp],
         "nf4moe_vocab_ce_backward": [vp, vp, vp, i64, vp, vp, vp, vp, vp, sz, vp],
         "nf4moe_vocab_distill_forward": [vp, vp, i64, vp, vp, ctypes.c_int, i32, f32, vp, vp, vp, vp, vp, sz, vp],

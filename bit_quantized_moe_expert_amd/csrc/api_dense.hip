@@ -88,6 +88,8 @@ nf4moe_status_t check_teacher(int32_t k, float tau) {
 struct HeadCarve {
   float2 *stats;
   float *picked;
+  uint32_t *list;
+  int32_t *offsets;
   uint16_t *P;
   uint64_t *live;
   float *part;
@@ -95,11 +97,16 @@ struct HeadCarve {
   int slices;
   size_t bytes;
 };
-HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, bool backward) {
+// k: teacher entries a row (0: labels).
+HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, int k, bool backward) {
   HeadCarve c = {};
   Bump b{(char *)ws};
+  if (k) {
+    c.list = b.take<uint32_t>((size_t)cdiv(T, 16) * 16 * k);
+    c.offsets = b.take<int32_t>((size_t)cdiv(T, 16) * (cdiv(h.V, kHeadChunk) + 1));
+  }
   if (!backward) {
-    c.stats = b.take<float2>((size_t)head_stat_tiles(T, h.V) * T);
+    c.stats = b.take<float2>((size_t)head_stat_chunks(T, h.V) * T);
     c.picked = b.take<float>(T);
   } else {
     c.piece = head_piece(T, h.V);
@@ -126,23 +133,18 @@ HeadArgs head_args(const nf4moe_head_t &h, const uint16_t *x, int64_t T, const i
 
 // The gradients of either loss, a piece of the vocabulary after the other.
 nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint16_t *dw, hipStream_t s) {
-  a.P = c.P, a.live = c.live;
-  hipError_t e = dw ? launch_head_live(a, s) : hipSuccess;
+  a.P = c.P, a.live = c.live, a.list = c.list, a.offsets = c.offsets;
+  hipError_t e = launch_head_prepare(a, dw != nullptr, s);
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += c.piece) {
     a.v0 = v0, a.vn = a.V - v0 < c.piece ? a.V - v0 : c.piece, a.vp = c.piece;
     e = launch_head_piece(a, s);
-    if (e == hipSuccess && dw) {
-      ProductArgs p = {};
-      p.x = a.P, p.ldx = c.piece, p.y = a.x, p.ldy = a.H, p.M = a.vn, p.N = a.H, p.K = a.T;
-      p.out = dw + v0 * a.H, p.slices = 1, p.live = c.live;
-      e = launch_product(p, true, s);
-    }
-    if (e == hipSuccess && dx) {
-      ProductArgs p = {};
-      p.x = a.P, p.ldx = c.piece, p.y = a.w + v0 * a.H, p.ldy = a.H, p.M = a.T, p.N = a.H, p.K = a.vn;
-      p.out = c.part ? nullptr : dx, p.part = c.part, p.add = v0 > 0, p.slices = c.slices;
-      e = launch_product(p, false, s);
-    }
+    if (e != hipSuccess) break;
+    ProductArgs px = {}, pw = {};
+    px.x = a.P, px.ldx = c.piece, px.y = a.w + v0 * a.H, px.ldy = a.H, px.M = a.T, px.N = a.H, px.K = a.vn;
+    px.out = c.part ? nullptr : dx, px.part = c.part, px.add = v0 > 0, px.slices = c.slices;
+    pw.x = a.P, pw.ldx = c.piece, pw.y = a.x, pw.ldy = a.H, pw.M = a.vn, pw.N = a.H, pw.K = a.T;
+    pw.out = dw + v0 * a.H, pw.slices = 1, pw.live = c.live;
+    e = launch_products(dx ? &px : nullptr, dw ? &pw : nullptr, s);
   }
   if (e == hipSuccess && dx && c.part) e = launch_join(c.part, c.slices, a.T * a.H, dx, s);
   return hip_status(e, "head backward launch");
@@ -159,7 +161,7 @@ nf4moe_status_t run_head_backward(const nf4moe_head_t &h, HeadArgs a, const floa
   if (!aligned(a.x, 16) || !aligned(h.w, 16) || !aligned(a.ids, 4) || !aligned(dloss, 4) || !aligned(lse, 4) ||
       !aligned(a.q, 4) || !aligned(a.logits, 4))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
-  const HeadCarve c = carve_head(ws, h, T, true);
+  const HeadCarve c = carve_head(ws, h, T, a.k, true);
   nf4moe_status_t st = check_ws(ws, ws_bytes, c.bytes);
   if (st != NF4MOE_OK) return st;
   const uint64_t xb = 2 * (uint64_t)T * h.H, wb = 2 * (uint64_t)h.V * h.H, eb = 4 * (uint64_t)T * (a.k ? a.k : 1);
@@ -227,25 +229,19 @@ nf4moe_status_t nf4moe_gated_ffn_backward(const nf4moe_gated_ffn_t *ffn, const u
   FfnArgs a = ffn_args(f, x, T);
   a.dh = dh, a.dgu = c.dgu, a.h = h;
   hipError_t e = launch_ffn_dgu(a, s);
-  if (e == hipSuccess && dw13) {
-    ProductArgs p = {};
-    p.x = c.dgu, p.ldx = 2 * (int64_t)f.I, p.y = x, p.ldy = f.H, p.M = 2 * (int64_t)f.I, p.N = f.H, p.K = T;
-    p.out = dw13, p.slices = 1;
-    e = launch_product(p, true, s);
-  }
-  if (e == hipSuccess && dx) {
-    ProductArgs p = {};
-    p.x = c.dgu, p.ldx = 2 * (int64_t)f.I, p.y = f.w13, p.ldy = f.H, p.M = T, p.N = f.H, p.K = 2 * (int64_t)f.I;
-    p.out = c.part ? nullptr : dx, p.part = c.part, p.slices = c.slices;
-    e = launch_product(p, false, s);
-    if (e == hipSuccess && c.part) e = launch_join(c.part, c.slices, T * f.H, dx, s);
-  }
+  ProductArgs px = {}, pw = {};
+  px.x = c.dgu, px.ldx = 2 * (int64_t)f.I, px.y = f.w13, px.ldy = f.H, px.M = T, px.N = f.H, px.K = 2 * (int64_t)f.I;
+  px.out = c.part ? nullptr : dx, px.part = c.part, px.slices = c.slices;
+  pw.x = c.dgu, pw.ldx = 2 * (int64_t)f.I, pw.y = x, pw.ldy = f.H, pw.M = 2 * (int64_t)f.I, pw.N = f.H, pw.K = T;
+  pw.out = dw13, pw.slices = 1;
+  if (e == hipSuccess) e = launch_products(dx ? &px : nullptr, dw13 ? &pw : nullptr, s);
+  if (e == hipSuccess && dx && c.part) e = launch_join(c.part, c.slices, T * f.H, dx, s);
   return hip_status(e, "gated feed-forward backward launch");
 }
 
-size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_t backward) {
-  if (T < 1 || check_head(head, T) != NF4MOE_OK) return 0;
-  return carve_head(nullptr, *head, T, backward != 0).bytes;
+size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_t k, int32_t backward) {
+  if (T < 1 || k < 0 || k > kMaxTeacher || check_head(head, T) != NF4MOE_OK) return 0;
+  return carve_head(nullptr, *head, T, k, backward != 0).bytes;
 }
 
 nf4moe_status_t nf4moe_vocab_ce_forward(const nf4moe_head_t *head, const uint16_t *x, int64_t T, const int32_t *labels,
@@ -255,7 +251,7 @@ nf4moe_status_t nf4moe_vocab_ce_forward(const nf4moe_head_t *head, const uint16_
   if (!x || !head->w || !labels || !loss || !lse) return fail(NF4MOE_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(x, 16) || !aligned(head->w, 16) || !aligned(labels, 4) || !aligned(loss, 4) || !aligned(lse, 4))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
-  const HeadCarve c = carve_head(ws, *head, T, false);
+  const HeadCarve c = carve_head(ws, *head, T, 0, false);
   st = check_ws(ws, ws_bytes, c.bytes);
   if (st != NF4MOE_OK) return st;
   const uint64_t rows = 4 * (uint64_t)T;
@@ -288,7 +284,7 @@ nf4moe_status_t nf4moe_vocab_distill_forward(const nf4moe_head_t *head, const ui
   if (!aligned(x, 16) || !aligned(head->w, 16) || !aligned(ids, 4) || !aligned(teacher, dt_bytes(teacher_dtype)) ||
       !aligned(loss, 4) || !aligned(lse, 4) || !aligned(q, 4) || !aligned(logits, 4))
     return fail(NF4MOE_ERR_INVALID_ARG, "misaligned pointer");
-  const HeadCarve c = carve_head(ws, *head, T, false);
+  const HeadCarve c = carve_head(ws, *head, T, k, false);
   st = check_ws(ws, ws_bytes, c.bytes);
   if (st != NF4MOE_OK) return st;
   const uint64_t rows = 4 * (uint64_t)T, n = (uint64_t)T * k;
@@ -298,7 +294,7 @@ nf4moe_status_t nf4moe_vocab_distill_forward(const nf4moe_head_t *head, const ui
   if (st != NF4MOE_OK) return st;
   HeadArgs a = head_args(*head, x, T, ids);
   a.k = k, a.tau = temperature, a.teacher = teacher, a.teacher_bf16 = teacher_dtype == NF4MOE_DT_BF16;
-  a.loss = loss, a.lse = lse, a.q = q, a.logits = logits, a.stats = c.stats;
+  a.loss = loss, a.lse = lse, a.q = q, a.logits = logits, a.stats = c.stats, a.list = c.list, a.offsets = c.offsets;
   return hip_status(launch_head_forward(a, (hipStream_t)stream), "head launch");
 }
 

@@ -21,9 +21,10 @@ struct ProductArgs {
   int slices;
   const uint64_t *live;
 };
-// x as it lies or turned, y turned: the two products of a backward pass.
-hipError_t launch_product(const ProductArgs &a, bool x_turned, hipStream_t s);
-// Slices of K that fill the card for the product with x as it lies.
+// The two products of a backward pass, both with y turned: `dx` with x as it lies, `dw` with x
+// turned, together in one launch where both are given (K > 0).
+hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStream_t s);
+// Slices of K that fill the card (or half of it, beside a second product) for dx.
 int product_slices(int64_t M, int64_t N, int64_t K);
 // out bf16 [n] = the sum of the slices' parts, in order.
 hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s);
@@ -53,17 +54,22 @@ struct HeadArgs {
   bool teacher_bf16;
   float *loss, *lse;         // [T]
   float *q, *logits;         // [T, k]
-  float2 *stats;             // [n tiles][T]: (maximum, sum) of a tile's columns
+  float2 *stats;             // [head_stat_chunks][T]: (maximum, sum) of a chunk of columns
   float *picked;             // [T] the label's logit
+  // both: the teacher's entries of each 16 rows, sorted by their 128 columns (kHeadChunk)
+  uint32_t *list;            // [T / 16][16 k]: j << 11 | row % 16 << 7 | id % 128
+  int32_t *offsets;          // [T / 16][chunks + 1]
   // backward
   const float *dloss;        // [T]
   int64_t v0, vn, vp;        // the piece of the vocabulary, and the row stride of P
   uint16_t *P;               // [T, vp]
   uint64_t *live;            // [T / 64]
 };
-int64_t head_stat_tiles(int64_t T, int64_t V);
+constexpr int kHeadChunk = 128;
+int64_t head_stat_chunks(int64_t T, int64_t V);
 hipError_t launch_head_forward(const HeadArgs &a, hipStream_t s);
-hipError_t launch_head_live(const HeadArgs &a, hipStream_t s);
+// Before the pieces: live (with `with_live`), and the teacher's lists.
+hipError_t launch_head_prepare(const HeadArgs &a, bool with_live, hipStream_t s);
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s);
 int64_t head_piece(int64_t T, int64_t V);
 

@@ -5,8 +5,8 @@
 // the up rows of the same columns in alternating groups, so a lane holds g and u of the same
 // places and the activation needs no exchange; neither g nor u reaches memory.
 // Backward: the same product again, dgu = dh through the activation written in w13's row
-// order, then dx = dgu W13 and dW13 = dgu^T x, which read W13 and x as they lie (gemm16.h's
-// turned sides).
+// order, then dx = dgu W13 and dW13 = dgu^T x in one launch, which read W13 and x as they lie
+// (gemm16.h's turned sides).
 #include "dense.h"
 #include "gemm16.h"
 #include "internal.h"
@@ -29,127 +29,179 @@ __device__ inline float glu_slopes(int glu, float alpha, float limit, float g, f
   return uc * gs;
 }
 
+template <class T>
+struct FfnPlace : GemmTiles {
+  const FfnArgs &p;
+  __device__ FfnPlace(const FfnArgs &a, int b, int nb)
+      : GemmTiles{b, nb, (int)((a.T + T::BM - 1) / T::BM), (a.I + T::BN / 2 - 1) / (T::BN / 2), 1, a.H}, p(a) {}
+  __device__ bool at(int r, int64_t &m0, int64_t &c0) const {
+    int m, n, slice;
+    if (!find(r, m, n, slice)) return false;
+    m0 = (int64_t)m * T::BM, c0 = (int64_t)n * (T::BN / 2);
+    return true;
+  }
+  __device__ bool operator()(int r, typename T::X &x, typename T::Y &y, GemmRange &k) const {
+    int64_t m0, c0;
+    if (!at(r, m0, c0)) return false;
+    x.init(p.x, p.H, m0, p.T);
+    y.template init_pair<T::G>(p.w13, p.w13 + (p.inter ? 1 : (int64_t)p.I) * p.H, (p.inter ? 2 : 1) * (int64_t)p.H, c0, p.I);
+    k = {0, p.H};
+    return true;
+  }
+};
+
 // BACK: dgu (and h where asked for) instead of h.
 template <class T, bool BACK>
-__global__ __launch_bounds__(T::THREADS) void k_ffn(FfnArgs p) {
-  constexpr int G = T::G, HN = T::BN / 2;
+__global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
+  constexpr int G = T::G, HC = 16 * G;   // a wave's columns of h
   __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-  const int mt = (int)((p.T + T::BM - 1) / T::BM), nt = (p.I + HN - 1) / HN;
-  int tm, tn;
-  if (!gemm_tile_of(blockIdx.x, mt, nt, tm, tn)) return;
-  const int64_t m0 = (int64_t)tm * T::BM, c0 = (int64_t)tn * HN;
+  const FfnPlace<T> place(p, blockIdx.x, gridDim.x);
+  int64_t m0, c0;
+  if (!place.at(0, m0, c0)) return;
   T t;
-  t.x.init(p.x, p.H, m0, p.T);
-  if (p.inter) t.y.template init_pair<G>(p.w13, p.w13 + p.H, 2 * (int64_t)p.H, c0, p.I);
-  else t.y.template init_pair<G>(p.w13, p.w13 + (int64_t)p.I * p.H, p.H, c0, p.I);
-  t.run(lds, 0, p.H, nullptr);
-  const int wn = T::wave_n(), g4 = 4 * (int)(threadIdx.x >> 4 & 3);
+  t.run(lds, nullptr, place, [&](int r) __attribute__((always_inline)) {
+    place.at(r, m0, c0);
+    c0 += T::wave_n() * HC;
+    char *mine = T::scratch(lds);
+    const int lane = epilogue_lane();
+    const int64_t cols = p.I - c0, ld2 = 2 * (int64_t)p.I;
+    [[maybe_unused]] uint2 d[T::MB][G];
+    if constexpr (BACK) {   // asked for together
 #pragma unroll
-  for (int mb = 0; mb < T::MB; ++mb) {
-    const int r = T::row_of(mb);
-    char *row = lds + r * T::PITCH;
+      for (int mb = 0; mb < T::MB; ++mb)
 #pragma unroll
-    for (int nb = 0; nb < G; ++nb) {
-      const int c = (wn * G + nb) * 16 + g4;   // column of the tile's HN
-      f32x4_t &gv = t.acc[nb][mb], &uv = t.acc[nb + G][mb];
+        for (int nb = 0; nb < G; ++nb) {
+          const int64_t row = m0 + T::row_at(mb) + (lane & 15);
+          d[mb][nb] = make_uint2(0, 0);
+          if (row < p.T && T::col_of(lane, nb) < cols) d[mb][nb] = *reinterpret_cast<const uint2 *>(p.dh + row * p.I + c0 + T::col_of(lane, nb));
+        }
+    }
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) {
+      const int64_t row0 = m0 + T::row_at(mb), rows = p.T - row0;
+      if (rows <= 0) break;   // the wave
       if constexpr (!BACK) {
-        float h[4];
+        const BlockRow<HC> out{mine, lane};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = glu_value(p.glu, p.alpha, p.limit, gv[j], uv[j]);
-        *reinterpret_cast<uint2 *>(row + 2 * c) = pack4(h[0], h[1], h[2], h[3]);
+        for (int nb = 0; nb < G; ++nb) {
+          float h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[j] = glu_value(p.glu, p.alpha, p.limit, t.acc[nb][mb][j], t.acc[nb + G][mb][j]);
+          out.put(T::col_of(lane, nb), pack4(h[0], h[1], h[2], h[3]));
+        }
+        out.out(p.h + row0 * p.I + c0, p.I, rows, cols);
       } else {
-        uint2 d = make_uint2(0, 0);
-        if (m0 + r < p.T && c0 + c < p.I) d = *reinterpret_cast<const uint2 *>(p.dh + (m0 + r) * p.I + c0 + c);
-        const float dh[4] = {bf16lo_to_f32(d.x), bf16hi_to_f32(d.x), bf16lo_to_f32(d.y), bf16hi_to_f32(d.y)};
-        float dg[4], du[4];
+        const BlockRow<HC> one{mine, lane}, two{mine + 32 * HC, lane};
+        const BlockRow<2 * HC> both{mine, lane};
+        uint2 h[G];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float by_g, by_u;
-          // h takes g's place for the second pass
-          gv[j] = glu_slopes(p.glu, p.alpha, p.limit, gv[j], uv[j], by_g, by_u);
-          dg[j] = dh[j] * by_g, du[j] = dh[j] * by_u;
+        for (int nb = 0; nb < G; ++nb) {
+          const float dh[4] = {bf16lo_to_f32(d[mb][nb].x), bf16hi_to_f32(d[mb][nb].x), bf16lo_to_f32(d[mb][nb].y), bf16hi_to_f32(d[mb][nb].y)};
+          float dg[4], du[4], hv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float by_g, by_u;
+            hv[j] = glu_slopes(p.glu, p.alpha, p.limit, t.acc[nb][mb][j], t.acc[nb + G][mb][j], by_g, by_u);
+            dg[j] = dh[j] * by_g, du[j] = dh[j] * by_u;
+          }
+          h[nb] = pack4(hv[0], hv[1], hv[2], hv[3]);
+          const int c = T::col_of(lane, nb);
+          if (p.inter) {
+            both.put(2 * c, pack4(dg[0], du[0], dg[1], du[1]));
+            both.put(2 * c + 4, pack4(dg[2], du[2], dg[3], du[3]));
+          } else {
+            one.put(c, pack4(dg[0], dg[1], dg[2], dg[3]));
+            two.put(c, pack4(du[0], du[1], du[2], du[3]));
+          }
         }
+        uint16_t *dgu = p.dgu + row0 * ld2;
         if (p.inter) {
-          *reinterpret_cast<uint2 *>(row + 4 * c) = pack4(dg[0], du[0], dg[1], du[1]);
-          *reinterpret_cast<uint2 *>(row + 4 * c + 8) = pack4(dg[2], du[2], dg[3], du[3]);
+          both.out(dgu + 2 * c0, ld2, rows, 2 * cols);
         } else {
-          *reinterpret_cast<uint2 *>(row + 2 * c) = pack4(dg[0], dg[1], dg[2], dg[3]);
-          *reinterpret_cast<uint2 *>(row + 2 * (HN + c)) = pack4(du[0], du[1], du[2], du[3]);
+          one.out(dgu + c0, ld2, rows, cols);
+          two.out(dgu + p.I + c0, ld2, rows, cols);
+        }
+        if (p.h) {
+#pragma unroll
+          for (int nb = 0; nb < G; ++nb) one.put(T::col_of(lane, nb), h[nb]);
+          one.out(p.h + row0 * p.I + c0, p.I, rows, cols);
         }
       }
     }
-  }
-  lds_barrier();
-  const int64_t rows = p.T - m0, cols = p.I - c0;
-  if constexpr (!BACK) {
-    store_tile<T::BM, HN, T::THREADS>(lds, T::PITCH, p.h + m0 * p.I + c0, p.I, rows, cols);
-  } else {
-    const int64_t ld = 2 * (int64_t)p.I;
-    if (p.inter) {
-      store_tile<T::BM, T::BN, T::THREADS>(lds, T::PITCH, p.dgu + m0 * ld + 2 * c0, ld, rows, 2 * cols);
-    } else {
-      store_tile<T::BM, HN, T::THREADS>(lds, T::PITCH, p.dgu + m0 * ld + c0, ld, rows, cols);
-      store_tile<T::BM, HN, T::THREADS>(lds + 2 * HN, T::PITCH, p.dgu + m0 * ld + p.I + c0, ld, rows, cols);
-    }
-    if (!p.h) return;   // the whole grid
-    lds_barrier();
-#pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb)
-#pragma unroll
-      for (int nb = 0; nb < G; ++nb) {
-        const f32x4_t &h = t.acc[nb][mb];
-        *reinterpret_cast<uint2 *>(lds + T::row_of(mb) * T::PITCH + 2 * ((wn * G + nb) * 16 + g4)) = pack4(h[0], h[1], h[2], h[3]);
-      }
-    lds_barrier();
-    store_tile<T::BM, HN, T::THREADS>(lds, T::PITCH, p.h + m0 * p.I + c0, p.I, rows, cols);
-  }
+  });
 }
 
 template <class T>
-__global__ __launch_bounds__(T::THREADS) void k_product(ProductArgs p) {
-  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-  const int mt = (int)((p.M + T::BM - 1) / T::BM), nt = (int)((p.N + T::BN - 1) / T::BN);
-  int tm, tn;
-  if (!gemm_tile_of(blockIdx.x, mt, nt, tm, tn)) return;
-  const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
+struct ProductPlace : GemmTiles {
+  const ProductArgs &p;
+  __device__ ProductPlace(const ProductArgs &a, int b, int nb)
+      : GemmTiles{b, nb, (int)((a.M + T::BM - 1) / T::BM), (int)((a.N + T::BN - 1) / T::BN), a.slices, a.K}, p(a) {}
+  __device__ bool operator()(int r, typename T::X &x, typename T::Y &y, GemmRange &k) const {
+    int m, n, slice;
+    if (!find(r, m, n, slice)) return false;
+    x.init(p.x, p.ldx, (int64_t)m * T::BM, p.M);
+    y.init(p.y, p.ldy, (int64_t)n * T::BN, p.N);
+    k = range_of(slice);
+    return true;
+  }
+};
+
+// The tiles of workgroup b of nb of a product.
+template <class T>
+__device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &p, char *lds, int b, int nb) {
+  const ProductPlace<T> place(p, b, nb);
+  int m, n, slice;
+  if (!place.find(0, m, n, slice)) return;
   T t;
-  t.x.init(p.x, p.ldx, m0, p.M);
-  t.y.init(p.y, p.ldy, n0, p.N);
-  // slices of whole steps
-  const int64_t steps = (p.K + kGemmBK - 1) / kGemmBK, each = (steps + p.slices - 1) / p.slices;
-  const int64_t k0 = blockIdx.y * each * kGemmBK, k1 = k0 + each * kGemmBK < p.K ? k0 + each * kGemmBK : p.K;
-  t.run(lds, k0, k1, p.live);
-  if (p.out) {
+  t.run(lds, p.live, place, [&](int r) __attribute__((always_inline)) {
+    place.find(r, m, n, slice);
+    const int64_t n0 = (int64_t)n * T::BN + T::cols_at(), cols = p.N - n0;
+    if (cols <= 0) return;   // the wave
+    float *part = p.part + (int64_t)slice * p.M * p.N;
+    const int lane = epilogue_lane();
 #pragma unroll
-    for (int mb = 0; mb < T::MB; ++mb)
+    for (int mb = 0; mb < T::MB; ++mb) {
+      const int64_t row0 = (int64_t)m * T::BM + T::row_at(mb), rows = p.M - row0;
+      if (rows <= 0) break;   // the wave
+      if (p.out) {
+        const BlockRow<16 * T::NB> out{T::scratch(lds), lane};
 #pragma unroll
-      for (int nb = 0; nb < T::NB; ++nb) {
-        const f32x4_t &v = t.acc[nb][mb];
-        *reinterpret_cast<uint2 *>(lds + T::row_of(mb) * T::PITCH + 2 * T::col_of(nb)) = pack4(v[0], v[1], v[2], v[3]);
+        for (int nb2 = 0; nb2 < T::NB; ++nb2) {
+          const f32x4_t &v = t.acc[nb2][mb];
+          out.put(T::col_of(lane, nb2), pack4(v[0], v[1], v[2], v[3]));
+        }
+        out.out(p.out + row0 * p.N + n0, p.N, rows, cols);
+        continue;
       }
-    lds_barrier();
-    store_tile<T::BM, T::BN, T::THREADS>(lds, T::PITCH, p.out + m0 * p.N + n0, p.N, p.M - m0, p.N - n0);
-    return;
-  }
-  float *part = p.part + (int64_t)blockIdx.y * p.M * p.N;
-#pragma unroll
-  for (int mb = 0; mb < T::MB; ++mb) {
-    const int64_t m = m0 + T::row_of(mb);
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb) {
-      const int64_t n = n0 + T::col_of(nb);
-      if (n >= p.N) continue;
-      float4 *at = reinterpret_cast<float4 *>(part + m * p.N + n);
-      const f32x4_t &v = t.acc[nb][mb];
-      float4 o = make_float4(v[0], v[1], v[2], v[3]);
+      if ((lane & 15) >= rows) continue;
+      float *at = part + (row0 + (lane & 15)) * p.N + n0;
+      float4 was[T::NB];
       if (p.add) {
-        const float4 was = *at;
-        o = make_float4(was.x + o.x, was.y + o.y, was.z + o.z, was.w + o.w);
+#pragma unroll
+        for (int nb2 = 0; nb2 < T::NB; ++nb2)
+          if (T::col_of(lane, nb2) < cols) was[nb2] = *reinterpret_cast<const float4 *>(at + T::col_of(lane, nb2));
+      } else {
+#pragma unroll
+        for (int nb2 = 0; nb2 < T::NB; ++nb2) was[nb2] = make_float4(0, 0, 0, 0);
       }
-      *at = o;
+#pragma unroll
+      for (int nb2 = 0; nb2 < T::NB; ++nb2) {
+        const f32x4_t &v = t.acc[nb2][mb];
+        if (T::col_of(lane, nb2) < cols)
+          *reinterpret_cast<float4 *>(at + T::col_of(lane, nb2)) =
+              make_float4(was[nb2].x + v[0], was[nb2].y + v[1], was[nb2].z + v[2], was[nb2].w + v[3]);
+      }
     }
-  }
+  });
+}
+
+// Workgroups 0 .. nbx - 1 take dx's tiles, the others dw's.
+template <class TX, class TW>
+__global__ __launch_bounds__(TX::THREADS, TX::WAVES_SIMD) void k_products(ProductArgs dx, ProductArgs dw, int nbx) {
+  static_assert(TX::THREADS == TW::THREADS, "one workgroup size");
+  __shared__ __attribute__((aligned(16))) char lds[TX::LDS > TW::LDS ? TX::LDS : TW::LDS];
+  if ((int)blockIdx.x < nbx) product_tiles<TX>(dx, lds, blockIdx.x, nbx);
+  else product_tiles<TW>(dw, lds, (int)blockIdx.x - nbx, (int)gridDim.x - nbx);
 }
 
 // 8 values a thread, n a multiple of 8.
@@ -170,32 +222,34 @@ __global__ __launch_bounds__(256) void k_join(const float *part, int slices, int
 template <bool BACK>
 hipError_t ffn(const FfnArgs &a, hipStream_t s) {
   auto tiles = [&](int bm, int hn) { return cdiv(a.T, bm) * cdiv(a.I, hn); };
-  if (tiles(256, 128) >= 160) {
-    using T = GemmTile<4, 8, 4, 2, false, false, 4>;
-    hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(cdiv(a.T, 256), cdiv(a.I, 128))), dim3(T::THREADS), 0, s, a);
-  } else if (tiles(128, 64) >= 160) {
-    using T = GemmTile<4, 4, 2, 2, false, false, 2>;
-    hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(cdiv(a.T, 128), cdiv(a.I, 64))), dim3(T::THREADS), 0, s, a);
-  } else {
-    using T = GemmTile<2, 4, 2, 1, false, false, 2>;
-    hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(cdiv(a.T, 64), cdiv(a.I, 32))), dim3(T::THREADS), 0, s, a);
-  }
-  return hipGetLastError();
+  auto go = [&](auto tile) {
+    using T = decltype(tile);
+    hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(tiles(T::BM, T::BN / 2), T::MOST)), dim3(T::THREADS), 0, s, a);
+    return hipGetLastError();
+  };
+  if (tiles(256, 128) >= 160) return go(GemmTile<4, 8, 4, 2, false, false, 4>());
+  if (tiles(128, 64) >= 160) return go(GemmTile<4, 4, 2, 2, false, false, 2>());
+  return go(GemmTile<2, 4, 2, 1, false, false, 2>());
 }
 
-template <bool XT, bool MASK>
-hipError_t product(const ProductArgs &a, hipStream_t s) {
-  auto tiles = [&](int bm, int bn) { return cdiv(a.M, bm) * cdiv(a.N, bn) * a.slices; };
-  if (tiles(256, 256) >= 160) {
-    using T = GemmTile<4, 8, 4, 2, XT, true, 0, MASK>;
-    hipLaunchKernelGGL((k_product<T>), dim3(gemm_grid(cdiv(a.M, 256), cdiv(a.N, 256)), a.slices), dim3(T::THREADS), 0, s, a);
-  } else if (tiles(128, 128) >= 160) {
-    using T = GemmTile<4, 4, 2, 2, XT, true, 0, MASK>;
-    hipLaunchKernelGGL((k_product<T>), dim3(gemm_grid(cdiv(a.M, 128), cdiv(a.N, 128)), a.slices), dim3(T::THREADS), 0, s, a);
+template <int MB, int NB, int WM, int WN, bool MASK>
+hipError_t products(const ProductArgs &dx, const ProductArgs &dw, hipStream_t s) {
+  using TX = GemmTile<MB, NB, WM, WN, false, true>;
+  using TW = GemmTile<MB, NB, WM, WN, true, true, 0, MASK>;
+  const int64_t tx = dx.K ? cdiv(dx.M, TX::BM) * cdiv(dx.N, TX::BN) * dx.slices : 0;
+  const int64_t tw = dw.K ? cdiv(dw.M, TW::BM) * cdiv(dw.N, TW::BN) : 0;
+  int nbx = 0, nbw = 0;
+  if (tx + tw <= TX::MOST) {
+    nbx = tx ? gemm_grid(tx, TX::MOST) : 0, nbw = tw ? gemm_grid(tw, TW::MOST) : 0;
   } else {
-    using T = GemmTile<2, 2, 2, 2, XT, true, 0, MASK>;
-    hipLaunchKernelGGL((k_product<T>), dim3(gemm_grid(cdiv(a.M, 64), cdiv(a.N, 64)), a.slices), dim3(T::THREADS), 0, s, a);
+    // the workgroups that run at a time, shared by the steps that either product takes
+    const double sx = (double)tx * (double)cdiv(dx.K, dx.slices ? dx.slices : 1), sw = (double)tw * (double)dw.K;
+    const int share = (int)(TX::MOST / 8 * sx / (sx + sw) + 0.5) * 8;
+    nbx = !tx ? 0 : !tw ? TX::MOST : share < 8 ? 8 : share > TX::MOST - 8 ? TX::MOST - 8 : share;
+    if (tx) nbx = gemm_grid(tx, nbx);
+    nbw = tw ? gemm_grid(tw, TX::MOST - nbx) : 0;
   }
+  hipLaunchKernelGGL((k_products<TX, TW>), dim3(nbx + nbw), dim3(TX::THREADS), 0, s, dx, dw, nbx);
   return hipGetLastError();
 }
 
@@ -204,14 +258,21 @@ hipError_t product(const ProductArgs &a, hipStream_t s) {
 hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s) { return ffn<false>(a, s); }
 hipError_t launch_ffn_dgu(const FfnArgs &a, hipStream_t s) { return ffn<true>(a, s); }
 
-hipError_t launch_product(const ProductArgs &a, bool x_turned, hipStream_t s) {
-  if (!x_turned) return product<false, false>(a, s);
-  return a.live ? product<true, true>(a, s) : product<true, false>(a, s);
+hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStream_t s) {
+  const ProductArgs none = {};
+  const ProductArgs &x = dx ? *dx : none, &w = dw ? *dw : none;
+  auto tiles = [&](int b) {
+    return (dx ? cdiv(x.M, b) * cdiv(x.N, b) * x.slices : 0) + (dw ? cdiv(w.M, b) * cdiv(w.N, b) : 0);
+  };
+  const bool mask = dw && w.live;
+  if (tiles(256) >= 160) return mask ? products<4, 8, 4, 2, true>(x, w, s) : products<4, 8, 4, 2, false>(x, w, s);
+  if (tiles(128) >= 160) return mask ? products<4, 4, 2, 2, true>(x, w, s) : products<4, 4, 2, 2, false>(x, w, s);
+  return mask ? products<2, 2, 2, 2, true>(x, w, s) : products<2, 2, 2, 2, false>(x, w, s);
 }
 
 int product_slices(int64_t M, int64_t N, int64_t K) {
   const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), steps = cdiv(K, kGemmBK);
-  int64_t s = tiles >= 160 ? 1 : 256 / tiles;
+  int64_t s = 128 / tiles;
   if (s > steps / 8) s = steps / 8;   // at least 8 steps each
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }

@@ -14,7 +14,9 @@
 // one phase ahead. The one barrier of a step stands before its last phase: its own tile is then
 // in registers, the next step's has landed, and the loads of the step after that go out into
 // the place that is free now, in the last phase and the first of the next step. Loads and
-// fragment reads are dealt out between the products.
+// fragment reads are dealt out between the products. A workgroup goes through several tiles
+// without draining this: the loads run on into the next tile's first steps while the tile's
+// epilogue works, in a part of LDS of its own, a wave for itself and without barriers.
 //
 // LDS layouts, without bank conflicts (64 banks, 256 bytes a cycle: 16 lanes of a 16-byte read, 32
 // of an 8-byte one) for the fragment reads. A load's LDS places are fixed, so its lanes ask for
@@ -55,6 +57,23 @@ template <int N>
 __device__ inline void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+
+// Orders a wave's LDS accesses, whose lanes read what others wrote (the hardware keeps their order).
+__device__ inline void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// k values of [kbeg, kend), kbeg a multiple of 64; at least one step (of zeros where there is none).
+struct GemmRange {
+  int64_t kbeg, kend;
+  __device__ int64_t first() const { return kbeg / kGemmBK; }
+  __device__ int64_t last() const {
+    const int64_t l = (kend + kGemmBK - 1) / kGemmBK;
+    return l > first() ? l : first() + 1;
+  }
+};
 
 // One side of a tile: BR rows (of m or n) by a step's 64 k, on its way from memory to fragments.
 template <int BR_, int THREADS, bool TURNED_>
@@ -115,6 +134,11 @@ struct GemmSide {
     }
   }
 
+  __device__ void no_more() {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) voff[i] = kOutside;
+  }
+
   // Piece i of a step's 64 k to LDS at `lds` (this side's stage), zeros from `left` on. live: bit k
   // says whether the step's k row counts (turned sides with MASK).
   template <bool MASK, int G>
@@ -159,140 +183,198 @@ struct GemmTile {
   static_assert(NB % 2 == 0, "two halves of the n blocks");
   using X = GemmSide<BM, THREADS, XT_>;
   using Y = GemmSide<BN, THREADS, YT_>;
-  // Steps of either side in LDS (a third of x, 160 KB, gained nothing).
-  static constexpr int XS = 2, YS = 2, YAT = XS * X::BYTES;
-  static_assert(YS == 2 && XS >= YS, "the order of the loads");
-  // a row of a bf16 output tile in LDS, 16 bytes apart so that 16 rows lie in different banks
-  static constexpr int PITCH = BN * 2 + 16;
-  static constexpr int STAGES = YAT + YS * Y::BYTES, LDS = STAGES > BM * PITCH ? STAGES : BM * PITCH;
+  // Two steps in LDS, and behind them for each wave a block row of its output in bf16.
+  static constexpr int STAGE = X::BYTES + Y::BYTES, SCRATCH = 512 * NB, LDS = 2 * STAGE + SCRATCH * WM * WN;
+  // workgroups that run at a time (by LDS, and 16 waves a CU at these kernels' registers)
+  static constexpr int BY_LDS = (160 << 10) / LDS, BY_WAVES = 16 / (WM * WN);
+  static constexpr int PER_CU = BY_LDS < BY_WAVES ? BY_LDS : BY_WAVES, MOST = 256 * PER_CU;
+  static constexpr int WAVES_SIMD = (PER_CU * WM * WN + 3) / 4;
   X x;
   Y y;
   f32x4_t acc[NB][MB];
 
-  // k values of [kbeg, kend), kbeg a multiple of 64 (0 without a split). live: a word for each 64 k.
-  __device__ __attribute__((always_inline)) void run(char *lds, int64_t kbeg, int64_t kend, const uint64_t *live) {
+  // All of the workgroup's tiles. place(r, x, y): the sides of tile r and its k range (false: there is no
+  // tile r; tile 0 exists); done(r): the epilogue, with the sums in acc. live: a word for each 64 k.
+  template <class Place, class Done>
+  __device__ __attribute__((always_inline)) void run(char *lds, const uint64_t *live, Place place, Done done) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int m = 0; m < MB; ++m)
-        acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const int64_t s0 = kbeg / kGemmBK, s1 = (kend + kGemmBK - 1) / kGemmBK;
-    if (s0 >= s1) return;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-    constexpr int P = X::PER + Y::PER, NP = NB / 2;
-    // Piece i (first of y, then of x) of the steps whose turn it is; past the end zeros, so that the
-    // number of loads on their way is known.
-    auto left = [&](int64_t s) __attribute__((always_inline)) {
-      const int64_t l = kend - s * kGemmBK;
-      return (int)(l < kGemmBK ? l : kGemmBK);
+    constexpr int P = X::PER + Y::PER, NP = NB / 2, P3 = P / 2;   // P3 loads in a step's last phase, the others in the next one's first
+    // where the loads are: tile, step, and what they may touch
+    int tile = 0;
+    GemmRange at;
+    uint64_t mask = 0;
+    place(0, x, y, at);
+    int64_t step = at.first();
+    auto read_mask = [&]() __attribute__((always_inline)) {
+      if constexpr (MASK) mask = step * kGemmBK < at.kend ? live[step] : 0;
     };
-    auto load_x = [&](int64_t s, int i) __attribute__((always_inline)) {
-      x.template load<false, 0>(i, s, left(s), 0, lds0 + (uint32_t)((s - s0) % XS) * X::BYTES);
+    auto load = [&](int stage, int i) __attribute__((always_inline)) {
+      const int64_t l = at.kend - step * kGemmBK;
+      const int left = (int)(l < kGemmBK ? l : kGemmBK);
+      const uint32_t to = lds0 + (uint32_t)stage * STAGE;
+      if (i < Y::PER) y.template load<MASK, G>(i, step, left, mask, to + X::BYTES);
+      else x.template load<false, 0>(i - Y::PER, step, left, 0, to);
     };
-    auto load_y = [&](int64_t s, int i) __attribute__((always_inline)) {
-      y.template load<MASK, G>(i, s, left(s), MASK && s < s1 ? live[s] : 0, lds0 + YAT + (uint32_t)((s - s0) % YS) * Y::BYTES);
-    };
-    auto load = [&](int64_t done, int i) __attribute__((always_inline)) {   // where step `done` was
-      if (i < Y::PER) load_y(done + YS, i);
-      else if (i < P) load_x(done + XS, i - Y::PER);
+    auto advance = [&]() __attribute__((always_inline)) {
+      if (++step < at.last()) return;
+      if (place(++tile, x, y, at)) {
+        step = at.first();
+      } else {
+        x.no_more(), y.no_more();
+        step = 0, at = {0, 0};
+      }
     };
     bf16x8_t fx[2][MB], fy[2][NP];
     // Phase p: k slice p / 2, half p % 2 of the n blocks.
-    auto frag_y = [&](int64_t s, int p, int n) __attribute__((always_inline)) {
-      fy[p & 1][n] = Y::frag(lds + YAT + (int)((s - s0) % YS) * Y::BYTES, wn * NB + p % 2 * NP + n, p / 2);
+    auto frag_y = [&](int stage, int p, int n) __attribute__((always_inline)) {
+      fy[p & 1][n] = Y::frag(lds + stage * STAGE + X::BYTES, wn * NB + p % 2 * NP + n, p / 2);
     };
-    auto frag_x = [&](int64_t s, int p, int m) __attribute__((always_inline)) {
-      fx[p / 2][m] = X::frag(lds + (int)((s - s0) % XS) * X::BYTES, wm * MB + m, p / 2);
+    auto frag_x = [&](int stage, int p, int m) __attribute__((always_inline)) {
+      fx[p / 2][m] = X::frag(lds + stage * STAGE, wm * MB + m, p / 2);
     };
-    auto mma = [&](int p, int n) __attribute__((always_inline)) {
+    read_mask();
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        f32x4_t &c = acc[p % 2 * NP + n][m];
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fy[p & 1][n], fx[p / 2][m], c, 0, 0, 0);
-      }
-    };
-    constexpr int P3 = P / 2;   // loads in the last phase, the others in the next step's first
+    for (int i = 0; i < P; ++i) load(0, i);
+    advance();
+    read_mask();
 #pragma unroll
-    for (int j = -XS; j < 0; ++j)
-#pragma unroll
-      for (int i = 0; i < (j == -1 ? P3 : P); ++i)
-        if (j + (i < Y::PER ? YS : XS) >= 0) load(s0 + j, i);
-    wait_loads<(XS - 2) * X::PER + P3>();
+    for (int i = 0; i < P3; ++i) load(1, i);
+    wait_loads<P3>();
     lds_barrier();
+    int stage = 0;
+    GemmRange now;
+    for (int r = 0; place.range(r, now); ++r) {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) frag_y(s0, 0, n);
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-    for (int m = 0; m < MB; ++m) frag_x(s0, 0, m);
-    for (int64_t s = s0; s < s1; ++s) {
+        for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        if (p == 3) {
-          wait_loads<(XS - 2) * X::PER>();   // step s + 1 has landed
-          lds_barrier();
-        }
-        const int64_t of = p == 3 ? s + 1 : s;
-        const int q = (p + 1) % 4;
+      for (int n = 0; n < NP; ++n) frag_y(stage, 0, n);   // (again: no registers are held through an epilogue)
 #pragma unroll
-        for (int n = 0; n < NP; ++n) {
-          frag_y(of, q, n);
-          if (q % 2 == 0) {
+      for (int m = 0; m < MB; ++m) frag_x(stage, 0, m);
+      for (int64_t s = now.first(); s < now.last(); ++s, stage ^= 1) {
 #pragma unroll
-            for (int m = n * MB / NP; m < (n + 1) * MB / NP; ++m) frag_x(of, q, m);
-          }
+        for (int p = 0; p < 4; ++p) {
+          if (p == 1) advance();
           if (p == 3) {
-#pragma unroll
-            for (int i = n * P3 / NP; i < (n + 1) * P3 / NP; ++i) load(s, i);
+            wait_loads<0>();   // the next step has landed
+            lds_barrier();
           }
-          if (p == 0) {
+          const int of = p == 3 ? stage ^ 1 : stage, q = (p + 1) % 4;
 #pragma unroll
-            for (int i = P3 + n * (P - P3) / NP; i < P3 + (n + 1) * (P - P3) / NP; ++i) load(s - 1, i);
+          for (int n = 0; n < NP; ++n) {
+            frag_y(of, q, n);
+            if (q % 2 == 0) {
+#pragma unroll
+              for (int m = n * MB / NP; m < (n + 1) * MB / NP; ++m) frag_x(of, q, m);
+            }
+            if (p == 2 && n == 0) read_mask();   // its wait is the barrier's
+            if (p == 3) {
+#pragma unroll
+              for (int i = n * P3 / NP; i < (n + 1) * P3 / NP; ++i) load(stage, i);
+            }
+            if (p == 0) {
+#pragma unroll
+              for (int i = P3 + n * (P - P3) / NP; i < P3 + (n + 1) * (P - P3) / NP; ++i) load(stage ^ 1, i);
+            }
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+              f32x4_t &c = acc[p % 2 * NP + n][m];
+              c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fy[p & 1][n], fx[p / 2][m], c, 0, 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
-          mma(p, n);
-          __builtin_amdgcn_sched_barrier(0);
         }
       }
+      done(r);
     }
-    wait_loads<0>();
-    lds_barrier();  // the caller may use the LDS
+    wait_loads<0>();   // none may land after the workgroup's LDS is another's
   }
   __device__ static int wave_m() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WM; }
   __device__ static int wave_n() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) / WM; }
-  // Tile row of this lane's values in block mb, and the first tile column of its four in block nb.
-  __device__ static int row_of(int mb) { return (wave_m() * MB + mb) * 16 + (int)(threadIdx.x & 15); }
-  __device__ static int col_of(int nb) { return (wave_n() * NB + nb) * 16 + 4 * (int)(threadIdx.x >> 4 & 3); }
+  // First tile row of this wave's block row mb (a lane's values are of its row lane % 16), first tile
+  // column of the wave, and the wave's column of a lane's four in block nb.
+  __device__ static int row_at(int mb) { return (wave_m() * MB + mb) * 16; }
+  __device__ static int cols_at() { return wave_n() * NB * 16; }
+  __device__ static int col_of(int lane, int nb) { return nb * 16 + 4 * (lane >> 4); }
+  __device__ static char *scratch(char *lds) {
+    return lds + 2 * STAGE + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * SCRATCH;
+  }
 };
 
-// Rows of a bf16 tile in LDS (pitch bytes apart) to memory, 16 bytes a thread: COLS columns from
-// byte `at` of a row on. rows and cols: how many exist (cols a multiple of 8, out 16-byte aligned).
-template <int ROWS, int COLS, int THREADS>
-__device__ inline void store_tile(const char *lds, int pitch, uint16_t *out, int64_t ld, int64_t rows, int64_t cols) {
-  constexpr int C = COLS / 8, STEP = THREADS / C;
-  static_assert(THREADS % C == 0 && ROWS % STEP == 0, "pieces of a tile");
-  const int c = threadIdx.x % C, r0 = threadIdx.x / C;
-  if (8 * c >= cols) return;
-#pragma unroll
-  for (int i = 0; i < ROWS / STEP; ++i) {
-    const int r = r0 + i * STEP;
-    if (r < rows) *reinterpret_cast<uint4 *>(out + r * ld + 8 * c) = *reinterpret_cast<const uint4 *>(lds + r * pitch + 16 * c);
-  }
+// The lane, as a value that epilogues' addresses are computed from where they are needed and not
+// before the main loop, whose registers they would take.
+__device__ inline int epilogue_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
 }
 __device__ inline uint2 pack4(float a, float b, float c, float d) {
   return make_uint2(f32x2_to_bf16x2_rne(a, b), f32x2_to_bf16x2_rne(c, d));
 }
 
-// The tile of workgroup b of `total` = mt * nt: each XCD (b % 8) takes a run of tiles in an order
-// that goes down 4 tiles of m, then on in n, so that the tiles it works on at a time share
-// their operands in its L2. False where the workgroup has none.
-__device__ inline bool gemm_tile_of(int b, int mt, int nt, int &m, int &n) {
-  const int total = mt * nt, per = (total + 7) >> 3;
-  const int at = (b & 7) * per + (b >> 3);
-  if ((b >> 3) >= per || at >= total) return false;
-  const int band = at / (4 * nt), in = at - band * 4 * nt;
-  const int high = mt - band * 4 < 4 ? mt - band * 4 : 4;
-  m = band * 4 + in % high, n = in / high;
-  return true;
-}
-inline int gemm_grid(int64_t mt, int64_t nt) { return (int)((mt * nt + 7) / 8 * 8); }
+// A wave's block row, 16 rows of COLS bf16, on its way from the products' layout to whole rows in
+// memory: through the wave's own LDS, 16-byte pieces moved so that neither side has bank
+// conflicts, and out in 16 bytes a lane.
+template <int COLS>
+struct BlockRow {
+  static constexpr int C = COLS / 8;
+  static_assert(C == 16 || C == 8 || C == 4 || C == 2, "pieces of a row");
+  char *lds;
+  int lane;
+  __device__ static int place(int row, int piece) { return (row * C + (piece ^ (row * C / 16))) * 16; }
+  // four values of this lane's row, from column `col` on (a multiple of 4)
+  __device__ void put(int col, uint2 v) const {
+    *reinterpret_cast<uint2 *>(lds + place(lane & 15, col >> 3) + (col & 4) * 2) = v;
+  }
+  __device__ uint16_t *one(int row, int col) const {
+    return reinterpret_cast<uint16_t *>(lds + place(row, col >> 3) + (col & 7) * 2);
+  }
+  // rows and cols: how many exist (cols a multiple of 8, out 16-byte aligned)
+  __device__ void out(uint16_t *to, int64_t ld, int64_t rows, int64_t cols) const {
+    wave_lds_order();
+    const int c = lane % C;
+    constexpr int N = 16 * C / 64 > 0 ? 16 * C / 64 : 1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = lane / C + i * (64 / C);
+      if (r < rows && r < 16 && 8 * c < cols)
+        *reinterpret_cast<uint4 *>(to + r * ld + 8 * c) = *reinterpret_cast<const uint4 *>(lds + place(r, c));
+    }
+    wave_lds_order();
+  }
+};
+
+// The tiles of workgroup b of nb (a multiple of 8) of mt * nt tiles in `slices` of k: each XCD (b % 8)
+// takes a run of tiles in an order that goes down 4 tiles of m, then on in n, so that the 32
+// tiles that it works on at a time share their operands in its L2 (without this 1064 TFLOP/s for 1470).
+struct GemmTiles {
+  int b, nb, mt, nt, slices;
+  int64_t K;
+  __device__ bool find(int r, int &m, int &n, int &slice) const {
+    const int each = mt * nt, total = each * slices, per = (total + 7) >> 3, i = (b >> 3) + r * (nb >> 3);
+    const int at = (b & 7) * per + i;
+    if (i >= per || at >= total) return false;
+    slice = at / each;
+    const int in = at - slice * each, band = in / (4 * nt), rest = in - band * 4 * nt;
+    const int high = mt - band * 4 < 4 ? mt - band * 4 : 4;
+    n = rest / high, m = band * 4 + rest - n * high;
+    return true;
+  }
+  // slices of whole steps
+  __device__ GemmRange range_of(int slice) const {
+    const int64_t steps = (K + kGemmBK - 1) / kGemmBK, each = (steps + slices - 1) / slices, k0 = slice * each * kGemmBK;
+    return {k0, k0 + each * kGemmBK < K ? k0 + each * kGemmBK : K};
+  }
+  __device__ bool range(int r, GemmRange &g) const {
+    int m, n, slice;
+    if (!find(r, m, n, slice)) return false;
+    g = range_of(slice);
+    return true;
+  }
+};
+// Workgroups for that many tiles where `most` run at a time.
+inline int gemm_grid(int64_t tiles, int most) { return (int)((tiles < most ? tiles : most) + 7) / 8 * 8; }
 
 }  // namespace nf4moe

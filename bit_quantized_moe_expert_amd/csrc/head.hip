@@ -32,100 +32,114 @@ __device__ inline void join_stats(float &m, float &s, float m2, float s2) {
   m = top;
 }
 
-// A wave's block row mb of logits (16 rows, 16 NB columns) as fp32 rows in its own part of LDS.
 template <class T>
-struct Staged {
-  static constexpr int PITCH = 16 * T::NB * 4 + 16, BYTES = 16 * PITCH;   // rows 4 banks apart
-  static constexpr int LDS = BYTES * T::WM * T::WN;
+struct HeadPlace : GemmTiles {
+  const HeadArgs &p;
+  __device__ HeadPlace(const HeadArgs &a, int b, int nb)
+      : GemmTiles{b, nb, (int)((a.T + T::BM - 1) / T::BM), (int)((a.vn + T::BN - 1) / T::BN), 1, a.H}, p(a) {}
+  // the tile's first row, and its first column of the piece
+  __device__ bool at(int r, int64_t &m0, int64_t &n0) const {
+    int m, n, slice;
+    if (!find(r, m, n, slice)) return false;
+    m0 = (int64_t)m * T::BM, n0 = (int64_t)n * T::BN;
+    return true;
+  }
+  __device__ bool operator()(int r, typename T::X &x, typename T::Y &y, GemmRange &k) const {
+    int64_t m0, n0;
+    if (!at(r, m0, n0)) return false;
+    x.init(p.x, p.H, m0, p.T);
+    y.init(p.w + p.v0 * p.H, p.H, n0, p.vn);
+    k = {0, p.H};
+    return true;
+  }
 };
 
+// f(row, column of the wave's `cols`, entry j) for the teacher's entries of the 16 rows from row0 on
+// whose ids lie in the `cols` columns from v on (cols divides kHeadChunk, v is a multiple of cols).
+template <class F>
+__device__ inline void each_entry(const HeadArgs &p, int lane, int64_t row0, int64_t v, int cols, F &&f) {
+  const int64_t block = row0 >> 4, chunks = (p.V + kHeadChunk - 1) / kHeadChunk;
+  const int32_t *off = p.offsets + block * (chunks + 1) + v / kHeadChunk;
+  const uint32_t *list = p.list + block * 16 * p.k;
+  const int first = off[0], last = off[1];
+  for (int e = first + lane; e < last; e += 64) {
+    const uint32_t w = list[e];
+    const int col = (int)(w & 127) - (int)(v & 127);
+    if (col >= 0 && col < cols) f((int)(w >> 7 & 15), col, (int)(w >> 11));
+  }
+}
+
 template <class T, bool TEACH>
-__global__ __launch_bounds__(T::THREADS) void k_head_stats(HeadArgs p) {
-  constexpr int SIZE = TEACH && Staged<T>::LDS > T::LDS ? Staged<T>::LDS : T::LDS;
-  __shared__ __attribute__((aligned(16))) char lds[SIZE];
-  const int mt = (int)((p.T + T::BM - 1) / T::BM), nt = (int)((p.V + T::BN - 1) / T::BN);
-  int tm, tn;
-  if (!gemm_tile_of(blockIdx.x, mt, nt, tm, tn)) return;
-  const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;
+__global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadArgs p) {
+  constexpr int COLS = 16 * T::NB;   // a wave's
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+  const HeadPlace<T> place(p, blockIdx.x, gridDim.x);
+  int64_t m0, n0;
+  if (!place.at(0, m0, n0)) return;
   T t;
-  t.x.init(p.x, p.H, m0, p.T);
-  t.y.init(p.w, p.H, n0, p.V);
-  t.run(lds, 0, p.H, nullptr);
-  const int wn = T::wave_n(), wave = (int)threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int left = (int)(p.V - n0 < T::BN ? p.V - n0 : T::BN);   // columns that exist
-  const float c = kLog2e / p.tau;
-  float ms[T::MB], ss[T::MB];
+  t.run(lds, nullptr, place, [&](int r) __attribute__((always_inline)) {
+    place.at(r, m0, n0);
+    n0 += T::cols_at();
+    const int lane = epilogue_lane(), left = (int)(p.V - n0 < COLS ? p.V - n0 : COLS);   // columns that exist
+    if (left <= 0) return;   // the wave
+    const float c = kLog2e / p.tau;
 #pragma unroll
-  for (int mb = 0; mb < T::MB; ++mb) {
-    const int64_t row = m0 + T::row_of(mb);
-    if constexpr (!TEACH) {   // the label's logit, by the one lane that has it
-      int want = -1;
-      if (row < p.T) {
-        const int64_t at = (int64_t)p.ids[row] - n0;
-        want = at >= 0 && at < left ? (int)at : -1;
+    for (int mb = 0; mb < T::MB; ++mb) {
+      const int64_t row0 = m0 + T::row_at(mb), row = row0 + (lane & 15);
+      if (row0 >= p.T) break;   // the wave
+      if constexpr (!TEACH) {   // the labels' logits, each by the one lane that has it
+        int want = -1;
+        if (row < p.T) {
+          const int64_t at = (int64_t)p.ids[row] - n0;
+          want = at >= 0 && at < left ? (int)at : -1;
+        }
+        if (__any(want >= 0)) {
+#pragma unroll
+          for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (want == T::col_of(lane, nb) + i) p.picked[row] = t.acc[nb][mb][i];
+        }
+      } else {   // half of the columns at a time as fp32 rows in the wave's own LDS, in 16-byte pieces
+        using Row = BlockRow<COLS>;
+        char *mine = T::scratch(lds);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int nb = 0; nb < T::NB / 2; ++nb)
+            *reinterpret_cast<f32x4_t *>(mine + Row::place(lane & 15, 4 * nb + (lane >> 4))) = t.acc[half * T::NB / 2 + nb][mb];
+          wave_lds_order();
+          each_entry(p, lane, row0, n0, COLS, [&](int er, int col, int j) {
+            const int at = col - half * COLS / 2;
+            if (at >= 0 && at < COLS / 2)
+              p.logits[(row0 + er) * p.k + j] = *reinterpret_cast<const float *>(mine + Row::place(er, at >> 2) + 4 * (at & 3));
+          });
+          wave_lds_order();
+        }
       }
-      float got = 0.0f;
-      bool here = false;
+      if (left < COLS) {
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (T::col_of(lane, nb) + i >= left) t.acc[nb][mb][i] = -__builtin_inff();
+      }
+      float m = -__builtin_inff(), s = 0.0f;
 #pragma unroll
       for (int nb = 0; nb < T::NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool hit = want == T::col_of(nb) + i;
-          got = hit ? t.acc[nb][mb][i] : got;
-          here |= hit;
-        }
-      if (here) p.picked[row] = got;
-    } else {
-      // rows of fp32 in the wave's own part of LDS; its lanes look the entries' ids through
-      char *mine = lds + wave * Staged<T>::BYTES;
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, t.acc[nb][mb][i]);
+      m *= c;
+      const float top = fmaxf(m, kLowest);
 #pragma unroll
-      for (int nb = 0; nb < T::NB; ++nb) {
-        const f32x4_t &v = t.acc[nb][mb];
-        *reinterpret_cast<float4 *>(mine + (lane & 15) * Staged<T>::PITCH + 4 * (nb * 16 + 4 * (lane >> 4))) =
-            make_float4(v[0], v[1], v[2], v[3]);
-      }
-      lds_barrier();
-      const int64_t r0 = m0 + (T::wave_m() * T::MB + mb) * 16;
-      const int rows = (int)(p.T - r0 < 16 ? p.T - r0 : 16), first = wn * 16 * T::NB;
-      const int last = left < first + 16 * T::NB ? left : first + 16 * T::NB;
-      for (int e = lane; e < rows * p.k; e += 64) {
-        const int64_t at = (int64_t)p.ids[r0 * p.k + e] - n0;
-        if (at >= first && at < last)
-          p.logits[r0 * p.k + e] = *reinterpret_cast<const float *>(mine + e / p.k * Staged<T>::PITCH + 4 * (at - first));
-      }
-      lds_barrier();
+      for (int nb = 0; nb < T::NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += __builtin_amdgcn_exp2f(t.acc[nb][mb][i] * c - top);
+      join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
+      join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
+      if (lane < 16 && row < p.T) p.stats[n0 / COLS * p.T + row] = make_float2(m, s);
     }
-    float m = -__builtin_inff();
-#pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float z = T::col_of(nb) + i < left ? t.acc[nb][mb][i] * c : -__builtin_inff();
-        t.acc[nb][mb][i] = z;
-        m = fmaxf(m, z);
-      }
-    const float top = fmaxf(m, kLowest);
-    float s = 0.0f;
-#pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s += __builtin_amdgcn_exp2f(t.acc[nb][mb][i] - top);
-    join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
-    join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
-    ms[mb] = m, ss[mb] = s;
-  }
-  // the waves of a row, in order
-  float2 *red = reinterpret_cast<float2 *>(lds);
-#pragma unroll
-  for (int mb = 0; mb < T::MB; ++mb)
-    if (lane < 16) red[wn * T::BM + T::row_of(mb)] = make_float2(ms[mb], ss[mb]);
-  lds_barrier();
-  for (int r = threadIdx.x; r < T::BM; r += T::THREADS) {
-    if (m0 + r >= p.T) continue;
-    float2 v = red[r];
-    for (int w = 1; w < T::WN; ++w) join_stats(v.x, v.y, red[w * T::BM + r].x, red[w * T::BM + r].y);
-    p.stats[(int64_t)tn * p.T + m0 + r] = v;
-  }
+  });
 }
 
 // A wave a row: q [k] from the teacher's logits. Entries outside the vocabulary count for
@@ -243,55 +257,109 @@ __global__ __launch_bounds__(256) void k_head_live(HeadArgs p) {
   if ((threadIdx.x & 63) == 0 && row < p.T) p.live[row >> 6] = bits;
 }
 
-template <class T, bool TEACH>
-__global__ __launch_bounds__(T::THREADS) void k_head_piece(HeadArgs p) {
-  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
-  const int mt = (int)((p.T + T::BM - 1) / T::BM), nt = (int)((p.vn + T::BN - 1) / T::BN);
-  int tm, tn;
-  if (!gemm_tile_of(blockIdx.x, mt, nt, tm, tn)) return;
-  const int64_t m0 = (int64_t)tm * T::BM, n0 = (int64_t)tn * T::BN;   // column of the piece
-  T t;
-  t.x.init(p.x, p.H, m0, p.T);
-  t.y.init(p.w + p.v0 * p.H, p.H, n0, p.vn);
-  t.run(lds, 0, p.H, nullptr);
-  const int left = (int)(p.vn - n0 < T::BN ? p.vn - n0 : T::BN);
-  const float c = kLog2e / p.tau;
-#pragma unroll
-  for (int mb = 0; mb < T::MB; ++mb) {
-    const int r = T::row_of(mb);
-    const int64_t row = m0 + r;
-    const bool on = row < p.T && row_on(p, row);
-    const float coef = on ? p.dloss[row] * p.tau : 0.0f, lse = on ? p.lse[row] * kLog2e : 0.0f;
-    int64_t want = -1;
-    if (!TEACH && on) want = (int64_t)p.ids[row] - p.v0 - n0;
-#pragma unroll
-    for (int nb = 0; nb < T::NB; ++nb) {
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = T::col_of(nb) + j;
-        float d = __builtin_amdgcn_exp2f(t.acc[nb][mb][j] * c - lse);
-        if (!TEACH) d -= want == n ? 1.0f : 0.0f;
-        v[j] = on && n < left ? coef * d : 0.0f;
-      }
-      *reinterpret_cast<uint2 *>(lds + r * T::PITCH + 2 * T::col_of(nb)) = pack4(v[0], v[1], v[2], v[3]);
-    }
+// A workgroup 16 rows: their entries by chunk of kHeadChunk columns (counts, a scan, places). BACK: those
+// with a probability; else those with an id in the vocabulary. Within a chunk their order is open:
+// each writes to a place of its own.
+template <bool BACK>
+__global__ __launch_bounds__(256) void k_head_lists(HeadArgs p) {
+  extern __shared__ int32_t count[];   // [chunks]
+  __shared__ int32_t total[256];
+  const int t = threadIdx.x, chunks = (int)((p.V + kHeadChunk - 1) / kHeadChunk), each = (chunks + 255) / 256;
+  const int64_t row0 = (int64_t)blockIdx.x * 16, n = (p.T - row0 < 16 ? p.T - row0 : 16) * p.k, base = row0 * p.k;
+  for (int i = t; i < chunks; i += 256) count[i] = 0;
+  lds_barrier();
+  auto id_of = [&](int64_t e) {
+    const int32_t id = p.ids[base + e];
+    return id < 0 || id >= p.V || (BACK && p.q[base + e] == 0.0f) ? -1 : id;
+  };
+  for (int64_t e = t; e < n; e += 256) {
+    const int32_t id = id_of(e);
+    if (id >= 0) atomicAdd(&count[id / kHeadChunk], 1);
   }
   lds_barrier();
-  if constexpr (TEACH) {   // the entries' places, from their logits in fp32
-    const int64_t rows = p.T - m0 < T::BM ? p.T - m0 : T::BM;
-    for (int64_t e = threadIdx.x; e < rows * p.k; e += T::THREADS) {
-      const int64_t at = (int64_t)p.ids[m0 * p.k + e] - p.v0 - n0;
-      if (at < 0 || at >= left) continue;
-      const float q = p.q[m0 * p.k + e];
-      const int r = (int)(e / p.k);
-      if (q == 0.0f || !row_on(p, m0 + r)) continue;
-      const float d = __builtin_amdgcn_exp2f(p.logits[m0 * p.k + e] * c - p.lse[m0 + r] * kLog2e) - q;
-      *reinterpret_cast<uint16_t *>(lds + r * T::PITCH + 2 * at) = (uint16_t)f32_to_bf16_rne(p.dloss[m0 + r] * p.tau * d);
-    }
+  int sum = 0;
+  for (int i = t * each; i < (t + 1) * each && i < chunks; ++i) sum += count[i];
+  total[t] = sum;
+  lds_barrier();
+  for (int d = 1; d < 256; d *= 2) {
+    const int v = t >= d ? total[t - d] : 0;
+    lds_barrier();
+    total[t] += v;
     lds_barrier();
   }
-  store_tile<T::BM, T::BN, T::THREADS>(lds, T::PITCH, p.P + m0 * p.vp + n0, p.vp, p.T - m0, p.vp - n0);
+  int at = total[t] - sum;
+  int32_t *off = p.offsets + (int64_t)blockIdx.x * (chunks + 1);
+  for (int i = t * each; i < (t + 1) * each && i < chunks; ++i) {
+    const int v = count[i];
+    off[i] = at, count[i] = at;
+    at += v;
+  }
+  if (t == 255) off[chunks] = total[255];
+  lds_barrier();
+  for (int64_t e = t; e < n; e += 256) {
+    const int32_t id = id_of(e);
+    if (id < 0) continue;
+    const int row = (int)(e / p.k), j = (int)(e - (int64_t)row * p.k);
+    p.list[base + atomicAdd(&count[id / kHeadChunk], 1)] = (uint32_t)j << 11 | (uint32_t)row << 7 | (uint32_t)(id % kHeadChunk);
+  }
+}
+
+template <class T, bool TEACH>
+__global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadArgs p) {
+  constexpr int COLS = 16 * T::NB;   // a wave's
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+  const HeadPlace<T> place(p, blockIdx.x, gridDim.x);
+  int64_t m0, n0;
+  if (!place.at(0, m0, n0)) return;
+  T t;
+  t.run(lds, nullptr, place, [&](int r) __attribute__((always_inline)) {
+    place.at(r, m0, n0);
+    n0 += T::cols_at();
+    const int lane = epilogue_lane(), left = (int)(p.vn - n0 < COLS ? p.vn - n0 : COLS);
+    if (left <= 0) return;   // the wave
+    const float c = kLog2e / p.tau;
+    const BlockRow<COLS> out{T::scratch(lds), lane};
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) {
+      const int64_t row0 = m0 + T::row_at(mb), row = row0 + (lane & 15);
+      if (row0 >= p.T) break;   // the wave
+      const bool on = row < p.T && row_on(p, row);
+      const float coef = on ? p.dloss[row] * p.tau : 0.0f, lse = on ? p.lse[row] * kLog2e : 0.0f;
+      int want = -1;
+      if (!TEACH && on) {
+        const int64_t at = (int64_t)p.ids[row] - p.v0 - n0;
+        want = at >= 0 && at < left ? (int)at : -1;
+      }
+      const bool some = !TEACH && __any(want >= 0), all = __all(on) && left == COLS;
+#pragma unroll
+      for (int nb = 0; nb < T::NB; ++nb) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __builtin_amdgcn_exp2f(t.acc[nb][mb][j] * c - lse);
+        if (some) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] -= want == T::col_of(lane, nb) + j ? 1.0f : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= coef;
+        if (!all) {   // rows without a gradient and columns past the vocabulary, whatever they hold
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = on && T::col_of(lane, nb) + j < left ? v[j] : 0.0f;
+        }
+        out.put(T::col_of(lane, nb), pack4(v[0], v[1], v[2], v[3]));
+      }
+      if constexpr (TEACH) {   // the entries' places, from their logits in fp32
+        wave_lds_order();
+        each_entry(p, lane, row0, p.v0 + n0, COLS, [&](int er, int col, int j) {
+          const int64_t er0 = row0 + er, e = er0 * p.k + j;
+          if (!row_on(p, er0)) return;
+          const float d = __builtin_amdgcn_exp2f(p.logits[e] * c - p.lse[er0] * kLog2e) - p.q[e];
+          *out.one(er, col) = (uint16_t)f32_to_bf16_rne(p.dloss[er0] * p.tau * d);
+        });
+      }
+      out.out(p.P + row0 * p.vp + n0, p.vp, p.T - row0, p.vp - n0);
+    }
+  });
 }
 
 // The tile of a call: the largest that gives most of the CUs one.
@@ -315,36 +383,43 @@ void by_head_tile(HeadTile t, F &&f) {
 
 }  // namespace
 
-int64_t head_stat_tiles(int64_t T, int64_t V) { return cdiv(V, head_tile(T, V).bn); }
+int64_t head_stat_chunks(int64_t T, int64_t V) {
+  int64_t n = 0;
+  by_head_tile(head_tile(T, V), [&](auto tile) { n = cdiv(V, 16 * decltype(tile)::NB); });
+  return n;
+}
 
-hipError_t launch_head_forward(const HeadArgs &a, hipStream_t s) {
+hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
+  HeadArgs a = args;
+  a.v0 = 0, a.vn = a.V;
   if (a.k) {
     hipLaunchKernelGGL(k_head_teacher, dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(k_head_lists<false>, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 4 * cdiv(a.V, kHeadChunk), s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const HeadTile ht = head_tile(a.T, a.V);
-  by_head_tile(ht, [&](auto tile) {
+  by_head_tile(head_tile(a.T, a.V), [&](auto tile) {
     using T = decltype(tile);
-    const dim3 grid(gemm_grid(cdiv(a.T, T::BM), cdiv(a.V, T::BN)));
+    const dim3 grid(gemm_grid(cdiv(a.T, T::BM) * cdiv(a.V, T::BN), T::MOST));
     if (a.k) hipLaunchKernelGGL((k_head_stats<T, true>), grid, dim3(T::THREADS), 0, s, a);
     else hipLaunchKernelGGL((k_head_stats<T, false>), grid, dim3(T::THREADS), 0, s, a);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_head_join, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 0, s, a, (int)cdiv(a.V, ht.bn));
+  hipLaunchKernelGGL(k_head_join, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 0, s, a, (int)head_stat_chunks(a.T, a.V));
   return hipGetLastError();
 }
 
-hipError_t launch_head_live(const HeadArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(k_head_live, dim3((unsigned)cdiv(a.T, 256)), dim3(256), 0, s, a);
+hipError_t launch_head_prepare(const HeadArgs &a, bool with_live, hipStream_t s) {
+  if (with_live) hipLaunchKernelGGL(k_head_live, dim3((unsigned)cdiv(a.T, 256)), dim3(256), 0, s, a);
+  if (a.k) hipLaunchKernelGGL(k_head_lists<true>, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 4 * cdiv(a.V, kHeadChunk), s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s) {
   by_head_tile(head_tile(a.T, a.vn), [&](auto tile) {
     using T = decltype(tile);
-    const dim3 grid(gemm_grid(cdiv(a.T, T::BM), cdiv(a.vn, T::BN)));
+    const dim3 grid(gemm_grid(cdiv(a.T, T::BM) * cdiv(a.vn, T::BN), T::MOST));
     if (a.k) hipLaunchKernelGGL((k_head_piece<T, true>), grid, dim3(T::THREADS), 0, s, a);
     else hipLaunchKernelGGL((k_head_piece<T, false>), grid, dim3(T::THREADS), 0, s, a);
   });

@@ -92,19 +92,19 @@ def vocab_ce_forward(x, w, labels):
     loss = x.new_empty((T,), dtype=_F32)
     lse = _like(loss)
     L = M.lib()
-    ws, wsp, nb = _scratch(x, L.nf4moe_vocab_workspace_bytes(st, T, 0))
+    ws, wsp, nb = _scratch(x, L.nf4moe_vocab_workspace_bytes(st, T, 0, 0))
     _run(i, L.nf4moe_vocab_ce_forward, st, xp, T, lp, loss.data_ptr(), lse.data_ptr(), wsp, nb)
     return loss, lse
 
 
-def _head_backward(x, w, T, i, st, need, call):
+def _head_backward(x, w, T, k, st, need, call):
     _need(need, ("dx", "dw"))
     out = {}
     if "dx" in need:
         out["dx"] = _like(x)
     if "dw" in need:
         out["dw"] = _like(w)
-    ws, wsp, nb = _scratch(x, M.lib().nf4moe_vocab_workspace_bytes(st, T, 1))
+    ws, wsp, nb = _scratch(x, M.lib().nf4moe_vocab_workspace_bytes(st, T, k, 1))
     call(_p(out.get("dx")), _p(out.get("dw")), wsp, nb)
     return out
 
@@ -115,7 +115,7 @@ def vocab_ce_backward(dloss, x, w, labels, lse, *, need=("dx", "dw")):
     nothing, whatever x and dloss hold there. The same bits on every run."""
     st, xp, T, i = _head_args(x, w)
     gp, lp, sp = _arg(dloss, "dloss", (T,), _F32, i), _arg(labels, "labels", (T,), _I32, i), _arg(lse, "lse", (T,), _F32, i)
-    return _head_backward(x, w, T, i, st, need, lambda dx, dw, ws, nb: _run(
+    return _head_backward(x, w, T, 0, st, need, lambda dx, dw, ws, nb: _run(
         i, M.lib().nf4moe_vocab_ce_backward, st, gp, xp, T, lp, sp, dx, dw, ws, nb))
 
 
@@ -132,13 +132,13 @@ def vocab_distill_forward(x, w, ids, teacher, *, temperature: float = 1.0):
     ip = _arg(ids, "ids", (T, shape[1]), _I32, i)
     _dims(teacher, "teacher", 2)
     dt = _dt(teacher, "teacher")
-    tp = _arg(teacher, "teacher", shape, teacher.dtype, i)
+    tp, k = _arg(teacher, "teacher", shape, teacher.dtype, i), _i32(shape[1], "k")
     loss = x.new_empty((T,), dtype=_F32)
     lse, q = _like(loss), _like(ids, dtype=_F32)
     logits = _like(q)
     L = M.lib()
-    ws, wsp, nb = _scratch(x, L.nf4moe_vocab_workspace_bytes(st, T, 0))
-    _run(i, L.nf4moe_vocab_distill_forward, st, xp, T, ip, tp, dt, _i32(shape[1], "k"), temperature, loss.data_ptr(),
+    ws, wsp, nb = _scratch(x, L.nf4moe_vocab_workspace_bytes(st, T, k, 0))
+    _run(i, L.nf4moe_vocab_distill_forward, st, xp, T, ip, tp, dt, k, temperature, loss.data_ptr(),
          lse.data_ptr(), q.data_ptr(), logits.data_ptr(), wsp, nb)
     return dict(loss=loss, lse=lse, q=q, logits=logits)
 
@@ -148,11 +148,11 @@ def vocab_distill_backward(dloss, x, w, ids, q, logits, lse, *, temperature: flo
     lse. Returns a dict of those in `need`: dx bf16 [T, H], dw bf16 [V, H]. The same bits on
     every run."""
     st, xp, T, i = _head_args(x, w)
-    k = _dims(ids, "ids", 2)[1]
+    k = _i32(_dims(ids, "ids", 2)[1], "k")
     gp, ip = _arg(dloss, "dloss", (T,), _F32, i), _arg(ids, "ids", (T, k), _I32, i)
     qp, op, sp = _arg(q, "q", (T, k), _F32, i), _arg(logits, "logits", (T, k), _F32, i), _arg(lse, "lse", (T,), _F32, i)
-    return _head_backward(x, w, T, i, st, need, lambda dx, dw, ws, nb: _run(
-        i, M.lib().nf4moe_vocab_distill_backward, st, gp, xp, T, ip, qp, op, sp, _i32(k, "k"), temperature, dx, dw, ws, nb))
+    return _head_backward(x, w, T, k, st, need, lambda dx, dw, ws, nb: _run(
+        i, M.lib().nf4moe_vocab_distill_backward, st, gp, xp, T, ip, qp, op, sp, k, temperature, dx, dw, ws, nb))
 
 
 def _ln_args(x, w, b, y_dtype, eps):

@@ -560,9 +560,9 @@ typedef struct {
 } nf4moe_head_t;
 
 /* nf4moe_vocab_workspace_bytes -- workspace of the forward (backward = 0) or the backward (1) of
- * either loss for T rows; 0 for T < 1 or invalid sizes. The backward's holds the gradient of
- * one piece of the vocabulary at a time (at most 128 MB, or 256 columns). */
-size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_t backward);
+ * the cross entropy (k = 0) or of the distillation from k entries a row, for T rows; 0 for T < 1 or
+ * invalid sizes. The backward's holds the gradient of one piece of the vocabulary at a time (at most 128 MB, or 256 columns). */
+size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_t k, int32_t backward);
 
 /* nf4moe_vocab_ce_forward -- softmax cross entropy: lse[t] = log sum_v exp(l[t, v]) and loss[t] =
  * lse[t] - l[t, labels[t]], fp32 [T]; a label outside [0, V) (-100, say) means loss 0 and no

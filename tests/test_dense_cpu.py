@@ -160,7 +160,7 @@ def ds_bwd(d=None, dloss=far(0), x=far(1), T=4, labels=far(2), q=far(10), logits
 
 
 def test_head_validation():
-    for f, back in ((ce_fwd, 0), (ds_fwd, 0), (ce_bwd, 1), (ds_bwd, 1)):
+    for f, k, back in ((ce_fwd, 0, 0), (ds_fwd, 3, 0), (ce_bwd, 0, 1), (ds_bwd, 3, 1)):
         for bad in (dict(H=0), dict(H=12), dict(H=(1 << 20) + 8), dict(V=0), dict(V=-3), dict(V=(1 << 21) + 1)):
             assert f(head_desc(**bad)) == INVALID, bad
         assert f(T=-1) == INVALID and f(T=(1 << 30) + 1) == INVALID
@@ -169,7 +169,7 @@ def test_head_validation():
         for name in ("x", "labels", "lse"):
             assert f(**{name: None}) == INVALID, name
         assert f(x=far(0) + 8) == INVALID and f(labels=far(1) + 2) == INVALID and f(lse=far(3) + 1) == INVALID
-        need = L.nf4moe_vocab_workspace_bytes(head_desc(), 4, back)
+        need = L.nf4moe_vocab_workspace_bytes(head_desc(), 4, k, back)
         assert need > 0 and f(n=need - 1) == WORKSPACE and f(ws=None) == WORKSPACE and f(ws=far(20) + 64) == INVALID
         if not GPU:
             assert f(n=need) == HIP
@@ -185,14 +185,15 @@ def test_head_validation():
             assert f(tau=tau) == INVALID, tau
     assert ds_fwd(tdt=2) == INVALID and ds_fwd(t=None) == INVALID and ds_fwd(t=far(2) + 2) == INVALID
     assert ds_fwd(t=far(2) + 1, tdt=1) == INVALID
-    assert L.nf4moe_vocab_workspace_bytes(head_desc(), 0, 1) == 0 and L.nf4moe_vocab_workspace_bytes(head_desc(V=0), 4, 0) == 0
+    assert L.nf4moe_vocab_workspace_bytes(head_desc(), 0, 0, 1) == 0 and L.nf4moe_vocab_workspace_bytes(head_desc(V=0), 4, 0, 0) == 0
+    assert L.nf4moe_vocab_workspace_bytes(head_desc(), 4, -1, 0) == 0 and L.nf4moe_vocab_workspace_bytes(head_desc(), 4, 1025, 1) == 0
 
 
 def test_head_backward_workspace_is_bounded():
     """P never takes more than 128 MB or 256 columns, whatever the vocabulary."""
     for T in (1, 100, 4096, 65536, 1 << 20):
         for V in (100, 50304, 1 << 21):
-            n = L.nf4moe_vocab_workspace_bytes(head_desc(H=64, V=V), T, 1)
+            n = L.nf4moe_vocab_workspace_bytes(head_desc(H=64, V=V), T, 0, 1)
             if not n:       # too many tiles
                 continue
             P = max(128 << 20, 2 * 256 * T)
@@ -259,7 +260,7 @@ def test_outputs_over_other_arrays_are_refused():
     overlaps_refused(lambda dh, x, w13, dx, dw13, h, workspace: L.nf4moe_gated_ffn_backward(d(w13), dh, x, T, dx, dw13, h, workspace, need, None),
                      dict(dx=2 * T * H, dw13=4 * I * H, h=2 * T * I, workspace=need), dict(dh=2 * T * I, x=2 * T * H, w13=4 * I * H))
     d = lambda w: head_desc(H, V, w)  # noqa: E731
-    n0, n1 = (L.nf4moe_vocab_workspace_bytes(head_desc(H, V), T, b) for b in (0, 1))
+    n0, n1, m0, m1 = (L.nf4moe_vocab_workspace_bytes(head_desc(H, V), T, e, b) for e in (0, k) for b in (0, 1))
     xw = dict(x=2 * T * H, w=2 * V * H)
     overlaps_refused(lambda x, w, labels, loss, lse, workspace: ce_fwd(d(w), x, T, labels, loss, lse, workspace, n0),
                      dict(loss=4 * T, lse=4 * T, workspace=n0), dict(**xw, labels=4 * T))
@@ -267,11 +268,11 @@ def test_outputs_over_other_arrays_are_refused():
                      dict(dx=2 * T * H, dw=2 * V * H, workspace=n1), dict(**xw, ids=4 * T, dloss=4 * T, lse=4 * T))
     e = 4 * T * k
     overlaps_refused(lambda x, w, ids, teacher, loss, lse, q, logits, workspace: ds_fwd(
-        d(w), x, T, ids, teacher, 0, k, 1.0, loss, lse, q, logits, workspace, n0),
-        dict(loss=4 * T, lse=4 * T, q=e, logits=e, workspace=n0), dict(**xw, ids=e, teacher=e))
+        d(w), x, T, ids, teacher, 0, k, 1.0, loss, lse, q, logits, workspace, m0),
+        dict(loss=4 * T, lse=4 * T, q=e, logits=e, workspace=m0), dict(**xw, ids=e, teacher=e))
     overlaps_refused(lambda x, w, ids, q, logits, dloss, lse, dx, dw, workspace: ds_bwd(
-        d(w), dloss, x, T, ids, q, logits, lse, k, 1.0, dx, dw, workspace, n1),
-        dict(dx=2 * T * H, dw=2 * V * H, workspace=n1), dict(**xw, ids=e, q=e, logits=e, dloss=4 * T, lse=4 * T))
+        d(w), dloss, x, T, ids, q, logits, lse, k, 1.0, dx, dw, workspace, m1),
+        dict(dx=2 * T * H, dw=2 * V * H, workspace=m1), dict(**xw, ids=e, q=e, logits=e, dloss=4 * T, lse=4 * T))
     for xdt, ydt in ((0, 1), (1, 0)):
         xb, yb = T * H * (4 - 2 * xdt), T * H * (4 - 2 * ydt)
         d = lambda w, b=None: ln_desc(H, xdt, ydt, w, b)  # noqa: E731, B023
