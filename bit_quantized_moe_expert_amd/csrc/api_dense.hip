@@ -58,11 +58,12 @@ struct FfnCarve {
   int slices;
   size_t bytes;
 };
+// One size whatever outputs are asked for: that of dx alone, which has the most slices.
 FfnCarve carve_ffn(void *ws, const nf4moe_gated_ffn_t &f, int64_t T) {
   FfnCarve c = {};
   Bump b{(char *)ws};
   c.dgu = b.take<uint16_t>((size_t)T * 2 * f.I);
-  c.slices = product_slices(T, f.H, 2 * (int64_t)f.I);
+  c.slices = product_slices(T, f.H, 2 * (int64_t)f.I, true);
   if (c.slices > 1) c.part = b.take<float>((size_t)c.slices * T * f.H);
   c.bytes = b.off;
   return c;
@@ -97,7 +98,7 @@ struct HeadCarve {
   int slices;
   size_t bytes;
 };
-// k: teacher entries a row (0: labels).
+// k: teacher entries a row (0: labels). One size whatever outputs are asked for.
 HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, int k, bool backward) {
   HeadCarve c = {};
   Bump b{(char *)ws};
@@ -106,13 +107,13 @@ HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, int k, bool ba
     c.offsets = b.take<int32_t>((size_t)cdiv(T, 16) * (cdiv(h.V, kHeadChunk) + 1));
   }
   if (!backward) {
-    c.stats = b.take<float2>((size_t)head_stat_chunks(T, h.V) * T);
+    c.stats = b.take<float2>((size_t)head_stat_chunks(T, h.V, h.H) * T);
     c.picked = b.take<float>(T);
   } else {
     c.piece = head_piece(T, h.V);
     c.P = b.take<uint16_t>((size_t)T * c.piece);
     c.live = b.take<uint64_t>((size_t)cdiv(T, 64));
-    c.slices = product_slices(T, h.H, c.piece < h.V ? c.piece : h.V);
+    c.slices = product_slices(T, h.H, c.piece < h.V ? c.piece : h.V, true);
     if (c.slices > 1 || c.piece < h.V) c.part = b.take<float>((size_t)c.slices * T * h.H);
   }
   c.bytes = b.off;
@@ -133,6 +134,8 @@ HeadArgs head_args(const nf4moe_head_t &h, const uint16_t *x, int64_t T, const i
 
 // The gradients of either loss, a piece of the vocabulary after the other.
 nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint16_t *dw, hipStream_t s) {
+  const int slices = product_slices(a.T, a.H, c.piece < a.V ? c.piece : a.V, !dw);
+  const bool parts = slices > 1 || c.piece < a.V;
   a.P = c.P, a.live = c.live, a.list = c.list, a.offsets = c.offsets;
   hipError_t e = launch_head_prepare(a, dw != nullptr, s);
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += c.piece) {
@@ -141,12 +144,12 @@ nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint
     if (e != hipSuccess) break;
     ProductArgs px = {}, pw = {};
     px.x = a.P, px.ldx = c.piece, px.y = a.w + v0 * a.H, px.ldy = a.H, px.M = a.T, px.N = a.H, px.K = a.vn;
-    px.out = c.part ? nullptr : dx, px.part = c.part, px.add = v0 > 0, px.slices = c.slices;
+    px.out = parts ? nullptr : dx, px.part = c.part, px.add = v0 > 0, px.slices = slices;
     pw.x = a.P, pw.ldx = c.piece, pw.y = a.x, pw.ldy = a.H, pw.M = a.vn, pw.N = a.H, pw.K = a.T;
     pw.out = dw + v0 * a.H, pw.slices = 1, pw.live = c.live;
     e = launch_products(dx ? &px : nullptr, dw ? &pw : nullptr, s);
   }
-  if (e == hipSuccess && dx && c.part) e = launch_join(c.part, c.slices, a.T * a.H, dx, s);
+  if (e == hipSuccess && dx && parts) e = launch_join(c.part, slices, a.T * a.H, dx, s);
   return hip_status(e, "head backward launch");
 }
 
@@ -229,13 +232,14 @@ nf4moe_status_t nf4moe_gated_ffn_backward(const nf4moe_gated_ffn_t *ffn, const u
   FfnArgs a = ffn_args(f, x, T);
   a.dh = dh, a.dgu = c.dgu, a.h = h;
   hipError_t e = launch_ffn_dgu(a, s);
+  const int slices = product_slices(T, f.H, 2 * (int64_t)f.I, !dw13);
   ProductArgs px = {}, pw = {};
   px.x = c.dgu, px.ldx = 2 * (int64_t)f.I, px.y = f.w13, px.ldy = f.H, px.M = T, px.N = f.H, px.K = 2 * (int64_t)f.I;
-  px.out = c.part ? nullptr : dx, px.part = c.part, px.slices = c.slices;
+  px.out = slices > 1 ? nullptr : dx, px.part = c.part, px.slices = slices;
   pw.x = c.dgu, pw.ldx = 2 * (int64_t)f.I, pw.y = x, pw.ldy = f.H, pw.M = 2 * (int64_t)f.I, pw.N = f.H, pw.K = T;
   pw.out = dw13, pw.slices = 1;
   if (e == hipSuccess) e = launch_products(dx ? &px : nullptr, dw13 ? &pw : nullptr, s);
-  if (e == hipSuccess && dx && c.part) e = launch_join(c.part, c.slices, T * f.H, dx, s);
+  if (e == hipSuccess && dx && slices > 1) e = launch_join(c.part, slices, T * f.H, dx, s);
   return hip_status(e, "gated feed-forward backward launch");
 }
 

@@ -24,8 +24,8 @@ struct ProductArgs {
 // The two products of a backward pass, both with y turned: `dx` with x as it lies, `dw` with x
 // turned, together in one launch where both are given (K > 0).
 hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStream_t s);
-// Slices of K that fill the card (or half of it, beside a second product) for dx.
-int product_slices(int64_t M, int64_t N, int64_t K);
+// Slices of K that fill the card (alone) or half of it (beside a second product) for dx.
+int product_slices(int64_t M, int64_t N, int64_t K, bool alone);
 // out bf16 [n] = the sum of the slices' parts, in order.
 hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s);
 
@@ -66,7 +66,7 @@ struct HeadArgs {
   uint64_t *live;            // [T / 64]
 };
 constexpr int kHeadChunk = 128;
-int64_t head_stat_chunks(int64_t T, int64_t V);
+int64_t head_stat_chunks(int64_t T, int64_t V, int H);
 hipError_t launch_head_forward(const HeadArgs &a, hipStream_t s);
 // Before the pieces: live (with `with_live`), and the teacher's lists.
 hipError_t launch_head_prepare(const HeadArgs &a, bool with_live, hipStream_t s);

@@ -131,6 +131,28 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
   });
 }
 
+// Up to 16 MB tokens: a workgroup takes eight gate rows and their up rows.
+template <int MB>
+__global__ __launch_bounds__(512) void k_ffn_few(FfnArgs p) {
+  using F = FewRows<1, MB, 8>;
+  __shared__ __attribute__((aligned(16))) char lds[F::LDS];
+  const int c0 = (int)blockIdx.x * 8, T = (int)p.T;
+  f32x4_t v = F::run(
+      lds, p.H,
+      [&](int i) {
+        const int64_t c = c0 + (i & 7);
+        return p.w13 + (p.inter ? 2 * c + (i >> 3) : c + (i >> 3) * (int64_t)p.I) * p.H;
+      },
+      [&](int i) { return p.x + (int64_t)(i < T ? i : T - 1) * p.H; });
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, token = 16 * wave + (lane & 15);
+  if (wave >= MB) return;
+  float h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = glu_value(p.glu, p.alpha, p.limit, v[j], __shfl_xor(v[j], 32, kWave));   // (lanes 0 .. 31: the gate rows)
+  if (lane < 32 && token < T)
+    *reinterpret_cast<uint2 *>(p.h + (int64_t)token * p.I + c0 + 4 * (lane >> 4)) = pack4(h[0], h[1], h[2], h[3]);
+}
+
 template <class T>
 struct ProductPlace : GemmTiles {
   const ProductArgs &p;
@@ -219,29 +241,42 @@ __global__ __launch_bounds__(256) void k_join(const float *part, int slices, int
   *reinterpret_cast<uint4 *>(out + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-template <bool BACK>
-hipError_t ffn(const FfnArgs &a, hipStream_t s) {
-  auto tiles = [&](int bm, int hn) { return cdiv(a.T, bm) * cdiv(a.I, hn); };
-  auto go = [&](auto tile) {
-    using T = decltype(tile);
-    hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(gemm_grid(tiles(T::BM, T::BN / 2), T::MOST)), dim3(T::THREADS), 0, s, a);
-    return hipGetLastError();
-  };
-  if (tiles(256, 128) >= 160) return go(GemmTile<4, 8, 4, 2, false, false, 4>());
-  if (tiles(128, 64) >= 160) return go(GemmTile<4, 4, 2, 2, false, false, 2>());
-  return go(GemmTile<2, 4, 2, 1, false, false, 2>());
+int64_t ffn_tile_count(const void *args, int b) {
+  const FfnArgs &a = *static_cast<const FfnArgs *>(args);
+  return cdiv(a.T, b) * cdiv(a.I, b / 2);
 }
 
-template <int MB, int NB, int WM, int WN, bool MASK>
+template <bool BACK>
+hipError_t ffn(const FfnArgs &a, hipStream_t s) {
+  auto go = [&](auto tile) {
+    using T = typename decltype(tile)::type;
+    const int64_t tiles = cdiv(a.T, T::BM) * cdiv(a.I, T::BN / 2);
+    const int grid = T::KS > 1 ? (int)cdiv(tiles, 8) * 8 : gemm_grid(tiles, T::MOST);
+    hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(grid), dim3(T::THREADS), 0, s, a);
+    return hipGetLastError();
+  };
+  switch (gemm_class(ffn_tile_count, &a, cdiv(a.H, kGemmBK))) {
+    case 256: return go(TileTag<GemmTile<4, 8, 4, 2, false, false, 4>>());
+    case 128: return go(TileTag<GemmTile<4, 4, 2, 2, false, false, 2>>());
+    case 64: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2>>());
+    default: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2, false, 4>>());
+  }
+}
+
+struct ProductPair {
+  const ProductArgs &x, &w;
+};
+int64_t product_tile_count(const void *args, int b) {
+  const ProductPair &a = *static_cast<const ProductPair *>(args);
+  return (a.x.K ? cdiv(a.x.M, b) * cdiv(a.x.N, b) * a.x.slices : 0) + (a.w.K ? cdiv(a.w.M, b) * cdiv(a.w.N, b) : 0);
+}
+
+template <class TX, class TW>
 hipError_t products(const ProductArgs &dx, const ProductArgs &dw, hipStream_t s) {
-  using TX = GemmTile<MB, NB, WM, WN, false, true>;
-  using TW = GemmTile<MB, NB, WM, WN, true, true, 0, MASK>;
   const int64_t tx = dx.K ? cdiv(dx.M, TX::BM) * cdiv(dx.N, TX::BN) * dx.slices : 0;
   const int64_t tw = dw.K ? cdiv(dw.M, TW::BM) * cdiv(dw.N, TW::BN) : 0;
-  int nbx = 0, nbw = 0;
-  if (tx + tw <= TX::MOST) {
-    nbx = tx ? gemm_grid(tx, TX::MOST) : 0, nbw = tw ? gemm_grid(tw, TW::MOST) : 0;
-  } else {
+  int nbx = (int)cdiv(tx, 8) * 8, nbw = (int)cdiv(tw, 8) * 8;
+  if (TX::KS == 1 && tx + tw > TX::MOST) {
     // the workgroups that run at a time, shared by the steps that either product takes
     const double sx = (double)tx * (double)cdiv(dx.K, dx.slices ? dx.slices : 1), sw = (double)tw * (double)dw.K;
     const int share = (int)(TX::MOST / 8 * sx / (sx + sw) + 0.5) * 8;
@@ -252,27 +287,42 @@ hipError_t products(const ProductArgs &dx, const ProductArgs &dw, hipStream_t s)
   hipLaunchKernelGGL((k_products<TX, TW>), dim3(nbx + nbw), dim3(TX::THREADS), 0, s, dx, dw, nbx);
   return hipGetLastError();
 }
+template <int MB, int NB, int WM, int WN, bool MASK, int KS = 1>
+hipError_t products_of(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
+  return products<GemmTile<MB, NB, WM, WN, false, true, 0, false, KS>, GemmTile<MB, NB, WM, WN, true, true, 0, MASK, KS>>(x, w, s);
+}
+template <bool MASK>
+hipError_t products(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
+  const ProductPair both{x, w};
+  const int64_t steps = cdiv(x.K > w.K ? x.K : w.K, kGemmBK);
+  switch (gemm_class(product_tile_count, &both, steps)) {
+    case 256: return products_of<4, 8, 4, 2, MASK>(x, w, s);
+    case 128: return products_of<4, 4, 2, 2, MASK>(x, w, s);
+    case 64: return products_of<2, 2, 2, 2, MASK>(x, w, s);
+    default: return products_of<2, 2, 2, 2, MASK, 4>(x, w, s);
+  }
+}
 
 }  // namespace
 
-hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s) { return ffn<false>(a, s); }
+hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s) {
+  if (a.T > 32) return ffn<false>(a, s);
+  // (the widest I is 2^20: 2^17 workgroups of 512)
+  if (a.T > 16) hipLaunchKernelGGL(k_ffn_few<2>, dim3((unsigned)(a.I / 8)), dim3(512), 0, s, a);
+  else hipLaunchKernelGGL(k_ffn_few<1>, dim3((unsigned)(a.I / 8)), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
 hipError_t launch_ffn_dgu(const FfnArgs &a, hipStream_t s) { return ffn<true>(a, s); }
 
 hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStream_t s) {
   const ProductArgs none = {};
   const ProductArgs &x = dx ? *dx : none, &w = dw ? *dw : none;
-  auto tiles = [&](int b) {
-    return (dx ? cdiv(x.M, b) * cdiv(x.N, b) * x.slices : 0) + (dw ? cdiv(w.M, b) * cdiv(w.N, b) : 0);
-  };
-  const bool mask = dw && w.live;
-  if (tiles(256) >= 160) return mask ? products<4, 8, 4, 2, true>(x, w, s) : products<4, 8, 4, 2, false>(x, w, s);
-  if (tiles(128) >= 160) return mask ? products<4, 4, 2, 2, true>(x, w, s) : products<4, 4, 2, 2, false>(x, w, s);
-  return mask ? products<2, 2, 2, 2, true>(x, w, s) : products<2, 2, 2, 2, false>(x, w, s);
+  return w.live ? products<true>(x, w, s) : products<false>(x, w, s);
 }
 
-int product_slices(int64_t M, int64_t N, int64_t K) {
+int product_slices(int64_t M, int64_t N, int64_t K, bool alone) {
   const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), steps = cdiv(K, kGemmBK);
-  int64_t s = 128 / tiles;
+  int64_t s = (alone ? 256 : 128) / tiles;
   if (s > steps / 8) s = steps / 8;   // at least 8 steps each
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }

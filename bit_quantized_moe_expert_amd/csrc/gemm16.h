@@ -73,9 +73,15 @@ struct GemmRange {
     const int64_t l = (kend + kGemmBK - 1) / kGemmBK;
     return l > first() ? l : first() + 1;
   }
+  // Part g of n, whole steps; the first is the longest.
+  __device__ GemmRange part(int g, int n) const {
+    const int64_t each = (last() - first() + n - 1) / n * kGemmBK, b = kbeg + g * each;
+    return {b, b + each < kend ? b + each : kend};
+  }
 };
 
-// One side of a tile: BR rows (of m or n) by a step's 64 k, on its way from memory to fragments.
+// One side of a tile: BR rows (of m or n) by a step's 64 k, on its way from memory to fragments, moved by
+// THREADS threads (`tid` among them).
 template <int BR_, int THREADS, bool TURNED_>
 struct GemmSide {
   static constexpr int BR = BR_;
@@ -98,9 +104,11 @@ struct GemmSide {
   __device__ static int turned_swizzle(int k) {
     return ROWC >= 16 ? (k & 3) << 1 | (k & 8) : (k & 2) | (k & 8) >> 1;
   }
+  __device__ static int tid() { return (int)threadIdx.x % THREADS; }
+  __device__ static int wave() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % (THREADS / 64); }
   __device__ void place() {
-    row = threadIdx.x / ROWC;
-    piece = (int)(threadIdx.x % ROWC) ^ (TURNED ? turned_swizzle(row) : row >> 1 & 7);
+    row = tid() / ROWC;
+    piece = tid() % ROWC ^ (TURNED ? turned_swizzle(row) : row >> 1 & 7);
   }
 
   // Element (r, k) at p[r * ld + k], turned at p[k * ld + r]; the tile's first row is r0, rows at
@@ -146,10 +154,9 @@ struct GemmSide {
     const int k = TURNED ? row + i * RSTEP : piece * 8;
     bool in = k < left;
     if constexpr (MASK) in = in && (live >> (k & 63) & 1);
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int which = G > 0 ? i * RSTEP / (16 * (G > 0 ? G : 1)) % 2 : 0;
     load_to_lds(rsrc_at(base[which] + step * kstep), in ? voff[i] : kOutside,
-                lds + (uint32_t)(wave * 64 + i * THREADS) * 16);
+                lds + (uint32_t)(wave() * 64 + i * THREADS) * 16);
   }
   // Fragment of the tile's rows 16 blk .. + 15 at the step's k 32 kk .. + 31: lane's row lane % 16, its k
   // 8 (lane / 16) .. + 7.
@@ -174,21 +181,24 @@ struct GemmSide {
 };
 
 // MB x NB blocks of 16 x 16 a wave, WM x WN waves; XT / YT: a side is turned. G > 0: the n side
-// is pairs (init_pair<G>). MASK: k rows of the turned n side count by their bit in `live`.
-template <int MB_, int NB_, int WM_, int WN_, bool XT_ = false, bool YT_ = false, int G_ = 0, bool MASK_ = false>
+// is pairs (init_pair<G>). MASK: k rows of the turned n side count by their bit in `live`. KS > 1: so many
+// groups of WM x WN waves share a tile, each with a part of its k (small products, whose time is the
+// steps' latency); a workgroup has one tile then.
+template <int MB_, int NB_, int WM_, int WN_, bool XT_ = false, bool YT_ = false, int G_ = 0, bool MASK_ = false, int KS_ = 1>
 struct GemmTile {
+  static constexpr int KS = KS_, GROUP = 64 * WM_ * WN_;
   static constexpr int MB = MB_, NB = NB_, WM = WM_, WN = WN_, G = G_;
   static constexpr bool MASK = MASK_;
-  static constexpr int BM = 16 * MB * WM, BN = 16 * NB * WN, THREADS = 64 * WM * WN;
+  static constexpr int BM = 16 * MB * WM, BN = 16 * NB * WN, THREADS = GROUP * KS;
   static_assert(NB % 2 == 0, "two halves of the n blocks");
-  using X = GemmSide<BM, THREADS, XT_>;
-  using Y = GemmSide<BN, THREADS, YT_>;
+  using X = GemmSide<BM, GROUP, XT_>;
+  using Y = GemmSide<BN, GROUP, YT_>;
   // Two steps in LDS, and behind them for each wave a block row of its output in bf16.
-  static constexpr int STAGE = X::BYTES + Y::BYTES, SCRATCH = 512 * NB, LDS = 2 * STAGE + SCRATCH * WM * WN;
+  static constexpr int STAGE = X::BYTES + Y::BYTES, SCRATCH = 512 * NB, LDS = 2 * STAGE * KS + SCRATCH * WM * WN;
   // workgroups that run at a time (by LDS, and 16 waves a CU at these kernels' registers)
-  static constexpr int BY_LDS = (160 << 10) / LDS, BY_WAVES = 16 / (WM * WN);
+  static constexpr int BY_LDS = (160 << 10) / LDS, BY_WAVES = 16 / (WM * WN * KS);
   static constexpr int PER_CU = BY_LDS < BY_WAVES ? BY_LDS : BY_WAVES, MOST = 256 * PER_CU;
-  static constexpr int WAVES_SIMD = (PER_CU * WM * WN + 3) / 4;
+  static constexpr int WAVES_SIMD = (PER_CU * WM * WN * KS + 3) / 4;
   X x;
   Y y;
   f32x4_t acc[NB][MB];
@@ -197,7 +207,9 @@ struct GemmTile {
   // tile r; tile 0 exists); done(r): the epilogue, with the sums in acc. live: a word for each 64 k.
   template <class Place, class Done>
   __device__ __attribute__((always_inline)) void run(char *lds, const uint64_t *live, Place place, Done done) {
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), wm = wave % WM, wn = wave / WM;
+    const int wm = wave_m(), wn = wave_n(), group = KS > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / GROUP) : 0;
+    char *const all = lds;
+    if constexpr (KS > 1) lds += group * 2 * STAGE;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
     constexpr int P = X::PER + Y::PER, NP = NB / 2, P3 = P / 2;   // P3 loads in a step's last phase, the others in the next one's first
     // where the loads are: tile, step, and what they may touch
@@ -205,6 +217,7 @@ struct GemmTile {
     GemmRange at;
     uint64_t mask = 0;
     place(0, x, y, at);
+    if constexpr (KS > 1) at = at.part(group, KS);
     int64_t step = at.first();
     auto read_mask = [&]() __attribute__((always_inline)) {
       if constexpr (MASK) mask = step * kGemmBK < at.kend ? live[step] : 0;
@@ -218,7 +231,7 @@ struct GemmTile {
     };
     auto advance = [&]() __attribute__((always_inline)) {
       if (++step < at.last()) return;
-      if (place(++tile, x, y, at)) {
+      if (KS == 1 && place(++tile, x, y, at)) {
         step = at.first();
       } else {
         x.no_more(), y.no_more();
@@ -244,7 +257,8 @@ struct GemmTile {
     lds_barrier();
     int stage = 0;
     GemmRange now;
-    for (int r = 0; place.range(r, now); ++r) {
+    for (int r = 0; (KS == 1 || r == 0) && place.range(r, now); ++r) {
+      if constexpr (KS > 1) now = now.part(0, KS);   // as many steps for every group
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -287,19 +301,42 @@ struct GemmTile {
           }
         }
       }
+      if constexpr (KS > 1) {   // the groups' sums, added in their order
+        wait_loads<0>();
+        lds_barrier();
+        const int t = X::tid();
+        f32x4_t *mine = reinterpret_cast<f32x4_t *>(lds);
+        static_assert(NB * MB * 16 * GROUP <= 2 * STAGE, "a group's sums in its own stages");
+        if (group > 0) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < MB; ++m) mine[(n * MB + m) * GROUP + t] = acc[n][m];
+        }
+        lds_barrier();
+        if (group > 0) return;   // the wave; no barrier follows
+        for (int g = 1; g < KS; ++g) {
+          const f32x4_t *other = reinterpret_cast<const f32x4_t *>(all + g * 2 * STAGE);
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < MB; ++m) acc[n][m] += other[(n * MB + m) * GROUP + t];
+        }
+      }
       done(r);
     }
+    if constexpr (KS > 1) return;
     wait_loads<0>();   // none may land after the workgroup's LDS is another's
   }
-  __device__ static int wave_m() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) % WM; }
-  __device__ static int wave_n() { return __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) / WM; }
+  __device__ static int wave_m() { return X::wave() % WM; }
+  __device__ static int wave_n() { return X::wave() / WM; }
   // First tile row of this wave's block row mb (a lane's values are of its row lane % 16), first tile
   // column of the wave, and the wave's column of a lane's four in block nb.
   __device__ static int row_at(int mb) { return (wave_m() * MB + mb) * 16; }
   __device__ static int cols_at() { return wave_n() * NB * 16; }
   __device__ static int col_of(int lane, int nb) { return nb * 16 + 4 * (lane >> 4); }
   __device__ static char *scratch(char *lds) {
-    return lds + 2 * STAGE + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * SCRATCH;
+    return lds + 2 * STAGE * KS + X::wave() * SCRATCH;
   }
 };
 
@@ -346,6 +383,67 @@ struct BlockRow {
   }
 };
 
+// A few rows of x (16 MB) against NB blocks of 16 rows of y, whose reading is what takes the time: W
+// waves share K, each lane loads its fragments from memory as they are needed, many at a time, and the
+// waves' sums meet in LDS. A row of either side is any row: y_row(i) for the rows 0 .. 16 NB - 1 of the
+// group, x_row(i) for 0 .. 16 MB - 1 (rows that do not exist: any that do, their sums are not used).
+template <int NB_, int MB_, int W_>
+struct FewRows {
+  static constexpr int NB = NB_, MB = MB_, W = W_, BLOCKS = NB * MB, THREADS = 64 * W, LDS = W * BLOCKS * 1024;
+  static_assert(BLOCKS <= W, "a wave for each block of the sums");
+  // The sums of block (wave / MB, wave % MB) in waves 0 .. BLOCKS - 1, as GemmTile's acc holds them.
+  template <class YRow, class XRow>
+  __device__ __attribute__((always_inline)) static f32x4_t run(char *lds, int K, YRow y_row, XRow x_row) {
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const uint16_t *yp[NB], *xp[MB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) yp[n] = y_row(16 * n + i);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) xp[m] = x_row(16 * m + i);
+    f32x4_t acc[NB][MB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int pieces = K / 8, steps = (pieces + 3) / 4, first = steps * wave / W, last = steps * (wave + 1) / W;
+    constexpr int U = NB >= 4 ? 4 : 8;   // steps in flight
+    for (int s0 = first; s0 < last; s0 += U) {
+      uint4 ry[U][NB], rx[U][MB];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = (s0 + u) * 4 + g, in = at < pieces ? at : 0;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) ry[u][n] = *reinterpret_cast<const uint4 *>(yp[n] + 8 * in);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) rx[u][m] = *reinterpret_cast<const uint4 *>(xp[m] + 8 * in);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = s0 + u < last && (s0 + u) * 4 + g < pieces;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int m = 0; m < MB; ++m)
+            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, in ? ry[u][n] : zero),
+                                                                __builtin_bit_cast(bf16x8_t, in ? rx[u][m] : zero), acc[n][m], 0, 0, 0);
+      }
+    }
+    f32x4_t *red = reinterpret_cast<f32x4_t *>(lds);
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int m = 0; m < MB; ++m) red[(wave * BLOCKS + n * MB + m) * 64 + lane] = acc[n][m];
+    lds_barrier();
+    f32x4_t sum = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (wave < BLOCKS) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) sum += red[(w * BLOCKS + wave) * 64 + lane];
+    }
+    return sum;
+  }
+};
+
 // The tiles of workgroup b of nb (a multiple of 8) of mt * nt tiles in `slices` of k: each XCD (b % 8)
 // takes a run of tiles in an order that goes down 4 tiles of m, then on in n, so that the 32
 // tiles that it works on at a time share their operands in its L2 (without this 1064 TFLOP/s for 1470).
@@ -373,6 +471,25 @@ struct GemmTiles {
     g = range_of(slice);
     return true;
   }
+};
+// About how long `tiles` tiles take that run `slots` at a time, in rounds of 256 tiles of 256 x 256: a
+// whole round takes `full`, a last one with few tiles `least` at the least (fewer CUs at work run faster).
+// Measured for 2048 k (us): 64 tiles of 256 x 256 42, 256 as 49; of 128 x 128 128 tiles 20.9, 256 27, 512 35;
+// of 64 x 64 256 tiles 16.6, 512 22, 1024 28.9, 2048 54.
+inline double gemm_rounds(int64_t tiles, int slots, double full, double least) {
+  const int64_t whole = tiles / slots, rest = tiles % slots;
+  return whole * full + (rest ? least + (full - least) * rest / slots : 0.0);
+}
+// The tile for that: 256, 128 or 64, or 16 for small products (64 x 64 with the k shared by groups of waves).
+inline int gemm_class(int64_t (*tiles)(const void *, int), const void *of, int64_t steps) {
+  const double l = gemm_rounds(tiles(of, 256), 256, 1.0, 0.85), m = gemm_rounds(tiles(of, 128), 512, 0.68, 0.42),
+               q = gemm_rounds(tiles(of, 64), 1024, 0.52, 0.35);
+  if (tiles(of, 64) <= 256 && steps >= 8) return 16;
+  return l <= m && l <= q ? 256 : m <= q ? 128 : 64;
+}
+template <class T>
+struct TileTag {
+  using type = T;
 };
 // Workgroups for that many tiles where `most` run at a time.
 inline int gemm_grid(int64_t tiles, int most) { return (int)((tiles < most ? tiles : most) + 7) / 8 * 8; }

@@ -142,6 +142,53 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadAr
   });
 }
 
+// Up to 16 MB rows: a workgroup takes 64 columns, a chunk of statistics is 16 of them.
+template <int MB, bool TEACH>
+__global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
+  using F = FewRows<4, MB, 8>;
+  __shared__ __attribute__((aligned(16))) char lds[F::LDS];
+  const int64_t n0 = (int64_t)blockIdx.x * 64;
+  const int T = (int)p.T;
+  f32x4_t v = F::run(
+      lds, p.H, [&](int i) { return p.w + (n0 + i < p.V ? n0 + i : p.V - 1) * p.H; },
+      [&](int i) { return p.x + (int64_t)(i < T ? i : T - 1) * p.H; });
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if constexpr (TEACH) lds_barrier();   // (the sums have been read)
+  if (wave >= F::BLOCKS) return;
+  const int64_t c0 = n0 + 16 * (wave / MB), row0 = 16 * (wave % MB), row = row0 + (lane & 15);
+  const int left = (int)(p.V - c0 < 16 ? p.V - c0 : 16), col = 4 * (lane >> 4);
+  if (left <= 0) return;
+  if constexpr (!TEACH) {
+    if (row < T) {
+      const int64_t want = (int64_t)p.ids[row] - c0 - col;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (want == j && col + j < left) p.picked[row] = v[j];
+    }
+  } else if (row0 < T) {
+    f32x4_t *mine = reinterpret_cast<f32x4_t *>(lds) + wave * 64;
+    mine[lane] = v;
+    wave_lds_order();
+    each_entry(p, lane, row0, c0, 16, [&](int er, int c, int j) {
+      p.logits[(row0 + er) * p.k + j] = reinterpret_cast<const float *>(mine + (c >> 2) * 16 + er)[c & 3];
+    });
+  }
+  const float scale = kLog2e / p.tau;
+  float m = -__builtin_inff(), s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (col + j >= left) v[j] = -__builtin_inff();
+    m = fmaxf(m, v[j]);
+  }
+  m *= scale;
+  const float top = fmaxf(m, kLowest);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s += __builtin_amdgcn_exp2f(v[j] * scale - top);
+  join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
+  join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
+  if (lane < 16 && row < T) p.stats[c0 / 16 * p.T + row] = make_float2(m, s);
+}
+
 // A wave a row: q [k] from the teacher's logits. Entries outside the vocabulary count for
 // nothing, an id's later occurrences add to its first; a row without a finite entry has all zeros.
 // Also zeros the picked logits of entries outside.
@@ -192,29 +239,31 @@ __global__ __launch_bounds__(256) void k_head_teacher(HeadArgs p) {
   }
 }
 
-// 16 rows a workgroup, 16 threads each: the tiles' pairs to lse, and the loss.
-__global__ __launch_bounds__(256) void k_head_join(HeadArgs p, int nt) {
-  __shared__ float2 red[16][17];
-  __shared__ float row_lse[16];
-  const int r = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int64_t row = (int64_t)blockIdx.x * 16 + r;
+// R rows a workgroup, 256 / R threads each: the chunks' pairs to lse, and the loss.
+template <int R>
+__global__ __launch_bounds__(256) void k_head_join(HeadArgs p, int chunks) {
+  constexpr int PARTS = 256 / R, IN_WAVE = 64 / R;   // threads of a row, and those of them in a wave
+  __shared__ float2 red[2][4][R];
+  const int r = threadIdx.x % R, part = threadIdx.x / R, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * R + r;
   const bool live = row < p.T;
   float m = -__builtin_inff(), s = 0.0f;
   if (live) {
-#pragma unroll 4
-    for (int n = part; n < nt; n += 16) {
+#pragma unroll 8
+    for (int n = part; n < chunks; n += PARTS) {
       const float2 v = p.stats[(int64_t)n * p.T + row];
       join_stats(m, s, v.x, v.y);
     }
   }
-  red[part][r] = make_float2(m, s);
+#pragma unroll
+  for (int d = R; d < 64; d *= 2) join_stats(m, s, __shfl_xor(m, d, kWave), __shfl_xor(s, d, kWave));
+  if (lane < R) red[0][wave][r] = make_float2(m, s);
   lds_barrier();
-  if (part == 0) {
-    for (int i = 1; i < 16; ++i) join_stats(m, s, red[i][r].x, red[i][r].y);
-    row_lse[r] = (m + log2f(s)) * kLn2;
-  }
-  lds_barrier();
-  const float lse = row_lse[r];
+  m = red[0][0][r].x, s = red[0][0][r].y;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) join_stats(m, s, red[0][w][r].x, red[0][w][r].y);
+  const float lse = (m + log2f(s)) * kLn2;
+  static_assert(IN_WAVE >= 1, "rows of a wave");
   if (p.k == 0) {
     if (part == 0 && live) {
       const int32_t id = p.ids[row];
@@ -225,18 +274,19 @@ __global__ __launch_bounds__(256) void k_head_join(HeadArgs p, int nt) {
   }
   float sum = 0.0f, any = 0.0f;
   if (live) {
-    for (int j = part; j < p.k; j += 16) {
+    for (int j = part; j < p.k; j += PARTS) {
       const float q = p.q[row * p.k + j];
       if (q == 0.0f) continue;
       any = 1.0f;
       sum += q * (logf(q) - p.logits[row * p.k + j] / p.tau + lse);
     }
   }
-  lds_barrier();
-  red[part][r] = make_float2(sum, any);
+#pragma unroll
+  for (int d = R; d < 64; d *= 2) sum += __shfl_xor(sum, d, kWave), any += __shfl_xor(any, d, kWave);
+  if (lane < R) red[1][wave][r] = make_float2(sum, any);
   lds_barrier();
   if (part == 0 && live) {
-    for (int i = 1; i < 16; ++i) sum += red[i][r].x, any += red[i][r].y;
+    for (int w = 1; w < 4; ++w) sum += red[1][w][r].x, any += red[1][w][r].y;
     p.loss[row] = any != 0.0f ? p.tau * p.tau * sum : 0.0f;
     p.lse[row] = any != 0.0f ? lse : __builtin_inff();
   }
@@ -362,30 +412,37 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
   });
 }
 
-// The tile of a call: the largest that gives most of the CUs one.
-struct HeadTile {
-  int bm, bn;
+struct HeadSize {
+  int64_t T, V;
 };
-HeadTile head_tile(int64_t T, int64_t V) {
-  if (cdiv(T, 256) * cdiv(V, 256) >= 160 && T > 128) return {256, 256};
-  if (cdiv(T, 128) * cdiv(V, 128) >= 160 && T > 32) return {128, 128};
-  if (T > 32) return {64, 64};
-  return {32, 64};
+int64_t head_tile_count(const void *size, int b) {
+  const HeadSize &a = *static_cast<const HeadSize *>(size);
+  return cdiv(a.T, b) * cdiv(a.V, b);
 }
-
+// f(the tile of a call)
 template <class F>
-void by_head_tile(HeadTile t, F &&f) {
-  if (t.bm == 256) f(GemmTile<4, 8, 4, 2>());
-  else if (t.bm == 128) f(GemmTile<4, 4, 2, 2>());
-  else if (t.bm == 64) f(GemmTile<2, 2, 2, 2>());
-  else f(GemmTile<2, 2, 1, 2>());
+void by_head_tile(int64_t T, int64_t V, int H, F &&f) {
+  const HeadSize size{T, V};
+  switch (gemm_class(head_tile_count, &size, cdiv(H, kGemmBK))) {
+    case 256: return f(TileTag<GemmTile<4, 8, 4, 2>>());
+    case 128: return f(TileTag<GemmTile<4, 4, 2, 2>>());
+    case 64: return f(TileTag<GemmTile<2, 2, 2, 2>>());
+    default: return f(TileTag<GemmTile<2, 2, 2, 2, false, false, 0, false, 4>>());
+  }
 }
+template <class T>
+dim3 head_grid(int64_t rows, int64_t cols) {
+  const int64_t tiles = cdiv(rows, T::BM) * cdiv(cols, T::BN);
+  return dim3(T::KS > 1 ? (unsigned)cdiv(tiles, 8) * 8 : gemm_grid(tiles, T::MOST));
+}
+constexpr int kFewTokens = 32;
 
 }  // namespace
 
-int64_t head_stat_chunks(int64_t T, int64_t V) {
+int64_t head_stat_chunks(int64_t T, int64_t V, int H) {
+  if (T <= kFewTokens) return cdiv(V, 16);
   int64_t n = 0;
-  by_head_tile(head_tile(T, V), [&](auto tile) { n = cdiv(V, 16 * decltype(tile)::NB); });
+  by_head_tile(T, V, H, [&](auto tile) { n = cdiv(V, 16 * decltype(tile)::type::NB); });
   return n;
 }
 
@@ -398,15 +455,27 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  by_head_tile(head_tile(a.T, a.V), [&](auto tile) {
-    using T = decltype(tile);
-    const dim3 grid(gemm_grid(cdiv(a.T, T::BM) * cdiv(a.V, T::BN), T::MOST));
-    if (a.k) hipLaunchKernelGGL((k_head_stats<T, true>), grid, dim3(T::THREADS), 0, s, a);
-    else hipLaunchKernelGGL((k_head_stats<T, false>), grid, dim3(T::THREADS), 0, s, a);
-  });
+  if (a.T <= kFewTokens) {
+    const dim3 grid((unsigned)cdiv(a.V, 64)), block(512);
+    if (a.T <= 16 && a.k) hipLaunchKernelGGL((k_head_few<1, true>), grid, block, 0, s, a);
+    else if (a.T <= 16) hipLaunchKernelGGL((k_head_few<1, false>), grid, block, 0, s, a);
+    else if (a.k) hipLaunchKernelGGL((k_head_few<2, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_head_few<2, false>), grid, block, 0, s, a);
+  } else {
+    by_head_tile(a.T, a.V, a.H, [&](auto tile) {
+      using T = typename decltype(tile)::type;
+      const dim3 grid = head_grid<T>(a.T, a.V);
+      if (a.k) hipLaunchKernelGGL((k_head_stats<T, true>), grid, dim3(T::THREADS), 0, s, a);
+      else hipLaunchKernelGGL((k_head_stats<T, false>), grid, dim3(T::THREADS), 0, s, a);
+    });
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_head_join, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 0, s, a, (int)head_stat_chunks(a.T, a.V));
+  const int chunks = (int)head_stat_chunks(a.T, a.V, a.H);
+  // enough workgroups whatever T: a row a workgroup, four or 16
+  if (a.T <= 256) hipLaunchKernelGGL(k_head_join<1>, dim3((unsigned)a.T), dim3(256), 0, s, a, chunks);
+  else if (a.T <= 2048) hipLaunchKernelGGL(k_head_join<4>, dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a, chunks);
+  else hipLaunchKernelGGL(k_head_join<16>, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 0, s, a, chunks);
   return hipGetLastError();
 }
 
@@ -417,9 +486,9 @@ hipError_t launch_head_prepare(const HeadArgs &a, bool with_live, hipStream_t s)
 }
 
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s) {
-  by_head_tile(head_tile(a.T, a.vn), [&](auto tile) {
-    using T = decltype(tile);
-    const dim3 grid(gemm_grid(cdiv(a.T, T::BM) * cdiv(a.vn, T::BN), T::MOST));
+  by_head_tile(a.T, a.vn, a.H, [&](auto tile) {
+    using T = typename decltype(tile)::type;
+    const dim3 grid = head_grid<T>(a.T, a.vn);
     if (a.k) hipLaunchKernelGGL((k_head_piece<T, true>), grid, dim3(T::THREADS), 0, s, a);
     else hipLaunchKernelGGL((k_head_piece<T, false>), grid, dim3(T::THREADS), 0, s, a);
   });

@@ -96,9 +96,10 @@ def test_gated_ffn(T, H, I, kind, inter):
     near(got, h, 1, "h"), near(out["dx"], dx, 2, "dx"), near(out["dw13"], dw, 2, "dw13")
     again = M.gated_ffn_backward(dh, x, w, need=("dx", "dw13", "h"), **kw)
     assert all(torch.equal(out[n], again[n]) for n in out)
-    for n in ("dx", "dw13"):
+    for n, ref, e in (("dx", dx, ex), ("dw13", dw, ew)):    # alone: the sums may be cut differently
         one = M.gated_ffn_backward(dh, x, w, need=(n,), **kw)
-        assert list(one) == [n] and torch.equal(one[n], out[n])
+        assert list(one) == [n]
+        R.within(one[n], ref, B * ref.abs() + (1 + B) * e, n + " alone")
 
 
 def test_gated_ffn_without_rows():
@@ -175,8 +176,10 @@ def test_vocab_ce(T, H, V):
     assert not out["dx"][dead].any() and not got_loss[dead].any()
     again = M.vocab_ce_backward(dloss, x, w, labels, got_lse)
     assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dw"], out["dw"])
-    assert torch.equal(M.vocab_ce_backward(dloss, x, w, labels, got_lse, need=("dx",))["dx"], out["dx"])
-    assert torch.equal(M.vocab_ce_backward(dloss, x, w, labels, got_lse, need=("dw",))["dw"], out["dw"])
+    for n, ref, e in (("dx", dx, ex), ("dw", dw, ew)):      # alone: the sums may be cut differently
+        one = M.vocab_ce_backward(dloss, x, w, labels, got_lse, need=(n,))
+        assert list(one) == [n]
+        R.within(one[n], ref, B * ref.abs() + (1 + B) * e, n + " alone")
 
 
 def distill_case(T, H, V, k, tdt, seed=0):
@@ -221,7 +224,8 @@ def test_vocab_distill(T, H, V, k, tau, tdt):
     assert not out["dx"][~row].any()
     again = M.vocab_distill_backward(*args, temperature=tau, need=("dw", "dx"))
     assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dw"], out["dw"])
-    assert torch.equal(M.vocab_distill_backward(*args, temperature=tau, need=("dx",))["dx"], out["dx"])
+    one = M.vocab_distill_backward(*args, temperature=tau, need=("dx",))
+    R.within(one["dx"], dx, B * dx.abs() + (1 + B) * ex, "dx alone")
 
 
 def test_distill_of_one_sure_entry_is_cross_entropy():
