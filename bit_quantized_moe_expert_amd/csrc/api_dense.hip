@@ -136,8 +136,8 @@ HeadArgs head_args(const nf4moe_head_t &h, const uint16_t *x, int64_t T, const i
 nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint16_t *dw, hipStream_t s) {
   const int slices = product_slices(a.T, a.H, c.piece < a.V ? c.piece : a.V, !dw);
   const bool parts = slices > 1 || c.piece < a.V;
-  a.P = c.P, a.live = c.live, a.list = c.list, a.offsets = c.offsets;
-  hipError_t e = launch_head_prepare(a, dw != nullptr, s);
+  a.P = c.P, a.live = dw ? c.live : nullptr, a.list = c.list, a.offsets = c.offsets;
+  hipError_t e = a.k ? launch_head_entries(a, s) : hipSuccess;
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += c.piece) {
     a.v0 = v0, a.vn = a.V - v0 < c.piece ? a.V - v0 : c.piece, a.vp = c.piece;
     e = launch_head_piece(a, s);

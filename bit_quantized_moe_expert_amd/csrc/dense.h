@@ -63,13 +63,13 @@ struct HeadArgs {
   const float *dloss;        // [T]
   int64_t v0, vn, vp;        // the piece of the vocabulary, and the row stride of P
   uint16_t *P;               // [T, vp]
-  uint64_t *live;            // [T / 64]
+  uint64_t *live;            // [T / 64] or null: a bit for each row, set where it has a gradient (written with the first piece)
 };
 constexpr int kHeadChunk = 128;
 int64_t head_stat_chunks(int64_t T, int64_t V, int H);
 hipError_t launch_head_forward(const HeadArgs &a, hipStream_t s);
-// Before the pieces: live (with `with_live`), and the teacher's lists.
-hipError_t launch_head_prepare(const HeadArgs &a, bool with_live, hipStream_t s);
+// The teacher's lists for the backward's pieces.
+hipError_t launch_head_entries(const HeadArgs &a, hipStream_t s);
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s);
 int64_t head_piece(int64_t T, int64_t V);
 

@@ -2,9 +2,9 @@
 // logits, without ever storing the logits l = x W^T [T, V].
 //
 // Forward: a tile of logits is reduced in registers to a maximum and a sum of exponentials a row
-// (k_head_stats), the tiles' pairs are joined row by row (k_head_join):
+// (k_head_stats, k_head_few), these pairs are joined row by row (k_head_join):
 //   lse = log sum_v exp(l_v / tau);  CE: loss = lse - l_label
-//   distillation: q = softmax of the teacher's given logits / tau (k_head_teacher),
+//   distillation: q = softmax of the teacher's given logits / tau (k_head_entries),
 //   loss = tau^2 sum_j q_j (log q_j - l_{id_j} / tau + lse)
 // The logits that the loss names are picked out of the tile that holds them.
 // Backward, by pieces of the vocabulary that the last-level cache can hold: the tile's logits again,
@@ -54,20 +54,49 @@ struct HeadPlace : GemmTiles {
   }
 };
 
-// f(row, column of the wave's `cols`, entry j) for the teacher's entries of the 16 rows from row0 on
-// whose ids lie in the `cols` columns from v on (cols divides kHeadChunk, v is a multiple of cols).
-template <class F>
-__device__ inline void each_entry(const HeadArgs &p, int lane, int64_t row0, int64_t v, int cols, F &&f) {
-  const int64_t block = row0 >> 4, chunks = (p.V + kHeadChunk - 1) / kHeadChunk;
-  const int32_t *off = p.offsets + block * (chunks + 1) + v / kHeadChunk;
-  const uint32_t *list = p.list + block * 16 * p.k;
-  const int first = off[0], last = off[1];
-  for (int e = first + lane; e < last; e += 64) {
-    const uint32_t w = list[e];
-    const int col = (int)(w & 127) - (int)(v & 127);
-    if (col >= 0 && col < cols) f((int)(w >> 7 & 15), col, (int)(w >> 11));
+// The teacher's entries of 16 MB rows in the COLS columns from v on (COLS divides kHeadChunk, v is a
+// multiple of it): the lists of MB blocks of 16 rows, their first 64 entries in a register each, asked for
+// together, since every one of these loads has the whole latency of memory.
+template <int MB, int COLS>
+struct TileEntries {
+  uint32_t w[MB];
+  int first[MB], n[MB];
+  int at;   // of v in its chunk
+  __device__ void load(const HeadArgs &p, int lane, int64_t row0, int64_t v) {
+    const int64_t chunks = (p.V + kHeadChunk - 1) / kHeadChunk;
+    at = (int)(v % kHeadChunk);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      const int64_t block = (row0 >> 4) + mb;
+      first[mb] = n[mb] = 0;
+      if (16 * block < p.T) {
+        const int32_t *off = p.offsets + block * (chunks + 1) + v / kHeadChunk;
+        first[mb] = off[0], n[mb] = off[1] - off[0];
+      }
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      w[mb] = 0;
+      if (lane < n[mb]) w[mb] = p.list[((row0 >> 4) + mb) * 16 * p.k + first[mb] + lane];
+    }
   }
-}
+  // f(row of the block, column of COLS, entry j) where word `of` is one of these columns
+  template <class F>
+  __device__ void one(uint32_t of, F &&f) const {
+    const int col = (int)(of & 127) - at;
+    if (col >= 0 && col < COLS) f((int)(of >> 7 & 15), col, (int)(of >> 11));
+  }
+  // those of block mb past the first 64
+  template <class F>
+  __device__ void rest(const HeadArgs &p, int lane, int64_t row0, int mb, F &&f) const {
+    for (int e = 64 + lane; e < n[mb]; e += 64) one(p.list[((row0 >> 4) + mb) * 16 * p.k + first[mb] + e], f);
+  }
+  template <class F>
+  __device__ void each(const HeadArgs &p, int lane, int64_t row0, int mb, F &&f) const {
+    if (lane < n[mb]) one(w[mb], f);
+    rest(p, lane, row0, mb, f);
+  }
+};
 
 template <class T, bool TEACH>
 __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadArgs p) {
@@ -83,6 +112,8 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadAr
     const int lane = epilogue_lane(), left = (int)(p.V - n0 < COLS ? p.V - n0 : COLS);   // columns that exist
     if (left <= 0) return;   // the wave
     const float c = kLog2e / p.tau;
+    [[maybe_unused]] TileEntries<T::MB, COLS> entries;
+    if constexpr (TEACH) entries.load(p, lane, m0 + T::row_at(0), n0);
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb) {
       const int64_t row0 = m0 + T::row_at(mb), row = row0 + (lane & 15);
@@ -109,7 +140,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadAr
           for (int nb = 0; nb < T::NB / 2; ++nb)
             *reinterpret_cast<f32x4_t *>(mine + Row::place(lane & 15, 4 * nb + (lane >> 4))) = t.acc[half * T::NB / 2 + nb][mb];
           wave_lds_order();
-          each_entry(p, lane, row0, n0, COLS, [&](int er, int col, int j) {
+          entries.each(p, lane, m0 + T::row_at(0), mb, [&](int er, int col, int j) {
             const int at = col - half * COLS / 2;
             if (at >= 0 && at < COLS / 2)
               p.logits[(row0 + er) * p.k + j] = *reinterpret_cast<const float *>(mine + Row::place(er, at >> 2) + 4 * (at & 3));
@@ -169,7 +200,9 @@ __global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
     f32x4_t *mine = reinterpret_cast<f32x4_t *>(lds) + wave * 64;
     mine[lane] = v;
     wave_lds_order();
-    each_entry(p, lane, row0, c0, 16, [&](int er, int c, int j) {
+    TileEntries<1, 16> entries;
+    entries.load(p, lane, row0, c0);
+    entries.each(p, lane, row0, 0, [&](int er, int c, int j) {
       p.logits[(row0 + er) * p.k + j] = reinterpret_cast<const float *>(mine + (c >> 2) * 16 + er)[c & 3];
     });
   }
@@ -187,56 +220,6 @@ __global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
   join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
   join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
   if (lane < 16 && row < T) p.stats[c0 / 16 * p.T + row] = make_float2(m, s);
-}
-
-// A wave a row: q [k] from the teacher's logits. Entries outside the vocabulary count for
-// nothing, an id's later occurrences add to its first; a row without a finite entry has all zeros.
-// Also zeros the picked logits of entries outside.
-__global__ __launch_bounds__(256) void k_head_teacher(HeadArgs p) {
-  __shared__ float val[4][kMaxTeacher];
-  __shared__ int32_t ids[4][kMaxTeacher];
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + w;
-  const bool live = row < p.T;
-  const int64_t base = (live ? row : 0) * p.k;
-  float m = -__builtin_inff();
-  bool nan = false;
-  for (int j = lane; j < p.k; j += 64) {
-    int32_t id = p.ids[base + j];
-    float t = p.teacher_bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p.teacher)[base + j])
-                             : reinterpret_cast<const float *>(p.teacher)[base + j];
-    if (id < 0 || id >= p.V) {
-      id = -1, t = -__builtin_inff();
-      if (live) p.logits[base + j] = 0.0f;
-    }
-    ids[w][j] = id, val[w][j] = t;
-    nan |= t != t;
-    m = fmaxf(m, t);
-  }
-  m = wave_max(m);
-  nan = __any(nan);
-  float sum = 0.0f;
-  for (int j = lane; j < p.k; j += 64) {
-    const float e = m == -__builtin_inff() ? 0.0f : expf((val[w][j] - m) / p.tau);
-    val[w][j] = e;
-    sum += e;
-  }
-  sum = wave_sum(sum);
-  lds_barrier();
-  if (!live) return;
-  for (int j = lane; j < p.k; j += 64) {
-    const int32_t id = ids[w][j];
-    float e = 0.0f;
-    bool first = id >= 0;
-    if (first) {
-      for (int i = 0; i < p.k; ++i) {
-        if (ids[w][i] != id) continue;
-        if (i < j) first = false;
-        e += val[w][i];
-      }
-    }
-    p.q[base + j] = nan && id >= 0 ? __builtin_nanf("") : first && m != -__builtin_inff() ? e / sum : 0.0f;
-  }
 }
 
 // R rows a workgroup, 256 / R threads each: the chunks' pairs to lse, and the loss.
@@ -300,53 +283,102 @@ __device__ inline bool row_on(const HeadArgs &p, int64_t row) {
   return id >= 0 && id < p.V;
 }
 
-// A wave 64 rows.
-__global__ __launch_bounds__(256) void k_head_live(HeadArgs p) {
-  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const uint64_t bits = __ballot(row < p.T && row_on(p, row));
-  if ((threadIdx.x & 63) == 0 && row < p.T) p.live[row >> 6] = bits;
+// q [k] of a row from the teacher's logits, by a wave with `val` and `ids` [k] of its own in LDS.
+// Entries outside the vocabulary count for nothing, an id's later occurrences add to its first; a
+// row without an entry above -inf has all zeros. Also zeros the logits of entries outside.
+__device__ inline void teacher_row(const HeadArgs &p, int64_t row, int lane, float *val, int32_t *ids) {
+  const int64_t base = row * p.k;
+  float m = -__builtin_inff();
+  bool nan = false;
+  for (int j = lane; j < p.k; j += 64) {
+    int32_t id = p.ids[base + j];
+    float t = p.teacher_bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t *>(p.teacher)[base + j])
+                             : reinterpret_cast<const float *>(p.teacher)[base + j];
+    if (id < 0 || id >= p.V) {
+      id = -1, t = -__builtin_inff();
+      p.logits[base + j] = 0.0f;
+    }
+    ids[j] = id, val[j] = t;
+    nan |= t != t;
+    m = fmaxf(m, t);
+  }
+  m = wave_max(m);
+  nan = __any(nan);
+  float sum = 0.0f;
+  for (int j = lane; j < p.k; j += 64) {
+    const float e = m == -__builtin_inff() ? 0.0f : expf((val[j] - m) / p.tau);
+    val[j] = e;
+    sum += e;
+  }
+  sum = wave_sum(sum);
+  wave_lds_order();
+  for (int j = lane; j < p.k; j += 64) {
+    const int32_t id = ids[j];
+    float e = 0.0f;
+    bool first = id >= 0;
+    if (first) {
+      for (int i = 0; i < p.k; ++i) {
+        if (ids[i] != id) continue;
+        if (i < j) first = false;
+        e += val[i];
+      }
+    }
+    p.q[base + j] = nan && id >= 0 ? __builtin_nanf("") : first && m != -__builtin_inff() ? e / sum : 0.0f;
+  }
+  wave_lds_order();
 }
 
-// A workgroup 16 rows: their entries by chunk of kHeadChunk columns (counts, a scan, places). BACK: those
-// with a probability; else those with an id in the vocabulary. Within a chunk their order is open:
-// each writes to a place of its own.
+// A workgroup 16 rows: the teacher's probabilities (forward), and the rows' entries by chunk of
+// kHeadChunk columns (counts, a scan, places). BACK: those with a probability; else those with an id in
+// the vocabulary. Within a chunk their order is open: each writes to a place of its own.
+constexpr int kEntryThreads = 1024;
+// Rows whose ids and values are in LDS at a time, beside the counts of 2^21 / kHeadChunk chunks.
+__host__ __device__ inline int entry_rows(int k) { return k <= 512 ? 16 : 8; }
 template <bool BACK>
-__global__ __launch_bounds__(256) void k_head_lists(HeadArgs p) {
-  extern __shared__ int32_t count[];   // [chunks]
-  __shared__ int32_t total[256];
-  const int t = threadIdx.x, chunks = (int)((p.V + kHeadChunk - 1) / kHeadChunk), each = (chunks + 255) / 256;
+__global__ __launch_bounds__(kEntryThreads) void k_head_entries(HeadArgs p) {
+  extern __shared__ int32_t shared[];   // [chunks], and for the forward [entry_rows][k] ids and values
+  __shared__ int32_t total[kEntryThreads / 64];
+  const int t = threadIdx.x, chunks = (int)((p.V + kHeadChunk - 1) / kHeadChunk), each = (chunks + kEntryThreads - 1) / kEntryThreads;
+  int32_t *count = shared;
   const int64_t row0 = (int64_t)blockIdx.x * 16, n = (p.T - row0 < 16 ? p.T - row0 : 16) * p.k, base = row0 * p.k;
-  for (int i = t; i < chunks; i += 256) count[i] = 0;
+  if constexpr (!BACK) {
+    const int w = t >> 6, rows = entry_rows(p.k);
+    int32_t *ids = shared + chunks + 2 * w * p.k;
+    for (int64_t row = row0 + w; w < rows && row < row0 + 16 && row < p.T; row += rows)
+      teacher_row(p, row, t & 63, reinterpret_cast<float *>(ids + p.k), ids);
+  }
+  for (int i = t; i < chunks; i += kEntryThreads) count[i] = 0;
   lds_barrier();
   auto id_of = [&](int64_t e) {
     const int32_t id = p.ids[base + e];
     return id < 0 || id >= p.V || (BACK && p.q[base + e] == 0.0f) ? -1 : id;
   };
-  for (int64_t e = t; e < n; e += 256) {
+  for (int64_t e = t; e < n; e += kEntryThreads) {
     const int32_t id = id_of(e);
     if (id >= 0) atomicAdd(&count[id / kHeadChunk], 1);
   }
   lds_barrier();
   int sum = 0;
   for (int i = t * each; i < (t + 1) * each && i < chunks; ++i) sum += count[i];
-  total[t] = sum;
-  lds_barrier();
-  for (int d = 1; d < 256; d *= 2) {
-    const int v = t >= d ? total[t - d] : 0;
-    lds_barrier();
-    total[t] += v;
-    lds_barrier();
+  int upto = sum;   // in the wave, then over the waves
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int v = __shfl_up(upto, d, kWave);
+    upto += (t & 63) >= d ? v : 0;
   }
-  int at = total[t] - sum;
+  if ((t & 63) == 63) total[t >> 6] = upto;
+  lds_barrier();
+  for (int w = 0; w < t >> 6; ++w) upto += total[w];
+  int at = upto - sum;
   int32_t *off = p.offsets + (int64_t)blockIdx.x * (chunks + 1);
   for (int i = t * each; i < (t + 1) * each && i < chunks; ++i) {
     const int v = count[i];
     off[i] = at, count[i] = at;
     at += v;
   }
-  if (t == 255) off[chunks] = total[255];
+  if (t == kEntryThreads - 1) off[chunks] = upto;
   lds_barrier();
-  for (int64_t e = t; e < n; e += 256) {
+  for (int64_t e = t; e < n; e += kEntryThreads) {
     const int32_t id = id_of(e);
     if (id < 0) continue;
     const int row = (int)(e / p.k), j = (int)(e - (int64_t)row * p.k);
@@ -369,6 +401,23 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
     if (left <= 0) return;   // the wave
     const float c = kLog2e / p.tau;
     const BlockRow<COLS> out{T::scratch(lds), lane};
+    // an entry's P, from its logit in fp32
+    [[maybe_unused]] auto entry_value = [&](int64_t row, int j) __attribute__((always_inline)) {
+      const int64_t e = row * p.k + j;
+      if (!row_on(p, row)) return 0.0f;
+      return p.dloss[row] * p.tau * (__builtin_amdgcn_exp2f(p.logits[e] * c - p.lse[row] * kLog2e) - p.q[e]);
+    };
+    [[maybe_unused]] TileEntries<T::MB, COLS> entries;
+    [[maybe_unused]] float value[T::MB];
+    if constexpr (TEACH) {
+      entries.load(p, lane, m0 + T::row_at(0), p.v0 + n0);
+#pragma unroll
+      for (int mb = 0; mb < T::MB; ++mb) {
+        value[mb] = 0.0f;
+        if (lane < entries.n[mb])
+          value[mb] = entry_value(m0 + T::row_at(mb) + (entries.w[mb] >> 7 & 15), (int)(entries.w[mb] >> 11));
+      }
+    }
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb) {
       const int64_t row0 = m0 + T::row_at(mb), row = row0 + (lane & 15);
@@ -380,6 +429,9 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
         const int64_t at = (int64_t)p.ids[row] - p.v0 - n0;
         want = at >= 0 && at < left ? (int)at : -1;
       }
+      // the rows that count in dw's product, by the wave that has the vocabulary's first columns
+      const uint64_t rows_on = __ballot(on);
+      if (p.live && p.v0 + n0 == 0 && lane == 0) reinterpret_cast<uint16_t *>(p.live)[row0 >> 4] = (uint16_t)rows_on;
       const bool some = !TEACH && __any(want >= 0), all = __all(on) && left == COLS;
 #pragma unroll
       for (int nb = 0; nb < T::NB; ++nb) {
@@ -398,13 +450,12 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
         }
         out.put(T::col_of(lane, nb), pack4(v[0], v[1], v[2], v[3]));
       }
-      if constexpr (TEACH) {   // the entries' places, from their logits in fp32
+      if constexpr (TEACH) {   // the entries' places
         wave_lds_order();
-        each_entry(p, lane, row0, p.v0 + n0, COLS, [&](int er, int col, int j) {
-          const int64_t er0 = row0 + er, e = er0 * p.k + j;
-          if (!row_on(p, er0)) return;
-          const float d = __builtin_amdgcn_exp2f(p.logits[e] * c - p.lse[er0] * kLog2e) - p.q[e];
-          *out.one(er, col) = (uint16_t)f32_to_bf16_rne(p.dloss[er0] * p.tau * d);
+        if (lane < entries.n[mb])
+          entries.one(entries.w[mb], [&](int er, int col, int) { *out.one(er, col) = (uint16_t)f32_to_bf16_rne(value[mb]); });
+        entries.rest(p, lane, m0 + T::row_at(0), mb, [&](int er, int col, int j) {
+          *out.one(er, col) = (uint16_t)f32_to_bf16_rne(entry_value(row0 + er, j));
         });
       }
       out.out(p.P + row0 * p.vp + n0, p.vp, p.T - row0, p.vp - n0);
@@ -450,8 +501,8 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
   HeadArgs a = args;
   a.v0 = 0, a.vn = a.V;
   if (a.k) {
-    hipLaunchKernelGGL(k_head_teacher, dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a);
-    hipLaunchKernelGGL(k_head_lists<false>, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 4 * cdiv(a.V, kHeadChunk), s, a);
+    hipLaunchKernelGGL(k_head_entries<false>, dim3((unsigned)cdiv(a.T, 16)), dim3(kEntryThreads),
+                       4 * cdiv(a.V, kHeadChunk) + 8 * entry_rows(a.k) * a.k, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -479,9 +530,8 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_head_prepare(const HeadArgs &a, bool with_live, hipStream_t s) {
-  if (with_live) hipLaunchKernelGGL(k_head_live, dim3((unsigned)cdiv(a.T, 256)), dim3(256), 0, s, a);
-  if (a.k) hipLaunchKernelGGL(k_head_lists<true>, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 4 * cdiv(a.V, kHeadChunk), s, a);
+hipError_t launch_head_entries(const HeadArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL(k_head_entries<true>, dim3((unsigned)cdiv(a.T, 16)), dim3(kEntryThreads), 4 * cdiv(a.V, kHeadChunk), s, a);
   return hipGetLastError();
 }
 

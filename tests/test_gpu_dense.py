@@ -228,6 +228,28 @@ def test_vocab_distill(T, H, V, k, tau, tdt):
     R.within(one["dx"], dx, B * dx.abs() + (1 + B) * ex, "dx alone")
 
 
+def test_distill_over_the_largest_vocabulary():
+    """2^21 columns and 1024 entries a row: the entries' lists at their largest."""
+    T, H, V, k = 18, 8, 1 << 21, 1024
+    rn = gen(4)
+    x, w = rn(T, H, dt=BF16), rn(V, H, std=1.0, dt=BF16)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    ids = torch.randint(-1, V, (T, k), generator=g, device=DEV)
+    ids[:, 0], ids[:, 1] = V - 1, 0
+    ids, t, dloss = ids.to(I32), rn(T, k), torch.ones(T, device=DEV)
+    loss, lse, q, logits = R.distill(x, w, ids, t, 1.0)
+    got = M.vocab_distill_forward(x, w, ids, t)
+    # an H of 8: sums of 8 products, 2^21 terms of the sum of exponentials in chunks of 16 columns and 256 threads
+    R.within(got["lse"], lse, 16 * U * 40 + 600 * U + 4 * U * lse.abs(), "lse")
+    R.within(got["logits"], logits, 16 * U * (x.double().abs().sum(1).amax() * 5), "logits")
+    R.within(got["q"], q, q * (8 * 5 + 2 * k + 16) * U + 2.0 ** -120, "q")
+    assert R.off(got["loss"], loss) < 1e-4
+    out = M.vocab_distill_backward(dloss, x, w, ids, got["q"], got["logits"], got["lse"])
+    P = R.distill_P(dloss, x, w, ids, got["q"], torch.isfinite(lse), 1.0)
+    near(out["dw"], P.T @ x.double(), 2, "dw")
+    assert R.off(out["dx"], P @ w.double()) < 2 * B     # 144 values: two roundings, each at most b of its sum's terms
+
+
 def test_distill_of_one_sure_entry_is_cross_entropy():
     """One entry a row: q is 1, the loss and the gradients are the cross entropy's."""
     x, w, labels, dloss = head_case(140, 128, 2111)
