@@ -406,7 +406,7 @@ struct FewRows {
 #pragma unroll
       for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const int pieces = K / 8, steps = (pieces + 3) / 4, first = steps * wave / W, last = steps * (wave + 1) / W;
-    constexpr int U = NB >= 4 ? 4 : 8;   // steps in flight
+    constexpr int U = NB >= 4 ? 2 : 8;   // steps in flight (four for NB = 4 cost workgroups a CU)
     for (int s0 = first; s0 < last; s0 += U) {
       uint4 ry[U][NB], rx[U][MB];
 #pragma unroll

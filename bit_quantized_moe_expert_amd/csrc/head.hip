@@ -173,7 +173,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadAr
   });
 }
 
-// Up to 16 MB rows: a workgroup takes 64 columns, a chunk of statistics is 16 of them.
+// Up to 16 MB rows: a workgroup takes 64 columns, a chunk of statistics.
 template <int MB, bool TEACH>
 __global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
   using F = FewRows<4, MB, 8>;
@@ -184,42 +184,50 @@ __global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
       lds, p.H, [&](int i) { return p.w + (n0 + i < p.V ? n0 + i : p.V - 1) * p.H; },
       [&](int i) { return p.x + (int64_t)(i < T ? i : T - 1) * p.H; });
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if constexpr (TEACH) lds_barrier();   // (the sums have been read)
-  if (wave >= F::BLOCKS) return;
+  lds_barrier();   // the sums have been read
   const int64_t c0 = n0 + 16 * (wave / MB), row0 = 16 * (wave % MB), row = row0 + (lane & 15);
   const int left = (int)(p.V - c0 < 16 ? p.V - c0 : 16), col = 4 * (lane >> 4);
-  if (left <= 0) return;
-  if constexpr (!TEACH) {
-    if (row < T) {
-      const int64_t want = (int64_t)p.ids[row] - c0 - col;
+  float2 *stats = reinterpret_cast<float2 *>(lds + F::BLOCKS * 1024);   // [4][16 MB]
+  if (wave < F::BLOCKS) {
+    if constexpr (!TEACH) {
+      if (row < T) {
+        const int64_t want = (int64_t)p.ids[row] - c0 - col;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (want == j && col + j < left) p.picked[row] = v[j];
+        for (int j = 0; j < 4; ++j)
+          if (want == j && col + j < left) p.picked[row] = v[j];
+      }
+    } else if (row0 < T && left > 0) {
+      f32x4_t *mine = reinterpret_cast<f32x4_t *>(lds) + wave * 64;
+      mine[lane] = v;
+      wave_lds_order();
+      TileEntries<1, 16> entries;
+      entries.load(p, lane, row0, c0);
+      entries.each(p, lane, row0, 0, [&](int er, int c, int j) {
+        p.logits[(row0 + er) * p.k + j] = reinterpret_cast<const float *>(mine + (c >> 2) * 16 + er)[c & 3];
+      });
     }
-  } else if (row0 < T) {
-    f32x4_t *mine = reinterpret_cast<f32x4_t *>(lds) + wave * 64;
-    mine[lane] = v;
-    wave_lds_order();
-    TileEntries<1, 16> entries;
-    entries.load(p, lane, row0, c0);
-    entries.each(p, lane, row0, 0, [&](int er, int c, int j) {
-      p.logits[(row0 + er) * p.k + j] = reinterpret_cast<const float *>(mine + (c >> 2) * 16 + er)[c & 3];
-    });
-  }
-  const float scale = kLog2e / p.tau;
-  float m = -__builtin_inff(), s = 0.0f;
+    const float scale = kLog2e / p.tau;
+    float m = -__builtin_inff(), s = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (col + j >= left) v[j] = -__builtin_inff();
-    m = fmaxf(m, v[j]);
-  }
-  m *= scale;
-  const float top = fmaxf(m, kLowest);
+    for (int j = 0; j < 4; ++j) {
+      if (col + j >= left) v[j] = -__builtin_inff();
+      m = fmaxf(m, v[j]);
+    }
+    m *= scale;
+    const float top = fmaxf(m, kLowest);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) s += __builtin_amdgcn_exp2f(v[j] * scale - top);
-  join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
-  join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
-  if (lane < 16 && row < T) p.stats[c0 / 16 * p.T + row] = make_float2(m, s);
+    for (int j = 0; j < 4; ++j) s += __builtin_amdgcn_exp2f(v[j] * scale - top);
+    join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
+    join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
+    if (lane < 16) stats[wave / MB * 16 * MB + row] = make_float2(m, s);
+  }
+  lds_barrier();
+  const int r = threadIdx.x;
+  if (r >= 16 * MB || r >= T) return;
+  float2 a = stats[r];
+#pragma unroll
+  for (int n = 1; n < F::NB; ++n) join_stats(a.x, a.y, stats[n * 16 * MB + r].x, stats[n * 16 * MB + r].y);
+  p.stats[(int64_t)blockIdx.x * p.T + r] = a;
 }
 
 // R rows a workgroup, 256 / R threads each: the chunks' pairs to lse, and the loss.
@@ -491,7 +499,7 @@ constexpr int kFewTokens = 32;
 }  // namespace
 
 int64_t head_stat_chunks(int64_t T, int64_t V, int H) {
-  if (T <= kFewTokens) return cdiv(V, 16);
+  if (T <= kFewTokens) return cdiv(V, 64);
   int64_t n = 0;
   by_head_tile(T, V, H, [&](auto tile) { n = cdiv(V, 16 * decltype(tile)::type::NB); });
   return n;
