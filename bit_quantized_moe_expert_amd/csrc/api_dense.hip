@@ -53,18 +53,21 @@ FfnArgs ffn_args(const nf4moe_gated_ffn_t &f, const uint16_t *x, int64_t T) {
 }
 
 struct FfnCarve {
-  uint16_t *dgu;
+  uint16_t *dgu, *x2;
   float *part;
-  int slices;
+  int64_t rows;   // of dgu
   size_t bytes;
 };
 // One size whatever outputs are asked for: that of dx alone, which has the most slices.
 FfnCarve carve_ffn(void *ws, const nf4moe_gated_ffn_t &f, int64_t T) {
   FfnCarve c = {};
   Bump b{(char *)ws};
-  c.dgu = b.take<uint16_t>((size_t)T * 2 * f.I);
-  c.slices = product_slices(T, f.H, 2 * (int64_t)f.I, true);
-  if (c.slices > 1) c.part = b.take<float>((size_t)c.slices * T * f.H);
+  const bool few = T <= kTwoParts;
+  c.rows = few ? 2 * T : T;
+  c.dgu = b.take<uint16_t>((size_t)c.rows * 2 * f.I);
+  if (few) c.x2 = b.take<uint16_t>((size_t)c.rows * f.H);
+  const int slices = product_slices(c.rows, f.H, 2 * (int64_t)f.I, true);
+  if (few || slices > 1) c.part = b.take<float>((size_t)slices * c.rows * f.H);
   c.bytes = b.off;
   return c;
 }
@@ -91,11 +94,10 @@ struct HeadCarve {
   float *picked;
   uint32_t *list;
   int32_t *offsets;
-  uint16_t *P;
+  uint16_t *P, *x2;
   uint64_t *live;
   float *part;
-  int64_t piece;
-  int slices;
+  int64_t piece, rows;   // rows of P
   size_t bytes;
 };
 // k: teacher entries a row (0: labels). One size whatever outputs are asked for.
@@ -111,10 +113,13 @@ HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, int k, bool ba
     c.picked = b.take<float>(T);
   } else {
     c.piece = head_piece(T, h.V);
-    c.P = b.take<uint16_t>((size_t)T * c.piece);
-    c.live = b.take<uint64_t>((size_t)cdiv(T, 64));
-    c.slices = product_slices(T, h.H, c.piece < h.V ? c.piece : h.V, true);
-    if (c.slices > 1 || c.piece < h.V) c.part = b.take<float>((size_t)c.slices * T * h.H);
+    const bool few = T <= kTwoParts;
+    c.rows = few ? 2 * T : T;
+    c.P = b.take<uint16_t>((size_t)c.rows * c.piece);
+    if (few) c.x2 = b.take<uint16_t>((size_t)c.rows * h.H);
+    else c.live = b.take<uint64_t>((size_t)cdiv(T, 64));
+    const int slices = product_slices(c.rows, h.H, c.piece < h.V ? c.piece : h.V, true);
+    if (few || slices > 1 || c.piece < h.V) c.part = b.take<float>((size_t)slices * c.rows * h.H);
   }
   c.bytes = b.off;
   return c;
@@ -134,22 +139,24 @@ HeadArgs head_args(const nf4moe_head_t &h, const uint16_t *x, int64_t T, const i
 
 // The gradients of either loss, a piece of the vocabulary after the other.
 nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint16_t *dw, hipStream_t s) {
-  const int slices = product_slices(a.T, a.H, c.piece < a.V ? c.piece : a.V, !dw);
-  const bool parts = slices > 1 || c.piece < a.V;
-  a.P = c.P, a.live = dw ? c.live : nullptr, a.list = c.list, a.offsets = c.offsets;
+  const bool few = a.T <= kTwoParts;
+  const int slices = product_slices(c.rows, a.H, c.piece < a.V ? c.piece : a.V, !dw);
+  const bool parts = few || slices > 1 || c.piece < a.V;
+  a.P = c.P, a.live = dw ? c.live : nullptr, a.x2 = dw ? c.x2 : nullptr, a.list = c.list, a.offsets = c.offsets;
   hipError_t e = a.k ? launch_head_entries(a, s) : hipSuccess;
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += c.piece) {
     a.v0 = v0, a.vn = a.V - v0 < c.piece ? a.V - v0 : c.piece, a.vp = c.piece;
     e = launch_head_piece(a, s);
     if (e != hipSuccess) break;
     ProductArgs px = {}, pw = {};
-    px.x = a.P, px.ldx = c.piece, px.y = a.w + v0 * a.H, px.ldy = a.H, px.M = a.T, px.N = a.H, px.K = a.vn;
+    px.x = a.P, px.ldx = c.piece, px.y = a.w + v0 * a.H, px.ldy = a.H, px.M = c.rows, px.N = a.H, px.K = a.vn;
     px.out = parts ? nullptr : dx, px.part = c.part, px.add = v0 > 0, px.slices = slices;
-    pw.x = a.P, pw.ldx = c.piece, pw.y = a.x, pw.ldy = a.H, pw.M = a.vn, pw.N = a.H, pw.K = a.T;
+    pw.x = a.P, pw.ldx = c.piece, pw.y = few ? c.x2 : a.x, pw.ldy = a.H, pw.M = a.vn, pw.N = a.H, pw.K = c.rows;
     pw.out = dw + v0 * a.H, pw.slices = 1, pw.live = c.live;
     e = launch_products(dx ? &px : nullptr, dw ? &pw : nullptr, s);
   }
-  if (e == hipSuccess && dx && parts) e = launch_join(c.part, slices, a.T * a.H, dx, s);
+  // (few rows: a slice's second half are the second parts' rows, as one slice more)
+  if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, a.T * a.H, dx, s);
   return hip_status(e, "head backward launch");
 }
 
@@ -230,16 +237,19 @@ nf4moe_status_t nf4moe_gated_ffn_backward(const nf4moe_gated_ffn_t *ffn, const u
                      {{"dh", dh, hb}, {"x", x, xb}, {"w13", f.w13, wb}});
   if (st != NF4MOE_OK) return st;
   FfnArgs a = ffn_args(f, x, T);
-  a.dh = dh, a.dgu = c.dgu, a.h = h;
+  a.dh = dh, a.dgu = c.dgu, a.h = h, a.x2 = dw13 ? c.x2 : nullptr;
   hipError_t e = launch_ffn_dgu(a, s);
-  const int slices = product_slices(T, f.H, 2 * (int64_t)f.I, !dw13);
+  const bool few = T <= kTwoParts;
+  const int slices = product_slices(c.rows, f.H, 2 * (int64_t)f.I, !dw13);
+  const bool parts = few || slices > 1;
   ProductArgs px = {}, pw = {};
-  px.x = c.dgu, px.ldx = 2 * (int64_t)f.I, px.y = f.w13, px.ldy = f.H, px.M = T, px.N = f.H, px.K = 2 * (int64_t)f.I;
-  px.out = slices > 1 ? nullptr : dx, px.part = c.part, px.slices = slices;
-  pw.x = c.dgu, pw.ldx = 2 * (int64_t)f.I, pw.y = x, pw.ldy = f.H, pw.M = 2 * (int64_t)f.I, pw.N = f.H, pw.K = T;
+  px.x = c.dgu, px.ldx = 2 * (int64_t)f.I, px.y = f.w13, px.ldy = f.H, px.M = c.rows, px.N = f.H, px.K = 2 * (int64_t)f.I;
+  px.out = parts ? nullptr : dx, px.part = c.part, px.slices = slices;
+  pw.x = c.dgu, pw.ldx = 2 * (int64_t)f.I, pw.y = few ? c.x2 : x, pw.ldy = f.H, pw.M = 2 * (int64_t)f.I, pw.N = f.H, pw.K = c.rows;
   pw.out = dw13, pw.slices = 1;
   if (e == hipSuccess) e = launch_products(dx ? &px : nullptr, dw13 ? &pw : nullptr, s);
-  if (e == hipSuccess && dx && slices > 1) e = launch_join(c.part, slices, T * f.H, dx, s);
+  // (few rows: a slice's second half are the second parts' rows, as one slice more)
+  if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, T * f.H, dx, s);
   return hip_status(e, "gated feed-forward backward launch");
 }
 

@@ -7,6 +7,11 @@
 
 namespace nf4moe {
 
+// Up to so many rows a backward holds what it rounds between its products (dgu, P) as the sum of two bf16
+// parts, the second in rows T .. 2 T - 1, and x twice. One row's largest value may be most of its
+// gradients, and the rounding of it all of their error (up to 2^-8; many rows' roundings average out), and
+// the products' tiles have the room.
+constexpr int kTwoParts = 64;
 constexpr int kDenseMaxWidth = 1 << 20;   // H and I: 256 rows of it are below 2^31 bytes
 
 // out[m][n] = sum_k X(m, k) Y(n, k) in bf16, or in fp32 to `part` by slices of K (added to what is
@@ -36,12 +41,14 @@ struct FfnArgs {
   const uint16_t *x, *w13;   // [T, H], [2I, H]
   uint16_t *h;               // [T, I] (backward: optional)
   const uint16_t *dh;        // [T, I]
-  uint16_t *dgu;             // [T, 2I] in w13's row order
+  uint16_t *dgu;             // [T, 2I] in w13's row order; up to kTwoParts rows: [2 T, 2I], in two parts
+  uint16_t *x2;              // up to kTwoParts rows: [2 T, H], x twice (or null)
 };
 hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s);
 hipError_t launch_ffn_dgu(const FfnArgs &a, hipStream_t s);
 
 constexpr int kMaxTeacher = 1024;
+constexpr int kHeadFewRows = 32;   // up to so many rows the head's forward has a form of its own
 // The vocabulary head: logits x W^T, by k_head_* kernels that never store them.
 struct HeadArgs {
   int64_t T, V;
@@ -62,7 +69,8 @@ struct HeadArgs {
   // backward
   const float *dloss;        // [T]
   int64_t v0, vn, vp;        // the piece of the vocabulary, and the row stride of P
-  uint16_t *P;               // [T, vp]
+  uint16_t *P;               // [T, vp]; up to kTwoParts rows: [2 T, vp], in two parts
+  uint16_t *x2;              // up to kTwoParts rows: [2 T, H], x twice, zeros in the rows that do not count (or null)
   uint64_t *live;            // [T / 64] or null: a bit for each row, set where it has a gradient (written with the first piece)
 };
 constexpr int kHeadChunk = 128;

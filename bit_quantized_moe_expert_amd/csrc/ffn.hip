@@ -50,11 +50,20 @@ struct FfnPlace : GemmTiles {
   }
 };
 
-// BACK: dgu (and h where asked for) instead of h.
-template <class T, bool BACK>
+// BACK: dgu (and h where asked for) instead of h. FEW: up to kTwoParts rows, dgu in two parts and x twice.
+template <class T, bool BACK, bool FEW>
 __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
+  static_assert(BACK || !FEW, "two parts of what a backward rounds");
   constexpr int G = T::G, HC = 16 * G;   // a wave's columns of h
   __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+  if constexpr (FEW) {
+    const int n = (int)p.T * (p.H / 8);   // 16-byte pieces
+    for (int i = (int)blockIdx.x * T::THREADS + threadIdx.x; p.x2 && i < n; i += (int)gridDim.x * T::THREADS) {
+      const uint4 v = reinterpret_cast<const uint4 *>(p.x)[i];
+      reinterpret_cast<uint4 *>(p.x2)[i] = v;
+      reinterpret_cast<uint4 *>(p.x2)[n + i] = v;
+    }
+  }
   const FfnPlace<T> place(p, blockIdx.x, gridDim.x);
   int64_t m0, c0;
   if (!place.at(0, m0, c0)) return;
@@ -94,6 +103,26 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
         const BlockRow<HC> one{mine, lane}, two{mine + 32 * HC, lane};
         const BlockRow<2 * HC> both{mine, lane};
         uint2 h[G];
+        [[maybe_unused]] float low[2][FEW ? G : 1][4];
+        auto put = [&](int nb, const float (&dg)[4], const float (&du)[4]) __attribute__((always_inline)) {
+          const int c = T::col_of(lane, nb);
+          if (p.inter) {
+            both.put(2 * c, pack4(dg[0], du[0], dg[1], du[1]));
+            both.put(2 * c + 4, pack4(dg[2], du[2], dg[3], du[3]));
+          } else {
+            one.put(c, pack4(dg[0], dg[1], dg[2], dg[3]));
+            two.put(c, pack4(du[0], du[1], du[2], du[3]));
+          }
+        };
+        auto out = [&](int64_t first) __attribute__((always_inline)) {
+          uint16_t *dgu = p.dgu + (first + row0) * ld2;
+          if (p.inter) {
+            both.out(dgu + 2 * c0, ld2, rows, 2 * cols);
+          } else {
+            one.out(dgu + c0, ld2, rows, cols);
+            two.out(dgu + p.I + c0, ld2, rows, cols);
+          }
+        };
 #pragma unroll
         for (int nb = 0; nb < G; ++nb) {
           const float dh[4] = {bf16lo_to_f32(d[mb][nb].x), bf16hi_to_f32(d[mb][nb].x), bf16lo_to_f32(d[mb][nb].y), bf16hi_to_f32(d[mb][nb].y)};
@@ -103,23 +132,19 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
             float by_g, by_u;
             hv[j] = glu_slopes(p.glu, p.alpha, p.limit, t.acc[nb][mb][j], t.acc[nb + G][mb][j], by_g, by_u);
             dg[j] = dh[j] * by_g, du[j] = dh[j] * by_u;
+            if constexpr (FEW) {
+              low[0][nb][j] = dg[j] - bf16_to_f32(f32_to_bf16_rne(dg[j]));
+              low[1][nb][j] = du[j] - bf16_to_f32(f32_to_bf16_rne(du[j]));
+            }
           }
           h[nb] = pack4(hv[0], hv[1], hv[2], hv[3]);
-          const int c = T::col_of(lane, nb);
-          if (p.inter) {
-            both.put(2 * c, pack4(dg[0], du[0], dg[1], du[1]));
-            both.put(2 * c + 4, pack4(dg[2], du[2], dg[3], du[3]));
-          } else {
-            one.put(c, pack4(dg[0], dg[1], dg[2], dg[3]));
-            two.put(c, pack4(du[0], du[1], du[2], du[3]));
-          }
+          put(nb, dg, du);
         }
-        uint16_t *dgu = p.dgu + row0 * ld2;
-        if (p.inter) {
-          both.out(dgu + 2 * c0, ld2, rows, 2 * cols);
-        } else {
-          one.out(dgu + c0, ld2, rows, cols);
-          two.out(dgu + p.I + c0, ld2, rows, cols);
+        out(0);
+        if constexpr (FEW) {
+#pragma unroll
+          for (int nb = 0; nb < G; ++nb) put(nb, low[0][nb], low[1][nb]);
+          out(p.T);
         }
         if (p.h) {
 #pragma unroll
@@ -252,10 +277,18 @@ hipError_t ffn(const FfnArgs &a, hipStream_t s) {
     using T = typename decltype(tile)::type;
     const int64_t tiles = cdiv(a.T, T::BM) * cdiv(a.I, T::BN / 2);
     const int grid = T::KS > 1 ? (int)cdiv(tiles, 8) * 8 : gemm_grid(tiles, T::MOST);
-    hipLaunchKernelGGL((k_ffn<T, BACK>), dim3(grid), dim3(T::THREADS), 0, s, a);
+    if constexpr (BACK && T::BM == 64) {   // (the tiles of few rows)
+      if (a.T <= kTwoParts) {
+        hipLaunchKernelGGL((k_ffn<T, true, true>), dim3(grid), dim3(T::THREADS), 0, s, a);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((k_ffn<T, BACK, false>), dim3(grid), dim3(T::THREADS), 0, s, a);
     return hipGetLastError();
   };
-  switch (gemm_class(ffn_tile_count, &a, cdiv(a.H, kGemmBK))) {
+  int c = gemm_class(ffn_tile_count, &a, cdiv(a.H, kGemmBK));
+  if (a.T <= kTwoParts && c > 64) c = 64;
+  switch (c) {
     case 256: return go(TileTag<GemmTile<4, 8, 4, 2, false, false, 4>>());
     case 128: return go(TileTag<GemmTile<4, 4, 2, 2, false, false, 2>>());
     case 64: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2>>());

@@ -43,14 +43,16 @@ constexpr int kGemmBK = 64;
 // reads as zeros.
 constexpr uint32_t kOutside = 0x80000000u;
 __device__ inline u32x4_t rsrc_at(const char *p) {
-  const uint64_t a = (uint64_t)p;
-  return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, kOutside, 0x00027000u};
+  const uint64_t a = (uint64_t)p;   // the same in every lane
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)), kOutside, 0x00027000u};
 }
 // 16 bytes a lane from the descriptor's memory to LDS at `lds` + 16 lane. The load has no output
 // register; wait_loads and a barrier come before anyone reads what it wrote. (The compiler sets m0
 // right before its own uses of it and keeps nothing there.)
 __device__ inline void load_to_lds(u32x4_t rsrc, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rsrc));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(__builtin_amdgcn_readfirstlane((int)lds)),
+               "v"(off), "s"(rsrc));
 }
 // Until at most N of this wave's loads (in order) are on their way.
 template <int N>

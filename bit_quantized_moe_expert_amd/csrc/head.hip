@@ -394,10 +394,20 @@ __global__ __launch_bounds__(kEntryThreads) void k_head_entries(HeadArgs p) {
   }
 }
 
-template <class T, bool TEACH>
+// FEW: up to kTwoParts rows, P in two parts and x twice.
+template <class T, bool TEACH, bool FEW>
 __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadArgs p) {
   constexpr int COLS = 16 * T::NB;   // a wave's
   __shared__ __attribute__((aligned(16))) char lds[T::LDS];
+  if constexpr (FEW) {
+    const int row16 = p.H / 8, n = (int)p.T * row16;   // 16-byte pieces
+    for (int i = (int)blockIdx.x * T::THREADS + threadIdx.x; p.x2 && p.v0 == 0 && i < n; i += (int)gridDim.x * T::THREADS) {
+      uint4 v = reinterpret_cast<const uint4 *>(p.x)[i];
+      if (!row_on(p, i / row16)) v = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4 *>(p.x2)[i] = v;
+      reinterpret_cast<uint4 *>(p.x2)[n + i] = v;
+    }
+  }
   const HeadPlace<T> place(p, blockIdx.x, gridDim.x);
   int64_t m0, n0;
   if (!place.at(0, m0, n0)) return;
@@ -441,6 +451,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
       const uint64_t rows_on = __ballot(on);
       if (p.live && p.v0 + n0 == 0 && lane == 0) reinterpret_cast<uint16_t *>(p.live)[row0 >> 4] = (uint16_t)rows_on;
       const bool some = !TEACH && __any(want >= 0), all = __all(on) && left == COLS;
+      [[maybe_unused]] uint2 low[T::NB];
 #pragma unroll
       for (int nb = 0; nb < T::NB; ++nb) {
         float v[4];
@@ -456,7 +467,11 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = on && T::col_of(lane, nb) + j < left ? v[j] : 0.0f;
         }
-        out.put(T::col_of(lane, nb), pack4(v[0], v[1], v[2], v[3]));
+        const uint2 high = pack4(v[0], v[1], v[2], v[3]);
+        if constexpr (FEW)
+          low[nb] = pack4(v[0] - bf16lo_to_f32(high.x), v[1] - bf16hi_to_f32(high.x), v[2] - bf16lo_to_f32(high.y),
+                          v[3] - bf16hi_to_f32(high.y));
+        out.put(T::col_of(lane, nb), high);
       }
       if constexpr (TEACH) {   // the entries' places
         wave_lds_order();
@@ -466,7 +481,21 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
           *out.one(er, col) = (uint16_t)f32_to_bf16_rne(entry_value(row0 + er, j));
         });
       }
-      out.out(p.P + row0 * p.vp + n0, p.vp, p.T - row0, p.vp - n0);
+      uint16_t *to = p.P + row0 * p.vp + n0;
+      out.out(to, p.vp, p.T - row0, p.vp - n0);
+      if constexpr (FEW) {
+        auto rest_of = [](float v) { return (uint16_t)f32_to_bf16_rne(v - bf16_to_f32(f32_to_bf16_rne(v))); };
+#pragma unroll
+        for (int nb = 0; nb < T::NB; ++nb) out.put(T::col_of(lane, nb), low[nb]);
+        if constexpr (TEACH) {
+          wave_lds_order();
+          if (lane < entries.n[mb])
+            entries.one(entries.w[mb], [&](int er, int col, int) { *out.one(er, col) = rest_of(value[mb]); });
+          entries.rest(p, lane, m0 + T::row_at(0), mb,
+                       [&](int er, int col, int j) { *out.one(er, col) = rest_of(entry_value(row0 + er, j)); });
+        }
+        out.out(to + p.T * p.vp, p.vp, p.T - row0, p.vp - n0);
+      }
     }
   });
 }
@@ -482,7 +511,9 @@ int64_t head_tile_count(const void *size, int b) {
 template <class F>
 void by_head_tile(int64_t T, int64_t V, int H, F &&f) {
   const HeadSize size{T, V};
-  switch (gemm_class(head_tile_count, &size, cdiv(H, kGemmBK))) {
+  int c = gemm_class(head_tile_count, &size, cdiv(H, kGemmBK));
+  if (T <= kTwoParts && c > 64) c = 64;
+  switch (c) {
     case 256: return f(TileTag<GemmTile<4, 8, 4, 2>>());
     case 128: return f(TileTag<GemmTile<4, 4, 2, 2>>());
     case 64: return f(TileTag<GemmTile<2, 2, 2, 2>>());
@@ -494,12 +525,11 @@ dim3 head_grid(int64_t rows, int64_t cols) {
   const int64_t tiles = cdiv(rows, T::BM) * cdiv(cols, T::BN);
   return dim3(T::KS > 1 ? (unsigned)cdiv(tiles, 8) * 8 : gemm_grid(tiles, T::MOST));
 }
-constexpr int kFewTokens = 32;
 
 }  // namespace
 
 int64_t head_stat_chunks(int64_t T, int64_t V, int H) {
-  if (T <= kFewTokens) return cdiv(V, 64);
+  if (T <= kHeadFewRows) return cdiv(V, 64);
   int64_t n = 0;
   by_head_tile(T, V, H, [&](auto tile) { n = cdiv(V, 16 * decltype(tile)::type::NB); });
   return n;
@@ -514,7 +544,7 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.T <= kFewTokens) {
+  if (a.T <= kHeadFewRows) {
     const dim3 grid((unsigned)cdiv(a.V, 64)), block(512);
     if (a.T <= 16 && a.k) hipLaunchKernelGGL((k_head_few<1, true>), grid, block, 0, s, a);
     else if (a.T <= 16) hipLaunchKernelGGL((k_head_few<1, false>), grid, block, 0, s, a);
@@ -547,8 +577,15 @@ hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s) {
   by_head_tile(a.T, a.vn, a.H, [&](auto tile) {
     using T = typename decltype(tile)::type;
     const dim3 grid = head_grid<T>(a.T, a.vn);
-    if (a.k) hipLaunchKernelGGL((k_head_piece<T, true>), grid, dim3(T::THREADS), 0, s, a);
-    else hipLaunchKernelGGL((k_head_piece<T, false>), grid, dim3(T::THREADS), 0, s, a);
+    if constexpr (T::BM == 64) {   // (the tiles of few rows)
+      if (a.T <= kTwoParts) {
+        if (a.k) hipLaunchKernelGGL((k_head_piece<T, true, true>), grid, dim3(T::THREADS), 0, s, a);
+        else hipLaunchKernelGGL((k_head_piece<T, false, true>), grid, dim3(T::THREADS), 0, s, a);
+        return;
+      }
+    }
+    if (a.k) hipLaunchKernelGGL((k_head_piece<T, true, false>), grid, dim3(T::THREADS), 0, s, a);
+    else hipLaunchKernelGGL((k_head_piece<T, false, false>), grid, dim3(T::THREADS), 0, s, a);
   });
   return hipGetLastError();
 }

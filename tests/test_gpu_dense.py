@@ -37,6 +37,12 @@ def near(got, ref, roundings, what):
         assert R.off(got, ref) < (0.6, 0.85)[roundings - 1] * B, what
 
 
+def few(got, ref, T, what):
+    """Up to 64 rows nothing is rounded to bf16 but the output: b of the norm at most, whatever the values."""
+    if T <= 64 and ref.norm() > 0:
+        assert R.off(got, ref) < 1.02 * B, what
+
+
 def product_bound(x, w):
     """How far fp32 sums of x w^T may be off."""
     return 2 * x.shape[1] * U * (x.double().abs() @ w.double().abs().T)
@@ -94,6 +100,7 @@ def test_gated_ffn(T, H, I, kind, inter):
     ew = R.join((rg + 2 * T * U * (dg.abs() + rg)).T @ xa, (ru + 2 * T * U * (du.abs() + ru)).T @ xa, inter)
     R.within(out["dw13"], dw, B * dw.abs() + (1 + B) * ew, "dw13")
     near(got, h, 1, "h"), near(out["dx"], dx, 2, "dx"), near(out["dw13"], dw, 2, "dw13")
+    few(out["dx"], dx, T, "dx"), few(out["dw13"], dw, T, "dw13")
     again = M.gated_ffn_backward(dh, x, w, need=("dx", "dw13", "h"), **kw)
     assert all(torch.equal(out[n], again[n]) for n in out)
     for n, ref, e in (("dx", dx, ex), ("dw13", dw, ew)):    # alone: the sums may be cut differently
@@ -172,6 +179,8 @@ def test_vocab_ce(T, H, V):
     R.within(out["dx"], dx, B * dx.abs() + (1 + B) * ex, "dx")
     R.within(out["dw"], dw, B * dw.abs() + (1 + B) * ew, "dw")
     near(out["dx"], dx, 2, "dx"), near(out["dw"], dw, 2, "dw")
+    if V > 1:    # (of one class P is a rounding error of 1 - 1)
+        few(out["dx"], dx, T, "dx"), few(out["dw"], dw, T, "dw")
     dead = (labels < 0) | (labels >= V)
     assert not out["dx"][dead].any() and not got_loss[dead].any()
     again = M.vocab_ce_backward(dloss, x, w, labels, got_lse)
@@ -222,6 +231,8 @@ def test_vocab_distill(T, H, V, k, tau, tdt):
     R.within(out["dx"], dx, B * dx.abs() + (1 + B) * ex, "dx")
     R.within(out["dw"], dw, B * dw.abs() + (1 + B) * ew, "dw")
     assert not out["dx"][~row].any()
+    if V > 1:
+        few(out["dx"], dx, T, "dx"), few(out["dw"], dw, T, "dw")
     again = M.vocab_distill_backward(*args, temperature=tau, need=("dw", "dx"))
     assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dw"], out["dw"])
     one = M.vocab_distill_backward(*args, temperature=tau, need=("dx",))
