@@ -13,6 +13,7 @@ using namespace nf4moe;
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxHeadRows = (int64_t)1 << 25;   // 64 threads a row (k_head_entries) are inside a dispatch's 2^32
 constexpr int kMaxVocab = 1 << 21;   // 256 rows of P are below 2^31 bytes
 
 nf4moe_status_t check_width(int v, const char *name) {
@@ -78,6 +79,7 @@ nf4moe_status_t check_head(const nf4moe_head_t *h, int64_t T) {
   nf4moe_status_t st = check_width(h->H, "H");
   if (st != NF4MOE_OK) return st;
   if (h->V < 1 || h->V > kMaxVocab) return fail(NF4MOE_ERR_INVALID_ARG, "V=%d outside 1..%d", h->V, kMaxVocab);
+  if (T > kMaxHeadRows) return fail(NF4MOE_ERR_UNSUPPORTED, "T=%lld rows are too many for one call (2^25)", (long long)T);
   st = check_size(T, h->V);
   if (st == NF4MOE_OK) st = check_size(T, h->H);
   if (st == NF4MOE_OK) st = check_size(h->V, h->H);
@@ -112,9 +114,9 @@ HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, int k, bool ba
     c.stats = b.take<float2>((size_t)head_stat_chunks(T, h.V, h.H) * T);
     c.picked = b.take<float>(T);
   } else {
-    c.piece = head_piece(T, h.V);
     const bool few = T <= kTwoParts;
     c.rows = few ? 2 * T : T;
+    c.piece = head_piece(c.rows, h.V);
     c.P = b.take<uint16_t>((size_t)c.rows * c.piece);
     if (few) c.x2 = b.take<uint16_t>((size_t)c.rows * h.H);
     else c.live = b.take<uint64_t>((size_t)cdiv(T, 64));

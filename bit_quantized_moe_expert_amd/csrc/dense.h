@@ -79,7 +79,7 @@ hipError_t launch_head_forward(const HeadArgs &a, hipStream_t s);
 // The teacher's lists for the backward's pieces.
 hipError_t launch_head_entries(const HeadArgs &a, hipStream_t s);
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s);
-int64_t head_piece(int64_t T, int64_t V);
+int64_t head_piece(int64_t rows, int64_t V);   // rows of P, one at least
 
 struct LayerNormArgs {
   int64_t T;

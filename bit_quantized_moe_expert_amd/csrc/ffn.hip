@@ -15,13 +15,22 @@ namespace nf4moe {
 
 namespace {
 
-// h and the activation's derivatives by gate and up. The clamped form's gradient is that of the
+// The clamps by comparisons, which a NaN passes through (the minimum of a NaN and a limit is the limit).
+__device__ inline float not_above(float v, float limit) { return v > limit ? limit : v; }
+__device__ inline float within(float v, float limit) { return not_above(v < -limit ? -limit : v, limit); }
+
+// h from gate and up, as glu_value.
+__device__ inline float glu_of(int glu, float alpha, float limit, float g, float u) {
+  if (glu == 1) return (within(u, limit) + 1.0f) * sig_gate(not_above(g, limit), alpha);
+  return sig_gate(g, 1.0f) * u;
+}
+// The same, and the activation's derivatives by gate and up. The clamped form's gradient is that of the
 // unclamped side at the limit itself.
 __device__ inline float glu_slopes(int glu, float alpha, float limit, float g, float u, float &by_g, float &by_u) {
   const bool clamped = glu == 1;
   const float a = clamped ? alpha : 1.0f;
-  const float gc = clamped ? fminf(g, limit) : g;
-  const float uc = clamped ? fminf(fmaxf(u, -limit), limit) + 1.0f : u;
+  const float gc = clamped ? not_above(g, limit) : g;
+  const float uc = clamped ? within(u, limit) + 1.0f : u;
   const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gc * (-1.44269504088896341f * a)));
   const float gs = gc * s;
   by_u = clamped && fabsf(u) > limit ? 0.0f : gs;
@@ -95,7 +104,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
         for (int nb = 0; nb < G; ++nb) {
           float h[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = glu_value(p.glu, p.alpha, p.limit, t.acc[nb][mb][j], t.acc[nb + G][mb][j]);
+          for (int j = 0; j < 4; ++j) h[j] = glu_of(p.glu, p.alpha, p.limit, t.acc[nb][mb][j], t.acc[nb + G][mb][j]);
           out.put(T::col_of(lane, nb), pack4(h[0], h[1], h[2], h[3]));
         }
         out.out(p.h + row0 * p.I + c0, p.I, rows, cols);
@@ -173,7 +182,7 @@ __global__ __launch_bounds__(512) void k_ffn_few(FfnArgs p) {
   if (wave >= MB) return;
   float h[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) h[j] = glu_value(p.glu, p.alpha, p.limit, v[j], __shfl_xor(v[j], 32, kWave));   // (lanes 0 .. 31: the gate rows)
+  for (int j = 0; j < 4; ++j) h[j] = glu_of(p.glu, p.alpha, p.limit, v[j], __shfl_xor(v[j], 32, kWave));   // (lanes 0 .. 31: the gate rows)
   if (lane < 32 && token < T)
     *reinterpret_cast<uint2 *>(p.h + (int64_t)token * p.I + c0 + 4 * (lane >> 4)) = pack4(h[0], h[1], h[2], h[3]);
 }
@@ -251,10 +260,8 @@ __global__ __launch_bounds__(TX::THREADS, TX::WAVES_SIMD) void k_products(Produc
   else product_tiles<TW>(dw, lds, (int)blockIdx.x - nbx, (int)gridDim.x - nbx);
 }
 
-// 8 values a thread, n a multiple of 8.
-__global__ __launch_bounds__(256) void k_join(const float *part, int slices, int64_t n, uint16_t *out) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
+// 8 values a thread at a time, n a multiple of 8.
+__device__ inline void join8(const float *part, int slices, int64_t n, uint16_t *out, int64_t i) {
   float4 a = make_float4(0, 0, 0, 0), b = a;
   for (int s = 0; s < slices; ++s) {
     const float4 *at = reinterpret_cast<const float4 *>(part + s * n + i);
@@ -264,6 +271,10 @@ __global__ __launch_bounds__(256) void k_join(const float *part, int slices, int
   }
   const uint2 lo = pack4(a.x, a.y, a.z, a.w), hi = pack4(b.x, b.y, b.z, b.w);
   *reinterpret_cast<uint4 *>(out + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+__global__ __launch_bounds__(256) void k_join(const float *part, int slices, int64_t n, uint16_t *out) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048)
+    join8(part, slices, n, out, i);
 }
 
 int64_t ffn_tile_count(const void *args, int b) {
@@ -361,7 +372,8 @@ int product_slices(int64_t M, int64_t N, int64_t K, bool alone) {
 }
 
 hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s) {
-  hipLaunchKernelGGL(k_join, dim3((unsigned)cdiv(n, 2048)), dim3(256), 0, s, part, slices, n, out);
+  const int64_t g = cdiv(n, 2048);   // (up to 2^23 workgroups: inside a dispatch's 2^32 threads)
+  hipLaunchKernelGGL(k_join, dim3((unsigned)(g < 1 << 23 ? g : 1 << 23)), dim3(256), 0, s, part, slices, n, out);
   return hipGetLastError();
 }
 

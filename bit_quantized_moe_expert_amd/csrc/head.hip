@@ -590,11 +590,11 @@ hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Columns of a piece: P [T, piece] in bf16 takes at most 128 MB of the 256 MB last-level cache, so that
-// the two products read it from there; whole rounds of 256 tiles where T allows (4096 columns for
+// Columns of a piece: P [rows, piece] in bf16 takes at most 128 MB of the 256 MB last-level cache, so that
+// the two products read it from there; whole rounds of 256 tiles where the rows allow (4096 columns for
 // 4096 rows), at least 256.
-int64_t head_piece(int64_t T, int64_t V) {
-  int64_t n = ((int64_t)1 << 26) / (T > 0 ? T : 1);
+int64_t head_piece(int64_t rows, int64_t V) {
+  int64_t n = ((int64_t)1 << 26) / rows;
   if (n >= V) return (V + 255) / 256 * 256;
   n = n >= 4096 ? n / 4096 * 4096 : n / 256 * 256;
   return n < 256 ? 256 : n;

@@ -56,8 +56,9 @@ def gated_ffn_backward(dh, x, w13, *, glu: int = 0, alpha: float = 0.0, limit: f
                        need=("dx", "dw13")):
     """Gradients of gated_ffn_forward for dh bf16 [T, I], from x and w13 alone (gate and up
     are computed again). Returns a dict of those in `need`: dx bf16 [T, H], dw13 bf16 [2I,
-    H] in w13's row order, h (the forward's output, for the next weight's gradient). The
-    same bits on every run."""
+    H] in w13's row order, and beside them h (the forward's output, for the next weight's
+    gradient). The same bits on every run of the same call (dx alone may be summed in
+    another order than beside dw13)."""
     _need(need, ("dx", "dw13", "h"))
     st, xp, T, H, I, i = _ffn_args(x, w13, glu, alpha, limit, interleaved)
     dp = _arg(dh, "dh", (T, I), _BF16, i)
@@ -112,7 +113,8 @@ def _head_backward(x, w, T, k, st, need, call):
 def vocab_ce_backward(dloss, x, w, labels, lse, *, need=("dx", "dw")):
     """Gradients of vocab_ce_forward for dloss fp32 [T], with the forward's lse. Returns a
     dict of those in `need`: dx bf16 [T, H], dw bf16 [V, H]. Rows without a label count for
-    nothing, whatever x and dloss hold there. The same bits on every run."""
+    nothing, whatever x and dloss hold there. The same bits on every run of the same call (dx
+    alone may be summed in another order than beside dw)."""
     st, xp, T, i = _head_args(x, w)
     gp, lp, sp = _arg(dloss, "dloss", (T,), _F32, i), _arg(labels, "labels", (T,), _I32, i), _arg(lse, "lse", (T,), _F32, i)
     return _head_backward(x, w, T, 0, st, need, lambda dx, dw, ws, nb: _run(
@@ -145,8 +147,8 @@ def vocab_distill_forward(x, w, ids, teacher, *, temperature: float = 1.0):
 
 def vocab_distill_backward(dloss, x, w, ids, q, logits, lse, *, temperature: float = 1.0, need=("dx", "dw")):
     """Gradients of vocab_distill_forward for dloss fp32 [T], with the forward's q, logits and
-    lse. Returns a dict of those in `need`: dx bf16 [T, H], dw bf16 [V, H]. The same bits on
-    every run."""
+    lse. Returns a dict of those in `need`: dx bf16 [T, H], dw bf16 [V, H]. The same bits as
+    in vocab_ce_backward."""
     st, xp, T, i = _head_args(x, w)
     k = _i32(_dims(ids, "ids", 2)[1], "k")
     gp, ip = _arg(dloss, "dloss", (T,), _F32, i), _arg(ids, "ids", (T, k), _I32, i)

@@ -521,8 +521,10 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
  * those of the fine-tuning calls above. Matrices are bf16, contiguous and 16-byte aligned, their
  * widths (H, I) multiples of 8 up to 2^20; products are summed in fp32, every output is
  * rounded once; the gradient of a product (dgu, P below) is rounded to bf16 where it becomes
- * an operand of the next. The same bits on every run. UNSUPPORTED past 2^22 tiles of 256 x
- * 256 of one product, or 2^38 values.
+ * an operand of the next, up to 64 rows to the sum of two bf16 values. The same bits on every run of
+ * the same call (dx asked for without the weight's gradient may be summed in another order than
+ * beside it). UNSUPPORTED past 2^22 tiles of 256 x 256 of one product, 2^38 values, or 2^25 rows of
+ * a vocabulary loss.
  *
  * Gated feed-forward: g = x Wg^T, u = x Wu^T, h = the gated activation (nf4moe_glu_t) of g and u.
  * ------------------------------------------------------------------------- */
@@ -546,8 +548,8 @@ size_t nf4moe_gated_ffn_workspace_bytes(const nf4moe_gated_ffn_t *ffn, int64_t T
  *   dx   bf16 [T, H]    dgu W13           (NULL: not computed)
  *   dw13 bf16 [2I, H]   dgu^T x, in w13's row order   (NULL: not computed)
  *   h    bf16 [T, I]    the forward's output again (optional)
- * The clamped form's gradient is that of the unclamped side at the limit itself. T == 0 writes
- * zeros to dw13. Errors: INVALID_ARG (neither dx nor dw13 among them), WORKSPACE, UNSUPPORTED. */
+ * The clamped form's gradient is that of the unclamped side at the limit itself; a NaN passes through
+ * its clamps. T == 0 writes zeros to dw13. Errors: INVALID_ARG (neither dx nor dw13 among them), WORKSPACE, UNSUPPORTED. */
 nf4moe_status_t nf4moe_gated_ffn_backward(const nf4moe_gated_ffn_t *ffn, const uint16_t *dh, const uint16_t *x, int64_t T,
                                           uint16_t *dx, uint16_t *dw13, uint16_t *h, void *ws, size_t ws_bytes,
                                           void *stream);
@@ -561,7 +563,8 @@ typedef struct {
 
 /* nf4moe_vocab_workspace_bytes -- workspace of the forward (backward = 0) or the backward (1) of
  * the cross entropy (k = 0) or of the distillation from k entries a row, for T rows; 0 for T < 1 or
- * invalid sizes. The backward's holds the gradient of one piece of the vocabulary at a time (at most 128 MB, or 256 columns). */
+ * invalid sizes. The backward's holds the gradient P of one piece of the vocabulary at a
+ * time: at most 128 MB of it, or 256 columns. */
 size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_t k, int32_t backward);
 
 /* nf4moe_vocab_ce_forward -- softmax cross entropy: lse[t] = log sum_v exp(l[t, v]) and loss[t] =

@@ -200,6 +200,25 @@ def test_head_backward_workspace_is_bounded():
             assert n <= P + 2 * 256 * T + 64 * T * 64 * 4 + T + 4096, (T, V, n)
 
 
+def test_head_backward_workspace_of_few_rows():
+    """Up to 64 rows P has two parts: together at most 128 MB, or 256 columns."""
+    for T in (1, 33, 48, 64):
+        for V in (100, 50304, 1 << 21):
+            n = L.nf4moe_vocab_workspace_bytes(head_desc(H=64, V=V), T, 0, 1)
+            # x twice and dx's parts of two rows a row, 64 slices at most
+            assert 0 < n <= (128 << 20) + 2 * T * 64 * 2 + 64 * 2 * T * 64 * 4 + 4096, (T, V, n)
+
+
+def test_head_rows_past_a_dispatch_are_refused():
+    for f in (ce_fwd, ce_bwd, ds_fwd, ds_bwd):
+        d = head_desc(H=8, V=100)
+        assert f(d, T=(1 << 25) + 1) == UNSUPPORTED and "2^25" in L.nf4moe_last_error().decode()
+        assert L.nf4moe_vocab_workspace_bytes(d, (1 << 25) + 1, 0, 1) == 0 < L.nf4moe_vocab_workspace_bytes(d, 1 << 25, 0, 1)
+        if not GPU:
+            # (the arrays lie far apart: none of them is longer than 2^40 bytes)
+            assert f(d, T=1 << 25, n=BIG >> 22) == HIP
+
+
 def ln_desc(H=64, xdt=1, ydt=1, w=far(9), b=far(10), eps=1e-5):
     return dense._LAYER_NORM.pack(H, xdt, ydt, w or 0, b or 0, eps)
 

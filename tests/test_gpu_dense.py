@@ -135,6 +135,23 @@ def test_gated_ffn_not_finite_stays_in_its_row():
     assert torch.equal(got[rows], want[rows]) and torch.isnan(got[77]).all()
 
 
+@pytest.mark.parametrize("T", [5, 40, 200])
+@pytest.mark.parametrize("inter", [0, 1])
+def test_clamped_ffn_shows_a_nan(T, inter):
+    """A NaN passes through the clamps, forward and backward, to its row and to the weights' gradient."""
+    x, w, dh = ffn_case(T, 128, 64, 1)
+    how = dict(glu=1, alpha=1.702, limit=7.0, interleaved=inter)
+    want = M.gated_ffn_forward(x, w, **how)
+    grad = M.gated_ffn_backward(dh, x, w, need=("dx", "dw13", "h"), **how)
+    x[3, 5] = NAN
+    got = M.gated_ffn_forward(x, w, **how)
+    out = M.gated_ffn_backward(dh, x, w, need=("dx", "dw13", "h"), **how)
+    rows = torch.arange(T, device=DEV) != 3
+    assert torch.equal(got[rows], want[rows]) and torch.isnan(got[3]).all()
+    assert torch.equal(out["h"][rows], grad["h"][rows]) and torch.isnan(out["h"][3]).all()
+    assert torch.equal(out["dx"][rows], grad["dx"][rows]) and torch.isnan(out["dx"][3]).all() and torch.isnan(out["dw13"]).all()
+
+
 # ------------------------------------------------------------------ losses of a head
 HEAD_SIZES = [(1, 8, 1), (1, 64, 5), (2, 2048, 3001), (17, 2048, 3001), (33, 72, 777), (64, 128, 64), (129, 264, 4099),
               (300, 128, 20001), (515, 1024, 2003), (4096, 64, 20003), (20000, 32, 5003)]
