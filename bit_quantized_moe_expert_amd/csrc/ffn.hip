@@ -277,9 +277,9 @@ __global__ __launch_bounds__(256) void k_join(const float *part, int slices, int
     join8(part, slices, n, out, i);
 }
 
-int64_t ffn_tile_count(const void *args, int b) {
+int64_t ffn_tile_count(const void *args, int bm, int bn) {
   const FfnArgs &a = *static_cast<const FfnArgs *>(args);
-  return cdiv(a.T, b) * cdiv(a.I, b / 2);
+  return cdiv(a.T, bm) * cdiv(a.I, bn / 2);
 }
 
 template <bool BACK>
@@ -301,6 +301,7 @@ hipError_t ffn(const FfnArgs &a, hipStream_t s) {
   if (a.T <= kTwoParts && c > 64) c = 64;
   switch (c) {
     case 256: return go(TileTag<GemmTile<4, 8, 4, 2, false, false, 4>>());
+    case 192: return go(TileTag<GemmTile<3, 8, 4, 2, false, false, 4>>());
     case 128: return go(TileTag<GemmTile<4, 4, 2, 2, false, false, 2>>());
     case 64: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2>>());
     default: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2, false, 4>>());
@@ -310,9 +311,12 @@ hipError_t ffn(const FfnArgs &a, hipStream_t s) {
 struct ProductPair {
   const ProductArgs &x, &w;
 };
-int64_t product_tile_count(const void *args, int b) {
+int64_t product_tile_count(const void *args, int bm, int bn) {
   const ProductPair &a = *static_cast<const ProductPair *>(args);
-  return (a.x.K ? cdiv(a.x.M, b) * cdiv(a.x.N, b) * a.x.slices : 0) + (a.w.K ? cdiv(a.w.M, b) * cdiv(a.w.N, b) : 0);
+  const int64_t x = a.x.K ? cdiv(a.x.M, bm) * cdiv(a.x.N, bn) * a.x.slices : 0;
+  if (!a.w.K) return x;
+  if (bm == 192) return (int64_t)1 << 40;   // (dx alone: a turned side of 192 rows has no whole pieces a thread)
+  return x + cdiv(a.w.M, bm) * cdiv(a.w.N, bn);
 }
 
 template <class TX, class TW>
@@ -341,6 +345,7 @@ hipError_t products(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
   const int64_t steps = cdiv(x.K > w.K ? x.K : w.K, kGemmBK);
   switch (gemm_class(product_tile_count, &both, steps)) {
     case 256: return products_of<4, 8, 4, 2, MASK>(x, w, s);
+    case 192: return products<GemmTile<3, 8, 4, 2, false, true>, GemmTile<4, 8, 4, 2, true, true>>(x, w, s);
     case 128: return products_of<4, 4, 2, 2, MASK>(x, w, s);
     case 64: return products_of<2, 2, 2, 2, MASK>(x, w, s);
     default: return products_of<2, 2, 2, 2, MASK, 4>(x, w, s);

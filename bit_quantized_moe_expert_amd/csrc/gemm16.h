@@ -476,17 +476,19 @@ struct GemmTiles {
 };
 // About how long `tiles` tiles take that run `slots` at a time, in rounds of 256 tiles of 256 x 256: a
 // whole round takes `full`, a last one with few tiles `least` at the least (fewer CUs at work run faster).
-// Measured for 2048 k (us): 64 tiles of 256 x 256 42, 256 as 49; of 128 x 128 128 tiles 20.9, 256 27, 512 35;
-// of 64 x 64 256 tiles 16.6, 512 22, 1024 28.9, 2048 54.
+// Measured for 2048 k (us): 64 tiles of 256 x 256 42, 256 as 49; of 192 x 256 64 tiles 34.5, 224 40.7; of
+// 128 x 128 128 tiles 20.9, 256 27, 512 35; of 64 x 64 256 tiles 16.6, 512 22, 1024 28.9, 2048 54.
 inline double gemm_rounds(int64_t tiles, int slots, double full, double least) {
   const int64_t whole = tiles / slots, rest = tiles % slots;
   return whole * full + (rest ? least + (full - least) * rest / slots : 0.0);
 }
-// The tile for that: 256, 128 or 64, or 16 for small products (64 x 64 with the k shared by groups of waves).
-inline int gemm_class(int64_t (*tiles)(const void *, int), const void *of, int64_t steps) {
-  const double l = gemm_rounds(tiles(of, 256), 256, 1.0, 0.85), m = gemm_rounds(tiles(of, 128), 512, 0.68, 0.42),
-               q = gemm_rounds(tiles(of, 64), 1024, 0.52, 0.35);
-  if (tiles(of, 64) <= 256 && steps >= 8) return 16;
+// The tile for that: 256, 192 (by 256 columns), 128 or 64, or 16 for small products (64 x 64 with the k shared
+// by groups of waves). tiles(of, BM, BN): how many there are.
+inline int gemm_class(int64_t (*tiles)(const void *, int, int), const void *of, int64_t steps) {
+  if (tiles(of, 64, 64) <= 256 && steps >= 8) return 16;
+  const double l = gemm_rounds(tiles(of, 256, 256), 256, 1.0, 0.85), k = gemm_rounds(tiles(of, 192, 256), 256, 0.78, 0.66),
+               m = gemm_rounds(tiles(of, 128, 128), 512, 0.68, 0.42), q = gemm_rounds(tiles(of, 64, 64), 1024, 0.52, 0.35);
+  if (k < l && k < m && k < q) return 192;
   return l <= m && l <= q ? 256 : m <= q ? 128 : 64;
 }
 template <class T>

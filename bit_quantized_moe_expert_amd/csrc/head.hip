@@ -503,9 +503,9 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
 struct HeadSize {
   int64_t T, V;
 };
-int64_t head_tile_count(const void *size, int b) {
+int64_t head_tile_count(const void *size, int bm, int bn) {
   const HeadSize &a = *static_cast<const HeadSize *>(size);
-  return cdiv(a.T, b) * cdiv(a.V, b);
+  return cdiv(a.T, bm) * cdiv(a.V, bn);
 }
 // f(the tile of a call)
 template <class F>
@@ -515,6 +515,7 @@ void by_head_tile(int64_t T, int64_t V, int H, F &&f) {
   if (T <= kTwoParts && c > 64) c = 64;
   switch (c) {
     case 256: return f(TileTag<GemmTile<4, 8, 4, 2>>());
+    case 192: return f(TileTag<GemmTile<3, 8, 4, 2>>());
     case 128: return f(TileTag<GemmTile<4, 4, 2, 2>>());
     case 64: return f(TileTag<GemmTile<2, 2, 2, 2>>());
     default: return f(TileTag<GemmTile<2, 2, 2, 2, false, false, 0, false, 4>>());
