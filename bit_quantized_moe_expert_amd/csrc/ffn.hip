@@ -260,21 +260,48 @@ __global__ __launch_bounds__(TX::THREADS, TX::WAVES_SIMD) void k_products(Produc
   else product_tiles<TW>(dw, lds, (int)blockIdx.x - nbx, (int)gridDim.x - nbx);
 }
 
-// 8 values a thread at a time, n a multiple of 8.
-__device__ inline void join8(const float *part, int slices, int64_t n, uint16_t *out, int64_t i) {
-  float4 a = make_float4(0, 0, 0, 0), b = a;
-  for (int s = 0; s < slices; ++s) {
-    const float4 *at = reinterpret_cast<const float4 *>(part + s * n + i);
-    const float4 u = at[0], v = at[1];
-    a = make_float4(a.x + u.x, a.y + u.y, a.z + u.z, a.w + u.w);
-    b = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
-  }
-  const uint2 lo = pack4(a.x, a.y, a.z, a.w), hi = pack4(b.x, b.y, b.z, b.w);
-  *reinterpret_cast<uint4 *>(out + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-}
+// Few slices: 8 values a thread at a time, n a multiple of 8.
 __global__ __launch_bounds__(256) void k_join(const float *part, int slices, int64_t n, uint16_t *out) {
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048)
-    join8(part, slices, n, out, i);
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
+    float4 a = make_float4(0, 0, 0, 0), b = a;
+    for (int s = 0; s < slices; ++s) {
+      const float4 *at = reinterpret_cast<const float4 *>(part + s * n + i);
+      const float4 u = at[0], v = at[1];
+      a = make_float4(a.x + u.x, a.y + u.y, a.z + u.z, a.w + u.w);
+      b = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
+    }
+    const uint2 lo = pack4(a.x, a.y, a.z, a.w), hi = pack4(b.x, b.y, b.z, b.w);
+    *reinterpret_cast<uint4 *>(out + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+}
+// Many: a workgroup 256 values at a time, wave w the slices w, w + 8, .. in order, asked for eight together;
+// then the waves in order. (128 slices of 3168 values: 19 us by k_join, two workgroups with 128 trips to
+// memory each, 4 by this.)
+__global__ __launch_bounds__(512) void k_join_many(const float *part, int slices, int64_t n, uint16_t *out) {
+  __shared__ float4 red[8][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < n; i0 += (int64_t)gridDim.x * 256) {
+    const int64_t i = i0 + 4 * lane;
+    float4 a = make_float4(0, 0, 0, 0);
+    if (i < n) {
+#pragma unroll 8
+      for (int s = wave; s < slices; s += 8) {
+        const float4 v = *reinterpret_cast<const float4 *>(part + s * n + i);
+        a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+      }
+    }
+    red[wave][lane] = a;
+    lds_barrier();
+    if (wave == 0 && i < n) {
+#pragma unroll
+      for (int w = 1; w < 8; ++w) {
+        const float4 v = red[w][lane];
+        a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+      }
+      *reinterpret_cast<uint2 *>(out + i) = pack4(a.x, a.y, a.z, a.w);
+    }
+    lds_barrier();
+  }
 }
 
 int64_t ffn_tile_count(const void *args, int bm, int bn) {
@@ -377,8 +404,10 @@ int product_slices(int64_t M, int64_t N, int64_t K, bool alone) {
 }
 
 hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s) {
-  const int64_t g = cdiv(n, 2048);   // (up to 2^23 workgroups: inside a dispatch's 2^32 threads)
-  hipLaunchKernelGGL(k_join, dim3((unsigned)(g < 1 << 23 ? g : 1 << 23)), dim3(256), 0, s, part, slices, n, out);
+  const int64_t g = cdiv(n, slices > 4 ? 256 : 2048), most = 1 << 22;   // (well inside a dispatch's 2^32 threads)
+  const dim3 grid((unsigned)(g < most ? g : most));
+  if (slices > 4) hipLaunchKernelGGL(k_join_many, grid, dim3(512), 0, s, part, slices, n, out);
+  else hipLaunchKernelGGL(k_join, grid, dim3(256), 0, s, part, slices, n, out);
   return hipGetLastError();
 }
 
