@@ -315,7 +315,7 @@ hipError_t ffn(const FfnArgs &a, hipStream_t s) {
     using T = typename decltype(tile)::type;
     const int64_t tiles = cdiv(a.T, T::BM) * cdiv(a.I, T::BN / 2);
     const int grid = T::KS > 1 ? (int)cdiv(tiles, 8) * 8 : gemm_grid(tiles, T::MOST);
-    if constexpr (BACK && T::BM == 64) {   // (the tiles of few rows)
+    if constexpr (BACK && T::BM <= 64) {   // (the tiles of few rows)
       if (a.T <= kTwoParts) {
         hipLaunchKernelGGL((k_ffn<T, true, true>), dim3(grid), dim3(T::THREADS), 0, s, a);
         return hipGetLastError();
@@ -331,7 +331,8 @@ hipError_t ffn(const FfnArgs &a, hipStream_t s) {
     case 192: return go(TileTag<GemmTile<3, 8, 4, 2, false, false, 4>>());
     case 128: return go(TileTag<GemmTile<4, 4, 2, 2, false, false, 2>>());
     case 64: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2>>());
-    default: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2, false, 4>>());
+    case 16: return go(TileTag<GemmTile<2, 4, 2, 1, false, false, 2, false, 4>>());
+    default: return go(TileTag<GemmTile<1, 2, 2, 1, false, false, 1, false, 8>>());
   }
 }
 

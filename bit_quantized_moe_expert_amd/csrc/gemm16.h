@@ -482,9 +482,11 @@ inline double gemm_rounds(int64_t tiles, int slots, double full, double least) {
   const int64_t whole = tiles / slots, rest = tiles % slots;
   return whole * full + (rest ? least + (full - least) * rest / slots : 0.0);
 }
-// The tile for that: 256, 192 (by 256 columns), 128 or 64, or 16 for small products (64 x 64 with the k shared
-// by groups of waves). tiles(of, BM, BN): how many there are.
+// The tile for that: 256, 192 (by 256 columns), 128 or 64, or for small products, whose time is their steps'
+// latency, 64 x 64 with the k shared by four groups of waves (16) or 32 x 32 with eight (8), where a CU each has
+// a tile: for 2048 k 72 tiles of 16 12.0 us, the same in 240 tiles of 8 9.3. tiles(of, BM, BN): how many there are.
 inline int gemm_class(int64_t (*tiles)(const void *, int, int), const void *of, int64_t steps) {
+  if (tiles(of, 32, 32) <= 256 && steps >= 16) return 8;
   if (tiles(of, 64, 64) <= 256 && steps >= 8) return 16;
   const double l = gemm_rounds(tiles(of, 256, 256), 256, 1.0, 0.85), k = gemm_rounds(tiles(of, 192, 256), 256, 0.78, 0.66),
                m = gemm_rounds(tiles(of, 128, 128), 512, 0.68, 0.42), q = gemm_rounds(tiles(of, 64, 64), 1024, 0.52, 0.35);

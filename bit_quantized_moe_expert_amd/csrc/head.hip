@@ -518,7 +518,8 @@ void by_head_tile(int64_t T, int64_t V, int H, F &&f) {
     case 192: return f(TileTag<GemmTile<3, 8, 4, 2>>());
     case 128: return f(TileTag<GemmTile<4, 4, 2, 2>>());
     case 64: return f(TileTag<GemmTile<2, 2, 2, 2>>());
-    default: return f(TileTag<GemmTile<2, 2, 2, 2, false, false, 0, false, 4>>());
+    case 16: return f(TileTag<GemmTile<2, 2, 2, 2, false, false, 0, false, 4>>());
+    default: return f(TileTag<GemmTile<1, 2, 2, 1, false, false, 0, false, 8>>());
   }
 }
 template <class T>
@@ -578,7 +579,7 @@ hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s) {
   by_head_tile(a.T, a.vn, a.H, [&](auto tile) {
     using T = typename decltype(tile)::type;
     const dim3 grid = head_grid<T>(a.T, a.vn);
-    if constexpr (T::BM == 64) {   // (the tiles of few rows)
+    if constexpr (T::BM <= 64) {   // (the tiles of few rows)
       if (a.T <= kTwoParts) {
         if (a.k) hipLaunchKernelGGL((k_head_piece<T, true, true>), grid, dim3(T::THREADS), 0, s, a);
         else hipLaunchKernelGGL((k_head_piece<T, false, true>), grid, dim3(T::THREADS), 0, s, a);
