@@ -48,7 +48,6 @@ hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s);
 hipError_t launch_ffn_dgu(const FfnArgs &a, hipStream_t s);
 
 constexpr int kMaxTeacher = 1024;
-constexpr int kHeadFewRows = 32;   // up to so many rows the head's forward has a form of its own
 // The vocabulary head: logits x W^T, by k_head_* kernels that never store them.
 struct HeadArgs {
   int64_t T, V;

@@ -408,7 +408,7 @@ struct FewRows {
 #pragma unroll
       for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const int pieces = K / 8, steps = (pieces + 3) / 4, first = steps * wave / W, last = steps * (wave + 1) / W;
-    constexpr int U = NB >= 4 ? 2 : 8;   // steps in flight (four for NB = 4 cost workgroups a CU)
+    constexpr int U = 8;   // steps in flight
     for (int s0 = first; s0 < last; s0 += U) {
       uint4 ry[U][NB], rx[U][MB];
 #pragma unroll
@@ -443,6 +443,51 @@ struct FewRows {
       for (int w = 0; w < W; ++w) sum += red[(w * BLOCKS + wave) * 64 + lane];
     }
     return sum;
+  }
+};
+
+// A few rows of x (16 MB, at most 32) against 64 rows of y, many of them: a stream of y's steps of 64 k through a
+// ring of STAGES places in LDS, all but two of them on their way; a wave has 16 rows of y. 17 rows against 32003 of
+// 2048 k, statistics and loss with them: 31.8 us with six places (two workgroups a CU), 34.2 with four (three),
+// 35.3 with eight (one), and 38.4 with loads to registers as in FewRows, whose next ones wait for their sums.
+template <int MB_, int STAGES_>
+struct FewStream {
+  static constexpr int MB = MB_, STAGES = STAGES_, THREADS = 256;
+  using X = GemmSide<32, THREADS, false>;
+  using Y = GemmSide<64, THREADS, false>;
+  static constexpr int STAGE = X::BYTES + Y::BYTES, LDS = STAGES * STAGE, P = X::PER + Y::PER;
+  // acc as GemmTile's: rows 16 wave .. of y, 16 m .. of x. The workgroup's LDS is free after it.
+  __device__ __attribute__((always_inline)) static void run(char *lds, int K, X &x, Y &y, f32x4_t (&acc)[MB]) {
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+    const int steps = (K + kGemmBK - 1) / kGemmBK, wave = X::wave();
+    auto load = [&](int step, int stage) __attribute__((always_inline)) {
+      const int left = K - step * kGemmBK;   // (none past the end: zeros)
+      const uint32_t to = lds0 + (uint32_t)stage * STAGE;
+#pragma unroll
+      for (int i = 0; i < Y::PER; ++i) y.template load<false, 0>(i, step, left, 0, to + X::BYTES);
+#pragma unroll
+      for (int i = 0; i < X::PER; ++i) x.template load<false, 0>(i, step, left, 0, to);
+    };
+#pragma unroll
+    for (int m = 0; m < MB; ++m) acc[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) load(s, s);
+    int at = 0;
+    for (int s = 0; s < steps; ++s) {
+      wait_loads<P *(STAGES - 2)>();
+      lds_barrier();   // step s has landed, and step s - 1's place has been read
+      load(s + STAGES - 1, at == 0 ? STAGES - 1 : at - 1);
+      const char *from = lds + at * STAGE;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const bf16x8_t fy = Y::frag(from + X::BYTES, wave, kk);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fy, X::frag(from, m, kk), acc[m], 0, 0, 0);
+      }
+      at = at + 1 == STAGES ? 0 : at + 1;
+    }
+    wait_loads<0>();
+    lds_barrier();
   }
 };
 

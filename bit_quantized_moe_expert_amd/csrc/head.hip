@@ -173,22 +173,28 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadAr
   });
 }
 
-// Up to 16 MB rows: a workgroup takes 64 columns, a chunk of statistics.
+// Up to 16 MB rows: a workgroup takes 64 columns, a chunk of statistics, a wave 16 of them.
 template <int MB, bool TEACH>
-__global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
-  using F = FewRows<4, MB, 8>;
+__global__ __launch_bounds__(256) void k_head_few(HeadArgs p) {
+  using F = FewStream<MB, 6>;   // (144 KB for two workgroups a CU)
   __shared__ __attribute__((aligned(16))) char lds[F::LDS];
   const int64_t n0 = (int64_t)blockIdx.x * 64;
   const int T = (int)p.T;
-  f32x4_t v = F::run(
-      lds, p.H, [&](int i) { return p.w + (n0 + i < p.V ? n0 + i : p.V - 1) * p.H; },
-      [&](int i) { return p.x + (int64_t)(i < T ? i : T - 1) * p.H; });
+  typename F::X x;
+  typename F::Y y;
+  x.init(p.x, p.H, 0, p.T);
+  y.init(p.w, p.H, n0, p.V);
+  f32x4_t acc[MB];
+  F::run(lds, p.H, x, y, acc);
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
-  lds_barrier();   // the sums have been read
-  const int64_t c0 = n0 + 16 * (wave / MB), row0 = 16 * (wave % MB), row = row0 + (lane & 15);
+  const int64_t c0 = n0 + 16 * wave;
   const int left = (int)(p.V - c0 < 16 ? p.V - c0 : 16), col = 4 * (lane >> 4);
-  float2 *stats = reinterpret_cast<float2 *>(lds + F::BLOCKS * 1024);   // [4][16 MB]
-  if (wave < F::BLOCKS) {
+  const float scale = kLog2e / p.tau;
+  float2 *stats = reinterpret_cast<float2 *>(lds + 4 * 1024);   // [4][16 MB], behind a kilobyte a wave
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const int64_t row0 = 16 * mb, row = row0 + (lane & 15);
+    f32x4_t v = acc[mb];
     if constexpr (!TEACH) {
       if (row < T) {
         const int64_t want = (int64_t)p.ids[row] - c0 - col;
@@ -205,8 +211,8 @@ __global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
       entries.each(p, lane, row0, 0, [&](int er, int c, int j) {
         p.logits[(row0 + er) * p.k + j] = reinterpret_cast<const float *>(mine + (c >> 2) * 16 + er)[c & 3];
       });
+      wave_lds_order();
     }
-    const float scale = kLog2e / p.tau;
     float m = -__builtin_inff(), s = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -219,14 +225,14 @@ __global__ __launch_bounds__(512) void k_head_few(HeadArgs p) {
     for (int j = 0; j < 4; ++j) s += __builtin_amdgcn_exp2f(v[j] * scale - top);
     join_stats(m, s, __shfl_xor(m, 16, kWave), __shfl_xor(s, 16, kWave));
     join_stats(m, s, __shfl_xor(m, 32, kWave), __shfl_xor(s, 32, kWave));
-    if (lane < 16) stats[wave / MB * 16 * MB + row] = make_float2(m, s);
+    if (lane < 16) stats[wave * 16 * MB + row] = make_float2(m, s);
   }
   lds_barrier();
   const int r = threadIdx.x;
   if (r >= 16 * MB || r >= T) return;
   float2 a = stats[r];
 #pragma unroll
-  for (int n = 1; n < F::NB; ++n) join_stats(a.x, a.y, stats[n * 16 * MB + r].x, stats[n * 16 * MB + r].y);
+  for (int n = 1; n < 4; ++n) join_stats(a.x, a.y, stats[n * 16 * MB + r].x, stats[n * 16 * MB + r].y);
   p.stats[(int64_t)blockIdx.x * p.T + r] = a;
 }
 
@@ -528,10 +534,14 @@ dim3 head_grid(int64_t rows, int64_t cols) {
   return dim3(T::KS > 1 ? (unsigned)cdiv(tiles, 8) * 8 : gemm_grid(tiles, T::MOST));
 }
 
+// The form for few rows, where half of the CUs have columns of it at least: 17 rows, H 4096, stream and tiles in us:
+// V 4000 20.6 and 16.5, 8000 20.7 and 20.7, 12000 21.3 and 27.6, 32003 47.5 and 58.9.
+bool head_few(int64_t T, int64_t V) { return T <= 32 && V > 64 * 128; }
+
 }  // namespace
 
 int64_t head_stat_chunks(int64_t T, int64_t V, int H) {
-  if (T <= kHeadFewRows) return cdiv(V, 64);
+  if (head_few(T, V)) return cdiv(V, 64);
   int64_t n = 0;
   by_head_tile(T, V, H, [&](auto tile) { n = cdiv(V, 16 * decltype(tile)::type::NB); });
   return n;
@@ -546,12 +556,15 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.T <= kHeadFewRows) {
-    const dim3 grid((unsigned)cdiv(a.V, 64)), block(512);
-    if (a.T <= 16 && a.k) hipLaunchKernelGGL((k_head_few<1, true>), grid, block, 0, s, a);
-    else if (a.T <= 16) hipLaunchKernelGGL((k_head_few<1, false>), grid, block, 0, s, a);
-    else if (a.k) hipLaunchKernelGGL((k_head_few<2, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_head_few<2, false>), grid, block, 0, s, a);
+  if (head_few(a.T, a.V)) {
+    const dim3 grid((unsigned)cdiv(a.V, 64)), block(256);
+    const auto go = [&](auto mb) {
+      constexpr int MB = decltype(mb)::value;
+      if (a.k) hipLaunchKernelGGL((k_head_few<MB, true>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((k_head_few<MB, false>), grid, block, 0, s, a);
+    };
+    if (a.T <= 16) go(std::integral_constant<int, 1>());
+    else go(std::integral_constant<int, 2>());
   } else {
     by_head_tile(a.T, a.V, a.H, [&](auto tile) {
       using T = typename decltype(tile)::type;

@@ -154,7 +154,8 @@ def test_clamped_ffn_shows_a_nan(T, inter):
 
 # ------------------------------------------------------------------ losses of a head
 HEAD_SIZES = [(1, 8, 1), (1, 64, 5), (2, 2048, 3001), (17, 2048, 3001), (33, 72, 777), (64, 128, 64), (129, 264, 4099),
-              (300, 128, 20001), (515, 1024, 2003), (4096, 64, 20003), (20000, 32, 5003), (520, 264, 32003), (65, 1024, 301)]
+              (300, 128, 20001), (515, 1024, 2003), (4096, 64, 20003), (20000, 32, 5003), (520, 264, 32003), (65, 1024, 301),
+              (1, 8, 8193), (16, 2048, 8203), (17, 520, 20001), (32, 72, 32003)]
 
 
 def head_case(T, H, V, seed=0, std=2.5):
@@ -219,7 +220,8 @@ def distill_case(T, H, V, k, tdt, seed=0):
 
 @pytest.mark.parametrize("tau,tdt", [(1.0, BF16), (2.5, F32), (0.5, F32)])
 @pytest.mark.parametrize("T,H,V,k", [(1, 8, 1, 1), (1, 64, 50, 3), (17, 256, 3001, 16), (65, 72, 333, 65), (129, 128, 4099, 200),
-                                     (70, 64, 2000, 1024), (600, 520, 20001, 32), (4096, 32, 17003, 7), (520, 264, 32003, 40), (40, 1040, 500, 9), (100, 1024, 700, 9)])
+                                     (70, 64, 2000, 1024), (600, 520, 20001, 32), (4096, 32, 17003, 7), (520, 264, 32003, 40), (40, 1040, 500, 9), (100, 1024, 700, 9),
+                                     (5, 64, 9001, 20), (16, 1032, 8200, 65), (31, 264, 12001, 130)])
 def test_vocab_distill(T, H, V, k, tau, tdt):
     x, w, ids, t, dloss = distill_case(T, H, V, k, tdt)
     el = product_bound(x, w) / tau
