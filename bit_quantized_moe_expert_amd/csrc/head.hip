@@ -10,8 +10,14 @@
 // Backward, by pieces of the vocabulary that the last-level cache can hold: the tile's logits again,
 //   P = dloss (exp(l - lse) - [v is the label])         or dloss tau (softmax - q)
 // rounded to bf16 (half a step of 2^-8 of each value, no more than the gradients' own
-// rounding; P is the operand of two bf16 products), then dx += P W and dW = P^T x.
-// All of it is bound by the matrix cores; a handful of rows by the reading of W.
+// rounding; P is the operand of two bf16 products; up to kTwoParts rows it has two parts, which
+// leave 2^-17), then dx += P W and dW = P^T x.
+// All of it is bound by the matrix cores and their power; a handful of rows by the reading of W.
+//
+// Measured, us, with H 2048, V 50304: 4096 rows forward 640 to 660 (1280 to 1320 TFLOP/s), both gradients
+// 1975 to 2070 (1225 to 1280 of 2532 GFLOP). The head's 17 rows with V 32003 (131 MB): 28 + 4 to join. Distillation,
+// k 64, 2048 rows, H 2880: 500 to 520, of which the teacher's entries 15 and the joining 8; its gradient dx of 515
+// rows, H 1024, V 32003: 111 to 114 for 5 (entries) + 60 (P) + 40 (product) + 9 (its 21 slices).
 //
 // Exponentials are taken in powers of two: z = l log2(e) / tau.
 #include "dense.h"
