@@ -198,8 +198,8 @@ __global__ __launch_bounds__(512) void k_ffn_few(FfnArgs p) {
 template <class T>
 struct ProductPlace : GemmTiles {
   const ProductArgs &p;
-  __device__ ProductPlace(const ProductArgs &a, int b, int nb)
-      : GemmTiles{b, nb, (int)((a.M + T::BM - 1) / T::BM), (int)((a.N + T::BN - 1) / T::BN), a.slices, a.K}, p(a) {}
+  __device__ ProductPlace(const ProductArgs &a, int b, int nb, int log)
+      : GemmTiles{b, nb, (int)((a.M + T::BM - 1) / T::BM), (int)((a.N + T::BN - 1) / T::BN), a.slices, a.K, log}, p(a) {}
   __device__ bool operator()(int r, typename T::X &x, typename T::Y &y, GemmRange &k) const {
     int m, n, slice;
     if (!find(r, m, n, slice)) return false;
@@ -212,8 +212,8 @@ struct ProductPlace : GemmTiles {
 
 // The tiles of workgroup b of nb of a product.
 template <class T>
-__device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &p, char *lds, int b, int nb) {
-  const ProductPlace<T> place(p, b, nb);
+__device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &p, char *lds, int b, int nb, int log = 3) {
+  const ProductPlace<T> place(p, b, nb, log);
   int m, n, slice;
   if (!place.find(0, m, n, slice)) return;
   T t;
@@ -261,12 +261,21 @@ __device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &
 
 // Workgroups 0 .. nbx - 1 take dx's tiles, the others dw's: side by side they fill the card together, where
 // dx by itself has its k in slices to be joined (4096 rows, H 2048, I 8192: dx 240 us alone, dw 231, both 434).
+// nbx < 0, for large products of equal steps: half of the XCDs each, so that an L2 holds the operands
+// of one product (1 to 1.7 % of a whole backward).
 template <class TX, class TW>
 __global__ __launch_bounds__(TX::THREADS, TX::WAVES_SIMD) void k_products(ProductArgs dx, ProductArgs dw, int nbx) {
   static_assert(TX::THREADS == TW::THREADS, "one workgroup size");
   __shared__ __attribute__((aligned(16))) char lds[TX::LDS > TW::LDS ? TX::LDS : TW::LDS];
-  if ((int)blockIdx.x < nbx) product_tiles<TX>(dx, lds, blockIdx.x, nbx);
-  else product_tiles<TW>(dw, lds, (int)blockIdx.x - nbx, (int)gridDim.x - nbx);
+  const int b = blockIdx.x, nb = gridDim.x;
+  if (nbx < 0) {   // half of the XCDs each
+    const int half = (b >> 3) * 4 + (b & 3);
+    if ((b & 7) < 4) product_tiles<TX>(dx, lds, half, nb / 2, 2);
+    else product_tiles<TW>(dw, lds, half, nb / 2, 2);
+    return;
+  }
+  if (b < nbx) product_tiles<TX>(dx, lds, b, nbx);
+  else product_tiles<TW>(dw, lds, b - nbx, nb - nbx);
 }
 
 // Few slices: 8 values a thread at a time, n a multiple of 8.
@@ -369,7 +378,8 @@ hipError_t products(const ProductArgs &dx, const ProductArgs &dw, hipStream_t s)
     if (tx) nbx = gemm_grid(tx, nbx);
     nbw = tw ? gemm_grid(tw, TX::MOST - nbx) : 0;
   }
-  hipLaunchKernelGGL((k_products<TX, TW>), dim3(nbx + nbw), dim3(TX::THREADS), 0, s, dx, dw, nbx);
+  const int split = TX::KS == 1 && nbx == TX::MOST / 2 && nbw == nbx ? -1 : nbx;
+  hipLaunchKernelGGL((k_products<TX, TW>), dim3(nbx + nbw), dim3(TX::THREADS), 0, s, dx, dw, split);
   return hipGetLastError();
 }
 template <int MB, int NB, int WM, int WN, bool MASK, int KS = 1>

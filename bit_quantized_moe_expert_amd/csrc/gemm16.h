@@ -504,9 +504,10 @@ struct FewStream {
 struct GemmTiles {
   int b, nb, mt, nt, slices;
   int64_t K;
+  int log = 3;   // of the XCDs that b counts through
   __device__ bool find(int r, int &m, int &n, int &slice) const {
-    const int each = mt * nt, total = each * slices, per = (total + 7) >> 3, i = (b >> 3) + r * (nb >> 3);
-    const int at = (b & 7) * per + i;
+    const int xcds = 1 << log, each = mt * nt, total = each * slices, per = (total + xcds - 1) >> log, i = (b >> log) + r * (nb >> log);
+    const int at = (b & (xcds - 1)) * per + i;
     if (i >= per || at >= total) return false;
     slice = at / each;
     const int in = at - slice * each, band = in / (4 * nt), rest = in - band * 4 * nt;

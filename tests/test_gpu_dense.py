@@ -155,7 +155,8 @@ def test_clamped_ffn_shows_a_nan(T, inter):
 # ------------------------------------------------------------------ losses of a head
 HEAD_SIZES = [(1, 8, 1), (1, 64, 5), (2, 2048, 3001), (17, 2048, 3001), (33, 72, 777), (64, 128, 64), (129, 264, 4099),
               (300, 128, 20001), (515, 1024, 2003), (4096, 64, 20003), (20000, 32, 5003), (520, 264, 32003), (65, 1024, 301),
-              (1, 8, 8193), (16, 2048, 8203), (17, 520, 20001), (32, 72, 32003)]
+              (1, 8, 8193), (16, 2048, 8203), (17, 520, 20001), (32, 72, 32003),
+              (2048, 1024, 20001)]
 
 
 def head_case(T, H, V, seed=0, std=2.5):
