@@ -16,7 +16,7 @@
 //
 // Measured, us, with H 2048, V 50304: 4096 rows forward 640 to 660 (1280 to 1320 TFLOP/s), both gradients
 // 1975 to 2070 (1225 to 1280 of 2532 GFLOP). The head's 17 rows with V 32003 (131 MB): 28 + 4 to join. Distillation,
-// k 64, 2048 rows, H 2880: 500 to 520, of which the teacher's entries 15 and the joining 8; its gradient dx of 515
+// k 64, 2048 rows, H 2880: 495 to 515, of which the teacher's entries 12 and the joining 6; its gradient dx of 515
 // rows, H 1024, V 32003: 111 to 114 for 5 (entries) + 60 (P) + 40 (product) + 9 (its 21 slices).
 //
 // Exponentials are taken in powers of two: z = l log2(e) / tau.
@@ -242,11 +242,12 @@ __global__ __launch_bounds__(256) void k_head_few(HeadArgs p) {
   p.stats[(int64_t)blockIdx.x * p.T + r] = a;
 }
 
-// R rows a workgroup, 256 / R threads each: the chunks' pairs to lse, and the loss.
-template <int R>
-__global__ __launch_bounds__(256) void k_head_join(HeadArgs p, int chunks) {
-  constexpr int PARTS = 256 / R, IN_WAVE = 64 / R;   // threads of a row, and those of them in a wave
-  __shared__ float2 red[2][4][R];
+// R rows a workgroup of W waves, 64 W / R threads each: the chunks' pairs to lse, and the loss.
+template <int R, int W>
+__global__ __launch_bounds__(64 * W) void k_head_join(HeadArgs p, int chunks) {
+  constexpr int PARTS = 64 * W / R;   // threads of a row
+  static_assert(R <= 64, "rows of a wave");
+  __shared__ float2 red[2][W][R];
   const int r = threadIdx.x % R, part = threadIdx.x / R, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t row = (int64_t)blockIdx.x * R + r;
   const bool live = row < p.T;
@@ -264,9 +265,8 @@ __global__ __launch_bounds__(256) void k_head_join(HeadArgs p, int chunks) {
   lds_barrier();
   m = red[0][0][r].x, s = red[0][0][r].y;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) join_stats(m, s, red[0][w][r].x, red[0][w][r].y);
+  for (int w = 1; w < W; ++w) join_stats(m, s, red[0][w][r].x, red[0][w][r].y);
   const float lse = (m + log2f(s)) * kLn2;
-  static_assert(IN_WAVE >= 1, "rows of a wave");
   if (p.k == 0) {
     if (part == 0 && live) {
       const int32_t id = p.ids[row];
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(256) void k_head_join(HeadArgs p, int chunks) {
   if (lane < R) red[1][wave][r] = make_float2(sum, any);
   lds_barrier();
   if (part == 0 && live) {
-    for (int w = 1; w < 4; ++w) sum += red[1][w][r].x, any += red[1][w][r].y;
+    for (int w = 1; w < W; ++w) sum += red[1][w][r].x, any += red[1][w][r].y;
     p.loss[row] = any != 0.0f ? p.tau * p.tau * sum : 0.0f;
     p.lse[row] = any != 0.0f ? lse : __builtin_inff();
   }
@@ -303,11 +303,21 @@ __device__ inline bool row_on(const HeadArgs &p, int64_t row) {
   return id >= 0 && id < p.V;
 }
 
-// q [k] of a row from the teacher's logits, by a wave with `val` and `ids` [k] of its own in LDS.
-// Entries outside the vocabulary count for nothing, an id's later occurrences add to its first; a
-// row without an entry above -inf has all zeros. Also zeros the logits of entries outside.
-__device__ inline void teacher_row(const HeadArgs &p, int64_t row, int lane, float *val, int32_t *ids) {
+// Places of a row's table of ids: a power of two, half of them free.
+__host__ __device__ inline int table_size(int k) {
+  int n = 64;
+  while (n < 2 * k) n *= 2;
+  return n;
+}
+// q [k] of a row from the teacher's logits, by a wave with `val` and `ids` [k] and `table` [table_size(k)]
+// of its own in LDS. Entries outside the vocabulary count for nothing, an id's later occurrences add to
+// its first; a row without an entry above -inf has all zeros. Also zeros the logits of entries outside
+// and leaves their ids as -1. An id that occurs twice is noticed by a table of ids with open places (which of
+// its entries is the place's is open, whether there are two is not), and only for it the wave goes through all.
+__device__ inline void teacher_row(const HeadArgs &p, int64_t row, int lane, float *val, int32_t *ids, uint32_t *table) {
+  constexpr uint32_t kTwice = 0x80000000u;
   const int64_t base = row * p.k;
+  const int places = table_size(p.k), shift = __clz(places) + 1;   // of a 32-bit hash
   float m = -__builtin_inff();
   bool nan = false;
   for (int j = lane; j < p.k; j += 64) {
@@ -322,6 +332,7 @@ __device__ inline void teacher_row(const HeadArgs &p, int64_t row, int lane, flo
     nan |= t != t;
     m = fmaxf(m, t);
   }
+  for (int i = lane; i < places; i += 64) table[i] = 0;
   m = wave_max(m);
   nan = __any(nan);
   float sum = 0.0f;
@@ -332,49 +343,88 @@ __device__ inline void teacher_row(const HeadArgs &p, int64_t row, int lane, flo
   }
   sum = wave_sum(sum);
   wave_lds_order();
+  auto hash = [&](int32_t id) { return (int)((uint32_t)id * 2654435769u >> shift); };
   for (int j = lane; j < p.k; j += 64) {
     const int32_t id = ids[j];
-    float e = 0.0f;
-    bool first = id >= 0;
-    if (first) {
-      for (int i = 0; i < p.k; ++i) {
-        if (ids[i] != id) continue;
-        if (i < j) first = false;
-        e += val[i];
+    if (id < 0) continue;
+    for (int at = hash(id);; at = (at + 1) & (places - 1)) {
+      const uint32_t was = atomicCAS(&table[at], 0u, (uint32_t)j + 1);
+      if (was == 0) break;
+      if (ids[(was & ~kTwice) - 1] == id) {
+        atomicOr(&table[at], kTwice);
+        break;
       }
     }
-    p.q[base + j] = nan && id >= 0 ? __builtin_nanf("") : first && m != -__builtin_inff() ? e / sum : 0.0f;
+  }
+  wave_lds_order();
+  for (int j0 = 0; j0 < p.k; j0 += 64) {
+    const int j = j0 + lane;
+    const int32_t id = j < p.k ? ids[j] : -1;
+    bool twice = false, mine = false;   // its place is shared; it is this entry's
+    if (id >= 0) {
+      int at = hash(id);
+      while (ids[(table[at] & ~kTwice) - 1] != id) at = (at + 1) & (places - 1);   // it is there
+      twice = table[at] & kTwice, mine = (table[at] & ~kTwice) == (uint32_t)j + 1;
+    }
+    const bool none = id < 0 || m == -__builtin_inff();
+    if (j < p.k && (nan || !twice || none)) p.q[base + j] = nan && id >= 0 ? __builtin_nanf("") : none ? 0.0f : val[j] / sum;
+    for (uint64_t of = __ballot(twice && mine && !nan && !none); of; of &= of - 1) {   // the wave, an id at a time
+      const int32_t want = __shfl(id, __builtin_ctzll(of), kWave);
+      float e = 0.0f;
+      int first = p.k;
+      for (int i = lane; i < p.k; i += 64)
+        if (ids[i] == want) e += val[i], first = first < i ? first : i;
+      e = wave_sum(e);
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int other = __shfl_xor(first, d, kWave);
+        first = first < other ? first : other;
+      }
+      for (int i = lane; i < p.k; i += 64)
+        if (ids[i] == want) p.q[base + i] = i == first ? e / sum : 0.0f;
+    }
   }
   wave_lds_order();
 }
 
-// A workgroup 16 rows: the teacher's probabilities (forward), and the rows' entries by chunk of
-// kHeadChunk columns (counts, a scan, places). BACK: those with a probability; else those with an id in
-// the vocabulary. Within a chunk their order is open: each writes to a place of its own.
+// A workgroup 16 rows, a wave one of them: the teacher's probabilities (forward), and the rows' entries by
+// chunk of kHeadChunk columns (counts, a scan, places). BACK: those with a probability; else those with an
+// id in the vocabulary. Within a chunk their order is open: each writes to a place of its own.
+// 2048 rows of 64 entries 12 us (every id against every other: 15), 17 of 512 37 (405), of 1024 140 (2100).
 constexpr int kEntryThreads = 1024;
-// Rows whose ids and values are in LDS at a time, beside the counts of 2^21 / kHeadChunk chunks.
-__host__ __device__ inline int entry_rows(int k) { return k <= 512 ? 16 : 8; }
+// LDS words of a row: ids, and for the forward values and the table.
+__host__ __device__ inline int entry_words(int k, bool back) { return back ? k : 2 * k + table_size(k); }
+// Rows that are in LDS at a time, beside the counts of 2^21 / kHeadChunk chunks at the most.
+inline int entry_rows(int k, int64_t chunks, bool back) {
+  int rows = 16;
+  while (4 * (chunks + (int64_t)rows * entry_words(k, back)) > (159 << 10)) rows /= 2;
+  return rows;
+}
 template <bool BACK>
-__global__ __launch_bounds__(kEntryThreads) void k_head_entries(HeadArgs p) {
-  extern __shared__ int32_t shared[];   // [chunks], and for the forward [entry_rows][k] ids and values
+__global__ __launch_bounds__(kEntryThreads) void k_head_entries(HeadArgs p, int rows) {
+  extern __shared__ int32_t shared[];   // [chunks], [rows][entry_words]
   __shared__ int32_t total[kEntryThreads / 64];
-  const int t = threadIdx.x, chunks = (int)((p.V + kHeadChunk - 1) / kHeadChunk), each = (chunks + kEntryThreads - 1) / kEntryThreads;
-  int32_t *count = shared;
-  const int64_t row0 = (int64_t)blockIdx.x * 16, n = (p.T - row0 < 16 ? p.T - row0 : 16) * p.k, base = row0 * p.k;
+  const int t = threadIdx.x, w = t >> 6, lane = t & 63;
+  const int chunks = (int)((p.V + kHeadChunk - 1) / kHeadChunk), each = (chunks + kEntryThreads - 1) / kEntryThreads;
+  int32_t *count = shared, *ids = shared + chunks + w * entry_words(p.k, BACK);
+  const int64_t row0 = (int64_t)blockIdx.x * 16, row = row0 + w, base = row * p.k;
   if constexpr (!BACK) {
-    const int w = t >> 6, rows = entry_rows(p.k);
-    int32_t *ids = shared + chunks + 2 * w * p.k;
-    for (int64_t row = row0 + w; w < rows && row < row0 + 16 && row < p.T; row += rows)
-      teacher_row(p, row, t & 63, reinterpret_cast<float *>(ids + p.k), ids);
+    if (w < rows)
+      for (int64_t r = row; r < row0 + 16 && r < p.T; r += rows)
+        teacher_row(p, r, lane, reinterpret_cast<float *>(ids + p.k), ids, reinterpret_cast<uint32_t *>(ids + 2 * p.k));
   }
   for (int i = t; i < chunks; i += kEntryThreads) count[i] = 0;
   lds_barrier();
-  auto id_of = [&](int64_t e) {
-    const int32_t id = p.ids[base + e];
-    return id < 0 || id >= p.V || (BACK && p.q[base + e] == 0.0f) ? -1 : id;
+  const int n = row < p.T ? p.k : 0;
+  const bool held = !BACK && rows == 16;   // the wave's row is in its LDS
+  auto id_of = [&](int j) {
+    if (held) return (int)ids[j];
+    const int32_t id = p.ids[base + j];
+    return id < 0 || id >= p.V || (BACK && p.q[base + j] == 0.0f) ? -1 : (int)id;
   };
-  for (int64_t e = t; e < n; e += kEntryThreads) {
-    const int32_t id = id_of(e);
+  for (int j = lane; j < n; j += 64) {
+    const int id = id_of(j);
+    if (BACK) ids[j] = id;
     if (id >= 0) atomicAdd(&count[id / kHeadChunk], 1);
   }
   lds_barrier();
@@ -384,11 +434,11 @@ __global__ __launch_bounds__(kEntryThreads) void k_head_entries(HeadArgs p) {
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const int v = __shfl_up(upto, d, kWave);
-    upto += (t & 63) >= d ? v : 0;
+    upto += lane >= d ? v : 0;
   }
-  if ((t & 63) == 63) total[t >> 6] = upto;
+  if (lane == 63) total[w] = upto;
   lds_barrier();
-  for (int w = 0; w < t >> 6; ++w) upto += total[w];
+  for (int i = 0; i < w; ++i) upto += total[i];
   int at = upto - sum;
   int32_t *off = p.offsets + (int64_t)blockIdx.x * (chunks + 1);
   for (int i = t * each; i < (t + 1) * each && i < chunks; ++i) {
@@ -398,11 +448,10 @@ __global__ __launch_bounds__(kEntryThreads) void k_head_entries(HeadArgs p) {
   }
   if (t == kEntryThreads - 1) off[chunks] = upto;
   lds_barrier();
-  for (int64_t e = t; e < n; e += kEntryThreads) {
-    const int32_t id = id_of(e);
-    if (id < 0) continue;
-    const int row = (int)(e / p.k), j = (int)(e - (int64_t)row * p.k);
-    p.list[base + atomicAdd(&count[id / kHeadChunk], 1)] = (uint32_t)j << 11 | (uint32_t)row << 7 | (uint32_t)(id % kHeadChunk);
+  uint32_t *list = p.list + row0 * p.k;
+  for (int j = lane; j < n; j += 64) {
+    const int id = BACK ? (int)ids[j] : id_of(j);
+    if (id >= 0) list[atomicAdd(&count[id / kHeadChunk], 1)] = (uint32_t)j << 11 | (uint32_t)w << 7 | (uint32_t)(id % kHeadChunk);
   }
 }
 
@@ -512,6 +561,15 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
   });
 }
 
+template <bool BACK>
+hipError_t launch_entries(const HeadArgs &a, hipStream_t s) {
+  const int64_t chunks = cdiv(a.V, kHeadChunk);
+  const int rows = entry_rows(a.k, chunks, BACK);
+  hipLaunchKernelGGL(k_head_entries<BACK>, dim3((unsigned)cdiv(a.T, 16)), dim3(kEntryThreads),
+                     4 * (chunks + (int64_t)rows * entry_words(a.k, BACK)), s, a, rows);
+  return hipGetLastError();
+}
+
 struct HeadSize {
   int64_t T, V;
 };
@@ -557,9 +615,7 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
   HeadArgs a = args;
   a.v0 = 0, a.vn = a.V;
   if (a.k) {
-    hipLaunchKernelGGL(k_head_entries<false>, dim3((unsigned)cdiv(a.T, 16)), dim3(kEntryThreads),
-                       4 * cdiv(a.V, kHeadChunk) + 8 * entry_rows(a.k) * a.k, s, a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_entries<false>(a, s);
     if (e != hipSuccess) return e;
   }
   if (head_few(a.T, a.V)) {
@@ -582,16 +638,16 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int chunks = (int)head_stat_chunks(a.T, a.V, a.H);
-  // enough workgroups whatever T: a row a workgroup, four or 16
-  if (a.T <= 256) hipLaunchKernelGGL(k_head_join<1>, dim3((unsigned)a.T), dim3(256), 0, s, a, chunks);
-  else if (a.T <= 2048) hipLaunchKernelGGL(k_head_join<4>, dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a, chunks);
-  else hipLaunchKernelGGL(k_head_join<16>, dim3((unsigned)cdiv(a.T, 16)), dim3(256), 0, s, a, chunks);
+  // enough workgroups whatever T, and 64 or 128 bytes of a chunk's pairs each where there are rows for it (2048 rows,
+  // V 50304: eight rows 5.0 us, four 6.6; 4096: 7.7, and 16 rows 4.9)
+  if (a.T <= 256) hipLaunchKernelGGL((k_head_join<1, 4>), dim3((unsigned)a.T), dim3(256), 0, s, a, chunks);
+  else if (a.T <= 2048) hipLaunchKernelGGL((k_head_join<8, 16>), dim3((unsigned)cdiv(a.T, 8)), dim3(1024), 0, s, a, chunks);
+  else hipLaunchKernelGGL((k_head_join<16, 4>), dim3((unsigned)cdiv(a.T, 16)), dim3(256), 0, s, a, chunks);
   return hipGetLastError();
 }
 
 hipError_t launch_head_entries(const HeadArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(k_head_entries<true>, dim3((unsigned)cdiv(a.T, 16)), dim3(kEntryThreads), 4 * cdiv(a.V, kHeadChunk), s, a);
-  return hipGetLastError();
+  return launch_entries<true>(a, s);
 }
 
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s) {

@@ -281,6 +281,29 @@ def test_distill_over_the_largest_vocabulary():
     assert R.off(out["dx"], P @ w.double()) < 2 * B     # 144 values: two roundings, each at most b of its sum's terms
 
 
+@pytest.mark.parametrize("k", [2, 64, 65, 300, 1024])
+def test_distill_of_ids_that_a_row_names_often(k):
+    """One id everywhere, two ids in turn, each id twice, ids that differ by a power of two, an id with a stranger."""
+    H, V = 64, 70001
+    rn = gen(9)
+    x, w, t = rn(5, H, dt=BF16), rn(V, H, std=0.3, dt=BF16), rn(5, k)
+    j = torch.arange(k, device=DEV)
+    ids = torch.stack([0 * j + 7, 3 + j % 2 * (V - 4), j // 2 * 65, (j * 4096) % 65536, torch.where(j == k - 1, -1, 69000)]).to(I32)
+    loss, lse, q, logits = R.distill(x, w, ids, t, 1.0)
+    got = M.vocab_distill_forward(x, w, ids, t)
+    tt = t.double().abs().amax(1)[:, None]
+    R.within(got["q"], q, q * (8 * tt + 2 * k + 16) * U + 2.0 ** -120, "q")
+    assert (got["q"][0, 0] - 1).abs() < 4 * k * U and not got["q"][0, 1:].any() and got["q"][4, k - 1] == 0
+    el = product_bound(x, w)
+    R.within(got["logits"], logits, torch.where(ids >= 0, el.gather(1, ids.clamp(min=0).long()), 0.0) + U * logits.abs(), "logits")
+    again = M.vocab_distill_forward(x, w, ids, t)
+    assert all(torch.equal(got[n], again[n]) for n in got)
+    dloss = torch.ones(5, device=DEV)
+    P = R.distill_P(dloss, x, w, ids, got["q"], torch.isfinite(lse), 1.0)
+    out = M.vocab_distill_backward(dloss, x, w, ids, got["q"], got["logits"], got["lse"])
+    near(out["dx"], P @ w.double(), 2, "dx"), near(out["dw"], P.T @ x.double(), 2, "dw")
+
+
 def test_distill_of_one_sure_entry_is_cross_entropy():
     """One entry a row: q is 1, the loss and the gradients are the cross entropy's."""
     x, w, labels, dloss = head_case(140, 128, 2111)
