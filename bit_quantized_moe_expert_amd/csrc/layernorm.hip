@@ -23,7 +23,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_ln_forward(LayerNormA
   __shared__ float red[2][THREADS / 64];
   const int t = threadIdx.x % TPR, H = p.H;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
-  const bool live = row < p.T;   // rows past the end (TPR = 64) read row 0 and store nothing
+  const bool live = row < p.T;   // rows past the end read row 0 and store nothing
   const int64_t base = (live ? row : 0) * H;
   Raw8<XBF> raw[NC] = {};
 #pragma unroll
@@ -81,7 +81,8 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_ln_backward(LayerNormArgs
   constexpr int THREADS = back_threads(TPR), SLOTS = THREADS / TPR;
   __shared__ float red[2][2 * THREADS / 64];   // in turn for even and odd rounds
   extern __shared__ float slot_sum[];          // [2][H] (SLOTS > 1, H <= 2048: at most 16 KB)
-  const int t = threadIdx.x % TPR, slot = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR), H = p.H;
+  const int t = threadIdx.x % TPR, H = p.H;
+  const int slot = TPR >= 64 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR) : (int)threadIdx.x / TPR;
   const float invH = 1.0f / (float)H;
   float w[NC][8];
 #pragma unroll
@@ -146,7 +147,17 @@ __global__ __launch_bounds__(back_threads(TPR)) void k_ln_backward(LayerNormArgs
   }
   if (!p.dw && !p.db) return;   // the whole grid
   float *out = p.partial + (int64_t)blockIdx.x * 2 * H;
-  for (int s = 0; s < SLOTS; ++s) {
+  // the slots of a wave by exchanges, then the waves (or wider slots) in order
+  constexpr int IN_WAVE = TPR < 64 ? 64 / TPR : 1;
+  if constexpr (IN_WAVE > 1) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int d = TPR; d < 64; d *= 2) sw[c][j] += __shfl_xor(sw[c][j], d, kWave), sb[c][j] += __shfl_xor(sb[c][j], d, kWave);
+  }
+  for (int s = 0; s < SLOTS; s += IN_WAVE) {
     if (slot == s) {
       float *dst = SLOTS == 1 ? out : slot_sum;
 #pragma unroll
@@ -185,18 +196,31 @@ __global__ __launch_bounds__(1024) void k_ln_colsum(LayerNormArgs p) {
   out[col] = s;
 }
 
-int ln_tpr(int H) { return H <= 512 ? 64 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024; }
+// The fewest threads that a row fits, 8 values each (2^20 rows of 64 by 64 threads each: 308 us, by 8 62).
+int ln_tpr(int H) {
+  int n = 8;
+  while (n < 1024 && 8 * n < H) n *= 2;
+  return n;
+}
 int ln_slots(int H) { return back_threads(ln_tpr(H)) / ln_tpr(H); }
 
 // f(TPR, NC) as integral constants, by the width of a row.
 template <class F>
 void by_width(int H, F &&f) {
   using std::integral_constant;
-  if (H <= 512) f(integral_constant<int, 64>(), integral_constant<int, 1>());
-  else if (H <= 2048) f(integral_constant<int, 256>(), integral_constant<int, 1>());
-  else if (H <= 4096) f(integral_constant<int, 512>(), integral_constant<int, 1>());
-  else if (H <= 8192) f(integral_constant<int, 1024>(), integral_constant<int, 1>());
-  else f(integral_constant<int, 1024>(), integral_constant<int, 2>());
+  const integral_constant<int, 1> one;
+  switch (ln_tpr(H)) {
+    case 8: return f(integral_constant<int, 8>(), one);
+    case 16: return f(integral_constant<int, 16>(), one);
+    case 32: return f(integral_constant<int, 32>(), one);
+    case 64: return f(integral_constant<int, 64>(), one);
+    case 128: return f(integral_constant<int, 128>(), one);
+    case 256: return f(integral_constant<int, 256>(), one);
+    case 512: return f(integral_constant<int, 512>(), one);
+    default:
+      if (H <= 8192) return f(integral_constant<int, 1024>(), one);
+      return f(integral_constant<int, 1024>(), integral_constant<int, 2>());
+  }
 }
 // f(XBF, YBF, ODD)
 template <class F>

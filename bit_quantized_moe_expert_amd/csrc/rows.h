@@ -106,7 +106,14 @@ __device__ inline void store_row8(void *p, int64_t base, int i, int H, const flo
 template <int TPR, int NV>
 __device__ inline void row_sum(float (&v)[NV], float *red) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) v[k] = wave_sum(v[k]);
+  for (int k = 0; k < NV; ++k) {
+    if constexpr (TPR >= 64) {
+      v[k] = wave_sum(v[k]);
+    } else {   // several rows a wave
+#pragma unroll
+      for (int d = 1; d < TPR; d *= 2) v[k] += __shfl_xor(v[k], d, kWave);
+    }
+  }
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     const int wave = threadIdx.x >> 6;
