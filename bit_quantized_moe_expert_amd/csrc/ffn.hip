@@ -13,7 +13,7 @@
 // library 198), of 4099, H = I = 2880 108 to 114 (1190 to 1260, the ragged tiles' part of it 10 %); backward of
 // the first 645 to 683 (1210 to 1280 of 825 GFLOP). All of these are bound by the matrix cores and their
 // power. One row, H 2048, I 1024: 5.2, of which the 8.4 MB of weights would take 1.6: a launch's
-// latency and memory's. 131 rows, H 2048, I 768, backward: 24.4 for 10 (gate, up, dgu) + 13
+// latency and memory's; 32 rows, H 4096, I 14336 45 for 235 MB (5.2 TB/s). 131 rows, H 2048, I 768, backward: 24.4 for 10 (gate, up, dgu) + 13
 // (products) + 4 (dx's slices joined), the latencies of three dependent launches.
 #include "dense.h"
 #include "gemm16.h"
@@ -173,10 +173,9 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
   });
 }
 
-// Up to 16 MB tokens: a workgroup takes eight gate rows and their up rows.
-template <int MB>
+// Up to 16 tokens: a workgroup takes eight gate rows and their up rows.
 __global__ __launch_bounds__(512) void k_ffn_few(FfnArgs p) {
-  using F = FewRows<1, MB, 8>;
+  using F = FewRows<8>;
   __shared__ __attribute__((aligned(16))) char lds[F::LDS];
   const int c0 = (int)blockIdx.x * 8, T = (int)p.T;
   f32x4_t v = F::run(
@@ -186,13 +185,42 @@ __global__ __launch_bounds__(512) void k_ffn_few(FfnArgs p) {
         return p.w13 + (p.inter ? 2 * c + (i >> 3) : c + (i >> 3) * (int64_t)p.I) * p.H;
       },
       [&](int i) { return p.x + (int64_t)(i < T ? i : T - 1) * p.H; });
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, token = 16 * wave + (lane & 15);
-  if (wave >= MB) return;
+  const int lane = threadIdx.x & 63, token = lane & 15;
+  if (threadIdx.x >= 64) return;
   float h[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) h[j] = glu_of(p.glu, p.alpha, p.limit, v[j], __shfl_xor(v[j], 32, kWave));   // (lanes 0 .. 31: the gate rows)
   if (lane < 32 && token < T)
     *reinterpret_cast<uint2 *>(p.h + (int64_t)token * p.I + c0 + 4 * (lane >> 4)) = pack4(h[0], h[1], h[2], h[3]);
+}
+
+// Up to 32 tokens, many columns: a workgroup takes 32 gate rows and their up rows, a wave 16 of each for 16 tokens.
+__global__ __launch_bounds__(256) void k_ffn_stream(FfnArgs p) {
+  using F = FewStream<6, 2>;   // (144 KB for two workgroups a CU)
+  __shared__ __attribute__((aligned(16))) char lds[F::LDS];
+  const int64_t c0 = (int64_t)blockIdx.x * 32;
+  typename F::X x;
+  typename F::Y y;
+  x.init(p.x, p.H, 0, p.T);
+  y.template init_pair<2>(p.w13, p.w13 + (p.inter ? 1 : (int64_t)p.I) * p.H, (p.inter ? 2 : 1) * (int64_t)p.H, c0, p.I);
+  const int wave = F::X::wave(), lane = threadIdx.x & 63, nb = wave & 1, mb = wave >> 1;
+  f32x4_t g = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, u = g;
+  const bool mine = 16 * mb < p.T;   // the wave
+  F::run(lds, p.H, x, y, [&](const char *xs, const char *ys) __attribute__((always_inline)) {
+    if (!mine) return;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const bf16x8_t fx = F::X::frag(xs, mb, kk);
+      g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(F::Y::frag(ys, nb, kk), fx, g, 0, 0, 0);
+      u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(F::Y::frag(ys, nb + 2, kk), fx, u, 0, 0, 0);
+    }
+  });
+  const int64_t token = 16 * mb + (lane & 15), col = c0 + 16 * nb + 4 * (lane >> 4);
+  if (token >= p.T || col >= p.I) return;
+  float h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = glu_of(p.glu, p.alpha, p.limit, g[j], u[j]);
+  *reinterpret_cast<uint2 *>(p.h + token * p.I + col) = pack4(h[0], h[1], h[2], h[3]);
 }
 
 template <class T>
@@ -402,10 +430,16 @@ hipError_t products(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s) {
-  if (a.T > 32) return ffn<false>(a, s);
-  // (the widest I is 2^20: 2^17 workgroups of 512)
-  if (a.T > 16) hipLaunchKernelGGL(k_ffn_few<2>, dim3((unsigned)(a.I / 8)), dim3(512), 0, s, a);
-  else hipLaunchKernelGGL(k_ffn_few<1>, dim3((unsigned)(a.I / 8)), dim3(512), 0, s, a);
+  // Few rows, in us by tokens, H, I, as few / tiles / stream: 16 2048 1024 7.1 / 8.0 / 10.0; 16 2048 4096 9.9 / 10.4 /
+  // 10.2; 1 2048 14336 23.5 / 34 / 25; 8 2048 14336 31 / 34 / 25; 32 4096 4096 28 / 20 / 21; 1 1024 14336 20 / 18 /
+  // 12; 16 512 4096 9.8 / 7.6 / 7.7; 16 8192 14336 126 / 130 / 91.
+  const bool wide = a.I >= 8192 || (a.H <= 1024 && a.I > 2048);
+  if (a.T <= 32 && wide && (a.T > 4 || a.H < 2048))
+    hipLaunchKernelGGL(k_ffn_stream, dim3((unsigned)cdiv(a.I, 32)), dim3(256), 0, s, a);
+  else if (a.T <= 16)   // (the widest I is 2^20: 2^17 workgroups of 512)
+    hipLaunchKernelGGL(k_ffn_few, dim3((unsigned)(a.I / 8)), dim3(512), 0, s, a);
+  else
+    return ffn<false>(a, s);
   return hipGetLastError();
 }
 hipError_t launch_ffn_dgu(const FfnArgs &a, hipStream_t s) { return ffn<true>(a, s); }

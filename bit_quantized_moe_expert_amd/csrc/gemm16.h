@@ -392,91 +392,71 @@ struct BlockRow {
   }
 };
 
-// A few rows of x (16 MB) against NB blocks of 16 rows of y where there are few of those: W
-// waves share K, each lane loads its fragments from memory as they are needed, many at a time, and the
-// waves' sums meet in LDS. A row of either side is any row: y_row(i) for the rows 0 .. 16 NB - 1 of the
-// group, x_row(i) for 0 .. 16 MB - 1 (rows that do not exist: any that do, their sums are not used).
-template <int NB_, int MB_, int W_>
+// Up to 16 rows of x against 16 rows of y, for few workgroups of them: W waves share K, each lane loads its
+// fragments from memory as they are needed, eight steps at a time, and the waves' sums meet in LDS. A row of either side
+// is any row: y_row(i) and x_row(i) for i in 0 .. 15 (rows that do not exist: any that do, their sums are not used).
+template <int W>
 struct FewRows {
-  static constexpr int NB = NB_, MB = MB_, W = W_, BLOCKS = NB * MB, THREADS = 64 * W, LDS = W * BLOCKS * 1024;
-  static_assert(BLOCKS <= W, "a wave for each block of the sums");
-  // The sums of block (wave / MB, wave % MB) in waves 0 .. BLOCKS - 1, as GemmTile's acc holds them.
+  static constexpr int THREADS = 64 * W, LDS = W * 1024;
+  // The sums in wave 0, as GemmTile's acc holds them.
   template <class YRow, class XRow>
   __device__ __attribute__((always_inline)) static f32x4_t run(char *lds, int K, YRow y_row, XRow x_row) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    const uint16_t *yp[NB], *xp[MB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) yp[n] = y_row(16 * n + i);
-#pragma unroll
-    for (int m = 0; m < MB; ++m) xp[m] = x_row(16 * m + i);
-    f32x4_t acc[NB][MB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int m = 0; m < MB; ++m) acc[n][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const uint16_t *yp = y_row(i), *xp = x_row(i);
+    f32x4_t acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const int pieces = K / 8, steps = (pieces + 3) / 4, first = steps * wave / W, last = steps * (wave + 1) / W;
     constexpr int U = 8;   // steps in flight
     for (int s0 = first; s0 < last; s0 += U) {
-      uint4 ry[U][NB], rx[U][MB];
+      uint4 ry[U], rx[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int at = (s0 + u) * 4 + g, in = at < pieces ? at : 0;
-#pragma unroll
-        for (int n = 0; n < NB; ++n) ry[u][n] = *reinterpret_cast<const uint4 *>(yp[n] + 8 * in);
-#pragma unroll
-        for (int m = 0; m < MB; ++m) rx[u][m] = *reinterpret_cast<const uint4 *>(xp[m] + 8 * in);
+        ry[u] = *reinterpret_cast<const uint4 *>(yp + 8 * in);
+        rx[u] = *reinterpret_cast<const uint4 *>(xp + 8 * in);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const bool in = s0 + u < last && (s0 + u) * 4 + g < pieces;
         const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int m = 0; m < MB; ++m)
-            acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, in ? ry[u][n] : zero),
-                                                                __builtin_bit_cast(bf16x8_t, in ? rx[u][m] : zero), acc[n][m], 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, in ? ry[u] : zero),
+                                                      __builtin_bit_cast(bf16x8_t, in ? rx[u] : zero), acc, 0, 0, 0);
       }
     }
     f32x4_t *red = reinterpret_cast<f32x4_t *>(lds);
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int m = 0; m < MB; ++m) red[(wave * BLOCKS + n * MB + m) * 64 + lane] = acc[n][m];
+    red[wave * 64 + lane] = acc;
     lds_barrier();
     f32x4_t sum = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (wave < BLOCKS) {
+    if (wave == 0) {
 #pragma unroll
-      for (int w = 0; w < W; ++w) sum += red[(w * BLOCKS + wave) * 64 + lane];
+      for (int w = 0; w < W; ++w) sum += red[w * 64 + lane];
     }
     return sum;
   }
 };
 
-// A few rows of x (16 MB, at most 32) against 64 rows of y, many of them: a stream of y's steps of 64 k through a
-// ring of STAGES places in LDS, all but two of them on their way; a wave has 16 rows of y. 17 rows against 32003 of
+// Up to 32 rows of x against 64 rows of y, many of them: a stream of y's steps of 64 k through a
+// ring of STAGES places in LDS, all but two of them on their way (Y_GROUP: y's rows are pairs, as GemmTile's G). 17 rows against 32003 of
 // 2048 k, statistics and loss with them: 31.8 us with six places (two workgroups a CU), 34.2 with four (three),
 // 35.3 with eight (one), and 38.4 with loads to registers as in FewRows, whose next ones wait for their sums.
-template <int MB_, int STAGES_>
+template <int STAGES, int Y_GROUP>
 struct FewStream {
-  static constexpr int MB = MB_, STAGES = STAGES_, THREADS = 256;
+  static constexpr int THREADS = 256;
   using X = GemmSide<32, THREADS, false>;
   using Y = GemmSide<64, THREADS, false>;
   static constexpr int STAGE = X::BYTES + Y::BYTES, LDS = STAGES * STAGE, P = X::PER + Y::PER;
-  // acc as GemmTile's: rows 16 wave .. of y, 16 m .. of x. The workgroup's LDS is free after it.
-  __device__ __attribute__((always_inline)) static void run(char *lds, int K, X &x, Y &y, f32x4_t (&acc)[MB]) {
+  // step(x, y): the products of a step of 64 k from its places (GemmSide's frag). The workgroup's LDS is free after it.
+  template <class Step>
+  __device__ __attribute__((always_inline)) static void run(char *lds, int K, const X &x, const Y &y, Step step) {
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-    const int steps = (K + kGemmBK - 1) / kGemmBK, wave = X::wave();
-    auto load = [&](int step, int stage) __attribute__((always_inline)) {
-      const int left = K - step * kGemmBK;   // (none past the end: zeros)
+    const int steps = (K + kGemmBK - 1) / kGemmBK;
+    auto load = [&](int s, int stage) __attribute__((always_inline)) {
+      const int left = K - s * kGemmBK;   // (none past the end: zeros)
       const uint32_t to = lds0 + (uint32_t)stage * STAGE;
 #pragma unroll
-      for (int i = 0; i < Y::PER; ++i) y.template load<false, 0>(i, step, left, 0, to + X::BYTES);
+      for (int i = 0; i < Y::PER; ++i) y.template load<false, Y_GROUP>(i, s, left, 0, to + X::BYTES);
 #pragma unroll
-      for (int i = 0; i < X::PER; ++i) x.template load<false, 0>(i, step, left, 0, to);
+      for (int i = 0; i < X::PER; ++i) x.template load<false, 0>(i, s, left, 0, to);
     };
-#pragma unroll
-    for (int m = 0; m < MB; ++m) acc[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) load(s, s);
     int at = 0;
@@ -484,13 +464,7 @@ struct FewStream {
       wait_loads<P *(STAGES - 2)>();
       lds_barrier();   // step s has landed, and step s - 1's place has been read
       load(s + STAGES - 1, at == 0 ? STAGES - 1 : at - 1);
-      const char *from = lds + at * STAGE;
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const bf16x8_t fy = Y::frag(from + X::BYTES, wave, kk);
-#pragma unroll
-        for (int m = 0; m < MB; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fy, X::frag(from, m, kk), acc[m], 0, 0, 0);
-      }
+      step(lds + at * STAGE, lds + at * STAGE + X::BYTES);
       at = at + 1 == STAGES ? 0 : at + 1;
     }
     wait_loads<0>();

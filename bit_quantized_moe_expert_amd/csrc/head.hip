@@ -182,7 +182,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadAr
 // Up to 16 MB rows: a workgroup takes 64 columns, a chunk of statistics, a wave 16 of them.
 template <int MB, bool TEACH>
 __global__ __launch_bounds__(256) void k_head_few(HeadArgs p) {
-  using F = FewStream<MB, 6>;   // (144 KB for two workgroups a CU)
+  using F = FewStream<6, 0>;   // (144 KB for two workgroups a CU)
   __shared__ __attribute__((aligned(16))) char lds[F::LDS];
   const int64_t n0 = (int64_t)blockIdx.x * 64;
   const int T = (int)p.T;
@@ -191,8 +191,17 @@ __global__ __launch_bounds__(256) void k_head_few(HeadArgs p) {
   x.init(p.x, p.H, 0, p.T);
   y.init(p.w, p.H, n0, p.V);
   f32x4_t acc[MB];
-  F::run(lds, p.H, x, y, acc);
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
+#pragma unroll
+  for (int m = 0; m < MB; ++m) acc[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int wave = F::X::wave(), lane = threadIdx.x & 63;
+  F::run(lds, p.H, x, y, [&](const char *xs, const char *ys) __attribute__((always_inline)) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const bf16x8_t fy = F::Y::frag(ys, wave, kk);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fy, F::X::frag(xs, m, kk), acc[m], 0, 0, 0);
+    }
+  });
   const int64_t c0 = n0 + 16 * wave;
   const int left = (int)(p.V - c0 < 16 ? p.V - c0 : 16), col = 4 * (lane >> 4);
   const float scale = kLog2e / p.tau;

@@ -51,7 +51,7 @@ def product_bound(x, w):
 # ------------------------------------------------------------------ gated feed-forward
 FFN_SIZES = [(1, 8, 8), (1, 2048, 1024), (2, 72, 2056), (3, 264, 40), (16, 1024, 264), (17, 128, 72), (31, 64, 136),
              (64, 200, 72), (65, 128, 520), (131, 2048, 768), (257, 520, 264), (1000, 192, 2048), (4099, 64, 1032),
-             (8193, 72, 136)]
+             (8193, 72, 136), (1, 72, 2080), (7, 2048, 8200), (16, 1024, 2056), (17, 40, 8232), (32, 2056, 8192), (4, 2048, 8192)]
 
 
 def ffn_case(T, H, I, glu, seed=0):
