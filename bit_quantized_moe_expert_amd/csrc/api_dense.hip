@@ -55,11 +55,11 @@ FfnArgs ffn_args(const nf4moe_gated_ffn_t &f, const uint16_t *x, int64_t T) {
 
 struct FfnCarve {
   uint16_t *dgu, *x2;
-  float *part;
+  float *part, *wpart;   // slices of dx and of dw13
   int64_t rows;   // of dgu
   size_t bytes;
 };
-// One size whatever outputs are asked for: that of dx alone, which has the most slices.
+// One size whatever outputs are asked for: that of each alone, which has the most slices.
 FfnCarve carve_ffn(void *ws, const nf4moe_gated_ffn_t &f, int64_t T) {
   FfnCarve c = {};
   Bump b{(char *)ws};
@@ -67,8 +67,10 @@ FfnCarve carve_ffn(void *ws, const nf4moe_gated_ffn_t &f, int64_t T) {
   c.rows = few ? 2 * T : T;
   c.dgu = b.take<uint16_t>((size_t)c.rows * 2 * f.I);
   if (few) c.x2 = b.take<uint16_t>((size_t)c.rows * f.H);
-  const int slices = product_slices(c.rows, f.H, 2 * (int64_t)f.I, true);
+  const int slices = product_slices(c.rows, f.H, 2 * (int64_t)f.I, true, 8);
   if (few || slices > 1) c.part = b.take<float>((size_t)slices * c.rows * f.H);
+  const int wslices = product_slices(2 * (int64_t)f.I, f.H, c.rows, true, 12);
+  if (wslices > 1) c.wpart = b.take<float>((size_t)wslices * 2 * f.I * f.H);
   c.bytes = b.off;
   return c;
 }
@@ -98,7 +100,7 @@ struct HeadCarve {
   int32_t *offsets;
   uint16_t *P, *x2;
   uint64_t *live;
-  float *part;
+  float *part, *wpart;   // slices of dx and of a piece of dw
   int64_t piece, rows;   // rows of P
   size_t bytes;
 };
@@ -120,8 +122,11 @@ HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, int k, bool ba
     c.P = b.take<uint16_t>((size_t)c.rows * c.piece);
     if (few) c.x2 = b.take<uint16_t>((size_t)c.rows * h.H);
     else c.live = b.take<uint64_t>((size_t)cdiv(T, 64));
-    const int slices = product_slices(c.rows, h.H, c.piece < h.V ? c.piece : h.V, true);
+    const int slices = product_slices(c.rows, h.H, c.piece < h.V ? c.piece : h.V, true, 8);
     if (few || slices > 1 || c.piece < h.V) c.part = b.take<float>((size_t)slices * c.rows * h.H);
+    const int64_t most = c.piece < h.V ? c.piece : h.V;
+    const int wslices = product_slices(most, h.H, c.rows, true, 12);
+    if (wslices > 1) c.wpart = b.take<float>((size_t)wslices * most * h.H);
   }
   c.bytes = b.off;
   return c;
@@ -142,8 +147,9 @@ HeadArgs head_args(const nf4moe_head_t &h, const uint16_t *x, int64_t T, const i
 // The gradients of either loss, a piece of the vocabulary after the other.
 nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint16_t *dw, hipStream_t s) {
   const bool few = a.T <= kTwoParts;
-  const int slices = product_slices(c.rows, a.H, c.piece < a.V ? c.piece : a.V, !dw);
+  const int slices = product_slices(c.rows, a.H, c.piece < a.V ? c.piece : a.V, !dw, 8);
   const bool parts = few || slices > 1 || c.piece < a.V;
+  const int wslices = product_slices(c.piece < a.V ? c.piece : a.V, a.H, c.rows, !dx, 12);
   a.P = c.P, a.live = dw ? c.live : nullptr, a.x2 = dw ? c.x2 : nullptr, a.list = c.list, a.offsets = c.offsets;
   hipError_t e = a.k ? launch_head_entries(a, s) : hipSuccess;
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += c.piece) {
@@ -154,8 +160,9 @@ nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint
     px.x = a.P, px.ldx = c.piece, px.y = a.w + v0 * a.H, px.ldy = a.H, px.M = c.rows, px.N = a.H, px.K = a.vn;
     px.out = parts ? nullptr : dx, px.part = c.part, px.add = v0 > 0, px.slices = slices;
     pw.x = a.P, pw.ldx = c.piece, pw.y = few ? c.x2 : a.x, pw.ldy = a.H, pw.M = a.vn, pw.N = a.H, pw.K = c.rows;
-    pw.out = dw + v0 * a.H, pw.slices = 1, pw.live = c.live;
+    pw.out = wslices > 1 ? nullptr : dw + v0 * a.H, pw.part = c.wpart, pw.slices = wslices, pw.live = c.live;
     e = launch_products(dx ? &px : nullptr, dw ? &pw : nullptr, s);
+    if (e == hipSuccess && dw && wslices > 1) e = launch_join(c.wpart, wslices, a.vn * a.H, dw + v0 * a.H, s);
   }
   // (few rows: a slice's second half are the second parts' rows, as one slice more)
   if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, a.T * a.H, dx, s);
@@ -242,16 +249,18 @@ nf4moe_status_t nf4moe_gated_ffn_backward(const nf4moe_gated_ffn_t *ffn, const u
   a.dh = dh, a.dgu = c.dgu, a.h = h, a.x2 = dw13 ? c.x2 : nullptr;
   hipError_t e = launch_ffn_dgu(a, s);
   const bool few = T <= kTwoParts;
-  const int slices = product_slices(c.rows, f.H, 2 * (int64_t)f.I, !dw13);
+  const int slices = product_slices(c.rows, f.H, 2 * (int64_t)f.I, !dw13, 8);
   const bool parts = few || slices > 1;
+  const int wslices = product_slices(2 * (int64_t)f.I, f.H, c.rows, !dx, 12);
   ProductArgs px = {}, pw = {};
   px.x = c.dgu, px.ldx = 2 * (int64_t)f.I, px.y = f.w13, px.ldy = f.H, px.M = c.rows, px.N = f.H, px.K = 2 * (int64_t)f.I;
   px.out = parts ? nullptr : dx, px.part = c.part, px.slices = slices;
   pw.x = c.dgu, pw.ldx = 2 * (int64_t)f.I, pw.y = few ? c.x2 : x, pw.ldy = f.H, pw.M = 2 * (int64_t)f.I, pw.N = f.H, pw.K = c.rows;
-  pw.out = dw13, pw.slices = 1;
+  pw.out = wslices > 1 ? nullptr : dw13, pw.part = c.wpart, pw.slices = wslices;
   if (e == hipSuccess) e = launch_products(dx ? &px : nullptr, dw13 ? &pw : nullptr, s);
   // (few rows: a slice's second half are the second parts' rows, as one slice more)
   if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, T * f.H, dx, s);
+  if (e == hipSuccess && dw13 && wslices > 1) e = launch_join(c.wpart, wslices, 2 * cells, dw13, s);
   return hip_status(e, "gated feed-forward backward launch");
 }
 

@@ -29,8 +29,9 @@ struct ProductArgs {
 // The two products of a backward pass, both with y turned: `dx` with x as it lies, `dw` with x
 // turned, together in one launch where both are given (K > 0).
 hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStream_t s);
-// Slices of K that fill the card (alone) or half of it (beside a second product) for dx.
-int product_slices(int64_t M, int64_t N, int64_t K, bool alone);
+// Slices of K, of `least` steps of 64 at least, that fill the card (alone) or half of it (beside a second
+// product): of 8 for dx, of 12 for dw, which has two turned operands and more to join.
+int product_slices(int64_t M, int64_t N, int64_t K, bool alone, int least);
 // out bf16 [n] = the sum of the slices' parts, in order.
 hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s);
 

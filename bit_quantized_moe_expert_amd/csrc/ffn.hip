@@ -390,17 +390,17 @@ int64_t product_tile_count(const void *args, int bm, int bn) {
   const int64_t x = a.x.K ? cdiv(a.x.M, bm) * cdiv(a.x.N, bn) * a.x.slices : 0;
   if (!a.w.K) return x;
   if (bm == 192) return (int64_t)1 << 40;   // (dx alone: a turned side of 192 rows has no whole pieces a thread)
-  return x + cdiv(a.w.M, bm) * cdiv(a.w.N, bn);
+  return x + cdiv(a.w.M, bm) * cdiv(a.w.N, bn) * a.w.slices;
 }
 
 template <class TX, class TW>
 hipError_t products(const ProductArgs &dx, const ProductArgs &dw, hipStream_t s) {
   const int64_t tx = dx.K ? cdiv(dx.M, TX::BM) * cdiv(dx.N, TX::BN) * dx.slices : 0;
-  const int64_t tw = dw.K ? cdiv(dw.M, TW::BM) * cdiv(dw.N, TW::BN) : 0;
+  const int64_t tw = dw.K ? cdiv(dw.M, TW::BM) * cdiv(dw.N, TW::BN) * dw.slices : 0;
   int nbx = (int)cdiv(tx, 8) * 8, nbw = (int)cdiv(tw, 8) * 8;
   if (TX::KS == 1 && tx + tw > TX::MOST) {
     // the workgroups that run at a time, shared by the steps that either product takes
-    const double sx = (double)tx * (double)cdiv(dx.K, dx.slices ? dx.slices : 1), sw = (double)tw * (double)dw.K;
+    const double sx = (double)tx * (double)cdiv(dx.K, dx.slices ? dx.slices : 1), sw = (double)tw * (double)cdiv(dw.K, dw.slices ? dw.slices : 1);
     const int share = (int)(TX::MOST / 8 * sx / (sx + sw) + 0.5) * 8;
     nbx = !tx ? 0 : !tw ? TX::MOST : share < 8 ? 8 : share > TX::MOST - 8 ? TX::MOST - 8 : share;
     if (tx) nbx = gemm_grid(tx, nbx);
@@ -450,10 +450,10 @@ hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStre
   return w.live ? products<true>(x, w, s) : products<false>(x, w, s);
 }
 
-int product_slices(int64_t M, int64_t N, int64_t K, bool alone) {
+int product_slices(int64_t M, int64_t N, int64_t K, bool alone, int least) {
   const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), steps = cdiv(K, kGemmBK);
   int64_t s = (alone ? 256 : 128) / tiles;
-  if (s > steps / 8) s = steps / 8;   // at least 8 steps each
+  if (s > steps / least) s = steps / least;
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
