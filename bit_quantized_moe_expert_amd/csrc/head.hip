@@ -119,17 +119,23 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_stats(HeadAr
     if (left <= 0) return;   // the wave
     const float c = kLog2e / p.tau;
     [[maybe_unused]] TileEntries<T::MB, COLS> entries;
-    if constexpr (TEACH) entries.load(p, lane, m0 + T::row_at(0), n0);
+    [[maybe_unused]] int32_t id[T::MB];
+    if constexpr (TEACH) {
+      entries.load(p, lane, m0 + T::row_at(0), n0);
+    } else {   // asked for together
+#pragma unroll
+      for (int mb = 0; mb < T::MB; ++mb) {
+        const int64_t row = m0 + T::row_at(mb) + (lane & 15);
+        id[mb] = p.ids[row < p.T ? row : p.T - 1];
+      }
+    }
 #pragma unroll
     for (int mb = 0; mb < T::MB; ++mb) {
       const int64_t row0 = m0 + T::row_at(mb), row = row0 + (lane & 15);
       if (row0 >= p.T) break;   // the wave
       if constexpr (!TEACH) {   // the labels' logits, each by the one lane that has it
-        int want = -1;
-        if (row < p.T) {
-          const int64_t at = (int64_t)p.ids[row] - n0;
-          want = at >= 0 && at < left ? (int)at : -1;
-        }
+        const int64_t at = (int64_t)id[mb] - n0;
+        const int want = row < p.T && at >= 0 && at < left ? (int)at : -1;
         if (__any(want >= 0)) {
 #pragma unroll
           for (int nb = 0; nb < T::NB; ++nb)
@@ -497,6 +503,14 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
     };
     [[maybe_unused]] TileEntries<T::MB, COLS> entries;
     [[maybe_unused]] float value[T::MB];
+    [[maybe_unused]] int32_t id[T::MB];
+    float dloss[T::MB], row_lse[T::MB];   // asked for together
+#pragma unroll
+    for (int mb = 0; mb < T::MB; ++mb) {
+      const int64_t row = m0 + T::row_at(mb) + (lane & 15), in = row < p.T ? row : p.T - 1;
+      if constexpr (!TEACH) id[mb] = p.ids[in];
+      dloss[mb] = p.dloss[in], row_lse[mb] = p.lse[in];
+    }
     if constexpr (TEACH) {
       entries.load(p, lane, m0 + T::row_at(0), p.v0 + n0);
 #pragma unroll
@@ -510,13 +524,16 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
     for (int mb = 0; mb < T::MB; ++mb) {
       const int64_t row0 = m0 + T::row_at(mb), row = row0 + (lane & 15);
       if (row0 >= p.T) break;   // the wave
-      const bool on = row < p.T && row_on(p, row);
-      const float coef = on ? p.dloss[row] * p.tau : 0.0f, lse = on ? p.lse[row] * kLog2e : 0.0f;
+      bool on = row < p.T;
       int want = -1;
-      if (!TEACH && on) {
-        const int64_t at = (int64_t)p.ids[row] - p.v0 - n0;
-        want = at >= 0 && at < left ? (int)at : -1;
+      if constexpr (TEACH) {
+        on = on && row_lse[mb] != __builtin_inff();
+      } else {
+        on = on && id[mb] >= 0 && id[mb] < p.V;
+        const int64_t at = (int64_t)id[mb] - p.v0 - n0;
+        want = on && at >= 0 && at < left ? (int)at : -1;
       }
+      const float coef = on ? dloss[mb] * p.tau : 0.0f, lse = on ? row_lse[mb] * kLog2e : 0.0f;
       // the rows that count in dw's product, by the wave that has the vocabulary's first columns
       const uint64_t rows_on = __ballot(on);
       if (p.live && p.v0 + n0 == 0 && lane == 0) reinterpret_cast<uint16_t *>(p.live)[row0 >> 4] = (uint16_t)rows_on;

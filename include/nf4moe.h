@@ -571,8 +571,8 @@ size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_
  * lse[t] - l[t, labels[t]], fp32 [T]; a label outside [0, V) (-100, say) means loss 0 and no
  * gradient. T == 0 is a no-op. Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED.
  *
- * nf4moe_vocab_ce_backward -- for dloss fp32 [T] (the gradient of loss; not read where a row has no
- * label) and the forward's lse, with P = dloss (softmax(l) - onehot(label)):
+ * nf4moe_vocab_ce_backward -- for dloss fp32 [T] (the gradient of loss; where a row has no label it may
+ * hold anything) and the forward's lse, with P = dloss (softmax(l) - onehot(label)):
  *   dx bf16 [T, H] = P W;  dw bf16 [V, H] = P^T x     (either may be NULL)
  * A row without a label counts for nothing whatever its x holds. T == 0 writes zeros to dw. */
 nf4moe_status_t nf4moe_vocab_ce_forward(const nf4moe_head_t *head, const uint16_t *x, int64_t T, const int32_t *labels,
