@@ -10,7 +10,7 @@
 // operand of bf16 products; up to kTwoParts rows it is held in two parts, which leave 2^-17.
 //
 // Measured, us: forward of 4096 rows, H 2048, I 8192 210 (1311 TFLOP/s; the bare products by a
-// library 198), of 4099, H = I = 2880 108 to 114 (1190 to 1260, the ragged tiles' part of it 10 %); backward of
+// library 198), of 4099, H = I = 2880 108 to 114 (1190 to 1260, 5 % more in its padding); backward of
 // the first 645 to 683 (1210 to 1280 of 825 GFLOP). All of these are bound by the matrix cores and their
 // power. One row, H 2048, I 1024: 5.2, of which the 8.4 MB of weights would take 1.6: a launch's
 // latency and memory's; 32 rows, H 4096, I 14336 45 for 235 MB (5.2 TB/s). 131 rows, H 2048, I 768,

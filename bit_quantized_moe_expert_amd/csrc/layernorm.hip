@@ -6,8 +6,8 @@
 //   dx = dx_base + rstd (a - mean(a) - n mean(a n));  dw = sum_t dy n;  db = sum_t dy
 // Everything is fp32 in registers, each output rounded once. Both directions are bound by memory
 // traffic. Rows lie as in the block norms' kernels: TPR threads a row, 8 NC values each, so that a row is read
-// once and its sums meet in one exchange through LDS. Measured, us: 8190 x 2880 fp32 to bf16 27 to 31 (142
-// MB, 4.6 to 5.2 TB/s, a copy's rate 5.4); backward of 8192 x 2048 bf16 with a base 27 (134 MB, 5.0 TB/s) and
+// once and its sums meet in one exchange through LDS. Measured, us: 8190 x 2880 fp32 to bf16 28.5 (142
+// MB, 5.0 TB/s, a copy's rate 5.4); backward of 8192 x 2048 bf16 with a base 27 (134 MB, 5.0 TB/s) and
 // 4 for the column sums; 4 rows 3.0.
 #include "dense.h"
 #include "internal.h"
@@ -205,29 +205,7 @@ int ln_tpr(int H) {
 }
 int ln_slots(int H) { return back_threads(ln_tpr(H)) / ln_tpr(H); }
 
-// f(TPR, NC) as integral constants, by the width of a row. Forward: up to 32 values a thread, whose loads go out
-// together, and so fewer waves to a row's sum (8190 x 2880 bf16: 512 threads of 8 values 24.6 us, 128 of 24 19.5; 4096 x
-// 4096 fp32 22.0 and 19.0).
-template <class F>
-void by_width_forward(int H, F &&f) {
-  using std::integral_constant;
-  const auto more = [&](auto tpr) {
-    constexpr int TPR = decltype(tpr)::value;
-    if (H <= 24 * TPR) f(tpr, integral_constant<int, 3>());
-    else f(tpr, integral_constant<int, 4>());
-  };
-  const integral_constant<int, 1> one;
-  const integral_constant<int, 64> wave;
-  if (H <= 64) f(integral_constant<int, 8>(), one);
-  else if (H <= 128) f(integral_constant<int, 16>(), one);
-  else if (H <= 256) f(integral_constant<int, 32>(), one);
-  else if (H <= 512) f(wave, one);
-  else if (H <= 1024) f(wave, integral_constant<int, 2>());
-  else if (H <= 2048) more(wave);
-  else if (H <= 4096) more(integral_constant<int, 128>());
-  else if (H <= 8192) more(integral_constant<int, 256>());
-  else more(integral_constant<int, 512>());
-}
+// f(TPR, NC) as integral constants, by the width of a row.
 template <class F>
 void by_width(int H, F &&f) {
   using std::integral_constant;
@@ -244,6 +222,26 @@ void by_width(int H, F &&f) {
       if (H <= 8192) return f(integral_constant<int, 1024>(), one);
       return f(integral_constant<int, 1024>(), integral_constant<int, 2>());
   }
+}
+// Forward: up to 32 values a thread, whose loads go out together, and so fewer waves to a row's sum (8190 x
+// 2880 bf16: 512 threads of 8 values 24.6 us, 128 of 24 19.5; 4096 x 4096 fp32 22.0 and 19.0); 16 above 4096, where
+// many rows ran slower with 32 (16384 x 8192 bf16: 8 values 138, 16 121, 32 140). A few rows, whose time is one
+// row's, take 8 (4 x 2048: 3.0 and 4.0).
+template <class F>
+void by_width_forward(int64_t T, int H, F &&f) {
+  using std::integral_constant;
+  if (T <= 256 || H <= 512) return by_width(H, f);
+  const auto more = [&](auto tpr) {
+    constexpr int TPR = decltype(tpr)::value;
+    if (H <= 24 * TPR) f(tpr, integral_constant<int, 3>());
+    else f(tpr, integral_constant<int, 4>());
+  };
+  const integral_constant<int, 64> wave;
+  if (H <= 1024) f(wave, integral_constant<int, 2>());
+  else if (H <= 2048) more(wave);
+  else if (H <= 4096) more(integral_constant<int, 128>());
+  else if (H <= 8192) f(integral_constant<int, 512>(), integral_constant<int, 2>());
+  else f(integral_constant<int, 1024>(), integral_constant<int, 2>());
 }
 // f(XBF, YBF, ODD)
 template <class F>
@@ -274,7 +272,7 @@ hipError_t launch_layer_norm_forward(const LayerNormArgs &a, hipStream_t s) {
     p.x = (const char *)a.x + n * (a.x_bf16 ? 2 : 4), p.y = (char *)a.y + n * (a.y_bf16 ? 2 : 4);
     p.mean = a.mean + r0, p.rstd = a.rstd + r0;
     by_types(p, [&](auto xb, auto yb, auto odd) {
-      by_width_forward(p.H, [&](auto tpr, auto nc) {
+      by_width_forward(a.T, p.H, [&](auto tpr, auto nc) {
         constexpr int threads = tpr.value > 256 ? tpr.value : 256;
         hipLaunchKernelGGL((k_ln_forward<xb.value, yb.value, tpr.value, nc.value, odd.value>),
                            dim3((unsigned)cdiv(p.T, threads / tpr.value)), dim3(threads), 0, s, p);

@@ -413,7 +413,7 @@ def test_head_past_32_bit_offsets():
 
 # ------------------------------------------------------------------ layer norm
 @pytest.mark.parametrize("xdt,ydt", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
-@pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (5, 8), (130, 64), (2000, 118), (700, 200), (20003, 24), (515, 1000), (77, 1500), (5, 3500), (33, 5001), (3, 12000), (4, 513), (300, 2048), (67, 2880), (9, 4100),
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (5, 8), (130, 64), (2000, 118), (700, 200), (20003, 24), (515, 1000), (77, 1500), (5, 3500), (33, 5001), (3, 12000), (259, 1500), (300, 3500), (270, 5001), (257, 12000), (4, 513), (300, 2048), (67, 2880), (9, 4100),
                                  (700, 4096), (6, 8191), (5, 8192), (3, 16383), (600, 16384)])
 def test_layer_norm(T, H, xdt, ydt):
     rn = gen(T + H)
