@@ -100,6 +100,7 @@ struct HeadCarve {
   int32_t *offsets;
   uint16_t *P, *x2;
   uint64_t *live;
+  float *unit;
   float *part, *wpart;   // slices of dx and of a piece of dw
   int64_t piece, rows;   // rows of P
   size_t bytes;
@@ -121,7 +122,7 @@ HeadCarve carve_head(void *ws, const nf4moe_head_t &h, int64_t T, int k, bool ba
     c.piece = head_piece(c.rows, h.V);
     c.P = b.take<uint16_t>((size_t)c.rows * c.piece);
     if (few) c.x2 = b.take<uint16_t>((size_t)c.rows * h.H);
-    else c.live = b.take<uint64_t>((size_t)cdiv(T, 64));
+    else c.live = b.take<uint64_t>((size_t)cdiv(T, 64)), c.unit = b.take<float>(1);
     const int slices = product_slices(c.rows, h.H, c.piece < h.V ? c.piece : h.V, true, 8);
     if (few || slices > 1 || c.piece < h.V) c.part = b.take<float>((size_t)slices * c.rows * h.H);
     const int64_t most = c.piece < h.V ? c.piece : h.V;
@@ -150,8 +151,8 @@ nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint
   const int slices = product_slices(c.rows, a.H, c.piece < a.V ? c.piece : a.V, !dw, 8);
   const bool parts = few || slices > 1 || c.piece < a.V;
   const int wslices = product_slices(c.piece < a.V ? c.piece : a.V, a.H, c.rows, !dx, 12);
-  a.P = c.P, a.live = dw ? c.live : nullptr, a.x2 = dw ? c.x2 : nullptr, a.list = c.list, a.offsets = c.offsets;
-  hipError_t e = a.k ? launch_head_entries(a, s) : hipSuccess;
+  a.P = c.P, a.live = dw ? c.live : nullptr, a.x2 = dw ? c.x2 : nullptr, a.list = c.list, a.offsets = c.offsets, a.unit = c.unit;
+  hipError_t e = launch_head_prepare(a, s);
   for (int64_t v0 = 0; v0 < a.V && e == hipSuccess; v0 += c.piece) {
     a.v0 = v0, a.vn = a.V - v0 < c.piece ? a.V - v0 : c.piece, a.vp = c.piece;
     e = launch_head_piece(a, s);
@@ -161,11 +162,11 @@ nf4moe_status_t head_backward(HeadArgs a, const HeadCarve &c, uint16_t *dx, uint
     px.out = parts ? nullptr : dx, px.part = c.part, px.add = v0 > 0, px.slices = slices;
     pw.x = a.P, pw.ldx = c.piece, pw.y = few ? c.x2 : a.x, pw.ldy = a.H, pw.M = a.vn, pw.N = a.H, pw.K = c.rows;
     pw.out = wslices > 1 ? nullptr : dw + v0 * a.H, pw.part = c.wpart, pw.slices = wslices, pw.live = c.live;
-    e = launch_products(dx ? &px : nullptr, dw ? &pw : nullptr, s);
-    if (e == hipSuccess && dw && wslices > 1) e = launch_join(c.wpart, wslices, a.vn * a.H, dw + v0 * a.H, s);
+    e = launch_products(dx ? &px : nullptr, dw ? &pw : nullptr, c.unit, s);
+    if (e == hipSuccess && dw && wslices > 1) e = launch_join(c.wpart, wslices, a.vn * a.H, c.unit, dw + v0 * a.H, s);
   }
   // (few rows: a slice's second half are the second parts' rows, as one slice more)
-  if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, a.T * a.H, dx, s);
+  if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, a.T * a.H, c.unit, dx, s);
   return hip_status(e, "head backward launch");
 }
 
@@ -257,10 +258,10 @@ nf4moe_status_t nf4moe_gated_ffn_backward(const nf4moe_gated_ffn_t *ffn, const u
   px.out = parts ? nullptr : dx, px.part = c.part, px.slices = slices;
   pw.x = c.dgu, pw.ldx = 2 * (int64_t)f.I, pw.y = few ? c.x2 : x, pw.ldy = f.H, pw.M = 2 * (int64_t)f.I, pw.N = f.H, pw.K = c.rows;
   pw.out = wslices > 1 ? nullptr : dw13, pw.part = c.wpart, pw.slices = wslices;
-  if (e == hipSuccess) e = launch_products(dx ? &px : nullptr, dw13 ? &pw : nullptr, s);
+  if (e == hipSuccess) e = launch_products(dx ? &px : nullptr, dw13 ? &pw : nullptr, nullptr, s);
   // (few rows: a slice's second half are the second parts' rows, as one slice more)
-  if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, T * f.H, dx, s);
-  if (e == hipSuccess && dw13 && wslices > 1) e = launch_join(c.wpart, wslices, 2 * cells, dw13, s);
+  if (e == hipSuccess && dx && parts) e = launch_join(c.part, few ? 2 * slices : slices, T * f.H, nullptr, dx, s);
+  if (e == hipSuccess && dw13 && wslices > 1) e = launch_join(c.wpart, wslices, 2 * cells, nullptr, dw13, s);
   return hip_status(e, "gated feed-forward backward launch");
 }
 

@@ -9,8 +9,10 @@ namespace nf4moe {
 
 // Up to so many rows a backward holds what it rounds between its products (dgu, P) as the sum of two bf16
 // parts, the second in rows T .. 2 T - 1, and x twice. One row's largest value may be most of its
-// gradients, and the rounding of it all of their error (up to 2^-8; many rows' roundings average out), and
-// the products' tiles have the room.
+// gradients, and the rounding of it all of their error (up to 2^-8), and the products' tiles have the room.
+// More rows have one part: a row's own roundings are then those of its largest values (in dx, and in the rows of dw
+// that few others share), and what keeps them apart from row to row is that the values differ. So P leaves
+// out the one factor that all rows of a mean loss have in common (HeadArgs::unit).
 constexpr int kTwoParts = 64;
 constexpr int kDenseMaxWidth = 1 << 20;   // H and I: 256 rows of it are below 2^31 bytes
 
@@ -27,13 +29,14 @@ struct ProductArgs {
   const uint64_t *live;
 };
 // The two products of a backward pass, both with y turned: `dx` with x as it lies, `dw` with x
-// turned, together in one launch where both are given (K > 0).
-hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStream_t s);
+// turned, together in one launch where both are given (K > 0). *unit (null: 1) is a factor of `out`; parts go without
+// it, launch_join has it.
+hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, const float *unit, hipStream_t s);
 // Slices of K, of `least` steps of 64 at least, that fill the card (alone) or half of it (beside a second
 // product): of 8 for dx, of 12 for dw, which has two turned operands and more to join.
 int product_slices(int64_t M, int64_t N, int64_t K, bool alone, int least);
-// out bf16 [n] = the sum of the slices' parts, in order.
-hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s);
+// out bf16 [n] = the sum of the slices' parts, in order, times *unit (null: 1).
+hipError_t launch_join(const float *part, int slices, int64_t n, const float *unit, uint16_t *out, hipStream_t s);
 
 struct FfnArgs {
   int64_t T;
@@ -72,12 +75,14 @@ struct HeadArgs {
   uint16_t *P;               // [T, vp]; up to kTwoParts rows: [2 T, vp], in two parts
   uint16_t *x2;              // up to kTwoParts rows: [2 T, H], x twice, zeros in the rows that do not count (or null)
   uint64_t *live;            // [T / 64] or null: a bit for each row, set where it has a gradient (written with the first piece)
+  // more than kTwoParts rows (or null): the factor that P leaves out and the products' outputs get, in fp32
+  float *unit;
 };
 constexpr int kHeadChunk = 128;
 int64_t head_stat_chunks(int64_t T, int64_t V, int H);
 hipError_t launch_head_forward(const HeadArgs &a, hipStream_t s);
-// The teacher's lists for the backward's pieces.
-hipError_t launch_head_entries(const HeadArgs &a, hipStream_t s);
+// What comes before a backward's pieces: the teacher's lists, and the unit.
+hipError_t launch_head_prepare(const HeadArgs &a, hipStream_t s);
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s);
 int64_t head_piece(int64_t rows, int64_t V);   // rows of P, one at least
 

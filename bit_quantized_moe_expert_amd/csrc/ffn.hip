@@ -239,9 +239,11 @@ struct ProductPlace : GemmTiles {
   }
 };
 
-// The tiles of workgroup b of nb of a product.
-template <class T>
-__device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &p, char *lds, int b, int nb, int log = 3) {
+// The tiles of workgroup b of nb of a product. UNIT: outputs times *unit_at, one argument for both products, read where
+// it is used (in each product's arguments its address took 23 scalar registers more, spilled in the steps' loop,
+// and 1 to 2 %).
+template <class T, bool UNIT>
+__device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &p, const float *unit_at, char *lds, int b, int nb, int log = 3) {
   const ProductPlace<T> place(p, b, nb, log);
   int m, n, slice;
   if (!place.find(0, m, n, slice)) return;
@@ -257,10 +259,11 @@ __device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &
       const int64_t row0 = (int64_t)m * T::BM + T::row_at(mb), rows = p.M - row0;
       if (rows <= 0) break;   // the wave
       if (p.out) {
+        const float unit = UNIT ? *unit_at : 1.0f;
         const BlockRow<16 * T::NB> out{T::scratch(lds), lane};
 #pragma unroll
         for (int nb2 = 0; nb2 < T::NB; ++nb2) {
-          const f32x4_t &v = t.acc[nb2][mb];
+          const f32x4_t v = UNIT ? t.acc[nb2][mb] * unit : t.acc[nb2][mb];
           out.put(T::col_of(lane, nb2), pack4(v[0], v[1], v[2], v[3]));
         }
         out.out(p.out + row0 * p.N + n0, p.N, rows, cols);
@@ -292,23 +295,24 @@ __device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &
 // dx by itself has its k in slices to be joined (4096 rows, H 2048, I 8192: dx 240 us alone, dw 231, both 434).
 // nbx < 0, for large products of equal steps: half of the XCDs each, so that an L2 holds the operands
 // of one product (1 to 1.7 % of a whole backward).
-template <class TX, class TW>
-__global__ __launch_bounds__(TX::THREADS, TX::WAVES_SIMD) void k_products(ProductArgs dx, ProductArgs dw, int nbx) {
+template <class TX, class TW, bool UNIT>
+__global__ __launch_bounds__(TX::THREADS, TX::WAVES_SIMD) void k_products(ProductArgs dx, ProductArgs dw, const float *unit_at, int nbx) {
   static_assert(TX::THREADS == TW::THREADS, "one workgroup size");
   __shared__ __attribute__((aligned(16))) char lds[TX::LDS > TW::LDS ? TX::LDS : TW::LDS];
   const int b = blockIdx.x, nb = gridDim.x;
   if (nbx < 0) {   // half of the XCDs each
     const int half = (b >> 3) * 4 + (b & 3);
-    if ((b & 7) < 4) product_tiles<TX>(dx, lds, half, nb / 2, 2);
-    else product_tiles<TW>(dw, lds, half, nb / 2, 2);
+    if ((b & 7) < 4) product_tiles<TX, UNIT>(dx, unit_at, lds, half, nb / 2, 2);
+    else product_tiles<TW, UNIT>(dw, unit_at, lds, half, nb / 2, 2);
     return;
   }
-  if (b < nbx) product_tiles<TX>(dx, lds, b, nbx);
-  else product_tiles<TW>(dw, lds, b - nbx, nb - nbx);
+  if (b < nbx) product_tiles<TX, UNIT>(dx, unit_at, lds, b, nbx);
+  else product_tiles<TW, UNIT>(dw, unit_at, lds, b - nbx, nb - nbx);
 }
 
 // Few slices: 8 values a thread at a time, n a multiple of 8.
-__global__ __launch_bounds__(256) void k_join(const float *part, int slices, int64_t n, uint16_t *out) {
+__global__ __launch_bounds__(256) void k_join(const float *part, int slices, int64_t n, const float *unit, uint16_t *out) {
+  const float by = unit ? *unit : 1.0f;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (int64_t)gridDim.x * 2048) {
     float4 a = make_float4(0, 0, 0, 0), b = a;
     for (int s = 0; s < slices; ++s) {
@@ -317,15 +321,16 @@ __global__ __launch_bounds__(256) void k_join(const float *part, int slices, int
       a = make_float4(a.x + u.x, a.y + u.y, a.z + u.z, a.w + u.w);
       b = make_float4(b.x + v.x, b.y + v.y, b.z + v.z, b.w + v.w);
     }
-    const uint2 lo = pack4(a.x, a.y, a.z, a.w), hi = pack4(b.x, b.y, b.z, b.w);
+    const uint2 lo = pack4(a.x * by, a.y * by, a.z * by, a.w * by), hi = pack4(b.x * by, b.y * by, b.z * by, b.w * by);
     *reinterpret_cast<uint4 *>(out + i) = make_uint4(lo.x, lo.y, hi.x, hi.y);
   }
 }
 // Many: a workgroup 256 values at a time, wave w the slices w, w + 8, .. in order, asked for eight together;
 // then the waves in order. (128 slices of 3168 values: 19 us by k_join, two workgroups with 128 trips to
 // memory each, 4 by this.)
-__global__ __launch_bounds__(512) void k_join_many(const float *part, int slices, int64_t n, uint16_t *out) {
+__global__ __launch_bounds__(512) void k_join_many(const float *part, int slices, int64_t n, const float *unit, uint16_t *out) {
   __shared__ float4 red[8][64];
+  const float by = unit ? *unit : 1.0f;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < n; i0 += (int64_t)gridDim.x * 256) {
     const int64_t i = i0 + 4 * lane;
@@ -345,7 +350,7 @@ __global__ __launch_bounds__(512) void k_join_many(const float *part, int slices
         const float4 v = red[w][lane];
         a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
       }
-      *reinterpret_cast<uint2 *>(out + i) = pack4(a.x, a.y, a.z, a.w);
+      *reinterpret_cast<uint2 *>(out + i) = pack4(a.x * by, a.y * by, a.z * by, a.w * by);
     }
     lds_barrier();
   }
@@ -394,8 +399,8 @@ int64_t product_tile_count(const void *args, int bm, int bn) {
   return x + cdiv(a.w.M, bm) * cdiv(a.w.N, bn) * a.w.slices;
 }
 
-template <class TX, class TW>
-hipError_t products(const ProductArgs &dx, const ProductArgs &dw, hipStream_t s) {
+template <class TX, class TW, bool UNIT>
+hipError_t products(const ProductArgs &dx, const ProductArgs &dw, const float *unit, hipStream_t s) {
   const int64_t tx = dx.K ? cdiv(dx.M, TX::BM) * cdiv(dx.N, TX::BN) * dx.slices : 0;
   const int64_t tw = dw.K ? cdiv(dw.M, TW::BM) * cdiv(dw.N, TW::BN) * dw.slices : 0;
   int nbx = (int)cdiv(tx, 8) * 8, nbw = (int)cdiv(tw, 8) * 8;
@@ -408,23 +413,24 @@ hipError_t products(const ProductArgs &dx, const ProductArgs &dw, hipStream_t s)
     nbw = tw ? gemm_grid(tw, TX::MOST - nbx) : 0;
   }
   const int split = TX::KS == 1 && nbx == TX::MOST / 2 && nbw == nbx ? -1 : nbx;
-  hipLaunchKernelGGL((k_products<TX, TW>), dim3(nbx + nbw), dim3(TX::THREADS), 0, s, dx, dw, split);
+  hipLaunchKernelGGL((k_products<TX, TW, UNIT>), dim3(nbx + nbw), dim3(TX::THREADS), 0, s, dx, dw, unit, split);
   return hipGetLastError();
 }
-template <int MB, int NB, int WM, int WN, bool MASK, int KS = 1>
-hipError_t products_of(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
-  return products<GemmTile<MB, NB, WM, WN, false, true, 0, false, KS>, GemmTile<MB, NB, WM, WN, true, true, 0, MASK, KS>>(x, w, s);
+template <int MB, int NB, int WM, int WN, bool UNIT, int KS = 1>
+hipError_t products_of(const ProductArgs &x, const ProductArgs &w, const float *unit, hipStream_t s) {
+  return products<GemmTile<MB, NB, WM, WN, false, true, 0, false, KS>, GemmTile<MB, NB, WM, WN, true, true, 0, UNIT, KS>, UNIT>(x, w, unit, s);
 }
-template <bool MASK>
-hipError_t products(const ProductArgs &x, const ProductArgs &w, hipStream_t s) {
+// UNIT: those of a vocabulary loss of more than kTwoParts rows, whose outputs have a unit and whose rows for dw a mask.
+template <bool UNIT>
+hipError_t products(const ProductArgs &x, const ProductArgs &w, const float *unit, hipStream_t s) {
   const ProductPair both{x, w};
   const int64_t steps = cdiv(x.K > w.K ? x.K : w.K, kGemmBK);
   switch (gemm_class(product_tile_count, &both, steps)) {
-    case 256: return products_of<4, 8, 4, 2, MASK>(x, w, s);
-    case 192: return products<GemmTile<3, 8, 4, 2, false, true>, GemmTile<4, 8, 4, 2, true, true>>(x, w, s);
-    case 128: return products_of<4, 4, 2, 2, MASK>(x, w, s);
-    case 64: return products_of<2, 2, 2, 2, MASK>(x, w, s);
-    default: return products_of<2, 2, 2, 2, MASK, 4>(x, w, s);
+    case 256: return products_of<4, 8, 4, 2, UNIT>(x, w, unit, s);
+    case 192: return products<GemmTile<3, 8, 4, 2, false, true>, GemmTile<4, 8, 4, 2, true, true>, UNIT>(x, w, unit, s);
+    case 128: return products_of<4, 4, 2, 2, UNIT>(x, w, unit, s);
+    case 64: return products_of<2, 2, 2, 2, UNIT>(x, w, unit, s);
+    default: return products_of<2, 2, 2, 2, UNIT, 4>(x, w, unit, s);
   }
 }
 
@@ -445,10 +451,10 @@ hipError_t launch_ffn_forward(const FfnArgs &a, hipStream_t s) {
 }
 hipError_t launch_ffn_dgu(const FfnArgs &a, hipStream_t s) { return ffn<true>(a, s); }
 
-hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, hipStream_t s) {
+hipError_t launch_products(const ProductArgs *dx, const ProductArgs *dw, const float *unit, hipStream_t s) {
   const ProductArgs none = {};
   const ProductArgs &x = dx ? *dx : none, &w = dw ? *dw : none;
-  return w.live ? products<true>(x, w, s) : products<false>(x, w, s);
+  return unit ? products<true>(x, w, unit, s) : products<false>(x, w, unit, s);
 }
 
 int product_slices(int64_t M, int64_t N, int64_t K, bool alone, int least) {
@@ -458,11 +464,11 @@ int product_slices(int64_t M, int64_t N, int64_t K, bool alone, int least) {
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-hipError_t launch_join(const float *part, int slices, int64_t n, uint16_t *out, hipStream_t s) {
+hipError_t launch_join(const float *part, int slices, int64_t n, const float *unit, uint16_t *out, hipStream_t s) {
   const int64_t g = cdiv(n, slices > 4 ? 256 : 2048), most = 1 << 22;   // (well inside a dispatch's 2^32 threads)
   const dim3 grid((unsigned)(g < most ? g : most));
-  if (slices > 4) hipLaunchKernelGGL(k_join_many, grid, dim3(512), 0, s, part, slices, n, out);
-  else hipLaunchKernelGGL(k_join, grid, dim3(256), 0, s, part, slices, n, out);
+  if (slices > 4) hipLaunchKernelGGL(k_join_many, grid, dim3(512), 0, s, part, slices, n, unit, out);
+  else hipLaunchKernelGGL(k_join, grid, dim3(256), 0, s, part, slices, n, unit, out);
   return hipGetLastError();
 }
 

@@ -11,7 +11,10 @@
 //   P = dloss (exp(l - lse) - [v is the label])         or dloss tau (softmax - q)
 // rounded to bf16 (half a step of 2^-8 of each value, no more than the gradients' own
 // rounding; P is the operand of two bf16 products; up to kTwoParts rows it has two parts, which
-// leave 2^-17), then dx += P W and dW = P^T x.
+// leave 2^-17), then dx += P W and dW = P^T x. Of more rows P holds dloss / unit, and the products' sums are
+// multiplied by unit in fp32: in a mean loss, where dloss is the same in every row, a label's entry is then all
+// but a power of two and not dloss, whose rounding would be every row's (1020 rows of 1 / 1020: both
+// gradients off by 1.06 2^-8 in the 2-norm with it, by 0.6 2^-8 at most so).
 // All of it is bound by the matrix cores and their power; a handful of rows by the reading of W.
 //
 // Measured, us, with H 2048, V 50304: 4096 rows forward 640 to 660 (1280 to 1320 TFLOP/s), both gradients
@@ -402,6 +405,38 @@ __device__ inline void teacher_row(const HeadArgs &p, int64_t row, int lane, flo
   wave_lds_order();
 }
 
+// unit: the significand, 1 .. 2, of dloss tau in the first row where it is a normal number (no such row: 1). A power
+// of two is the quotient where dloss is the same, and dloss / unit keeps dloss's range. By a workgroup of
+// 1024 threads, 8192 rows a round, the first of them in nearly every call: 3 us by itself, none beside the entries.
+__device__ inline void head_unit(const HeadArgs &p) {
+  constexpr int U = 8;
+  __shared__ int least[2][16];
+  const int t = threadIdx.x, T = (int)p.T;   // (2^25 at the most)
+  int turn = 0;
+  for (int r0 = 0; r0 < T; r0 += U * 1024, turn ^= 1) {
+    int first = T;
+#pragma unroll
+    for (int i = U - 1; i >= 0; --i) {
+      const int row = r0 + i * 1024 + t, in = row < T ? row : T - 1;
+      const uint32_t size = __float_as_uint(p.dloss[in] * p.tau) & 0x7fffffffu;
+      if (row < T && row_on(p, in) && size >= 0x00800000u && size < 0x7f800000u) first = row;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) first = min(first, __shfl_xor(first, d, kWave));
+    if ((t & 63) == 0) least[turn][t >> 6] = first;
+    lds_barrier();   // (a place is written again two rounds on, behind the next round's barrier)
+#pragma unroll
+    for (int w = 0; w < 16; ++w) first = min(first, least[turn][w]);
+    if (first < T) {   // the whole workgroup
+      if (t == 0) *p.unit = __uint_as_float((__float_as_uint(p.dloss[first] * p.tau) & 0x007fffffu) | 0x3f800000u);
+      return;
+    }
+  }
+  if (t == 0) *p.unit = 1.0f;
+}
+
+__global__ __launch_bounds__(1024) void k_head_unit(HeadArgs p) { head_unit(p); }
+
 // A workgroup 16 rows, a wave one of them: the teacher's probabilities (forward), and the rows' entries by
 // chunk of kHeadChunk columns (counts, a scan, places). BACK: those with a probability; else those with an
 // id in the vocabulary. Within a chunk their order is open: each writes to a place of its own.
@@ -417,6 +452,10 @@ inline int entry_rows(int k, int64_t chunks, bool back) {
 }
 template <bool BACK>
 __global__ __launch_bounds__(kEntryThreads) void k_head_entries(HeadArgs p, int rows) {
+  if constexpr (BACK) {
+    static_assert(kEntryThreads == 1024, "the last workgroup, one more than the rows need where P leaves out a unit");
+    if ((int64_t)blockIdx.x * 16 >= p.T) return head_unit(p);
+  }
   extern __shared__ int32_t shared[];   // [chunks], [rows][entry_words]
   __shared__ int32_t total[kEntryThreads / 64];
   const int t = threadIdx.x, w = t >> 6, lane = t & 63;
@@ -493,13 +532,13 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
     n0 += T::cols_at();
     const int lane = epilogue_lane(), left = (int)(p.vn - n0 < COLS ? p.vn - n0 : COLS);
     if (left <= 0) return;   // the wave
-    const float c = kLog2e / p.tau;
+    const float c = kLog2e / p.tau, unit = FEW ? 1.0f : *p.unit;
     const BlockRow<COLS> out{T::scratch(lds), lane};
     // an entry's P, from its logit in fp32
     [[maybe_unused]] auto entry_value = [&](int64_t row, int j) __attribute__((always_inline)) {
       const int64_t e = row * p.k + j;
       if (!row_on(p, row)) return 0.0f;
-      return p.dloss[row] * p.tau * (__builtin_amdgcn_exp2f(p.logits[e] * c - p.lse[row] * kLog2e) - p.q[e]);
+      return p.dloss[row] * p.tau / unit * (__builtin_amdgcn_exp2f(p.logits[e] * c - p.lse[row] * kLog2e) - p.q[e]);
     };
     [[maybe_unused]] TileEntries<T::MB, COLS> entries;
     [[maybe_unused]] float value[T::MB];
@@ -533,7 +572,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
         const int64_t at = (int64_t)id[mb] - p.v0 - n0;
         want = on && at >= 0 && at < left ? (int)at : -1;
       }
-      const float coef = on ? dloss[mb] * p.tau : 0.0f, lse = on ? row_lse[mb] * kLog2e : 0.0f;
+      const float coef = on ? dloss[mb] * p.tau / unit : 0.0f, lse = on ? row_lse[mb] * kLog2e : 0.0f;
       // the rows that count in dw's product, by the wave that has the vocabulary's first columns
       const uint64_t rows_on = __ballot(on);
       if (p.live && p.v0 + n0 == 0 && lane == 0) reinterpret_cast<uint16_t *>(p.live)[row0 >> 4] = (uint16_t)rows_on;
@@ -591,7 +630,7 @@ template <bool BACK>
 hipError_t launch_entries(const HeadArgs &a, hipStream_t s) {
   const int64_t chunks = cdiv(a.V, kHeadChunk);
   const int rows = entry_rows(a.k, chunks, BACK);
-  hipLaunchKernelGGL(k_head_entries<BACK>, dim3((unsigned)cdiv(a.T, 16)), dim3(kEntryThreads),
+  hipLaunchKernelGGL(k_head_entries<BACK>, dim3((unsigned)cdiv(a.T, 16) + (BACK && a.unit ? 1 : 0)), dim3(kEntryThreads),
                      4 * (chunks + (int64_t)rows * entry_words(a.k, BACK)), s, a, rows);
   return hipGetLastError();
 }
@@ -672,8 +711,10 @@ hipError_t launch_head_forward(const HeadArgs &args, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_head_entries(const HeadArgs &a, hipStream_t s) {
-  return launch_entries<true>(a, s);
+hipError_t launch_head_prepare(const HeadArgs &a, hipStream_t s) {
+  if (a.k) return launch_entries<true>(a, s);
+  if (a.unit) hipLaunchKernelGGL(k_head_unit, dim3(1), dim3(1024), 0, s, a);
+  return hipGetLastError();
 }
 
 hipError_t launch_head_piece(const HeadArgs &a, hipStream_t s) {

@@ -521,7 +521,8 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
  * those of the fine-tuning calls above. Matrices are bf16, contiguous and 16-byte aligned, their
  * widths (H, I) multiples of 8 up to 2^20; products are summed in fp32, every output is
  * rounded once; the gradient of a product (dgu, P below) is rounded to bf16 where it becomes
- * an operand of the next, up to 64 rows to the sum of two bf16 values. The same bits on every run of
+ * an operand of the next, up to 64 rows to the sum of two bf16 values, P of more rows without a factor that
+ * their dloss have in common (1 / rows of a mean loss, say, is not rounded). The same bits on every run of
  * the same call (dx asked for without the weight's gradient may be summed in another order than
  * beside it). UNSUPPORTED past 2^22 tiles of 256 x 256 of one product, 2^38 values, or 2^25 rows of
  * a vocabulary loss.

@@ -1,0 +1,90 @@
+"""The dense operators where a rounding or a value that is not finite would show most: a mean loss, whose rows
+all have the same gradient; rows sure of their label; rows far from zero; infinities and masked rows in the
+forms of few rows. Bounds as in test_gpu_dense.py: u = 2^-24 and b = 2^-8 are half steps of fp32 and bf16."""
+import pytest
+
+import dense_ref as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import bit_quantized_moe_expert_amd as M  # noqa: E402
+from test_gpu_dense import B, BF16, DEV, F32, I32, INF, NAN, U, gen, near  # noqa: E402
+
+
+# ------------------------------------------------------------------ the gradient of a mean
+def mean_case(T, V, k, H=256):
+    """Rows unsure of their labels, P of a label all but -dloss."""
+    rn = gen(T + V)
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x, w = rn(T, H, dt=BF16), rn(V, H, std=H ** -0.5, dt=BF16)
+    labels = torch.randint(0, V, (T,), generator=g, device=DEV).to(I32)
+    return x, w, labels
+
+
+def head_gradients(x, w, labels, dloss, k):
+    """Through the cross entropy, or (k = 1) through the distillation from one sure entry."""
+    if not k:
+        return M.vocab_ce_backward(dloss, x, w, labels, M.vocab_ce_forward(x, w, labels)[1])
+    ids = labels[:, None].contiguous()
+    f = M.vocab_distill_forward(x, w, ids, torch.zeros(len(labels), 1, device=DEV))
+    return M.vocab_distill_backward(dloss, x, w, ids, f["q"], f["logits"], f["lse"])
+
+
+@pytest.mark.parametrize("k", [0, 1])
+@pytest.mark.parametrize("T,V,rows", [(1020, 8003, 1020), (4080, 4001, 4080), (130, 3001, 127), (1000, 20001, 1019)])
+def test_gradients_of_a_mean_loss(T, V, rows, k):
+    """dloss is 1 / rows everywhere: no rounding of it may be every row's."""
+    x, w, labels = mean_case(T, V, k)
+    dloss = torch.full((T,), 1.0 / rows, device=DEV)
+    out = head_gradients(x, w, labels, dloss, k)
+    P = R.ce_P(dloss, x, w, labels)
+    near(out["dx"], P @ w.double(), 2, "dx"), near(out["dw"], P.T @ x.double(), 2, "dw")
+
+
+@pytest.mark.parametrize("k", [0, 1])
+def test_gradients_of_a_mean_loss_behind_masked_rows(k):
+    """The mean over the rows with a label; those before them, and rows of weight zero, hold anything."""
+    T, V = 3000, 2003
+    x, w, labels = mean_case(T, V, k)
+    labels[:2100] = -100
+    dloss = torch.full((T,), 1.0 / 1020, device=DEV)
+    dloss[:2100] = torch.tensor([NAN, INF, 0.7], device=DEV).repeat(700)
+    dloss[2100:2103] = 0.0
+    out = head_gradients(x, w, labels, dloss, k)
+    P = R.ce_P(dloss, x, w, labels)
+    near(out["dx"], P @ w.double(), 2, "dx"), near(out["dw"], P.T @ x.double(), 2, "dw")
+    assert not out["dx"][:2103].any()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -120, 3.0 * 2.0 ** -131, 1.4e-45, 2.0 ** 90])
+def test_gradients_of_far_scales(scale):
+    """A mean's gradient in proportion to its dloss, whatever size that has; below fp32's normal numbers (and
+    bf16's) products go to zero as they like, with nothing but small values."""
+    x, w, labels = mean_case(200, 501, 0)
+    one = head_gradients(x, w, labels, torch.ones(200, device=DEV), 0)
+    out = head_gradients(x, w, labels, torch.full((200,), scale, device=DEV), 0)
+    for n in out:
+        want = one[n].double() * scale
+        R.within(out[n], want, 2 * B * want.abs() + 2.0 ** -124, n)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_a_gradient_that_is_not_finite_stays_in_its_row(bad):
+    x, w, labels = mean_case(150, 501, 0)
+    dloss = torch.full((150,), 1.0 / 51, device=DEV)
+    want = head_gradients(x, w, labels, dloss, 0)
+    dloss[0] = bad
+    out = head_gradients(x, w, labels, dloss, 0)
+    assert torch.equal(out["dx"][1:], want["dx"][1:])
+    assert not torch.isfinite(out["dx"][0]).any() and not torch.isfinite(out["dw"]).any()
+
+
+@pytest.mark.parametrize("k", [0, 1])
+def test_gradients_where_no_row_counts(k):
+    x, w, labels = mean_case(100, 300, k)
+    out = head_gradients(x, w, torch.full_like(labels, -100), torch.full((100,), NAN, device=DEV), k)
+    assert not out["dx"].any() and not out["dw"].any()
