@@ -88,3 +88,46 @@ def test_gradients_where_no_row_counts(k):
     x, w, labels = mean_case(100, 300, k)
     out = head_gradients(x, w, torch.full_like(labels, -100), torch.full((100,), NAN, device=DEV), k)
     assert not out["dx"].any() and not out["dw"].any()
+
+
+# ------------------------------------------------------------------ layer norm far from zero
+@pytest.mark.parametrize("T,H", [(5, 2880), (300, 2880), (700, 1000), (3, 129), (300, 6001), (260, 12000), (2, 16384)])
+@pytest.mark.parametrize("value", [1000.1, 10000.1, -0.3])
+def test_layer_norm_of_constant_rows(T, H, value):
+    """The first sum's error, e = s |value| with s = (24 + H / 64) u, is taken out to s of itself: the mean is the
+    value, y no more than s e rstd, and the variance's part of rstd s e^2 rstd^2."""
+    x = torch.full((T, H), value, device=DEV)
+    got = M.layer_norm_forward(x, eps=1e-5)
+    v, s, r = float(x[0, 0]), (24 + H / 64) * U, 1e-5 ** -0.5
+    e = s * abs(v)
+    assert (got["mean"] == v).all()
+    assert float(got["y"].abs().max()) <= s * e * r + U * e * r
+    assert float((got["rstd"].double() / r - 1).abs().max()) <= 2 * s * e * e * r * r + 8 * U
+
+
+@pytest.mark.parametrize("T,H", [(5, 2880), (300, 2880), (50, 1000), (300, 6001)])
+@pytest.mark.parametrize("shift,spread", [(1000.0, 1.0), (10000.0, 0.01), (-3.0, 1.0)])
+def test_layer_norm_of_rows_far_from_zero(T, H, shift, spread):
+    """x - mean is exact or off by u of itself, the mean's error e comes out to s of itself and of the spread."""
+    x = gen(3)(T, H, std=spread) + shift
+    y, mean, rstd = R.layer_norm(x, None, None, 0.0)
+    got = M.layer_norm_forward(x, eps=0.0)
+    s = (24 + H / 64) * U
+    e = s * x.double().abs().mean(1)
+    R.within(got["mean"], mean, U * mean.abs() + s * (e + 1 / rstd), "mean")
+    rel = 2 * s * (1 + (e * rstd) ** 2) + 8 * U          # of the variance, e^2 of the first mean in it
+    R.within(got["rstd"], rstd, rstd * rel, "rstd")
+    R.within(got["y"], y, (s * (e * rstd + 1) + 2 * U)[:, None] + y.abs() * (rel + 4 * U)[:, None], "y")
+
+
+@pytest.mark.parametrize("fill", [NAN, INF, -INF])
+@pytest.mark.parametrize("T", [4, 300])
+def test_layer_norm_not_finite_stays_in_its_row(T, fill):
+    x = gen(4)(T, 1000)
+    want = M.layer_norm_forward(x)
+    x[2, 7] = fill
+    got = M.layer_norm_forward(x)
+    rows = torch.arange(T, device=DEV) != 2
+    for n in got:
+        assert torch.equal(got[n][rows], want[n][rows])
+    assert torch.isnan(got["y"][2]).all() and torch.isnan(got["rstd"][2]) and not torch.isfinite(got["mean"][2])
