@@ -151,8 +151,8 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_ffn(FfnArgs p) {
             hv[j] = glu_slopes(p.glu, p.alpha, p.limit, t.acc[nb][mb][j], t.acc[nb + G][mb][j], by_g, by_u);
             dg[j] = dh[j] * by_g, du[j] = dh[j] * by_u;
             if constexpr (FEW) {
-              low[0][nb][j] = dg[j] - bf16_to_f32(f32_to_bf16_rne(dg[j]));
-              low[1][nb][j] = du[j] - bf16_to_f32(f32_to_bf16_rne(du[j]));
+              low[0][nb][j] = bf16_rest(dg[j]);
+              low[1][nb][j] = bf16_rest(du[j]);
             }
           }
           h[nb] = pack4(hv[0], hv[1], hv[2], hv[3]);

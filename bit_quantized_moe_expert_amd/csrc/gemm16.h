@@ -359,6 +359,12 @@ __device__ inline int epilogue_lane() {
 __device__ inline uint2 pack4(float a, float b, float c, float d) {
   return make_uint2(f32x2_to_bf16x2_rne(a, b), f32x2_to_bf16x2_rne(c, d));
 }
+// What bf16 leaves of v, a value's second part: nothing where bf16 has it infinite (v finite or not) or NaN, so that
+// the first part alone says so.
+__device__ inline float bf16_rest(float v) {
+  const float r = bf16_to_f32(f32_to_bf16_rne(v));
+  return fabsf(r) < __builtin_inff() ? v - r : 0.0f;
+}
 
 // A wave's block row, 16 rows of COLS bf16, on its way from the products' layout to whole rows in
 // memory: through the wave's own LDS, 16-byte pieces moved so that neither side has bank

@@ -593,11 +593,8 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = on && T::col_of(lane, nb) + j < left ? v[j] : 0.0f;
         }
-        const uint2 high = pack4(v[0], v[1], v[2], v[3]);
-        if constexpr (FEW)
-          low[nb] = pack4(v[0] - bf16lo_to_f32(high.x), v[1] - bf16hi_to_f32(high.x), v[2] - bf16lo_to_f32(high.y),
-                          v[3] - bf16hi_to_f32(high.y));
-        out.put(T::col_of(lane, nb), high);
+        if constexpr (FEW) low[nb] = pack4(bf16_rest(v[0]), bf16_rest(v[1]), bf16_rest(v[2]), bf16_rest(v[3]));
+        out.put(T::col_of(lane, nb), pack4(v[0], v[1], v[2], v[3]));
       }
       if constexpr (TEACH) {   // the entries' places
         wave_lds_order();
@@ -610,7 +607,7 @@ __global__ __launch_bounds__(T::THREADS, T::WAVES_SIMD) void k_head_piece(HeadAr
       uint16_t *to = p.P + row0 * p.vp + n0;
       out.out(to, p.vp, p.T - row0, p.vp - n0);
       if constexpr (FEW) {
-        auto rest_of = [](float v) { return (uint16_t)f32_to_bf16_rne(v - bf16_to_f32(f32_to_bf16_rne(v))); };
+        auto rest_of = [](float v) { return (uint16_t)f32_to_bf16_rne(bf16_rest(v)); };
 #pragma unroll
         for (int nb = 0; nb < T::NB; ++nb) out.put(T::col_of(lane, nb), low[nb]);
         if constexpr (TEACH) {

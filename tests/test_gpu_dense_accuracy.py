@@ -131,3 +131,49 @@ def test_layer_norm_not_finite_stays_in_its_row(T, fill):
     for n in got:
         assert torch.equal(got[n][rows], want[n][rows])
     assert torch.isnan(got["y"][2]).all() and torch.isnan(got["rstd"][2]) and not torch.isfinite(got["mean"][2])
+
+
+# ------------------------------------------------------------------ the forms of few rows
+def kinds(t):
+    """0 finite, 1 and -1 infinite, 2 NaN."""
+    return torch.where(torch.isnan(t), 2.0, torch.where(torch.isinf(t), torch.sign(t.float()), 0.0))
+
+
+@pytest.mark.parametrize("glu,inter", [(0, 0), (1, 1)])
+@pytest.mark.parametrize("T", [1, 5, 40, 64])
+def test_an_infinite_gradient_stays_infinite(T, glu, inter):
+    """dh of infinity, and one past bf16's largest value through the slope: what is not finite is what it is in a
+    longer batch, whose further rows have no gradient."""
+    H, I = 128, 72
+    rn = gen(T)
+    x, w = rn(65, H, dt=BF16), rn(2 * I, H, std=2.0 * H ** -0.5, dt=BF16)
+    how = dict(glu=glu, alpha=1.702, limit=7.0, interleaved=inter)
+    slopes = R.ffn(x, w, glu, 1.702, 7.0, inter)[3:]
+    assert (slopes[0][0].abs() > 1.1).any()
+    for value, col in ((INF, 7), (-INF, 9), (3.3e38, int(slopes[0][0].abs().argmax()))):
+        dh = torch.zeros(65, I, device=DEV, dtype=BF16)
+        dh[:T] = rn(T, I, std=0.3)
+        dh[0, col] = value
+        want = M.gated_ffn_backward(dh, x, w, **how)
+        got = M.gated_ffn_backward(dh[:T].contiguous(), x[:T].contiguous(), w, **how)
+        assert torch.equal(kinds(got["dx"]), kinds(want["dx"][:T])) and torch.equal(kinds(got["dw13"]), kinds(want["dw13"]))
+        assert torch.isinf(got["dw13"]).any() and torch.isinf(got["dx"][0]).any()
+        assert torch.isfinite(got["dx"][1:]).all()
+
+
+@pytest.mark.parametrize("k", [0, 1])
+@pytest.mark.parametrize("T", [1, 5, 40, 64])
+def test_an_infinite_loss_gradient_stays_infinite(T, k):
+    x, w, labels = mean_case(65, 601, k, H=128)
+    on = torch.arange(65, device=DEV) < T
+    labels = torch.where(on, labels, -100).to(I32)
+    for value in (INF, -INF):
+        dloss = torch.full((65,), 0.1, device=DEV)
+        dloss[0] = value
+        want = head_gradients(x, w, labels, dloss, k)
+        got = head_gradients(x[:T].contiguous(), w, labels[:T].contiguous(), dloss[:T].contiguous(), k)
+        assert torch.equal(kinds(got["dw"]), kinds(want["dw"])) and torch.isinf(got["dw"]).all()
+        assert not torch.isfinite(got["dx"][0]).any() and torch.isfinite(got["dx"][1:]).all()
+    dloss[0] = 3.4e38          # P of the label is past bf16's largest value
+    got = head_gradients(x[:T].contiguous(), w, labels[:T].contiguous(), dloss[:T].contiguous(), k)
+    assert not torch.isnan(got["dx"]).any() and not torch.isnan(got["dw"]).any()
