@@ -177,3 +177,33 @@ def test_an_infinite_loss_gradient_stays_infinite(T, k):
     dloss[0] = 3.4e38          # P of the label is past bf16's largest value
     got = head_gradients(x[:T].contiguous(), w, labels[:T].contiguous(), dloss[:T].contiguous(), k)
     assert not torch.isnan(got["dx"]).any() and not torch.isnan(got["dw"]).any()
+
+
+@pytest.mark.parametrize("fill", [NAN, INF, -INF, 3.3e38])
+@pytest.mark.parametrize("T", [2, 17, 40, 64])
+def test_few_rows_without_a_target_count_for_nothing(T, fill):
+    """Whatever x, dloss and the teacher hold in a masked row or entry."""
+    V = 3001
+    x, w, labels = mean_case(T, V, 0, H=128)
+    labels[::2] = torch.tensor([-100, V], device=DEV, dtype=I32).repeat(T)[:len(labels[::2])]
+    dloss = gen(T)(T)
+    dead = (labels < 0) | (labels >= V)
+    zero = lambda v: torch.where(dead if v.dim() == 1 else dead[:, None], torch.zeros_like(v), v)  # noqa: E731
+    put = lambda v: torch.where(dead if v.dim() == 1 else dead[:, None], torch.full_like(v, fill), v)  # noqa: E731
+    loss, lse = M.vocab_ce_forward(zero(x), w, labels)
+    loss2, lse2 = M.vocab_ce_forward(put(x), w, labels)
+    assert torch.equal(loss, loss2) and torch.equal(lse[~dead], lse2[~dead])
+    a = M.vocab_ce_backward(zero(dloss), zero(x), w, labels, zero(lse))
+    b = M.vocab_ce_backward(put(dloss), put(x), w, labels, put(lse2))
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dw"], b["dw"]) and torch.isfinite(b["dw"]).all()
+    assert not b["dx"][dead].any()
+    ids = torch.stack([labels, torch.full_like(labels, -1), (labels + 1) % V], 1)
+    ids = torch.where(dead[:, None], torch.full_like(ids, -7), ids).contiguous()
+    outside = (ids < 0) | (ids >= V)
+    t = gen(5)(T, 3)
+    t1, t2 = torch.where(outside, 0.0, t), torch.where(outside, fill, t)
+    p, r = M.vocab_distill_forward(zero(x), w, ids, t1), M.vocab_distill_forward(put(x), w, ids, t2)
+    assert all(torch.equal(p[n], r[n]) for n in p)
+    a = M.vocab_distill_backward(zero(dloss), zero(x), w, ids, p["q"], p["logits"], p["lse"])
+    b = M.vocab_distill_backward(put(dloss), put(x), w, ids, r["q"], r["logits"], r["lse"])
+    assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dw"], b["dw"]) and torch.isfinite(b["dw"]).all()
