@@ -90,6 +90,26 @@ def test_gradients_where_no_row_counts(k):
     assert not out["dx"].any() and not out["dw"].any()
 
 
+# ------------------------------------------------------------------ rows sure of their label
+@pytest.mark.parametrize("T,V", [(7, 1000), (30, 9001), (300, 1000), (2500, 301)])
+def test_the_loss_of_a_sure_row(T, V):
+    """Sums that are exact, logits up to 60, losses down to 0. exp2 of the largest term, the logarithm and the last
+    operations are 8 u of 1 together. A sum of about 1 loses no more of a smaller term than the term, so of all
+    of them the loss itself; nor than a u a step (300 + V / 512 of them)."""
+    H = 64
+    g = torch.Generator(device=DEV).manual_seed(T)
+    w = torch.randint(-1, 2, (V, H), generator=g, device=DEV).to(BF16)
+    labels = torch.randint(0, V, (T,), generator=g, device=DEV).to(I32)
+    x = w[labels.long()] * (torch.randint(1, 9, (T, 1), generator=g, device=DEV) / 8).to(BF16)
+    loss, lse = R.ce(x, w, labels)
+    got, got_lse = M.vocab_ce_forward(x, w, labels)
+    assert (loss < 1e-6).any() and (loss > 1e-3).any()
+    bound = 8 * U + torch.minimum(loss, torch.full_like(loss, (300 + V / 512) * U)) + 4 * U * loss
+    R.within(got, loss, bound, "loss")
+    d = M.vocab_distill_forward(x, w, labels[:, None].contiguous(), torch.zeros(T, 1, device=DEV))
+    R.within(d["loss"], loss, bound, "distillation from one entry")
+
+
 # ------------------------------------------------------------------ layer norm far from zero
 @pytest.mark.parametrize("T,H", [(5, 2880), (300, 2880), (700, 1000), (3, 129), (300, 6001), (260, 12000), (2, 16384)])
 @pytest.mark.parametrize("value", [1000.1, 10000.1, -0.3])
