@@ -1,4 +1,4 @@
-// The gated feed-forward block of dense bf16 weights (a shared expert), and the products
+// The gated feed-forward of dense bf16 weights (a shared expert's gate and up half), and the products
 // that the backward passes of the dense operators share.
 //
 // Forward: g = x Wg^T, u = x Wu^T, h = act(g, u) in one kernel: a tile takes the gate and
@@ -9,11 +9,11 @@
 // (gemm16.h's turned sides). dgu is rounded to bf16, half a step of 2^-8 of each value, because it is an
 // operand of bf16 products; up to kTwoParts rows it is held in two parts, which leave 2^-17.
 //
-// Measured, us: forward of 4096 rows, H 2048, I 8192 210 (1311 TFLOP/s; the bare products by a
-// library 198), of 4099, H = I = 2880 108 to 114 (1190 to 1260, 5 % more in its padding); backward of
+// Measured, us: forward of 4096 rows, H 2048, I 8192 210 to 213 (1290 to 1310 TFLOP/s; the bare products by a
+// library 198), of 4099, H = I = 2880 108 to 115 (1180 to 1260, 5 % more in its padding); backward of
 // the first 645 to 683 (1210 to 1280 of 825 GFLOP). All of these are bound by the matrix cores and their
 // power. One row, H 2048, I 1024: 5.2, of which the 8.4 MB of weights would take 1.6: a launch's
-// latency and memory's; 32 rows, H 4096, I 14336 45 for 235 MB (5.2 TB/s). 131 rows, H 2048, I 768,
+// latency and memory's; 32 rows, H 4096, I 14336 45 to 47 for 235 MB (5.0 to 5.2 TB/s). 131 rows, H 2048, I 768,
 // backward: 24.4 for 10 (gate, up, dgu) + 13 (products) + 4 (dx's slices joined), the latencies of
 // three dependent launches.
 #include "dense.h"
@@ -292,7 +292,8 @@ __device__ __attribute__((always_inline)) void product_tiles(const ProductArgs &
 }
 
 // Workgroups 0 .. nbx - 1 take dx's tiles, the others dw's: side by side they fill the card together, where
-// dx by itself has its k in slices to be joined (4096 rows, H 2048, I 8192: dx 240 us alone, dw 231, both 434).
+// dx by itself has its k in slices to be joined (4096 rows, H 2048, I 8192: dx 198 us alone and 13 to
+// join, dw 200, both 392).
 // nbx < 0, for large products of equal steps: half of the XCDs each, so that an L2 holds the operands
 // of one product (1 to 1.7 % of a whole backward).
 template <class TX, class TW, bool UNIT>

@@ -17,10 +17,10 @@
 // gradients off by 1.06 2^-8 in the 2-norm with it, by 0.6 2^-8 at most so).
 // All of it is bound by the matrix cores and their power; a handful of rows by the reading of W.
 //
-// Measured, us, with H 2048, V 50304: 4096 rows forward 640 to 660 (1280 to 1320 TFLOP/s), both gradients
-// 1975 to 2070 (1225 to 1280 of 2532 GFLOP). The head's 17 rows with V 32003 (131 MB): 28 + 4 to join. Distillation,
-// k 64, 2048 rows, H 2880: 495 to 515, of which the teacher's entries 12 and the joining 6; its gradient dx of 515
-// rows, H 1024, V 32003: 111 to 114 for 5 (entries) + 60 (P) + 40 (product) + 9 (its 21 slices).
+// Measured, us, with H 2048, V 50304: 4096 rows forward 643 to 663 (1270 to 1310 TFLOP/s), both gradients
+// 2010 to 2120 (1195 to 1260 of 2532 GFLOP). The head's 17 rows with V 32003 (131 MB): 28 + 4 to join. Distillation,
+// k 64, 2048 rows, H 2880: 505 to 522, of which the teacher's entries 12 and the joining 6; its gradient dx of 515
+// rows, H 1024, V 32003: 111 to 114 for 5 (entries) + 58 (P) + 39 (product) + 9 (its 21 slices).
 //
 // Exponentials are taken in powers of two: z = l log2(e) / tau. A row's maximum m is rounded, its terms
 // 2^(z - m) and what a loss needs of it, m - z, come from one fma of l each: lse - l / tau = (m - z + log2 s) ln 2, where
@@ -412,7 +412,8 @@ __device__ inline void teacher_row(const HeadArgs &p, int64_t row, int lane, flo
 
 // unit: the significand, 1 .. 2, of dloss tau in the first row where it is a normal number (no such row: 1). A power
 // of two is the quotient where dloss is the same, and dloss / unit keeps dloss's range. By a workgroup of
-// 1024 threads, 8192 rows a round, the first of them in nearly every call: 3 us by itself, none beside the entries.
+// 1024 threads, 8192 rows a round, the first of them in nearly every call: 2.4 us by itself for 131 rows, 5 for 4096, none
+// beside the entries.
 __device__ inline void head_unit(const HeadArgs &p) {
   constexpr int U = 8;
   __shared__ int least[2][16];

@@ -9,8 +9,8 @@
 //   dx = dx_base + rstd (a - mean(a) - n mean(a n));  dw = sum_t dy n;  db = sum_t dy
 // Everything is fp32 in registers, each output rounded once. Both directions are bound by memory
 // traffic. Rows lie as in the block norms' kernels: TPR threads a row, 8 NC values each, so that a row is read
-// once and a sum meets in one exchange through LDS. Measured, us: 8190 x 2880 fp32 to bf16 28.5 to 29.1 (142
-// MB, 5.0 TB/s, a copy's rate 5.4); backward of 8192 x 2048 bf16 with a base 27 (134 MB, 5.0 TB/s) and
+// once and a sum meets in one exchange through LDS. Measured, us: 8190 x 2880 fp32 to bf16 28.5 to 29 (142
+// MB, 4.9 to 5.0 TB/s, a copy's rate 5.4); backward of 8192 x 2048 bf16 with a base 27 (134 MB, 5.0 TB/s) and
 // 4 for the column sums; 4 rows 3.0.
 #include "dense.h"
 #include "internal.h"

@@ -1,5 +1,5 @@
 """Python binding of the dense bf16 ends of a training step around the frozen 4-bit MoE
-layer: the gated feed-forward (a shared expert), the losses of a vocabulary head (cross
+layer: a gated feed-forward's gate and up half (a shared expert's), the losses of a vocabulary head (cross
 entropy, distillation from a teacher's top logits) and layer norm.
 
 As in train.py, arguments are contiguous CUDA tensors of one device, sizes, types and

@@ -516,13 +516,13 @@ nf4moe_status_t nf4moe_adapter_backward(const nf4moe_adapters_t *ad, const uint1
                                         void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
- * The dense bf16 ends of a training step around the frozen layer: a gated feed-forward
- * (a shared expert), the losses of a vocabulary head, layer norm. The conventions are
- * those of the fine-tuning calls above. Matrices are bf16, contiguous and 16-byte aligned, their
- * widths (H, I) multiples of 8 up to 2^20; products are summed in fp32, every output is
- * rounded once; the gradient of a product (dgu, P below) is rounded to bf16 where it becomes
- * an operand of the next, up to 64 rows to the sum of two bf16 values, P of more rows without a factor that
- * their dloss have in common (1 / rows of a mean loss, say, is not rounded). The same bits on every run of
+ * The dense bf16 ends of a training step around the frozen layer: a gated feed-forward's gate
+ * and up half (of a shared expert; the down projection is the caller's), the losses of a
+ * vocabulary head, layer norm. The conventions are those of the fine-tuning calls above. Matrices
+ * are bf16, contiguous and 16-byte aligned, their widths (H, I) multiples of 8 up to 2^20;
+ * products are summed in fp32, every output is rounded once; the gradient of a product (dgu, P below) is rounded to bf16 where it becomes
+ * an operand of the next, up to 64 rows to the sum of two bf16 values, P of more rows without a
+ * factor that their dloss have in common (1 / rows of a mean loss, say, is not rounded). The same bits on every run of
  * the same call (dx asked for without the weight's gradient may be summed in another order than
  * beside it). UNSUPPORTED past 2^22 tiles of 256 x 256 of one product, 2^38 values, or 2^25 rows of
  * a vocabulary loss.
@@ -542,7 +542,9 @@ typedef struct {
 nf4moe_status_t nf4moe_gated_ffn_forward(const nf4moe_gated_ffn_t *ffn, const uint16_t *x, int64_t T, uint16_t *h,
                                          void *stream);
 
-/* nf4moe_gated_ffn_workspace_bytes -- workspace of the backward (0 for T < 1 or invalid sizes). */
+/* nf4moe_gated_ffn_workspace_bytes -- workspace of the backward (0 for T < 1 or invalid sizes), whatever outputs are
+ * asked for: dgu [T, 2I]; up to 64 rows twice that and x, and dx twice in fp32; and where sums are cut into slices
+ * fp32 parts of dx and of dw13, at most 64 MB each. */
 size_t nf4moe_gated_ffn_workspace_bytes(const nf4moe_gated_ffn_t *ffn, int64_t T);
 
 /* nf4moe_gated_ffn_backward -- gradients for dh bf16 [T, I], g and u computed again:
@@ -564,8 +566,9 @@ typedef struct {
 
 /* nf4moe_vocab_workspace_bytes -- workspace of the forward (backward = 0) or the backward (1) of
  * the cross entropy (k = 0) or of the distillation from k entries a row, for T rows; 0 for T < 1 or
- * invalid sizes. The backward's holds the gradient P of one piece of the vocabulary at a
- * time: at most 128 MB of it, or 256 columns. */
+ * invalid sizes. The backward's, whatever outputs are asked for, holds the gradient P of one piece of the vocabulary at
+ * a time, at most 128 MB of it, or 256 columns; dx in fp32 where the vocabulary has several pieces, up to 64 rows dx and
+ * x twice; and where sums are cut into slices fp32 parts of dx and of a piece of dw, at most 64 MB each. */
 size_t nf4moe_vocab_workspace_bytes(const nf4moe_head_t *head, int64_t T, int32_t k, int32_t backward);
 
 /* nf4moe_vocab_ce_forward -- softmax cross entropy: lse[t] = log sum_v exp(l[t, v]) and loss[t] =
